@@ -53,7 +53,10 @@ typedef enum {
     DASH_ERR_DEADLOCK = -5,   /* a schedule table cannot complete (cycle or missing predecessor) */
     DASH_ERR_NOMEM = -6,      /* workspace allocation failed */
     DASH_ERR_DEVICE = -7,     /* device is not sm_103 / lacks the needed shared memory */
-    DASH_ERR_SCRATCH = -8     /* problem needs more than dash_attn_bwd_noalloc's fixed scratch */
+    DASH_ERR_SCRATCH = -8,    /* problem needs more than dash_attn_bwd_noalloc's fixed scratch, or than the
+                               * workspace given to dash_attn_paged */
+    DASH_ERR_PAGE = -9        /* a page, slot, position or length on the device lies outside what the call was
+                               * given (reported by dash_get_status_paged) */
 } dash_status;
 
 typedef enum {
@@ -334,6 +337,197 @@ int dash_get_status_noalloc(dash_stream_t stream, int* code, int* info);
  * DASH_ERR_DEVICE off sm_103, DASH_ERR_CUDA on launch failure.
  */
 int dash_dq_finalize(const float* dq_accum, dash_bf16* dq, size_t numel, dash_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and serving: a paged key/value cache and the attention of
+ * new tokens over it (no counterpart on the pages, which schedule the training
+ * backward: these are the operators around it that a model trained with it
+ * needs).  Further conventions of these calls:
+ *  - Nothing is allocated, kept between calls or synchronized; every call can
+ *    be captured into a graph (make one call on the device first, so that the
+ *    kernels are loaded).  Calls on different streams are independent as long
+ *    as their outputs and workspaces are.
+ *  - Strides are in elements and never negative; rows are contiguous in D,
+ *    start 16-byte aligned, and strides of bf16 and fp32 data are multiples of
+ *    8 elements.
+ *  - What only the device knows (positions, slots, pages, lengths) is checked
+ *    there: nothing is read or written out of range, and the first value found
+ *    wrong is kept for dash_get_status_paged.
+ *  - Outputs are bitwise reproducible.
+ * ------------------------------------------------------------------------- */
+
+/* Vectors of D values: element (b, h, s, d) of `data` at
+ * b*stride_b + h*stride_h + s*stride_s + d. */
+typedef struct {
+    void* data;                /* device, 16-byte aligned */
+    int fp32;                  /* 1: fp32, 0: bf16 */
+    int heads;
+    int64_t stride_b, stride_h, stride_s;
+} dash_heads;
+
+/*
+ * dash_rope -- rotary positions: y = factor * R(position) x for every vector
+ * of x, and of x2 into y2 when x2 is not NULL (queries and keys of one layer,
+ * which share positions).  R turns value pair i < rot/2 by the angle
+ * position * inv_freq[i]:
+ *   y_a = factor * (x_a cos - x_b sin),  y_b = factor * (x_b cos + x_a sin),
+ * with (a, b) = (2i, 2i+1) when `interleaved` is 1 and (i, i + rot/2) when it
+ * is 0; values d >= rot are copied.  inverse = 1 turns by the negative angle:
+ * factor * R(-position) is the transpose of the forward, so the same call with
+ * inverse = 1 maps dL/dy to dL/dx (for dQ straight from the fp32 accumulator
+ * of dash_attn_bwd, in place of dash_dq_finalize).
+ *   x, x2: [B, heads, S, D], bf16 or fp32; y, y2: same shape, bf16 or fp32.
+ *   y may be x (same type and strides); otherwise they must not overlap.
+ *   positions: device int32, position of (b, s) at b*pos_stride_b + s
+ *   (pos_stride_b = 0: shared by the batch), any value; NULL: s itself.
+ *   inv_freq: HOST double [rot/2], radians per position; read before the call
+ *   returns.  dash_rope_freqs fills it for the usual long-context scalings.
+ *   D in {64, 128}, rot a multiple of 16, 16 <= rot <= D.
+ * The angle is formed as a 64-bit fraction of a turn (position times the
+ * frequency modulo one turn in integers), so far positions lose nothing; the
+ * rotation is fp32, rounded once to y's type.
+ * Returns DASH_OK (also for B or S = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or
+ * DASH_ERR_CUDA.
+ */
+int dash_rope(const dash_heads* x, const dash_heads* y, const dash_heads* x2, const dash_heads* y2,
+              const int32_t* positions, int64_t pos_stride_b, const double* inv_freq, int rot, int interleaved,
+              float factor, int inverse, int B, int S, int D, dash_stream_t stream);
+
+typedef enum {
+    DASH_ROPE_PLAIN = 0,      /* base^(-2i/rot) */
+    DASH_ROPE_LINEAR = 1,     /* every frequency divided by `scale` */
+    DASH_ROPE_BASE = 2,       /* the base raised so that the slowest pair is slowed by `scale` */
+    DASH_ROPE_WAVE = 3,       /* divided by `scale` below `lo` turns over `trained` tokens, kept above `hi`
+                               * turns, blended linearly in the number of turns between */
+    DASH_ROPE_RAMP = 4        /* the same with the blend linear in the pair's index (rounded outwards) */
+} dash_rope_scaling;
+
+/*
+ * dash_rope_freqs -- inv_freq [rot/2] (host, written) for a base and a
+ * long-context scaling, and *factor (written) = the factor that goes with it:
+ * 0.1 ln(scale) + 1 for DASH_ROPE_RAMP with scale > 1, else 1.
+ *   trained: context length of training; lo < hi: turns (WAVE and RAMP only).
+ * Host only.  Returns DASH_OK or DASH_ERR_ARG (null, rot odd or < 4, base <= 1,
+ * scale < 1, unknown scaling, trained < 1 or not 0 < lo < hi where they are used).
+ */
+int dash_rope_freqs(int rot, double base, int scaling, double scale, int trained, double lo, double hi,
+                    double* inv_freq, float* factor);
+
+typedef enum { DASH_CACHE_BF16 = 0, DASH_CACHE_E4M3 = 1 } dash_cache_type;
+
+/*
+ * A paged key/value cache: pages of page_size tokens, k and v each
+ * [num_pages, Hkv, page_size, D].  DASH_CACHE_E4M3 holds e4m3 values with one
+ * fp32 scale for each token and head, [num_pages, Hkv, page_size] (a cached
+ * vector stands for code * scale); DASH_CACHE_BF16 has no scales (NULL).
+ * All contiguous device memory, 16-byte aligned.  page_size: 16, 32, 64, 128
+ * or 256; D in {64, 128}.  Token offset o of page p is slot p*page_size + o.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int type, num_pages, page_size, Hkv, D;
+} dash_kv_cache;
+
+/* Rotation of new tokens on their way into the cache (see dash_rope). */
+typedef struct {
+    const double* inv_freq;        /* host [rot/2] */
+    const int32_t* positions;      /* device [T] */
+    int rot, interleaved;
+    float factor;
+    /* queries rotated by the same call: [T, Hq, D]; q NULL: none */
+    const dash_bf16* q;
+    int64_t q_stride_t, q_stride_h;
+    dash_bf16* q_out;              /* may be q (with its strides) */
+    int64_t q_out_stride_t, q_out_stride_h;
+    int Hq;
+} dash_write_rope;
+
+/*
+ * dash_kv_write -- write T new tokens into the cache: token t's keys and
+ * values k, v [T, Hkv, D] (bf16) go to slot slots[t] (device int64; negative:
+ * the token is not written).  rope (NULL: none): the keys are rotated first,
+ * and the queries into q_out, for every t.  Rounding happens once, from fp32:
+ * to bf16, or per vector to
+ *   scale = max(max|x| / 448, 2^-126),  code = e4m3_round_to_nearest_even(x / scale).
+ * (NaN stays NaN in its own value and does not enter the maximum; a vector
+ * that holds an infinity reads back as NaN.)  Slots must be distinct: of two
+ * tokens with the same slot either may remain.  A slot past the last page is
+ * not written (DASH_ERR_PAGE).
+ * Returns DASH_OK (also for T = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int64_t k_stride_t, int64_t k_stride_h,
+                  const dash_bf16* v, int64_t v_stride_t, int64_t v_stride_h, const int64_t* slots, int T,
+                  const dash_write_rope* rope, dash_stream_t stream);
+
+/*
+ * dash_kv_read -- read the first lens[b] tokens of B sequences back into
+ * contiguous bf16 tensors k, v [B, Hkv, S, D] (e.g. the keys and values of
+ * dash_attn_fwd_cross): value = bf16(code * scale), or the bf16 value itself.
+ * Token j of sequence b is offset j % page_size of page
+ * block_table[b*table_stride + j / page_size] (device int32, max_pages entries
+ * per sequence).  Rows j >= lens[b] are left as they were; so are rows of a
+ * page outside the cache, or past max_pages (DASH_ERR_PAGE).  lens[b] > S
+ * reads S rows.  stride_b/h/s are those of both outputs.
+ * Returns DASH_OK (also for B or S = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t table_stride, int max_pages,
+                 const int32_t* lens, dash_bf16* k, dash_bf16* v, int64_t stride_b, int64_t stride_h,
+                 int64_t stride_s, int B, int S, dash_stream_t stream);
+
+/*
+ * dash_attn_paged -- attention of the newest tokens of B sequences over their
+ * cached keys and values (dash_attn_fwd with the keys in pages, the queries
+ * packed, and the diagonal at the end of the sequence):
+ *   sequence b has len = kv_lens[b] cached tokens, of which the last
+ *   n = cu_q[b+1] - cu_q[b] are its new ones, already written; row
+ *   cu_q[b] + i of q [T, Hq, D] is the token at position p = len - n + i and
+ *   sees the keys j <= p (causal = 1), of them j > p - window when
+ *   window > 0; all len keys when causal = 0 (window must then be 0).
+ *   o[row, h, :] = sum_j P_j v[hk, j, :],  P = softmax_j(<q[row, h], k[hk, j]> / sqrt(D)),
+ *   lse[row, h] = log sum_j exp(...)   (natural log), hk = h / (Hq / Hkv).
+ * A row that sees no key (len = 0, or p < 0) gets o = 0 and lse = -inf.  Rows
+ * from cu_q[B] on are left as they were.  Pages that no new token of a
+ * sequence sees are not looked up (they may be freed), and cells outside its
+ * visible tokens may hold anything; the values of visible tokens are finite.
+ *   q bf16 with strides; o bf16 [T, Hq, D] contiguous; lse fp32 [T, Hq]
+ *   contiguous, or NULL; kv_lens int32 [B]; cu_q int32 [B+1], non-decreasing
+ *   from 0, or NULL: T/B tokens of each sequence; block_table as dash_kv_read.
+ *   max_q: an upper bound on n that the host knows (it selects the kernels);
+ *   Hq / Hkv at most 128.
+ *   workspace: device memory of at least dash_attn_paged_workspace bytes for
+ *   the same B, T, Hq, Hkv, D, max_q and max_kv = max_pages * page_size,
+ *   16-byte aligned, not shared with a call (or a captured graph's replay)
+ *   that may run at the same time; its contents need no set-up and mean
+ *   nothing afterwards.
+ * How a sequence's keys are split over the GPU depends on its own lengths and
+ * on Hq, Hkv and D alone: its outputs are the same bits whatever else is in
+ * the batch, and from run to run.
+ * A page outside the cache, a length past max_pages pages, n > max_q or a
+ * token past T is reported (DASH_ERR_PAGE) and its sequence's outputs are
+ * undefined; no other sequence is affected.
+ * Returns DASH_OK (also for B or T = 0), DASH_ERR_ARG, DASH_ERR_SCRATCH
+ * (workspace too small), DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q_stride_h, const dash_kv_cache* cache,
+                    const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_lens,
+                    const int32_t* cu_q, dash_bf16* o, float* lse, int B, int T, int Hq, int max_q, int causal,
+                    int window, void* workspace, size_t workspace_bytes, dash_stream_t stream);
+
+/* *bytes = the workspace dash_attn_paged needs (0: none).  Host only.  Returns DASH_OK or DASH_ERR_ARG. */
+int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int64_t max_kv, size_t* bytes);
+
+/*
+ * dash_get_status_paged -- synchronizes `stream`, reports the first error that
+ * dash_kv_write, dash_kv_read or dash_attn_paged recorded on the current
+ * device since the last report, on any stream, and clears it: *code = DASH_OK,
+ * DASH_ERR_PAGE or DASH_ERR_TIMEOUT; info[0..3] (may be NULL) = {operator
+ * (1 write, 2 read, 3 attention), sequence or token, value found, its bound}.
+ * Returns DASH_OK, DASH_ERR_ARG (code NULL) or DASH_ERR_CUDA.
+ */
+int dash_get_status_paged(dash_stream_t stream, int* code, int* info);
 
 /* ---------------------------------------------------------------------------
  * Status and configuration

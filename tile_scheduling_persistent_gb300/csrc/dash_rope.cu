@@ -1,0 +1,537 @@
+// dash_rope.cu -- rotary positions and the paged cache's writer and reader
+// (dash_rope, dash_kv_write, dash_kv_read; memory-bound kernels).
+//
+// Angles.  The rotation of pair i at position p is p * f_i radians modulo one
+// turn.  p * f_i in fp32 would be off by p * f_i * 2^-24 (0.06 rad at a
+// million), so the host turns f_i into the 64-bit fraction of a turn
+// F_i = round(f_i / 2pi * 2^64) mod 2^64, and the kernel forms p * F_i mod
+// 2^64: an integer product whose wrap-around is the reduction modulo one turn.
+// Its top 32 bits, as a signed number, are the angle in [-1/2, 1/2) turns; the
+// error is p * 2^-65 turns from F_i (and p * f_i * 2^-53 from the double f_i)
+// plus fp32's rounding of that fraction.  Two integer multiplies replace a
+// 64-bit floating multiply and reduction.
+//
+// Work.  One thread owns 16 values of a vector as two chunks of 8, such that
+// every chunk is one 16-byte access and the threads of a vector read
+// consecutive chunks; for rotated values the chunks are 8j.. and rot/2 + 8j..,
+// which hold both members of 8 pairs in either layout.  A thread forms the 8
+// angles of its (token, chunk) once and uses them for a run of heads.
+#include <math.h>
+
+#include "dash_internal.h"
+#include "dash_serve.cuh"
+
+namespace dash {
+
+namespace {
+
+constexpr int kMaxPairs = 64;   // D / 2 at D = 128
+
+struct Turns {
+    unsigned long long f[kMaxPairs];   // fraction of a turn per position, times 2^64
+    float factor;
+    int rot, interleaved;
+};
+
+// cos and sin (times factor; sin negated for the inverse) of the 8 pairs of chunk j of a vector.
+__device__ __forceinline__ void angles(const Turns& t, int j, long long pos, float sign, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // half layout: pairs 8j + e; interleaved: chunk 8j.. holds pairs 4j..4j+3, chunk rot/2 + 8j.. rot/4 + 4j..
+        const int i = t.interleaved ? (e < 4 ? 4 * j + e : t.rot / 4 + 4 * j + e - 4) : 8 * j + e;
+        const int frac = (int)(((unsigned long long)pos * t.f[i]) >> 32);
+        float s, c;
+        sincospif((float)frac * 0x1p-31f, &s, &c);   // 2 * frac * 2^-32 half turns
+        cs[e] = c * t.factor;
+        sn[e] = s * t.factor * sign;
+    }
+}
+
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&cs)[8], const float (&sn)[8],
+                                       int interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = a[2 * e], y = a[2 * e + 1], u = b[2 * e], w = b[2 * e + 1];
+            a[2 * e] = x * cs[e] - y * sn[e];
+            a[2 * e + 1] = y * cs[e] + x * sn[e];
+            b[2 * e] = u * cs[e + 4] - w * sn[e + 4];
+            b[2 * e + 1] = w * cs[e + 4] + u * sn[e + 4];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = a[e], y = b[e];
+            a[e] = x * cs[e] - y * sn[e];
+            b[e] = y * cs[e] + x * sn[e];
+        }
+    }
+}
+
+// Where the two chunks of thread `unit` (of D / 16) start in a vector.
+__device__ __forceinline__ void chunks(int unit, int rot, int& c0, int& c1) {
+    const int ru = rot / 16;
+    if (unit < ru) {
+        c0 = 8 * unit;
+        c1 = rot / 2 + 8 * unit;
+    } else {
+        c0 = rot + 16 * (unit - ru);
+        c1 = c0 + 8;
+    }
+}
+
+__device__ __forceinline__ void load8(const void* base, bool fp32, long long at, float (&x)[8]) {
+    if (fp32) {
+        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at);
+        const float4 u = p[0], w = p[1];
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+    } else {
+        unpack_bf16(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + at), x);
+    }
+}
+__device__ __forceinline__ void store8(void* base, bool fp32, long long at, const float (&x)[8]) {
+    if (fp32) {
+        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + at);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at) = pack_bf16x8(x);
+    }
+}
+
+// ---------------------------------------------------------------- rope
+struct RopeParams {
+    dash_heads x[2], y[2];
+    const int32_t* positions;
+    long long pos_stride_b;
+    Turns turns;
+    float sign;
+    int B, S, heads;   // heads: of both tensors
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int U = D / 16;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long token = i / U;
+    const int unit = (int)(i % U);
+    if (token >= (long long)p.B * p.S) return;
+    const int b = (int)(token / p.S), s = (int)(token % p.S);
+    const int per = (p.heads + gridDim.y - 1) / gridDim.y;
+    const int h0 = blockIdx.y * per, h1 = min(h0 + per, p.heads);
+    int c0, c1;
+    chunks(unit, p.turns.rot, c0, c1);
+    const bool turned = unit < p.turns.rot / 16;
+    float cs[8], sn[8];
+    if (turned) {
+        const long long pos = p.positions ? p.positions[b * p.pos_stride_b + s] : s;
+        angles(p.turns, unit, pos, p.sign, cs, sn);
+    }
+    for (int h = h0; h < h1; ++h) {
+        const int t = h >= p.x[0].heads;
+        const int hh = t ? h - p.x[0].heads : h;
+        const dash_heads& x = p.x[t];
+        const dash_heads& y = p.y[t];
+        const long long from = b * x.stride_b + hh * x.stride_h + s * x.stride_s;
+        const long long to = b * y.stride_b + hh * y.stride_h + s * y.stride_s;
+        float a[8], c[8];
+        load8(x.data, x.fp32, from + c0, a);
+        load8(x.data, x.fp32, from + c1, c);
+        if (turned) rotate(a, c, cs, sn, p.turns.interleaved);
+        store8(y.data, y.fp32, to + c0, a);
+        store8(y.data, y.fp32, to + c1, c);
+    }
+}
+
+// ---------------------------------------------------------------- cache write
+struct WriteParams {
+    dash_kv_cache c;
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16* q_out;
+    long long k_t, k_h, v_t, v_h, q_t, q_h, qo_t, qo_h;
+    const int64_t* slots;
+    const int32_t* positions;   // null: no rotation
+    Turns turns;
+    int T, Hq;                  // Hq: 0 without queries
+};
+
+// Heads of a token in the order queries, keys, values.  The threads of one
+// vector are U consecutive lanes, whose maximum a butterfly forms.
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ WriteParams p) {
+    constexpr int U = D / 16;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const bool live = i / U < p.T;   // whole vectors: lanes of one vector agree
+    const long long token = live ? i / U : p.T - 1;
+    const int unit = (int)(i % U);
+    const int heads = p.Hq + 2 * p.c.Hkv;
+    const int per = (heads + gridDim.y - 1) / gridDim.y;
+    const int h0 = blockIdx.y * per, h1 = min(h0 + per, heads);
+    const int rot = p.positions ? p.turns.rot : D;
+    int c0, c1;
+    chunks(unit, rot, c0, c1);
+    const bool turned = p.positions && unit < rot / 16;
+    float cs[8], sn[8];
+    if (turned) angles(p.turns, unit, p.positions[token], 1.f, cs, sn);
+
+    const long long slots = (long long)p.c.num_pages * p.c.page_size;
+    long long slot = p.slots[token];
+    if (slot >= slots && live && unit == 0 && blockIdx.y == 0)
+        serve_error(DASH_ERR_PAGE, kOpWrite, token, slot, slots);
+    const bool kept = live && slot >= 0 && slot < slots;
+    if (!kept) slot = 0;
+    const long long page = slot / p.c.page_size;
+    const int off = (int)(slot % p.c.page_size);
+
+    for (int h = h0; h < h1; ++h) {
+        float a[8], b[8];
+        if (h < p.Hq) {
+            const __nv_bfloat16* from = p.q + token * p.q_t + h * p.q_h;
+            load8(from, false, c0, a);
+            load8(from, false, c1, b);
+            if (turned) rotate(a, b, cs, sn, p.turns.interleaved);
+            if (live) {
+                __nv_bfloat16* to = p.q_out + token * p.qo_t + h * p.qo_h;
+                store8(to, false, c0, a);
+                store8(to, false, c1, b);
+            }
+            continue;
+        }
+        const bool val = h >= p.Hq + p.c.Hkv;
+        const int hk = h - p.Hq - (val ? p.c.Hkv : 0);
+        const __nv_bfloat16* from = val ? p.v + token * p.v_t + hk * p.v_h : p.k + token * p.k_t + hk * p.k_h;
+        load8(from, false, c0, a);
+        load8(from, false, c1, b);
+        if (!val && turned) rotate(a, b, cs, sn, p.turns.interleaved);
+        const long long cell = (page * p.c.Hkv + hk) * p.c.page_size + off;
+        void* pages = val ? p.c.v : p.c.k;
+        if (kE4M3) {
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));
+#pragma unroll
+            for (int w = U / 2; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+            const float scale = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f);
+            uint32_t q[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                q[e] = pack_e4m3x4(__fdiv_rn(a[4 * e], scale), __fdiv_rn(a[4 * e + 1], scale),
+                                   __fdiv_rn(a[4 * e + 2], scale), __fdiv_rn(a[4 * e + 3], scale));
+                q[2 + e] = pack_e4m3x4(__fdiv_rn(b[4 * e], scale), __fdiv_rn(b[4 * e + 1], scale),
+                                       __fdiv_rn(b[4 * e + 2], scale), __fdiv_rn(b[4 * e + 3], scale));
+            }
+            if (kept) {
+                uint8_t* to = reinterpret_cast<uint8_t*>(pages) + cell * D;
+                *reinterpret_cast<uint2*>(to + c0) = make_uint2(q[0], q[1]);
+                *reinterpret_cast<uint2*>(to + c1) = make_uint2(q[2], q[3]);
+                if (unit == 0) (val ? p.c.v_scale : p.c.k_scale)[cell] = scale;
+            }
+        } else if (kept) {
+            store8(pages, false, cell * D + c0, a);
+            store8(pages, false, cell * D + c1, b);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- cache read
+struct ReadParams {
+    dash_kv_cache c;
+    const int32_t* table;
+    long long table_stride, stride_b, stride_h, stride_s;
+    const int32_t* lens;
+    __nv_bfloat16 *k, *v;
+    int max_pages, B, S;
+};
+
+// One thread per 8 values of a token's key and value vector; blockIdx.y is the head, blockIdx.z the sequence.
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
+    constexpr int C = D / 8;
+    for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
+        const long long cap = (long long)p.max_pages * p.c.page_size;
+        long long len = p.lens[b];
+        if (len > cap || len < 0) {
+            if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+                serve_error(DASH_ERR_PAGE, kOpRead, b, len, cap);
+            len = len < 0 ? 0 : cap;
+        }
+        if (len > p.S) len = p.S;
+        for (int h = blockIdx.y; h < p.c.Hkv; h += gridDim.y)
+            for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < len * C; i += (long long)gridDim.x * 256) {
+                const long long j = i / C;
+                const int d = 8 * (int)(i % C);
+                const int page = p.table[b * p.table_stride + j / p.c.page_size];
+                if (page < 0 || page >= p.c.num_pages) {
+                    serve_error(DASH_ERR_PAGE, kOpRead, b, page, p.c.num_pages);
+                    continue;
+                }
+                const long long cell = ((long long)page * p.c.Hkv + h) * p.c.page_size + j % p.c.page_size;
+                const long long to = b * p.stride_b + h * p.stride_h + j * p.stride_s + d;
+                if (kE4M3) {
+                    float x[8];
+                    unpack_e4m3x8(*reinterpret_cast<const uint2*>((const uint8_t*)p.c.k + cell * D + d), x);
+                    const float ks = p.c.k_scale[cell], vs = p.c.v_scale[cell];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= ks;
+                    *reinterpret_cast<uint4*>(p.k + to) = pack_bf16x8(x);
+                    unpack_e4m3x8(*reinterpret_cast<const uint2*>((const uint8_t*)p.c.v + cell * D + d), x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= vs;
+                    *reinterpret_cast<uint4*>(p.v + to) = pack_bf16x8(x);
+                } else {
+                    *reinterpret_cast<uint4*>(p.k + to) =
+                        *reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.c.k + cell * D + d);
+                    *reinterpret_cast<uint4*>(p.v + to) =
+                        *reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.c.v + cell * D + d);
+                }
+            }
+    }
+}
+
+// ---------------------------------------------------------------- host
+// inv_freq as 64-bit fractions of a turn; false when one is not finite.
+bool make_turns(Turns* t, const double* inv_freq, int rot, int interleaved, float factor) {
+    const double inv2pi = 0.15915494309189533577;   // 1 / (2 pi)
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = inv_freq[i];
+        if (!(fabs(f) < 1e12)) return false;
+        const double turns = f * inv2pi;
+        double frac = turns - floor(turns);   // [0, 1], exact up to the product's rounding
+        // two 32-bit halves: each step is exact in a double
+        const double hi = floor(frac * 4294967296.0);
+        const double lo = floor((frac * 4294967296.0 - hi) * 4294967296.0);
+        t->f[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
+    }
+    t->rot = rot;
+    t->interleaved = interleaved;
+    t->factor = factor;
+    return true;
+}
+
+bool rope_args_ok(const double* inv_freq, int rot, int interleaved, float factor, int D) {
+    return inv_freq && (D == 64 || D == 128) && rot >= 16 && rot <= D && rot % 16 == 0 &&
+           (interleaved == 0 || interleaved == 1) && isfinite(factor);
+}
+
+// Written vectors: none may be another (a stride of 0 over more than one).
+bool distinct(int64_t a, int64_t na, int64_t b, int64_t nb, int64_t c, int64_t nc) {
+    return (na <= 1 || a > 0) && (nb <= 1 || b > 0) && (nc <= 1 || c > 0);
+}
+
+bool heads_ok(const dash_heads* t) {
+    return serve_aligned(t->data) && (t->fp32 == 0 || t->fp32 == 1) && t->heads > 0 &&
+           serve_strides(t->stride_b, t->stride_h) && serve_strides(t->stride_s, 0);
+}
+
+// Blocks along the heads: enough for two thousand blocks, a divisor-like split of the heads' loop.
+int head_groups(long long blocks, int heads) {
+    long long g = (2048 + blocks - 1) / blocks;
+    if (g > heads) g = heads;
+    const int per = (int)((heads + g - 1) / g);
+    return (heads + per - 1) / per;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA; }
+
+}  // namespace
+
+int serve_check_device() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return DASH_ERR_CUDA;
+    return (major == 10 && minor == 3) ? DASH_OK : DASH_ERR_DEVICE;
+}
+
+int take_error_rope(int* out5) { return take_serve_error(out5); }
+
+}  // namespace dash
+
+using namespace dash;
+
+extern "C" int dash_rope(const dash_heads* x, const dash_heads* y, const dash_heads* x2, const dash_heads* y2,
+                         const int32_t* positions, int64_t pos_stride_b, const double* inv_freq, int rot,
+                         int interleaved, float factor, int inverse, int B, int S, int D, dash_stream_t stream) {
+    if (!x || !y || !x2 != !y2) return DASH_ERR_ARG;
+    if (B < 0 || S < 0 || !rope_args_ok(inv_freq, rot, interleaved, factor, D) || (inverse != 0 && inverse != 1) ||
+        pos_stride_b < 0)
+        return DASH_ERR_ARG;
+    if (B == 0 || S == 0) return DASH_OK;
+    RopeParams prm;
+    for (int t = 0; t < (x2 ? 2 : 1); ++t) {
+        const dash_heads* a = t ? x2 : x;
+        const dash_heads* c = t ? y2 : y;
+        if (!heads_ok(a) || !heads_ok(c) || a->heads != c->heads ||
+            !distinct(c->stride_b, B, c->stride_h, c->heads, c->stride_s, S))
+            return DASH_ERR_ARG;
+        if (a->data == c->data && (a->fp32 != c->fp32 || a->stride_b != c->stride_b || a->stride_h != c->stride_h ||
+                                   a->stride_s != c->stride_s))
+            return DASH_ERR_ARG;
+        prm.x[t] = *a;
+        prm.y[t] = *c;
+    }
+    prm.heads = x->heads + (x2 ? x2->heads : 0);
+    if ((long long)B * S * (D / 16) > (1ll << 31) * 255 || prm.heads > 65535) return DASH_ERR_ARG;
+    if (!make_turns(&prm.turns, inv_freq, rot, interleaved, factor)) return DASH_ERR_ARG;
+    const int rc = serve_check_device();
+    if (rc) return rc;
+    prm.positions = positions;
+    prm.pos_stride_b = pos_stride_b;
+    prm.sign = inverse ? -1.f : 1.f;
+    prm.B = B;
+    prm.S = S;
+    const long long blocks = ((long long)B * S * (D / 16) + 255) / 256;
+    const dim3 grid((unsigned)blocks, (unsigned)head_groups(blocks, prm.heads));
+    if (D == 64)
+        rope_kernel<64><<<grid, 256, 0, (cudaStream_t)stream>>>(prm);
+    else
+        rope_kernel<128><<<grid, 256, 0, (cudaStream_t)stream>>>(prm);
+    return launched();
+}
+
+extern "C" int dash_rope_freqs(int rot, double base, int scaling, double scale, int trained, double lo, double hi,
+                               double* inv_freq, float* factor) {
+    if (!inv_freq || !factor || rot < 4 || rot % 2 || !(base > 1.0) || !(scale >= 1.0) || !isfinite(base) ||
+        !isfinite(scale) || scaling < DASH_ROPE_PLAIN || scaling > DASH_ROPE_RAMP)
+        return DASH_ERR_ARG;
+    const bool bands = scaling == DASH_ROPE_WAVE || scaling == DASH_ROPE_RAMP;
+    if (bands && (trained < 1 || !(lo > 0.0) || !(hi > lo) || !isfinite(hi))) return DASH_ERR_ARG;
+    const double two_pi = 6.28318530717958647693;
+    if (scaling == DASH_ROPE_BASE) base *= pow(scale, (double)rot / (rot - 2));
+    double first = 0, last = 0;
+    if (scaling == DASH_ROPE_RAMP) {   // the pair indexes that make hi and lo turns over the trained length
+        first = floor(rot * log(trained / (hi * two_pi)) / (2.0 * log(base)));
+        last = ceil(rot * log(trained / (lo * two_pi)) / (2.0 * log(base)));
+        first = first < 0 ? 0 : first;
+        last = last > rot - 1 ? rot - 1 : last;
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = pow(base, -2.0 * i / rot);
+        double keep = 1.0;   // share of the unscaled frequency
+        if (scaling == DASH_ROPE_LINEAR) keep = 0.0;
+        if (scaling == DASH_ROPE_WAVE) keep = (trained * f / two_pi - lo) / (hi - lo);
+        if (scaling == DASH_ROPE_RAMP) keep = 1.0 - (i - first) / (last - first > 1e-3 ? last - first : 1e-3);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        inv_freq[i] = scaling == DASH_ROPE_BASE ? f : f * (keep + (1.0 - keep) / scale);
+    }
+    *factor = (scaling == DASH_ROPE_RAMP && scale > 1.0) ? (float)(0.1 * log(scale) + 1.0) : 1.f;
+    return DASH_OK;
+}
+
+extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int64_t k_stride_t, int64_t k_stride_h,
+                             const dash_bf16* v, int64_t v_stride_t, int64_t v_stride_h, const int64_t* slots, int T,
+                             const dash_write_rope* rope, dash_stream_t stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (T < 0 || !serve_strides(k_stride_t, k_stride_h) || !serve_strides(v_stride_t, v_stride_h)) return DASH_ERR_ARG;
+    if (rope && !rope_args_ok(rope->inv_freq, rope->rot, rope->interleaved, rope->factor, cache->D)) return DASH_ERR_ARG;
+    if (T == 0) return DASH_OK;
+    if (!serve_aligned(k) || !serve_aligned(v) || !slots || ((uintptr_t)slots & 7u)) return DASH_ERR_ARG;
+    WriteParams prm;
+    prm.c = *cache;
+    prm.k = (const __nv_bfloat16*)k;
+    prm.v = (const __nv_bfloat16*)v;
+    prm.k_t = k_stride_t;
+    prm.k_h = k_stride_h;
+    prm.v_t = v_stride_t;
+    prm.v_h = v_stride_h;
+    prm.slots = slots;
+    prm.positions = nullptr;
+    prm.q = nullptr;
+    prm.q_out = nullptr;
+    prm.Hq = 0;
+    prm.T = T;
+    prm.turns.interleaved = 0;
+    if (rope) {
+        if (!rope->positions || ((uintptr_t)rope->positions & 3u)) return DASH_ERR_ARG;
+        if (!make_turns(&prm.turns, rope->inv_freq, rope->rot, rope->interleaved, rope->factor)) return DASH_ERR_ARG;
+        prm.positions = rope->positions;
+        if (rope->q) {
+            if (!serve_aligned(rope->q) || !serve_aligned(rope->q_out) || rope->Hq <= 0 ||
+                !serve_strides(rope->q_stride_t, rope->q_stride_h) ||
+                !serve_strides(rope->q_out_stride_t, rope->q_out_stride_h) ||
+                !distinct(rope->q_out_stride_t, T, rope->q_out_stride_h, rope->Hq, 0, 1))
+                return DASH_ERR_ARG;
+            if (rope->q == rope->q_out &&
+                (rope->q_stride_t != rope->q_out_stride_t || rope->q_stride_h != rope->q_out_stride_h))
+                return DASH_ERR_ARG;
+            prm.q = (const __nv_bfloat16*)rope->q;
+            prm.q_out = (__nv_bfloat16*)rope->q_out;
+            prm.q_t = rope->q_stride_t;
+            prm.q_h = rope->q_stride_h;
+            prm.qo_t = rope->q_out_stride_t;
+            prm.qo_h = rope->q_out_stride_h;
+            prm.Hq = rope->Hq;
+        }
+    }
+    if ((long long)prm.Hq + 2ll * cache->Hkv > 65535) return DASH_ERR_ARG;
+    if ((rc = serve_check_device())) return rc;
+    const int D = cache->D;
+    const long long blocks = ((long long)T * (D / 16) + 255) / 256;
+    const dim3 grid((unsigned)blocks, (unsigned)head_groups(blocks, prm.Hq + 2 * cache->Hkv));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cache->type == DASH_CACHE_E4M3) {
+        if (D == 64) write_kernel<64, true><<<grid, 256, 0, s>>>(prm);
+        else write_kernel<128, true><<<grid, 256, 0, s>>>(prm);
+    } else {
+        if (D == 64) write_kernel<64, false><<<grid, 256, 0, s>>>(prm);
+        else write_kernel<128, false><<<grid, 256, 0, s>>>(prm);
+    }
+    return launched();
+}
+
+extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t table_stride,
+                            int max_pages, const int32_t* lens, dash_bf16* k, dash_bf16* v, int64_t stride_b,
+                            int64_t stride_h, int64_t stride_s, int B, int S, dash_stream_t stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (B < 0 || S < 0 || max_pages < 0 || table_stride < 0 || !serve_strides(stride_b, stride_h) ||
+        !serve_strides(stride_s, 0))
+        return DASH_ERR_ARG;
+    if (B == 0 || S == 0) return DASH_OK;
+    if (!serve_aligned(k) || !serve_aligned(v) || !lens || ((uintptr_t)lens & 3u) || ((uintptr_t)block_table & 3u) ||
+        (max_pages > 0 && !block_table) || !distinct(stride_b, B, stride_h, cache->Hkv, stride_s, S))
+        return DASH_ERR_ARG;
+    if ((rc = serve_check_device())) return rc;
+    ReadParams prm;
+    prm.c = *cache;
+    prm.table = block_table;
+    prm.table_stride = table_stride;
+    prm.stride_b = stride_b;
+    prm.stride_h = stride_h;
+    prm.stride_s = stride_s;
+    prm.lens = lens;
+    prm.k = (__nv_bfloat16*)k;
+    prm.v = (__nv_bfloat16*)v;
+    prm.max_pages = max_pages;
+    prm.B = B;
+    prm.S = S;
+    const int D = cache->D;
+    long long x = ((long long)S * (D / 8) + 255) / 256;
+    const dim3 grid((unsigned)(x < 4096 ? x : 4096), (unsigned)(cache->Hkv < 65535 ? cache->Hkv : 65535),
+                    (unsigned)(B < 65535 ? B : 65535));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (cache->type == DASH_CACHE_E4M3) {
+        if (D == 64) read_kernel<64, true><<<grid, 256, 0, s>>>(prm);
+        else read_kernel<128, true><<<grid, 256, 0, s>>>(prm);
+    } else {
+        if (D == 64) read_kernel<64, false><<<grid, 256, 0, s>>>(prm);
+        else read_kernel<128, false><<<grid, 256, 0, s>>>(prm);
+    }
+    return launched();
+}
+
+extern "C" int dash_get_status_paged(dash_stream_t stream, int* code, int* info) {
+    if (!code) return DASH_ERR_ARG;
+    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return DASH_ERR_CUDA;
+    int a[5], b[5];
+    int rc = take_error_rope(a);
+    if (rc == DASH_OK) rc = take_error_paged(b);
+    if (rc) return rc;
+    const int* e = a[0] ? a : b;   // one record per translation unit; the writer's and reader's first
+    *code = e[0];
+    if (info)
+        for (int i = 0; i < 4; ++i) info[i] = e[1 + i];
+    return DASH_OK;
+}

@@ -18,9 +18,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdash.so")
 
 OK, ERR_ARG, ERR_CUDA, ERR_LAUNCH, ERR_TIMEOUT, ERR_DEADLOCK, ERR_NOMEM, ERR_DEVICE = 0, -1, -2, -3, -4, -5, -6, -7
-ERR_SCRATCH = -8
+ERR_SCRATCH, ERR_PAGE = -8, -9
 _NAMES = {0: "DASH_OK", -1: "DASH_ERR_ARG", -2: "DASH_ERR_CUDA", -3: "DASH_ERR_LAUNCH", -4: "DASH_ERR_TIMEOUT",
-          -5: "DASH_ERR_DEADLOCK", -6: "DASH_ERR_NOMEM", -7: "DASH_ERR_DEVICE", -8: "DASH_ERR_SCRATCH"}
+          -5: "DASH_ERR_DEADLOCK", -6: "DASH_ERR_NOMEM", -7: "DASH_ERR_DEVICE", -8: "DASH_ERR_SCRATCH",
+          -9: "DASH_ERR_PAGE"}
 
 EXPORTS = (
     "dash_attn_bwd_preprocess", "dash_attn_bwd", "dash_dq_finalize", "dash_get_status", "dash_set_timeout_ns",
@@ -29,6 +30,8 @@ EXPORTS = (
     "dash_attn_fwd", "dash_sim_schedule_band", "dash_attn_bwd_window", "dash_attn_fwd_window",
     "dash_sim_schedule_cross", "dash_attn_bwd_cross", "dash_attn_fwd_cross", "dash_head_split", "dash_key_blocks",
     "dash_noalloc_init", "dash_get_status_noalloc",
+    "dash_rope", "dash_rope_freqs", "dash_kv_write", "dash_kv_read", "dash_attn_paged", "dash_attn_paged_workspace",
+    "dash_get_status_paged",
 )
 
 
@@ -45,6 +48,24 @@ class _DebugOpts(ctypes.Structure):
                 ("kernel_event_end", ctypes.c_void_p), ("wait_cycles", ctypes.c_void_p),
                 ("event_trace", ctypes.c_void_p), ("window", ctypes.c_int), ("skv", ctypes.c_int),
                 ("head_split", ctypes.c_int)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("fp32", ctypes.c_int), ("heads", ctypes.c_int),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class _WriteRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("factor", ctypes.c_float), ("q", ctypes.c_void_p),
+                ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride_t", ctypes.c_int64), ("q_out_stride_h", ctypes.c_int64), ("Hq", ctypes.c_int)]
 
 
 _lib = None
@@ -75,6 +96,14 @@ def lib():
     L.dash_sim_schedule_cross.argtypes = [I] * 7 + [D, D, ctypes.POINTER(D), P, ctypes.POINTER(ctypes.c_int64)]
     L.dash_sim_check_ranks.argtypes = [I] * 7 + [P]
     L.dash_debug_tile_probe.argtypes = [P] * 6 + [I, I] + [P] * 7
+    L64, HP = ctypes.c_int64, ctypes.POINTER(_Heads)
+    L.dash_rope.argtypes = [HP, HP, HP, HP, P, L64, P, I, I, ctypes.c_float, I, I, I, I, P]
+    L.dash_rope_freqs.argtypes = [I, D, I, D, I, D, D, P, ctypes.POINTER(ctypes.c_float)]
+    L.dash_kv_write.argtypes = [ctypes.POINTER(_Cache), P, L64, L64, P, L64, L64, P, I, ctypes.POINTER(_WriteRope), P]
+    L.dash_kv_read.argtypes = [ctypes.POINTER(_Cache), P, L64, I, P, P, P, L64, L64, L64, I, I, P]
+    L.dash_attn_paged.argtypes = [P, L64, L64, ctypes.POINTER(_Cache), P, L64, I, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+    L.dash_attn_paged_workspace.argtypes = [I, I, I, I, I, I, L64, ctypes.POINTER(Z)]
+    L.dash_get_status_paged.argtypes = [P, ctypes.POINTER(I), ctypes.POINTER(I)]
     for name in EXPORTS:
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -311,3 +340,220 @@ def tile_probe(k, v, q, do, lse, delta, diag=False):
                                        *[_ptr(out[n]) for n in ("sT", "pT", "dpT", "dsT", "dv", "dk", "dq")]),
            "dash_debug_tile_probe")
     return out
+
+
+# ------------------------------------------------------------------ rotary positions, paged cache, paged attention
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wave": 3, "ramp": 4}
+
+
+def _need(ok, what, why):
+    """Arguments that the C entry cannot see (tensor shapes, types, devices)."""
+    if not ok:
+        err = DashError(ERR_ARG, what)
+        err.args = (err.args[0] + ": " + why,)
+        raise err
+
+
+def _data(t, dtype, what, name, shape=None):
+    """The address of a CUDA tensor of the current device, contiguous in its last dimension."""
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _need(False, what, "%s is a %s tensor on the current CUDA device" % (name, dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        _need(False, what, "%s has shape %s" % (name, shape))
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        _need(False, what, "%s is contiguous in its last dimension" % name)
+    return t.data_ptr()
+
+
+def _flat(t, dtype, what, name, shape=None):
+    """_data of a contiguous tensor."""
+    p = _data(t, dtype, what, name, shape)
+    if not t.is_contiguous():
+        _need(False, what, "%s is contiguous" % name)
+    return p
+
+
+def _heads(t, what, name):
+    """dash_heads of a [B, H, S, D] tensor."""
+    fp32 = t.dtype is torch.float32
+    p = _data(t, torch.float32 if fp32 else torch.bfloat16, what, name)
+    _need(t.dim() == 4, what, "%s is [B, H, S, D]" % name)
+    sb, sh, ss, _ = t.stride()
+    B, H, S, _ = t.shape
+    return _Heads(p, fp32, H, sb if B > 1 else 0, sh if H > 1 else 0, ss if S > 1 else 0)
+
+
+def _cache(k, v, k_scale, v_scale, what):
+    _need(k.dim() == 4, what, "the cache is [num_pages, Hkv, page_size, D]")
+    N, H, page, D = shape = tuple(k.shape)
+    if k.dtype is torch.bfloat16:
+        _need(k_scale is None and v_scale is None, what, "a bf16 cache has no scales")
+        return _Cache(_flat(k, k.dtype, what, "k_cache"), _flat(v, k.dtype, what, "v_cache", shape), None, None, 0,
+                      N, page, H, D)
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    _need(k_scale is not None and v_scale is not None, what, "an e4m3 cache has k_scale and v_scale")
+    return _Cache(_flat(k, e4m3, what, "k_cache"), _flat(v, e4m3, what, "v_cache", shape),
+                  _flat(k_scale, f32, what, "k_scale", shape[:3]), _flat(v_scale, f32, what, "v_scale", shape[:3]), 1,
+                  N, page, H, D)
+
+
+def _freqs(inv_freq, what):
+    if isinstance(inv_freq, torch.Tensor):
+        _need(not inv_freq.is_cuda and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
+              and inv_freq.is_contiguous(), what, "inv_freq is a float64 vector on the host")
+        return inv_freq, inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    a = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    _need(a.ndim == 1, what, "inv_freq is a float64 vector on the host")
+    return a, a.ctypes.data, 2 * a.shape[0]
+
+
+def rope_freqs(rot, base=10000.0, scaling="none", scale=1.0, trained=0, lo=1.0, hi=4.0):
+    """(inv_freq, factor): the float64 radians per position of the rot/2 pairs of
+    a rotary embedding, and the factor that goes with its long-context scaling
+    ("none", "linear", "base", "wave", "ramp"; see dash_rope_freqs)."""
+    out = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    factor = ctypes.c_float(1.0)
+    _check(lib().dash_rope_freqs(int(rot), float(base), ROPE_SCALINGS[scaling], float(scale), int(trained), float(lo),
+                                 float(hi), out.data_ptr(), ctypes.byref(factor)), "dash_rope_freqs")
+    return out, factor.value
+
+
+def rope(x, y, inv_freq, positions=None, x2=None, y2=None, interleaved=False, factor=1.0, inverse=False, stream=None):
+    """y <- rotary positions of x [B, H, S, D] (bf16 or fp32, any strides but the
+    last), and y2 of x2 with the same positions: int32 [S], [B, S] or None (0, 1, ...).
+    inv_freq: float64 [rot/2] on the host (rope_freqs); inverse=True is the
+    backward (y = dL/dx for x = dL/dy).  y may be x."""
+    what = "dash_rope"
+    keep, freqs, rot = _freqs(inv_freq, what)
+    a, b = _heads(x, what, "x"), _heads(y, what, "y")
+    _need(x.shape == y.shape, what, "y has the shape of x")
+    B, _, S, D = x.shape
+    a2 = b2 = None
+    if x2 is not None:
+        _need(y2 is not None and x2.shape == y2.shape and x2.dim() == 4 and x2.shape[0] == B
+              and x2.shape[2:] == x.shape[2:], what, "x2 and y2 are [B, H2, S, D]")
+        a2, b2 = ctypes.byref(_heads(x2, what, "x2")), ctypes.byref(_heads(y2, what, "y2"))
+    else:
+        _need(y2 is None, what, "y2 needs x2")
+    pos, pos_b = None, 0
+    if positions is not None:
+        pos = _data(positions, torch.int32, what, "positions")
+        _need(tuple(positions.shape) in ((S,), (B, S)), what, "positions is [S] or [B, S]")
+        pos_b = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    _check(lib().dash_rope(ctypes.byref(a), ctypes.byref(b), a2, b2, pos, pos_b, freqs, rot, int(bool(interleaved)),
+                           float(factor), int(bool(inverse)), B, S, D, _stream(stream)), what)
+
+
+def _token_strides(t):
+    """Strides of tokens and heads; those of a single one do not matter."""
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq=None, positions=None,
+             interleaved=False, factor=1.0, q=None, q_out=None, stream=None):
+    """Write new tokens' k, v [T, Hkv, D] (bf16, any token and head strides) into
+    the pages [num_pages, Hkv, page_size, D] at slots int64 [T] (page * page_size +
+    offset; negative: skipped); an e4m3 cache (torch.float8_e4m3fn) quantises each
+    vector with its own scale.  inv_freq and positions int32 [T]: k is rotated on
+    the way (see rope), and q [T, Hq, D] into q_out."""
+    what = "dash_kv_write"
+    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
+    bf = torch.bfloat16
+    T, shape = k.shape[0], (k.shape[0], c.Hkv, c.D)
+    kp, vp = _data(k, bf, what, "k", shape), _data(v, bf, what, "v", shape)
+    sp = _flat(slots, torch.int64, what, "slots", (T,))
+    r = keep = None
+    if inv_freq is not None:
+        _need(positions is not None, what, "a rotation needs positions")
+        keep, freqs, rot = _freqs(inv_freq, what)
+        r = _WriteRope(freqs, _flat(positions, torch.int32, what, "positions", (T,)), rot, int(bool(interleaved)),
+                       float(factor))
+        if q is not None:
+            _need(q_out is not None and q.dim() == 3 and q.shape[0] == T and q.shape[2] == c.D, what,
+                  "q and q_out are [T, Hq, D]")
+            r.q, r.q_out = _data(q, bf, what, "q"), _data(q_out, bf, what, "q_out", tuple(q.shape))
+            (r.q_stride_t, r.q_stride_h), r.Hq = _token_strides(q), q.shape[1]
+            r.q_out_stride_t, r.q_out_stride_h = _token_strides(q_out)
+    _need(r is not None or (q is None and positions is None), what, "q and positions need inv_freq")
+    _need(q_out is None or q is not None, what, "q_out needs q")
+    kt, kh = _token_strides(k)
+    vt, vh = _token_strides(v)
+    _check(lib().dash_kv_write(ctypes.byref(c), kp, kt, kh, vp, vt, vh, sp, T, ctypes.byref(r) if r else None,
+                               _stream(stream)), what)
+
+
+def _table(block_table, B, what):
+    p = _data(block_table, torch.int32, what, "block_table")
+    _need(block_table.dim() == 2 and block_table.shape[0] == B, what, "block_table is [B, pages]")
+    return p, (block_table.stride(0) if B > 1 else 0), block_table.shape[1]
+
+
+def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None):
+    """k, v [B, Hkv, S, D] (bf16, equal strides) <- the first lens[b] cached tokens of
+    each sequence; rows past lens[b] are left as they were.  block_table int32
+    [B, pages], lens int32 [B]."""
+    what = "dash_kv_read"
+    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
+    _need(k.dim() == 4 and k.shape[1] == c.Hkv and k.shape[3] == c.D, what, "k and v are [B, Hkv, S, D]")
+    B, _, S, _ = k.shape
+    tp, ts, pages = _table(block_table, B, what)
+    kp, vp = _data(k, torch.bfloat16, what, "k"), _data(v, torch.bfloat16, what, "v", tuple(k.shape))
+    a, b = _heads(k, what, "k"), _heads(v, what, "v")
+    _need((a.stride_b, a.stride_h, a.stride_s) == (b.stride_b, b.stride_h, b.stride_s), what, "k and v have equal strides")
+    _check(lib().dash_kv_read(ctypes.byref(c), tp, ts, pages, _flat(lens, torch.int32, what, "lens", (B,)), kp, vp,
+                              a.stride_b, a.stride_h, a.stride_s, B, S, _stream(stream)), what)
+
+
+def attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv):
+    """Bytes of workspace attn_paged needs; max_kv = pages per sequence * page_size."""
+    out = ctypes.c_size_t(0)
+    _check(lib().dash_attn_paged_workspace(int(B), int(T), int(Hq), int(Hkv), int(D), int(max_q), int(max_kv),
+                                           ctypes.byref(out)), "dash_attn_paged_workspace")
+    return out.value
+
+
+def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=None, lse=None, causal=True, window=None,
+               k_scale=None, v_scale=None, workspace=None, stream=None):
+    """o [T, Hq, D] (and lse fp32 [T, Hq]) <- attention of each sequence's newest
+    tokens q [T, Hq, D] over its kv_lens[b] cached tokens, the new ones among them
+    (see dash_attn_paged).  cu_q int32 [B+1] are the sequences' first rows (None:
+    T / B rows each) and max_q bounds their new tokens (None: T with cu_q, else
+    T / B).  workspace: uint8 tensor of attn_paged_workspace bytes (None: taken
+    from torch's allocator for this call)."""
+    what = "dash_attn_paged"
+    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
+    bf = torch.bfloat16
+    qp = _data(q, bf, what, "q")
+    _need(q.dim() == 3 and q.shape[2] == c.D, what, "q is [T, Hq, D]")
+    T, Hq, _ = q.shape
+    op = _flat(o, bf, what, "o", (T, Hq, c.D))
+    lp = _flat(lse, torch.float32, what, "lse", (T, Hq)) if lse is not None else None
+    B = kv_lens.shape[0]
+    tp, ts, pages = _table(block_table, B, what)
+    np_ = _flat(kv_lens, torch.int32, what, "kv_lens", (B,))
+    cp = _flat(cu_q, torch.int32, what, "cu_q", (B + 1,)) if cu_q is not None else None
+    if max_q is None:
+        max_q = T if cu_q is not None or B == 0 else T // B
+    _need(causal or window is None, what, "a sliding window needs a causal mask")
+    _need(window is None or window >= 1, what, "a window has at least one token")
+    if workspace is None:
+        need = attn_paged_workspace(B, T, Hq, c.Hkv, c.D, max_q, pages * c.page_size)
+        if need:
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            else:
+                with torch.cuda.stream(stream):   # the allocator's reuse then follows this stream
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    wp, wn = (_flat(workspace, torch.uint8, what, "workspace"), workspace.numel()) if workspace is not None else (None, 0)
+    qt, qh = _token_strides(q)
+    _check(lib().dash_attn_paged(qp, qt, qh, ctypes.byref(c), tp, ts, pages, np_, cp, op, lp, B, T, Hq, int(max_q),
+                                 int(bool(causal)), int(window or 0), wp, wn, _stream(stream)), what)
+
+
+def get_status_paged(stream=None):
+    """(code, info) of the first error that kv_write, kv_read or attn_paged recorded
+    on the current device since the last report; synchronizes `stream`."""
+    code = ctypes.c_int(0)
+    info = (ctypes.c_int * 4)()
+    _check(lib().dash_get_status_paged(_stream(stream), ctypes.byref(code), info), "dash_get_status_paged")
+    return code.value, list(info)
