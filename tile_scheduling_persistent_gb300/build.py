@@ -21,7 +21,7 @@ OUT = os.path.join(PKG, "libdash.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CUDA_SOURCES = ["dash_bwd.cu", "dash_fwd.cu", "dash_aux.cu", "dash_probe.cu", "dash_api.cu", "dash_noalloc.cu",
-                "dash_rope.cu", "dash_paged.cu"]
+                "dash_rope.cu", "dash_paged.cu", "dash_paged_tile.cu"]
 CXX_SOURCES = ["dash_sim.cpp"]
 
 

@@ -422,6 +422,22 @@ int make_tmap_2d(void* map_out, const void* base, long long rows, int D) {
     return encode_2d(map_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, D, 64);
 }
 
+int make_tmap_pages(void* map_out, const void* base, long long heads, int page, int D, bool e4m3, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return -2;
+    const cuuint64_t row = (cuuint64_t)D * (e4m3 ? 1 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {row, row * page};
+    const cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? D : 64), (cuuint32_t)rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(reinterpret_cast<CUtensorMap*>(map_out),
+                    e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    (e4m3 && D == 64) ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : -2;
+}
+
 // fp32 [rows, D], boxes of 32 columns x 128 rows (128 B rows, swizzled).
 int make_tmap_2d_f32(void* map_out, const void* base, long long rows, int D) {
     return encode_2d(map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, D, 32);

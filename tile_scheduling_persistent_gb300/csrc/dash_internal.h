@@ -49,6 +49,10 @@ unsigned long long timeout_ns();
 // Tensor maps (dash_api.cu).
 int make_tmap_2d(void* map_out, const void* base, long long rows, int D);
 int make_tmap_3d(void* map_out, const void* base, long long heads, int S, int D);
+// Cache pages [heads][page][D] (heads: pages times key/value heads), bf16 in
+// boxes of 64 columns, e4m3 in boxes of D columns (swizzled rows of 128 or 64
+// bytes), `rows` rows high.
+int make_tmap_pages(void* map_out, const void* base, long long heads, int page, int D, bool e4m3, int rows);
 int make_tmap_2d_f32(void* map_out, const void* base, long long rows, int D);
 
 }  // namespace dash

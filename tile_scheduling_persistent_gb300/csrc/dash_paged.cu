@@ -1,113 +1,763 @@
 // dash_paged.cu -- attention of the newest tokens of each sequence over its
-// paged key/value cache (dash_attn_paged).
+// paged key/value cache (dash_attn_paged): the entry points, the kernel for
+// sequences with few rows, and the kernel that joins key ranges.
 //
-// One warp per (token, query head), its keys one after another with a running
-// maximum m and sum l of the softmax:
-//   m' = max(m, s),  l = l 2^(m - m') + 2^(s - m'),  o = o 2^(m - m') + 2^(s - m') v
-// (scores in units of log2), o / l at the end.
+// Few rows (n * G <= 16: decoding, a drafted token or two).  The work is
+// reading the cache once: 4 n G D operations against 2 * 2 D bytes per key and
+// head is at most 16 operations per byte, where the GPU has 285 per byte of
+// memory bandwidth.  So everything serves the stream of pages:
+//   - one persistent CTA per SM; a producer warp walks the CTA's items and
+//     keeps a ring of 64-key stages (K and V, 128 to 160 KB) full by TMA, across item
+//     boundaries, each lane issuing one of a stage's copies (one per page,
+//     64-value column and K/V: pages of 16 tokens give 16 copies);
+//   - eight consumer warps; the stages alternate between two groups of four,
+//     each warp taking 16 keys of a stage: S = Q K^T (m16n8k16, 16 rows are the
+//     instruction's least), a running maximum and sum per row, O += P V, all in
+//     registers; 16-row products at 16 keys each use under a fifth of the
+//     matrix rate that mma.sync has, so the wider tcgen05 tiles (128 rows, of
+//     which 4 would be real) have nothing to add here;
+//   - at the end of an item the eight warps' (O, m, l) are joined in shared
+//     memory in a fixed order while the ring refills.
+//
+// e4m3 caches.  Codes become fp16 pairs in registers (exact: e4m3 has 3
+// fraction bits and exponents -9..8), so the products run in fp16: Q is scaled
+// by a power of two per row so that its largest value lies in [2^14, 2^15) --
+// values down to 2^-29 of it keep bf16's 8 bits -- and the scale returns in
+// fp32 with the key's own scale: s = (Q 2^a . code) * ks * 2^-a.  The value's
+// scale vs joins the weight before it is rounded: w = 2^(s + log2 vs - m'),
+// with m' the running maximum of s + log2 vs, so the largest contributions of
+// a row lie near 1 whatever the scales; the sum l keeps its own maximum m.
+//
+// Masked keys get s = -inf by a select, never by arithmetic, and value rows
+// outside the visible keys (stale or unwritten cells, freed pages) are zeroed
+// in shared memory before they meet a zero weight.
 #include <math.h>
+#include <string.h>
 
 #include "dash_internal.h"
-#include "dash_serve.cuh"
+#include "dash_paged.cuh"
 
 namespace dash {
 
 namespace {
 
-constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
+// ---------------------------------------------------------------- instructions
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (kHalf)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t codes, int upper) {
+    uint32_t h;
+    const uint16_t c = (uint16_t)(upper ? codes >> 16 : codes);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return h;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-struct PagedParams {
-    dash_kv_cache c;
-    const __nv_bfloat16* q;
-    long long q_t, q_h, table_stride;
-    const int32_t *table, *lens, *cu_q;
-    __nv_bfloat16* o;
-    float* lse;
-    int max_pages, B, T, Hq, max_q, causal, window;
+// ---------------------------------------------------------------- few rows
+template <int D, bool kE4M3>
+struct FewCfg {
+    static constexpr int kElem = kE4M3 ? 1 : 2;
+    static constexpr int kHalfStage = kFewKeys * D * kElem;   // K, then V
+    static constexpr int kStage = 2 * kHalfStage;
+    // even, so that a stage always belongs to the same group of consumers: a warp then waits for every phase of its
+    // stages' barriers in turn (of an odd count it would skip every other one, and parity cannot tell phase u from u + 2)
+    static constexpr int kStages = (163840 / kStage / 2 * 2) < 16 ? 163840 / kStage / 2 * 2 : 16;
+    static_assert(kStages % 2 == 0 && kStages >= 4, "stage ring");
+    static constexpr int kSlotRow = kE4M3 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
+    static constexpr int OFF_SCALE = kStages * kStage;        // [stage][K, V][kFewKeys] fp32
+    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? kStages * 2 * kFewKeys * 4 : 0);
+    static constexpr int OFF_M = OFF_SLOT + 4 * kFewRows * kSlotRow * 4;   // [parity][warp][row]
+    static constexpr int OFF_L = OFF_M + 2 * 8 * kFewRows * 4;             // [warp][row]
+    static constexpr int OFF_PLAN = OFF_L + 8 * kFewRows * 4;
+    static constexpr int OFF_BAR = (OFF_PLAN + (int)sizeof(Plan) + 15) / 16 * 16;
+    static constexpr int OFF_ABORT = OFF_BAR + 2 * kStages * 8;
+    static constexpr int kSmem = OFF_ABORT + 16;
+    static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(256) paged_row_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int E = D / 32;   // values of a vector per lane
-    const int lane = threadIdx.x & 31;
-    const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-    const long long cap = (long long)p.max_pages * p.c.page_size;
-    if (blockIdx.x == 0)   // what the host cannot see
-        for (int b = threadIdx.x; b < p.B; b += 256) {
-            const long long len = p.lens[b];
-            if (len < 0 || len > cap) serve_error(DASH_ERR_PAGE, kOpAttn, b, len, cap);
-            if (p.cu_q) {
-                const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1];
-                if (c0 < 0 || c1 < c0 || c1 > p.T) serve_error(DASH_ERR_PAGE, kOpAttn, b, c0 < 0 ? c0 : c1, p.T);
-                if (c1 - c0 > p.max_q) serve_error(DASH_ERR_PAGE, kOpAttn, b, c1 - c0, p.max_q);
-            }
-        }
-    const int row = (int)(w / p.Hq), h = (int)(w % p.Hq);
-    if (row >= p.T) return;
-    int b, first, n;
-    if (p.cu_q) {
-        int lo = 0, hi = p.B;   // the last b with cu_q[b] <= row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            (p.cu_q[mid] <= row ? lo : hi) = mid;
-        }
-        b = lo;
-        first = p.cu_q[b];
-        n = p.cu_q[b + 1] - first;
-    } else {
-        n = p.T / p.B;
-        b = row / n;
-        first = b * n;
+struct FewItem {
+    Seq s;
+    Cut c;
+    int b, hk, split, t0, t1;   // key tiles [t0, t1)
+};
+
+// The items of one CTA in ascending order: sequence b and the item in it.
+struct ItemWalk {
+    int b = 0;
+    __device__ __forceinline__ void at(const PagedParams& p, const Plan& plan, int item, FewItem& it) {
+        while (plan.items[b + 1] <= item) ++b;
+        it.s = plan.seq[b];
+        it.c = cut_few(p, it.s);
+        it.b = p.b0 + b;
+        const int local = item - plan.items[b];
+        it.split = local / p.c.Hkv;
+        it.hk = local - it.split * p.c.Hkv;
+        const int first = it.c.lo / kFewKeys;
+        it.t0 = first + it.split * it.c.st;
+        it.t1 = min(it.t0 + it.c.st, first + it.c.tiles);
     }
-    if (first < 0 || row - first >= n || row < first) return;
-    long long len = p.lens[b];
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    const long long pos = len - n + (row - first);
-    long long end = p.causal ? pos + 1 : len, begin = 0;
-    if (p.window && pos + 1 > p.window) begin = pos + 1 - p.window;
-    float q[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(p.q[row * p.q_t + h * p.q_h + lane * E + e]) * (kLog2eP / sqrtf((float)D));
-        o[e] = 0.f;
+};
+
+// Waits for a phase, at most timeout_ns; after a wait that ran out (reported) nothing waits any more, so that every
+// role reaches its end.
+__device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort) return;
+        if (ptx::globaltimer() - t0 > limit) {
+            serve_error(DASH_ERR_TIMEOUT, kOpAttn, blockIdx.x, 0, 0);
+            *abort = 1;
+            return;
+        }
     }
-    const int hk = h / (p.Hq / p.c.Hkv);
-    float m = -INFINITY, l = 0.f;
-    for (long long j = begin; j < end; ++j) {
-        int page = p.table[b * p.table_stride + j / p.c.page_size];
-        if (page < 0 || page >= p.c.num_pages) {
-            if (lane == 0) serve_error(DASH_ERR_PAGE, kOpAttn, b, page, p.c.num_pages);
-            page = 0;
-        }
-        const long long cell = ((long long)page * p.c.Hkv + hk) * p.c.page_size + j % p.c.page_size;
-        float s = 0.f, v[E];
-        for (int e = 0; e < E; e += 2) {
-            const long long at = cell * D + lane * E + e;
-            float2 k2, v2;
-            if (kE4M3) {
-                k2 = unpack_e4m3x2(*reinterpret_cast<const uint16_t*>((const uint8_t*)p.c.k + at));
-                v2 = unpack_e4m3x2(*reinterpret_cast<const uint16_t*>((const uint8_t*)p.c.v + at));
-            } else {
-                k2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>((const __nv_bfloat16*)p.c.k + at));
-                v2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>((const __nv_bfloat16*)p.c.v + at));
-            }
-            s += q[e] * k2.x + q[e + 1] * k2.y;
-            v[e] = v2.x, v[e + 1] = v2.y;
-        }
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        float vs = 1.f;
-        if (kE4M3) {
-            s *= p.c.k_scale[cell];
-            vs = p.c.v_scale[cell];
-        }
-        const float m2 = fmaxf(m, s), a = exp2f(m - m2), w2 = exp2f(s - m2);
-        l = l * a + w2;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + w2 * vs * v[e];
-        m = m2;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int e = 0; e < E; ++e) p.o[((long long)row * p.Hq + h) * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[(long long)row * p.Hq + h] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
 }
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int zero_counter) {
+    using C = FewCfg<D, kE4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t bar_full = sbase + C::OFF_BAR, bar_empty = bar_full + 8 * C::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 256) {
+        *abort = 0;
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 4);
+        }
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&p.tm_k);
+        ptx::prefetch_tensormap(&p.tm_v);
+    }
+    if (zero_counter && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+    make_plan(p, plan, true, blockIdx.x == 0);
+    launch_dependents();
+    const int items = plan.items[p.nb];
+    ItemWalk walk;
+    FewItem it;
+
+    if (warp == 8) {
+        // ================================================== producer
+        const int page = p.c.page_size, rows = page < kFewKeys ? page : kFewKeys;
+        const int subs = kFewKeys / rows;                 // copies of one kind along a stage's keys
+        const int kinds = kE4M3 ? 4 : D / 32;             // K (per 64 values), V (same), or K, V and their scales
+        const int sub = lane / kinds, kind = lane % kinds;
+        const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
+        int tc = 0;                                       // stages used so far
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            walk.at(p, plan, item, it);
+            if (it.t0 >= it.t1) continue;
+            const int e0 = max(it.t0 * kFewKeys, it.c.lo) >> p.page_shift;
+            const int e1 = (min(it.t1 * kFewKeys, it.c.hi) - 1) >> p.page_shift;
+            int eb = (it.t0 * kFewKeys) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
+            auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
+            int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
+            for (int t = it.t0; t < it.t1; ++t, ++tc) {
+                const int key = t * kFewKeys;
+                if ((key >> p.page_shift) - eb >= 32) {
+                    eb += 32;
+                    pages = next;
+                    next = fetch(eb + 32 + lane);
+                }
+                const int k0 = key + sub * rows;          // this lane's first key
+                const bool need = sub < subs && k0 + rows > it.c.lo && k0 < it.c.hi;
+                const int pg = __shfl_sync(0xffffffffu, pages, ((k0 >> p.page_shift) - eb) & 31);
+                const int stage = tc % C::kStages;
+                const uint32_t full = bar_full + 8 * stage;
+                const int count = __popc(__ballot_sync(0xffffffffu, need && kind == 0));
+                if (tc >= C::kStages) few_wait(bar_empty + 8 * stage, (uint32_t)((tc / C::kStages - 1) & 1), abort, p.timeout_ns);
+                if (__any_sync(0xffffffffu, *abort)) break;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, count * sub_bytes);
+                __syncwarp();
+                if (need) {
+                    const int y = k0 & (page - 1), head = pg * p.c.Hkv + it.hk;
+                    const uint32_t base = sbase + stage * C::kStage;
+                    if (!kE4M3) {
+                        constexpr int kBoxes = D / 64;
+                        const int box = kind % kBoxes, val = kind / kBoxes;
+                        ptx::tma_load_3d(base + val * C::kHalfStage + box * (kFewKeys * 128) + sub * rows * 128,
+                                         val ? &p.tm_v : &p.tm_k, 64 * box, y, head, full);
+                    } else if (kind < 2) {
+                        ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * D, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
+                    } else {
+                        const float* src = (kind == 3 ? p.c.v_scale : p.c.k_scale) + (long long)head * page + y;
+                        bulk_load(sbase + C::OFF_SCALE + ((stage * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src, rows * 4, full);
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, *abort)) break;
+        }
+        // let what was issued land before the CTA can end (the consumers have seen all of it unless a wait ran out)
+        if (*abort)
+            for (int u = max(tc - C::kStages, 0); u < tc; ++u) {
+                const uint64_t t0 = ptx::globaltimer();
+                while (!ptx::mbar_try_wait(bar_full + 8 * (u % C::kStages), (uint32_t)((u / C::kStages) & 1)) &&
+                       ptx::globaltimer() - t0 < 100000000ull) {
+                }
+            }
+        return;
+    }
+
+    // ================================================== consumers
+    const int g = lane >> 2, c4 = lane & 3;
+    const int group = warp >> 2, ws = warp & 3;
+    // key of column n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
+    // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
+    auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
+    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT);
+    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M);
+    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L);
+    int tc = 0, parity = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, parity ^= 1) {
+        walk.at(p, plan, item, it);
+        const int R = it.s.n * p.G;
+        const bool two = R > 8;   // rows 8..15 exist
+        // rows g and g + 8: their keys [lo, hi)
+        int hi[2], lo[2];
+        const __nv_bfloat16* qrow[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = min(g + 8 * h, R - 1), i = r / p.G;
+            seen_keys(p, it.s, i, i + 1, lo[h], hi[h]);
+            qrow[h] = p.q + (long long)(it.s.first + i) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
+        }
+        // tiles in [full_lo, full_hi) are seen whole by every row
+        int a0, a1, b0, b1;
+        seen_keys(p, it.s, 0, 1, a0, a1);
+        seen_keys(p, it.s, it.s.n - 1, it.s.n, b0, b1);
+        const int full_lo = b0, full_hi = a1;
+
+        uint32_t qf[D / 16][4];
+        float qs[2];   // scale of the scores of rows g, g + 8 (log2 units)
+        if (!kE4M3) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const int d = 16 * k + 2 * c4;
+                qf[k][0] = *reinterpret_cast<const uint32_t*>(qrow[0] + d);
+                qf[k][2] = *reinterpret_cast<const uint32_t*>(qrow[0] + d + 8);
+                qf[k][1] = two ? *reinterpret_cast<const uint32_t*>(qrow[1] + d) : 0u;
+                qf[k][3] = two ? *reinterpret_cast<const uint32_t*>(qrow[1] + d + 8) : 0u;
+            }
+            qs[0] = qs[1] = p.scale_log2e;
+        } else {
+            // step 4h + t holds values 64h + 16c + 4t + 0..3 of lane c
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = 0.f;
+                if (h == 0 || two) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(qrow[h] + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
+                        qf[k][h] = w.x;
+                        qf[k][2 + h] = w.y;
+                        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
+                                               fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) qf[k][h] = qf[k][2 + h] = 0u;
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                qs[h] = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t w = qf[k][2 * x + h];
+                        qf[k][2 * x + h] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                    }
+            }
+        }
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        for (int t = it.t0; t < it.t1; ++t, ++tc) {
+            if ((tc & 1) != group) continue;
+            const int stage = tc % C::kStages;
+            few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
+            __syncwarp();
+            const uint32_t sk = sbase + stage * C::kStage, sv = sk + C::kHalfStage;
+            const int key0 = t * kFewKeys + 16 * ws;   // this warp's first key
+            const bool edge = key0 < full_lo || key0 + 16 > full_hi;
+            if (edge) {   // value rows that no row sees: zero, whatever the cells hold
+                const int r = lane >> 1;
+                if (key0 + r < it.c.lo || key0 + r >= it.c.hi) {
+                    const int row = 16 * ws + r;
+                    constexpr int kRow = D * C::kElem / 2;   // bytes per lane
+#pragma unroll
+                    for (int x = 0; x < kRow; x += 16) {
+                        const int byte = (lane & 1) * kRow + x;   // rows are zeroed whole: the swizzle stays inside a row
+                        sts128(kE4M3 || D == 64 ? sv + row * (D * C::kElem) + byte
+                                                : sv + (byte >> 7) * (kFewKeys * 128) + row * 128 + (byte & 127),
+                               make_uint4(0, 0, 0, 0));
+                    }
+                }
+                __syncwarp();
+            }
+
+            float s[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+            if (!kE4M3) {
+                const int row = 16 * ws + (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t r[4];
+                    const int chunk = 2 * (k & 3) + ((lane >> 3) & 1);
+                    ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), r);
+                    mma16816<false>(s[0], qf[k], r[0], r[1]);
+                    mma16816<false>(s[1], qf[k], r[2], r[3]);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int row = 16 * ws + 8 * n + perm(g);
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        const int chunk = 4 * h + c4;
+                        const uint4 w = lds128(D == 128 ? sk + row * 128 + ((chunk ^ (row & 7)) << 4)
+                                                        : sk + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma16816<true>(s[n], qf[4 * h + x], half2_of_e4m3(ww[x], 0), half2_of_e4m3(ww[x], 1));
+                    }
+                }
+            }
+
+            // scores in log2 units; lv = log2 of the value scales (e4m3)
+            float lv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int at = 16 * ws + 8 * n + perm(2 * c4 + e);
+                    float ks = 1.f;
+                    if (kE4M3) {
+                        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + stage * 2 * kFewKeys;
+                        ks = sc[at];
+                        lv[n][e] = __log2f(sc[kFewKeys + at]);
+                    }
+                    s[n][e] *= qs[0] * ks;
+                    s[n][2 + e] *= qs[1] * ks;
+                    if (edge) {
+                        const int key = t * kFewKeys + at;
+                        if (key < lo[0] || key >= hi[0]) s[n][e] = -INFINITY;
+                        if (key < lo[1] || key >= hi[1]) s[n][2 + e] = -INFINITY;
+                        if (kE4M3 && (key < it.c.lo || key >= it.c.hi)) lv[n][e] = 0.f;
+                    }
+                }
+            // running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8
+            float mx[2], mw[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                mw[h] = mx[h];
+                if (kE4M3) {
+                    mw[h] = fmaxf(fmaxf(s[0][2 * h] + lv[0][0], s[0][2 * h + 1] + lv[0][1]),
+                                  fmaxf(s[1][2 * h] + lv[1][0], s[1][2 * h + 1] + lv[1][1]));
+                    mw[h] = fmaxf(mw[h], __shfl_xor_sync(0xffffffffu, mw[h], 1));
+                    mw[h] = fmaxf(mw[h], __shfl_xor_sync(0xffffffffu, mw[h], 2));
+                }
+            }
+            bool raise = mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f;
+            if (kE4M3) raise = raise || mw[0] > mv[0] + 8.f || mw[1] > mv[1] + 8.f;
+            if (__any_sync(0xffffffffu, raise)) {
+                float f[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float nm = fmaxf(m[h], mx[h]), nv = fmaxf(mv[h], mw[h]);
+                    l[h] *= nm == -INFINITY ? 1.f : ptx::ex2(m[h] - nm);
+                    f[h] = nv == -INFINITY ? 1.f : ptx::ex2(mv[h] - nv);
+                    m[h] = nm;
+                    mv[h] = nv;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][0] *= f[0];
+                    o[j][1] *= f[0];
+                    o[j][2] *= f[1];
+                    o[j][3] *= f[1];
+                }
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float mu = m[h] == -INFINITY ? 0.f : m[h], vu = mv[h] == -INFINITY ? 0.f : mv[h];
+                float w[2][2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = s[n][2 * h + e];
+                        const float pr = ptx::ex2(x - mu);
+                        l[h] += pr;
+                        w[n][e] = kE4M3 ? ptx::ex2(x + (lv[n][e] - vu)) : pr;
+                    }
+                // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
+                pa[h] = kE4M3 ? pack_half(w[0][0], w[0][1]) : pack_bf16(w[0][0], w[0][1]);
+                pa[2 + h] = kE4M3 ? pack_half(w[1][0], w[1][1]) : pack_bf16(w[1][0], w[1][1]);
+            }
+
+            if (!kE4M3) {
+                const int row = 16 * ws + (lane & 15);
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    uint32_t r[4];
+                    const int chunk = 2 * (j & 3) + (lane >> 4);
+                    ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), r);
+                    mma16816<false>(o[2 * j], pa, r[0], r[1]);
+                    mma16816<false>(o[2 * j + 1], pa, r[2], r[3]);
+                }
+            } else {
+                const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
+                constexpr int kWords = D / 32;   // words of a lane's D / 8 columns
+                uint32_t w[4][kWords];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = (x & 1 ? r1 : r0) + 8 * (x >> 1);
+                    if (D == 128) {
+                        const uint4 v = lds128(sv + row * 128 + ((g ^ (row & 7)) << 4));
+                        w[x][0] = v.x, w[x][1] = v.y, w[x][kWords - 2] = v.z, w[x][kWords - 1] = v.w;
+                    } else {
+                        const uint2 v = lds64(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                        w[x][0] = v.x, w[x][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < kWords; ++y) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {   // columns 4y + 2z, + 1: byte pairs of the two keys of each half
+                        const uint32_t sel = z ? 0x7362u : 0x5140u;
+                        const uint32_t lo2 = __byte_perm(w[0][y], w[1][y], sel), hi2 = __byte_perm(w[2][y], w[3][y], sel);
+                        mma16816<true>(o[4 * y + 2 * z], pa, half2_of_e4m3(lo2, 0), half2_of_e4m3(hi2, 0));
+                        mma16816<true>(o[4 * y + 2 * z + 1], pa, half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 1));
+                    }
+                }
+            }
+            if (edge) ptx::fence_proxy_async_smem();   // the zeroed rows before the next copy into the stage
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
+        }
+
+        // ---------------------------------------------- join the eight warps
+        float* const mp = mrow + parity * 8 * kFewRows;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if (c4 == 0) mp[warp * kFewRows + g + 8 * h] = m[h];
+        }
+        consumer_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) top = fmaxf(top, mp[w * kFewRows + g + 8 * h]);
+            // outputs carry 2^-mv (weights with their scales), sums 2^-m
+            const float fo = (top == -INFINITY || mv[h] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[h] : m[h]) - top);
+            l[h] *= (top == -INFINITY || m[h] == -INFINITY) ? 0.f : ptx::ex2(m[h] - top);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][2 * h] *= fo;
+                o[j][2 * h + 1] *= fo;
+            }
+            if (c4 == 0) lrow[warp * kFewRows + g + 8 * h] = l[h];
+        }
+        // rows past R hold copies; they are neither joined nor stored
+        auto each = [&](float* slot, bool add) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (g + 8 * h >= R) continue;
+                float* row = slot + (g + 8 * h) * C::kSlotRow;
+                if (!kE4M3) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        float2* q = reinterpret_cast<float2*>(row + 8 * j + 2 * c4);
+                        if (add) {
+                            const float2 v = *q;
+                            o[j][2 * h] += v.x;
+                            o[j][2 * h + 1] += v.y;
+                        } else {
+                            *q = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {   // values (2c + e) D/8 + 4k..: chunk index XOR c spreads the banks
+                            const int chunk = ((2 * c4 + e) * (D / 32) + k) ^ c4;
+                            float4* q = reinterpret_cast<float4*>(row + 4 * chunk);
+                            if (add) {
+                                const float4 v = *q;
+                                o[4 * k][2 * h + e] += v.x;
+                                o[4 * k + 1][2 * h + e] += v.y;
+                                o[4 * k + 2][2 * h + e] += v.z;
+                                o[4 * k + 3][2 * h + e] += v.w;
+                            } else {
+                                *q = make_float4(o[4 * k][2 * h + e], o[4 * k + 1][2 * h + e], o[4 * k + 2][2 * h + e],
+                                                 o[4 * k + 3][2 * h + e]);
+                            }
+                        }
+                }
+            }
+        };
+        float* const slot = slots + ws * kFewRows * C::kSlotRow;
+        if (group == 1) each(slot, false);
+        consumer_barrier();
+        if (group == 0) {
+            each(slot, true);
+            each(slot, false);
+        }
+        consumer_barrier();
+        for (int i = threadIdx.x; i < R * (D / 4); i += 256) {
+            const int r = i / (D / 4), q4 = i % (D / 4);
+            const int chunk = kE4M3 ? q4 ^ (q4 / (D / 16)) : q4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(slots + (w * kFewRows + r) * C::kSlotRow + 4 * chunk);
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                top = fmaxf(top, mp[w * kFewRows + r]);
+                sum += lrow[w * kFewRows + r];
+            }
+            if (it.c.ns == 1) {
+                const int tok = it.s.first + r / p.G, h = it.hk * p.G + r % p.G;
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
+                    make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+                if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
+            } else {
+                const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * R + r;
+                if (row < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
+                    *reinterpret_cast<float4*>(p.part_o + row * D + 4 * q4) = a;
+                    if (q4 == 0) p.part_ml[row] = make_float2(top, sum);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- joining key ranges
+// One block per row of a split sequence: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its ranges, warp w
+// taking ranges w, w + 4, ... and the four warps joined in order, so the additions have one fixed order.
+template <int D>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ PagedParams p) {
+    __shared__ Plan plan;
+    __shared__ float part[4][D];
+    __shared__ float part_l[4];
+    make_plan(p, plan, true, false);
+    wait_dependency();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int E = D / 32;
+    // plan.rows counts ns partial rows for each row: walk the sequences with the row index
+    int b = 0;
+    long long before = 0;   // rows of split sequences before b
+    for (long long w = blockIdx.x;; w += gridDim.x) {
+        int ns = 1, n = 0;
+        long long rows = 0;
+        for (; b < p.nb; ++b) {
+            n = plan.seq[b].n;
+            const int pr = plan.rows[b + 1] - plan.rows[b];
+            rows = pr ? (long long)n * p.Hq : 0;
+            if (rows && w < before + rows) {
+                ns = (int)(pr / rows);
+                break;
+            }
+            before += rows;
+        }
+        if (b >= p.nb) return;
+        const int local = (int)(w - before);   // (token, head)
+        const int i = local / p.Hq, h = local % p.Hq, hk = h / p.G;
+        const int R = n * p.G, r = i * p.G + h % p.G;
+        const long long base = plan.rows[b] + (long long)hk * R + r, step = (long long)p.c.Hkv * R;
+        if (base + (ns - 1) * step >= p.max_rows) continue;
+        float top = -INFINITY;
+        for (int s = lane; s < ns; s += 32) top = fmaxf(top, p.part_ml[base + s * step].x);
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float mu = top == -INFINITY ? 0.f : top;
+        float a[E], l = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = 0.f;
+#pragma unroll 8
+        for (int s = warp; s < ns; s += 4) {
+            const long long row = base + s * step;
+            const float2 ml = p.part_ml[row];
+            const float f = ptx::ex2(ml.x - mu);
+            l += f * ml.y;
+            if (E == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * lane);
+                a[0] += f * v.x;
+                a[1] += f * v.y;
+                a[E - 2] += f * v.z;
+                a[E - 1] += f * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p.part_o + row * D + 2 * lane);
+                a[0] += f * v.x;
+                a[1] += f * v.y;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
+        if (lane == 0) part_l[warp] = l;
+        __syncthreads();
+        const float sum = ((part_l[0] + part_l[1]) + part_l[2]) + part_l[3];
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const long long at = (long long)(plan.seq[b].first + i) * p.Hq + h;
+        if ((int)threadIdx.x < D / 2) {
+            const int d = 2 * threadIdx.x;
+            const float x = ((part[0][d] + part[1][d]) + part[2][d]) + part[3][d];
+            const float y = ((part[0][d + 1] + part[1][d + 1]) + part[2][d + 1]) + part[3][d + 1];
+            *reinterpret_cast<uint32_t*>(p.o + at * D + d) = pack_bf16(x * inv, y * inv);
+        }
+        if (p.lse && threadIdx.x == 127) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+int sm_count() {
+    static int count[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!count[dev] && cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return count[dev];
+}
+
+template <int D, bool kE4M3>
+int launch_few_t(const PagedParams& p, int zero_counter, int max_items, cudaStream_t s) {
+    using C = FewCfg<D, kE4M3>;
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+            return DASH_ERR_CUDA;
+        ready[dev] = true;
+    }
+    const int sms = sm_count();
+    if (sms <= 0) return DASH_ERR_CUDA;
+    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 288, C::kSmem, s>>>(p, zero_counter);
+    return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+// As the kernel before it in the stream ends; its plan is made while that one runs.
+template <int D>
+int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    const int sms = sm_count();
+    if (sms <= 0) return DASH_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)(max_rows < 8ll * sms ? max_rows : 8ll * sms));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+// Bounds that the host knows of a launch of nb sequences: items of the few-rows class, partial rows of both classes.
+struct Bounds {
+    long long few_items, rows;
+};
+
+Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv) {
+    const int G = Hq / Hkv;
+    Bounds r{0, 0};
+    const long long few_q = G > kFewRows ? 0 : (max_q < kFewRows / G ? max_q : kFewRows / G);   // tokens of a few-rows sequence
+    const long long n_few = nb < T ? nb : T;
+    if (few_q > 0) {
+        // a window may start inside a tile: one tile more than the length has
+        const long long tiles = max_kv / kFewKeys + 2, by_len = (tiles + kFewSplitTiles - 1) / kFewSplitTiles;
+        const long long ns = by_len < few_max_splits(Hkv) ? by_len : few_max_splits(Hkv);
+        r.few_items = n_few * Hkv * ns;
+        if (ns > 1) r.rows += (few_q * n_few < T ? few_q * n_few : T) * Hq * ns;
+    }
+    if ((long long)max_q * G > kFewRows) {
+        const long long ns = max_kv / kTileSplitKeys + 2;
+        const long long least = kFewRows / G + 1;                       // tokens of the smallest many-rows sequence
+        const long long n_many = T / least < nb ? T / least : nb;
+        // a split sequence has at most (2 * kTileFullItems + its items) items of kTileRows rows
+        const long long each = 3ll * kTileFullItems * kTileRows;
+        const long long by_items = n_many * each, by_len = T * Hq * (ns < 2 * kTileFullItems ? ns : 2 * kTileFullItems);
+        r.rows += by_items < by_len ? by_items : by_len;
+    }
+    return r;
+}
+
+constexpr size_t kWsHeader = 256;   // the many-rows kernel's item counter
 
 }  // namespace
 
@@ -120,9 +770,14 @@ using namespace dash;
 extern "C" int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int64_t max_kv,
                                          size_t* bytes) {
     if (!bytes || B < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || (D != 64 && D != 128) ||
-        max_q < 0 || max_kv < 0)
+        max_q < 0 || max_kv < 0 || max_kv >= (1ll << 31) - 512 || (long long)T * Hq >= (1ll << 31))
         return DASH_ERR_ARG;
     *bytes = 0;
+    if (B == 0 || T == 0) return DASH_OK;
+    const Bounds b = bounds(B < kMaxSeqs ? B : kMaxSeqs, T, Hq, Hkv, max_q, max_kv);
+    if (b.rows >= (1ll << 31) || b.few_items >= (1ll << 31)) return DASH_ERR_ARG;
+    const bool many = (long long)max_q * (Hq / Hkv) > kFewRows;
+    if (b.rows || many) *bytes = kWsHeader + (size_t)b.rows * (D * sizeof(float) + sizeof(float2));
     return DASH_OK;
 }
 
@@ -136,10 +791,10 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     if (max_pages < 0 || table_stride < 0 || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) ||
         !serve_strides(q_stride_t, q_stride_h))
         return DASH_ERR_ARG;
+    const int Hkv = cache->Hkv, D = cache->D;
+    const int64_t max_kv = (int64_t)max_pages * cache->page_size;
     size_t need = 0;
-    if ((rc = dash_attn_paged_workspace(B, T, Hq, cache->Hkv, cache->D, max_q, (int64_t)max_pages * cache->page_size,
-                                        &need)))
-        return rc;
+    if ((rc = dash_attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv, &need))) return rc;
     if (B == 0 || T == 0) return DASH_OK;
     if (!serve_aligned(q) || !serve_aligned(o) || ((uintptr_t)lse & 3u) || !kv_lens || ((uintptr_t)kv_lens & 3u) ||
         ((uintptr_t)cu_q & 3u) || ((uintptr_t)block_table & 3u) || (max_pages > 0 && !block_table) ||
@@ -147,7 +802,9 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         return DASH_ERR_ARG;
     if (workspace_bytes < need) return DASH_ERR_SCRATCH;
     if ((rc = serve_check_device())) return rc;
+
     PagedParams prm;
+    memset(&prm, 0, sizeof(prm));
     prm.c = *cache;
     prm.q = (const __nv_bfloat16*)q;
     prm.q_t = q_stride_t;
@@ -158,22 +815,43 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     prm.cu_q = cu_q;
     prm.o = (__nv_bfloat16*)o;
     prm.lse = lse;
+    prm.timeout_ns = timeout_ns();
     prm.max_pages = max_pages;
     prm.B = B;
     prm.T = T;
     prm.Hq = Hq;
+    prm.G = Hq / Hkv;
     prm.max_q = max_q;
     prm.causal = causal;
     prm.window = window;
-    const long long blocks = ((long long)T * Hq + 7) / 8;
-    if (blocks > 0x7fffffffll) return DASH_ERR_ARG;
+    while ((1 << prm.page_shift) < cache->page_size) ++prm.page_shift;
+    prm.scale_log2e = (1.0f / sqrtf((float)D)) * kLog2eP;
+    const bool e4m3 = cache->type == DASH_CACHE_E4M3;
+    const int rows = cache->page_size < kFewKeys ? cache->page_size : kFewKeys;
+    if (make_tmap_pages(&prm.tm_k, cache->k, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows) ||
+        make_tmap_pages(&prm.tm_v, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows))
+        return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    if (cache->type == DASH_CACHE_E4M3) {
-        if (cache->D == 64) paged_row_kernel<64, true><<<(unsigned)blocks, 256, 0, s>>>(prm);
-        else paged_row_kernel<128, true><<<(unsigned)blocks, 256, 0, s>>>(prm);
-    } else {
-        if (cache->D == 64) paged_row_kernel<64, false><<<(unsigned)blocks, 256, 0, s>>>(prm);
-        else paged_row_kernel<128, false><<<(unsigned)blocks, 256, 0, s>>>(prm);
+    for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {
+        prm.b0 = b0;
+        prm.nb = B - b0 < kMaxSeqs ? B - b0 : kMaxSeqs;
+        const Bounds bd = bounds(prm.nb, T, Hq, Hkv, max_q, max_kv);
+        if (need) {
+            prm.counter = (int*)workspace;
+            prm.part_o = (float*)((char*)workspace + kWsHeader);
+            prm.part_ml = (float2*)(prm.part_o + bd.rows * D);
+            prm.max_rows = bd.rows;
+        }
+        const bool many = (long long)max_q * prm.G > kFewRows;
+        const int items = (int)(bd.few_items < 1 ? 1 : bd.few_items);   // at least one block: it checks the lengths
+        if (e4m3)
+            rc = D == 64 ? launch_few_t<64, true>(prm, many, items, s) : launch_few_t<128, true>(prm, many, items, s);
+        else
+            rc = D == 64 ? launch_few_t<64, false>(prm, many, items, s) : launch_few_t<128, false>(prm, many, items, s);
+        if (rc) return rc;
+        if (many && (rc = launch_paged_many(prm, 0, s))) return rc;
+        if (bd.rows && (rc = D == 64 ? launch_combine<64>(prm, (long long)T * Hq, s) : launch_combine<128>(prm, (long long)T * Hq, s)))
+            return rc;
     }
-    return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    return DASH_OK;
 }

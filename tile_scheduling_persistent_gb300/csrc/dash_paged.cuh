@@ -1,0 +1,223 @@
+// dash_paged.cuh -- what the kernels of the paged attention share: how the
+// sequences of a call are cut into work items, and the partial results of
+// sequences whose keys are split.
+//
+// A sequence with n new tokens has n * G rows per key/value head (row r is
+// token r / G, head r % G of the group: one row of queries reads the same keys
+// for the whole group).  Two classes, by the sequence's own size:
+//   few rows  (n * G <= 16): memory bound; items of (head, key range), dash_paged.cu
+//   many rows              : items of (head, row tile, key range), dash_paged_tile.cu
+// Every cut depends on the sequence's own lengths and on Hkv, G and D, never on
+// the rest of the batch or on the number of SMs, so that a sequence's results
+// are the same bits in any batch.
+//
+// A sequence cut into ns > 1 key ranges leaves, for each range and row, the
+// unnormalised fp32 output, its maximum m (log2 units) and its sum l relative
+// to m; combine_kernel joins the ranges in ascending order.
+#pragma once
+#include "dash_ptx.cuh"
+#include "dash_serve.cuh"
+
+namespace dash {
+
+constexpr int kFewRows = 16;       // rows of one m16 matrix operand
+constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel
+constexpr int kFewSplitTiles = 4;  // at least this many stages per key range
+constexpr int kMaxSeqs = 1024;     // sequences per launch (their plan lies in shared memory)
+constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
+constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
+constexpr int kTileFullItems = 0;      // items that keep the GPU busy without a split
+constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
+
+struct PagedParams {
+    CUtensorMap tm_k, tm_v;        // [num_pages * Hkv][page_size][D], boxes of min(page_size, tile) rows
+    CUtensorMap tm_q;              // many rows: [T][Hq][D]
+    dash_kv_cache c;
+    const __nv_bfloat16* q;
+    long long q_t, q_h, table_stride;
+    const int32_t *table, *lens, *cu_q;
+    __nv_bfloat16* o;
+    float* lse;
+    float* part_o;                 // [rows of split sequences][D]
+    float2* part_ml;               // (m, l) of each
+    long long max_rows;            // rows that part_o and part_ml hold
+    int* counter;                  // many rows: next item
+    unsigned long long timeout_ns;
+    int b0, nb;                    // the launch's sequences
+    int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
+    float scale_log2e;
+};
+
+struct Seq {
+    int first, n, len;             // n = 0: nothing to do
+};
+
+// What the device alone knows about sequence b, checked; report: this thread reports what is wrong.
+__device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report) {
+    const long long cap = (long long)p.max_pages * p.c.page_size;
+    int c0, c1;
+    if (p.cu_q) {
+        c0 = p.cu_q[b];
+        c1 = p.cu_q[b + 1];
+    } else {
+        const int n = p.T / p.B;
+        c0 = b * n;
+        c1 = c0 + n;
+    }
+    const int len = p.lens[b];
+    Seq s{c0, c1 - c0, len};
+    if (c0 < 0 || c1 < c0 || c1 > p.T) {
+        if (report) serve_error(DASH_ERR_PAGE, kOpAttn, b, c0 < 0 ? c0 : c1, p.T);
+        s.n = 0;
+    } else if (s.n > p.max_q) {
+        if (report) serve_error(DASH_ERR_PAGE, kOpAttn, b, s.n, p.max_q);
+        s.n = 0;
+    } else if (len < 0 || len > cap) {
+        if (report) serve_error(DASH_ERR_PAGE, kOpAttn, b, len, cap);
+        s.n = 0;
+    }
+    return s;
+}
+
+__host__ __device__ inline bool few_rows(int n, int G) { return (long long)n * G <= kFewRows; }
+
+// Keys [lo, hi) that rows i0 .. i1 - 1 (tokens) of a sequence see.
+__device__ __forceinline__ void seen_keys(const PagedParams& p, const Seq& s, int i0, int i1, int& lo, int& hi) {
+    const int p0 = s.len - s.n + i0, p1 = s.len - s.n + i1;   // first position, one past the last
+    hi = p.causal ? (p1 < 0 ? 0 : p1) : s.len;
+    lo = (p.window && p0 + 1 > p.window) ? p0 + 1 - p.window : 0;
+}
+
+__host__ __device__ inline int few_max_splits(int Hkv) {   // about a thousand items for one long sequence: 6.7 per SM
+    const int n = 1024 / Hkv;
+    return n < 32 ? 32 : n > 256 ? 256 : n;
+}
+
+// Key ranges of a sequence: `tiles` key tiles of its class cut into ns ranges of st tiles.
+__host__ __device__ inline void few_split(int tiles, int Hkv, int& ns, int& st) {
+    const int most = few_max_splits(Hkv);
+    st = (tiles + most - 1) / most;
+    st = st < kFewSplitTiles ? kFewSplitTiles : st;
+    ns = (tiles + st - 1) / st;
+    ns = ns < 1 ? 1 : ns;
+}
+
+// The launch's plan in shared memory: sequences, and running counts.
+struct Plan {
+    Seq seq[kMaxSeqs];
+    int items[kMaxSeqs + 1];   // items of the class before each sequence
+    int rows[kMaxSeqs + 1];    // partial rows before each sequence (both classes)
+    int warp_sum[2][32];
+};
+
+struct Cut {
+    int lo, hi;                // keys seen by any row (few rows), tiles of them
+    int tiles, ns, st;
+    int items;                 // items of the sequence
+};
+
+__device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
+    Cut c;
+    seen_keys(p, s, 0, s.n, c.lo, c.hi);
+    c.tiles = c.hi > c.lo ? (c.hi - 1) / kFewKeys - c.lo / kFewKeys + 1 : 0;
+    few_split(c.tiles, p.c.Hkv, c.ns, c.st);
+    c.items = p.c.Hkv * c.ns;
+    return c;
+}
+
+// Many rows: key ranges of whole 128-key tiles of the sequence; row tiles of kTileRows rows.
+__device__ __forceinline__ Cut cut_many(const PagedParams& p, const Seq& s, int tokens_per_tile) {
+    Cut c;
+    seen_keys(p, s, 0, s.n, c.lo, c.hi);
+    c.tiles = c.hi > c.lo ? (c.hi - 1) / 128 - c.lo / 128 + 1 : 0;
+    const int row_tiles = (s.n + tokens_per_tile - 1) / tokens_per_tile;
+    const long long full = (long long)row_tiles * p.c.Hkv;
+    c.ns = 1;
+    if (full < kTileFullItems) {
+        const int want = (int)((2 * kTileFullItems + full - 1) / full);
+        const int most = (c.tiles + kTileSplitKeys / 128 - 1) / (kTileSplitKeys / 128);
+        c.ns = want < most ? want : most;
+        c.ns = c.ns < 1 ? 1 : c.ns;
+    }
+    c.st = (c.tiles + c.ns - 1) / c.ns;
+    c.ns = c.st > 0 ? (c.tiles + c.st - 1) / c.st : 1;
+    c.items = (int)full * c.ns;
+    return c;
+}
+
+// Tokens of one item of the many-rows kernel: two matrix tiles of 128 / G tokens.
+__host__ __device__ inline int tokens_per_item(int G) { return 2 * (128 / G); }
+
+// Fills plan for the launch's sequences: items of the `few` class (or of the other), and partial rows of both.  All
+// threads of the block call it; blockDim.x >= 128.  Ends with a barrier.
+__device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool few, bool report) {
+    const int per = (p.nb + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int t0 = (int)threadIdx.x * per;
+    int items = 0, rows = 0;
+    for (int i = t0; i < t0 + per && i < p.nb; ++i) {
+        const Seq s = load_seq(p, p.b0 + i, report);
+        plan.seq[i] = s;
+        if (s.n == 0) continue;
+        const bool f = few_rows(s.n, p.G);
+        const Cut c = f ? cut_few(p, s) : cut_many(p, s, tokens_per_item(p.G));
+        if (f == few) items += c.items;
+        if (c.ns > 1) rows += s.n * p.Hq * c.ns;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
+    int si = items, sr = rows;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, si, d), b = __shfl_up_sync(0xffffffffu, sr, d);
+        if (lane >= d) {
+            si += a;
+            sr += b;
+        }
+    }
+    if (lane == 31) {
+        plan.warp_sum[0][warp] = si;
+        plan.warp_sum[1][warp] = sr;
+    }
+    __syncthreads();
+    int bi = si - items, br = sr - rows;
+    for (int w = 0; w < warp; ++w) {
+        bi += plan.warp_sum[0][w];
+        br += plan.warp_sum[1][w];
+    }
+    for (int i = t0; i < t0 + per && i < p.nb; ++i) {
+        plan.items[i] = bi;
+        plan.rows[i] = br;
+        const Seq s = plan.seq[i];
+        if (s.n == 0) continue;
+        const bool f = few_rows(s.n, p.G);
+        const Cut c = f ? cut_few(p, s) : cut_many(p, s, tokens_per_item(p.G));
+        if (f == few) bi += c.items;
+        if (c.ns > 1) br += s.n * p.Hq * c.ns;
+    }
+    if (threadIdx.x == 0) {
+        int ti = 0, tr = 0;
+        for (int w = 0; w < warps; ++w) {
+            ti += plan.warp_sum[0][w];
+            tr += plan.warp_sum[1][w];
+        }
+        plan.items[p.nb] = ti;
+        plan.rows[p.nb] = tr;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Page of key j of sequence b, checked: a bad entry is reported and read as page 0.
+__device__ __forceinline__ int checked_page(const PagedParams& p, int b, int entry) {
+    const int page = p.table[(long long)b * p.table_stride + entry];
+    if (page < 0 || page >= p.c.num_pages) {
+        serve_error(DASH_ERR_PAGE, kOpAttn, b, page, p.c.num_pages);
+        return 0;
+    }
+    return page;
+}
+
+int launch_paged_many(const PagedParams& p, int max_items, cudaStream_t s);   // dash_paged_tile.cu
+
+}  // namespace dash

@@ -525,11 +525,13 @@ extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_tab
 extern "C" int dash_get_status_paged(dash_stream_t stream, int* code, int* info) {
     if (!code) return DASH_ERR_ARG;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return DASH_ERR_CUDA;
-    int a[5], b[5];
-    int rc = take_error_rope(a);
-    if (rc == DASH_OK) rc = take_error_paged(b);
+    // one record per translation unit: the writer's and reader's first
+    int r[3][5];
+    int rc = take_error_rope(r[0]);
+    if (rc == DASH_OK) rc = take_error_paged(r[1]);
+    if (rc == DASH_OK) rc = take_error_tile(r[2]);
     if (rc) return rc;
-    const int* e = a[0] ? a : b;   // one record per translation unit; the writer's and reader's first
+    const int* e = r[0][0] ? r[0] : r[1][0] ? r[1] : r[2];
     *code = e[0];
     if (info)
         for (int i = 0; i < 4; ++i) info[i] = e[1 + i];

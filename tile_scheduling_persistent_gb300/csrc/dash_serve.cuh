@@ -98,5 +98,6 @@ inline int check_cache(const dash_kv_cache* c) {
 int serve_check_device();   // DASH_OK on sm_103 (dash_rope.cu)
 int take_error_rope(int* out5);
 int take_error_paged(int* out5);
+int take_error_tile(int* out5);
 
 }  // namespace dash
