@@ -438,6 +438,22 @@ int make_tmap_pages(void* map_out, const void* base, long long heads, int page, 
     return r == CUDA_SUCCESS ? 0 : -2;
 }
 
+int make_tmap_rows(void* map_out, const void* base, int T, long long stride_t, int Hkv, int G, long long stride_h,
+                   int D, int tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return -2;
+    // strides of dimensions of size one are never used, but have to be valid
+    const cuuint64_t h = (cuuint64_t)(stride_h > 0 ? stride_h : D) * 2, t = (cuuint64_t)(stride_t > 0 ? stride_t : D) * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)T};
+    const cuuint64_t strides[3] = {h, h * G, t};
+    const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tokens};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(reinterpret_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : -2;
+}
+
 // fp32 [rows, D], boxes of 32 columns x 128 rows (128 B rows, swizzled).
 int make_tmap_2d_f32(void* map_out, const void* base, long long rows, int D) {
     return encode_2d(map_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, D, 32);

@@ -157,7 +157,7 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int zero_counter) {
+__global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
     using C = FewCfg<D, kE4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
@@ -176,7 +176,12 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
         ptx::prefetch_tensormap(&p.tm_k);
         ptx::prefetch_tensormap(&p.tm_v);
     }
-    if (zero_counter && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+    if (many && blockIdx.x == 0) {   // the many-rows kernel's plan and item counter
+        if (threadIdx.x == 0) *p.counter = 0;
+        make_plan(p, plan, false, false);
+        publish_plan(p, plan);
+        __syncthreads();
+    }
     make_plan(p, plan, true, blockIdx.x == 0);
     launch_dependents();
     const int items = plan.items[p.nb];
@@ -694,7 +699,7 @@ int sm_count() {
 }
 
 template <int D, bool kE4M3>
-int launch_few_t(const PagedParams& p, int zero_counter, int max_items, cudaStream_t s) {
+int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
     using C = FewCfg<D, kE4M3>;
     static bool ready[64] = {};
     int dev = 0;
@@ -707,7 +712,7 @@ int launch_few_t(const PagedParams& p, int zero_counter, int max_items, cudaStre
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 288, C::kSmem, s>>>(p, zero_counter);
+    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 288, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
@@ -757,7 +762,7 @@ Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv)
     return r;
 }
 
-constexpr size_t kWsHeader = 256;   // the many-rows kernel's item counter
+constexpr size_t kWsHeader = (256 + sizeof(Plan) + 255) / 256 * 256;   // the many-rows kernel's item counter and plan
 
 }  // namespace
 
@@ -789,7 +794,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     int rc = check_cache(cache);
     if (rc) return rc;
     if (max_pages < 0 || table_stride < 0 || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) ||
-        !serve_strides(q_stride_t, q_stride_h))
+        !serve_strides(q_stride_t, q_stride_h) || (T > 1 && q_stride_t == 0) || (Hq > 1 && q_stride_h == 0))
         return DASH_ERR_ARG;
     const int Hkv = cache->Hkv, D = cache->D;
     const int64_t max_kv = (int64_t)max_pages * cache->page_size;
@@ -838,6 +843,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         const Bounds bd = bounds(prm.nb, T, Hq, Hkv, max_q, max_kv);
         if (need) {
             prm.counter = (int*)workspace;
+            prm.plan = (Plan*)((char*)workspace + 256);
             prm.part_o = (float*)((char*)workspace + kWsHeader);
             prm.part_ml = (float2*)(prm.part_o + bd.rows * D);
             prm.max_rows = bd.rows;
@@ -849,7 +855,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         else
             rc = D == 64 ? launch_few_t<64, false>(prm, many, items, s) : launch_few_t<128, false>(prm, many, items, s);
         if (rc) return rc;
-        if (many && (rc = launch_paged_many(prm, 0, s))) return rc;
+        if (many && (rc = launch_paged_many(prm, sm_count(), s))) return rc;
         if (bd.rows && (rc = D == 64 ? launch_combine<64>(prm, (long long)T * Hq, s) : launch_combine<128>(prm, (long long)T * Hq, s)))
             return rc;
     }

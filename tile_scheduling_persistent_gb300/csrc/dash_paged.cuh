@@ -26,8 +26,10 @@ constexpr int kFewSplitTiles = 4;  // at least this many stages per key range
 constexpr int kMaxSeqs = 1024;     // sequences per launch (their plan lies in shared memory)
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
 constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
-constexpr int kTileFullItems = 0;      // items that keep the GPU busy without a split
+constexpr int kTileFullItems = 76;     // items that keep the GPU busy without a split
 constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
+
+struct Plan;
 
 struct PagedParams {
     CUtensorMap tm_k, tm_v;        // [num_pages * Hkv][page_size][D], boxes of min(page_size, tile) rows
@@ -42,6 +44,7 @@ struct PagedParams {
     float2* part_ml;               // (m, l) of each
     long long max_rows;            // rows that part_o and part_ml hold
     int* counter;                  // many rows: next item
+    Plan* plan;                    // many rows: the launch's plan
     unsigned long long timeout_ns;
     int b0, nb;                    // the launch's sequences
     int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
@@ -203,6 +206,15 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool
         plan.rows[p.nb] = tr;
     }
     __syncthreads();
+}
+
+// The shared-memory plan to global memory, for the many-rows kernel that follows.
+__device__ __forceinline__ void publish_plan(const PagedParams& p, const Plan& plan) {
+    for (int i = threadIdx.x; i <= p.nb; i += blockDim.x) {
+        if (i < p.nb) p.plan->seq[i] = plan.seq[i];
+        p.plan->items[i] = plan.items[i];
+        p.plan->rows[i] = plan.rows[i];
+    }
 }
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

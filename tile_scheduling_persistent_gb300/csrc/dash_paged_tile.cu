@@ -1,12 +1,35 @@
 // dash_paged_tile.cu -- attention over a paged cache for sequences with many
-// rows (n * G > 16).
+// rows (n * G > 16): chunks of prompts, drafted tokens of wide groups.
 //
-// One warp per (token, query head), its keys one after another with a running
-// maximum m and sum l of the softmax:
-//   m' = max(m, s),  l = l 2^(m - m') + 2^(s - m'),  o = o 2^(m - m') + 2^(s - m') v
-// (scores in units of log2), o / l at the end.
+// The rows of a key/value head's group are packed: row r of a sequence is
+// token r / G, head r % G, so that one read of a key tile serves the whole
+// group.  An item is 2 matrix tiles of 128 / G tokens each (A and B, M = 128),
+// one key/value head and a range of 128-key tiles:
+//   S = Q K_j^T     (tcgen05, bf16, fp32 in tensor memory)
+//   P = 2^(scale log2e S - m), bf16 into the columns of S; l += row sums
+//   O += P V_j      (A = P from tensor memory)
+// A persistent CTA takes items from a counter (which CTA runs an item does not
+// touch its bits).  The two tiles take turns: while the softmax warps of one
+// work, the tensor core runs the other's products
+//   ... PV_A(j) S_A(j+1) | PV_B(j) S_B(j+1) | PV_A(j+1) ...
+// and both use each K and V tile once staged, so 256 rows share its reads.
+// S_A(j+1) follows PV_A(j) in the tensor core's order, so one S/P buffer per
+// tile suffices, and a completed S(j+1) says that O holds the sum through j:
+// rescaling O (when a row's maximum has grown by more than 2^8) needs no
+// further wait.
+//
+// Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
+// tensor memory, 2 item scheduler, 3 idle, 4-7 softmax and epilogue of tile A,
+// 8-11 of tile B, and for e4m3 caches 12-15 converters: they read codes from
+// the pages, one tile ahead, and store them as bf16 (exact) in the layout that
+// TMA gives a bf16 cache; the scales stay outside the products: ks multiplies
+// the score, vs the weight before it is rounded to bf16.
+//
+// Tensor memory: S/P of A at column 0, of B at 128; O of A at 256, of B at 384.
 #include <math.h>
+#include <string.h>
 
+#include "dash_bwd.cuh"
 #include "dash_internal.h"
 #include "dash_paged.cuh"
 
@@ -14,86 +37,644 @@ namespace dash {
 
 namespace {
 
+constexpr int kKvStages = 4;   // K0 V0 K1 V1 ...
+constexpr int kItemSlots = 2;
+
+enum TileBar : int {
+    T_Q_FULL = 0,
+    T_Q_EMPTY,
+    T_KV_FULL,
+    T_KV_EMPTY = T_KV_FULL + kKvStages,
+    T_S_FULL = T_KV_EMPTY + kKvStages,   // A, B
+    T_P_READY = T_S_FULL + 2,
+    T_O_FULL = T_P_READY + 2,
+    T_ITEM_FULL = T_O_FULL + 2,
+    T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
+    T_PATCH = T_ITEM_EMPTY + kItemSlots,
+    T_COUNT
+};
+
+// One item as its roles see it.
+struct TileItem {
+    int b;              // sequence, -1: no more items
+    int hk, tok;        // key/value head; first token (row of q)
+    int ntok;           // its tokens (tile A holds the first 128 / G)
+    int pos;            // position of the first
+    int lo, hi;         // keys that any row of the sequence sees
+    int len;
+    int t0, t1;         // key tiles
+    int split;          // > 0: the sequence's keys are split
+    long long part;     // partial row of the item's first row
+};
+
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(256) paged_row_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int E = D / 32;   // values of a vector per lane
-    const int lane = threadIdx.x & 31;
-    const long long w = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-    const int row = (int)(w / p.Hq), h = (int)(w % p.Hq);
-    if (row >= p.T) return;
-    int b, first, n;
-    if (p.cu_q) {
-        int lo = 0, hi = p.B;   // the last b with cu_q[b] <= row
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            (p.cu_q[mid] <= row ? lo : hi) = mid;
+struct TileCfg {
+    static constexpr int kTile = D * 128 * 2;
+    static constexpr int kNBox = D / 64;
+    static constexpr int OFF_Q = 0;                                  // A, B
+    static constexpr int OFF_KV = 2 * kTile;
+    static constexpr int OFF_SCALE = OFF_KV + kKvStages * kTile;     // [4 tiles][K, V][128] fp32
+    static constexpr int OFF_ITEM = OFF_SCALE + (kE4M3 ? 4 * 2 * 128 * 4 : 0);
+    static constexpr int OFF_BAR = OFF_ITEM + kItemSlots * 64;
+    static constexpr int OFF_CTL = OFF_BAR + T_COUNT * 8;            // tensor memory address, abort flag
+    // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
+    static constexpr int kSmem = OFF_CTL + 16 > 120000 ? OFF_CTL + 16 : 120000;
+    static constexpr int kThreads = kE4M3 ? 512 : 384;
+    static_assert(sizeof(TileItem) <= 64 && kSmem <= 232448, "shared memory budget");
+};
+
+struct TileWait {
+    volatile int* abort;
+    unsigned long long limit;
+};
+
+// Waits for a phase, at most the timeout; once a wait has run out (reported) no role waits any more and all reach their
+// end: false.
+__device__ __noinline__ bool tile_wait_slow(uint32_t bar, uint32_t parity, const TileWait& w) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*w.abort) return false;
+        if (ptx::globaltimer() - t0 > w.limit) {
+            serve_error(DASH_ERR_TIMEOUT, kOpAttn, blockIdx.x, 1, 0);
+            *w.abort = 1;
+            return false;
         }
-        b = lo;
-    } else {
-        b = row / (p.T / p.B);
     }
-    const Seq q0 = load_seq(p, b, false);
-    first = q0.first;
-    n = q0.n;
-    if (first < 0 || row - first >= n || row < first || few_rows(n, p.G) || b < p.b0 || b >= p.b0 + p.nb) return;
-    long long len = q0.len;
-    const long long pos = len - n + (row - first);
-    long long end = p.causal ? pos + 1 : len, begin = 0;
-    if (p.window && pos + 1 > p.window) begin = pos + 1 - p.window;
-    float q[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(p.q[row * p.q_t + h * p.q_h + lane * E + e]) * p.scale_log2e;
-        o[e] = 0.f;
+    return true;
+}
+__device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const TileWait& w) {
+    return ptx::mbar_try_wait(bar, parity) || tile_wait_slow(bar, parity, w);
+}
+// Every lane of a warp: all go on, or none.
+__device__ __forceinline__ bool tile_wait_warp(uint32_t bar, uint32_t parity, const TileWait& w) {
+    return __all_sync(0xffffffffu, tile_wait(bar, parity, w));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Codes in the high bytes of two halves to a bf16 pair, exactly: exponent and fraction bits move into place, which
+// leaves the value times 2^-120.
+__device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t x) {
+    const uint32_t t = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x7b807b80u));
+    return r;
+}
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_kernel(const __grid_constant__ PagedParams p) {
+    using C = TileCfg<D, kE4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
+    volatile int* const abort = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
+    const TileItem* const slots = reinterpret_cast<const TileItem*>(smem + C::OFF_ITEM);   // 64 bytes apart
+    auto BAR = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
+    const TileWait tw{abort, p.timeout_ns};
+    const int tpt = 128 / p.G;   // tokens of a matrix tile
+    const int trows = tpt * p.G;
+
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < T_COUNT; ++i) {
+            int count = 1;
+            if (kE4M3 && i >= T_KV_FULL && i < T_KV_FULL + kKvStages) count = 4;   // the converter warps
+            if (i >= T_P_READY && i < T_P_READY + 2) count = 4;
+            if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
+            ptx::mbar_init(BAR(i), count);
+        }
+        ptx::fence_mbar_init();
     }
-    const int hk = h / p.G;
-    float m = -INFINITY, l = 0.f;
-    for (long long j = begin; j < end; ++j) {
-        const int page = checked_page(p, b, (int)(j / p.c.page_size));
-        const long long cell = ((long long)page * p.c.Hkv + hk) * p.c.page_size + j % p.c.page_size;
-        float s = 0.f, v[E];
-        for (int e = 0; e < E; e += 2) {
-            const long long at = cell * D + lane * E + e;
-            float2 k2, v2;
-            if (kE4M3) {
-                k2 = unpack_e4m3x2(*reinterpret_cast<const uint16_t*>((const uint8_t*)p.c.k + at));
-                v2 = unpack_e4m3x2(*reinterpret_cast<const uint16_t*>((const uint8_t*)p.c.v + at));
-            } else {
-                k2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>((const __nv_bfloat16*)p.c.k + at));
-                v2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>((const __nv_bfloat16*)p.c.v + at));
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32((const void*)tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    wait_dependency();
+    launch_dependents();
+
+    // The items one after another: slot, its phase, and its release.
+    int iu = 0;   // items taken
+    auto next_item = [&](TileItem& it) -> bool {   // whole warps
+        const int s = iu % kItemSlots;
+        if (!tile_wait_warp(BAR(T_ITEM_FULL + s), (uint32_t)((iu / kItemSlots) & 1), tw)) return false;
+        it = *reinterpret_cast<const TileItem*>(reinterpret_cast<const uint8_t*>(slots) + 64 * s);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(BAR(T_ITEM_EMPTY + s));
+        ++iu;
+        return it.b >= 0;
+    };
+
+    if (warp == 0) {
+        // ================================================== producer
+        TileItem it;
+        int kv = 0, qn = 0, patches = 0;   // stages and Q loads so far
+        bool ok = true;
+        if (lane == 0) {
+            ptx::prefetch_tensormap(&p.tm_q);
+            ptx::prefetch_tensormap(&p.tm_k);
+            ptx::prefetch_tensormap(&p.tm_v);
+        }
+        const int page = p.c.page_size, rows = page < 128 ? page : 128, subs = 128 / rows;
+        while (ok && next_item(it)) {
+            if (it.t0 >= it.t1) continue;
+            const bool two = it.ntok > tpt;
+            if (qn > 0 && !tile_wait_warp(BAR(T_Q_EMPTY), (uint32_t)((qn - 1) & 1), tw)) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(BAR(T_Q_FULL), (two ? 2 : 1) * C::kNBox * trows * 128);
+#pragma unroll 1
+                for (int x = 0; x < (two ? 2 : 1); ++x)
+                    for (int bx = 0; bx < C::kNBox; ++bx)
+                        tma_load_4d(sbase + C::OFF_Q + x * C::kTile + bx * kBox, &p.tm_q, 64 * bx, 0, it.hk, it.tok + x * tpt,
+                                    BAR(T_Q_FULL));
             }
-            s += q[e] * k2.x + q[e + 1] * k2.y;
-            v[e] = v2.x, v[e + 1] = v2.y;
+            ++qn;
+            if (kE4M3) continue;
+            const int sub = lane / C::kNBox, box = lane % C::kNBox;
+            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(it.t1 * 128, it.hi) - 1) >> p.page_shift;
+            int eb = (it.t0 * 128) >> p.page_shift;
+            auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
+            int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
+            for (int t = it.t0; ok && t < it.t1; ++t) {
+                const int key = t * 128;
+                if ((key >> p.page_shift) - eb >= 32) {
+                    eb += 32;
+                    pages = next;
+                    next = fetch(eb + 32 + lane);
+                }
+                const int k0 = key + sub * rows;
+                const bool need = sub < subs && k0 + rows > it.lo && k0 < it.hi;
+                const int pg = __shfl_sync(0xffffffffu, pages, ((k0 >> p.page_shift) - eb) & 31);
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need)) * (uint32_t)rows * 128;
+                const bool patch = key < it.lo || key + 128 > it.hi;
+#pragma unroll 1
+                for (int val = 0; val < 2; ++val, ++kv) {
+                    const int st = kv % kKvStages;
+                    if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), (uint32_t)((kv / kKvStages - 1) & 1), tw)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
+                    // value rows that no row of the sequence sees (unwritten, freed) meet a zero weight: they must be
+                    // zero, so such a tile lands on the producer's own barrier first
+                    const bool own = patch && val;
+                    const uint32_t bar = own ? BAR(T_PATCH) : BAR(T_KV_FULL + st);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (need)
+                        ptx::tma_load_3d(dst + box * kBox + sub * rows * 128, val ? &p.tm_v : &p.tm_k, 64 * box, k0 & (page - 1),
+                                         pg * p.c.Hkv + it.hk, bar);
+                    if (own) {
+                        if (!tile_wait_warp(BAR(T_PATCH), (uint32_t)(patches & 1), tw)) {
+                            ok = false;
+                            break;
+                        }
+                        ++patches;
+#pragma unroll 1
+                        for (int i = lane; i < 128 * C::kNBox * 8; i += 32) {
+                            const int r = (i >> 3) & 127;
+                            if (key + r < it.lo || key + r >= it.hi) sts128(dst + (i >> 10) * kBox + (i & 1023) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                    }
+                }
+            }
         }
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        float vs = 1.f;
-        if (kE4M3) {
-            s *= p.c.k_scale[cell];
-            vs = p.c.v_scale[cell];
+        // a wait ran out: let the copies in flight land (bounded) before the CTA can end
+        if (*abort) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (ptx::globaltimer() - t0 < 1000000ull) {
+            }
         }
-        const float m2 = fmaxf(m, s), a = exp2f(m - m2), w2 = exp2f(s - m2);
-        l = l * a + w2;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + w2 * vs * v[e];
-        m = m2;
+    } else if (warp == 1) {
+        // ================================================== MMA issuer
+        TileItem it;
+        int kv = 0, qn = 0, pu[2] = {0, 0};
+        const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+        bool ok = true;
+        while (ok && next_item(it)) {
+            const int nk = it.t1 - it.t0;
+            if (nk <= 0) continue;
+            const int tiles = it.ntok > tpt ? 2 : 1;
+            if (lane == 0) {
+                auto full = [&](int u) { return tile_wait(BAR(T_KV_FULL + u % kKvStages), (uint32_t)((u / kKvStages) & 1), tw); };
+                auto sKV = [&](int u) { return sbase + C::OFF_KV + (uint32_t)(u % kKvStages) * C::kTile; };
+                ok = tile_wait(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw) && full(kv);
+                if (ok) {
+                    ptx::tc_fence_after();
+                    for (int x = 0; x < tiles; ++x) {
+                        issue_s<D, D / 16>(tS[x], sbase + C::OFF_Q + x * C::kTile, sKV(kv));
+                        ptx::tc_commit(BAR(T_S_FULL + x));
+                    }
+                    ptx::tc_commit(BAR(T_KV_EMPTY + kv % kKvStages));
+                    if (nk == 1) ptx::tc_commit(BAR(T_Q_EMPTY));
+                }
+                for (int j = 0; ok && j < nk; ++j) {
+                    const int uv = kv + 2 * j + 1, uk = uv + 1;
+                    const bool more = j + 1 < nk;
+                    if (!full(uv)) ok = false;
+                    for (int x = 0; ok && x < tiles; ++x) {
+                        if (!tile_wait(BAR(T_P_READY + x), (uint32_t)(pu[x] & 1), tw)) {
+                            ok = false;
+                            break;
+                        }
+                        ++pu[x];
+                        ptx::tc_fence_after();
+                        issue_dv<D, 8>(tO[x], tS[x], sKV(uv), j > 0 ? 1u : 0u);   // O (+)= P V_j
+                        if (x == tiles - 1) ptx::tc_commit(BAR(T_KV_EMPTY + uv % kKvStages));
+                        if (more) {
+                            if (x == 0 && !full(uk)) {
+                                ok = false;
+                                break;
+                            }
+                            ptx::tc_fence_after();
+                            issue_s<D, D / 16>(tS[x], sbase + C::OFF_Q + x * C::kTile, sKV(uk));
+                            ptx::tc_commit(BAR(T_S_FULL + x));
+                            if (x == tiles - 1) {
+                                ptx::tc_commit(BAR(T_KV_EMPTY + uk % kKvStages));
+                                if (j + 2 == nk) ptx::tc_commit(BAR(T_Q_EMPTY));
+                            }
+                        } else {
+                            ptx::tc_commit(BAR(T_O_FULL + x));
+                        }
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            kv += 2 * nk;
+            ++qn;
+        }
+        // after a wait that ran out, the products in flight end before tensor memory is freed (below, after the barrier);
+        // otherwise every product has been waited for
+        if (*abort) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (ptx::globaltimer() - t0 < 1000000ull) {
+            }
+        }
+    } else if (warp == 2) {
+        // ================================================== scheduler
+        const Plan* plan = p.plan;
+        const int items = plan->items[p.nb];
+        for (int u = 0;; ++u) {
+            int item = 0;
+            if (lane == 0) item = atomicAdd(p.counter, 1);
+            item = __shfl_sync(0xffffffffu, item, 0);
+            const int s = u % kItemSlots;
+            if (u >= kItemSlots && !tile_wait_warp(BAR(T_ITEM_EMPTY + s), (uint32_t)((u / kItemSlots - 1) & 1), tw)) break;
+            TileItem it;
+            it.b = -1;
+            if (item < items) {
+                int lo = 0, hi = p.nb;   // the last sequence with items[i] <= item (it has items of its own)
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+                    const unsigned le = __ballot_sync(0xffffffffu, at < hi && plan->items[at] <= item);
+                    const int k = 31 - __clz(le);   // lane 0 always holds
+                    lo += k * step;
+                    hi = min(hi, lo + step);
+                }
+                const Seq q = plan->seq[lo];
+                const Cut c = cut_many(p, q, tokens_per_item(p.G));
+                const int local = item - plan->items[lo];
+                const int per = p.c.Hkv * c.ns, row_tiles = c.items / per;
+                const int rt = row_tiles - 1 - local / per;   // the longest causal rows first
+                const int split = (local % per) / p.c.Hkv;
+                const int i0 = rt * tokens_per_item(p.G);
+                it.b = p.b0 + lo;
+                it.hk = local % p.c.Hkv;
+                it.tok = q.first + i0;
+                it.ntok = min(tokens_per_item(p.G), q.n - i0);
+                it.pos = q.len - q.n + i0;
+                it.lo = c.lo;
+                it.hi = c.hi;
+                it.len = q.len;
+                it.split = c.ns > 1;
+                it.part = plan->rows[lo] + ((long long)split * p.c.Hkv + it.hk) * q.n * p.G + (long long)i0 * p.G;
+                int klo, khi;   // keys seen by the item's rows
+                seen_keys(p, q, i0, i0 + it.ntok, klo, khi);
+                const int first = c.lo / 128 + split * c.st;
+                it.t0 = max(first, klo / 128);
+                it.t1 = min(first + c.st, khi > klo ? (khi + 127) / 128 : 0);
+            }
+            if (lane == 0) {
+                *reinterpret_cast<TileItem*>(smem + C::OFF_ITEM + 64 * s) = it;
+                ptx::mbar_arrive(BAR(T_ITEM_FULL + s));
+            }
+            __syncwarp();
+            if (it.b < 0) break;
+        }
+    } else if (warp >= 4 && warp < 12) {
+        // ================================================== softmax and epilogue, one row per thread
+        const int x_ = (warp - 4) >> 2;   // tile A or B
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lane_off + 128u * (uint32_t)x_, tO = tmem + lane_off + 256u + 128u * (uint32_t)x_;
+        const float c = p.scale_log2e;
+        TileItem it;
+        int su = 0, ou = 0, kt = 0;   // S and O phases, key tiles of all items
+        bool ok = true;
+        while (ok && next_item(it)) {
+            const int nk = it.t1 - it.t0;
+            const int i = x_ * tpt + row / p.G;           // token of the item
+            const bool mine = x_ == 0 || it.ntok > tpt;   // the tile exists
+            const bool valid = mine && row < trows && i < it.ntok;
+            if (!mine) {
+                kt += nk > 0 ? nk : 0;
+                continue;
+            }
+            // this row's keys, and the key tiles that every row of the tile sees whole
+            const int pos = it.pos + i;
+            const int hi_r = p.causal ? pos + 1 : it.len, lo_r = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
+            const int pos0 = it.pos + x_ * tpt, pos1 = min(it.pos + it.ntok - 1, pos0 + tpt - 1);
+            const int full_hi = p.causal ? pos0 + 1 : it.len, full_lo = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < nk; ++j, ++su) {
+                if (!tile_wait_warp(BAR(T_S_FULL + x_), (uint32_t)(su & 1), tw)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                // Two passes over the scores, 32 columns at a time out of tensor memory: the maximum, then the weights.
+                // Holding all 128 in registers instead would not leave room for the next columns' loads.
+                const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + ((kt + j) & 3) * 256;
+                const int key = (it.t0 + j) * 128;
+                const bool edge = key < full_lo || key + 128 > full_hi;
+                const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
+                uint32_t r[2][32];
+                float part[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) part[k] = -INFINITY;
+                ptx::tmem_ld32(tS, r[0]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    ptx::tmem_ld_wait();
+                    if (h < 3) ptx::tmem_ld32(tS + 32 * (h + 1), r[(h + 1) & 1]);
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[h & 1][k]);
+                    if (kE4M3) {   // the keys' scales, times scale log2e
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 s4 = *reinterpret_cast<const float4*>(sc + 32 * h + k);
+                            const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
+                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                        }
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) part[k & 7] = fmaxf(part[k & 7], x[k]);
+                }
+                ptx::tmem_ld32(tS, r[0]);
+                const float mx = (kE4M3 ? 1.f : c) * fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
+                                                           fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
+                const bool raise = __any_sync(0xffffffffu, valid && mx > m_ref + 8.f);
+                if (raise) {
+                    const float m_new = fmaxf(m_ref, mx);
+                    const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref - m_new);
+                    m_ref = m_new;
+                    l *= alpha;
+                    if (j > 0) {
+                        ptx::tmem_ld_wait();   // r[0] is in flight
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            ptx::tmem_ld32(tO + 32 * cc, r[1]);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * alpha);
+                            ptx::tmem_st32(tO + 32 * cc, r[1]);
+                        }
+                    }
+                }
+                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) part[k] = 0.f;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    ptx::tmem_ld_wait();
+                    if (h < 3) ptx::tmem_ld32(tS + 32 * (h + 1), r[(h + 1) & 1]);
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float* s = reinterpret_cast<const float*>(&r[h & 1][k]);
+                        float4 s4 = make_float4(c, c, c, c);
+                        if (kE4M3) s4 = *reinterpret_cast<const float4*>(sc + 32 * h + k);
+                        const ptx::f2 u = ptx::fma2({s[0], s[1]}, {s4.x, s4.y}, {-m_use, -m_use});
+                        const ptx::f2 v = ptx::fma2({s[2], s[3]}, {s4.z, s4.w}, {-m_use, -m_use});
+                        x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        x[k] = ptx::ex2(x[k]);
+                        x[k + 1] = ptx::ex2(x[k + 1]);
+                        const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, {x[k], x[k + 1]});
+                        part[k & 7] = s.x;
+                        part[(k + 1) & 7] = s.y;
+                    }
+                    // P (with the values' scales) rounded to bf16, keys [0,64) -> columns [0,32), [64,128) -> [64,96)
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        if (kE4M3) {
+                            const float4 s4 = *reinterpret_cast<const float4*>(sc + 128 + 32 * h + k);
+                            const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
+                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                        }
+                        pk[k / 2] = pack_bf16(x[k], x[k + 1]);
+                        pk[k / 2 + 1] = pack_bf16(x[k + 2], x[k + 3]);
+                    }
+                    ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
+                }
+                l += ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + x_));
+            }
+            if (!ok) break;
+            kt += nk > 0 ? nk : 0;
+            if (nk > 0) {
+                if (!tile_wait_warp(BAR(T_O_FULL + x_), (uint32_t)(ou & 1), tw)) break;
+                ++ou;
+                ptx::tc_fence_after();
+            }
+            const int g = row % p.G;
+            const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
+            const long long pr = it.part + (long long)i * p.G + g;
+            const float inv = (it.split || !(l > 0.f)) ? 1.f : 1.f / l;
+            const bool empty = !(l > 0.f);
+            const bool keep = it.split && valid && pr < p.max_rows;
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t r[32];
+                if (nk > 0) {
+                    ptx::tmem_ld32(tO + 32 * cc, r);
+                    ptx::tmem_ld_wait();
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) r[k] = (nk <= 0 || empty) ? 0u : __float_as_uint(__uint_as_float(r[k]) * inv);
+                if (keep) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4*>(p.part_o + pr * D + 32 * cc + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                } else if (!it.split && valid) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        *reinterpret_cast<uint4*>(p.o + at * D + 32 * cc + k) =
+                            make_uint4(pack_bf16(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
+                                       pack_bf16(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])),
+                                       pack_bf16(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5])),
+                                       pack_bf16(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7])));
+                }
+            }
+            if (keep)
+                p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref, empty ? 0.f : l);
+            else if (!it.split && valid && p.lse)
+                p.lse[at] = empty ? -INFINITY : (m_ref + log2f(l)) * kLn2P;
+            ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
+        }
+    } else if (kE4M3 && warp >= 12) {
+        // ================================================== converters
+        constexpr int kChunks = D / 16;         // 16-byte chunks of codes per key
+        constexpr int kRows = 32 / kChunks;     // keys that one load instruction of a warp covers
+        constexpr int kLoads = 32 / kRows;      // loads of a warp's 32 keys of a tile
+        const int cw = warp - 12, chunk = lane % kChunks, sub = lane / kChunks;
+        TileItem it;
+        int kv = 0, kt = 0;
+        bool ok = true;
+        while (ok && next_item(it)) {
+            const int nk = it.t1 - it.t0;
+            if (nk <= 0) continue;
+            // codes of key 128 t + 32 cw + kRows l + sub, chunk `chunk`; keys outside the sequence's read as zero
+            // (a key's two scales come with its codes of K: the softmax needs both before V is staged)
+            auto load = [&](int u, uint4 (&w)[kLoads], float& ks, float& vs) {
+                const int t = it.t0 + (u >> 1);
+                const uint8_t* base = (const uint8_t*)((u & 1) ? p.c.v : p.c.k);
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
+                    const int key = 128 * t + 32 * cw + kRows * l + sub;
+                    w[l] = make_uint4(0, 0, 0, 0);
+                    if (key >= it.lo && key < it.hi) {
+                        const long long cell = ((long long)checked_page(p, it.b, key >> p.page_shift) * p.c.Hkv + it.hk) * p.c.page_size +
+                                               (key & (p.c.page_size - 1));
+                        w[l] = *reinterpret_cast<const uint4*>(base + cell * D + 16 * chunk);
+                    }
+                }
+                if (u & 1) return;
+                const int key = 128 * t + 32 * cw + lane;
+                ks = vs = 0.f;
+                if (key >= it.lo && key < it.hi) {
+                    const long long cell = ((long long)checked_page(p, it.b, key >> p.page_shift) * p.c.Hkv + it.hk) * p.c.page_size +
+                                           (key & (p.c.page_size - 1));
+                    ks = p.c.k_scale[cell] * p.scale_log2e;
+                    vs = p.c.v_scale[cell];
+                }
+            };
+            uint4 w[kLoads];
+            float ks, vs;
+            load(0, w, ks, vs);
+            for (int u = 0; u < 2 * nk; ++u, ++kv) {
+                const int st = kv % kKvStages;
+                if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), (uint32_t)((kv / kKvStages - 1) & 1), tw)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
+                if (!(u & 1)) {
+                    float* sc = reinterpret_cast<float*>(smem + C::OFF_SCALE) + ((kt + (u >> 1)) & 3) * 256 + 32 * cw + lane;
+                    sc[0] = ks;
+                    sc[128] = vs;
+                }
+                uint4 cur[kLoads];
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) cur[l] = w[l];
+                if (u + 1 < 2 * nk) load(u + 1, w, ks, vs);
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
+                    const int row = 32 * cw + kRows * l + sub;
+                    const uint32_t c4[4] = {cur[l].x, cur[l].y, cur[l].z, cur[l].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        o[2 * y] = bf16x2_of_e4m3(__byte_perm(c4[y], 0u, 0x1404));
+                        o[2 * y + 1] = bf16x2_of_e4m3(__byte_perm(c4[y], 0u, 0x3424));
+                    }
+                    // 16 values = two 16-byte chunks of the bf16 row; lanes of the upper half of a 128-value row store them
+                    // in the other order, which keeps the two boxes' banks apart
+                    const uint32_t line = dst + ((2 * chunk) >> 3) * kBox + row * 128;
+                    const int c0 = (2 * chunk) & 7, flip = (D == 128 && chunk >= 4) ? 1 : 0;
+                    const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
+                    sts128(line + (((c0 + flip) ^ (row & 7)) << 4), flip ? v1 : v0);
+                    sts128(line + (((c0 + 1 - flip) ^ (row & 7)) << 4), flip ? v0 : v1);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+            }
+            kt += nk;
+        }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int e = 0; e < E; ++e) p.o[((long long)row * p.Hq + h) * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-    if (p.lse && lane == 0) p.lse[(long long)row * p.Hq + h] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool kE4M3>
+int launch_tile_t(const PagedParams& p, int grid, cudaStream_t s) {
+    using C = TileCfg<D, kE4M3>;
+    static bool ready[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
+    if (!ready[dev]) {
+        if (cudaFuncSetAttribute(paged_tile_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+            return DASH_ERR_CUDA;
+        ready[dev] = true;
+    }
+    paged_tile_kernel<D, kE4M3><<<grid, C::kThreads, C::kSmem, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // namespace
 
 int take_error_tile(int* out5) { return take_serve_error(out5); }
 
-int launch_paged_many(const PagedParams& p, int, cudaStream_t s) {
-    const unsigned blocks = (unsigned)(((long long)p.T * p.Hq + 7) / 8);
-    if (p.c.type == DASH_CACHE_E4M3) {
-        if (p.c.D == 64) paged_row_kernel<64, true><<<blocks, 256, 0, s>>>(p);
-        else paged_row_kernel<128, true><<<blocks, 256, 0, s>>>(p);
-    } else {
-        if (p.c.D == 64) paged_row_kernel<64, false><<<blocks, 256, 0, s>>>(p);
-        else paged_row_kernel<128, false><<<blocks, 256, 0, s>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+int launch_paged_many(const PagedParams& few, int grid, cudaStream_t s) {
+    PagedParams p = few;
+    const int rows = p.c.page_size < 128 ? p.c.page_size : 128;
+    const long long heads = (long long)p.c.num_pages * p.c.Hkv;
+    const bool e4m3 = p.c.type == DASH_CACHE_E4M3;
+    if ((!e4m3 && (make_tmap_pages(&p.tm_k, p.c.k, heads, p.c.page_size, p.c.D, false, rows) ||
+                   make_tmap_pages(&p.tm_v, p.c.v, heads, p.c.page_size, p.c.D, false, rows))) ||
+        make_tmap_rows(&p.tm_q, p.q, p.T, p.q_t, p.c.Hkv, p.G, p.q_h, p.c.D, 128 / p.G))
+        return DASH_ERR_CUDA;
+    if (e4m3) return p.c.D == 64 ? launch_tile_t<64, true>(p, grid, s) : launch_tile_t<128, true>(p, grid, s);
+    return p.c.D == 64 ? launch_tile_t<64, false>(p, grid, s) : launch_tile_t<128, false>(p, grid, s);
 }
 
 }  // namespace dash
