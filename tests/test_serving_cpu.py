@@ -11,7 +11,31 @@ import torch
 from oracle import serving as V
 from tile_scheduling_persistent_gb300 import dash
 
-P = ctypes.c_void_p
+P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class Heads(ctypes.Structure):       # dash_heads
+    _fields_ = [("data", P), ("fp32", I), ("heads", I), ("stride_b", Z), ("stride_h", Z), ("stride_s", Z)]
+
+
+class Cache(ctypes.Structure):       # dash_kv_cache
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("type", I), ("num_pages", I), ("page_size", I),
+                ("Hkv", I), ("D", I)]
+
+
+class WriteRope(ctypes.Structure):   # dash_write_rope
+    _fields_ = [("inv_freq", P), ("positions", P), ("rot", I), ("interleaved", I), ("factor", ctypes.c_float), ("q", P),
+                ("q_stride_t", Z), ("q_stride_h", Z), ("q_out", P), ("q_out_stride_t", Z), ("q_out_stride_h", Z), ("Hq", I)]
+
+
+def test_the_bindings_layouts_are_the_structs():
+    for packed, cls in ((dash._HEADS, Heads), (dash._CACHE, Cache), (dash._WRITE_ROPE, WriteRope)):
+        assert packed.size == ctypes.sizeof(cls)
+        values = list(range(1, len(cls._fields_) + 1))
+        got = cls.from_buffer_copy(packed.pack(*values))
+        assert [getattr(got, f) for f, _ in cls._fields_] == values
+
+
 OK, BAD = 4096, 4098   # an aligned and a misaligned address, never dereferenced
 
 
@@ -55,7 +79,7 @@ def test_rope_freqs_refuses(L, kw):
 
 
 def heads(data=OK, fp32=0, n=2, sb=512, sh=128, ss=256):
-    return dash._Heads(data, fp32, n, sb, sh, ss)
+    return Heads(data, fp32, n, sb, sh, ss)
 
 
 FREQ = (ctypes.c_double * 64)(*[1.0 / (i + 1) for i in range(64)])
@@ -87,7 +111,7 @@ def test_empty_calls_do_nothing(L):
 
 
 def cache(k=OK, v=OK, ks=None, vs=None, typ=0, pages=4, page=16, H=2, D=64):
-    return dash._Cache(k, v, ks, vs, typ, pages, page, H, D)
+    return Cache(k, v, ks, vs, typ, pages, page, H, D)
 
 
 BAD_CACHES = [cache(k=None), cache(v=BAD), cache(ks=OK, vs=OK), cache(typ=1), cache(typ=1, ks=OK), cache(typ=1, ks=OK, vs=BAD),
@@ -101,7 +125,7 @@ def call_write(L, c=None, k=OK, ks=(128, 64), v=OK, vs=(128, 64), slots=OK, T=3,
 
 
 def write_rope(freq=FREQ, positions=OK, rot=64, inter=0, factor=1.0, q=OK, qs=(256, 64), q_out=2 * OK, qo=(256, 64), Hq=4):
-    return dash._WriteRope(ctypes.cast(freq, P) if freq else None, positions, rot, inter, factor, q, *qs, q_out, *qo, Hq)
+    return WriteRope(ctypes.cast(freq, P) if freq else None, positions, rot, inter, factor, q, *qs, q_out, *qo, Hq)
 
 
 @pytest.mark.parametrize("kw", [dict(c=c) for c in BAD_CACHES] + [

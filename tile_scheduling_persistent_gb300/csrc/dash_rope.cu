@@ -336,12 +336,16 @@ int launched() { return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_C
 }  // namespace
 
 int serve_check_device() {
+    static int known[64] = {};   // 1: sm_103
     int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+    if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
+    if (dev >= 0 && dev < 64 && known[dev]) return DASH_OK;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return DASH_ERR_CUDA;
-    return (major == 10 && minor == 3) ? DASH_OK : DASH_ERR_DEVICE;
+    if (major != 10 || minor != 3) return DASH_ERR_DEVICE;
+    if (dev >= 0 && dev < 64) known[dev] = 1;
+    return DASH_OK;
 }
 
 int take_error_rope(int* out5) { return take_serve_error(out5); }

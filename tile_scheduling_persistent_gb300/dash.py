@@ -7,7 +7,9 @@ streams come from PyTorch); the library fails loudly if it is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 import torch
@@ -50,22 +52,11 @@ class _DebugOpts(ctypes.Structure):
                 ("head_split", ctypes.c_int)]
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("fp32", ctypes.c_int), ("heads", ctypes.c_int),
-                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
-
-
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int), ("num_pages", ctypes.c_int),
-                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
-
-
-class _WriteRope(ctypes.Structure):
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("factor", ctypes.c_float), ("q", ctypes.c_void_p),
-                ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64), ("q_out", ctypes.c_void_p),
-                ("q_out_stride_t", ctypes.c_int64), ("q_out_stride_h", ctypes.c_int64), ("Hq", ctypes.c_int)]
+# The structs of the rotary and paged calls (dash_heads, dash_kv_cache, dash_write_rope): packed natively, which
+# costs a fifth of a ctypes.Structure on calls that last a few microseconds.
+_HEADS = struct.Struct("@Piiqqq")
+_CACHE = struct.Struct("@PPPPiiiii0P")
+_WRITE_ROPE = struct.Struct("@PPiifPqqPqqi0P")
 
 
 _lib = None
@@ -96,12 +87,12 @@ def lib():
     L.dash_sim_schedule_cross.argtypes = [I] * 7 + [D, D, ctypes.POINTER(D), P, ctypes.POINTER(ctypes.c_int64)]
     L.dash_sim_check_ranks.argtypes = [I] * 7 + [P]
     L.dash_debug_tile_probe.argtypes = [P] * 6 + [I, I] + [P] * 7
-    L64, HP = ctypes.c_int64, ctypes.POINTER(_Heads)
-    L.dash_rope.argtypes = [HP, HP, HP, HP, P, L64, P, I, I, ctypes.c_float, I, I, I, I, P]
+    L64 = ctypes.c_int64
+    L.dash_rope.argtypes = [P, P, P, P, P, L64, P, I, I, ctypes.c_float, I, I, I, I, P]
     L.dash_rope_freqs.argtypes = [I, D, I, D, I, D, D, P, ctypes.POINTER(ctypes.c_float)]
-    L.dash_kv_write.argtypes = [ctypes.POINTER(_Cache), P, L64, L64, P, L64, L64, P, I, ctypes.POINTER(_WriteRope), P]
-    L.dash_kv_read.argtypes = [ctypes.POINTER(_Cache), P, L64, I, P, P, P, L64, L64, L64, I, I, P]
-    L.dash_attn_paged.argtypes = [P, L64, L64, ctypes.POINTER(_Cache), P, L64, I, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+    L.dash_kv_write.argtypes = [P, P, L64, L64, P, L64, L64, P, I, P, P]
+    L.dash_kv_read.argtypes = [P, P, L64, I, P, P, P, L64, L64, L64, I, I, P]
+    L.dash_attn_paged.argtypes = [P, L64, L64, P, P, L64, I, P, P, P, P, I, I, I, I, I, I, P, Z, P]
     L.dash_attn_paged_workspace.argtypes = [I, I, I, I, I, I, L64, ctypes.POINTER(Z)]
     L.dash_get_status_paged.argtypes = [P, ctypes.POINTER(I), ctypes.POINTER(I)]
     for name in EXPORTS:
@@ -344,67 +335,81 @@ def tile_probe(k, v, q, do, lse, delta, diag=False):
 
 # ------------------------------------------------------------------ rotary positions, paged cache, paged attention
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wave": 3, "ramp": 4}
+_BF16, _F32, _I32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
-def _need(ok, what, why):
-    """Arguments that the C entry cannot see (tensor shapes, types, devices)."""
-    if not ok:
-        err = DashError(ERR_ARG, what)
-        err.args = (err.args[0] + ": " + why,)
-        raise err
+def _refuse(what, why):
+    """Arguments that the C entry cannot see: tensor shapes, types, devices."""
+    err = DashError(ERR_ARG, what)
+    err.args = (err.args[0] + ": " + why,)
+    raise err
 
 
-def _data(t, dtype, what, name, shape=None):
-    """The address of a CUDA tensor of the current device, contiguous in its last dimension."""
-    if t.dtype is not dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        _need(False, what, "%s is a %s tensor on the current CUDA device" % (name, dtype))
-    if shape is not None and tuple(t.shape) != shape:
-        _need(False, what, "%s has shape %s" % (name, shape))
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        _need(False, what, "%s is contiguous in its last dimension" % name)
+def _device_stream(stream, what):
+    """The current device, on which every tensor has to be, and the address of the stream (None: its current one)."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, (_raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream)
+    if stream.device_index != dev:
+        _refuse(what, "the stream belongs to the current device")
+    return dev, stream.cuda_stream
+
+
+def _flat(t, dtype, dev, what, name):
+    """The address of a contiguous tensor."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(what, "%s is a contiguous %s tensor on the current CUDA device" % (name, dtype))
     return t.data_ptr()
 
 
-def _flat(t, dtype, what, name, shape=None):
-    """_data of a contiguous tensor."""
-    p = _data(t, dtype, what, name, shape)
-    if not t.is_contiguous():
-        _need(False, what, "%s is contiguous" % name)
-    return p
+def _shaped(t, dtype, dev, what, name, shape):
+    if t.shape != shape:
+        _refuse(what, "%s has shape %s" % (name, tuple(shape)))
+    return _flat(t, dtype, dev, what, name)
 
 
-def _heads(t, what, name):
+def _rows(t, dtype, dev, what, name, dims):
+    """The address and strides of a tensor whose last dimension is contiguous; strides of single elements read as 0."""
+    st, sh = t.stride(), t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(sh) != dims or (st[-1] != 1 and sh[-1] > 1):
+        _refuse(what, "%s is a %d-dimensional %s tensor on the current CUDA device, contiguous in its last dimension" % (
+            name, dims, dtype))
+    return t.data_ptr(), [x if n > 1 else 0 for x, n in zip(st, sh)]
+
+
+def _heads(t, dev, what, name):
     """dash_heads of a [B, H, S, D] tensor."""
-    fp32 = t.dtype is torch.float32
-    p = _data(t, torch.float32 if fp32 else torch.bfloat16, what, name)
-    _need(t.dim() == 4, what, "%s is [B, H, S, D]" % name)
-    sb, sh, ss, _ = t.stride()
-    B, H, S, _ = t.shape
-    return _Heads(p, fp32, H, sb if B > 1 else 0, sh if H > 1 else 0, ss if S > 1 else 0)
+    dtype = t.dtype if t.dtype is _F32 else _BF16
+    p, (sb, sh, ss, _) = _rows(t, dtype, dev, what, name, 4)
+    return _HEADS.pack(p, dtype is _F32, t.shape[1], sb, sh, ss)
 
 
-def _cache(k, v, k_scale, v_scale, what):
-    _need(k.dim() == 4, what, "the cache is [num_pages, Hkv, page_size, D]")
-    N, H, page, D = shape = tuple(k.shape)
-    if k.dtype is torch.bfloat16:
-        _need(k_scale is None and v_scale is None, what, "a bf16 cache has no scales")
-        return _Cache(_flat(k, k.dtype, what, "k_cache"), _flat(v, k.dtype, what, "v_cache", shape), None, None, 0,
-                      N, page, H, D)
-    e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    _need(k_scale is not None and v_scale is not None, what, "an e4m3 cache has k_scale and v_scale")
-    return _Cache(_flat(k, e4m3, what, "k_cache"), _flat(v, e4m3, what, "v_cache", shape),
-                  _flat(k_scale, f32, what, "k_scale", shape[:3]), _flat(v_scale, f32, what, "v_scale", shape[:3]), 1,
-                  N, page, H, D)
+def _cache(k, v, k_scale, v_scale, dev, what):
+    """dash_kv_cache, its Hkv, page_size and D."""
+    shape = k.shape
+    if len(shape) != 4:
+        _refuse(what, "the cache is [num_pages, Hkv, page_size, D]")
+    N, H, page, D = shape
+    if k.dtype is _BF16:
+        if k_scale is not None or v_scale is not None:
+            _refuse(what, "a bf16 cache has no scales")
+        return _CACHE.pack(_flat(k, _BF16, dev, what, "k_cache"), _shaped(v, _BF16, dev, what, "v_cache", shape), 0, 0,
+                           0, N, page, H, D), H, page, D
+    if k_scale is None or v_scale is None:
+        _refuse(what, "an e4m3 cache has k_scale and v_scale")
+    return _CACHE.pack(_flat(k, _E4M3, dev, what, "k_cache"), _shaped(v, _E4M3, dev, what, "v_cache", shape),
+                       _shaped(k_scale, _F32, dev, what, "k_scale", shape[:3]),
+                       _shaped(v_scale, _F32, dev, what, "v_scale", shape[:3]), 1, N, page, H, D), H, page, D
 
 
 def _freqs(inv_freq, what):
-    if isinstance(inv_freq, torch.Tensor):
-        _need(not inv_freq.is_cuda and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
-              and inv_freq.is_contiguous(), what, "inv_freq is a float64 vector on the host")
-        return inv_freq, inv_freq.data_ptr(), 2 * inv_freq.shape[0]
-    a = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    _need(a.ndim == 1, what, "inv_freq is a float64 vector on the host")
-    return a, a.ctypes.data, 2 * a.shape[0]
+    """inv_freq as something to keep alive, its address and the rotated width."""
+    if not isinstance(inv_freq, torch.Tensor):
+        inv_freq = torch.as_tensor(np.ascontiguousarray(inv_freq, dtype=np.float64))
+    if inv_freq.dtype is not torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        _refuse(what, "inv_freq is a contiguous float64 vector on the host")
+    return inv_freq, inv_freq.data_ptr(), 2 * inv_freq.shape[0]
 
 
 def rope_freqs(rot, base=10000.0, scaling="none", scale=1.0, trained=0, lo=1.0, hi=4.0):
@@ -424,29 +429,28 @@ def rope(x, y, inv_freq, positions=None, x2=None, y2=None, interleaved=False, fa
     inv_freq: float64 [rot/2] on the host (rope_freqs); inverse=True is the
     backward (y = dL/dx for x = dL/dy).  y may be x."""
     what = "dash_rope"
+    dev, st = _device_stream(stream, what)
     keep, freqs, rot = _freqs(inv_freq, what)
-    a, b = _heads(x, what, "x"), _heads(y, what, "y")
-    _need(x.shape == y.shape, what, "y has the shape of x")
+    a, b = _heads(x, dev, what, "x"), _heads(y, dev, what, "y")
     B, _, S, D = x.shape
+    if x.shape != y.shape:
+        _refuse(what, "y has the shape of x")
     a2 = b2 = None
-    if x2 is not None:
-        _need(y2 is not None and x2.shape == y2.shape and x2.dim() == 4 and x2.shape[0] == B
-              and x2.shape[2:] == x.shape[2:], what, "x2 and y2 are [B, H2, S, D]")
-        a2, b2 = ctypes.byref(_heads(x2, what, "x2")), ctypes.byref(_heads(y2, what, "y2"))
-    else:
-        _need(y2 is None, what, "y2 needs x2")
+    if x2 is not None and y2 is not None:
+        a2, b2 = _heads(x2, dev, what, "x2"), _heads(y2, dev, what, "y2")
+        if x2.shape != y2.shape or x2.shape[0] != B or x2.shape[2] != S or x2.shape[3] != D:
+            _refuse(what, "x2 and y2 are [B, H2, S, D]")
+    elif x2 is not None or y2 is not None:
+        _refuse(what, "x2 and y2 go together")
     pos, pos_b = None, 0
     if positions is not None:
-        pos = _data(positions, torch.int32, what, "positions")
-        _need(tuple(positions.shape) in ((S,), (B, S)), what, "positions is [S] or [B, S]")
-        pos_b = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    _check(lib().dash_rope(ctypes.byref(a), ctypes.byref(b), a2, b2, pos, pos_b, freqs, rot, int(bool(interleaved)),
-                           float(factor), int(bool(inverse)), B, S, D, _stream(stream)), what)
-
-
-def _token_strides(t):
-    """Strides of tokens and heads; those of a single one do not matter."""
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+        pos, pst = _rows(positions, _I32, dev, what, "positions", positions.dim())
+        if positions.shape != (S,):
+            if positions.shape != (B, S):
+                _refuse(what, "positions is [S] or [B, S]")
+            pos_b = pst[0]
+    _check(lib().dash_rope(a, b, a2, b2, pos, pos_b, freqs, rot, bool(interleaved), factor, bool(inverse), B, S, D, st),
+           what)
 
 
 def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq=None, positions=None,
@@ -457,35 +461,40 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
     vector with its own scale.  inv_freq and positions int32 [T]: k is rotated on
     the way (see rope), and q [T, Hq, D] into q_out."""
     what = "dash_kv_write"
-    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
-    bf = torch.bfloat16
-    T, shape = k.shape[0], (k.shape[0], c.Hkv, c.D)
-    kp, vp = _data(k, bf, what, "k", shape), _data(v, bf, what, "v", shape)
-    sp = _flat(slots, torch.int64, what, "slots", (T,))
+    dev, st = _device_stream(stream, what)
+    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    (kp, (kt, kh, _)), (vp, (vt, vh, _)) = _rows(k, _BF16, dev, what, "k", 3), _rows(v, _BF16, dev, what, "v", 3)
+    T = k.shape[0]
+    if k.shape != (T, Hkv, D) or v.shape != k.shape:
+        _refuse(what, "k and v are [T, Hkv, D]")
+    sp = _shaped(slots, _I64, dev, what, "slots", (T,))
     r = keep = None
     if inv_freq is not None:
-        _need(positions is not None, what, "a rotation needs positions")
+        if positions is None:
+            _refuse(what, "a rotation needs positions")
         keep, freqs, rot = _freqs(inv_freq, what)
-        r = _WriteRope(freqs, _flat(positions, torch.int32, what, "positions", (T,)), rot, int(bool(interleaved)),
-                       float(factor))
+        qp = qt = qh = op = ot = oh = Hq = 0
         if q is not None:
-            _need(q_out is not None and q.dim() == 3 and q.shape[0] == T and q.shape[2] == c.D, what,
-                  "q and q_out are [T, Hq, D]")
-            r.q, r.q_out = _data(q, bf, what, "q"), _data(q_out, bf, what, "q_out", tuple(q.shape))
-            (r.q_stride_t, r.q_stride_h), r.Hq = _token_strides(q), q.shape[1]
-            r.q_out_stride_t, r.q_out_stride_h = _token_strides(q_out)
-    _need(r is not None or (q is None and positions is None), what, "q and positions need inv_freq")
-    _need(q_out is None or q is not None, what, "q_out needs q")
-    kt, kh = _token_strides(k)
-    vt, vh = _token_strides(v)
-    _check(lib().dash_kv_write(ctypes.byref(c), kp, kt, kh, vp, vt, vh, sp, T, ctypes.byref(r) if r else None,
-                               _stream(stream)), what)
+            if q_out is None or q.shape != q_out.shape:
+                _refuse(what, "q_out has the shape of q")
+            (qp, (qt, qh, _)), (op, (ot, oh, _)) = _rows(q, _BF16, dev, what, "q", 3), _rows(q_out, _BF16, dev, what, "q_out", 3)
+            Hq = q.shape[1]
+            if q.shape != (T, Hq, D):
+                _refuse(what, "q is [T, Hq, D]")
+        elif q_out is not None:
+            _refuse(what, "q_out needs q")
+        r = _WRITE_ROPE.pack(freqs, _shaped(positions, _I32, dev, what, "positions", (T,)), rot, bool(interleaved),
+                             factor, qp, qt, qh, op, ot, oh, Hq)
+    elif q is not None or q_out is not None or positions is not None:
+        _refuse(what, "q, q_out and positions need inv_freq")
+    _check(lib().dash_kv_write(c, kp, kt, kh, vp, vt, vh, sp, T, r, st), what)
 
 
-def _table(block_table, B, what):
-    p = _data(block_table, torch.int32, what, "block_table")
-    _need(block_table.dim() == 2 and block_table.shape[0] == B, what, "block_table is [B, pages]")
-    return p, (block_table.stride(0) if B > 1 else 0), block_table.shape[1]
+def _table(block_table, B, dev, what):
+    p, (ts, _) = _rows(block_table, _I32, dev, what, "block_table", 2)
+    if block_table.shape[0] != B:
+        _refuse(what, "block_table is [B, pages]")
+    return p, ts, block_table.shape[1]
 
 
 def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None):
@@ -493,22 +502,23 @@ def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=Non
     each sequence; rows past lens[b] are left as they were.  block_table int32
     [B, pages], lens int32 [B]."""
     what = "dash_kv_read"
-    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
-    _need(k.dim() == 4 and k.shape[1] == c.Hkv and k.shape[3] == c.D, what, "k and v are [B, Hkv, S, D]")
-    B, _, S, _ = k.shape
-    tp, ts, pages = _table(block_table, B, what)
-    kp, vp = _data(k, torch.bfloat16, what, "k"), _data(v, torch.bfloat16, what, "v", tuple(k.shape))
-    a, b = _heads(k, what, "k"), _heads(v, what, "v")
-    _need((a.stride_b, a.stride_h, a.stride_s) == (b.stride_b, b.stride_h, b.stride_s), what, "k and v have equal strides")
-    _check(lib().dash_kv_read(ctypes.byref(c), tp, ts, pages, _flat(lens, torch.int32, what, "lens", (B,)), kp, vp,
-                              a.stride_b, a.stride_h, a.stride_s, B, S, _stream(stream)), what)
+    dev, st = _device_stream(stream, what)
+    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    (kp, ks), (vp, vs) = _rows(k, _BF16, dev, what, "k", 4), _rows(v, _BF16, dev, what, "v", 4)
+    B, H, S, d = k.shape
+    if H != Hkv or d != D or v.shape != k.shape or ks != vs:
+        _refuse(what, "k and v are [B, Hkv, S, D] with equal strides")
+    tp, ts, pages = _table(block_table, B, dev, what)
+    _check(lib().dash_kv_read(c, tp, ts, pages, _shaped(lens, _I32, dev, what, "lens", (B,)), kp, vp, ks[0], ks[1],
+                              ks[2], B, S, st), what)
 
 
+@functools.lru_cache(maxsize=4096)   # a function of the sizes alone
 def attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv):
     """Bytes of workspace attn_paged needs; max_kv = pages per sequence * page_size."""
     out = ctypes.c_size_t(0)
-    _check(lib().dash_attn_paged_workspace(int(B), int(T), int(Hq), int(Hkv), int(D), int(max_q), int(max_kv),
-                                           ctypes.byref(out)), "dash_attn_paged_workspace")
+    _check(lib().dash_attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv, ctypes.byref(out)),
+           "dash_attn_paged_workspace")
     return out.value
 
 
@@ -521,33 +531,37 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     T / B).  workspace: uint8 tensor of attn_paged_workspace bytes (None: taken
     from torch's allocator for this call)."""
     what = "dash_attn_paged"
-    c = _cache(k_cache, v_cache, k_scale, v_scale, what)
-    bf = torch.bfloat16
-    qp = _data(q, bf, what, "q")
-    _need(q.dim() == 3 and q.shape[2] == c.D, what, "q is [T, Hq, D]")
-    T, Hq, _ = q.shape
-    op = _flat(o, bf, what, "o", (T, Hq, c.D))
-    lp = _flat(lse, torch.float32, what, "lse", (T, Hq)) if lse is not None else None
+    dev, st = _device_stream(stream, what)
+    c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    qp, (qt, qh, _) = _rows(q, _BF16, dev, what, "q", 3)
+    T, Hq, d = q.shape
+    if d != D:
+        _refuse(what, "q is [T, Hq, D]")
+    op = _shaped(o, _BF16, dev, what, "o", (T, Hq, D))
+    lp = _shaped(lse, _F32, dev, what, "lse", (T, Hq)) if lse is not None else None
     B = kv_lens.shape[0]
-    tp, ts, pages = _table(block_table, B, what)
-    np_ = _flat(kv_lens, torch.int32, what, "kv_lens", (B,))
-    cp = _flat(cu_q, torch.int32, what, "cu_q", (B + 1,)) if cu_q is not None else None
+    tp, ts, pages = _table(block_table, B, dev, what)
+    lens = _shaped(kv_lens, _I32, dev, what, "kv_lens", (B,))
+    cp = _shaped(cu_q, _I32, dev, what, "cu_q", (B + 1,)) if cu_q is not None else None
     if max_q is None:
         max_q = T if cu_q is not None or B == 0 else T // B
-    _need(causal or window is None, what, "a sliding window needs a causal mask")
-    _need(window is None or window >= 1, what, "a window has at least one token")
+    if window is None:
+        window = 0
+    elif not causal or window < 1:
+        _refuse(what, "a sliding window has at least one token, and a causal mask")
     if workspace is None:
-        need = attn_paged_workspace(B, T, Hq, c.Hkv, c.D, max_q, pages * c.page_size)
-        if need:
+        wn, wp = attn_paged_workspace(B, T, Hq, Hkv, D, max_q, pages * page), None
+        if wn:
             if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
             else:
                 with torch.cuda.stream(stream):   # the allocator's reuse then follows this stream
-                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wp, wn = (_flat(workspace, torch.uint8, what, "workspace"), workspace.numel()) if workspace is not None else (None, 0)
-    qt, qh = _token_strides(q)
-    _check(lib().dash_attn_paged(qp, qt, qh, ctypes.byref(c), tp, ts, pages, np_, cp, op, lp, B, T, Hq, int(max_q),
-                                 int(bool(causal)), int(window or 0), wp, wn, _stream(stream)), what)
+                    workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
+            wp = workspace.data_ptr()
+    else:
+        wp, wn = _flat(workspace, torch.uint8, dev, what, "workspace"), workspace.numel()
+    _check(lib().dash_attn_paged(qp, qt, qh, c, tp, ts, pages, lens, cp, op, lp, B, T, Hq, max_q, bool(causal), window,
+                                 wp, wn, st), what)
 
 
 def get_status_paged(stream=None):
