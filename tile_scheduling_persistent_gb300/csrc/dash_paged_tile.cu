@@ -47,7 +47,7 @@ enum TileBar : int {
     T_KV_EMPTY = T_KV_FULL + kKvStages,
     T_S_FULL = T_KV_EMPTY + kKvStages,   // A, B
     T_P_READY = T_S_FULL + 2,
-    T_O_FULL = T_P_READY + 2,
+    T_O_FULL = T_P_READY + 4,            // [tile][half of the keys]
     T_ITEM_FULL = T_O_FULL + 2,
     T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
     T_PATCH = T_ITEM_EMPTY + kItemSlots,
@@ -80,6 +80,12 @@ struct TileCfg {
     // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
     static constexpr int kSmem = OFF_CTL + 16 > 120000 ? OFF_CTL + 16 : 120000;
     static constexpr int kThreads = kE4M3 ? 512 : 384;
+    // registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
+    static constexpr int kRegsLaunch = kE4M3 ? 128 : 168;
+    static constexpr int kRegsCtl = kE4M3 ? 64 : 72;
+    static constexpr int kRegsConv = 80;
+    static constexpr int kRegsSoftmax = kE4M3 ? 184 : 216;
+    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
     static_assert(sizeof(TileItem) <= 64 && kSmem <= 232448, "shared memory budget");
 };
 
@@ -90,7 +96,8 @@ struct TileWait {
 
 // Waits for a phase, at most the timeout; once a wait has run out (reported) no role waits any more and all reach their
 // end: false.
-__device__ __noinline__ bool tile_wait_slow(uint32_t bar, uint32_t parity, const TileWait& w) {
+// (Inlined: a call would take its caller's registers through the ABI's limits and spill the softmax.)
+__device__ __forceinline__ bool tile_wait_slow(uint32_t bar, uint32_t parity, const TileWait& w) {
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait(bar, parity)) {
         if (*w.abort) return false;
@@ -129,6 +136,65 @@ __device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t x) {
     return r;
 }
 
+// ---------------------------------------------------------------- products
+// A product's 16 instructions have to leave in fewer cycles than the tensor core takes for them (64 each), from one warp.
+// So the whole warp runs the issuer's code -- uniform control flow, values in uniform registers -- with the elected
+// thread as a predicate of the instruction alone, and a shared-memory descriptor is one 32-bit addition: the upper half
+// is constant (8-row groups 1024 bytes apart, version 1, 128-byte swizzle), the lower holds the address over 16 and, from
+// bit 16, the distance between 64-column boxes over 16.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescK = 1u << 16;                       // K-major: no second distance
+constexpr uint32_t kDescMn = ((uint32_t)kBox >> 4) << 16;   // MN-major
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(leader), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "r"(leader), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+// S[128 x 128] = Q[128 x D] K[128 x D]^T, both K-major (lower descriptor halves)
+template <int D>
+__device__ __forceinline__ void product_s(uint32_t leader, uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo) {
+    constexpr uint32_t idesc = ptx::idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+        mma_ss_if(leader, d_tmem, q_lo + off, k_lo + off, idesc, kk > 0);
+    }
+}
+// O[128 x D] (+)= P[128 x 64] (tensor memory, keys 64h ..) * V rows 64h .. (MN-major)
+template <int D>
+__device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, int h, uint32_t acc) {
+    constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, h + kk > 0 ? 1u : acc);
+}
+
 template <int D, bool kE4M3>
 __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_kernel(const __grid_constant__ PagedParams p) {
     using C = TileCfg<D, kE4M3>;
@@ -148,7 +214,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
             if (kE4M3 && i >= T_KV_FULL && i < T_KV_FULL + kKvStages) count = 4;   // the converter warps
-            if (i >= T_P_READY && i < T_P_READY + 2) count = 4;
+            if (i >= T_P_READY && i < T_P_READY + 4) count = 4;
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
         }
@@ -177,6 +243,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         return it.b >= 0;
     };
 
+    // Each warpgroup first re-sizes its registers, then runs its role.
+    if (warp < 4) {
+    ptx::setmaxnreg_dec<C::kRegsCtl>();
     if (warp == 0) {
         // ================================================== producer
         TileItem it;
@@ -263,59 +332,66 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     } else if (warp == 1) {
         // ================================================== MMA issuer
         TileItem it;
-        int kv = 0, qn = 0, pu[2] = {0, 0};
-        const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+        const uint32_t leader = elect_one();
+        const uint32_t lo0 = sbase >> 4;
+        int st = 0, qn = 0, pu[2] = {0, 0};   // KV stage of the next K; Q loads; weights so far of A, B
+        uint32_t ph = 0;                      // its barrier's phase
         bool ok = true;
         while (ok && next_item(it)) {
-            const int nk = it.t1 - it.t0;
+            const int nk = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
             if (nk <= 0) continue;
-            const int tiles = it.ntok > tpt ? 2 : 1;
-            if (lane == 0) {
-                auto full = [&](int u) { return tile_wait(BAR(T_KV_FULL + u % kKvStages), (uint32_t)((u / kKvStages) & 1), tw); };
-                auto sKV = [&](int u) { return sbase + C::OFF_KV + (uint32_t)(u % kKvStages) * C::kTile; };
-                ok = tile_wait(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw) && full(kv);
-                if (ok) {
-                    ptx::tc_fence_after();
-                    for (int x = 0; x < tiles; ++x) {
-                        issue_s<D, D / 16>(tS[x], sbase + C::OFF_Q + x * C::kTile, sKV(kv));
-                        ptx::tc_commit(BAR(T_S_FULL + x));
-                    }
-                    ptx::tc_commit(BAR(T_KV_EMPTY + kv % kKvStages));
-                    if (nk == 1) ptx::tc_commit(BAR(T_Q_EMPTY));
+            const int tiles = __shfl_sync(0xffffffffu, it.ntok > tpt ? 2 : 1, 0);
+            ok = tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw) && tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (x < tiles) {
+                    product_s<D>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
+                                 lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
+                    commit_if(leader, BAR(T_S_FULL + x));
                 }
-                for (int j = 0; ok && j < nk; ++j) {
-                    const int uv = kv + 2 * j + 1, uk = uv + 1;
-                    const bool more = j + 1 < nk;
-                    if (!full(uv)) ok = false;
-                    for (int x = 0; ok && x < tiles; ++x) {
-                        if (!tile_wait(BAR(T_P_READY + x), (uint32_t)(pu[x] & 1), tw)) {
-                            ok = false;
-                            break;
-                        }
-                        ++pu[x];
+            commit_if(leader, BAR(T_KV_EMPTY + st));
+            if (nk == 1) commit_if(leader, BAR(T_Q_EMPTY));
+            for (int j = 0; ok && j < nk; ++j) {
+                const int sv = st + 1;                  // stages of V_j and K_{j+1}: K and V alternate
+                st = (st + 2) % kKvStages;
+                const uint32_t pv = ph;
+                ph ^= st == 0 ? 1u : 0u;
+                const bool more = j + 1 < nk;
+                ok = tile_wait_warp(BAR(T_KV_FULL + sv), pv, tw);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= tiles || !ok) continue;
+                    // O (+)= P V_j, in two halves of the keys as the weights become ready
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && tile_wait_warp(BAR(T_P_READY + 2 * x + h), (uint32_t)(pu[x] & 1), tw);
+                        if (!ok) break;
                         ptx::tc_fence_after();
-                        issue_dv<D, 8>(tO[x], tS[x], sKV(uv), j > 0 ? 1u : 0u);   // O (+)= P V_j
-                        if (x == tiles - 1) ptx::tc_commit(BAR(T_KV_EMPTY + uv % kKvStages));
-                        if (more) {
-                            if (x == 0 && !full(uk)) {
-                                ok = false;
-                                break;
-                            }
-                            ptx::tc_fence_after();
-                            issue_s<D, D / 16>(tS[x], sbase + C::OFF_Q + x * C::kTile, sKV(uk));
-                            ptx::tc_commit(BAR(T_S_FULL + x));
-                            if (x == tiles - 1) {
-                                ptx::tc_commit(BAR(T_KV_EMPTY + uk % kKvStages));
-                                if (j + 2 == nk) ptx::tc_commit(BAR(T_Q_EMPTY));
-                            }
-                        } else {
-                            ptx::tc_commit(BAR(T_O_FULL + x));
+                        product_pv<D>(leader, tmem + 256 + 128 * x, tmem + 128 * x, lo0 + kDescMn + ((C::OFF_KV + sv * C::kTile) >> 4),
+                                      h, j > 0 ? 1u : 0u);
+                    }
+                    if (!ok) continue;
+                    ++pu[x];
+                    const bool last = x == tiles - 1;
+                    if (last) commit_if(leader, BAR(T_KV_EMPTY + sv));
+                    if (more) {
+                        if (x == 0) ok = tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
+                        if (!ok) continue;
+                        ptx::tc_fence_after();
+                        product_s<D>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
+                                     lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
+                        commit_if(leader, BAR(T_S_FULL + x));
+                        if (last) {
+                            commit_if(leader, BAR(T_KV_EMPTY + st));
+                            if (j + 2 == nk) commit_if(leader, BAR(T_Q_EMPTY));
                         }
+                    } else {
+                        commit_if(leader, BAR(T_O_FULL + x));
                     }
                 }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-            kv += 2 * nk;
             ++qn;
         }
         // after a wait that ran out, the products in flight end before tensor memory is freed (below, after the barrier);
@@ -376,7 +452,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             __syncwarp();
             if (it.b < 0) break;
         }
-    } else if (warp >= 4 && warp < 12) {
+    }
+    } else if (warp < 12) {
+        ptx::setmaxnreg_inc<C::kRegsSoftmax>();
         // ================================================== softmax and epilogue, one row per thread
         const int x_ = (warp - 4) >> 2;   // tile A or B
         const int row = 32 * (warp & 3) + lane;
@@ -407,43 +485,38 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     break;
                 }
                 ptx::tc_fence_after();
-                // Two passes over the scores, 32 columns at a time out of tensor memory: the maximum, then the weights.
-                // Holding all 128 in registers instead would not leave room for the next columns' loads.
+                float x[128];
+                {
+                    uint32_t r[4][32];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
+                }
                 const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + ((kt + j) & 3) * 256;
+                if (kE4M3) {   // the keys' scales, times scale log2e
+#pragma unroll
+                    for (int k = 0; k < 128; k += 4) {
+                        const float4 s4 = *reinterpret_cast<const float4*>(sc + k);
+                        const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
+                        x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                    }
+                }
                 const int key = (it.t0 + j) * 128;
-                const bool edge = key < full_lo || key + 128 > full_hi;
-                const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
-                uint32_t r[2][32];
+                if (key < full_lo || key + 128 > full_hi) {
+                    const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (k < ka || k >= kb) x[k] = -INFINITY;
+                }
+                // row maximum and sum over interleaved partials: short chains, one fixed order
                 float part[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) part[k] = -INFINITY;
-                ptx::tmem_ld32(tS, r[0]);
+                for (int k = 0; k < 4; ++k) part[k] = fmaxf(x[2 * k], x[2 * k + 1]);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    ptx::tmem_ld_wait();
-                    if (h < 3) ptx::tmem_ld32(tS + 32 * (h + 1), r[(h + 1) & 1]);
-                    float x[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[h & 1][k]);
-                    if (kE4M3) {   // the keys' scales, times scale log2e
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(sc + 32 * h + k);
-                            const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
-                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
-                        }
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) part[k & 7] = fmaxf(part[k & 7], x[k]);
-                }
-                ptx::tmem_ld32(tS, r[0]);
-                const float mx = (kE4M3 ? 1.f : c) * fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
-                                                           fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
+                for (int k = 8; k < 128; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
+                const float mx = (kE4M3 ? 1.f : c) * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                 const bool raise = __any_sync(0xffffffffu, valid && mx > m_ref + 8.f);
                 if (raise) {
                     const float m_new = fmaxf(m_ref, mx);
@@ -451,66 +524,50 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     m_ref = m_new;
                     l *= alpha;
                     if (j > 0) {
-                        ptx::tmem_ld_wait();   // r[0] is in flight
 #pragma unroll 1
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            ptx::tmem_ld32(tO + 32 * cc, r[1]);
+                        for (int cc = 0; cc < D / 16; ++cc) {
+                            uint32_t r[16];
+                            ptx::tmem_ld16(tO + 16 * cc, r);
                             ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * alpha);
-                            ptx::tmem_st32(tO + 32 * cc, r[1]);
+                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+                            ptx::tmem_st16(tO + 16 * cc, r);
                         }
                     }
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) part[k] = 0.f;
+                // P (with the values' scales) rounded to bf16, keys [0,64) -> columns [0,32), [64,128) -> [64,96); the
+                // products with the first 64 keys start while the rest is worked out
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    ptx::tmem_ld_wait();
-                    if (h < 3) ptx::tmem_ld32(tS + 32 * (h + 1), r[(h + 1) & 1]);
-                    float x[32];
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float* s = reinterpret_cast<const float*>(&r[h & 1][k]);
-                        float4 s4 = make_float4(c, c, c, c);
-                        if (kE4M3) s4 = *reinterpret_cast<const float4*>(sc + 32 * h + k);
-                        const ptx::f2 u = ptx::fma2({s[0], s[1]}, {s4.x, s4.y}, {-m_use, -m_use});
-                        const ptx::f2 v = ptx::fma2({s[2], s[3]}, {s4.z, s4.w}, {-m_use, -m_use});
-                        x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        x[k] = ptx::ex2(x[k]);
-                        x[k + 1] = ptx::ex2(x[k + 1]);
+                    for (int k = 32 * h; k < 32 * h + 32; k += 2) {
+                        const ptx::f2 y = kE4M3 ? ptx::sub2({x[k], x[k + 1]}, {m_use, m_use})
+                                                : ptx::fma2({x[k], x[k + 1]}, {c, c}, {-m_use, -m_use});
+                        x[k] = ptx::ex2(y.x);
+                        x[k + 1] = ptx::ex2(y.y);
                         const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, {x[k], x[k + 1]});
                         part[k & 7] = s.x;
                         part[(k + 1) & 7] = s.y;
-                    }
-                    // P (with the values' scales) rounded to bf16, keys [0,64) -> columns [0,32), [64,128) -> [64,96)
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
+                        ptx::f2 w{x[k], x[k + 1]};
                         if (kE4M3) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(sc + 128 + 32 * h + k);
-                            const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
-                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                            const float2 s2 = *reinterpret_cast<const float2*>(sc + 128 + k);
+                            w = ptx::mul2(w, {s2.x, s2.y});
                         }
-                        pk[k / 2] = pack_bf16(x[k], x[k + 1]);
-                        pk[k / 2 + 1] = pack_bf16(x[k + 2], x[k + 3]);
+                        pk[(k >> 1) & 15] = pack_bf16(w.x, w.y);
                     }
                     ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
+                    if (h & 1) {
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + 2 * x_ + (h >> 1)));
+                    }
                 }
                 l += ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + x_));
             }
             if (!ok) break;
             kt += nk > 0 ? nk : 0;
@@ -554,7 +611,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 p.lse[at] = empty ? -INFINITY : (m_ref + log2f(l)) * kLn2P;
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
         }
-    } else if (kE4M3 && warp >= 12) {
+    } else if (kE4M3) {
+        ptx::setmaxnreg_dec<C::kRegsConv>();
         // ================================================== converters
         constexpr int kChunks = D / 16;         // 16-byte chunks of codes per key
         constexpr int kRows = 32 / kChunks;     // keys that one load instruction of a warp covers
@@ -566,34 +624,48 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         while (ok && next_item(it)) {
             const int nk = it.t1 - it.t0;
             if (nk <= 0) continue;
-            // codes of key 128 t + 32 cw + kRows l + sub, chunk `chunk`; keys outside the sequence's read as zero
-            // (a key's two scales come with its codes of K: the softmax needs both before V is staged)
-            auto load = [&](int u, uint4 (&w)[kLoads], float& ks, float& vs) {
-                const int t = it.t0 + (u >> 1);
-                const uint8_t* base = (const uint8_t*)((u & 1) ? p.c.v : p.c.k);
-#pragma unroll
-                for (int l = 0; l < kLoads; ++l) {
-                    const int key = 128 * t + 32 * cw + kRows * l + sub;
-                    w[l] = make_uint4(0, 0, 0, 0);
-                    if (key >= it.lo && key < it.hi) {
-                        const long long cell = ((long long)checked_page(p, it.b, key >> p.page_shift) * p.c.Hkv + it.hk) * p.c.page_size +
-                                               (key & (p.c.page_size - 1));
-                        w[l] = *reinterpret_cast<const uint4*>(base + cell * D + 16 * chunk);
-                    }
+            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(it.t1 * 128, it.hi) - 1) >> p.page_shift;
+            int eb = (it.t0 * 128) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
+            auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
+            int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
+            // Unit u is K (even) or V (odd) of key tile t0 + u / 2.  This lane's addresses in it: first and second 16 keys of
+            // the warp's 32 (a page holds at least 16), and which keys the sequence sees.
+            long long cell[2] = {0, 0};
+            int key0 = 0;
+            auto aim = [&](int t) {
+                if (((t * 128) >> p.page_shift) - eb >= 32) {
+                    eb += 32;
+                    pages = next;
+                    next = fetch(eb + 32 + lane);
                 }
-                if (u & 1) return;
-                const int key = 128 * t + 32 * cw + lane;
-                ks = vs = 0.f;
-                if (key >= it.lo && key < it.hi) {
-                    const long long cell = ((long long)checked_page(p, it.b, key >> p.page_shift) * p.c.Hkv + it.hk) * p.c.page_size +
-                                           (key & (p.c.page_size - 1));
-                    ks = p.c.k_scale[cell] * p.scale_log2e;
-                    vs = p.c.v_scale[cell];
+                key0 = t * 128 + 32 * cw;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = key0 + 16 * h;
+                    const int pg = __shfl_sync(0xffffffffu, pages, ((key >> p.page_shift) - eb) & 31);
+                    cell[h] = ((long long)pg * p.c.Hkv + it.hk) * p.c.page_size + (key & (p.c.page_size - 1));
                 }
             };
+            auto load = [&](int l, const void* base) {
+                const int r = kRows * l + sub;   // of the warp's 32 keys
+                const int key = key0 + r;
+                if (key < it.lo || key >= it.hi) return make_uint4(0, 0, 0, 0);
+                return __ldg(reinterpret_cast<const uint4*>((const uint8_t*)base + (cell[l >= kLoads / 2] + (r & 15)) * D + 16 * chunk));
+            };
             uint4 w[kLoads];
-            float ks, vs;
-            load(0, w, ks, vs);
+            float ks = 0.f, vs = 0.f;   // a key's two scales come with K: the softmax needs both before V is staged
+            auto scales = [&]() {
+                const int key = key0 + lane;
+                const bool in = key >= it.lo && key < it.hi;
+                const long long at = cell[lane >> 4] + (lane & 15);
+                ks = in ? p.c.k_scale[at] * p.scale_log2e : 0.f;
+                vs = in ? p.c.v_scale[at] : 0.f;
+            };
+            aim(it.t0);
+            scales();
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) w[l] = load(l, p.c.k);
+#pragma unroll 1
             for (int u = 0; u < 2 * nk; ++u, ++kv) {
                 const int st = kv % kKvStages;
                 if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), (uint32_t)((kv / kKvStages - 1) & 1), tw)) {
@@ -606,14 +678,17 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     sc[0] = ks;
                     sc[128] = vs;
                 }
-                uint4 cur[kLoads];
+                const bool more = u + 1 < 2 * nk;
+                if (more && (u & 1)) {
+                    aim(it.t0 + (u + 1) / 2);
+                    scales();
+                }
+                const void* base = (u & 1) ? p.c.k : p.c.v;   // of the next unit
 #pragma unroll
-                for (int l = 0; l < kLoads; ++l) cur[l] = w[l];
-                if (u + 1 < 2 * nk) load(u + 1, w, ks, vs);
-#pragma unroll
-                for (int l = 0; l < kLoads; ++l) {
+                for (int l = 0; l < kLoads; ++l) {   // convert a chunk, and load the next unit's in its place
                     const int row = 32 * cw + kRows * l + sub;
-                    const uint32_t c4[4] = {cur[l].x, cur[l].y, cur[l].z, cur[l].w};
+                    const uint32_t c4[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
+                    if (more) w[l] = load(l, base);
                     uint32_t o[8];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
