@@ -20,12 +20,22 @@
 //
 // Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
 // tensor memory, 2 item scheduler, 3 idle, 4-7 softmax and epilogue of tile A,
-// 8-11 of tile B, and for e4m3 caches 12-15 converters: they read codes from
-// the pages, one tile ahead, and store them as bf16 (exact) in the layout that
-// TMA gives a bf16 cache; the scales stay outside the products: ks multiplies
-// the score, vs the weight before it is rounded to bf16.
+// 8-11 of tile B, and for e4m3 caches 12-15 converters.
+//
+// e4m3 caches.  The converters read codes from the pages one tile ahead and
+// store them, as TMA would a bf16 cache's tile, in fp16; the products then run
+// in fp16.  K holds the codes themselves (exact), and the softmax multiplies
+// the scores by the keys' scales in fp32: scores, maxima and sums lose nothing.
+// V holds code * scale, rounded once to fp16 (2^-11, against 2^-8 of the
+// output's bf16): a second scale for each column would cost the softmax as
+// much again as its exponentials, since its reads of shared memory wait behind
+// the tensor core's.  fp16's range is met with powers of two, undone in fp32:
+// V by the largest scale so far in the item in [2^6, 2^7) (codes reach 448; when
+// it grows, O is rescaled as for a grown maximum), Q by row, its largest value
+// in [2^14, 2^15), converted in place.
 //
 // Tensor memory: S/P of A at column 0, of B at 128; O of A at 256, of B at 384.
+#include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
 
@@ -43,6 +53,7 @@ constexpr int kItemSlots = 2;
 enum TileBar : int {
     T_Q_FULL = 0,
     T_Q_EMPTY,
+    T_Q_READY,           // e4m3: converted
     T_KV_FULL,
     T_KV_EMPTY = T_KV_FULL + kKvStages,
     T_S_FULL = T_KV_EMPTY + kKvStages,   // A, B
@@ -73,8 +84,10 @@ struct TileCfg {
     static constexpr int kNBox = D / 64;
     static constexpr int OFF_Q = 0;                                  // A, B
     static constexpr int OFF_KV = 2 * kTile;
-    static constexpr int OFF_SCALE = OFF_KV + kKvStages * kTile;     // [4 tiles][K, V][128] fp32
-    static constexpr int OFF_ITEM = OFF_SCALE + (kE4M3 ? 4 * 2 * 128 * 4 : 0);
+    static constexpr int OFF_QFAC = OFF_KV + kKvStages * kTile;      // e4m3: [2 items][A, B][128] fp32, 2^-a of each row
+    static constexpr int OFF_KSC = OFF_QFAC + (kE4M3 ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
+    static constexpr int OFF_VFAC = OFF_KSC + (kE4M3 ? 4 * 128 * 4 : 0);        // [4 tiles] the factor of V
+    static constexpr int OFF_ITEM = OFF_VFAC + (kE4M3 ? 16 : 0);
     static constexpr int OFF_BAR = OFF_ITEM + kItemSlots * 64;
     static constexpr int OFF_CTL = OFF_BAR + T_COUNT * 8;            // tensor memory address, abort flag
     // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
@@ -82,8 +95,8 @@ struct TileCfg {
     static constexpr int kThreads = kE4M3 ? 512 : 384;
     // registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
     static constexpr int kRegsLaunch = kE4M3 ? 128 : 168;
-    static constexpr int kRegsCtl = kE4M3 ? 64 : 72;
-    static constexpr int kRegsConv = 80;
+    static constexpr int kRegsCtl = kE4M3 ? 48 : 72;
+    static constexpr int kRegsConv = 96;
     static constexpr int kRegsSoftmax = kE4M3 ? 184 : 216;
     static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
     static_assert(sizeof(TileItem) <= 64 && kSmem <= 232448, "shared memory budget");
@@ -127,13 +140,34 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// Codes in the high bytes of two halves to a bf16 pair, exactly: exponent and fraction bits move into place, which
-// leaves the value times 2^-120.
-__device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t x) {
-    const uint32_t t = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+// Two codes as fp16 (exact).
+__device__ __forceinline__ uint32_t half_codes(uint32_t codes, int upper) {
+    uint32_t c;
+    const uint16_t two = (uint16_t)(upper ? codes >> 16 : codes);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(two));
+    return c;
+}
+// Two values times a scale given as two fp16 parts (hi + lo, each twice): one rounding to fp16.
+__device__ __forceinline__ uint32_t scaled_codes(uint32_t c, uint32_t hi, uint32_t lo) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x7b807b80u));
+    asm("{\n\t.reg .b32 t;\n\tmul.rn.f16x2 t, %1, %3;\n\tfma.rn.f16x2 %0, %1, %2, t;\n\t}" : "=r"(r) : "r"(c), "r"(hi), "r"(lo));
     return r;
+}
+// 2^(k - e) and 2^(e - k) for x in [2^e, 2^(e+1)), k <= 14; both normal (a smaller x counts as 2^-112).
+__device__ __forceinline__ void power_to(float x, int k, float& up, float& down) {
+    const int e = min(max((int)(__float_as_uint(x) >> 23 & 255u) - 127, -112), 127);
+    up = __uint_as_float((uint32_t)(127 + k - e) << 23);
+    down = __uint_as_float((uint32_t)(127 - k + e) << 23);
 }
 
 // ---------------------------------------------------------------- products
@@ -177,9 +211,11 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
         : "memory");
 }
 // S[128 x 128] = Q[128 x D] K[128 x D]^T, both K-major (lower descriptor halves)
-template <int D>
+// (kHalf: fp16 operands)
+constexpr uint32_t kBf16Bits = (1u << 7) | (1u << 10);
+template <int D, bool kHalf>
 __device__ __forceinline__ void product_s(uint32_t leader, uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo) {
-    constexpr uint32_t idesc = ptx::idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idesc = ptx::idesc_bf16(128, 128, 0, 0) & ~(kHalf ? kBf16Bits : 0u);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
@@ -187,9 +223,9 @@ __device__ __forceinline__ void product_s(uint32_t leader, uint32_t d_tmem, uint
     }
 }
 // O[128 x D] (+)= P[128 x 64] (tensor memory, keys 64h ..) * V rows 64h .. (MN-major)
-template <int D>
+template <int D, bool kHalf>
 __device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, int h, uint32_t acc) {
-    constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1);
+    constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1) & ~(kHalf ? kBf16Bits : 0u);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
         mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, h + kk > 0 ? 1u : acc);
@@ -213,7 +249,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kE4M3 && i >= T_KV_FULL && i < T_KV_FULL + kKvStages) count = 4;   // the converter warps
+            if (kE4M3 && (i == T_Q_READY || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // the converter warps
             if (i >= T_P_READY && i < T_P_READY + 4) count = 4;
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
@@ -341,13 +377,13 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             const int nk = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
             if (nk <= 0) continue;
             const int tiles = __shfl_sync(0xffffffffu, it.ntok > tpt ? 2 : 1, 0);
-            ok = tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw) && tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
+            ok = tile_wait_warp(BAR(kE4M3 ? T_Q_READY : T_Q_FULL), (uint32_t)(qn & 1), tw) && tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
             if (!ok) break;
             ptx::tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (x < tiles) {
-                    product_s<D>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
+                    product_s<D, kE4M3>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
                                  lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
                     commit_if(leader, BAR(T_S_FULL + x));
                 }
@@ -369,7 +405,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                         ok = ok && tile_wait_warp(BAR(T_P_READY + 2 * x + h), (uint32_t)(pu[x] & 1), tw);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        product_pv<D>(leader, tmem + 256 + 128 * x, tmem + 128 * x, lo0 + kDescMn + ((C::OFF_KV + sv * C::kTile) >> 4),
+                        product_pv<D, kE4M3>(leader, tmem + 256 + 128 * x, tmem + 128 * x, lo0 + kDescMn + ((C::OFF_KV + sv * C::kTile) >> 4),
                                       h, j > 0 ? 1u : 0u);
                     }
                     if (!ok) continue;
@@ -380,7 +416,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                         if (x == 0) ok = tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
                         if (!ok) continue;
                         ptx::tc_fence_after();
-                        product_s<D>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
+                        product_s<D, kE4M3>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
                                      lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
                         commit_if(leader, BAR(T_S_FULL + x));
                         if (last) {
@@ -460,9 +496,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         const int row = 32 * (warp & 3) + lane;
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lane_off + 128u * (uint32_t)x_, tO = tmem + lane_off + 256u + 128u * (uint32_t)x_;
-        const float c = p.scale_log2e;
+        float c = p.scale_log2e;
         TileItem it;
-        int su = 0, ou = 0, kt = 0;   // S and O phases, key tiles of all items
+        int su = 0, ou = 0, kt = 0, qn = 0;   // S and O phases, key tiles and Q loads of all items
         bool ok = true;
         while (ok && next_item(it)) {
             const int nk = it.t1 - it.t0;
@@ -471,6 +507,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             const bool valid = mine && row < trows && i < it.ntok;
             if (!mine) {
                 kt += nk > 0 ? nk : 0;
+                qn += nk > 0 ? 1 : 0;
                 continue;
             }
             // this row's keys, and the key tiles that every row of the tile sees whole
@@ -478,7 +515,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             const int hi_r = p.causal ? pos + 1 : it.len, lo_r = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
             const int pos0 = it.pos + x_ * tpt, pos1 = min(it.pos + it.ntok - 1, pos0 + tpt - 1);
             const int full_hi = p.causal ? pos0 + 1 : it.len, full_lo = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = -INFINITY, l = 0.f, vfac = 1.f;   // O holds the sum over vfac
             for (int j = 0; j < nk; ++j, ++su) {
                 if (!tile_wait_warp(BAR(T_S_FULL + x_), (uint32_t)(su & 1), tw)) {
                     ok = false;
@@ -486,22 +523,45 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 }
                 ptx::tc_fence_after();
                 float x[128];
-                {
+                if (!kE4M3) {
                     uint32_t r[4][32];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
-                }
-                const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + ((kt + j) & 3) * 256;
-                if (kE4M3) {   // the keys' scales, times scale log2e
+                } else {   // times the keys' scales, those of the next 32 columns on their way meanwhile
+                    const float4* sc = reinterpret_cast<const float4*>(smem + C::OFF_KSC) + ((kt + j) & 3) * 32;
+                    float4 s4[2][8];
 #pragma unroll
-                    for (int k = 0; k < 128; k += 4) {
-                        const float4 s4 = *reinterpret_cast<const float4*>(sc + k);
-                        const ptx::f2 u = ptx::mul2({x[k], x[k + 1]}, {s4.x, s4.y}), v = ptx::mul2({x[k + 2], x[k + 3]}, {s4.z, s4.w});
-                        x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                    for (int k = 0; k < 8; ++k) s4[0][k] = sc[k];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t r[32];
+                        ptx::tmem_ld32(tS + 32 * h, r);
+                        if (h < 3) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) s4[(h + 1) & 1][k] = sc[8 * (h + 1) + k];
+                        }
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = s4[h & 1][k];
+                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])}, {f.x, f.y});
+                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])}, {f.z, f.w});
+                            x[32 * h + 4 * k] = u.x, x[32 * h + 4 * k + 1] = u.y, x[32 * h + 4 * k + 2] = v.x, x[32 * h + 4 * k + 3] = v.y;
+                        }
                     }
+                }
+                float grown = 1.f;   // of O, when the values' power of two has grown
+                if (kE4M3) {
+                    const float f = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[(kt + j) & 3];
+                    if (j == 0) {
+                        c = p.scale_log2e * reinterpret_cast<const float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x_) * 128 + row];
+                        vfac = f;
+                    }
+                    if (f != vfac) grown = vfac / f;
+                    vfac = f;
                 }
                 const int key = (it.t0 + j) * 128;
                 if (key < full_lo || key + 128 > full_hi) {
@@ -516,13 +576,14 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 for (int k = 0; k < 4; ++k) part[k] = fmaxf(x[2 * k], x[2 * k + 1]);
 #pragma unroll
                 for (int k = 8; k < 128; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
-                const float mx = (kE4M3 ? 1.f : c) * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                const bool raise = __any_sync(0xffffffffu, valid && mx > m_ref + 8.f);
+                const float mx = c * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                const bool raise = __any_sync(0xffffffffu, (valid && mx > m_ref + 8.f) || (kE4M3 && grown != 1.f));
                 if (raise) {
                     const float m_new = fmaxf(m_ref, mx);
                     const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref - m_new);
                     m_ref = m_new;
                     l *= alpha;
+                    const float alpha_o = kE4M3 ? alpha * grown : alpha;
                     if (j > 0) {
 #pragma unroll 1
                         for (int cc = 0; cc < D / 16; ++cc) {
@@ -530,7 +591,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             ptx::tmem_ld16(tO + 16 * cc, r);
                             ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_o);
                             ptx::tmem_st16(tO + 16 * cc, r);
                         }
                     }
@@ -538,26 +599,20 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) part[k] = 0.f;
-                // P (with the values' scales) rounded to bf16, keys [0,64) -> columns [0,32), [64,128) -> [64,96); the
+                // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys [0,64) -> columns [0,32), [64,128) -> [64,96); the
                 // products with the first 64 keys start while the rest is worked out
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 32 * h; k < 32 * h + 32; k += 2) {
-                        const ptx::f2 y = kE4M3 ? ptx::sub2({x[k], x[k + 1]}, {m_use, m_use})
-                                                : ptx::fma2({x[k], x[k + 1]}, {c, c}, {-m_use, -m_use});
+                        const ptx::f2 y = ptx::fma2({x[k], x[k + 1]}, {c, c}, {-m_use, -m_use});
                         x[k] = ptx::ex2(y.x);
                         x[k + 1] = ptx::ex2(y.y);
                         const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, {x[k], x[k + 1]});
                         part[k & 7] = s.x;
                         part[(k + 1) & 7] = s.y;
-                        ptx::f2 w{x[k], x[k + 1]};
-                        if (kE4M3) {
-                            const float2 s2 = *reinterpret_cast<const float2*>(sc + 128 + k);
-                            w = ptx::mul2(w, {s2.x, s2.y});
-                        }
-                        pk[(k >> 1) & 15] = pack_bf16(w.x, w.y);
+                        pk[(k >> 1) & 15] = kE4M3 ? pack_half(x[k], x[k + 1]) : pack_bf16(x[k], x[k + 1]);
                     }
                     ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
                     if (h & 1) {
@@ -571,6 +626,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             }
             if (!ok) break;
             kt += nk > 0 ? nk : 0;
+            qn += nk > 0 ? 1 : 0;
             if (nk > 0) {
                 if (!tile_wait_warp(BAR(T_O_FULL + x_), (uint32_t)(ou & 1), tw)) break;
                 ++ou;
@@ -579,7 +635,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             const int g = row % p.G;
             const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
             const long long pr = it.part + (long long)i * p.G + g;
-            const float inv = (it.split || !(l > 0.f)) ? 1.f : 1.f / l;
+            const float inv = vfac * ((it.split || !(l > 0.f)) ? 1.f : 1.f / l);
             const bool empty = !(l > 0.f);
             const bool keep = it.split && valid && pr < p.max_rows;
 #pragma unroll
@@ -619,7 +675,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         constexpr int kLoads = 32 / kRows;      // loads of a warp's 32 keys of a tile
         const int cw = warp - 12, chunk = lane % kChunks, sub = lane / kChunks;
         TileItem it;
-        int kv = 0, kt = 0;
+        int kv = 0, kt = 0, qn = 0;
         bool ok = true;
         while (ok && next_item(it)) {
             const int nk = it.t1 - it.t0;
@@ -653,16 +709,27 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 return __ldg(reinterpret_cast<const uint4*>((const uint8_t*)base + (cell[l >= kLoads / 2] + (r & 15)) * D + 16 * chunk));
             };
             uint4 w[kLoads];
-            float ks = 0.f, vs = 0.f;   // a key's two scales come with K: the softmax needs both before V is staged
-            auto scales = [&]() {
-                const int key = key0 + lane;
-                const bool in = key >= it.lo && key < it.hi;
-                const long long at = cell[lane >> 4] + (lane & 15);
-                ks = in ? p.c.k_scale[at] * p.scale_log2e : 0.f;
-                vs = in ? p.c.v_scale[at] : 0.f;
+            // Scales of a key tile (they come with K): the key's own of K, those of this warp's keys of V, and the largest of
+            // V so far, for which every warp reads the whole tile's.
+            float ks = 0.f, vs = 0.f, vtop = 0.f;
+            auto scales = [&](int t) {
+                float v4[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int key = t * 128 + 32 * c + lane;
+                    const bool in = key >= it.lo && key < it.hi;
+                    const int pg = __shfl_sync(0xffffffffu, pages, ((key >> p.page_shift) - eb) & 31);
+                    const long long at = ((long long)pg * p.c.Hkv + it.hk) * p.c.page_size + (key & (p.c.page_size - 1));
+                    v4[c] = in ? __ldg(p.c.v_scale + at) : 0.f;
+                    if (c == cw) ks = in ? __ldg(p.c.k_scale + at) : 0.f;
+                }
+                vs = cw == 0 ? v4[0] : cw == 1 ? v4[1] : cw == 2 ? v4[2] : v4[3];
+                vtop = fmaxf(vtop, fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3])));
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, d));
             };
             aim(it.t0);
-            scales();
+            scales(it.t0);
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) w[l] = load(l, p.c.k);
 #pragma unroll 1
@@ -673,15 +740,18 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     break;
                 }
                 const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
+                float vup, vback;
+                power_to(vtop, 6, vup, vback);
+                const float scale = vs * vup;
                 if (!(u & 1)) {
-                    float* sc = reinterpret_cast<float*>(smem + C::OFF_SCALE) + ((kt + (u >> 1)) & 3) * 256 + 32 * cw + lane;
-                    sc[0] = ks;
-                    sc[128] = vs;
+                    const int slot = (kt + (u >> 1)) & 3;
+                    reinterpret_cast<float*>(smem + C::OFF_KSC)[slot * 128 + 32 * cw + lane] = ks;
+                    if (cw == 0 && lane == 0) reinterpret_cast<float*>(smem + C::OFF_VFAC)[slot] = vback;
                 }
                 const bool more = u + 1 < 2 * nk;
                 if (more && (u & 1)) {
                     aim(it.t0 + (u + 1) / 2);
-                    scales();
+                    scales(it.t0 + (u + 1) / 2);
                 }
                 const void* base = (u & 1) ? p.c.k : p.c.v;   // of the next unit
 #pragma unroll
@@ -690,12 +760,24 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     const uint32_t c4[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
                     if (more) w[l] = load(l, base);
                     uint32_t o[8];
+                    if (u & 1) {
+                        const float sc = __shfl_sync(0xffffffffu, scale, kRows * l + sub);
+                        const uint32_t hi = pack_half(sc, sc);
+                        const float rest = sc - __half2float(__ushort_as_half((uint16_t)hi));
+                        const uint32_t lo = pack_half(rest, rest);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        o[2 * y] = bf16x2_of_e4m3(__byte_perm(c4[y], 0u, 0x1404));
-                        o[2 * y + 1] = bf16x2_of_e4m3(__byte_perm(c4[y], 0u, 0x3424));
+                        for (int y = 0; y < 4; ++y) {
+                            o[2 * y] = scaled_codes(half_codes(c4[y], 0), hi, lo);
+                            o[2 * y + 1] = scaled_codes(half_codes(c4[y], 1), hi, lo);
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            o[2 * y] = half_codes(c4[y], 0);
+                            o[2 * y + 1] = half_codes(c4[y], 1);
+                        }
                     }
-                    // 16 values = two 16-byte chunks of the bf16 row; lanes of the upper half of a 128-value row store them
+                    // 16 values = two 16-byte chunks of the fp16 row; lanes of the upper half of a 128-value row store them
                     // in the other order, which keeps the two boxes' banks apart
                     const uint32_t line = dst + ((2 * chunk) >> 3) * kBox + row * 128;
                     const int c0 = (2 * chunk) & 7, flip = (D == 128 && chunk >= 4) ? 1 : 0;
@@ -706,6 +788,40 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                if (u != 1) continue;
+                // With the first tile staged: the item's queries, one row per thread (of A, then of B)
+                if (!tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll 1
+                for (int x = 0; x < (it.ntok > tpt ? 2 : 1); ++x) {
+                    const int row = 32 * cw + lane;
+                    const uint32_t line = sbase + C::OFF_Q + x * C::kTile + row * 128;
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        float f[8];
+                        unpack_bf16(lds128(line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                    }
+                    float up, down;
+                    power_to(top, 14, up, down);
+                    reinterpret_cast<float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x) * 128 + row] = down;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t at = line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4);
+                        float f[8];
+                        unpack_bf16(lds128(at), f);
+                        sts128(at, make_uint4(pack_half(f[0] * up, f[1] * up), pack_half(f[2] * up, f[3] * up),
+                                              pack_half(f[4] * up, f[5] * up), pack_half(f[6] * up, f[7] * up)));
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY));
+                ++qn;
             }
             kt += nk;
         }
