@@ -96,9 +96,11 @@ struct TileCfg {
     // registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
     static constexpr int kRegsLaunch = kE4M3 ? 128 : 168;
     static constexpr int kRegsCtl = kE4M3 ? 48 : 72;
-    static constexpr int kRegsConv = 96;
-    static constexpr int kRegsSoftmax = kE4M3 ? 184 : 216;
+    static constexpr int kRegsConv = 144;
+    static constexpr int kRegsSoftmax = kE4M3 ? 160 : 216;
     static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
+    // dec must not raise and inc must not lower what the launch granted
+    static_assert(kRegsCtl <= kRegsLaunch && kRegsConv >= 128 && kRegsSoftmax >= kRegsLaunch, "register split");
     static_assert(sizeof(TileItem) <= 64 && kSmem <= 232448, "shared memory budget");
 };
 
@@ -522,36 +524,73 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     break;
                 }
                 ptx::tc_fence_after();
-                float x[128];
-                if (!kE4M3) {
+                // Scores of 32 columns at a time.  bf16 caches: all 128 stay in registers.  e4m3 caches, whose converters
+                // take their share of the registers: the first 64 do, the others are read and scaled again for their weights
+                // (spilled registers would wait behind the tensor core's operand reads).
+                constexpr int kKeep = kE4M3 ? 2 : 4;
+                const float4* sc = reinterpret_cast<const float4*>(smem + C::OFF_KSC) + ((kt + j) & 3) * 32;
+                const int key = (it.t0 + j) * 128;
+                const bool edge = key < full_lo || key + 128 > full_hi;
+                const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
+                auto finish = [&](int h, const uint32_t (&r)[32], float (&x)[32]) {
+                    if (kE4M3) {   // times the keys' scales
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 f = sc[8 * h + k / 4];
+                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[k]), __uint_as_float(r[k + 1])}, {f.x, f.y});
+                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])}, {f.z, f.w});
+                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]);
+                    }
+                    if (kE4M3 && edge) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
+                    }
+                };
+                float x[kKeep][32];
+                float part[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part[k] = -INFINITY;
+                // row maximum (and, below, sum) over interleaved partials: short chains, one fixed order
+                auto top4 = [&](const float (&x)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
+                };
+                if constexpr (kE4M3) {
+                    uint32_t r[2][32];
+                    ptx::tmem_ld32(tS + 96, r[1]);
+                    ptx::tmem_ld_wait();
+                    float y[32];
+#pragma unroll
+                    for (int h = 3; h >= 0; --h) {
+                        if (h > 0) ptx::tmem_ld32(tS + 32 * (h - 1), r[(h - 1) & 1]);
+                        if (h >= 2) {
+                            finish(h, r[h & 1], y);
+                            top4(y);
+                        } else {
+                            finish(h, r[h & 1], x[h]);
+                            top4(x[h]);
+                        }
+                        if (h > 0) ptx::tmem_ld_wait();
+                    }
+                } else {
                     uint32_t r[4][32];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
-                } else {   // times the keys' scales, those of the next 32 columns on their way meanwhile
-                    const float4* sc = reinterpret_cast<const float4*>(smem + C::OFF_KSC) + ((kt + j) & 3) * 32;
-                    float4 s4[2][8];
+                    for (int h = 0; h < 4; ++h) finish(h, r[h], x[h & (kKeep - 1)]);
+                    if (edge) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) s4[0][k] = sc[k];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t r[32];
-                        ptx::tmem_ld32(tS + 32 * h, r);
-                        if (h < 3) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) s4[(h + 1) & 1][k] = sc[8 * (h + 1) + k];
-                        }
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = s4[h & 1][k];
-                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])}, {f.x, f.y});
-                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])}, {f.z, f.w});
-                            x[32 * h + 4 * k] = u.x, x[32 * h + 4 * k + 1] = u.y, x[32 * h + 4 * k + 2] = v.x, x[32 * h + 4 * k + 3] = v.y;
-                        }
+                        for (int k = 0; k < 128; ++k)
+                            if (k < ka || k >= kb) x[(k >> 5) & (kKeep - 1)][k & 31] = -INFINITY;
                     }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) top4(x[h & (kKeep - 1)]);
                 }
                 float grown = 1.f;   // of O, when the values' power of two has grown
                 if (kE4M3) {
@@ -563,19 +602,6 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     if (f != vfac) grown = vfac / f;
                     vfac = f;
                 }
-                const int key = (it.t0 + j) * 128;
-                if (key < full_lo || key + 128 > full_hi) {
-                    const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k < ka || k >= kb) x[k] = -INFINITY;
-                }
-                // row maximum and sum over interleaved partials: short chains, one fixed order
-                float part[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) part[k] = fmaxf(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-                for (int k = 8; k < 128; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
                 const float mx = c * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                 const bool raise = __any_sync(0xffffffffu, (valid && mx > m_ref + 8.f) || (kE4M3 && grown != 1.f));
                 if (raise) {
@@ -603,16 +629,25 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 // products with the first 64 keys start while the rest is worked out
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
+                    float y[32];
+                    if constexpr (kE4M3) {
+                        if (h >= kKeep) {
+                            uint32_t r[32];
+                            ptx::tmem_ld32(tS + 32 * h, r);
+                            ptx::tmem_ld_wait();
+                            finish(h, r, y);
+                        }
+                    }
                     uint32_t pk[16];
 #pragma unroll
-                    for (int k = 32 * h; k < 32 * h + 32; k += 2) {
-                        const ptx::f2 y = ptx::fma2({x[k], x[k + 1]}, {c, c}, {-m_use, -m_use});
-                        x[k] = ptx::ex2(y.x);
-                        x[k + 1] = ptx::ex2(y.y);
-                        const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, {x[k], x[k + 1]});
+                    for (int k = 0; k < 32; k += 2) {
+                        const float s0 = h < kKeep ? x[h & (kKeep - 1)][k] : y[k], s1 = h < kKeep ? x[h & (kKeep - 1)][k + 1] : y[k + 1];
+                        const ptx::f2 e = ptx::fma2({s0, s1}, {c, c}, {-m_use, -m_use});
+                        const ptx::f2 w{ptx::ex2(e.x), ptx::ex2(e.y)};
+                        const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, w);
                         part[k & 7] = s.x;
                         part[(k + 1) & 7] = s.y;
-                        pk[(k >> 1) & 15] = kE4M3 ? pack_half(x[k], x[k + 1]) : pack_bf16(x[k], x[k + 1]);
+                        pk[k >> 1] = kE4M3 ? pack_half(w.x, w.y) : pack_bf16(w.x, w.y);
                     }
                     ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
                     if (h & 1) {
@@ -668,7 +703,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
         }
     } else if (kE4M3) {
-        ptx::setmaxnreg_dec<C::kRegsConv>();
+        ptx::setmaxnreg_inc<C::kRegsConv>();
         // ================================================== converters
         constexpr int kChunks = D / 16;         // 16-byte chunks of codes per key
         constexpr int kRows = 32 / kChunks;     // keys that one load instruction of a warp covers
@@ -708,12 +743,10 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 if (key < it.lo || key >= it.hi) return make_uint4(0, 0, 0, 0);
                 return __ldg(reinterpret_cast<const uint4*>((const uint8_t*)base + (cell[l >= kLoads / 2] + (r & 15)) * D + 16 * chunk));
             };
-            uint4 w[kLoads];
             // Scales of a key tile (they come with K): the key's own of K, those of this warp's keys of V, and the largest of
             // V so far, for which every warp reads the whole tile's.
-            float ks = 0.f, vs = 0.f, vtop = 0.f;
-            auto scales = [&](int t) {
-                float v4[4];
+            float ks = 0.f, vs = 0.f, vtop = 0.f, v4[4];
+            auto load_scales = [&](int t) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int key = t * 128 + 32 * c + lane;
@@ -723,21 +756,19 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     v4[c] = in ? __ldg(p.c.v_scale + at) : 0.f;
                     if (c == cw) ks = in ? __ldg(p.c.k_scale + at) : 0.f;
                 }
+            };
+            auto use_scales = [&]() {
                 vs = cw == 0 ? v4[0] : cw == 1 ? v4[1] : cw == 2 ? v4[2] : v4[3];
                 vtop = fmaxf(vtop, fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3])));
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, d));
             };
-            aim(it.t0);
-            scales(it.t0);
-#pragma unroll
-            for (int l = 0; l < kLoads; ++l) w[l] = load(l, p.c.k);
-#pragma unroll 1
-            for (int u = 0; u < 2 * nk; ++u, ++kv) {
+            // One unit: the codes `w` (loaded during the unit before it) into a stage; `next` (loaded first, so that the proxy
+            // fence at the end, which waits for every access before it, finds them there) are the following unit's.
+            auto unit = [&](int u, const uint4 (&w)[kLoads], uint4 (&next)[kLoads]) -> bool {
                 const int st = kv % kKvStages;
                 if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), (uint32_t)((kv / kKvStages - 1) & 1), tw)) {
-                    ok = false;
-                    break;
+                    return false;
                 }
                 const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
                 float vup, vback;
@@ -751,14 +782,17 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 const bool more = u + 1 < 2 * nk;
                 if (more && (u & 1)) {
                     aim(it.t0 + (u + 1) / 2);
-                    scales(it.t0 + (u + 1) / 2);
+                    load_scales(it.t0 + (u + 1) / 2);
                 }
-                const void* base = (u & 1) ? p.c.k : p.c.v;   // of the next unit
+                if (more) {
+                    const void* base = (u & 1) ? p.c.k : p.c.v;
 #pragma unroll
-                for (int l = 0; l < kLoads; ++l) {   // convert a chunk, and load the next unit's in its place
+                    for (int l = 0; l < kLoads; ++l) next[l] = load(l, base);
+                }
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
                     const int row = 32 * cw + kRows * l + sub;
                     const uint32_t c4[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
-                    if (more) w[l] = load(l, base);
                     uint32_t o[8];
                     if (u & 1) {
                         const float sc = __shfl_sync(0xffffffffu, scale, kRows * l + sub);
@@ -785,15 +819,14 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     sts128(line + (((c0 + flip) ^ (row & 7)) << 4), flip ? v1 : v0);
                     sts128(line + (((c0 + 1 - flip) ^ (row & 7)) << 4), flip ? v0 : v1);
                 }
+                if (more && (u & 1)) use_scales();
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
-                if (u != 1) continue;
+                ++kv;
+                if (u != 1) return true;
                 // With the first tile staged: the item's queries, one row per thread (of A, then of B)
-                if (!tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw)) {
-                    ok = false;
-                    break;
-                }
+                if (!tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw)) return false;
 #pragma unroll 1
                 for (int x = 0; x < (it.ntok > tpt ? 2 : 1); ++x) {
                     const int row = 32 * cw + lane;
@@ -822,7 +855,16 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY));
                 ++qn;
-            }
+                return true;
+            };
+            uint4 wk[kLoads], wv[kLoads];
+            aim(it.t0);
+            load_scales(it.t0);
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) wk[l] = load(l, p.c.k);
+            use_scales();
+#pragma unroll 1
+            for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
             kt += nk;
         }
     }
