@@ -62,6 +62,8 @@ enum TileBar : int {
     T_ITEM_FULL = T_O_FULL + 2,
     T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
     T_PATCH = T_ITEM_EMPTY + kItemSlots,
+    T_SCALES,            // e4m3: the keys' scales of key tile t, slot t % 4
+    T_SCALES_END = T_SCALES + 3,
     T_COUNT
 };
 
@@ -96,8 +98,8 @@ struct TileCfg {
     // registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
     static constexpr int kRegsLaunch = kE4M3 ? 128 : 168;
     static constexpr int kRegsCtl = kE4M3 ? 48 : 72;
-    static constexpr int kRegsConv = 144;
-    static constexpr int kRegsSoftmax = kE4M3 ? 160 : 216;
+    static constexpr int kRegsConv = 128;
+    static constexpr int kRegsSoftmax = kE4M3 ? 168 : 216;
     static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
     // dec must not raise and inc must not lower what the launch granted
     static_assert(kRegsCtl <= kRegsLaunch && kRegsConv >= 128 && kRegsSoftmax >= kRegsLaunch, "register split");
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kE4M3 && (i == T_Q_READY || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // the converter warps
+            if (kE4M3 && (i == T_Q_READY || (i >= T_SCALES && i <= T_SCALES_END) || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // the converter warps
             if (i >= T_P_READY && i < T_P_READY + 4) count = 4;
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
@@ -519,26 +521,41 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             const int full_hi = p.causal ? pos0 + 1 : it.len, full_lo = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
             float m_ref = -INFINITY, l = 0.f, vfac = 1.f;   // O holds the sum over vfac
             for (int j = 0; j < nk; ++j, ++su) {
+                // e4m3: the keys' scales.  A read of shared memory takes some 400 cycles while the tensor core streams its
+                // operands, so they are read two blocks of 32 columns ahead (volatile reads stay in place): columns 64..
+                // before the scores are there, and the blocks 0 and 1 serve the maximum last and the weights first.
+                uint4 s4[2][8];   // block h in s4[h & 1]
+                float vnow = 1.f;
+                const uint32_t scales = sbase + C::OFF_KSC + ((kt + j) & 3) * 512;
+                if constexpr (kE4M3) {
+                    if (!tile_wait_warp(BAR(T_SCALES + ((kt + j) & 3)), (uint32_t)(((kt + j) >> 2) & 1), tw)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) s4[k >> 3][k & 7] = lds128(scales + 16 * (16 + k));
+                    vnow = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[(kt + j) & 3];
+                    if (j == 0) c = p.scale_log2e;
+                }
                 if (!tile_wait_warp(BAR(T_S_FULL + x_), (uint32_t)(su & 1), tw)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                // Scores of 32 columns at a time.  bf16 caches: all 128 stay in registers.  e4m3 caches, whose converters
-                // take their share of the registers: the first 64 do, the others are read and scaled again for their weights
-                // (spilled registers would wait behind the tensor core's operand reads).
-                constexpr int kKeep = kE4M3 ? 2 : 4;
-                const float4* sc = reinterpret_cast<const float4*>(smem + C::OFF_KSC) + ((kt + j) & 3) * 32;
+                // Scores of 32 columns at a time.  bf16 caches: all 128 stay in registers.  e4m3 caches, whose converters and
+                // scales take their share of the registers: read (and scaled) once for the maximum and again for the weights
+                // (spilled registers would wait as reads of shared memory do).
+                constexpr int kKeep = kE4M3 ? 1 : 4;
                 const int key = (it.t0 + j) * 128;
                 const bool edge = key < full_lo || key + 128 > full_hi;
                 const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
-                auto finish = [&](int h, const uint32_t (&r)[32], float (&x)[32]) {
+                auto finish = [&](int h, const uint32_t (&r)[32], float (&x)[32], const uint4 (&sc)[8]) {
                     if (kE4M3) {   // times the keys' scales
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
-                            const float4 f = sc[8 * h + k / 4];
-                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[k]), __uint_as_float(r[k + 1])}, {f.x, f.y});
-                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])}, {f.z, f.w});
+                            const uint4 f = sc[k / 4];
+                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[k]), __uint_as_float(r[k + 1])}, {__uint_as_float(f.x), __uint_as_float(f.y)});
+                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])}, {__uint_as_float(f.z), __uint_as_float(f.w)});
                             x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
                         }
                     } else {
@@ -561,21 +578,18 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     for (int k = 0; k < 32; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
                 };
                 if constexpr (kE4M3) {
-                    uint32_t r[2][32];
-                    ptx::tmem_ld32(tS + 96, r[1]);
-                    ptx::tmem_ld_wait();
-                    float y[32];
 #pragma unroll
                     for (int h = 3; h >= 0; --h) {
-                        if (h > 0) ptx::tmem_ld32(tS + 32 * (h - 1), r[(h - 1) & 1]);
+                        uint32_t r[32];
+                        float y[32];
+                        ptx::tmem_ld32(tS + 32 * h, r);
+                        ptx::tmem_ld_wait();
+                        finish(h, r, y, s4[h & 1]);
+                        top4(y);
                         if (h >= 2) {
-                            finish(h, r[h & 1], y);
-                            top4(y);
-                        } else {
-                            finish(h, r[h & 1], x[h]);
-                            top4(x[h]);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) s4[h & 1][k] = lds128(scales + 16 * (8 * (h - 2) + k));
                         }
-                        if (h > 0) ptx::tmem_ld_wait();
                     }
                 } else {
                     uint32_t r[4][32];
@@ -583,7 +597,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     for (int h = 0; h < 4; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) finish(h, r[h], x[h & (kKeep - 1)]);
+                    for (int h = 0; h < 4; ++h) finish(h, r[h], x[h & (kKeep - 1)], s4[0]);
                     if (edge) {
 #pragma unroll
                         for (int k = 0; k < 128; ++k)
@@ -594,13 +608,12 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 }
                 float grown = 1.f;   // of O, when the values' power of two has grown
                 if (kE4M3) {
-                    const float f = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[(kt + j) & 3];
                     if (j == 0) {
-                        c = p.scale_log2e * reinterpret_cast<const float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x_) * 128 + row];
-                        vfac = f;
+                        c *= reinterpret_cast<const float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x_) * 128 + row];
+                        vfac = vnow;
                     }
-                    if (f != vfac) grown = vfac / f;
-                    vfac = f;
+                    if (vnow != vfac) grown = vfac / vnow;
+                    vfac = vnow;
                 }
                 const float mx = c * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                 const bool raise = __any_sync(0xffffffffu, (valid && mx > m_ref + 8.f) || (kE4M3 && grown != 1.f));
@@ -631,17 +644,19 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 for (int h = 0; h < 4; ++h) {
                     float y[32];
                     if constexpr (kE4M3) {
-                        if (h >= kKeep) {
-                            uint32_t r[32];
-                            ptx::tmem_ld32(tS + 32 * h, r);
-                            ptx::tmem_ld_wait();
-                            finish(h, r, y);
+                        uint32_t r[32];
+                        ptx::tmem_ld32(tS + 32 * h, r);
+                        ptx::tmem_ld_wait();
+                        finish(h, r, y, s4[h & 1]);
+                        if (h < 2) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) s4[h & 1][k] = lds128(scales + 16 * (8 * (h + 2) + k));
                         }
                     }
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const float s0 = h < kKeep ? x[h & (kKeep - 1)][k] : y[k], s1 = h < kKeep ? x[h & (kKeep - 1)][k + 1] : y[k + 1];
+                        const float s0 = kE4M3 ? y[k] : x[h & (kKeep - 1)][k], s1 = kE4M3 ? y[k + 1] : x[h & (kKeep - 1)][k + 1];
                         const ptx::f2 e = ptx::fma2({s0, s1}, {c, c}, {-m_use, -m_use});
                         const ptx::f2 w{ptx::ex2(e.x), ptx::ex2(e.y)};
                         const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, w);
@@ -822,7 +837,10 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 if (more && (u & 1)) use_scales();
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                if (lane == 0) {
+                    ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                    if (!(u & 1)) ptx::mbar_arrive(BAR(T_SCALES + ((kt + (u >> 1)) & 3)));
+                }
                 ++kv;
                 if (u != 1) return true;
                 // With the first tile staged: the item's queries, one row per thread (of A, then of B)
