@@ -6,18 +6,21 @@
 // reading the cache once: 4 n G D operations against 2 * 2 D bytes per key and
 // head is at most 16 operations per byte, where the GPU has 285 per byte of
 // memory bandwidth.  So everything serves the stream of pages:
-//   - one persistent CTA per SM; a producer warp walks the CTA's items and
-//     keeps a ring of 64-key stages (K and V, 128 to 160 KB) full by TMA, across item
-//     boundaries, each lane issuing one of a stage's copies (one per page,
-//     64-value column and K/V: pages of 16 tokens give 16 copies);
-//   - eight consumer warps; the stages alternate between two groups of four,
-//     each warp taking 16 keys of a stage: S = Q K^T (m16n8k16, 16 rows are the
-//     instruction's least), a running maximum and sum per row, O += P V, all in
-//     registers; 16-row products at 16 keys each use under a fifth of the
-//     matrix rate that mma.sync has, so the wider tcgen05 tiles (128 rows, of
-//     which 4 would be real) have nothing to add here;
-//   - at the end of an item the eight warps' (O, m, l) are joined in shared
-//     memory in a fixed order while the ring refills.
+//   - one persistent CTA per SM with two independent halves, each a producer
+//     warp and four consumers working through items of their own: while one
+//     half joins the results of an item or waits for the next one's queries,
+//     the other streams;
+//   - a half's producer walks its items and keeps a ring of 64-key stages (K
+//     and V, 64 KB) full by TMA, across item boundaries, each lane
+//     issuing one of a stage's copies (one per page, 64-value column and K/V:
+//     pages of 16 tokens give 16 copies);
+//   - each consumer warp takes 16 keys of a stage: S = Q K^T (m16n8k16, 16 rows
+//     are the instruction's least), a running maximum and sum per row, O += P V,
+//     all in registers; 16-row products at 16 keys each use under a fifth of
+//     the matrix rate that mma.sync has, so the wider tcgen05 tiles (128 rows,
+//     of which 4 would be real) have nothing to add here;
+//   - at the end of an item the four warps' (O, m, l) are joined in shared
+//     memory in a fixed order.
 //
 // e4m3 caches.  Codes become fp16 pairs in registers (exact: e4m3 has 3
 // fraction bits and exponents -9..8), so the products run in fp16: Q is scaled
@@ -94,7 +97,8 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The four consumer warps of one half.
+__device__ __forceinline__ void consumer_barrier(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
 // ---------------------------------------------------------------- few rows
 template <int D, bool kE4M3>
@@ -102,18 +106,16 @@ struct FewCfg {
     static constexpr int kElem = kE4M3 ? 1 : 2;
     static constexpr int kHalfStage = kFewKeys * D * kElem;   // K, then V
     static constexpr int kStage = 2 * kHalfStage;
-    // even, so that a stage always belongs to the same group of consumers: a warp then waits for every phase of its
-    // stages' barriers in turn (of an odd count it would skip every other one, and parity cannot tell phase u from u + 2)
-    static constexpr int kStages = (163840 / kStage / 2 * 2) < 16 ? 163840 / kStage / 2 * 2 : 16;
-    static_assert(kStages % 2 == 0 && kStages >= 4, "stage ring");
+    static constexpr int kStages = (65536 / kStage) < 8 ? 65536 / kStage : 8;   // of each half
+    static_assert(kStages >= 2, "stage ring");
     static constexpr int kSlotRow = kE4M3 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
-    static constexpr int OFF_SCALE = kStages * kStage;        // [stage][K, V][kFewKeys] fp32
-    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? kStages * 2 * kFewKeys * 4 : 0);
-    static constexpr int OFF_M = OFF_SLOT + 4 * kFewRows * kSlotRow * 4;   // [parity][warp][row]
-    static constexpr int OFF_L = OFF_M + 2 * 8 * kFewRows * 4;             // [warp][row]
+    static constexpr int OFF_SCALE = 2 * kStages * kStage;        // [half][stage][K, V][kFewKeys] fp32
+    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? 2 * kStages * 2 * kFewKeys * 4 : 0);   // [half][warp][row]
+    static constexpr int OFF_M = OFF_SLOT + 8 * kFewRows * kSlotRow * 4;   // [half][parity][warp][row]
+    static constexpr int OFF_L = OFF_M + 2 * 8 * kFewRows * 4;             // [half][warp][row]
     static constexpr int OFF_PLAN = OFF_L + 8 * kFewRows * 4;
     static constexpr int OFF_BAR = (OFF_PLAN + (int)sizeof(Plan) + 15) / 16 * 16;
-    static constexpr int OFF_ABORT = OFF_BAR + 2 * kStages * 8;
+    static constexpr int OFF_ABORT = OFF_BAR + 4 * kStages * 8;   // after [half][full, empty]
     static constexpr int kSmem = OFF_ABORT + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -157,20 +159,23 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
+__global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
     using C = FewCfg<D, kE4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
     const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t bar_full = sbase + C::OFF_BAR, bar_empty = bar_full + 8 * C::kStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = warp < 8 ? warp >> 2 : warp - 8;
+    const uint32_t ring = sbase + half * C::kStages * C::kStage;
+    const uint32_t bar_full = sbase + C::OFF_BAR + half * 16 * C::kStages, bar_empty = bar_full + 8 * C::kStages;
 
     if (threadIdx.x == 256) {
         *abort = 0;
-        for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
-            ptx::mbar_init(bar_empty + 8 * s, 4);
+        for (int s = 0; s < 2 * C::kStages; ++s) {
+            const uint32_t bar = sbase + C::OFF_BAR + (s / C::kStages) * 16 * C::kStages + 8 * (s % C::kStages);
+            ptx::mbar_init(bar, 1);
+            ptx::mbar_init(bar + 8 * C::kStages, 4);
         }
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&p.tm_k);
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
     ItemWalk walk;
     FewItem it;
 
-    if (warp == 8) {
+    if (warp >= 8) {
         // ================================================== producer
         const int page = p.c.page_size, rows = page < kFewKeys ? page : kFewKeys;
         const int subs = kFewKeys / rows;                 // copies of one kind along a stage's keys
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
         const int sub = lane / kinds, kind = lane % kinds;
         const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
         int tc = 0;                                       // stages used so far
-        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        for (int item = half * gridDim.x + blockIdx.x; item < items; item += 2 * gridDim.x) {
             walk.at(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
             const int e0 = max(it.t0 * kFewKeys, it.c.lo) >> p.page_shift;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
                 __syncwarp();
                 if (need) {
                     const int y = k0 & (page - 1), head = pg * p.c.Hkv + it.hk;
-                    const uint32_t base = sbase + stage * C::kStage;
+                    const uint32_t base = ring + stage * C::kStage;
                     if (!kE4M3) {
                         constexpr int kBoxes = D / 64;
                         const int box = kind % kBoxes, val = kind / kBoxes;
@@ -233,7 +238,8 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
                         ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * D, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
                     } else {
                         const float* src = (kind == 3 ? p.c.v_scale : p.c.k_scale) + (long long)head * page + y;
-                        bulk_load(sbase + C::OFF_SCALE + ((stage * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src, rows * 4, full);
+                        bulk_load(sbase + C::OFF_SCALE + (((half * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src,
+                                  rows * 4, full);
                     }
                 }
             }
@@ -252,15 +258,15 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
 
     // ================================================== consumers
     const int g = lane >> 2, c4 = lane & 3;
-    const int group = warp >> 2, ws = warp & 3;
+    const int ws = warp & 3;
     // key of column n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
     // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
     auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
-    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT);
-    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M);
-    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L);
+    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + half * 4 * kFewRows * C::kSlotRow;
+    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + half * 2 * 4 * kFewRows;
+    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + half * 4 * kFewRows;
     int tc = 0, parity = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x, parity ^= 1) {
+    for (int item = half * gridDim.x + blockIdx.x; item < items; item += 2 * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
         const int R = it.s.n * p.G;
         const bool two = R > 8;   // rows 8..15 exist
@@ -333,11 +339,10 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
         float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
         for (int t = it.t0; t < it.t1; ++t, ++tc) {
-            if ((tc & 1) != group) continue;
             const int stage = tc % C::kStages;
             few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
             __syncwarp();
-            const uint32_t sk = sbase + stage * C::kStage, sv = sk + C::kHalfStage;
+            const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
             const int key0 = t * kFewKeys + 16 * ws;   // this warp's first key
             const bool edge = key0 < full_lo || key0 + 16 > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
                     const int at = 16 * ws + 8 * n + perm(2 * c4 + e);
                     float ks = 1.f;
                     if (kE4M3) {
-                        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + stage * 2 * kFewKeys;
+                        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + (half * C::kStages + stage) * 2 * kFewKeys;
                         ks = sc[at];
                         lv[n][e] = __log2f(sc[kFewKeys + at]);
                     }
@@ -505,78 +510,44 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
             if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
         }
 
-        // ---------------------------------------------- join the eight warps
-        float* const mp = mrow + parity * 8 * kFewRows;
+        // ---------------------------------------------- join the four warps
+        float* const mp = mrow + parity * 4 * kFewRows;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (c4 == 0) mp[warp * kFewRows + g + 8 * h] = m[h];
+            if (c4 == 0) mp[ws * kFewRows + g + 8 * h] = m[h];
         }
-        consumer_barrier();
+        consumer_barrier(half);
+        float* const slot = slots + ws * kFewRows * C::kSlotRow;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if (g + 8 * h >= R) continue;   // rows past R hold copies; they are neither joined nor stored
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) top = fmaxf(top, mp[w * kFewRows + g + 8 * h]);
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * kFewRows + g + 8 * h]);
             // outputs carry 2^-mv (weights with their scales), sums 2^-m
             const float fo = (top == -INFINITY || mv[h] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[h] : m[h]) - top);
-            l[h] *= (top == -INFINITY || m[h] == -INFINITY) ? 0.f : ptx::ex2(m[h] - top);
+            if (c4 == 0) lrow[ws * kFewRows + g + 8 * h] = l[h] * ((top == -INFINITY || m[h] == -INFINITY) ? 0.f : ptx::ex2(m[h] - top));
+            float* row = slot + (g + 8 * h) * C::kSlotRow;
+            if (!kE4M3) {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                o[j][2 * h] *= fo;
-                o[j][2 * h + 1] *= fo;
-            }
-            if (c4 == 0) lrow[warp * kFewRows + g + 8 * h] = l[h];
-        }
-        // rows past R hold copies; they are neither joined nor stored
-        auto each = [&](float* slot, bool add) {
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2*>(row + 8 * j + 2 * c4) = make_float2(o[j][2 * h] * fo, o[j][2 * h + 1] * fo);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (g + 8 * h >= R) continue;
-                float* row = slot + (g + 8 * h) * C::kSlotRow;
-                if (!kE4M3) {
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        float2* q = reinterpret_cast<float2*>(row + 8 * j + 2 * c4);
-                        if (add) {
-                            const float2 v = *q;
-                            o[j][2 * h] += v.x;
-                            o[j][2 * h + 1] += v.y;
-                        } else {
-                            *q = make_float2(o[j][2 * h], o[j][2 * h + 1]);
-                        }
+                    for (int k = 0; k < D / 32; ++k) {   // values (2c + e) D/8 + 4k..: chunk index XOR c spreads the banks
+                        const int chunk = ((2 * c4 + e) * (D / 32) + k) ^ c4;
+                        *reinterpret_cast<float4*>(row + 4 * chunk) =
+                            make_float4(o[4 * k][2 * h + e] * fo, o[4 * k + 1][2 * h + e] * fo, o[4 * k + 2][2 * h + e] * fo,
+                                        o[4 * k + 3][2 * h + e] * fo);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {   // values (2c + e) D/8 + 4k..: chunk index XOR c spreads the banks
-                            const int chunk = ((2 * c4 + e) * (D / 32) + k) ^ c4;
-                            float4* q = reinterpret_cast<float4*>(row + 4 * chunk);
-                            if (add) {
-                                const float4 v = *q;
-                                o[4 * k][2 * h + e] += v.x;
-                                o[4 * k + 1][2 * h + e] += v.y;
-                                o[4 * k + 2][2 * h + e] += v.z;
-                                o[4 * k + 3][2 * h + e] += v.w;
-                            } else {
-                                *q = make_float4(o[4 * k][2 * h + e], o[4 * k + 1][2 * h + e], o[4 * k + 2][2 * h + e],
-                                                 o[4 * k + 3][2 * h + e]);
-                            }
-                        }
-                }
             }
-        };
-        float* const slot = slots + ws * kFewRows * C::kSlotRow;
-        if (group == 1) each(slot, false);
-        consumer_barrier();
-        if (group == 0) {
-            each(slot, true);
-            each(slot, false);
         }
-        consumer_barrier();
-        for (int i = threadIdx.x; i < R * (D / 4); i += 256) {
+        consumer_barrier(half);
+        for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
             const int r = i / (D / 4), q4 = i % (D / 4);
             const int chunk = kE4M3 ? q4 ^ (q4 / (D / 16)) : q4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -590,7 +561,7 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
                 a.w += v.w;
             }
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < 4; ++w) {
                 top = fmaxf(top, mp[w * kFewRows + r]);
                 sum += lrow[w * kFewRows + r];
             }
@@ -613,80 +584,119 @@ __global__ void __launch_bounds__(288, 1) paged_few_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- joining key ranges
 // One block per row of a split sequence: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its ranges, warp w
-// taking ranges w, w + 4, ... and the four warps joined in order, so the additions have one fixed order.
+// taking ranges w, w + 8, ... and the eight warps joined in order, so the additions have one fixed order.  The block
+// finds its first row while the kernel before it runs: it keeps its share of the plan in registers and little shared
+// memory, so that it fits beside that kernel's CTA on an SM.
 template <int D>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ PagedParams p) {
-    __shared__ Plan plan;
-    __shared__ float part[4][D];
-    __shared__ float part_l[4];
-    make_plan(p, plan, true, false);
-    wait_dependency();
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int E = D / 32, kSeqs = kMaxSeqs / 256;
+    struct Row {
+        int first, n, ns, local;   // its sequence; (token, head) in it
+        long long base;            // partial row of the sequence's first row
+    };
+    __shared__ Row found;
+    __shared__ int sums[2][8];
+    __shared__ float part[8][D];
+    __shared__ float part_l[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int E = D / 32;
-    // plan.rows counts ns partial rows for each row: walk the sequences with the row index
-    int b = 0;
-    long long before = 0;   // rows of split sequences before b
-    for (long long w = blockIdx.x;; w += gridDim.x) {
-        int ns = 1, n = 0;
-        long long rows = 0;
-        for (; b < p.nb; ++b) {
-            n = plan.seq[b].n;
-            const int pr = plan.rows[b + 1] - plan.rows[b];
-            rows = pr ? (long long)n * p.Hq : 0;
-            if (rows && w < before + rows) {
-                ns = (int)(pr / rows);
-                break;
-            }
-            before += rows;
+    // this thread's sequences: rows to join (n * Hq of split ones) and partial rows (times ns), and the counts before
+    Seq seq[kSeqs];
+    int ns_[kSeqs], rows = 0, parts = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqs; ++k) {
+        const int i = kSeqs * threadIdx.x + k;
+        ns_[k] = 1;
+        if (i >= p.nb) continue;
+        seq[k] = load_seq(p, p.b0 + i, false);
+        if (seq[k].n == 0) continue;
+        ns_[k] = (few_rows(seq[k].n, p.G) ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G))).ns;
+        if (ns_[k] > 1) {
+            rows += seq[k].n * p.Hq;
+            parts += seq[k].n * p.Hq * ns_[k];
         }
-        if (b >= p.nb) return;
-        const int local = (int)(w - before);   // (token, head)
-        const int i = local / p.Hq, h = local % p.Hq, hk = h / p.G;
-        const int R = n * p.G, r = i * p.G + h % p.G;
-        const long long base = plan.rows[b] + (long long)hk * R + r, step = (long long)p.c.Hkv * R;
-        if (base + (ns - 1) * step >= p.max_rows) continue;
-        float top = -INFINITY;
-        for (int s = lane; s < ns; s += 32) top = fmaxf(top, p.part_ml[base + s * step].x);
+    }
+    int sr = rows, sp = parts;
 #pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float mu = top == -INFINITY ? 0.f : top;
-        float a[E], l = 0.f;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sr, d), y = __shfl_up_sync(0xffffffffu, sp, d);
+        if (lane >= d) sr += x, sp += y;
+    }
+    if (lane == 31) sums[0][warp] = sr, sums[1][warp] = sp;
+    __syncthreads();
+    int total = 0;
+    sr -= rows, sp -= parts;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) sr += sums[0][w], sp += sums[1][w];
+        total += sums[0][w];
+    }
+    bool waited = false;
+    for (int w = blockIdx.x; w < total; w += gridDim.x) {
+        if (w >= sr && w < sr + rows) {   // one thread of the block
+            int r0 = sr;
+            long long p0 = sp;
 #pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = 0.f;
-#pragma unroll 8
-        for (int s = warp; s < ns; s += 4) {
-            const long long row = base + s * step;
-            const float2 ml = p.part_ml[row];
-            const float f = ptx::ex2(ml.x - mu);
-            l += f * ml.y;
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * lane);
-                a[0] += f * v.x;
-                a[1] += f * v.y;
-                a[E - 2] += f * v.z;
-                a[E - 1] += f * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(p.part_o + row * D + 2 * lane);
-                a[0] += f * v.x;
-                a[1] += f * v.y;
+            for (int k = 0; k < kSeqs; ++k) {
+                const int here = ns_[k] > 1 ? seq[k].n * p.Hq : 0;
+                if (w >= r0 && w < r0 + here) found = Row{seq[k].first, seq[k].n, ns_[k], w - r0, p0};
+                r0 += here;
+                p0 += (long long)here * ns_[k];
             }
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
-        if (lane == 0) part_l[warp] = l;
         __syncthreads();
-        const float sum = ((part_l[0] + part_l[1]) + part_l[2]) + part_l[3];
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const long long at = (long long)(plan.seq[b].first + i) * p.Hq + h;
-        if ((int)threadIdx.x < D / 2) {
-            const int d = 2 * threadIdx.x;
-            const float x = ((part[0][d] + part[1][d]) + part[2][d]) + part[3][d];
-            const float y = ((part[0][d + 1] + part[1][d + 1]) + part[2][d + 1]) + part[3][d + 1];
-            *reinterpret_cast<uint32_t*>(p.o + at * D + d) = pack_bf16(x * inv, y * inv);
+        const Row row = found;
+        if (!waited) wait_dependency();
+        waited = true;
+        const int i = row.local / p.Hq, h = row.local % p.Hq, hk = h / p.G;
+        const int R = row.n * p.G;
+        const long long base = row.base + (long long)hk * R + i * p.G + h % p.G, step = (long long)p.c.Hkv * R;
+        if (base + (row.ns - 1) * step < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
+            float top = -INFINITY;
+            for (int s = lane; s < row.ns; s += 32) top = fmaxf(top, p.part_ml[base + s * step].x);
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float mu = top == -INFINITY ? 0.f : top;
+            float a[E], l = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] = 0.f;
+#pragma unroll 4
+            for (int s = warp; s < row.ns; s += 8) {
+                const long long at = base + s * step;
+                const float2 ml = p.part_ml[at];
+                const float f = ptx::ex2(ml.x - mu);
+                l += f * ml.y;
+                if (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+                    a[0] += f * v.x;
+                    a[1] += f * v.y;
+                    a[E - 2] += f * v.z;
+                    a[E - 1] += f * v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + 2 * lane);
+                    a[0] += f * v.x;
+                    a[1] += f * v.y;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
+            if (lane == 0) part_l[warp] = l;
+            __syncthreads();
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sum += part_l[x];
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const long long at = (long long)(row.first + i) * p.Hq + h;
+            if ((int)threadIdx.x < D / 2) {
+                const int d = 2 * threadIdx.x;
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) x += part[v][d], y += part[v][d + 1];
+                *reinterpret_cast<uint32_t*>(p.o + at * D + d) = pack_bf16(x * inv, y * inv);
+            }
+            if (p.lse && threadIdx.x == 255) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
         }
-        if (p.lse && threadIdx.x == 127) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
         __syncthreads();
     }
+    if (!waited) wait_dependency();
 }
 
 // ---------------------------------------------------------------- host
@@ -712,7 +722,7 @@ int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) 
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 288, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 320, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
@@ -723,7 +733,7 @@ int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
     cfg.gridDim = dim3((unsigned)(max_rows < 8ll * sms ? max_rows : 8ll * sms));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -744,9 +754,8 @@ Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv)
     const long long few_q = G > kFewRows ? 0 : (max_q < kFewRows / G ? max_q : kFewRows / G);   // tokens of a few-rows sequence
     const long long n_few = nb < T ? nb : T;
     if (few_q > 0) {
-        // a window may start inside a tile: one tile more than the length has
-        const long long tiles = max_kv / kFewKeys + 2, by_len = (tiles + kFewSplitTiles - 1) / kFewSplitTiles;
-        const long long ns = by_len < few_max_splits(Hkv) ? by_len : few_max_splits(Hkv);
+        const long long tiles = (max_kv + kFewKeys - 1) / kFewKeys, by_len = (tiles + kFewSplitTiles - 1) / kFewSplitTiles;
+        const long long ns = tiles <= kFewWholeTiles ? 1 : by_len < few_max_splits(Hkv) ? by_len : few_max_splits(Hkv);
         r.few_items = n_few * Hkv * ns;
         if (ns > 1) r.rows += (few_q * n_few < T ? few_q * n_few : T) * Hq * ns;
     }

@@ -22,8 +22,10 @@ namespace dash {
 
 constexpr int kFewRows = 16;       // rows of one m16 matrix operand
 constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel
-constexpr int kFewSplitTiles = 4;  // at least this many stages per key range
-constexpr int kMaxSeqs = 1024;     // sequences per launch (their plan lies in shared memory)
+constexpr int kFewSplitTiles = 2;  // at least this many stages per key range
+constexpr int kFewWholeTiles = 4;  // sequences of so many stages are not split: joining costs more than it gains
+constexpr int kFewWorkers = 304;   // two halves of a CTA on each of a GB300's 152 SMs
+constexpr int kMaxSeqs = 512;      // sequences per launch (their plan lies in shared memory)
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
 constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
 constexpr int kTileFullItems = 76;     // items that keep the GPU busy without a split
@@ -91,14 +93,22 @@ __device__ __forceinline__ void seen_keys(const PagedParams& p, const Seq& s, in
     lo = (p.window && p0 + 1 > p.window) ? p0 + 1 - p.window : 0;
 }
 
-__host__ __device__ inline int few_max_splits(int Hkv) {   // about a thousand items for one long sequence: 6.7 per SM
-    const int n = 1024 / Hkv;
-    return n < 32 ? 32 : n > 256 ? 256 : n;
+// The most key ranges of a sequence: the least number of rounds of all workers (at most 4) that one sequence's items
+// nearly fill (to 31/32), so that a long sequence alone, and any number of them, leave few workers idle in the last round.
+__host__ __device__ inline int few_max_splits(int Hkv) {
+    int best = 1, best_items = 0, best_rounds = 1;
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+        const int ns = kFewWorkers * rounds / Hkv, items = ns * Hkv;
+        if (ns < 1) continue;
+        if (items * best_rounds > best_items * rounds) best = ns, best_items = items, best_rounds = rounds;
+        if (items * 32 >= kFewWorkers * rounds * 31) break;
+    }
+    return best;
 }
 
 // Key ranges of a sequence: `tiles` key tiles of its class cut into ns ranges of st tiles.
 __host__ __device__ inline void few_split(int tiles, int Hkv, int& ns, int& st) {
-    const int most = few_max_splits(Hkv);
+    const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(Hkv);
     st = (tiles + most - 1) / most;
     st = st < kFewSplitTiles ? kFewSplitTiles : st;
     ns = (tiles + st - 1) / st;
