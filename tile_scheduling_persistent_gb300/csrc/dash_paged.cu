@@ -14,11 +14,13 @@
 //     and V, 64 KB) full by TMA, across item boundaries, each lane
 //     issuing one of a stage's copies (one per page, 64-value column and K/V:
 //     pages of 16 tokens give 16 copies);
-//   - each consumer warp takes 16 keys of a stage: S = Q K^T (m16n8k16, 16 rows
-//     are the instruction's least), a running maximum and sum per row, O += P V,
-//     all in registers; 16-row products at 16 keys each use under a fifth of
-//     the matrix rate that mma.sync has, so the wider tcgen05 tiles (128 rows,
-//     of which 4 would be real) have nothing to add here;
+//   - each consumer warp takes 16 keys of a stage, all in registers, with the
+//     keys (and the values' columns) on the 16-row side of m16n8k16 and the
+//     query rows on its 8-column side: S^T = K Q^T, a running maximum and sum
+//     per column, O^T += V^T P^T.  One such pair of products covers 8 query
+//     rows (kRowTiles = 2 covers 16); with the rows on the 16-row side, half
+//     of the work would go to rows that a group of 8 heads does not have.  The
+//     wider tcgen05 tiles (128 rows, 4 or 8 of them real) have nothing to add;
 //   - at the end of an item the four warps' (O, m, l) are joined in shared
 //     memory in a fixed order.
 //
@@ -68,6 +70,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The transpose of an 8 x 8 matrix of 16-bit values in fragment layout.
+__device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t codes, int upper) {
     uint32_t h;
     const uint16_t c = (uint16_t)(upper ? codes >> 16 : codes);
@@ -108,7 +121,7 @@ struct FewCfg {
     static constexpr int kStage = 2 * kHalfStage;
     static constexpr int kStages = (65536 / kStage) < 8 ? 65536 / kStage : 8;   // of each half
     static_assert(kStages >= 2, "stage ring");
-    static constexpr int kSlotRow = kE4M3 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
+    static constexpr int kSlotRow = !kE4M3 ? D + 4 : D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
     static constexpr int OFF_SCALE = 2 * kStages * kStage;        // [half][stage][K, V][kFewKeys] fp32
     static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? 2 * kStages * 2 * kFewKeys * 4 : 0);   // [half][warp][row]
     static constexpr int OFF_M = OFF_SLOT + 8 * kFewRows * kSlotRow * 4;   // [half][parity][warp][row]
@@ -158,7 +171,7 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, int kRowTiles>
 __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
     using C = FewCfg<D, kE4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -257,9 +270,11 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
     }
 
     // ================================================== consumers
+    // Fragment of a lane: g = lane / 4, c = lane % 4.  S^T and P^T: keys g and g + 8 of the warp's 16, query rows
+    // 8 t + 2c and + 1; O^T: columns of the values as commented below, the same query rows.
     const int g = lane >> 2, c4 = lane & 3;
     const int ws = warp & 3;
-    // key of column n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
+    // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
     // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
     auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
     float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + half * 4 * kFewRows * C::kSlotRow;
@@ -269,81 +284,81 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
     for (int item = half * gridDim.x + blockIdx.x; item < items; item += 2 * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
         const int R = it.s.n * p.G;
-        const bool two = R > 8;   // rows 8..15 exist
-        // rows g and g + 8: their keys [lo, hi)
-        int hi[2], lo[2];
-        const __nv_bfloat16* qrow[2];
+        // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
+        int hi[kRowTiles][2], lo[kRowTiles][2], full_lo, full_hi, skip;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = min(g + 8 * h, R - 1), i = r / p.G;
-            seen_keys(p, it.s, i, i + 1, lo[h], hi[h]);
-            qrow[h] = p.q + (long long)(it.s.first + i) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
-        }
-        // tiles in [full_lo, full_hi) are seen whole by every row
-        int a0, a1, b0, b1;
-        seen_keys(p, it.s, 0, 1, a0, a1);
-        seen_keys(p, it.s, it.s.n - 1, it.s.n, b0, b1);
-        const int full_lo = b0, full_hi = a1;
-
-        uint32_t qf[D / 16][4];
-        float qs[2];   // scale of the scores of rows g, g + 8 (log2 units)
-        if (!kE4M3) {
+        for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const int d = 16 * k + 2 * c4;
-                qf[k][0] = *reinterpret_cast<const uint32_t*>(qrow[0] + d);
-                qf[k][2] = *reinterpret_cast<const uint32_t*>(qrow[0] + d + 8);
-                qf[k][1] = two ? *reinterpret_cast<const uint32_t*>(qrow[1] + d) : 0u;
-                qf[k][3] = two ? *reinterpret_cast<const uint32_t*>(qrow[1] + d + 8) : 0u;
+            for (int e = 0; e < 2; ++e) {
+                const int i = min(8 * t + 2 * c4 + e, R - 1) / p.G;
+                seen_keys(p, it.s, i, i + 1, lo[t][e], hi[t][e]);
             }
-            qs[0] = qs[1] = p.scale_log2e;
-        } else {
-            // step 4h + t holds values 64h + 16c + 4t + 0..3 of lane c
+        seen_keys(p, it.s, 0, 1, skip, full_hi);
+        seen_keys(p, it.s, it.s.n - 1, it.s.n, full_lo, skip);
+
+        // Q^T: row 8 t + g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3
+        uint32_t qf[kRowTiles][D / 16][2];
+        float qs[kRowTiles][2];   // scale of the scores of rows 8 t + 2c + e (log2 units)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int t = 0; t < kRowTiles; ++t) {
+            const int r = min(8 * t + g, R - 1);
+            const __nv_bfloat16* q =
+                p.q + (long long)(it.s.first + r / p.G) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
+            if (!kE4M3) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qf[t][k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
+                    qf[t][k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
+                }
+                qs[t][0] = qs[t][1] = p.scale_log2e;
+            } else {
                 float top = 0.f;
-                if (h == 0 || two) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(qrow[h] + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
-                        qf[k][h] = w.x;
-                        qf[k][2 + h] = w.y;
-                        top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
-                                               fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) qf[k][h] = qf[k][2 + h] = 0u;
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
+                    qf[t][k][0] = w.x;
+                    qf[t][k][1] = w.y;
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
+                                           fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
                 const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
                 const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                qs[h] = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                const float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                qs[t][0] = __shfl_sync(0xffffffffu, down, 8 * c4);
+                qs[t][1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t w = qf[k][2 * x + h];
-                        qf[k][2 * x + h] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                        const uint32_t w = qf[t][k][x];
+                        qf[t][k][x] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
                     }
             }
         }
 
-        float o[D / 8][4];
+        float o[kRowTiles][D / 16][4], m[kRowTiles][2], mv[kRowTiles][2], l[kRowTiles][2];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int t = 0; t < kRowTiles; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[t][e] = mv[t][e] = -INFINITY;
+                l[t][e] = 0.f;
+            }
+        }
 
-        for (int t = it.t0; t < it.t1; ++t, ++tc) {
+        for (int kt = it.t0; kt < it.t1; ++kt, ++tc) {
             const int stage = tc % C::kStages;
             few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
             __syncwarp();
             const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
-            const int key0 = t * kFewKeys + 16 * ws;   // this warp's first key
+            const int key0 = kt * kFewKeys + 16 * ws;   // this warp's first key
             const bool edge = key0 < full_lo || key0 + 16 > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
                 const int r = lane >> 1;
@@ -361,125 +376,141 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
                 __syncwarp();
             }
 
-            float s[2][4];
+            float s[kRowTiles][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
             if (!kE4M3) {
-                const int row = 16 * ws + (lane & 7) + 8 * (lane >> 4);
+                const int row = 16 * ws + (lane & 15);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    uint32_t r[4];
-                    const int chunk = 2 * (k & 3) + ((lane >> 3) & 1);
-                    ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), r);
-                    mma16816<false>(s[0], qf[k], r[0], r[1]);
-                    mma16816<false>(s[1], qf[k], r[2], r[3]);
+                    uint32_t a[4];
+                    const int chunk = 2 * (k & 3) + (lane >> 4);
+                    ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+#pragma unroll
+                    for (int t = 0; t < kRowTiles; ++t) mma16816<false>(s[t], a, qf[t][k][0], qf[t][k][1]);
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int row = 16 * ws + 8 * n + perm(g);
+                for (int h = 0; h < D / 64; ++h) {
+                    const int chunk = 4 * h + c4;
+                    uint32_t w[2][4];
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const int chunk = 4 * h + c4;
-                        const uint4 w = lds128(D == 128 ? sk + row * 128 + ((chunk ^ (row & 7)) << 4)
+                    for (int n = 0; n < 2; ++n) {
+                        const int row = 16 * ws + 8 * n + perm(g);
+                        const uint4 v = lds128(D == 128 ? sk + row * 128 + ((chunk ^ (row & 7)) << 4)
                                                         : sk + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                        w[n][0] = v.x, w[n][1] = v.y, w[n][2] = v.z, w[n][3] = v.w;
+                    }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma16816<true>(s[n], qf[4 * h + x], half2_of_e4m3(ww[x], 0), half2_of_e4m3(ww[x], 1));
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t a[4] = {half2_of_e4m3(w[0][x], 0), half2_of_e4m3(w[1][x], 0), half2_of_e4m3(w[0][x], 1),
+                                               half2_of_e4m3(w[1][x], 1)};
+#pragma unroll
+                        for (int t = 0; t < kRowTiles; ++t) mma16816<true>(s[t], a, qf[t][4 * h + x][0], qf[t][4 * h + x][1]);
                     }
                 }
             }
 
             // scores in log2 units; lv = log2 of the value scales (e4m3)
-            float lv[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+            float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+            if (kE4M3) {
+                const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) +
+                                  (half * C::kStages + stage) * 2 * kFewKeys + 16 * ws + perm(g);
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int at = 16 * ws + 8 * n + perm(2 * c4 + e);
-                    float ks = 1.f;
-                    if (kE4M3) {
-                        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + (half * C::kStages + stage) * 2 * kFewKeys;
-                        ks = sc[at];
-                        lv[n][e] = __log2f(sc[kFewKeys + at]);
-                    }
-                    s[n][e] *= qs[0] * ks;
-                    s[n][2 + e] *= qs[1] * ks;
-                    if (edge) {
-                        const int key = t * kFewKeys + at;
-                        if (key < lo[0] || key >= hi[0]) s[n][e] = -INFINITY;
-                        if (key < lo[1] || key >= hi[1]) s[n][2 + e] = -INFINITY;
-                        if (kE4M3 && (key < it.c.lo || key >= it.c.hi)) lv[n][e] = 0.f;
-                    }
-                }
-            // running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8
-            float mx[2], mw[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                mw[h] = mx[h];
-                if (kE4M3) {
-                    mw[h] = fmaxf(fmaxf(s[0][2 * h] + lv[0][0], s[0][2 * h + 1] + lv[0][1]),
-                                  fmaxf(s[1][2 * h] + lv[1][0], s[1][2 * h + 1] + lv[1][1]));
-                    mw[h] = fmaxf(mw[h], __shfl_xor_sync(0xffffffffu, mw[h], 1));
-                    mw[h] = fmaxf(mw[h], __shfl_xor_sync(0xffffffffu, mw[h], 2));
+                for (int n = 0; n < 2; ++n) {
+                    ks[n] = sc[8 * n];
+                    lv[n] = lg2(sc[kFewKeys + 8 * n]);
                 }
             }
-            bool raise = mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f;
-            if (kE4M3) raise = raise || mw[0] > mv[0] + 8.f || mw[1] > mv[1] + 8.f;
-            if (__any_sync(0xffffffffu, raise)) {
-                float f[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float nm = fmaxf(m[h], mx[h]), nv = fmaxf(mv[h], mw[h]);
-                    l[h] *= nm == -INFINITY ? 1.f : ptx::ex2(m[h] - nm);
-                    f[h] = nv == -INFINITY ? 1.f : ptx::ex2(mv[h] - nv);
-                    m[h] = nm;
-                    mv[h] = nv;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][0] *= f[0];
-                    o[j][1] *= f[0];
-                    o[j][2] *= f[1];
-                    o[j][3] *= f[1];
-                }
-            }
-            uint32_t pa[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float mu = m[h] == -INFINITY ? 0.f : m[h], vu = mv[h] == -INFINITY ? 0.f : mv[h];
-                float w[2][2];
+            for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = s[n][2 * h + e];
-                        const float pr = ptx::ex2(x - mu);
-                        l[h] += pr;
-                        w[n][e] = kE4M3 ? ptx::ex2(x + (lv[n][e] - vu)) : pr;
+                    for (int e = 0; e < 2; ++e) s[t][2 * n + e] *= kE4M3 ? qs[t][e] * ks[n] : qs[t][e];
+            if (edge) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int key = key0 + 8 * n + perm(g);
+#pragma unroll
+                    for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (key < lo[t][e] || key >= hi[t][e]) s[t][2 * n + e] = -INFINITY;
+                    if (key < it.c.lo || key >= it.c.hi) lv[n] = 0.f;
+                }
+            }
+            // running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8
+            float mx[kRowTiles][2], mw[kRowTiles][2];
+            bool raise = false;
+#pragma unroll
+            for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[t][e] = fmaxf(s[t][e], s[t][2 + e]);
+                    mw[t][e] = kE4M3 ? fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) : 0.f;
+#pragma unroll
+                    for (int d = 4; d <= 16; d <<= 1) {
+                        mx[t][e] = fmaxf(mx[t][e], __shfl_xor_sync(0xffffffffu, mx[t][e], d));
+                        if (kE4M3) mw[t][e] = fmaxf(mw[t][e], __shfl_xor_sync(0xffffffffu, mw[t][e], d));
                     }
+                    raise = raise || mx[t][e] > m[t][e] + 8.f || (kE4M3 && mw[t][e] > mv[t][e] + 8.f);
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int t = 0; t < kRowTiles; ++t) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float nm = fmaxf(m[t][e], mx[t][e]), nv = kE4M3 ? fmaxf(mv[t][e], mw[t][e]) : nm;
+                        l[t][e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[t][e] - nm);
+                        f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - nv);
+                        m[t][e] = nm;
+                        mv[t][e] = nv;
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[t][j][0] *= f[0];
+                        o[t][j][1] *= f[1];
+                        o[t][j][2] *= f[0];
+                        o[t][j][3] *= f[1];
+                    }
+                }
+            }
+            uint32_t pb[kRowTiles][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
+#pragma unroll
+            for (int t = 0; t < kRowTiles; ++t) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mu = m[t][e] == -INFINITY ? 0.f : m[t][e], vu = mv[t][e] == -INFINITY ? 0.f : mv[t][e];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float x = s[t][2 * n + e];
+                        const float pr = ptx::ex2(x - mu);
+                        l[t][e] += pr;
+                        w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n] - vu)) : pr;
+                    }
+                }
                 // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
-                pa[h] = kE4M3 ? pack_half(w[0][0], w[0][1]) : pack_bf16(w[0][0], w[0][1]);
-                pa[2 + h] = kE4M3 ? pack_half(w[1][0], w[1][1]) : pack_bf16(w[1][0], w[1][1]);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    pb[t][n] = transposed8x8(kE4M3 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
             }
 
-            if (!kE4M3) {
-                const int row = 16 * ws + (lane & 15);
+            if (!kE4M3) {   // tile j of O^T: value columns 16j + g and + 8
+                const int row = 16 * ws + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    uint32_t r[4];
-                    const int chunk = 2 * (j & 3) + (lane >> 4);
-                    ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), r);
-                    mma16816<false>(o[2 * j], pa, r[0], r[1]);
-                    mma16816<false>(o[2 * j + 1], pa, r[2], r[3]);
+                    uint32_t a[4];
+                    const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
+                    ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+#pragma unroll
+                    for (int t = 0; t < kRowTiles; ++t) mma16816<false>(o[t][j], a, pb[t][0], pb[t][1]);
                 }
-            } else {
+            } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
                 constexpr int kWords = D / 32;   // words of a lane's D / 8 columns
                 uint32_t w[4][kWords];
@@ -495,15 +526,15 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
                     }
                 }
 #pragma unroll
-                for (int y = 0; y < kWords; ++y) {
+                for (int y = 0; y < kWords; ++y)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {   // columns 4y + 2z, + 1: byte pairs of the two keys of each half
                         const uint32_t sel = z ? 0x7362u : 0x5140u;
                         const uint32_t lo2 = __byte_perm(w[0][y], w[1][y], sel), hi2 = __byte_perm(w[2][y], w[3][y], sel);
-                        mma16816<true>(o[4 * y + 2 * z], pa, half2_of_e4m3(lo2, 0), half2_of_e4m3(hi2, 0));
-                        mma16816<true>(o[4 * y + 2 * z + 1], pa, half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 1));
+                        const uint32_t a[4] = {half2_of_e4m3(lo2, 0), half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 0), half2_of_e4m3(hi2, 1)};
+#pragma unroll
+                        for (int t = 0; t < kRowTiles; ++t) mma16816<true>(o[t][2 * y + z], a, pb[t][0], pb[t][1]);
                     }
-                }
             }
             if (edge) ptx::fence_proxy_async_smem();   // the zeroed rows before the next copy into the stage
             __syncwarp();
@@ -513,43 +544,47 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
         // ---------------------------------------------- join the four warps
         float* const mp = mrow + parity * 4 * kFewRows;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (c4 == 0) mp[ws * kFewRows + g + 8 * h] = m[h];
-        }
+        for (int t = 0; t < kRowTiles; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
+                if (g == 0) mp[ws * kFewRows + 8 * t + 2 * c4 + e] = m[t][e];
+            }
         consumer_barrier(half);
         float* const slot = slots + ws * kFewRows * C::kSlotRow;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (g + 8 * h >= R) continue;   // rows past R hold copies; they are neither joined nor stored
-            float top = -INFINITY;
+        for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * kFewRows + g + 8 * h]);
-            // outputs carry 2^-mv (weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || mv[h] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[h] : m[h]) - top);
-            if (c4 == 0) lrow[ws * kFewRows + g + 8 * h] = l[h] * ((top == -INFINITY || m[h] == -INFINITY) ? 0.f : ptx::ex2(m[h] - top));
-            float* row = slot + (g + 8 * h) * C::kSlotRow;
-            if (!kE4M3) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * t + 2 * c4 + e;
+                if (r >= R) continue;   // rows past R hold copies; they are neither joined nor stored
+                float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-                    *reinterpret_cast<float2*>(row + 8 * j + 2 * c4) = make_float2(o[j][2 * h] * fo, o[j][2 * h + 1] * fo);
-            } else {
+                for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * kFewRows + r]);
+                // outputs carry 2^-mv (weights with their scales), sums 2^-m
+                const float fo = (top == -INFINITY || mv[t][e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - top);
+                if (g == 0) lrow[ws * kFewRows + r] = l[t][e] * ((top == -INFINITY || m[t][e] == -INFINITY) ? 0.f : ptx::ex2(m[t][e] - top));
+                float* row = slot + r * C::kSlotRow;
+                if (!kE4M3) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {   // values (2c + e) D/8 + 4k..: chunk index XOR c spreads the banks
-                        const int chunk = ((2 * c4 + e) * (D / 32) + k) ^ c4;
-                        *reinterpret_cast<float4*>(row + 4 * chunk) =
-                            make_float4(o[4 * k][2 * h + e] * fo, o[4 * k + 1][2 * h + e] * fo, o[4 * k + 2][2 * h + e] * fo,
-                                        o[4 * k + 3][2 * h + e] * fo);
+                    for (int j = 0; j < D / 16; ++j) {
+                        row[16 * j + g] = o[t][j][e] * fo;
+                        row[16 * j + g + 8] = o[t][j][2 + e] * fo;
                     }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {   // values (D / 8) g + 4k..: the chunk XOR c spreads the banks
+                        const int chunk = ((D / 32) * g + k) ^ (D == 128 ? c4 : c4 >> 1);
+                        *reinterpret_cast<float4*>(row + 4 * chunk) =
+                            make_float4(o[t][2 * k][e] * fo, o[t][2 * k][2 + e] * fo, o[t][2 * k + 1][e] * fo, o[t][2 * k + 1][2 + e] * fo);
+                    }
+                }
             }
-        }
         consumer_barrier(half);
         for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
-            const int r = i / (D / 4), q4 = i % (D / 4);
-            const int chunk = kE4M3 ? q4 ^ (q4 / (D / 16)) : q4;
+            const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
+            const int chunk = kE4M3 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -708,7 +743,7 @@ int sm_count() {
     return count[dev];
 }
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, int kRowTiles>
 int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
     using C = FewCfg<D, kE4M3>;
     static bool ready[64] = {};
@@ -716,14 +751,28 @@ int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) 
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+            cudaSuccess)
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3><<<max_items < sms ? max_items : sms, 320, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kE4M3, kRowTiles><<<max_items < sms ? max_items : sms, 320, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+// kRowTiles: 8 query rows are enough when no few-rows sequence of the call can have more (its rows are whole groups);
+// a row's bits are the same either way.
+int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
+    const int tokens = p.max_q < kFewRows / p.G ? p.max_q : kFewRows / p.G;
+    const bool two = tokens * p.G > 8;
+    if (p.c.type == DASH_CACHE_E4M3) {
+        if (p.c.D == 64) return two ? launch_few_t<64, true, 2>(p, many, max_items, s) : launch_few_t<64, true, 1>(p, many, max_items, s);
+        return two ? launch_few_t<128, true, 2>(p, many, max_items, s) : launch_few_t<128, true, 1>(p, many, max_items, s);
+    }
+    if (p.c.D == 64) return two ? launch_few_t<64, false, 2>(p, many, max_items, s) : launch_few_t<64, false, 1>(p, many, max_items, s);
+    return two ? launch_few_t<128, false, 2>(p, many, max_items, s) : launch_few_t<128, false, 1>(p, many, max_items, s);
 }
 
 // As the kernel before it in the stream ends; its plan is made while that one runs.
@@ -859,10 +908,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         }
         const bool many = (long long)max_q * prm.G > kFewRows;
         const int items = (int)(bd.few_items < 1 ? 1 : bd.few_items);   // at least one block: it checks the lengths
-        if (e4m3)
-            rc = D == 64 ? launch_few_t<64, true>(prm, many, items, s) : launch_few_t<128, true>(prm, many, items, s);
-        else
-            rc = D == 64 ? launch_few_t<64, false>(prm, many, items, s) : launch_few_t<128, false>(prm, many, items, s);
+        rc = launch_few(prm, many, items, s);
         if (rc) return rc;
         if (many && (rc = launch_paged_many(prm, sm_count(), s))) return rc;
         if (bd.rows && (rc = D == 64 ? launch_combine<64>(prm, (long long)T * Hq, s) : launch_combine<128>(prm, (long long)T * Hq, s)))
