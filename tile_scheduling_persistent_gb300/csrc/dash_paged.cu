@@ -110,25 +110,29 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// The four consumer warps of one half.
+// The four consumer warps of one group.
 __device__ __forceinline__ void consumer_barrier(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 
 // ---------------------------------------------------------------- few rows
-template <int D, bool kE4M3>
+// kRowTiles: matrix tiles of 8 query rows; kGroups: independent groups of four consumer warps and a producer.
+template <int D, bool kE4M3, int kRowTiles, int kGroups>
 struct FewCfg {
+    static constexpr int kRows = 8 * kRowTiles;
+    static constexpr int kThreads = kGroups * 160;
     static constexpr int kElem = kE4M3 ? 1 : 2;
     static constexpr int kHalfStage = kFewKeys * D * kElem;   // K, then V
     static constexpr int kStage = 2 * kHalfStage;
-    static constexpr int kStages = (65536 / kStage) < 8 ? 65536 / kStage : 8;   // of each half
+    static constexpr int kRing = kGroups == 2 ? 65536 : 51200;                     // bytes of a group's stages
+    static constexpr int kStages = (kRing / kStage) < 8 ? kRing / kStage : 8;      // of each group
     static_assert(kStages >= 2, "stage ring");
     static constexpr int kSlotRow = !kE4M3 ? D + 4 : D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
-    static constexpr int OFF_SCALE = 2 * kStages * kStage;        // [half][stage][K, V][kFewKeys] fp32
-    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? 2 * kStages * 2 * kFewKeys * 4 : 0);   // [half][warp][row]
-    static constexpr int OFF_M = OFF_SLOT + 8 * kFewRows * kSlotRow * 4;   // [half][parity][warp][row]
-    static constexpr int OFF_L = OFF_M + 2 * 8 * kFewRows * 4;             // [half][warp][row]
-    static constexpr int OFF_PLAN = OFF_L + 8 * kFewRows * 4;
+    static constexpr int OFF_SCALE = kGroups * kStages * kStage;   // [group][stage][K, V][kFewKeys] fp32
+    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? kGroups * kStages * 2 * kFewKeys * 4 : 0);   // [group][warp][row]
+    static constexpr int OFF_M = OFF_SLOT + kGroups * 4 * kRows * kSlotRow * 4;   // [group][parity][warp][row]
+    static constexpr int OFF_L = OFF_M + kGroups * 2 * 4 * kRows * 4;             // [group][warp][row]
+    static constexpr int OFF_PLAN = OFF_L + kGroups * 4 * kRows * 4;
     static constexpr int OFF_BAR = (OFF_PLAN + (int)sizeof(Plan) + 15) / 16 * 16;
-    static constexpr int OFF_ABORT = OFF_BAR + 4 * kStages * 8;   // after [half][full, empty]
+    static constexpr int OFF_ABORT = OFF_BAR + kGroups * 2 * kStages * 8;         // after [group][full, empty]
     static constexpr int kSmem = OFF_ABORT + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -171,21 +175,21 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-template <int D, bool kE4M3, int kRowTiles>
-__global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
-    using C = FewCfg<D, kE4M3>;
+template <int D, bool kE4M3, int kRowTiles, int kGroups>
+__global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
+    using C = FewCfg<D, kE4M3, kRowTiles, kGroups>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
     const uint32_t sbase = ptx::smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = warp < 8 ? warp >> 2 : warp - 8;
+    const int half = warp < 4 * kGroups ? warp >> 2 : warp - 4 * kGroups;
     const uint32_t ring = sbase + half * C::kStages * C::kStage;
     const uint32_t bar_full = sbase + C::OFF_BAR + half * 16 * C::kStages, bar_empty = bar_full + 8 * C::kStages;
 
-    if (threadIdx.x == 256) {
+    if (threadIdx.x == 128 * kGroups) {
         *abort = 0;
-        for (int s = 0; s < 2 * C::kStages; ++s) {
+        for (int s = 0; s < kGroups * C::kStages; ++s) {
             const uint32_t bar = sbase + C::OFF_BAR + (s / C::kStages) * 16 * C::kStages + 8 * (s % C::kStages);
             ptx::mbar_init(bar, 1);
             ptx::mbar_init(bar + 8 * C::kStages, 4);
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
     ItemWalk walk;
     FewItem it;
 
-    if (warp >= 8) {
+    if (warp >= 4 * kGroups) {
         // ================================================== producer
         const int page = p.c.page_size, rows = page < kFewKeys ? page : kFewKeys;
         const int subs = kFewKeys / rows;                 // copies of one kind along a stage's keys
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
         const int sub = lane / kinds, kind = lane % kinds;
         const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
         int tc = 0;                                       // stages used so far
-        for (int item = half * gridDim.x + blockIdx.x; item < items; item += 2 * gridDim.x) {
+        for (int item = half * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
             walk.at(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
             const int e0 = max(it.t0 * kFewKeys, it.c.lo) >> p.page_shift;
@@ -277,11 +281,11 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
     // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
     // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
     auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
-    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + half * 4 * kFewRows * C::kSlotRow;
-    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + half * 2 * 4 * kFewRows;
-    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + half * 4 * kFewRows;
+    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + half * 4 * C::kRows * C::kSlotRow;
+    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + half * 2 * 4 * C::kRows;
+    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + half * 4 * C::kRows;
     int tc = 0, parity = 0;
-    for (int item = half * gridDim.x + blockIdx.x; item < items; item += 2 * gridDim.x, parity ^= 1) {
+    for (int item = half * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
         const int R = it.s.n * p.G;
         // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
@@ -542,17 +546,17 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
         }
 
         // ---------------------------------------------- join the four warps
-        float* const mp = mrow + parity * 4 * kFewRows;
+        float* const mp = mrow + parity * 4 * C::kRows;
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
-                if (g == 0) mp[ws * kFewRows + 8 * t + 2 * c4 + e] = m[t][e];
+                if (g == 0) mp[ws * C::kRows + 8 * t + 2 * c4 + e] = m[t][e];
             }
         consumer_barrier(half);
-        float* const slot = slots + ws * kFewRows * C::kSlotRow;
+        float* const slot = slots + ws * C::kRows * C::kSlotRow;
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
@@ -561,10 +565,10 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
                 if (r >= R) continue;   // rows past R hold copies; they are neither joined nor stored
                 float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * kFewRows + r]);
+                for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
                 // outputs carry 2^-mv (weights with their scales), sums 2^-m
                 const float fo = (top == -INFINITY || mv[t][e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - top);
-                if (g == 0) lrow[ws * kFewRows + r] = l[t][e] * ((top == -INFINITY || m[t][e] == -INFINITY) ? 0.f : ptx::ex2(m[t][e] - top));
+                if (g == 0) lrow[ws * C::kRows + r] = l[t][e] * ((top == -INFINITY || m[t][e] == -INFINITY) ? 0.f : ptx::ex2(m[t][e] - top));
                 float* row = slot + r * C::kSlotRow;
                 if (!kE4M3) {
 #pragma unroll
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float4 v = *reinterpret_cast<const float4*>(slots + (w * kFewRows + r) * C::kSlotRow + 4 * chunk);
+                const float4 v = *reinterpret_cast<const float4*>(slots + (w * C::kRows + r) * C::kSlotRow + 4 * chunk);
                 a.x += v.x;
                 a.y += v.y;
                 a.z += v.z;
@@ -597,8 +601,8 @@ __global__ void __launch_bounds__(320, 1) paged_few_kernel(const __grid_constant
             }
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                top = fmaxf(top, mp[w * kFewRows + r]);
-                sum += lrow[w * kFewRows + r];
+                top = fmaxf(top, mp[w * C::kRows + r]);
+                sum += lrow[w * C::kRows + r];
             }
             if (it.c.ns == 1) {
                 const int tok = it.s.first + r / p.G, h = it.hk * p.G + r % p.G;
@@ -743,36 +747,38 @@ int sm_count() {
     return count[dev];
 }
 
-template <int D, bool kE4M3, int kRowTiles>
+template <int D, bool kE4M3, int kRowTiles, int kGroups>
 int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
-    using C = FewCfg<D, kE4M3>;
+    using C = FewCfg<D, kE4M3, kRowTiles, kGroups>;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kRowTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
-            cudaSuccess)
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kRowTiles, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3, kRowTiles><<<max_items < sms ? max_items : sms, 320, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kE4M3, kRowTiles, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-// kRowTiles: 8 query rows are enough when no few-rows sequence of the call can have more (its rows are whole groups);
-// a row's bits are the same either way.
+// Row tiles: 8 query rows are enough when no few-rows sequence of the call can have more (its rows are whole groups);
+// a row's bits are the same either way.  Three groups where their registers allow it.
 int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
     const int tokens = p.max_q < kFewRows / p.G ? p.max_q : kFewRows / p.G;
     const bool two = tokens * p.G > 8;
     if (p.c.type == DASH_CACHE_E4M3) {
-        if (p.c.D == 64) return two ? launch_few_t<64, true, 2>(p, many, max_items, s) : launch_few_t<64, true, 1>(p, many, max_items, s);
-        return two ? launch_few_t<128, true, 2>(p, many, max_items, s) : launch_few_t<128, true, 1>(p, many, max_items, s);
+        if (p.c.D == 64)
+            return two ? launch_few_t<64, true, 2, 2>(p, many, max_items, s) : launch_few_t<64, true, 1, 3>(p, many, max_items, s);
+        return two ? launch_few_t<128, true, 2, 2>(p, many, max_items, s) : launch_few_t<128, true, 1, 3>(p, many, max_items, s);
     }
-    if (p.c.D == 64) return two ? launch_few_t<64, false, 2>(p, many, max_items, s) : launch_few_t<64, false, 1>(p, many, max_items, s);
-    return two ? launch_few_t<128, false, 2>(p, many, max_items, s) : launch_few_t<128, false, 1>(p, many, max_items, s);
+    if (p.c.D == 64)
+        return two ? launch_few_t<64, false, 2, 2>(p, many, max_items, s) : launch_few_t<64, false, 1, 3>(p, many, max_items, s);
+    return two ? launch_few_t<128, false, 2, 2>(p, many, max_items, s) : launch_few_t<128, false, 1, 2>(p, many, max_items, s);
 }
 
 // As the kernel before it in the stream ends; its plan is made while that one runs.
