@@ -9,18 +9,26 @@
 //   P = 2^(scale log2e S - m), bf16 into the columns of S; l += row sums
 //   O += P V_j      (A = P from tensor memory)
 // A persistent CTA takes items from a counter (which CTA runs an item does not
-// touch its bits).  The two tiles take turns: while the softmax warps of one
-// work, the tensor core runs the other's products
+// touch its bits).  The two tiles take turns: while the softmax warps work on
+// one, the tensor core runs the other's products
 //   ... PV_A(j) S_A(j+1) | PV_B(j) S_B(j+1) | PV_A(j+1) ...
 // and both use each K and V tile once staged, so 256 rows share its reads.
 // S_A(j+1) follows PV_A(j) in the tensor core's order, so one S/P buffer per
 // tile suffices, and a completed S(j+1) says that O holds the sum through j:
 // rescaling O (when a row's maximum has grown by more than 2^8) needs no
-// further wait.
+// further wait.  An item with one tile of rows uses the two buffers in turn,
+// S(j+1) being issued before PV(j).
+//
+// Two warpgroups share the softmax of a tile by columns (keys 0-63 and 64-127
+// of each key tile; a thread has one row of A and the same row of B), because
+// the time from S to P is what the other tile's products have to cover: 1024
+// cycles at D = 128, where one warpgroup alone takes 1350 for 128 columns.  The
+// price is one vote of all 256 threads for each tile (does any row outgrow its
+// maximum?); the maxima themselves are exchanged only when one does.
 //
 // Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
-// tensor memory, 2 item scheduler, 3 idle, 4-7 softmax and epilogue of tile A,
-// 8-11 of tile B, and for e4m3 caches 12-15 converters.
+// tensor memory, 2 item scheduler, 3 idle, 4-7 and 8-11 softmax and epilogue,
+// and for e4m3 caches 12-15 converters.
 //
 // e4m3 caches.  The converters read codes from the pages one tile ahead and
 // store them, as TMA would a bf16 cache's tile, in fp16; the products then run
@@ -29,12 +37,12 @@
 // V holds code * scale, rounded once to fp16 (2^-11, against 2^-8 of the
 // output's bf16): a second scale for each column would cost the softmax as
 // much again as its exponentials, since its reads of shared memory wait behind
-// the tensor core's.  fp16's range is met with powers of two, undone in fp32:
+// the tensor core's (K's are read once for A and B, while S is being formed).  fp16's range is met with powers of two, undone in fp32:
 // V by the largest scale so far in the item in [2^6, 2^7) (codes reach 448; when
 // it grows, O is rescaled as for a grown maximum), Q by row, its largest value
 // in [2^14, 2^15), converted in place.
 //
-// Tensor memory: S/P of A at column 0, of B at 128; O of A at 256, of B at 384.
+// Tensor memory: S/P buffers at columns 0 and 128; O of A at 256, of B at 384.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -51,23 +59,24 @@ constexpr int kKvStages = 4;   // K0 V0 K1 V1 ...
 constexpr int kItemSlots = 2;
 
 enum TileBar : int {
-    T_Q_FULL = 0,
-    T_Q_EMPTY,
-    T_Q_READY,           // e4m3: converted
+    T_Q_FULL = 0,                          // slots A, B
+    T_Q_EMPTY = T_Q_FULL + 2,
+    T_Q_READY = T_Q_EMPTY + 2,             // e4m3: an item's queries are converted
     T_KV_FULL,
     T_KV_EMPTY = T_KV_FULL + kKvStages,
-    T_S_FULL = T_KV_EMPTY + kKvStages,   // A, B
+    T_S_FULL = T_KV_EMPTY + kKvStages,     // S/P buffers
     T_P_READY = T_S_FULL + 2,
-    T_O_FULL = T_P_READY + 4,            // [tile][half of the keys]
-    T_ITEM_FULL = T_O_FULL + 2,
+    T_O_FULL = T_P_READY + 2,              // A, B
+    T_PV_DONE = T_O_FULL + 2,              // items of one tile: every product with V
+    T_ITEM_FULL,
     T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
     T_PATCH = T_ITEM_EMPTY + kItemSlots,
-    T_SCALES,            // e4m3: the keys' scales of key tile t, slot t % 4
-    T_SCALES_END = T_SCALES + 3,
-    T_COUNT
+    T_SCALES,                              // e4m3: the keys' scales of key tile t, slot t % 4
+    T_COUNT = T_SCALES + 4
 };
 
-// One item as its roles see it.
+// One item as its roles see it; the scheduler counts the uses of every barrier before it, so that no role has to
+// follow items in which it has no part.
 struct TileItem {
     int b;              // sequence, -1: no more items
     int hk, tok;        // key/value head; first token (row of q)
@@ -75,8 +84,12 @@ struct TileItem {
     int pos;            // position of the first
     int lo, hi;         // keys that any row of the sequence sees
     int len;
-    int t0, t1;         // key tiles
-    int split;          // > 0: the sequence's keys are split
+    int t0, nk;         // key tiles t0 .. t0 + nk - 1
+    int split;          // 1: the sequence's keys are split
+    int tiles;          // 1 or 2
+    int buf, slot;      // items of one tile: first S/P buffer, Q slot
+    int kv, kt, qi;     // K and V stages, key tiles, items with keys before it
+    int s_use[2], q_use[2], o_use[2], pv;
     long long part;     // partial row of the item's first row
 };
 
@@ -86,25 +99,28 @@ struct TileCfg {
     static constexpr int kNBox = D / 64;
     static constexpr int OFF_Q = 0;                                  // A, B
     static constexpr int OFF_KV = 2 * kTile;
-    static constexpr int OFF_QFAC = OFF_KV + kKvStages * kTile;      // e4m3: [2 items][A, B][128] fp32, 2^-a of each row
+    static constexpr int OFF_MAX = OFF_KV + kKvStages * kTile;       // [column half][128 rows] fp32
+    static constexpr int OFF_SUM = OFF_MAX + 2 * 128 * 4;            // [A, B][column half][128 rows] fp32
+    static constexpr int OFF_QFAC = OFF_SUM + 4 * 128 * 4;           // e4m3: [2 items][A, B][128] fp32, 2^-a of each row
     static constexpr int OFF_KSC = OFF_QFAC + (kE4M3 ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
     static constexpr int OFF_VFAC = OFF_KSC + (kE4M3 ? 4 * 128 * 4 : 0);        // [4 tiles] the factor of V
     static constexpr int OFF_ITEM = OFF_VFAC + (kE4M3 ? 16 : 0);
-    static constexpr int OFF_BAR = OFF_ITEM + kItemSlots * 64;
+    static constexpr int kItemBytes = 128;
+    static constexpr int OFF_BAR = OFF_ITEM + kItemSlots * kItemBytes;
     static constexpr int OFF_CTL = OFF_BAR + T_COUNT * 8;            // tensor memory address, abort flag
     // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
     static constexpr int kSmem = OFF_CTL + 16 > 120000 ? OFF_CTL + 16 : 120000;
     static constexpr int kThreads = kE4M3 ? 512 : 384;
-    // registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
-    static constexpr int kRegsLaunch = kE4M3 ? 128 : 168;
-    static constexpr int kRegsCtl = kE4M3 ? 48 : 72;
-    static constexpr int kRegsConv = 128;
-    static constexpr int kRegsSoftmax = kE4M3 ? 168 : 216;
-    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
+    // e4m3: registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
+    static constexpr int kRegsLaunch = 128, kRegsCtl = 56, kRegsConv = 120, kRegsSoftmax = 168;
+    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + 128 * kRegsConv <= 512 * kRegsLaunch, "register split");
     // dec must not raise and inc must not lower what the launch granted
-    static_assert(kRegsCtl <= kRegsLaunch && kRegsConv >= 128 && kRegsSoftmax >= kRegsLaunch, "register split");
-    static_assert(sizeof(TileItem) <= 64 && kSmem <= 232448, "shared memory budget");
+    static_assert(kRegsCtl <= kRegsLaunch && kRegsConv <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch, "register split");
+    static_assert(sizeof(TileItem) <= kItemBytes && kSmem <= 232448, "shared memory budget");
 };
+
+// One of two counts (an index that is not known when compiling would put the item into local memory).
+__device__ __forceinline__ int pick(const int (&a)[2], int i) { return i ? a[1] : a[0]; }
 
 struct TileWait {
     volatile int* abort;
@@ -226,13 +242,22 @@ __device__ __forceinline__ void product_s(uint32_t leader, uint32_t d_tmem, uint
         mma_ss_if(leader, d_tmem, q_lo + off, k_lo + off, idesc, kk > 0);
     }
 }
-// O[128 x D] (+)= P[128 x 64] (tensor memory, keys 64h ..) * V rows 64h .. (MN-major)
+// O[128 x D] (+)= P[128 x 128] (tensor memory, keys 64h.. from column 64h) * V (MN-major)
 template <int D, bool kHalf>
-__device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, int h, uint32_t acc) {
+__device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t acc) {
     constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1) & ~(kHalf ? kBf16Bits : 0u);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-        mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, h + kk > 0 ? 1u : acc);
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ts_if(leader, d_tmem, p_tmem + (kk >> 2) * 64 + (kk & 3) * 8, v_lo + (uint32_t)(kk * 2048 >> 4), idesc, kk > 0 ? 1u : acc);
+}
+// A vote of the 256 softmax threads; also their barrier.
+__device__ __forceinline__ bool any_of_256(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
 }
 
 template <int D, bool kE4M3>
@@ -243,7 +268,6 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile uint32_t* const tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* const abort = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
-    const TileItem* const slots = reinterpret_cast<const TileItem*>(smem + C::OFF_ITEM);   // 64 bytes apart
     auto BAR = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
     const TileWait tw{abort, p.timeout_ns};
     const int tpt = 128 / p.G;   // tokens of a matrix tile
@@ -253,8 +277,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kE4M3 && (i == T_Q_READY || (i >= T_SCALES && i <= T_SCALES_END) || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // the converter warps
-            if (i >= T_P_READY && i < T_P_READY + 4) count = 4;
+            if (kE4M3 && (i == T_Q_READY || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
+            if (i >= T_P_READY && i < T_P_READY + 2) count = 8;                                                         // softmax warps
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
         }
@@ -276,20 +300,21 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     auto next_item = [&](TileItem& it) -> bool {   // whole warps
         const int s = iu % kItemSlots;
         if (!tile_wait_warp(BAR(T_ITEM_FULL + s), (uint32_t)((iu / kItemSlots) & 1), tw)) return false;
-        it = *reinterpret_cast<const TileItem*>(reinterpret_cast<const uint8_t*>(slots) + 64 * s);
+        it = *reinterpret_cast<const TileItem*>(smem + C::OFF_ITEM + C::kItemBytes * s);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(BAR(T_ITEM_EMPTY + s));
         ++iu;
         return it.b >= 0;
     };
+    auto parity = [](int uses) -> uint32_t { return (uint32_t)uses & 1u; };   // phase that the wait for use `uses` completes
 
-    // Each warpgroup first re-sizes its registers, then runs its role.
+    // e4m3: each warpgroup first re-sizes its registers, then runs its role.
     if (warp < 4) {
-    ptx::setmaxnreg_dec<C::kRegsCtl>();
+    if constexpr (kE4M3) ptx::setmaxnreg_dec<C::kRegsCtl>();
     if (warp == 0) {
         // ================================================== producer
         TileItem it;
-        int kv = 0, qn = 0, patches = 0;   // stages and Q loads so far
+        int patches = 0;
         bool ok = true;
         if (lane == 0) {
             ptx::prefetch_tensormap(&p.tm_q);
@@ -298,25 +323,28 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         }
         const int page = p.c.page_size, rows = page < 128 ? page : 128, subs = 128 / rows;
         while (ok && next_item(it)) {
-            if (it.t0 >= it.t1) continue;
-            const bool two = it.ntok > tpt;
-            if (qn > 0 && !tile_wait_warp(BAR(T_Q_EMPTY), (uint32_t)((qn - 1) & 1), tw)) break;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(BAR(T_Q_FULL), (two ? 2 : 1) * C::kNBox * trows * 128);
+            if (it.nk <= 0) continue;
 #pragma unroll 1
-                for (int x = 0; x < (two ? 2 : 1); ++x)
+            for (int x = 0; ok && x < it.tiles; ++x) {
+                const int slot = it.tiles == 2 ? x : it.slot;
+                const int before = pick(it.q_use, slot);
+                if (before > 0) ok = tile_wait_warp(BAR(T_Q_EMPTY + slot), parity(before - 1), tw);
+                if (!ok) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(BAR(T_Q_FULL + slot), C::kNBox * trows * 128);
                     for (int bx = 0; bx < C::kNBox; ++bx)
-                        tma_load_4d(sbase + C::OFF_Q + x * C::kTile + bx * kBox, &p.tm_q, 64 * bx, 0, it.hk, it.tok + x * tpt,
-                                    BAR(T_Q_FULL));
+                        tma_load_4d(sbase + C::OFF_Q + slot * C::kTile + bx * kBox, &p.tm_q, 64 * bx, 0, it.hk, it.tok + x * tpt,
+                                    BAR(T_Q_FULL + slot));
+                }
             }
-            ++qn;
             if (kE4M3) continue;
             const int sub = lane / C::kNBox, box = lane % C::kNBox;
-            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(it.t1 * 128, it.hi) - 1) >> p.page_shift;
-            int eb = (it.t0 * 128) >> p.page_shift;
+            const int t1 = it.t0 + it.nk;
+            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(t1 * 128, it.hi) - 1) >> p.page_shift;
+            int eb = (it.t0 * 128) >> p.page_shift, kv = it.kv;
             auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
             int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
-            for (int t = it.t0; ok && t < it.t1; ++t) {
+            for (int t = it.t0; ok && t < t1; ++t) {
                 const int key = t * 128;
                 if ((key >> p.page_shift) - eb >= 32) {
                     eb += 32;
@@ -374,65 +402,94 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         TileItem it;
         const uint32_t leader = elect_one();
         const uint32_t lo0 = sbase >> 4;
-        int st = 0, qn = 0, pu[2] = {0, 0};   // KV stage of the next K; Q loads; weights so far of A, B
-        uint32_t ph = 0;                      // its barrier's phase
         bool ok = true;
         while (ok && next_item(it)) {
-            const int nk = __shfl_sync(0xffffffffu, it.t1 - it.t0, 0);
+            // through a shuffle: the compiler then knows them to be the same in every lane
+            auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+            const int nk = uni(it.nk), tiles = uni(it.tiles), slot = uni(it.slot), kv0 = uni(it.kv);
+            const int s_use[2] = {uni(it.s_use[0]), uni(it.s_use[1])};
             if (nk <= 0) continue;
-            const int tiles = __shfl_sync(0xffffffffu, it.ntok > tpt ? 2 : 1, 0);
-            ok = tile_wait_warp(BAR(kE4M3 ? T_Q_READY : T_Q_FULL), (uint32_t)(qn & 1), tw) && tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
-            if (!ok) break;
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (x < tiles) {
-                    product_s<D, kE4M3>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
-                                 lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
-                    commit_if(leader, BAR(T_S_FULL + x));
-                }
-            commit_if(leader, BAR(T_KV_EMPTY + st));
-            if (nk == 1) commit_if(leader, BAR(T_Q_EMPTY));
-            for (int j = 0; ok && j < nk; ++j) {
-                const int sv = st + 1;                  // stages of V_j and K_{j+1}: K and V alternate
-                st = (st + 2) % kKvStages;
-                const uint32_t pv = ph;
-                ph ^= st == 0 ? 1u : 0u;
-                const bool more = j + 1 < nk;
-                ok = tile_wait_warp(BAR(T_KV_FULL + sv), pv, tw);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x >= tiles || !ok) continue;
-                    // O (+)= P V_j, in two halves of the keys as the weights become ready
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && tile_wait_warp(BAR(T_P_READY + 2 * x + h), (uint32_t)(pu[x] & 1), tw);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        product_pv<D, kE4M3>(leader, tmem + 256 + 128 * x, tmem + 128 * x, lo0 + kDescMn + ((C::OFF_KV + sv * C::kTile) >> 4),
-                                      h, j > 0 ? 1u : 0u);
-                    }
-                    if (!ok) continue;
-                    ++pu[x];
-                    const bool last = x == tiles - 1;
-                    if (last) commit_if(leader, BAR(T_KV_EMPTY + sv));
-                    if (more) {
-                        if (x == 0) ok = tile_wait_warp(BAR(T_KV_FULL + st), ph, tw);
-                        if (!ok) continue;
-                        ptx::tc_fence_after();
-                        product_s<D, kE4M3>(leader, tmem + 128 * x, lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4),
-                                     lo0 + kDescK + ((C::OFF_KV + st * C::kTile) >> 4));
-                        commit_if(leader, BAR(T_S_FULL + x));
-                        if (last) {
-                            commit_if(leader, BAR(T_KV_EMPTY + st));
-                            if (j + 2 == nk) commit_if(leader, BAR(T_Q_EMPTY));
-                        }
-                    } else {
-                        commit_if(leader, BAR(T_O_FULL + x));
-                    }
+            auto full = [&](int u) { return tile_wait_warp(BAR(T_KV_FULL + u % kKvStages), parity(u / kKvStages), tw); };
+            auto stage = [&](int u) { return lo0 + ((C::OFF_KV + (u % kKvStages) * C::kTile) >> 4); };
+            auto q_lo = [&](int x) { return lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4); };
+            auto empty = [&](int u) { commit_if(leader, BAR(T_KV_EMPTY + u % kKvStages)); };
+            auto scores = [&](int buf, int q, int u) {
+                product_s<D, kE4M3>(leader, tmem + 128 * buf, q_lo(q), stage(u) + kDescK);
+                commit_if(leader, BAR(T_S_FULL + buf));
+            };
+            auto values = [&](int buf, int x, int u, int j) {   // O (+)= P V_j
+                product_pv<D, kE4M3>(leader, tmem + 256 + 128 * x, tmem + 128 * buf, stage(u) + kDescMn, j > 0 ? 1u : 0u);
+            };
+            if (kE4M3) {
+                ok = tile_wait_warp(BAR(T_Q_READY), parity(it.qi), tw);
+            } else {
+                for (int x = 0; ok && x < tiles; ++x) {
+                    const int q = tiles == 2 ? x : slot;
+                    ok = tile_wait_warp(BAR(T_Q_FULL + q), parity(pick(it.q_use, q)), tw);
                 }
             }
-            ++qn;
+            ok = ok && full(kv0);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (tiles == 2) {
+                scores(0, 0, kv0);
+                scores(1, 1, kv0);
+                empty(kv0);
+                for (int j = 0; j < nk; ++j) {
+                    const int uv = kv0 + 2 * j + 1, uk = uv + 1;
+                    const bool more = j + 1 < nk;
+                    if (!more) {   // after the last S
+                        commit_if(leader, BAR(T_Q_EMPTY + 0));
+                        commit_if(leader, BAR(T_Q_EMPTY + 1));
+                    }
+                    ok = full(uv) && tile_wait_warp(BAR(T_P_READY + 0), parity(s_use[0] + j), tw);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    values(0, 0, uv, j);
+                    if (more) {
+                        ok = full(uk);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        scores(0, 0, uk);
+                    } else {
+                        commit_if(leader, BAR(T_O_FULL + 0));
+                    }
+                    ok = tile_wait_warp(BAR(T_P_READY + 1), parity(s_use[1] + j), tw);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    values(1, 1, uv, j);
+                    empty(uv);
+                    if (more) {
+                        scores(1, 1, uk);
+                        empty(uk);
+                    } else {
+                        commit_if(leader, BAR(T_O_FULL + 1));
+                    }
+                }
+            } else {
+                int buf = uni(it.buf);
+                scores(buf, slot, kv0);
+                empty(kv0);
+                for (int j = 0; j < nk; ++j, buf ^= 1) {
+                    const int uv = kv0 + 2 * j + 1, uk = uv + 1;
+                    if (j + 1 < nk) {
+                        ok = full(uk);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        scores(buf ^ 1, slot, uk);
+                        empty(uk);
+                    } else {
+                        commit_if(leader, BAR(T_Q_EMPTY + slot));
+                    }
+                    ok = full(uv) && tile_wait_warp(BAR(T_P_READY + buf), parity(pick(s_use, buf) + (j >> 1)), tw);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    values(buf, 0, uv, j);
+                    empty(uv);
+                    commit_if(leader, BAR(T_PV_DONE));
+                    if (j + 1 == nk) commit_if(leader, BAR(T_O_FULL + 0));
+                }
+            }
         }
         // after a wait that ran out, the products in flight end before tensor memory is freed (below, after the barrier);
         // otherwise every product has been waited for
@@ -445,6 +502,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         // ================================================== scheduler
         const Plan* plan = p.plan;
         const int items = plan->items[p.nb];
+        int buf = 0, slot = 0, kv = 0, kt = 0, qi = 0, pv = 0, s_use[2] = {0, 0}, q_use[2] = {0, 0}, o_use[2] = {0, 0};
         for (int u = 0;; ++u) {
             int item = 0;
             if (lane == 0) item = atomicAdd(p.counter, 1);
@@ -483,10 +541,42 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 seen_keys(p, q, i0, i0 + it.ntok, klo, khi);
                 const int first = c.lo / 128 + split * c.st;
                 it.t0 = max(first, klo / 128);
-                it.t1 = min(first + c.st, khi > klo ? (khi + 127) / 128 : 0);
+                it.nk = max(min(first + c.st, khi > klo ? (khi + 127) / 128 : 0) - it.t0, 0);
+                it.tiles = it.ntok > tpt ? 2 : 1;
+                it.buf = buf;
+                it.slot = slot;
+                it.kv = kv;
+                it.kt = kt;
+                it.qi = qi;
+                it.pv = pv;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    it.s_use[x] = s_use[x];
+                    it.q_use[x] = q_use[x];
+                    it.o_use[x] = o_use[x];
+                }
+                if (it.nk > 0) {
+                    kv += 2 * it.nk;
+                    kt += it.nk;
+                    ++qi;
+                    if (it.tiles == 2) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) s_use[x] += it.nk, ++q_use[x], ++o_use[x];
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            s_use[x] += (it.nk + (x == buf ? 1 : 0)) / 2;
+                            q_use[x] += x == slot ? 1 : 0;
+                        }
+                        ++o_use[0];
+                        pv += it.nk;
+                        buf ^= it.nk & 1;
+                        slot ^= 1;
+                    }
+                }
             }
             if (lane == 0) {
-                *reinterpret_cast<TileItem*>(smem + C::OFF_ITEM + 64 * s) = it;
+                *reinterpret_cast<TileItem*>(smem + C::OFF_ITEM + C::kItemBytes * s) = it;
                 ptx::mbar_arrive(BAR(T_ITEM_FULL + s));
             }
             __syncwarp();
@@ -494,243 +584,201 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         }
     }
     } else if (warp < 12) {
-        ptx::setmaxnreg_inc<C::kRegsSoftmax>();
-        // ================================================== softmax and epilogue, one row per thread
-        const int x_ = (warp - 4) >> 2;   // tile A or B
+        if constexpr (kE4M3) ptx::setmaxnreg_inc<C::kRegsSoftmax>();
+        // ================================================== softmax and epilogue
+        // A thread has one row of each tile; its warpgroup keys 64 w .. of every key tile, and columns D/2 w .. of O.
+        const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
-        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lane_off + 128u * (uint32_t)x_, tO = tmem + lane_off + 256u + 128u * (uint32_t)x_;
-        float c = p.scale_log2e;
+        const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float* const mx_own = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * w + row;
+        float* const mx_other = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * (w ^ 1) + row;
         TileItem it;
-        int su = 0, ou = 0, kt = 0, qn = 0;   // S and O phases, key tiles and Q loads of all items
-        bool ok = true;
-        while (ok && next_item(it)) {
-            const int nk = it.t1 - it.t0;
-            const int i = x_ * tpt + row / p.G;           // token of the item
-            const bool mine = x_ == 0 || it.ntok > tpt;   // the tile exists
-            const bool valid = mine && row < trows && i < it.ntok;
-            if (!mine) {
-                kt += nk > 0 ? nk : 0;
-                qn += nk > 0 ? 1 : 0;
-                continue;
+        for (;;) {
+            const bool more = next_item(it);
+            // all eight warps take an item, or none: nobody is left alone at the votes below (after a wait that ran out,
+            // the others just do not wait)
+            if (any_of_256(!more)) break;
+            const int nk = it.nk;
+            // this row's keys, and the key tiles that every row of its tile sees whole
+            int lo_r[2], hi_r[2], full_lo[2], full_hi[2];
+            bool valid[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = x * tpt + row / p.G, pos = it.pos + i;
+                valid[x] = row < trows && i < it.ntok;
+                hi_r[x] = p.causal ? pos + 1 : it.len;
+                lo_r[x] = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
+                const int pos0 = it.pos + x * tpt, pos1 = min(it.pos + it.ntok - 1, pos0 + tpt - 1);
+                full_hi[x] = p.causal ? pos0 + 1 : it.len;
+                full_lo[x] = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
             }
-            // this row's keys, and the key tiles that every row of the tile sees whole
-            const int pos = it.pos + i;
-            const int hi_r = p.causal ? pos + 1 : it.len, lo_r = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
-            const int pos0 = it.pos + x_ * tpt, pos1 = min(it.pos + it.ntok - 1, pos0 + tpt - 1);
-            const int full_hi = p.causal ? pos0 + 1 : it.len, full_lo = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
-            float m_ref = -INFINITY, l = 0.f, vfac = 1.f;   // O holds the sum over vfac
-            for (int j = 0; j < nk; ++j, ++su) {
-                // e4m3: the keys' scales.  A read of shared memory takes some 400 cycles while the tensor core streams its
-                // operands, so they are read two blocks of 32 columns ahead (volatile reads stay in place): columns 64..
-                // before the scores are there, and the blocks 0 and 1 serve the maximum last and the weights first.
-                uint4 s4[2][8];   // block h in s4[h & 1]
-                float vnow = 1.f;
-                const uint32_t scales = sbase + C::OFF_KSC + ((kt + j) & 3) * 512;
+            float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, c[2] = {p.scale_log2e, p.scale_log2e};
+            float vfac = 1.f;   // O holds the sum over vfac
+            for (int j = 0; j < nk; ++j) {
+                const int key = (it.t0 + j) * 128 + 64 * w;   // the first of this warpgroup's keys
+                uint4 s4[kE4M3 ? 16 : 1];                      // e4m3: their scales
+                float grown = 1.f;                             // of O, when the values' power of two has grown
                 if constexpr (kE4M3) {
-                    if (!tile_wait_warp(BAR(T_SCALES + ((kt + j) & 3)), (uint32_t)(((kt + j) >> 2) & 1), tw)) {
-                        ok = false;
-                        break;
-                    }
+                    const int t = it.kt + j;
+                    tile_wait_warp(BAR(T_SCALES + (t & 3)), parity(t >> 2), tw);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) s4[k >> 3][k & 7] = lds128(scales + 16 * (16 + k));
-                    vnow = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[(kt + j) & 3];
-                    if (j == 0) c = p.scale_log2e;
+                    for (int k = 0; k < 16; ++k) s4[k] = lds128(sbase + C::OFF_KSC + (t & 3) * 512 + 256 * w + 16 * k);
+                    const float f = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[t & 3];
+                    if (j == 0) vfac = f;
+                    if (f != vfac) grown = vfac / f;
+                    vfac = f;
                 }
-                if (!tile_wait_warp(BAR(T_S_FULL + x_), (uint32_t)(su & 1), tw)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                // Scores of 32 columns at a time.  bf16 caches: all 128 stay in registers.  e4m3 caches, whose converters and
-                // scales take their share of the registers: read (and scaled) once for the maximum and again for the weights
-                // (spilled registers would wait as reads of shared memory do).
-                constexpr int kKeep = kE4M3 ? 1 : 4;
-                const int key = (it.t0 + j) * 128;
-                const bool edge = key < full_lo || key + 128 > full_hi;
-                const int ka = lo_r - key, kb = hi_r - key;   // visible columns [ka, kb)
-                auto finish = [&](int h, const uint32_t (&r)[32], float (&x)[32], const uint4 (&sc)[8]) {
-                    if (kE4M3) {   // times the keys' scales
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const uint4 f = sc[k / 4];
-                            const ptx::f2 u = ptx::mul2({__uint_as_float(r[k]), __uint_as_float(r[k + 1])}, {__uint_as_float(f.x), __uint_as_float(f.y)});
-                            const ptx::f2 v = ptx::mul2({__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])}, {__uint_as_float(f.z), __uint_as_float(f.w)});
-                            x[k] = u.x, x[k + 1] = u.y, x[k + 2] = v.x, x[k + 3] = v.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]);
-                    }
-                    if (kE4M3 && edge) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * h + k < ka || 32 * h + k >= kb) x[k] = -INFINITY;
-                    }
-                };
-                float x[kKeep][32];
-                float part[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) part[k] = -INFINITY;
-                // row maximum (and, below, sum) over interleaved partials: short chains, one fixed order
-                auto top4 = [&](const float (&x)[32]) {
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], x[k]), x[k + 1]);
-                };
-                if constexpr (kE4M3) {
-#pragma unroll
-                    for (int h = 3; h >= 0; --h) {
-                        uint32_t r[32];
-                        float y[32];
-                        ptx::tmem_ld32(tS + 32 * h, r);
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= it.tiles) continue;
+                    const int buf = it.tiles == 2 ? x : (it.buf + j) & 1;
+                    const uint32_t tS = tbase + 128u * (uint32_t)buf + 64u * (uint32_t)w;
+                    tile_wait_warp(BAR(T_S_FULL + buf), parity(pick(it.s_use, buf) + (it.tiles == 2 ? j : j >> 1)), tw);
+                    ptx::tc_fence_after();
+                    float y[64];
+                    {
+                        uint32_t r[2][32];
+                        ptx::tmem_ld32(tS, r[0]);
+                        ptx::tmem_ld32(tS + 32, r[1]);
                         ptx::tmem_ld_wait();
-                        finish(h, r, y, s4[h & 1]);
-                        top4(y);
-                        if (h >= 2) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) s4[h & 1][k] = lds128(scales + 16 * (8 * (h - 2) + k));
-                        }
+                        for (int k = 0; k < 64; ++k) y[k] = __uint_as_float(r[k >> 5][k & 31]);
                     }
-                } else {
-                    uint32_t r[4][32];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) finish(h, r[h], x[h & (kKeep - 1)], s4[0]);
-                    if (edge) {
-#pragma unroll
-                        for (int k = 0; k < 128; ++k)
-                            if (k < ka || k >= kb) x[(k >> 5) & (kKeep - 1)][k & 31] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) top4(x[h & (kKeep - 1)]);
-                }
-                float grown = 1.f;   // of O, when the values' power of two has grown
-                if (kE4M3) {
-                    if (j == 0) {
-                        c *= reinterpret_cast<const float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x_) * 128 + row];
-                        vfac = vnow;
-                    }
-                    if (vnow != vfac) grown = vfac / vnow;
-                    vfac = vnow;
-                }
-                const float mx = c * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                const bool raise = __any_sync(0xffffffffu, (valid && mx > m_ref + 8.f) || (kE4M3 && grown != 1.f));
-                if (raise) {
-                    const float m_new = fmaxf(m_ref, mx);
-                    const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref - m_new);
-                    m_ref = m_new;
-                    l *= alpha;
-                    const float alpha_o = kE4M3 ? alpha * grown : alpha;
-                    if (j > 0) {
-#pragma unroll 1
-                        for (int cc = 0; cc < D / 16; ++cc) {
-                            uint32_t r[16];
-                            ptx::tmem_ld16(tO + 16 * cc, r);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_o);
-                            ptx::tmem_st16(tO + 16 * cc, r);
-                        }
-                    }
-                }
-                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) part[k] = 0.f;
-                // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys [0,64) -> columns [0,32), [64,128) -> [64,96); the
-                // products with the first 64 keys start while the rest is worked out
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float y[32];
                     if constexpr (kE4M3) {
-                        uint32_t r[32];
-                        ptx::tmem_ld32(tS + 32 * h, r);
-                        ptx::tmem_ld_wait();
-                        finish(h, r, y, s4[h & 1]);
-                        if (h < 2) {
+                        if (j == 0)
+                            c[x] *= reinterpret_cast<const float*>(
+                                smem + C::OFF_QFAC)[((it.qi & 1) * 2 + (it.tiles == 2 ? x : it.slot)) * 128 + row];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) s4[h & 1][k] = lds128(scales + 16 * (8 * (h + 2) + k));
+                        for (int k = 0; k < 16; ++k) {
+                            const ptx::f2 u = ptx::mul2({y[4 * k], y[4 * k + 1]}, {__uint_as_float(s4[k].x), __uint_as_float(s4[k].y)});
+                            const ptx::f2 v = ptx::mul2({y[4 * k + 2], y[4 * k + 3]}, {__uint_as_float(s4[k].z), __uint_as_float(s4[k].w)});
+                            y[4 * k] = u.x, y[4 * k + 1] = u.y, y[4 * k + 2] = v.x, y[4 * k + 3] = v.y;
                         }
                     }
-                    uint32_t pk[16];
+                    if (key < full_lo[x] || key + 64 > full_hi[x]) {
+                        const int ka = lo_r[x] - key, kb = hi_r[x] - key;   // visible columns [ka, kb)
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const float s0 = kE4M3 ? y[k] : x[h & (kKeep - 1)][k], s1 = kE4M3 ? y[k + 1] : x[h & (kKeep - 1)][k + 1];
-                        const ptx::f2 e = ptx::fma2({s0, s1}, {c, c}, {-m_use, -m_use});
-                        const ptx::f2 w{ptx::ex2(e.x), ptx::ex2(e.y)};
-                        const ptx::f2 s = ptx::add2({part[k & 7], part[(k + 1) & 7]}, w);
-                        part[k & 7] = s.x;
-                        part[(k + 1) & 7] = s.y;
-                        pk[k >> 1] = kE4M3 ? pack_half(w.x, w.y) : pack_bf16(w.x, w.y);
+                        for (int k = 0; k < 64; ++k)
+                            if (k < ka || k >= kb) y[k] = -INFINITY;
                     }
-                    ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
-                    if (h & 1) {
-                        ptx::tmem_st_wait();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + 2 * x_ + (h >> 1)));
+                    // row maximum and sum over interleaved partials: short chains, one fixed order
+                    float part[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) part[k] = fmaxf(y[2 * k], y[2 * k + 1]);
+#pragma unroll
+                    for (int k = 8; k < 64; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
+                    float mx = c[x] * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                    if (any_of_256((valid[x] && mx > m_ref[x] + 8.f) || (kE4M3 && grown != 1.f))) {
+                        *mx_own = mx;
+                        any_of_256(false);
+                        mx = fmaxf(mx, *mx_other);
+                        const float m_new = fmaxf(m_ref[x], mx);
+                        const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref[x] - m_new);
+                        m_ref[x] = m_new;
+                        l[x] *= alpha;
+                        const float alpha_o = kE4M3 ? alpha * grown : alpha;
+                        if (j > 0) {
+                            // (one tile: S(j) was issued before PV(j-1))
+                            if (it.tiles == 1) tile_wait_warp(BAR(T_PV_DONE), parity(it.pv + j - 1), tw);
+                            ptx::tc_fence_after();
+#pragma unroll 1
+                            for (int cc = 0; cc < D / 32; ++cc) {
+                                const uint32_t tO = tbase + 256u + 128u * (uint32_t)x + (uint32_t)(D / 2 * w + 16 * cc);
+                                uint32_t r[16];
+                                ptx::tmem_ld16(tO, r);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha_o);
+                                ptx::tmem_st16(tO, r);
+                            }
+                        }
                     }
+                    const float m_use = m_ref[x] == -INFINITY ? 0.f : m_ref[x];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys 64 w .. at columns 64 w .. + 31
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const ptx::f2 e = ptx::fma2({y[32 * h + k], y[32 * h + k + 1]}, {c[x], c[x]}, {-m_use, -m_use});
+                            const ptx::f2 v{ptx::ex2(e.x), ptx::ex2(e.y)};
+                            const ptx::f2 s = ptx::add2({sum[k & 3], sum[(k + 1) & 3]}, v);
+                            sum[k & 3] = s.x;
+                            sum[(k + 1) & 3] = s.y;
+                            pk[k >> 1] = kE4M3 ? pack_half(v.x, v.y) : pack_bf16(v.x, v.y);
+                        }
+                        ptx::tmem_st16(tS + 16 * h, pk);
+                    }
+                    l[x] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + buf));
                 }
-                l += ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
             }
-            if (!ok) break;
-            kt += nk > 0 ? nk : 0;
-            qn += nk > 0 ? 1 : 0;
-            if (nk > 0) {
-                if (!tile_wait_warp(BAR(T_O_FULL + x_), (uint32_t)(ou & 1), tw)) break;
-                ++ou;
-                ptx::tc_fence_after();
-            }
-            const int g = row % p.G;
-            const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
-            const long long pr = it.part + (long long)i * p.G + g;
-            const float inv = vfac * ((it.split || !(l > 0.f)) ? 1.f : 1.f / l);
-            const bool empty = !(l > 0.f);
-            const bool keep = it.split && valid && pr < p.max_rows;
+            // the rows' sums over both halves of the columns, in one order
+            float* const sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+            for (int x = 0; x < 2; ++x) sums[(2 * x + w) * 128 + row] = l[x];
+            any_of_256(false);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t r[32];
+            for (int x = 0; x < 2; ++x) {
+                if (x >= it.tiles) continue;
                 if (nk > 0) {
-                    ptx::tmem_ld32(tO + 32 * cc, r);
-                    ptx::tmem_ld_wait();
+                    tile_wait_warp(BAR(T_O_FULL + x), parity(it.o_use[x]), tw);
+                    ptx::tc_fence_after();
                 }
+                const float total = sums[2 * x * 128 + row] + sums[(2 * x + 1) * 128 + row];
+                const int i = x * tpt + row / p.G, g = row % p.G;
+                const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
+                const long long pr = it.part + (long long)i * p.G + g;
+                const bool empty = !(total > 0.f);
+                const float inv = vfac * (it.split || empty ? 1.f : 1.f / total);
+                const bool keep = it.split && valid[x] && pr < p.max_rows;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) r[k] = (nk <= 0 || empty) ? 0u : __float_as_uint(__uint_as_float(r[k]) * inv);
-                if (keep) {
+                for (int cc = 0; cc < D / 64; ++cc) {
+                    const int col = D / 2 * w + 32 * cc;
+                    uint32_t r[32];
+                    if (nk > 0) {
+                        ptx::tmem_ld32(tbase + 256u + 128u * (uint32_t)x + (uint32_t)col, r);
+                        ptx::tmem_ld_wait();
+                    }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4*>(p.part_o + pr * D + 32 * cc + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
-                } else if (!it.split && valid) {
+                    for (int k = 0; k < 32; ++k) r[k] = (nk <= 0 || empty) ? 0u : __float_as_uint(__uint_as_float(r[k]) * inv);
+                    if (keep) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4*>(p.o + at * D + 32 * cc + k) =
-                            make_uint4(pack_bf16(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
-                                       pack_bf16(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])),
-                                       pack_bf16(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5])),
-                                       pack_bf16(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7])));
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(p.part_o + pr * D + col + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                    } else if (!it.split && valid[x]) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8)
+                            *reinterpret_cast<uint4*>(p.o + at * D + col + k) =
+                                make_uint4(pack_bf16(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
+                                           pack_bf16(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])),
+                                           pack_bf16(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5])),
+                                           pack_bf16(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7])));
+                    }
                 }
+                if (w == 0 && keep)
+                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[x], empty ? 0.f : total);
+                else if (w == 0 && !it.split && valid[x] && p.lse)
+                    p.lse[at] = empty ? -INFINITY : (m_ref[x] + log2f(total)) * kLn2P;
             }
-            if (keep)
-                p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref, empty ? 0.f : l);
-            else if (!it.split && valid && p.lse)
-                p.lse[at] = empty ? -INFINITY : (m_ref + log2f(l)) * kLn2P;
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
         }
     } else if (kE4M3) {
-        ptx::setmaxnreg_inc<C::kRegsConv>();
+        ptx::setmaxnreg_dec<C::kRegsConv>();
         // ================================================== converters
         constexpr int kChunks = D / 16;         // 16-byte chunks of codes per key
         constexpr int kRows = 32 / kChunks;     // keys that one load instruction of a warp covers
         constexpr int kLoads = 32 / kRows;      // loads of a warp's 32 keys of a tile
         const int cw = warp - 12, chunk = lane % kChunks, sub = lane / kChunks;
         TileItem it;
-        int kv = 0, kt = 0, qn = 0;
         bool ok = true;
         while (ok && next_item(it)) {
-            const int nk = it.t1 - it.t0;
+            const int nk = it.nk;
             if (nk <= 0) continue;
-            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(it.t1 * 128, it.hi) - 1) >> p.page_shift;
+            const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min((it.t0 + nk) * 128, it.hi) - 1) >> p.page_shift;
             int eb = (it.t0 * 128) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
             auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
             int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
@@ -781,16 +829,14 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             // One unit: the codes `w` (loaded during the unit before it) into a stage; `next` (loaded first, so that the proxy
             // fence at the end, which waits for every access before it, finds them there) are the following unit's.
             auto unit = [&](int u, const uint4 (&w)[kLoads], uint4 (&next)[kLoads]) -> bool {
-                const int st = kv % kKvStages;
-                if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), (uint32_t)((kv / kKvStages - 1) & 1), tw)) {
-                    return false;
-                }
+                const int kv = it.kv + u, st = kv % kKvStages;
+                if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), parity(kv / kKvStages - 1), tw)) return false;
                 const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
                 float vup, vback;
                 power_to(vtop, 6, vup, vback);
                 const float scale = vs * vup;
                 if (!(u & 1)) {
-                    const int slot = (kt + (u >> 1)) & 3;
+                    const int slot = (it.kt + (u >> 1)) & 3;
                     reinterpret_cast<float*>(smem + C::OFF_KSC)[slot * 128 + 32 * cw + lane] = ks;
                     if (cw == 0 && lane == 0) reinterpret_cast<float*>(smem + C::OFF_VFAC)[slot] = vback;
                 }
@@ -839,16 +885,16 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 __syncwarp();
                 if (lane == 0) {
                     ptx::mbar_arrive(BAR(T_KV_FULL + st));
-                    if (!(u & 1)) ptx::mbar_arrive(BAR(T_SCALES + ((kt + (u >> 1)) & 3)));
+                    if (!(u & 1)) ptx::mbar_arrive(BAR(T_SCALES + ((it.kt + (u >> 1)) & 3)));
                 }
-                ++kv;
                 if (u != 1) return true;
                 // With the first tile staged: the item's queries, one row per thread (of A, then of B)
-                if (!tile_wait_warp(BAR(T_Q_FULL), (uint32_t)(qn & 1), tw)) return false;
 #pragma unroll 1
-                for (int x = 0; x < (it.ntok > tpt ? 2 : 1); ++x) {
+                for (int x = 0; x < it.tiles; ++x) {
+                    const int q = it.tiles == 2 ? x : it.slot;
+                    if (!tile_wait_warp(BAR(T_Q_FULL + q), parity(pick(it.q_use, q)), tw)) return false;
                     const int row = 32 * cw + lane;
-                    const uint32_t line = sbase + C::OFF_Q + x * C::kTile + row * 128;
+                    const uint32_t line = sbase + C::OFF_Q + q * C::kTile + row * 128;
                     float top = 0.f;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
@@ -859,7 +905,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     }
                     float up, down;
                     power_to(top, 14, up, down);
-                    reinterpret_cast<float*>(smem + C::OFF_QFAC)[((qn & 1) * 2 + x) * 128 + row] = down;
+                    reinterpret_cast<float*>(smem + C::OFF_QFAC)[((it.qi & 1) * 2 + q) * 128 + row] = down;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         const uint32_t at = line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4);
@@ -872,7 +918,6 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY));
-                ++qn;
                 return true;
             };
             uint4 wk[kLoads], wv[kLoads];
@@ -883,7 +928,6 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             use_scales();
 #pragma unroll 1
             for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
-            kt += nk;
         }
     }
 
