@@ -37,6 +37,11 @@ CASES = {
     "chunk_long": (4, 1, 128, 32, [5000], [70], None, 0),
     "mixed": (16, 4, 64, 16, [1300, 1, 500, 64, 0], [1, 1, 260, 0, 1], None, 4),
     "mixed_window": (8, 8, 128, 32, [900, 800, 33], [1, 140, 33], 300, 0),
+    # several items for every SM, and mixtures of one and two row tiles
+    "decode_many": (16, 8, 64, 16, [37 * i % 900 + 1 for i in range(70)], [1] * 70, None, 0),
+    "verify_many": (32, 8, 128, 32, [301 * i % 1900 + 6 for i in range(40)], [5] * 40, None, 0),
+    "verify_many_window": (32, 8, 64, 16, [301 * i % 1900 + 6 for i in range(40)], [6] * 40, 500, 0),
+    "chunk_many": (8, 8, 128, 64, [211 * i % 700 + 300 for i in range(30)], [17 * i % 300 + 17 for i in range(30)], None, 3),
     "group_128": (128, 1, 64, 16, [90, 300], [1, 3], None, 0),
 }
 

@@ -19,12 +19,14 @@
 // further wait.  An item with one tile of rows uses the two buffers in turn,
 // S(j+1) being issued before PV(j).
 //
-// Two warpgroups share the softmax of a tile by columns (keys 0-63 and 64-127
-// of each key tile; a thread has one row of A and the same row of B), because
-// the time from S to P is what the other tile's products have to cover: 1024
-// cycles at D = 128, where one warpgroup alone takes 1350 for 128 columns.  The
-// price is one vote of all 256 threads for each tile (does any row outgrow its
-// maximum?); the maxima themselves are exchanged only when one does.
+// bf16 caches: a warpgroup each for A and B, one row per thread (items of one
+// tile go to the two in turn, so that one's epilogue overlaps the other's
+// loop); the first half of P's keys is multiplied while the second is worked
+// out.  e4m3 caches: scaling the scores comes on top, so the two share every
+// tile by columns (keys 0-63 and 64-127; a thread has one row of A and the
+// same row of B), which reads the scales once for both.  The price is one vote
+// of the 256 threads for each tile (does any row outgrow its maximum?); the
+// maxima themselves are exchanged only when one does.
 //
 // Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
 // tensor memory, 2 item scheduler, 3 idle, 4-7 and 8-11 softmax and epilogue,
@@ -64,9 +66,11 @@ enum TileBar : int {
     T_Q_READY = T_Q_EMPTY + 2,             // e4m3: an item's queries are converted
     T_KV_FULL,
     T_KV_EMPTY = T_KV_FULL + kKvStages,
-    T_S_FULL = T_KV_EMPTY + kKvStages,     // S/P buffers
-    T_P_READY = T_S_FULL + 2,
-    T_O_FULL = T_P_READY + 2,              // A, B
+    // [row tile or slot][buffer]: whoever waits for one of these sees every phase of it (parity cannot tell a phase from the
+    // one after the next, and a warpgroup does not follow the items of the other)
+    T_S_FULL = T_KV_EMPTY + kKvStages,
+    T_P_READY = T_S_FULL + 4,              // [buffer][half of the keys]
+    T_O_FULL = T_P_READY + 4,              // A, B
     T_PV_DONE = T_O_FULL + 2,              // items of one tile: every product with V
     T_ITEM_FULL,
     T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
@@ -87,9 +91,9 @@ struct TileItem {
     int t0, nk;         // key tiles t0 .. t0 + nk - 1
     int split;          // 1: the sequence's keys are split
     int tiles;          // 1 or 2
-    int buf, slot;      // items of one tile: first S/P buffer, Q slot
+    int buf, slot;      // items of one tile: first S/P buffer; Q slot, O and (bf16) softmax warpgroup
     int kv, kt, qi;     // K and V stages, key tiles, items with keys before it
-    int s_use[2], q_use[2], o_use[2], pv;
+    int s_use[2], p_use[2], q_use[2], o_use[2], pv;   // [buffer] for S and P, [slot] for Q and O
     long long part;     // partial row of the item's first row
 };
 
@@ -111,11 +115,12 @@ struct TileCfg {
     // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
     static constexpr int kSmem = OFF_CTL + 16 > 120000 ? OFF_CTL + 16 : 120000;
     static constexpr int kThreads = kE4M3 ? 512 : 384;
-    // e4m3: registers of the three kinds of warpgroups (setmaxnreg), within what the launch grants
-    static constexpr int kRegsLaunch = 128, kRegsCtl = 56, kRegsConv = 120, kRegsSoftmax = 168;
-    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + 128 * kRegsConv <= 512 * kRegsLaunch, "register split");
+    // registers of the kinds of warpgroups (setmaxnreg), within what the launch grants
+    static constexpr int kRegsLaunch = kE4M3 ? 128 : 168, kRegsCtl = kE4M3 ? 56 : 72, kRegsConv = 120;
+    static constexpr int kRegsSoftmax = kE4M3 ? 168 : 216;
+    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
     // dec must not raise and inc must not lower what the launch granted
-    static_assert(kRegsCtl <= kRegsLaunch && kRegsConv <= kRegsLaunch && kRegsSoftmax >= kRegsLaunch, "register split");
+    static_assert(kRegsCtl <= kRegsLaunch && (!kE4M3 || kRegsConv <= kRegsLaunch) && kRegsSoftmax >= kRegsLaunch, "register split");
     static_assert(sizeof(TileItem) <= kItemBytes && kSmem <= 232448, "shared memory budget");
 };
 
@@ -242,13 +247,13 @@ __device__ __forceinline__ void product_s(uint32_t leader, uint32_t d_tmem, uint
         mma_ss_if(leader, d_tmem, q_lo + off, k_lo + off, idesc, kk > 0);
     }
 }
-// O[128 x D] (+)= P[128 x 128] (tensor memory, keys 64h.. from column 64h) * V (MN-major)
+// O[128 x D] (+)= P[128 x 64] (tensor memory, keys 64h ..) * V rows 64h .. (MN-major)
 template <int D, bool kHalf>
-__device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t acc) {
+__device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_lo, int h, uint32_t acc) {
     constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1) & ~(kHalf ? kBf16Bits : 0u);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_ts_if(leader, d_tmem, p_tmem + (kk >> 2) * 64 + (kk & 3) * 8, v_lo + (uint32_t)(kk * 2048 >> 4), idesc, kk > 0 ? 1u : acc);
+    for (int kk = 0; kk < 4; ++kk)
+        mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, h + kk > 0 ? 1u : acc);
 }
 // A vote of the 256 softmax threads; also their barrier.
 __device__ __forceinline__ bool any_of_256(bool v) {
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
             if (kE4M3 && (i == T_Q_READY || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
-            if (i >= T_P_READY && i < T_P_READY + 2) count = 8;                                                         // softmax warps
+            if (i >= T_P_READY && i < T_P_READY + 4) count = 4;                                                         // a softmax warpgroup
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
         }
@@ -308,9 +313,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     };
     auto parity = [](int uses) -> uint32_t { return (uint32_t)uses & 1u; };   // phase that the wait for use `uses` completes
 
-    // e4m3: each warpgroup first re-sizes its registers, then runs its role.
+    // Each warpgroup first re-sizes its registers, then runs its role.
     if (warp < 4) {
-    if constexpr (kE4M3) ptx::setmaxnreg_dec<C::kRegsCtl>();
+    ptx::setmaxnreg_dec<C::kRegsCtl>();
     if (warp == 0) {
         // ================================================== producer
         TileItem it;
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             // through a shuffle: the compiler then knows them to be the same in every lane
             auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
             const int nk = uni(it.nk), tiles = uni(it.tiles), slot = uni(it.slot), kv0 = uni(it.kv);
-            const int s_use[2] = {uni(it.s_use[0]), uni(it.s_use[1])};
+            const int p_use[2] = {uni(it.p_use[0]), uni(it.p_use[1])};
             if (nk <= 0) continue;
             auto full = [&](int u) { return tile_wait_warp(BAR(T_KV_FULL + u % kKvStages), parity(u / kKvStages), tw); };
             auto stage = [&](int u) { return lo0 + ((C::OFF_KV + (u % kKvStages) * C::kTile) >> 4); };
@@ -415,10 +420,22 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             auto empty = [&](int u) { commit_if(leader, BAR(T_KV_EMPTY + u % kKvStages)); };
             auto scores = [&](int buf, int q, int u) {
                 product_s<D, kE4M3>(leader, tmem + 128 * buf, q_lo(q), stage(u) + kDescK);
-                commit_if(leader, BAR(T_S_FULL + buf));
+                commit_if(leader, BAR(T_S_FULL + 2 * q + buf));
             };
-            auto values = [&](int buf, int x, int u, int j) {   // O (+)= P V_j
-                product_pv<D, kE4M3>(leader, tmem + 256 + 128 * x, tmem + 128 * buf, stage(u) + kDescMn, j > 0 ? 1u : 0u);
+            // O_x (+)= P V_j.  bf16: in two halves of the keys, as the weights become ready.  e4m3: each half's warpgroup
+            // also rescales its half of O's columns, so both have to be there.
+            auto values = [&](int buf, int x, int u, int j, int use) -> bool {
+                const uint32_t d = tmem + 256 + 128 * x, a = tmem + 128 * buf, b = stage(u) + kDescMn;
+                if (!tile_wait_warp(BAR(T_P_READY + 2 * buf), parity(use), tw)) return false;
+                if (kE4M3 && !tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
+                ptx::tc_fence_after();
+                product_pv<D, kE4M3>(leader, d, a, b, 0, j > 0 ? 1u : 0u);
+                if (!kE4M3) {
+                    if (!tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
+                    ptx::tc_fence_after();
+                }
+                product_pv<D, kE4M3>(leader, d, a, b, 1, 1u);
+                return true;
             };
             if (kE4M3) {
                 ok = tile_wait_warp(BAR(T_Q_READY), parity(it.qi), tw);
@@ -442,10 +459,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                         commit_if(leader, BAR(T_Q_EMPTY + 0));
                         commit_if(leader, BAR(T_Q_EMPTY + 1));
                     }
-                    ok = full(uv) && tile_wait_warp(BAR(T_P_READY + 0), parity(s_use[0] + j), tw);
+                    ok = full(uv) && values(0, 0, uv, j, p_use[0] + j);
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    values(0, 0, uv, j);
                     if (more) {
                         ok = full(uk);
                         if (!ok) break;
@@ -454,10 +469,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     } else {
                         commit_if(leader, BAR(T_O_FULL + 0));
                     }
-                    ok = tile_wait_warp(BAR(T_P_READY + 1), parity(s_use[1] + j), tw);
+                    ok = values(1, 1, uv, j, p_use[1] + j);
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    values(1, 1, uv, j);
                     empty(uv);
                     if (more) {
                         scores(1, 1, uk);
@@ -481,13 +494,11 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     } else {
                         commit_if(leader, BAR(T_Q_EMPTY + slot));
                     }
-                    ok = full(uv) && tile_wait_warp(BAR(T_P_READY + buf), parity(pick(s_use, buf) + (j >> 1)), tw);
+                    ok = full(uv) && values(buf, slot, uv, j, pick(p_use, buf) + (j >> 1));
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    values(buf, 0, uv, j);
                     empty(uv);
                     commit_if(leader, BAR(T_PV_DONE));
-                    if (j + 1 == nk) commit_if(leader, BAR(T_O_FULL + 0));
+                    if (j + 1 == nk) commit_if(leader, BAR(T_O_FULL + slot));
                 }
             }
         }
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         // ================================================== scheduler
         const Plan* plan = p.plan;
         const int items = plan->items[p.nb];
-        int buf = 0, slot = 0, kv = 0, kt = 0, qi = 0, pv = 0, s_use[2] = {0, 0}, q_use[2] = {0, 0}, o_use[2] = {0, 0};
+        int buf = 0, slot = 0, kv = 0, kt = 0, qi = 0, pv = 0, s_use[2][2] = {{0, 0}, {0, 0}}, p_use[2] = {0, 0}, q_use[2] = {0, 0}, o_use[2] = {0, 0};
         for (int u = 0;; ++u) {
             int item = 0;
             if (lane == 0) item = atomicAdd(p.counter, 1);
@@ -551,7 +562,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 it.pv = pv;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    it.s_use[x] = s_use[x];
+                    it.s_use[x] = it.tiles == 2 ? s_use[x][x] : (slot ? s_use[1][x] : s_use[0][x]);
+                    it.p_use[x] = p_use[x];
                     it.q_use[x] = q_use[x];
                     it.o_use[x] = o_use[x];
                 }
@@ -561,14 +573,16 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     ++qi;
                     if (it.tiles == 2) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) s_use[x] += it.nk, ++q_use[x], ++o_use[x];
+                        for (int x = 0; x < 2; ++x) s_use[x][x] += it.nk, p_use[x] += it.nk, ++q_use[x], ++o_use[x];
                     } else {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            s_use[x] += (it.nk + (x == buf ? 1 : 0)) / 2;
+                            const int uses = (it.nk + (x == buf ? 1 : 0)) / 2;
+                            (slot ? s_use[1][x] : s_use[0][x]) += uses;
+                            p_use[x] += uses;
                             q_use[x] += x == slot ? 1 : 0;
+                            o_use[x] += x == slot ? 1 : 0;
                         }
-                        ++o_use[0];
                         pv += it.nk;
                         buf ^= it.nk & 1;
                         slot ^= 1;
@@ -584,42 +598,56 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         }
     }
     } else if (warp < 12) {
-        if constexpr (kE4M3) ptx::setmaxnreg_inc<C::kRegsSoftmax>();
+        ptx::setmaxnreg_inc<C::kRegsSoftmax>();
         // ================================================== softmax and epilogue
-        // A thread has one row of each tile; its warpgroup keys 64 w .. of every key tile, and columns D/2 w .. of O.
+        // e4m3: this warpgroup w has keys 64 w .. of every key tile and columns D/2 w .. of O, of both row tiles (n = 0, 1);
+        // bf16: everything of row tile w (n = 0).
+        constexpr int kN = kE4M3 ? 2 : 1, kCols = kE4M3 ? 64 : 128, kOut = kE4M3 ? D / 2 : D;
         const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t out0 = 256u + (kE4M3 ? (uint32_t)(kOut * w) : 0u);
         float* const mx_own = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * w + row;
         float* const mx_other = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * (w ^ 1) + row;
-        TileItem it;
-        for (;;) {
-            const bool more = next_item(it);
-            // all eight warps take an item, or none: nobody is left alone at the votes below (after a wait that ran out,
-            // the others just do not wait)
-            if (any_of_256(!more)) break;
-            const int nk = it.nk;
+        for (int u = 0;; ++u) {
+            // The item stays in its slot until the epilogue: what the loop over its key tiles needs is copied here.
+            const int at_slot = u % kItemSlots;
+            const TileItem& it = *reinterpret_cast<const TileItem*>(smem + C::OFF_ITEM + C::kItemBytes * at_slot);
+            const bool more = tile_wait_warp(BAR(T_ITEM_FULL + at_slot), parity(u / kItemSlots), tw) && it.b >= 0;
+            // e4m3: all eight warps take an item, or none: nobody is left alone at the votes below (after a wait that ran
+            // out, the others just do not wait)
+            if (kE4M3 ? any_of_256(!more) : !more) break;
+            const int nk = it.nk, tiles = it.tiles, t0 = it.t0, kt = it.kt, qi = it.qi, pv = it.pv, slot = it.slot;
+            const int use0 = it.s_use[0], use1 = it.s_use[1], buf0 = it.buf;
+            // row tile of the item, and whether it is this warpgroup's
+            auto tile = [&](int n) { return tiles == 1 ? 0 : kE4M3 ? n : w; };
+            auto mine = [&](int n) { return kE4M3 ? n < tiles : tiles == 2 || slot == w; };
+            auto o_of = [&](int n) { return tiles == 1 ? slot : tile(n); };
             // this row's keys, and the key tiles that every row of its tile sees whole
-            int lo_r[2], hi_r[2], full_lo[2], full_hi[2];
-            bool valid[2];
+            int lo_r[kN], hi_r[kN], full_lo[kN], full_hi[kN];
+            bool valid[kN];
+            float m_ref[kN], l[kN], c[kN];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = x * tpt + row / p.G, pos = it.pos + i;
-                valid[x] = row < trows && i < it.ntok;
-                hi_r[x] = p.causal ? pos + 1 : it.len;
-                lo_r[x] = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
-                const int pos0 = it.pos + x * tpt, pos1 = min(it.pos + it.ntok - 1, pos0 + tpt - 1);
-                full_hi[x] = p.causal ? pos0 + 1 : it.len;
-                full_lo[x] = (p.window && pos1 + 1 > p.window) ? pos1 + 1 - p.window : 0;
+            for (int n = 0; n < kN; ++n) {
+                const int x = tile(n), pos_ = it.pos, ntok = it.ntok, len = it.len;
+                const int i = x * tpt + row / p.G, pos = pos_ + i;
+                valid[n] = row < trows && i < ntok;
+                hi_r[n] = p.causal ? pos + 1 : len;
+                lo_r[n] = (p.window && pos + 1 > p.window) ? pos + 1 - p.window : 0;
+                const int first = pos_ + x * tpt, last = min(pos_ + ntok - 1, first + tpt - 1);
+                full_hi[n] = p.causal ? first + 1 : len;
+                full_lo[n] = (p.window && last + 1 > p.window) ? last + 1 - p.window : 0;
+                m_ref[n] = -INFINITY;
+                l[n] = 0.f;
+                c[n] = p.scale_log2e;
             }
-            float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, c[2] = {p.scale_log2e, p.scale_log2e};
             float vfac = 1.f;   // O holds the sum over vfac
-            for (int j = 0; j < nk; ++j) {
-                const int key = (it.t0 + j) * 128 + 64 * w;   // the first of this warpgroup's keys
-                uint4 s4[kE4M3 ? 16 : 1];                      // e4m3: their scales
-                float grown = 1.f;                             // of O, when the values' power of two has grown
+            for (int j = 0; j < nk && mine(0); ++j) {
+                const int key = (t0 + j) * 128 + (kE4M3 ? 64 * w : 0);   // the first of this thread's columns
+                uint4 s4[kE4M3 ? 16 : 1];                                 // e4m3: their scales
+                float grown = 1.f;                                        // of O, when the values' power of two has grown
                 if constexpr (kE4M3) {
-                    const int t = it.kt + j;
+                    const int t = kt + j;
                     tile_wait_warp(BAR(T_SCALES + (t & 3)), parity(t >> 2), tw);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) s4[k] = lds128(sbase + C::OFF_KSC + (t & 3) * 512 + 256 * w + 16 * k);
@@ -629,36 +657,37 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     vfac = f;
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (x >= it.tiles) continue;
-                    const int buf = it.tiles == 2 ? x : (it.buf + j) & 1;
-                    const uint32_t tS = tbase + 128u * (uint32_t)buf + 64u * (uint32_t)w;
-                    tile_wait_warp(BAR(T_S_FULL + buf), parity(pick(it.s_use, buf) + (it.tiles == 2 ? j : j >> 1)), tw);
+                for (int n = 0; n < kN; ++n) {
+                    if (!mine(n)) continue;
+                    const int buf = tiles == 2 ? tile(n) : (buf0 + j) & 1;
+                    const uint32_t tS = tbase + 128u * (uint32_t)buf + (kE4M3 ? 64u * (uint32_t)w : 0u);
+                    const bool ready = tile_wait_warp(BAR(T_S_FULL + 2 * o_of(n) + buf), parity((buf ? use1 : use0) + (tiles == 2 ? j : j >> 1)), tw);
+                    (void)ready;   // after a wait that ran out, values that nobody uses
                     ptx::tc_fence_after();
-                    float y[64];
+                    float y[kCols];
                     {
-                        uint32_t r[2][32];
-                        ptx::tmem_ld32(tS, r[0]);
-                        ptx::tmem_ld32(tS + 32, r[1]);
+                        uint32_t r[kCols / 32][32];
+#pragma unroll
+                        for (int h = 0; h < kCols / 32; ++h) ptx::tmem_ld32(tS + 32 * h, r[h]);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) y[k] = __uint_as_float(r[k >> 5][k & 31]);
+                        for (int k = 0; k < kCols; ++k) y[k] = __uint_as_float(r[k >> 5][k & 31]);
                     }
                     if constexpr (kE4M3) {
                         if (j == 0)
-                            c[x] *= reinterpret_cast<const float*>(
-                                smem + C::OFF_QFAC)[((it.qi & 1) * 2 + (it.tiles == 2 ? x : it.slot)) * 128 + row];
+                            c[n] *= reinterpret_cast<const float*>(
+                                smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? n : slot)) * 128 + row];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const ptx::f2 u = ptx::mul2({y[4 * k], y[4 * k + 1]}, {__uint_as_float(s4[k].x), __uint_as_float(s4[k].y)});
-                            const ptx::f2 v = ptx::mul2({y[4 * k + 2], y[4 * k + 3]}, {__uint_as_float(s4[k].z), __uint_as_float(s4[k].w)});
-                            y[4 * k] = u.x, y[4 * k + 1] = u.y, y[4 * k + 2] = v.x, y[4 * k + 3] = v.y;
+                            const ptx::f2 a = ptx::mul2({y[4 * k], y[4 * k + 1]}, {__uint_as_float(s4[k].x), __uint_as_float(s4[k].y)});
+                            const ptx::f2 b = ptx::mul2({y[4 * k + 2], y[4 * k + 3]}, {__uint_as_float(s4[k].z), __uint_as_float(s4[k].w)});
+                            y[4 * k] = a.x, y[4 * k + 1] = a.y, y[4 * k + 2] = b.x, y[4 * k + 3] = b.y;
                         }
                     }
-                    if (key < full_lo[x] || key + 64 > full_hi[x]) {
-                        const int ka = lo_r[x] - key, kb = hi_r[x] - key;   // visible columns [ka, kb)
+                    if (key < full_lo[n] || key + kCols > full_hi[n]) {
+                        const int ka = lo_r[n] - key, kb = hi_r[n] - key;   // visible columns [ka, kb)
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
+                        for (int k = 0; k < kCols; ++k)
                             if (k < ka || k >= kb) y[k] = -INFINITY;
                     }
                     // row maximum and sum over interleaved partials: short chains, one fixed order
@@ -666,24 +695,28 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
 #pragma unroll
                     for (int k = 0; k < 4; ++k) part[k] = fmaxf(y[2 * k], y[2 * k + 1]);
 #pragma unroll
-                    for (int k = 8; k < 64; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
-                    float mx = c[x] * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                    if (any_of_256((valid[x] && mx > m_ref[x] + 8.f) || (kE4M3 && grown != 1.f))) {
-                        *mx_own = mx;
-                        any_of_256(false);
-                        mx = fmaxf(mx, *mx_other);
-                        const float m_new = fmaxf(m_ref[x], mx);
-                        const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref[x] - m_new);
-                        m_ref[x] = m_new;
-                        l[x] *= alpha;
+                    for (int k = 8; k < kCols; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
+                    float mx = c[n] * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                    const bool over = valid[n] && mx > m_ref[n] + 8.f;
+                    const bool raise = kE4M3 ? any_of_256(over || grown != 1.f) : __any_sync(0xffffffffu, over);
+                    if (raise) {
+                        if (kE4M3) {
+                            *mx_own = mx;
+                            any_of_256(false);
+                            mx = fmaxf(mx, *mx_other);
+                        }
+                        const float m_new = fmaxf(m_ref[n], mx);
+                        const float alpha = m_new == -INFINITY ? 1.f : ptx::ex2(m_ref[n] - m_new);
+                        m_ref[n] = m_new;
+                        l[n] *= alpha;
                         const float alpha_o = kE4M3 ? alpha * grown : alpha;
                         if (j > 0) {
                             // (one tile: S(j) was issued before PV(j-1))
-                            if (it.tiles == 1) tile_wait_warp(BAR(T_PV_DONE), parity(it.pv + j - 1), tw);
+                            if (tiles == 1) tile_wait_warp(BAR(T_PV_DONE), parity(pv + j - 1), tw);
                             ptx::tc_fence_after();
 #pragma unroll 1
-                            for (int cc = 0; cc < D / 32; ++cc) {
-                                const uint32_t tO = tbase + 256u + 128u * (uint32_t)x + (uint32_t)(D / 2 * w + 16 * cc);
+                            for (int cc = 0; cc < kOut / 16; ++cc) {
+                                const uint32_t tO = tbase + out0 + 128u * (uint32_t)o_of(n) + (uint32_t)(16 * cc);
                                 uint32_t r[16];
                                 ptx::tmem_ld16(tO, r);
                                 ptx::tmem_ld_wait();
@@ -693,54 +726,63 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             }
                         }
                     }
-                    const float m_use = m_ref[x] == -INFINITY ? 0.f : m_ref[x];
+                    const float m_use = m_ref[n] == -INFINITY ? 0.f : m_ref[n];
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys 64 w .. at columns 64 w .. + 31
+                    // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys [0,64) -> columns [0,32), [64,128) -> [64,96)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < kCols / 32; ++h) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const ptx::f2 e = ptx::fma2({y[32 * h + k], y[32 * h + k + 1]}, {c[x], c[x]}, {-m_use, -m_use});
+                            const ptx::f2 e = ptx::fma2({y[32 * h + k], y[32 * h + k + 1]}, {c[n], c[n]}, {-m_use, -m_use});
                             const ptx::f2 v{ptx::ex2(e.x), ptx::ex2(e.y)};
                             const ptx::f2 s = ptx::add2({sum[k & 3], sum[(k + 1) & 3]}, v);
                             sum[k & 3] = s.x;
                             sum[(k + 1) & 3] = s.y;
                             pk[k >> 1] = kE4M3 ? pack_half(v.x, v.y) : pack_bf16(v.x, v.y);
                         }
-                        ptx::tmem_st16(tS + 16 * h, pk);
+                        ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
+                        if (h & 1) {
+                            ptx::tmem_st_wait();
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + 2 * buf + (kE4M3 ? w : h >> 1)));
+                        }
                     }
-                    l[x] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    ptx::tmem_st_wait();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(BAR(T_P_READY + buf));
+                    l[n] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
             }
-            // the rows' sums over both halves of the columns, in one order
-            float* const sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
-            for (int x = 0; x < 2; ++x) sums[(2 * x + w) * 128 + row] = l[x];
-            any_of_256(false);
+            float total[kN];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x >= it.tiles) continue;
+            for (int n = 0; n < kN; ++n) total[n] = l[n];
+            if constexpr (kE4M3) {   // the rows' sums over both halves of the columns, in one order
+                float* const sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) sums[(2 * n + w) * 128 + row] = l[n];
+                any_of_256(false);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) total[n] = sums[2 * n * 128 + row] + sums[(2 * n + 1) * 128 + row];
+            }
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                if (!mine(n)) continue;
+                const int o = o_of(n), i = tile(n) * tpt + row / p.G, g = row % p.G;
                 if (nk > 0) {
-                    tile_wait_warp(BAR(T_O_FULL + x), parity(it.o_use[x]), tw);
+                    tile_wait_warp(BAR(T_O_FULL + o), parity(pick(it.o_use, o)), tw);
                     ptx::tc_fence_after();
                 }
-                const float total = sums[2 * x * 128 + row] + sums[(2 * x + 1) * 128 + row];
-                const int i = x * tpt + row / p.G, g = row % p.G;
+                const bool split = it.split != 0;
                 const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
                 const long long pr = it.part + (long long)i * p.G + g;
-                const bool empty = !(total > 0.f);
-                const float inv = vfac * (it.split || empty ? 1.f : 1.f / total);
-                const bool keep = it.split && valid[x] && pr < p.max_rows;
+                const bool empty = !(total[n] > 0.f);
+                const float inv = vfac * (split || empty ? 1.f : 1.f / total[n]);
+                const bool keep = split && valid[n] && pr < p.max_rows;
 #pragma unroll
-                for (int cc = 0; cc < D / 64; ++cc) {
-                    const int col = D / 2 * w + 32 * cc;
+                for (int cc = 0; cc < kOut / 32; ++cc) {
+                    const int col = (kE4M3 ? kOut * w : 0) + 32 * cc;
                     uint32_t r[32];
                     if (nk > 0) {
-                        ptx::tmem_ld32(tbase + 256u + 128u * (uint32_t)x + (uint32_t)col, r);
+                        ptx::tmem_ld32(tbase + 256u + 128u * (uint32_t)o + (uint32_t)col, r);
                         ptx::tmem_ld_wait();
                     }
 #pragma unroll
@@ -749,7 +791,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<uint4*>(p.part_o + pr * D + col + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
-                    } else if (!it.split && valid[x]) {
+                    } else if (!split && valid[n]) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8)
                             *reinterpret_cast<uint4*>(p.o + at * D + col + k) =
@@ -759,12 +801,15 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                                            pack_bf16(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7])));
                     }
                 }
-                if (w == 0 && keep)
-                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[x], empty ? 0.f : total);
-                else if (w == 0 && !it.split && valid[x] && p.lse)
-                    p.lse[at] = empty ? -INFINITY : (m_ref[x] + log2f(total)) * kLn2P;
+                const bool stats = !kE4M3 || w == 0;
+                if (stats && keep)
+                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[n], empty ? 0.f : total[n]);
+                else if (stats && !split && valid[n] && p.lse)
+                    p.lse[at] = empty ? -INFINITY : (m_ref[n] + log2f(total[n])) * kLn2P;
             }
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(BAR(T_ITEM_EMPTY + at_slot));
         }
     } else if (kE4M3) {
         ptx::setmaxnreg_dec<C::kRegsConv>();
