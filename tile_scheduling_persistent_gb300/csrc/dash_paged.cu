@@ -198,13 +198,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         ptx::prefetch_tensormap(&p.tm_k);
         ptx::prefetch_tensormap(&p.tm_v);
     }
-    if (many && blockIdx.x == 0) {   // the many-rows kernel's plan and item counter
-        if (threadIdx.x == 0) *p.counter = 0;
-        make_plan(p, plan, false, false);
-        publish_plan(p, plan);
-        __syncthreads();
-    }
-    make_plan(p, plan, true, blockIdx.x == 0);
+    if (many && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+    make_plan(p, plan, blockIdx.x == 0, many && blockIdx.x == 0 ? p.plan : nullptr);
     launch_dependents();
     const int items = plan.items[p.nb];
     ItemWalk walk;
@@ -288,6 +283,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     for (int item = half * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
         const int R = it.s.n * p.G;
+        const int rt = kRowTiles == 1 || R <= 8 ? 1 : 2;   // row tiles of this item
         // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
         int hi[kRowTiles][2], lo[kRowTiles][2], full_lo, full_hi, skip;
 #pragma unroll
@@ -393,7 +389,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     const int chunk = 2 * (k & 3) + (lane >> 4);
                     ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
 #pragma unroll
-                    for (int t = 0; t < kRowTiles; ++t) mma16816<false>(s[t], a, qf[t][k][0], qf[t][k][1]);
+                    for (int t = 0; t < kRowTiles; ++t)
+                        if (t < rt) mma16816<false>(s[t], a, qf[t][k][0], qf[t][k][1]);
                 }
             } else {
 #pragma unroll
@@ -412,7 +409,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         const uint32_t a[4] = {half2_of_e4m3(w[0][x], 0), half2_of_e4m3(w[1][x], 0), half2_of_e4m3(w[0][x], 1),
                                                half2_of_e4m3(w[1][x], 1)};
 #pragma unroll
-                        for (int t = 0; t < kRowTiles; ++t) mma16816<true>(s[t], a, qf[t][4 * h + x][0], qf[t][4 * h + x][1]);
+                        for (int t = 0; t < kRowTiles; ++t)
+                            if (t < rt) mma16816<true>(s[t], a, qf[t][4 * h + x][0], qf[t][4 * h + x][1]);
                     }
                 }
             }
@@ -453,6 +451,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    if (t >= rt) continue;
                     mx[t][e] = fmaxf(s[t][e], s[t][2 + e]);
                     mw[t][e] = kE4M3 ? fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) : 0.f;
 #pragma unroll
@@ -465,6 +464,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int t = 0; t < kRowTiles; ++t) {
+                    if (t >= rt) continue;
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             uint32_t pb[kRowTiles][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
 #pragma unroll
             for (int t = 0; t < kRowTiles; ++t) {
+                if (t >= rt) continue;
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -512,7 +513,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
                     ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
 #pragma unroll
-                    for (int t = 0; t < kRowTiles; ++t) mma16816<false>(o[t][j], a, pb[t][0], pb[t][1]);
+                    for (int t = 0; t < kRowTiles; ++t)
+                        if (t < rt) mma16816<false>(o[t][j], a, pb[t][0], pb[t][1]);
                 }
             } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         const uint32_t lo2 = __byte_perm(w[0][y], w[1][y], sel), hi2 = __byte_perm(w[2][y], w[3][y], sel);
                         const uint32_t a[4] = {half2_of_e4m3(lo2, 0), half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 0), half2_of_e4m3(hi2, 1)};
 #pragma unroll
-                        for (int t = 0; t < kRowTiles; ++t) mma16816<true>(o[t][2 * y + z], a, pb[t][0], pb[t][1]);
+                        for (int t = 0; t < kRowTiles; ++t)
+                            if (t < rt) mma16816<true>(o[t][2 * y + z], a, pb[t][0], pb[t][1]);
                     }
             }
             if (edge) ptx::fence_proxy_async_smem();   // the zeroed rows before the next copy into the stage
@@ -622,120 +625,162 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 }
 
 // ---------------------------------------------------------------- joining key ranges
-// One block per row of a split sequence: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over its ranges, warp w
-// taking ranges w, w + 8, ... and the eight warps joined in order, so the additions have one fixed order.  The block
-// finds its first row while the kernel before it runs: it keeps its share of the plan in registers and little shared
-// memory, so that it fits beside that kernel's CTA on an SM.
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the ns ranges of a row of a split sequence.  A block takes units:
+// eight rows, one for each warp, which adds the ranges in ascending order; or one row of a sequence with many ranges
+// (more than kWarpRanges, where one warp's chain of loads would take tens of microseconds), warp w adding ranges w,
+// w + 8, ... and the eight sums added in order.  Which of the two depends on the row's own ns.  A block finds its first
+// unit while the kernel before it runs, with its share of the plan in registers and little shared memory, so that it fits
+// beside that kernel's CTA on an SM.
+constexpr int kWarpRanges = 48;
+
+// Adds ranges s0, s0 + step, ... of the partial rows base, base + stride, ...: (sum l, sum o of this lane's D / 32 columns)
+// relative to the maximum mu.
+template <int D>
+__device__ __forceinline__ void add_ranges(const PagedParams& p, long long base, long long stride, int s0, int step, int ns, float mu,
+                                           float (&a)[D / 32], float& l) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = 0.f;
+    for (int s = s0; s < ns; s += 8 * step) {   // eight loads at a time
+        float2 ml[8];
+        float v[8][E];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const long long at = base + (s + k * step) * stride;
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+            if (s + k * step < ns) {
+                ml[k] = p.part_ml[at];
+                const float* o = p.part_o + at * D + E * lane;
+                if (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(o);
+                    v[k][0] = x.x, v[k][1] = x.y, v[k][E - 2] = x.z, v[k][E - 1] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(o);
+                    v[k][0] = x.x, v[k][1] = x.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = ptx::ex2(ml[k].x - mu);
+            l += f * ml[k].y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] += f * v[k][e];
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ PagedParams p) {
     constexpr int E = D / 32, kSeqs = kMaxSeqs / 256;
-    struct Row {
-        int first, n, ns, local;   // its sequence; (token, head) in it
+    struct Unit {
+        int first, n, ns, local;   // its sequence; the first (token, head) in it
         long long base;            // partial row of the sequence's first row
     };
-    __shared__ Row found;
+    __shared__ Unit found[2];
     __shared__ int sums[2][8];
     __shared__ float part[8][D];
     __shared__ float part_l[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // this thread's sequences: rows to join (n * Hq of split ones) and partial rows (times ns), and the counts before
+    // this thread's sequences: units, partial rows, and the counts before
     Seq seq[kSeqs];
-    int ns_[kSeqs], rows = 0, parts = 0;
+    int ns_[kSeqs], units = 0, parts = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqs; ++k) seq[k] = Seq{0, 0, 0}, ns_[k] = 1;
+    auto units_of = [&](int k) {
+        const int rows = seq[k].n * p.Hq;
+        return ns_[k] <= 1 ? 0 : ns_[k] <= kWarpRanges ? (rows + 7) / 8 : rows;
+    };
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
         const int i = kSeqs * threadIdx.x + k;
-        ns_[k] = 1;
         if (i >= p.nb) continue;
         seq[k] = load_seq(p, p.b0 + i, false);
         if (seq[k].n == 0) continue;
         ns_[k] = (few_rows(seq[k].n, p.G) ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G))).ns;
-        if (ns_[k] > 1) {
-            rows += seq[k].n * p.Hq;
-            parts += seq[k].n * p.Hq * ns_[k];
-        }
+        units += units_of(k);
+        if (ns_[k] > 1) parts += seq[k].n * p.Hq * ns_[k];
     }
-    int sr = rows, sp = parts;
+    int su = units, sp = parts;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sr, d), y = __shfl_up_sync(0xffffffffu, sp, d);
-        if (lane >= d) sr += x, sp += y;
+        const int x = __shfl_up_sync(0xffffffffu, su, d), y = __shfl_up_sync(0xffffffffu, sp, d);
+        if (lane >= d) su += x, sp += y;
     }
-    if (lane == 31) sums[0][warp] = sr, sums[1][warp] = sp;
+    if (lane == 31) sums[0][warp] = su, sums[1][warp] = sp;
     __syncthreads();
     int total = 0;
-    sr -= rows, sp -= parts;
+    su -= units, sp -= parts;
     for (int w = 0; w < 8; ++w) {
-        if (w < warp) sr += sums[0][w], sp += sums[1][w];
+        if (w < warp) su += sums[0][w], sp += sums[1][w];
         total += sums[0][w];
     }
-    bool waited = false;
-    for (int w = blockIdx.x; w < total; w += gridDim.x) {
-        if (w >= sr && w < sr + rows) {   // one thread of the block
-            int r0 = sr;
+    int turn = 0;
+    for (int w = blockIdx.x; w < total; w += gridDim.x, turn ^= 1) {
+        if (w >= su && w < su + units) {   // one thread of the block
+            int u0 = su;
             long long p0 = sp;
 #pragma unroll
             for (int k = 0; k < kSeqs; ++k) {
-                const int here = ns_[k] > 1 ? seq[k].n * p.Hq : 0;
-                if (w >= r0 && w < r0 + here) found = Row{seq[k].first, seq[k].n, ns_[k], w - r0, p0};
-                r0 += here;
-                p0 += (long long)here * ns_[k];
+                const int here = units_of(k);
+                if (w >= u0 && w < u0 + here)
+                    found[turn] = Unit{seq[k].first, seq[k].n, ns_[k], (w - u0) * (ns_[k] <= kWarpRanges ? 8 : 1), p0};
+                u0 += here;
+                if (ns_[k] > 1) p0 += (long long)seq[k].n * p.Hq * ns_[k];
             }
         }
         __syncthreads();
-        const Row row = found;
-        if (!waited) wait_dependency();
-        waited = true;
-        const int i = row.local / p.Hq, h = row.local % p.Hq, hk = h / p.G;
-        const int R = row.n * p.G;
-        const long long base = row.base + (long long)hk * R + i * p.G + h % p.G, step = (long long)p.c.Hkv * R;
-        if (base + (row.ns - 1) * step < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
-            float top = -INFINITY;
-            for (int s = lane; s < row.ns; s += 32) top = fmaxf(top, p.part_ml[base + s * step].x);
+        if (w == (int)blockIdx.x) wait_dependency();
+        const Unit unit = found[turn];
+        const bool alone = unit.ns <= kWarpRanges;
+        const int local = unit.local + (alone ? warp : 0);
+        const int i = local / p.Hq, h = local % p.Hq, hk = h / p.G;
+        const int R = unit.n * p.G;
+        const long long stride = (long long)p.c.Hkv * R, base = unit.base + (long long)hk * R + i * p.G + h % p.G;
+        const long long at = (long long)(unit.first + i) * p.Hq + h;
+        const bool real = i < unit.n && base + (unit.ns - 1) * stride < p.max_rows;   // (the second: unless cu_q, reported, decreases)
+        float top = -INFINITY, l = 0.f, a[E];
+        if (real) {
+            for (int s = lane; s < unit.ns; s += 32) top = fmaxf(top, p.part_ml[base + s * stride].x);
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float mu = top == -INFINITY ? 0.f : top;
-            float a[E], l = 0.f;
+            add_ranges<D>(p, base, stride, alone ? 0 : warp, alone ? 1 : 8, unit.ns, top == -INFINITY ? 0.f : top, a, l);
+        }
+        if (!alone) {
+            if (real) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) a[e] = 0.f;
-#pragma unroll 4
-            for (int s = warp; s < row.ns; s += 8) {
-                const long long at = base + s * step;
-                const float2 ml = p.part_ml[at];
-                const float f = ptx::ex2(ml.x - mu);
-                l += f * ml.y;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
-                    a[0] += f * v.x;
-                    a[1] += f * v.y;
-                    a[E - 2] += f * v.z;
-                    a[E - 1] += f * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + 2 * lane);
-                    a[0] += f * v.x;
-                    a[1] += f * v.y;
+                for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
+                if (lane == 0) part_l[warp] = l;
+            }
+            __syncthreads();
+            if (real && warp == 0) {
+                l = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] = 0.f;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    l += part_l[v];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) a[e] += part[v][E * lane + e];
                 }
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
-            if (lane == 0) part_l[warp] = l;
             __syncthreads();
-            float sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) sum += part_l[x];
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const long long at = (long long)(row.first + i) * p.Hq + h;
-            if ((int)threadIdx.x < D / 2) {
-                const int d = 2 * threadIdx.x;
-                float x = 0.f, y = 0.f;
-#pragma unroll
-                for (int v = 0; v < 8; ++v) x += part[v][d], y += part[v][d + 1];
-                *reinterpret_cast<uint32_t*>(p.o + at * D + d) = pack_bf16(x * inv, y * inv);
-            }
-            if (p.lse && threadIdx.x == 255) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
         }
-        __syncthreads();
+        if (real && (alone || warp == 0)) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            __nv_bfloat16* o = p.o + at * D + E * lane;
+            if (E == 4)
+                *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[E - 2] * inv, a[E - 1] * inv));
+            else
+                *reinterpret_cast<uint32_t*>(o) = pack_bf16(a[0] * inv, a[1] * inv);
+            if (p.lse && lane == 0) p.lse[at] = l > 0.f ? (top + log2f(l)) * kLn2P : -INFINITY;
+        }
     }
-    if (!waited) wait_dependency();
+    if ((int)blockIdx.x >= total) wait_dependency();
 }
 
 // ---------------------------------------------------------------- host
@@ -787,7 +832,7 @@ int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    cfg.gridDim = dim3((unsigned)(max_rows < 8ll * sms ? max_rows : 8ll * sms));
+    cfg.gridDim = dim3((unsigned)(max_rows < 6ll * sms ? max_rows : 6ll * sms));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr;

@@ -120,7 +120,7 @@ struct Plan {
     Seq seq[kMaxSeqs];
     int items[kMaxSeqs + 1];   // items of the class before each sequence
     int rows[kMaxSeqs + 1];    // partial rows before each sequence (both classes)
-    int warp_sum[2][32];
+    int warp_sum[3][16];
 };
 
 struct Cut {
@@ -161,70 +161,77 @@ __device__ __forceinline__ Cut cut_many(const PagedParams& p, const Seq& s, int 
 // Tokens of one item of the many-rows kernel: two matrix tiles of 128 / G tokens.
 __host__ __device__ inline int tokens_per_item(int G) { return 2 * (128 / G); }
 
-// Fills plan for the launch's sequences: items of the `few` class (or of the other), and partial rows of both.  All
-// threads of the block call it; blockDim.x >= 128.  Ends with a barrier.
-__device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool few, bool report) {
+// Fills plan (shared memory) for the launch's sequences: items of the few-rows class, and partial rows of both; `many`, if
+// not null, is the same in global memory with the items of the many-rows class.  All threads of the block call it; at
+// most 16 warps, at least kMaxSeqs / 2 threads.  Ends with a barrier.
+__device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool report, Plan* many) {
     const int per = (p.nb + (int)blockDim.x - 1) / (int)blockDim.x;
     const int t0 = (int)threadIdx.x * per;
-    int items = 0, rows = 0;
-    for (int i = t0; i < t0 + per && i < p.nb; ++i) {
-        const Seq s = load_seq(p, p.b0 + i, report);
-        plan.seq[i] = s;
-        if (s.n == 0) continue;
-        const bool f = few_rows(s.n, p.G);
-        const Cut c = f ? cut_few(p, s) : cut_many(p, s, tokens_per_item(p.G));
-        if (f == few) items += c.items;
-        if (c.ns > 1) rows += s.n * p.Hq * c.ns;
+    constexpr int kPer = 2;
+    Seq seq[kPer];
+    int count[kPer][3], own[3] = {0, 0, 0};   // items of few and of many rows, partial rows
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        count[k][0] = count[k][1] = count[k][2] = 0;
+        if (k >= per || t0 + k >= p.nb) continue;
+        seq[k] = load_seq(p, p.b0 + t0 + k, report);
+        if (seq[k].n == 0) continue;
+        const bool f = few_rows(seq[k].n, p.G);
+        const Cut c = f ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G));
+        count[k][0] = f ? c.items : 0;
+        count[k][1] = f ? 0 : c.items;
+        count[k][2] = c.ns > 1 ? seq[k].n * p.Hq * c.ns : 0;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) own[x] += count[k][x];
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
-    int si = items, sr = rows;
+    int sum[3] = {own[0], own[1], own[2]};
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, si, d), b = __shfl_up_sync(0xffffffffu, sr, d);
-        if (lane >= d) {
-            si += a;
-            sr += b;
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const int v = __shfl_up_sync(0xffffffffu, sum[x], d);
+            if (lane >= d) sum[x] += v;
         }
-    }
     if (lane == 31) {
-        plan.warp_sum[0][warp] = si;
-        plan.warp_sum[1][warp] = sr;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) plan.warp_sum[x][warp] = sum[x];
     }
     __syncthreads();
-    int bi = si - items, br = sr - rows;
-    for (int w = 0; w < warp; ++w) {
-        bi += plan.warp_sum[0][w];
-        br += plan.warp_sum[1][w];
-    }
-    for (int i = t0; i < t0 + per && i < p.nb; ++i) {
-        plan.items[i] = bi;
-        plan.rows[i] = br;
-        const Seq s = plan.seq[i];
-        if (s.n == 0) continue;
-        const bool f = few_rows(s.n, p.G);
-        const Cut c = f ? cut_few(p, s) : cut_many(p, s, tokens_per_item(p.G));
-        if (f == few) bi += c.items;
-        if (c.ns > 1) br += s.n * p.Hq * c.ns;
+    int all[3] = {0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 3; ++x) sum[x] -= own[x];
+    for (int w = 0; w < warps; ++w)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const int v = plan.warp_sum[x][w];
+            all[x] += v;
+            if (w < warp) sum[x] += v;
+        }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = t0 + k;
+        if (k >= per || i >= p.nb) continue;
+        plan.seq[i] = seq[k];
+        plan.items[i] = sum[0];
+        plan.rows[i] = sum[2];
+        if (many) {
+            many->seq[i] = seq[k];
+            many->items[i] = sum[1];
+            many->rows[i] = sum[2];
+        }
+#pragma unroll
+        for (int x = 0; x < 3; ++x) sum[x] += count[k][x];
     }
     if (threadIdx.x == 0) {
-        int ti = 0, tr = 0;
-        for (int w = 0; w < warps; ++w) {
-            ti += plan.warp_sum[0][w];
-            tr += plan.warp_sum[1][w];
+        plan.items[p.nb] = all[0];
+        plan.rows[p.nb] = all[2];
+        if (many) {
+            many->items[p.nb] = all[1];
+            many->rows[p.nb] = all[2];
         }
-        plan.items[p.nb] = ti;
-        plan.rows[p.nb] = tr;
     }
     __syncthreads();
-}
-
-// The shared-memory plan to global memory, for the many-rows kernel that follows.
-__device__ __forceinline__ void publish_plan(const PagedParams& p, const Plan& plan) {
-    for (int i = threadIdx.x; i <= p.nb; i += blockDim.x) {
-        if (i < p.nb) p.plan->seq[i] = plan.seq[i];
-        p.plan->items[i] = plan.items[i];
-        p.plan->rows[i] = plan.rows[i];
-    }
 }
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
