@@ -9,13 +9,18 @@
 // Its top 32 bits, as a signed number, are the angle in [-1/2, 1/2) turns; the
 // error is p * 2^-65 turns from F_i (and p * f_i * 2^-53 from the double f_i)
 // plus fp32's rounding of that fraction.  Two integer multiplies replace a
-// 64-bit floating multiply and reduction.
+// 64-bit floating multiply and reduction.  The top bits also give the quadrant
+// exactly, which leaves an angle of at most an eighth of a turn for the fast
+// sine and cosine (off by 2^-21.4 at most); sincospif took three times the
+// instructions, a third of the kernel's time with few heads.
 //
 // Work.  One thread owns 16 values of a vector as two chunks of 8, such that
 // every chunk is one 16-byte access and the threads of a vector read
 // consecutive chunks; for rotated values the chunks are 8j.. and rot/2 + 8j..,
 // which hold both members of 8 pairs in either layout.  A thread forms the 8
-// angles of its (token, chunk) once and uses them for a run of heads.
+// angles of its (token, chunk) once and uses them for a run of heads, four
+// heads' loads at a time: these kernels only move data, and what limits them
+// is how many bytes are on their way.
 #include <math.h>
 
 #include "dash_internal.h"
@@ -39,11 +44,13 @@ __device__ __forceinline__ void angles(const Turns& t, int j, long long pos, flo
     for (int e = 0; e < 8; ++e) {
         // half layout: pairs 8j + e; interleaved: chunk 8j.. holds pairs 4j..4j+3, chunk rot/2 + 8j.. rot/4 + 4j..
         const int i = t.interleaved ? (e < 4 ? 4 * j + e : t.rot / 4 + 4 * j + e - 4) : 8 * j + e;
-        const int frac = (int)(((unsigned long long)pos * t.f[i]) >> 32);
-        float s, c;
-        sincospif((float)frac * 0x1p-31f, &s, &c);   // 2 * frac * 2^-32 half turns
-        cs[e] = c * t.factor;
-        sn[e] = s * t.factor * sign;
+        const uint32_t turn = (uint32_t)(((unsigned long long)pos * t.f[i]) >> 32);
+        const uint32_t quadrant = (turn + 0x20000000u) >> 30;                          // nearest quarter turn (mod 4)
+        const float x = (float)(int)(turn - (quadrant << 30)) * 1.46291807926715968e-9f;   // radians: 2 pi / 2^32
+        const float s0 = __sinf(x), c0 = __cosf(x);
+        const float s = (quadrant & 1u) ? c0 : s0, c = (quadrant & 1u) ? s0 : c0;
+        cs[e] = ((quadrant + 1u) & 2u) ? -c * t.factor : c * t.factor;
+        sn[e] = (quadrant & 2u) ? -s * (t.factor * sign) : s * (t.factor * sign);
     }
 }
 
@@ -80,22 +87,34 @@ __device__ __forceinline__ void chunks(int unit, int rot, int& c0, int& c1) {
     }
 }
 
-__device__ __forceinline__ void load8(const void* base, bool fp32, long long at, float (&x)[8]) {
-    if (fp32) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + at);
-        const float4 u = p[0], w = p[1];
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
-    } else {
-        unpack_bf16(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + at), x);
+// 8 values as they lie in memory, and in fp32.
+template <bool kF32>
+struct Raw8 {
+    uint4 w[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, long long at) {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + at * (kF32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) w[i] = __ldcs(p + i);
     }
-}
-__device__ __forceinline__ void store8(void* base, bool fp32, long long at, const float (&x)[8]) {
-    if (fp32) {
-        float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + at);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        if (kF32) {
+            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[kF32].x, w[kF32].y, w[kF32].z, w[kF32].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+        } else {
+            unpack_bf16(w[0], x);
+        }
+    }
+};
+template <bool kF32>
+__device__ __forceinline__ void store8(void* base, long long at, const float (&x)[8]) {
+    uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(base) + at * (kF32 ? 4 : 2));
+    if (kF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            p[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
     } else {
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at) = pack_bf16x8(x);
+        *p = pack_bf16x8(x);
     }
 }
 
@@ -106,40 +125,63 @@ struct RopeParams {
     long long pos_stride_b;
     Turns turns;
     float sign;
-    int B, S, heads;   // heads: of both tensors
+    int B, S, per;   // per: heads of a block
 };
 
+// Heads h0 .. h1 - 1 of one tensor, this thread's two chunks of each (at offsets c0, c1 from the vectors' start).
+template <bool kXf, bool kYf>
+__device__ __forceinline__ void turn_heads(const dash_heads& x, const dash_heads& y, long long from, long long to, int h0, int h1, int c0,
+                                           int c1, bool turned, int interleaved, const float (&cs)[8], const float (&sn)[8]) {
+    constexpr int kAtOnce = kXf ? 2 : 4;
+    for (int h = h0; h < h1; h += kAtOnce) {
+        Raw8<kXf> a[kAtOnce], b[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (h + i < h1) {
+                a[i].load(x.data, from + (h + i) * x.stride_h + c0);
+                b[i].load(x.data, from + (h + i) * x.stride_h + c1);
+            }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (h + i < h1) {
+                float u[8], v[8];
+                a[i].get(u);
+                b[i].get(v);
+                if (turned) rotate(u, v, cs, sn, interleaved);
+                store8<kYf>(y.data, to + (h + i) * y.stride_h + c0, u);
+                store8<kYf>(y.data, to + (h + i) * y.stride_h + c1, v);
+            }
+    }
+}
+
+// blockIdx.z: the tensor; blockIdx.y: a run of its heads.
 template <int D>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(128, 6) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int U = D / 16;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const dash_heads& x = p.x[blockIdx.z];
+    const dash_heads& y = p.y[blockIdx.z];
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const long long token = i / U;
     const int unit = (int)(i % U);
-    if (token >= (long long)p.B * p.S) return;
-    const int b = (int)(token / p.S), s = (int)(token % p.S);
-    const int per = (p.heads + gridDim.y - 1) / gridDim.y;
-    const int h0 = blockIdx.y * per, h1 = min(h0 + per, p.heads);
+    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, x.heads);
+    if (token >= (long long)p.B * p.S || h0 >= h1) return;
+    const int b = (int)(token / p.S), s = (int)(token - (long long)b * p.S);
     int c0, c1;
     chunks(unit, p.turns.rot, c0, c1);
     const bool turned = unit < p.turns.rot / 16;
+    const long long from = b * x.stride_b + s * x.stride_s, to = b * y.stride_b + s * y.stride_s;
+    const int il = p.turns.interleaved;
     float cs[8], sn[8];
     if (turned) {
         const long long pos = p.positions ? p.positions[b * p.pos_stride_b + s] : s;
         angles(p.turns, unit, pos, p.sign, cs, sn);
     }
-    for (int h = h0; h < h1; ++h) {
-        const int t = h >= p.x[0].heads;
-        const int hh = t ? h - p.x[0].heads : h;
-        const dash_heads& x = p.x[t];
-        const dash_heads& y = p.y[t];
-        const long long from = b * x.stride_b + hh * x.stride_h + s * x.stride_s;
-        const long long to = b * y.stride_b + hh * y.stride_h + s * y.stride_s;
-        float a[8], c[8];
-        load8(x.data, x.fp32, from + c0, a);
-        load8(x.data, x.fp32, from + c1, c);
-        if (turned) rotate(a, c, cs, sn, p.turns.interleaved);
-        store8(y.data, y.fp32, to + c0, a);
-        store8(y.data, y.fp32, to + c1, c);
+    if (x.fp32) {
+        if (y.fp32) turn_heads<true, true>(x, y, from, to, h0, h1, c0, c1, turned, il, cs, sn);
+        else turn_heads<true, false>(x, y, from, to, h0, h1, c0, c1, turned, il, cs, sn);
+    } else {
+        if (y.fp32) turn_heads<false, true>(x, y, from, to, h0, h1, c0, c1, turned, il, cs, sn);
+        else turn_heads<false, false>(x, y, from, to, h0, h1, c0, c1, turned, il, cs, sn);
     }
 }
 
@@ -152,21 +194,27 @@ struct WriteParams {
     const int64_t* slots;
     const int32_t* positions;   // null: no rotation
     Turns turns;
-    int T, Hq;                  // Hq: 0 without queries
+    int T, Hq, page_shift, per; // Hq: 0 without queries; per: heads of a block
 };
+
+// fl(x / d) from inv = fl(1 / d) with one correction of the quotient (Markstein, IBM J. Res. Dev. 34, 1990): the quotient
+// rounded correctly, at a third of a division's instructions, as one reciprocal serves a vector.
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, d, x), inv, q);
+}
 
 // Heads of a token in the order queries, keys, values.  The threads of one
 // vector are U consecutive lanes, whose maximum a butterfly forms.
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ WriteParams p) {
-    constexpr int U = D / 16;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ WriteParams p) {
+    constexpr int U = D / 16, kAtOnce = 4;
+    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const bool live = i / U < p.T;   // whole vectors: lanes of one vector agree
     const long long token = live ? i / U : p.T - 1;
     const int unit = (int)(i % U);
     const int heads = p.Hq + 2 * p.c.Hkv;
-    const int per = (heads + gridDim.y - 1) / gridDim.y;
-    const int h0 = blockIdx.y * per, h1 = min(h0 + per, heads);
+    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, heads);
     const int rot = p.positions ? p.turns.rot : D;
     int c0, c1;
     chunks(unit, rot, c0, c1);
@@ -180,55 +228,68 @@ __global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ Writ
         serve_error(DASH_ERR_PAGE, kOpWrite, token, slot, slots);
     const bool kept = live && slot >= 0 && slot < slots;
     if (!kept) slot = 0;
-    const long long page = slot / p.c.page_size;
-    const int off = (int)(slot % p.c.page_size);
+    const int page = (int)((unsigned long long)slot >> p.page_shift);
+    const int off = (int)(slot & (p.c.page_size - 1));
 
-    for (int h = h0; h < h1; ++h) {
-        float a[8], b[8];
-        if (h < p.Hq) {
-            const __nv_bfloat16* from = p.q + token * p.q_t + h * p.q_h;
-            load8(from, false, c0, a);
-            load8(from, false, c1, b);
-            if (turned) rotate(a, b, cs, sn, p.turns.interleaved);
-            if (live) {
-                __nv_bfloat16* to = p.q_out + token * p.qo_t + h * p.qo_h;
-                store8(to, false, c0, a);
-                store8(to, false, c1, b);
-            }
-            continue;
+    for (int hb = h0; hb < h1; hb += kAtOnce) {
+        Raw8<false> ra[kAtOnce], rb[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int h = hb + k;
+            if (h >= h1) continue;
+            const int kind = h < p.Hq ? 0 : h < p.Hq + p.c.Hkv ? 1 : 2;
+            const int hh = h - (kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.c.Hkv);
+            const __nv_bfloat16* base = kind == 0 ? p.q + token * p.q_t + hh * p.q_h
+                                      : kind == 1 ? p.k + token * p.k_t + hh * p.k_h : p.v + token * p.v_t + hh * p.v_h;
+            ra[k].load(base, c0);
+            rb[k].load(base, c1);
         }
-        const bool val = h >= p.Hq + p.c.Hkv;
-        const int hk = h - p.Hq - (val ? p.c.Hkv : 0);
-        const __nv_bfloat16* from = val ? p.v + token * p.v_t + hk * p.v_h : p.k + token * p.k_t + hk * p.k_h;
-        load8(from, false, c0, a);
-        load8(from, false, c1, b);
-        if (!val && turned) rotate(a, b, cs, sn, p.turns.interleaved);
-        const long long cell = (page * p.c.Hkv + hk) * p.c.page_size + off;
-        void* pages = val ? p.c.v : p.c.k;
-        if (kE4M3) {
-            float m = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));
-#pragma unroll
-            for (int w = U / 2; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-            const float scale = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f);
-            uint32_t q[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                q[e] = pack_e4m3x4(__fdiv_rn(a[4 * e], scale), __fdiv_rn(a[4 * e + 1], scale),
-                                   __fdiv_rn(a[4 * e + 2], scale), __fdiv_rn(a[4 * e + 3], scale));
-                q[2 + e] = pack_e4m3x4(__fdiv_rn(b[4 * e], scale), __fdiv_rn(b[4 * e + 1], scale),
-                                       __fdiv_rn(b[4 * e + 2], scale), __fdiv_rn(b[4 * e + 3], scale));
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int h = hb + k;
+            if (h >= h1) continue;   // the same in all threads
+            const int kind = h < p.Hq ? 0 : h < p.Hq + p.c.Hkv ? 1 : 2;
+            float a[8], b[8];
+            ra[k].get(a);
+            rb[k].get(b);
+            if (kind < 2 && turned) rotate(a, b, cs, sn, p.turns.interleaved);
+            if (kind == 0) {
+                if (live) {
+                    __nv_bfloat16* to = p.q_out + token * p.qo_t + h * p.qo_h;
+                    store8<false>(to, c0, a);
+                    store8<false>(to, c1, b);
+                }
+                continue;
             }
-            if (kept) {
-                uint8_t* to = reinterpret_cast<uint8_t*>(pages) + cell * D;
-                *reinterpret_cast<uint2*>(to + c0) = make_uint2(q[0], q[1]);
-                *reinterpret_cast<uint2*>(to + c1) = make_uint2(q[2], q[3]);
-                if (unit == 0) (val ? p.c.v_scale : p.c.k_scale)[cell] = scale;
+            const bool val = kind == 2;
+            const int hk = h - p.Hq - (val ? p.c.Hkv : 0);
+            const long long cell = ((long long)page * p.c.Hkv + hk) * p.c.page_size + off;
+            void* pages = val ? p.c.v : p.c.k;
+            if (kE4M3) {
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(b[e])));
+#pragma unroll
+                for (int w = U / 2; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                const float scale = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f), inv = __frcp_rn(scale);
+                uint32_t q[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    q[e] = pack_e4m3x4(quotient(a[4 * e], scale, inv), quotient(a[4 * e + 1], scale, inv),
+                                       quotient(a[4 * e + 2], scale, inv), quotient(a[4 * e + 3], scale, inv));
+                    q[2 + e] = pack_e4m3x4(quotient(b[4 * e], scale, inv), quotient(b[4 * e + 1], scale, inv),
+                                           quotient(b[4 * e + 2], scale, inv), quotient(b[4 * e + 3], scale, inv));
+                }
+                if (kept) {
+                    uint8_t* to = reinterpret_cast<uint8_t*>(pages) + cell * D;
+                    *reinterpret_cast<uint2*>(to + c0) = make_uint2(q[0], q[1]);
+                    *reinterpret_cast<uint2*>(to + c1) = make_uint2(q[2], q[3]);
+                    if (unit == 0) (val ? p.c.v_scale : p.c.k_scale)[cell] = scale;
+                }
+            } else if (kept) {
+                store8<false>(pages, cell * D + c0, a);
+                store8<false>(pages, cell * D + c1, b);
             }
-        } else if (kept) {
-            store8(pages, false, cell * D + c0, a);
-            store8(pages, false, cell * D + c1, b);
         }
     }
 }
@@ -240,49 +301,73 @@ struct ReadParams {
     long long table_stride, stride_b, stride_h, stride_s;
     const int32_t* lens;
     __nv_bfloat16 *k, *v;
-    int max_pages, B, S;
+    int max_pages, B, S, page_shift;
 };
 
-// One thread per 8 values of a token's key and value vector; blockIdx.y is the head, blockIdx.z the sequence.
+// 8 values as bf16: a cell's codes times its scale, or the values themselves.
+template <bool kE4M3>
+struct Cell8 {
+    uint4 w;
+    float scale;
+    __device__ __forceinline__ void load(const void* pages, const float* scales, long long cell, long long at) {
+        if (kE4M3) {
+            const uint2 u = __ldcs(reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(pages) + at));
+            w.x = u.x, w.y = u.y;
+            scale = scales[cell];
+        } else {
+            w = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pages) + at));
+        }
+    }
+    __device__ __forceinline__ uint4 get() const {
+        if (!kE4M3) return w;
+        float x[8];
+        unpack_e4m3x8(make_uint2(w.x, w.y), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= scale;
+        return pack_bf16x8(x);
+    }
+};
+
+// D / 8 threads per token, 4 tokens of each thread at a time; blockIdx.y is the head, blockIdx.z the sequence.
 template <int D, bool kE4M3>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
-    constexpr int C = D / 8;
+    constexpr int C = D / 8, kRows = 256 / C, kAtOnce = 4;
+    const int d = 8 * (threadIdx.x % C), r = threadIdx.x / C;
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const long long cap = (long long)p.max_pages * p.c.page_size;
-        long long len = p.lens[b];
-        if (len > cap || len < 0) {
+        long long given = p.lens[b];
+        if (given > cap || given < 0) {
             if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-                serve_error(DASH_ERR_PAGE, kOpRead, b, len, cap);
-            len = len < 0 ? 0 : cap;
+                serve_error(DASH_ERR_PAGE, kOpRead, b, given, cap);
+            given = given < 0 ? 0 : cap;
         }
-        if (len > p.S) len = p.S;
+        const int len = (int)(given < p.S ? given : p.S);
         for (int h = blockIdx.y; h < p.c.Hkv; h += gridDim.y)
-            for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < len * C; i += (long long)gridDim.x * 256) {
-                const long long j = i / C;
-                const int d = 8 * (int)(i % C);
-                const int page = p.table[b * p.table_stride + j / p.c.page_size];
-                if (page < 0 || page >= p.c.num_pages) {
-                    serve_error(DASH_ERR_PAGE, kOpRead, b, page, p.c.num_pages);
-                    continue;
+            for (int j0 = blockIdx.x * kRows * kAtOnce + r; j0 < len; j0 += gridDim.x * kRows * kAtOnce) {
+                Cell8<kE4M3> k[kAtOnce], v[kAtOnce];
+                bool ok[kAtOnce];
+                int page[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int j = j0 + i * kRows;
+                    page[i] = j < len ? p.table[b * p.table_stride + (j >> p.page_shift)] : 0;
                 }
-                const long long cell = ((long long)page * p.c.Hkv + h) * p.c.page_size + j % p.c.page_size;
-                const long long to = b * p.stride_b + h * p.stride_h + j * p.stride_s + d;
-                if (kE4M3) {
-                    float x[8];
-                    unpack_e4m3x8(*reinterpret_cast<const uint2*>((const uint8_t*)p.c.k + cell * D + d), x);
-                    const float ks = p.c.k_scale[cell], vs = p.c.v_scale[cell];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= ks;
-                    *reinterpret_cast<uint4*>(p.k + to) = pack_bf16x8(x);
-                    unpack_e4m3x8(*reinterpret_cast<const uint2*>((const uint8_t*)p.c.v + cell * D + d), x);
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int j = j0 + i * kRows;
+                    ok[i] = j < len && page[i] >= 0 && page[i] < p.c.num_pages;
+                    if (j < len && !ok[i]) serve_error(DASH_ERR_PAGE, kOpRead, b, page[i], p.c.num_pages);
+                    if (!ok[i]) continue;
+                    const long long cell = ((long long)page[i] * p.c.Hkv + h) * p.c.page_size + (j & (p.c.page_size - 1));
+                    k[i].load(p.c.k, p.c.k_scale, cell, cell * D + d);
+                    v[i].load(p.c.v, p.c.v_scale, cell, cell * D + d);
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= vs;
-                    *reinterpret_cast<uint4*>(p.v + to) = pack_bf16x8(x);
-                } else {
-                    *reinterpret_cast<uint4*>(p.k + to) =
-                        *reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.c.k + cell * D + d);
-                    *reinterpret_cast<uint4*>(p.v + to) =
-                        *reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.c.v + cell * D + d);
+                for (int i = 0; i < kAtOnce; ++i) {
+                    if (!ok[i]) continue;
+                    const long long to = b * p.stride_b + h * p.stride_h + (j0 + i * kRows) * p.stride_s + d;
+                    *reinterpret_cast<uint4*>(p.k + to) = k[i].get();
+                    *reinterpret_cast<uint4*>(p.v + to) = v[i].get();
                 }
             }
     }
@@ -323,12 +408,12 @@ bool heads_ok(const dash_heads* t) {
            serve_strides(t->stride_b, t->stride_h) && serve_strides(t->stride_s, 0);
 }
 
-// Blocks along the heads: enough for two thousand blocks, a divisor-like split of the heads' loop.
-int head_groups(long long blocks, int heads) {
-    long long g = (2048 + blocks - 1) / blocks;
-    if (g > heads) g = heads;
-    const int per = (int)((heads + g - 1) / g);
-    return (heads + per - 1) / per;
+// Heads of a block: runs of at least 8 where there are so many, which share
+// their angles, shorter ones only to have a few blocks for every SM.
+int heads_per_block(long long blocks, int heads) {
+    for (int per : {16, 8, 4, 2})
+        if (per <= heads && blocks * ((heads + per - 1) / per) >= (per > 8 ? 4096 : 1024)) return per;
+    return 1;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA; }
@@ -375,8 +460,7 @@ extern "C" int dash_rope(const dash_heads* x, const dash_heads* y, const dash_he
         prm.x[t] = *a;
         prm.y[t] = *c;
     }
-    prm.heads = x->heads + (x2 ? x2->heads : 0);
-    if ((long long)B * S * (D / 16) > (1ll << 31) * 255 || prm.heads > 65535) return DASH_ERR_ARG;
+    if ((long long)B * S * (D / 16) > (1ll << 31) * 127 || x->heads > 65535 || (x2 && x2->heads > 65535)) return DASH_ERR_ARG;
     if (!make_turns(&prm.turns, inv_freq, rot, interleaved, factor)) return DASH_ERR_ARG;
     const int rc = serve_check_device();
     if (rc) return rc;
@@ -385,12 +469,14 @@ extern "C" int dash_rope(const dash_heads* x, const dash_heads* y, const dash_he
     prm.sign = inverse ? -1.f : 1.f;
     prm.B = B;
     prm.S = S;
-    const long long blocks = ((long long)B * S * (D / 16) + 255) / 256;
-    const dim3 grid((unsigned)blocks, (unsigned)head_groups(blocks, prm.heads));
+    const long long blocks = ((long long)B * S * (D / 16) + 127) / 128;
+    const int most = x2 && x2->heads > x->heads ? x2->heads : x->heads;
+    prm.per = heads_per_block(blocks, most);
+    const dim3 grid((unsigned)blocks, (unsigned)((most + prm.per - 1) / prm.per), x2 ? 2 : 1);
     if (D == 64)
-        rope_kernel<64><<<grid, 256, 0, (cudaStream_t)stream>>>(prm);
+        rope_kernel<64><<<grid, 128, 0, (cudaStream_t)stream>>>(prm);
     else
-        rope_kernel<128><<<grid, 256, 0, (cudaStream_t)stream>>>(prm);
+        rope_kernel<128><<<grid, 128, 0, (cudaStream_t)stream>>>(prm);
     return launched();
 }
 
@@ -446,6 +532,7 @@ extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int
     prm.q_out = nullptr;
     prm.Hq = 0;
     prm.T = T;
+    prm.page_shift = __builtin_ctz((unsigned)cache->page_size);
     prm.turns.interleaved = 0;
     if (rope) {
         if (!rope->positions || ((uintptr_t)rope->positions & 3u)) return DASH_ERR_ARG;
@@ -472,15 +559,16 @@ extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int
     if ((long long)prm.Hq + 2ll * cache->Hkv > 65535) return DASH_ERR_ARG;
     if ((rc = serve_check_device())) return rc;
     const int D = cache->D;
-    const long long blocks = ((long long)T * (D / 16) + 255) / 256;
-    const dim3 grid((unsigned)blocks, (unsigned)head_groups(blocks, prm.Hq + 2 * cache->Hkv));
+    const long long blocks = ((long long)T * (D / 16) + 127) / 128;
+    prm.per = heads_per_block(blocks, prm.Hq + 2 * cache->Hkv);
+    const dim3 grid((unsigned)blocks, (unsigned)((prm.Hq + 2 * cache->Hkv + prm.per - 1) / prm.per));
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->type == DASH_CACHE_E4M3) {
-        if (D == 64) write_kernel<64, true><<<grid, 256, 0, s>>>(prm);
-        else write_kernel<128, true><<<grid, 256, 0, s>>>(prm);
+        if (D == 64) write_kernel<64, true><<<grid, 128, 0, s>>>(prm);
+        else write_kernel<128, true><<<grid, 128, 0, s>>>(prm);
     } else {
-        if (D == 64) write_kernel<64, false><<<grid, 256, 0, s>>>(prm);
-        else write_kernel<128, false><<<grid, 256, 0, s>>>(prm);
+        if (D == 64) write_kernel<64, false><<<grid, 128, 0, s>>>(prm);
+        else write_kernel<128, false><<<grid, 128, 0, s>>>(prm);
     }
     return launched();
 }
@@ -511,9 +599,10 @@ extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_tab
     prm.max_pages = max_pages;
     prm.B = B;
     prm.S = S;
+    prm.page_shift = __builtin_ctz((unsigned)cache->page_size);
     const int D = cache->D;
-    long long x = ((long long)S * (D / 8) + 255) / 256;
-    const dim3 grid((unsigned)(x < 4096 ? x : 4096), (unsigned)(cache->Hkv < 65535 ? cache->Hkv : 65535),
+    const long long x = ((long long)S + 4 * (2048 / D) - 1) / (4 * (2048 / D));   // 4 tokens of every thread
+    const dim3 grid((unsigned)(x < 65536 ? x : 65536), (unsigned)(cache->Hkv < 65535 ? cache->Hkv : 65535),
                     (unsigned)(B < 65535 ? B : 65535));
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->type == DASH_CACHE_E4M3) {
