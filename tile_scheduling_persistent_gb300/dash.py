@@ -356,33 +356,42 @@ def _device_stream(stream, what):
     return dev, stream.cuda_stream
 
 
-def _flat(t, dtype, dev, what, name):
+# These calls last a few microseconds, so the checks are written out where they are made: every method call on a tensor
+# costs some 50 ns.  A stride of a dimension of size one is read as 0.
+def _flat(t, dtype, dev, shape, what, name):
     """The address of a contiguous tensor."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(what, "%s is a contiguous %s tensor on the current CUDA device" % (name, dtype))
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(what, "%s is a contiguous %s tensor of shape %s on the current CUDA device" % (name, dtype, tuple(shape)))
     return t.data_ptr()
 
 
-def _shaped(t, dtype, dev, what, name, shape):
-    if t.shape != shape:
-        _refuse(what, "%s has shape %s" % (name, tuple(shape)))
-    return _flat(t, dtype, dev, what, name)
-
-
-def _rows(t, dtype, dev, what, name, dims):
-    """The address and strides of a tensor whose last dimension is contiguous; strides of single elements read as 0."""
-    st, sh = t.stride(), t.shape
-    if t.dtype is not dtype or t.get_device() != dev or len(sh) != dims or (st[-1] != 1 and sh[-1] > 1):
-        _refuse(what, "%s is a %d-dimensional %s tensor on the current CUDA device, contiguous in its last dimension" % (
-            name, dims, dtype))
-    return t.data_ptr(), [x if n > 1 else 0 for x, n in zip(st, sh)]
+def _tokens(t, dev, shape, what, name):
+    """The address and the token and head strides of a bf16 tensor [T, H, D]."""
+    if t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape or len(shape) != 3:
+        _refuse(what, "%s is a bf16 tensor of shape %s on the current CUDA device" % (name, tuple(shape)))
+    st, sh, sd = t.stride()
+    if sd != 1:
+        _refuse(what, "%s is contiguous in its last dimension" % name)
+    return t.data_ptr(), (st if shape[0] > 1 else 0), (sh if shape[1] > 1 else 0)
 
 
 def _heads(t, dev, what, name):
-    """dash_heads of a [B, H, S, D] tensor."""
-    dtype = t.dtype if t.dtype is _F32 else _BF16
-    p, (sb, sh, ss, _) = _rows(t, dtype, dev, what, name, 4)
-    return _HEADS.pack(p, dtype is _F32, t.shape[1], sb, sh, ss)
+    """dash_heads of a [B, H, S, D] tensor, and its strides."""
+    dtype = t.dtype
+    shape = t.shape
+    if len(shape) != 4 or t.get_device() != dev or (dtype is not _BF16 and dtype is not _F32):
+        _refuse(what, "%s is a bf16 or fp32 tensor [B, H, S, D] on the current CUDA device" % name)
+    sb, sh, ss, sd = t.stride()
+    if sd != 1:
+        _refuse(what, "%s is contiguous in its last dimension" % name)
+    B, H, S, _ = shape
+    if B == 1:
+        sb = 0
+    if H == 1:
+        sh = 0
+    if S == 1:
+        ss = 0
+    return _HEADS.pack(t.data_ptr(), dtype is _F32, H, sb, sh, ss), (sb, sh, ss)
 
 
 def _cache(k, v, k_scale, v_scale, dev, what):
@@ -391,23 +400,35 @@ def _cache(k, v, k_scale, v_scale, dev, what):
     if len(shape) != 4:
         _refuse(what, "the cache is [num_pages, Hkv, page_size, D]")
     N, H, page, D = shape
-    if k.dtype is _BF16:
+    dtype = k.dtype
+    kp, vp = _flat(k, dtype, dev, shape, what, "k_cache"), _flat(v, dtype, dev, shape, what, "v_cache")
+    if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             _refuse(what, "a bf16 cache has no scales")
-        return _CACHE.pack(_flat(k, _BF16, dev, what, "k_cache"), _shaped(v, _BF16, dev, what, "v_cache", shape), 0, 0,
-                           0, N, page, H, D), H, page, D
-    if k_scale is None or v_scale is None:
-        _refuse(what, "an e4m3 cache has k_scale and v_scale")
-    return _CACHE.pack(_flat(k, _E4M3, dev, what, "k_cache"), _shaped(v, _E4M3, dev, what, "v_cache", shape),
-                       _shaped(k_scale, _F32, dev, what, "k_scale", shape[:3]),
-                       _shaped(v_scale, _F32, dev, what, "v_scale", shape[:3]), 1, N, page, H, D), H, page, D
+        return _CACHE.pack(kp, vp, 0, 0, 0, N, page, H, D), H, page, D
+    if dtype is not _E4M3 or k_scale is None or v_scale is None:
+        _refuse(what, "the cache is bf16, or float8_e4m3fn with k_scale and v_scale")
+    shape = (N, H, page)
+    return _CACHE.pack(kp, vp, _flat(k_scale, _F32, dev, shape, what, "k_scale"),
+                       _flat(v_scale, _F32, dev, shape, what, "v_scale"), 1, N, page, H, D), H, page, D
+
+
+def _table(block_table, B, dev, what):
+    """The address of an int32 tensor [B, pages], its row stride and width."""
+    shape = block_table.shape
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or len(shape) != 2 or shape[0] != B:
+        _refuse(what, "block_table is an int32 tensor [B, pages] on the current CUDA device")
+    row, col = block_table.stride()
+    if col != 1 and shape[1] > 1:
+        _refuse(what, "block_table is contiguous in its last dimension")
+    return block_table.data_ptr(), (row if B > 1 else 0), shape[1]
 
 
 def _freqs(inv_freq, what):
     """inv_freq as something to keep alive, its address and the rotated width."""
     if not isinstance(inv_freq, torch.Tensor):
         inv_freq = torch.as_tensor(np.ascontiguousarray(inv_freq, dtype=np.float64))
-    if inv_freq.dtype is not torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() >= 0 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         _refuse(what, "inv_freq is a contiguous float64 vector on the host")
     return inv_freq, inv_freq.data_ptr(), 2 * inv_freq.shape[0]
 
@@ -431,24 +452,27 @@ def rope(x, y, inv_freq, positions=None, x2=None, y2=None, interleaved=False, fa
     what = "dash_rope"
     dev, st = _device_stream(stream, what)
     keep, freqs, rot = _freqs(inv_freq, what)
-    a, b = _heads(x, dev, what, "x"), _heads(y, dev, what, "y")
-    B, _, S, D = x.shape
-    if x.shape != y.shape:
+    a, b = _heads(x, dev, what, "x")[0], _heads(y, dev, what, "y")[0]
+    shape = x.shape
+    B, _, S, D = shape
+    if shape != y.shape:
         _refuse(what, "y has the shape of x")
     a2 = b2 = None
     if x2 is not None and y2 is not None:
-        a2, b2 = _heads(x2, dev, what, "x2"), _heads(y2, dev, what, "y2")
-        if x2.shape != y2.shape or x2.shape[0] != B or x2.shape[2] != S or x2.shape[3] != D:
+        a2, b2 = _heads(x2, dev, what, "x2")[0], _heads(y2, dev, what, "y2")[0]
+        shape = x2.shape
+        if shape != y2.shape or shape[0] != B or shape[2] != S or shape[3] != D:
             _refuse(what, "x2 and y2 are [B, H2, S, D]")
     elif x2 is not None or y2 is not None:
         _refuse(what, "x2 and y2 go together")
     pos, pos_b = None, 0
     if positions is not None:
-        pos, pst = _rows(positions, _I32, dev, what, "positions", positions.dim())
-        if positions.shape != (S,):
-            if positions.shape != (B, S):
+        if positions.shape == (S,):
+            pos = _flat(positions, _I32, dev, (S,), what, "positions")
+        else:
+            pos, pos_b, width = _table(positions, B, dev, what)
+            if width != S:
                 _refuse(what, "positions is [S] or [B, S]")
-            pos_b = pst[0]
     _check(lib().dash_rope(a, b, a2, b2, pos, pos_b, freqs, rot, bool(interleaved), factor, bool(inverse), B, S, D, st),
            what)
 
@@ -463,11 +487,11 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
     what = "dash_kv_write"
     dev, st = _device_stream(stream, what)
     c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
-    (kp, (kt, kh, _)), (vp, (vt, vh, _)) = _rows(k, _BF16, dev, what, "k", 3), _rows(v, _BF16, dev, what, "v", 3)
     T = k.shape[0]
-    if k.shape != (T, Hkv, D) or v.shape != k.shape:
-        _refuse(what, "k and v are [T, Hkv, D]")
-    sp = _shaped(slots, _I64, dev, what, "slots", (T,))
+    shape = (T, Hkv, D)
+    kp, kt, kh = _tokens(k, dev, shape, what, "k")
+    vp, vt, vh = _tokens(v, dev, shape, what, "v")
+    sp = _flat(slots, _I64, dev, (T,), what, "slots")
     r = keep = None
     if inv_freq is not None:
         if positions is None:
@@ -475,26 +499,19 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
         keep, freqs, rot = _freqs(inv_freq, what)
         qp = qt = qh = op = ot = oh = Hq = 0
         if q is not None:
-            if q_out is None or q.shape != q_out.shape:
-                _refuse(what, "q_out has the shape of q")
-            (qp, (qt, qh, _)), (op, (ot, oh, _)) = _rows(q, _BF16, dev, what, "q", 3), _rows(q_out, _BF16, dev, what, "q_out", 3)
+            if q_out is None or q.dim() != 3:
+                _refuse(what, "q and q_out are [T, Hq, D]")
             Hq = q.shape[1]
-            if q.shape != (T, Hq, D):
-                _refuse(what, "q is [T, Hq, D]")
+            shape = (T, Hq, D)
+            qp, qt, qh = _tokens(q, dev, shape, what, "q")
+            op, ot, oh = _tokens(q_out, dev, shape, what, "q_out")
         elif q_out is not None:
             _refuse(what, "q_out needs q")
-        r = _WRITE_ROPE.pack(freqs, _shaped(positions, _I32, dev, what, "positions", (T,)), rot, bool(interleaved),
-                             factor, qp, qt, qh, op, ot, oh, Hq)
+        r = _WRITE_ROPE.pack(freqs, _flat(positions, _I32, dev, (T,), what, "positions"), rot, bool(interleaved), factor,
+                             qp, qt, qh, op, ot, oh, Hq)
     elif q is not None or q_out is not None or positions is not None:
         _refuse(what, "q, q_out and positions need inv_freq")
     _check(lib().dash_kv_write(c, kp, kt, kh, vp, vt, vh, sp, T, r, st), what)
-
-
-def _table(block_table, B, dev, what):
-    p, (ts, _) = _rows(block_table, _I32, dev, what, "block_table", 2)
-    if block_table.shape[0] != B:
-        _refuse(what, "block_table is [B, pages]")
-    return p, ts, block_table.shape[1]
 
 
 def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None):
@@ -504,13 +521,14 @@ def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=Non
     what = "dash_kv_read"
     dev, st = _device_stream(stream, what)
     c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
-    (kp, ks), (vp, vs) = _rows(k, _BF16, dev, what, "k", 4), _rows(v, _BF16, dev, what, "v", 4)
-    B, H, S, d = k.shape
-    if H != Hkv or d != D or v.shape != k.shape or ks != vs:
-        _refuse(what, "k and v are [B, Hkv, S, D] with equal strides")
+    (_, ks), (_, vs) = _heads(k, dev, what, "k"), _heads(v, dev, what, "v")
+    shape = k.shape
+    B, H, S, d = shape
+    if H != Hkv or d != D or v.shape != shape or ks != vs or k.dtype is not _BF16 or v.dtype is not _BF16:
+        _refuse(what, "k and v are bf16 [B, Hkv, S, D] with equal strides")
     tp, ts, pages = _table(block_table, B, dev, what)
-    _check(lib().dash_kv_read(c, tp, ts, pages, _shaped(lens, _I32, dev, what, "lens", (B,)), kp, vp, ks[0], ks[1],
-                              ks[2], B, S, st), what)
+    _check(lib().dash_kv_read(c, tp, ts, pages, _flat(lens, _I32, dev, (B,), what, "lens"), k.data_ptr(), v.data_ptr(),
+                              *ks, B, S, st), what)
 
 
 @functools.lru_cache(maxsize=4096)   # a function of the sizes alone
@@ -533,16 +551,17 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     what = "dash_attn_paged"
     dev, st = _device_stream(stream, what)
     c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
-    qp, (qt, qh, _) = _rows(q, _BF16, dev, what, "q", 3)
-    T, Hq, d = q.shape
-    if d != D:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D:
         _refuse(what, "q is [T, Hq, D]")
-    op = _shaped(o, _BF16, dev, what, "o", (T, Hq, D))
-    lp = _shaped(lse, _F32, dev, what, "lse", (T, Hq)) if lse is not None else None
+    T, Hq, _ = shape
+    qp, qt, qh = _tokens(q, dev, shape, what, "q")
+    op = _flat(o, _BF16, dev, shape, what, "o")
+    lp = _flat(lse, _F32, dev, (T, Hq), what, "lse") if lse is not None else None
     B = kv_lens.shape[0]
     tp, ts, pages = _table(block_table, B, dev, what)
-    lens = _shaped(kv_lens, _I32, dev, what, "kv_lens", (B,))
-    cp = _shaped(cu_q, _I32, dev, what, "cu_q", (B + 1,)) if cu_q is not None else None
+    lens = _flat(kv_lens, _I32, dev, (B,), what, "kv_lens")
+    cp = _flat(cu_q, _I32, dev, (B + 1,), what, "cu_q") if cu_q is not None else None
     if max_q is None:
         max_q = T if cu_q is not None or B == 0 else T // B
     if window is None:
@@ -559,7 +578,8 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
                     workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
             wp = workspace.data_ptr()
     else:
-        wp, wn = _flat(workspace, torch.uint8, dev, what, "workspace"), workspace.numel()
+        wn = workspace.numel()
+        wp = _flat(workspace, torch.uint8, dev, (wn,), what, "workspace")
     _check(lib().dash_attn_paged(qp, qt, qh, c, tp, ts, pages, lens, cp, op, lp, B, T, Hq, max_q, bool(causal), window,
                                  wp, wn, st), what)
 
