@@ -644,13 +644,12 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             float vfac = 1.f;   // O holds the sum over vfac
             for (int j = 0; j < nk && mine(0); ++j) {
                 const int key = (t0 + j) * 128 + (kE4M3 ? 64 * w : 0);   // the first of this thread's columns
-                uint4 s4[kE4M3 ? 16 : 1];                                 // e4m3: their scales
+                uint4 s4[8];                                              // e4m3: scales of 32 of them
                 float grown = 1.f;                                        // of O, when the values' power of two has grown
+                const uint32_t sc = sbase + C::OFF_KSC + ((kt + j) & 3) * 512 + 256 * w;
                 if constexpr (kE4M3) {
                     const int t = kt + j;
                     tile_wait_warp(BAR(T_SCALES + (t & 3)), parity(t >> 2), tw);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) s4[k] = lds128(sbase + C::OFF_KSC + (t & 3) * 512 + 256 * w + 16 * k);
                     const float f = reinterpret_cast<const float*>(smem + C::OFF_VFAC)[t & 3];
                     if (j == 0) vfac = f;
                     if (f != vfac) grown = vfac / f;
@@ -660,6 +659,10 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 for (int n = 0; n < kN; ++n) {
                     if (!mine(n)) continue;
                     const int buf = tiles == 2 ? tile(n) : (buf0 + j) & 1;
+                    if (kE4M3) {   // read while the scores are formed
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) s4[k] = lds128(sc + 16 * k);
+                    }
                     const uint32_t tS = tbase + 128u * (uint32_t)buf + (kE4M3 ? 64u * (uint32_t)w : 0u);
                     const bool ready = tile_wait_warp(BAR(T_S_FULL + 2 * o_of(n) + buf), parity((buf ? use1 : use0) + (tiles == 2 ? j : j >> 1)), tw);
                     (void)ready;   // after a wait that ran out, values that nobody uses
@@ -679,9 +682,11 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                                 smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? n : slot)) * 128 + row];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const ptx::f2 a = ptx::mul2({y[4 * k], y[4 * k + 1]}, {__uint_as_float(s4[k].x), __uint_as_float(s4[k].y)});
-                            const ptx::f2 b = ptx::mul2({y[4 * k + 2], y[4 * k + 3]}, {__uint_as_float(s4[k].z), __uint_as_float(s4[k].w)});
+                            const uint4 f = s4[k & 7];
+                            const ptx::f2 a = ptx::mul2({y[4 * k], y[4 * k + 1]}, {__uint_as_float(f.x), __uint_as_float(f.y)});
+                            const ptx::f2 b = ptx::mul2({y[4 * k + 2], y[4 * k + 3]}, {__uint_as_float(f.z), __uint_as_float(f.w)});
                             y[4 * k] = a.x, y[4 * k + 1] = a.y, y[4 * k + 2] = b.x, y[4 * k + 3] = b.y;
+                            if (k < 8) s4[k] = lds128(sc + 128 + 16 * k);
                         }
                     }
                     if (key < full_lo[n] || key + kCols > full_hi[n]) {
