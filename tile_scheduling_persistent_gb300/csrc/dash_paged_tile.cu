@@ -819,10 +819,17 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     } else if (kE4M3) {
         ptx::setmaxnreg_dec<C::kRegsConv>();
         // ================================================== converters
-        constexpr int kChunks = D / 16;         // 16-byte chunks of codes per key
-        constexpr int kRows = 32 / kChunks;     // keys that one load instruction of a warp covers
+        constexpr int kRows = 512 / D;          // keys that one load instruction of a warp covers (16 codes a lane)
         constexpr int kLoads = 32 / kRows;      // loads of a warp's 32 keys of a tile
-        const int cw = warp - 12, chunk = lane % kChunks, sub = lane / kChunks;
+        // A lane's 16 codes become two 16-byte chunks of the fp16 row.  Eight consecutive lanes hold four chunk pairs of two
+        // neighbouring rows, whose swizzles differ in the lowest bit: no two of them meet in a bank.
+        const int cw = warp - 12;
+        const int chunk = D == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
+        const int sub = D == 128 ? ((lane >> 2) & 1) | (lane >> 4) << 1 : lane >> 2;
+        // offsets in a tile of the two chunks of key 32 cw + sub; kRows keys on, the row's swizzle flips chunk bit 2 (D = 128)
+        // or stays (D = 64)
+        const uint32_t line = (uint32_t)((2 * chunk) >> 3) * kBox + (uint32_t)(32 * cw + sub) * 128;
+        const uint32_t to0 = line + ((((2 * chunk) & 7) ^ (sub & 7)) << 4), to1 = line + ((((2 * chunk + 1) & 7) ^ (sub & 7)) << 4);
         TileItem it;
         bool ok = true;
         while (ok && next_item(it)) {
@@ -850,11 +857,23 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     cell[h] = ((long long)pg * p.c.Hkv + it.hk) * p.c.page_size + (key & (p.c.page_size - 1));
                 }
             };
-            auto load = [&](int l, const void* base) {
-                const int r = kRows * l + sub;   // of the warp's 32 keys
-                const int key = key0 + r;
-                if (key < it.lo || key >= it.hi) return make_uint4(0, 0, 0, 0);
-                return __ldg(reinterpret_cast<const uint4*>((const uint8_t*)base + (cell[l >= kLoads / 2] + (r & 15)) * D + 16 * chunk));
+            auto load = [&](const void* base, uint4 (&w)[kLoads]) {
+                const uint8_t* from[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) from[h] = (const uint8_t*)base + (cell[h] + sub) * D + 16 * chunk;
+                if (key0 >= it.lo && key0 + 32 <= it.hi) {
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l)
+                        w[l] = __ldg(reinterpret_cast<const uint4*>(from[l >= kLoads / 2] + (l & (kLoads / 2 - 1)) * (kRows * D)));
+                } else {   // keys outside the sequence's read as zero
+#pragma unroll
+                    for (int l = 0; l < kLoads; ++l) {
+                        const int key = key0 + kRows * l + sub;
+                        w[l] = make_uint4(0, 0, 0, 0);
+                        if (key >= it.lo && key < it.hi)
+                            w[l] = __ldg(reinterpret_cast<const uint4*>(from[l >= kLoads / 2] + (l & (kLoads / 2 - 1)) * (kRows * D)));
+                    }
+                }
             };
             // Scales of a key tile (they come with K): the key's own of K, those of this warp's keys of V, and the largest of
             // V so far, for which every warp reads the whole tile's.
@@ -895,21 +914,20 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     aim(it.t0 + (u + 1) / 2);
                     load_scales(it.t0 + (u + 1) / 2);
                 }
-                if (more) {
-                    const void* base = (u & 1) ? p.c.k : p.c.v;
-#pragma unroll
-                    for (int l = 0; l < kLoads; ++l) next[l] = load(l, base);
+                if (more) load((u & 1) ? p.c.k : p.c.v, next);
+                // fp16 parts of this lane's own key's scale (high part above, low part below)
+                uint32_t parts = 0;
+                if (u & 1) {
+                    const uint32_t hi = pack_half(scale, scale) & 0xffffu;
+                    parts = hi << 16 | (pack_half(scale - __half2float(__ushort_as_half((uint16_t)hi)), 0.f) & 0xffffu);
                 }
 #pragma unroll
                 for (int l = 0; l < kLoads; ++l) {
-                    const int row = 32 * cw + kRows * l + sub;
                     const uint32_t c4[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
                     uint32_t o[8];
                     if (u & 1) {
-                        const float sc = __shfl_sync(0xffffffffu, scale, kRows * l + sub);
-                        const uint32_t hi = pack_half(sc, sc);
-                        const float rest = sc - __half2float(__ushort_as_half((uint16_t)hi));
-                        const uint32_t lo = pack_half(rest, rest);
+                        const uint32_t both = __shfl_sync(0xffffffffu, parts, kRows * l + sub);
+                        const uint32_t hi = __byte_perm(both, 0u, 0x3232), lo = __byte_perm(both, 0u, 0x1010);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             o[2 * y] = scaled_codes(half_codes(c4[y], 0), hi, lo);
@@ -922,13 +940,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             o[2 * y + 1] = half_codes(c4[y], 1);
                         }
                     }
-                    // 16 values = two 16-byte chunks of the fp16 row; lanes of the upper half of a 128-value row store them
-                    // in the other order, which keeps the two boxes' banks apart
-                    const uint32_t line = dst + ((2 * chunk) >> 3) * kBox + row * 128;
-                    const int c0 = (2 * chunk) & 7, flip = (D == 128 && chunk >= 4) ? 1 : 0;
-                    const uint4 v0 = make_uint4(o[0], o[1], o[2], o[3]), v1 = make_uint4(o[4], o[5], o[6], o[7]);
-                    sts128(line + (((c0 + flip) ^ (row & 7)) << 4), flip ? v1 : v0);
-                    sts128(line + (((c0 + 1 - flip) ^ (row & 7)) << 4), flip ? v0 : v1);
+                    const uint32_t flip = D == 128 && (l & 1) ? 64u : 0u;
+                    sts128(((dst + to0) ^ flip) + l * kRows * 128, make_uint4(o[0], o[1], o[2], o[3]));
+                    sts128(((dst + to1) ^ flip) + l * kRows * 128, make_uint4(o[4], o[5], o[6], o[7]));
                 }
                 if (more && (u & 1)) use_scales();
                 ptx::fence_proxy_async_smem();
@@ -973,8 +987,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             uint4 wk[kLoads], wv[kLoads];
             aim(it.t0);
             load_scales(it.t0);
-#pragma unroll
-            for (int l = 0; l < kLoads; ++l) wk[l] = load(l, p.c.k);
+            load(p.c.k, wk);
             use_scales();
 #pragma unroll 1
             for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
