@@ -26,7 +26,11 @@
 // tile by columns (keys 0-63 and 64-127; a thread has one row of A and the
 // same row of B), which reads the scales once for both.  The price is one vote
 // of the 256 threads for each tile (does any row outgrow its maximum?); the
-// maxima themselves are exchanged only when one does.
+// maxima themselves are exchanged only when one does.  Measured against a
+// warpgroup for each row tile as for bf16 (the second 64 scores read twice, for
+// want of registers), Hq = 32, Hkv = 8: 16 x 5 tokens over about 5000 keys
+// 147 us against 165 (D = 128), 512 tokens over 8192 172 against 176, 2048 over
+// 8192 370 against 360, and with D = 64 280 against 282.
 //
 // Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
 // tensor memory, 2 item scheduler, 3 idle, 4-7 and 8-11 softmax and epilogue,
