@@ -382,7 +382,8 @@ typedef struct {
  *   (pos_stride_b = 0: shared by the batch), any value; NULL: s itself.
  *   inv_freq: HOST double [rot/2], radians per position; read before the call
  *   returns.  dash_rope_freqs fills it for the usual long-context scalings.
- *   D in {64, 128}, rot a multiple of 16, 16 <= rot <= D.
+ *   D in {64, 128}, rot a multiple of 16, 16 <= rot <= D; |inv_freq| < 1e12;
+ *   at most 65535 heads.
  * The angle is formed as a 64-bit fraction of a turn (position times the
  * frequency modulo one turn in integers), so far positions lose nothing; the
  * rotation is fp32, rounded once to y's type.
@@ -419,7 +420,8 @@ typedef enum { DASH_CACHE_BF16 = 0, DASH_CACHE_E4M3 = 1 } dash_cache_type;
  * A paged key/value cache: pages of page_size tokens, k and v each
  * [num_pages, Hkv, page_size, D].  DASH_CACHE_E4M3 holds e4m3 values with one
  * fp32 scale for each token and head, [num_pages, Hkv, page_size] (a cached
- * vector stands for code * scale); DASH_CACHE_BF16 has no scales (NULL).
+ * vector stands for code * scale; a scale is finite and not negative);
+ * DASH_CACHE_BF16 has no scales (NULL).  num_pages * Hkv < 2^31.
  * All contiguous device memory, 16-byte aligned.  page_size: 16, 32, 64, 128
  * or 256; D in {64, 128}.  Token offset o of page p is slot p*page_size + o.
  */
@@ -470,7 +472,7 @@ int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int64_t k_stri
  * block_table[b*table_stride + j / page_size] (device int32, max_pages entries
  * per sequence).  Rows j >= lens[b] are left as they were; so are rows of a
  * page outside the cache, or past max_pages (DASH_ERR_PAGE).  lens[b] > S
- * reads S rows.  stride_b/h/s are those of both outputs.
+ * reads S rows.  stride_b/h/s are those of both outputs.  S <= 2^30.
  * Returns DASH_OK (also for B or S = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t table_stride, int max_pages,
@@ -495,13 +497,18 @@ int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t
  *   q bf16 with strides; o bf16 [T, Hq, D] contiguous; lse fp32 [T, Hq]
  *   contiguous, or NULL; kv_lens int32 [B]; cu_q int32 [B+1], non-decreasing
  *   from 0, or NULL: T/B tokens of each sequence; block_table as dash_kv_read.
+ *   A stride of q may be 0 only where there is one token or one head.
  *   max_q: an upper bound on n that the host knows (it selects the kernels);
- *   Hq / Hkv at most 128.
+ *   Hq / Hkv at most 128; T * Hq < 2^31, max_pages * page_size < 2^31 - 512.
  *   workspace: device memory of at least dash_attn_paged_workspace bytes for
  *   the same B, T, Hq, Hkv, D, max_q and max_kv = max_pages * page_size,
  *   16-byte aligned, not shared with a call (or a captured graph's replay)
  *   that may run at the same time; its contents need no set-up and mean
  *   nothing afterwards.
+ * Weights are rounded to the type of the product they enter (bf16, fp16 for
+ * e4m3 caches) and o to bf16; scores, maxima and sums are fp32.  In sequences of
+ * more than 16 rows (n * Hq / Hkv) the values of an e4m3 cache are held to
+ * 2^-11 of themselves and 2^-31 of the largest value of the sequence's head.
  * How a sequence's keys are split over the GPU depends on its own lengths and
  * on Hq, Hkv and D alone: its outputs are the same bits whatever else is in
  * the batch, and from run to run.

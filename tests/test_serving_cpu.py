@@ -180,6 +180,18 @@ def test_workspace_refuses(L, a):
         dash.attn_paged_workspace(*a)
 
 
+def test_refuses_positions_off_their_alignment_and_outputs_past_2_30_rows(L):
+    x, y = heads(), heads(OK * 2)
+    assert L.dash_rope(ctypes.byref(x), ctypes.byref(y), None, None, OK + 2, 0, ctypes.cast(FREQ, P), 64, 0, 1.0, 0, 2, 4, 64,
+                       None) == dash.ERR_ARG
+    assert call_read(L, S=(1 << 30) + 1) == dash.ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(qs=(0, 64)), dict(qs=(256, 0))])
+def test_attn_refuses_queries_with_a_stride_of_zero(L, kw):
+    assert call_attn(L, **kw) == dash.ERR_ARG
+
+
 def test_status_refuses_null(L):
     assert L.dash_get_status_paged(None, None, None) == dash.ERR_ARG
 

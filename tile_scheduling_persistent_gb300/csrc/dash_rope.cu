@@ -444,7 +444,7 @@ extern "C" int dash_rope(const dash_heads* x, const dash_heads* y, const dash_he
                          int interleaved, float factor, int inverse, int B, int S, int D, dash_stream_t stream) {
     if (!x || !y || !x2 != !y2) return DASH_ERR_ARG;
     if (B < 0 || S < 0 || !rope_args_ok(inv_freq, rot, interleaved, factor, D) || (inverse != 0 && inverse != 1) ||
-        pos_stride_b < 0)
+        pos_stride_b < 0 || ((uintptr_t)positions & 3u))
         return DASH_ERR_ARG;
     if (B == 0 || S == 0) return DASH_OK;
     RopeParams prm;
@@ -578,7 +578,7 @@ extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_tab
                             int64_t stride_h, int64_t stride_s, int B, int S, dash_stream_t stream) {
     int rc = check_cache(cache);
     if (rc) return rc;
-    if (B < 0 || S < 0 || max_pages < 0 || table_stride < 0 || !serve_strides(stride_b, stride_h) ||
+    if (B < 0 || S < 0 || S > (1 << 30) || max_pages < 0 || table_stride < 0 || !serve_strides(stride_b, stride_h) ||
         !serve_strides(stride_s, 0))
         return DASH_ERR_ARG;
     if (B == 0 || S == 0) return DASH_OK;
