@@ -250,11 +250,11 @@ def test_scales_far_apart(n, D):
     check_attn(c, q, n, o, lse)
 
 
-@pytest.mark.parametrize("n", [[2, 1], [50, 70]])
+@pytest.mark.parametrize("n", [[1, 1], [2, 1], [50, 70]])
 @pytest.mark.parametrize("quant", [False, True])
 def test_queries_that_are_not_finite_stay_in_their_rows(n, quant):
     g = gen(43)
-    c = paged(g, [400, 333], 2, 128, 16, quant)
+    c = paged(g, [5000, 200], 2, 128, 16, quant)   # one split into key ranges, one not
     q = randn(g, sum(n), 8, 128)
     bad = [(0, 1), (0, 6), (sum(n) - 1, 3)]
     d = q.clone()
@@ -264,7 +264,7 @@ def test_queries_that_are_not_finite_stay_in_their_rows(n, quant):
     no_error()
     clean, clse = run_attn(c, q, n)
     for t, h in bad:
-        assert not bool(torch.isfinite(o[t, h]).all())
+        assert bool(torch.isnan(o[t, h]).any()) and bool(torch.isnan(lse[t, h]))   # as the formula has it
         o[t, h], lse[t, h] = clean[t, h], clse[t, h]
     check_attn(c, q, n, o, lse)
 

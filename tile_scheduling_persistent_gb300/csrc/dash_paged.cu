@@ -6,12 +6,13 @@
 // reading the cache once: 4 n G D operations against 2 * 2 D bytes per key and
 // head is at most 16 operations per byte, where the GPU has 285 per byte of
 // memory bandwidth.  So everything serves the stream of pages:
-//   - one persistent CTA per SM with two independent halves, each a producer
-//     warp and four consumers working through items of their own: while one
-//     half joins the results of an item or waits for the next one's queries,
-//     the other streams;
-//   - a half's producer walks its items and keeps a ring of 64-key stages (K
-//     and V, 64 KB) full by TMA, across item boundaries, each lane
+//   - one persistent CTA per SM with two or three independent groups, each a
+//     producer warp and four consumers working through items of their own:
+//     while one group joins the results of an item or waits for the next one's
+//     queries, the others stream.  Three groups need at most 128 registers a
+//     thread, which 16 query rows, or bf16 at D = 128, do not leave;
+//   - a group's producer walks its items and keeps a ring of 64-key stages (K
+//     and V, 50 or 64 KB) full by TMA, across item boundaries, each lane
 //     issuing one of a stage's copies (one per page, 64-value column and K/V:
 //     pages of 16 tokens give 16 copies);
 //   - each consumer warp takes 16 keys of a stage, all in registers, with the
@@ -111,7 +112,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 // The four consumer warps of one group.
-__device__ __forceinline__ void consumer_barrier(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ void consumer_barrier(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 
 // ---------------------------------------------------------------- few rows
 // kRowTiles: matrix tiles of 8 query rows; kGroups: independent groups of four consumer warps and a producer.
@@ -183,9 +184,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
     const uint32_t sbase = ptx::smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = warp < 4 * kGroups ? warp >> 2 : warp - 4 * kGroups;
-    const uint32_t ring = sbase + half * C::kStages * C::kStage;
-    const uint32_t bar_full = sbase + C::OFF_BAR + half * 16 * C::kStages, bar_empty = bar_full + 8 * C::kStages;
+    const int group = warp < 4 * kGroups ? warp >> 2 : warp - 4 * kGroups;
+    const uint32_t ring = sbase + group * C::kStages * C::kStage;
+    const uint32_t bar_full = sbase + C::OFF_BAR + group * 16 * C::kStages, bar_empty = bar_full + 8 * C::kStages;
 
     if (threadIdx.x == 128 * kGroups) {
         *abort = 0;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         const int sub = lane / kinds, kind = lane % kinds;
         const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
         int tc = 0;                                       // stages used so far
-        for (int item = half * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
+        for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
             walk.at(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
             const int e0 = max(it.t0 * kFewKeys, it.c.lo) >> p.page_shift;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * D, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
                     } else {
                         const float* src = (kind == 3 ? p.c.v_scale : p.c.k_scale) + (long long)head * page + y;
-                        bulk_load(sbase + C::OFF_SCALE + (((half * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src,
+                        bulk_load(sbase + C::OFF_SCALE + (((group * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src,
                                   rows * 4, full);
                     }
                 }
@@ -276,11 +277,11 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
     // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
     auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
-    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + half * 4 * C::kRows * C::kSlotRow;
-    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + half * 2 * 4 * C::kRows;
-    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + half * 4 * C::kRows;
+    float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + group * 4 * C::kRows * C::kSlotRow;
+    float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + group * 2 * 4 * C::kRows;
+    float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + group * 4 * C::kRows;
     int tc = 0, parity = 0;
-    for (int item = half * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
+    for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
         const int R = it.s.n * p.G;
         const int rt = kRowTiles == 1 || R <= 8 ? 1 : 2;   // row tiles of this item
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
             if (kE4M3) {
                 const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) +
-                                  (half * C::kStages + stage) * 2 * kFewKeys + 16 * ws + perm(g);
+                                  (group * C::kStages + stage) * 2 * kFewKeys + 16 * ws + perm(g);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     ks[n] = sc[8 * n];
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 for (int d = 4; d <= 16; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
                 if (g == 0) mp[ws * C::kRows + 8 * t + 2 * c4 + e] = m[t][e];
             }
-        consumer_barrier(half);
+        consumer_barrier(group);
         float* const slot = slots + ws * C::kRows * C::kSlotRow;
 #pragma unroll
         for (int t = 0; t < kRowTiles; ++t)
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     }
                 }
             }
-        consumer_barrier(half);
+        consumer_barrier(group);
         for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
             const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
             const int chunk = kE4M3 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
@@ -609,10 +610,10 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             }
             if (it.c.ns == 1) {
                 const int tok = it.s.first + r / p.G, h = it.hk * p.G + r % p.G;
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key; NaN stays NaN
                 *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
                     make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-                if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum > 0.f ? (top + log2f(sum)) * kLn2P : -INFINITY;
+                if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2P;
             } else {
                 const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * R + r;
                 if (row < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
@@ -771,13 +772,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
             __syncthreads();
         }
         if (real && (alone || warp == 0)) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;   // 0: no key; NaN stays NaN
             __nv_bfloat16* o = p.o + at * D + E * lane;
             if (E == 4)
                 *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[E - 2] * inv, a[E - 1] * inv));
             else
                 *reinterpret_cast<uint32_t*>(o) = pack_bf16(a[0] * inv, a[1] * inv);
-            if (p.lse && lane == 0) p.lse[at] = l > 0.f ? (top + log2f(l)) * kLn2P : -INFINITY;
+            if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2P;
         }
     }
     if ((int)blockIdx.x >= total) wait_dependency();

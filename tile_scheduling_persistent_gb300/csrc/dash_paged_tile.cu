@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 const bool split = it.split != 0;
                 const long long at = (long long)(it.tok + i) * p.Hq + it.hk * p.G + g;   // row of o and lse
                 const long long pr = it.part + (long long)i * p.G + g;
-                const bool empty = !(total[n] > 0.f);
+                const bool empty = total[n] == 0.f;   // no key; NaN stays NaN
                 const float inv = vfac * (split || empty ? 1.f : 1.f / total[n]);
                 const bool keep = split && valid[n] && pr < p.max_rows;
 #pragma unroll
