@@ -855,8 +855,9 @@ Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv)
     const long long few_q = G > kFewRows ? 0 : (max_q < kFewRows / G ? max_q : kFewRows / G);   // tokens of a few-rows sequence
     const long long n_few = nb < T ? nb : T;
     if (few_q > 0) {
-        const long long tiles = (max_kv + kFewKeys - 1) / kFewKeys, by_len = (tiles + kFewSplitTiles - 1) / kFewSplitTiles;
-        const long long ns = tiles <= kFewWholeTiles ? 1 : by_len < few_max_splits(Hkv) ? by_len : few_max_splits(Hkv);
+        const long long tiles = (max_kv + kFewKeys - 1) / kFewKeys;
+        const long long two = few_most_ranges(tiles, kFewWorkers, Hkv), three = few_most_ranges(tiles, kFewWorkers3, Hkv);
+        const long long ns = two > three ? two : three;
         r.few_items = n_few * Hkv * ns;
         if (ns > 1) r.rows += (few_q * n_few < T ? few_q * n_few : T) * Hq * ns;
     }

@@ -22,9 +22,9 @@ namespace dash {
 
 constexpr int kFewRows = 16;       // rows of one m16 matrix operand
 constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel
-constexpr int kFewSplitTiles = 2;  // at least this many stages per key range
 constexpr int kFewWholeTiles = 4;  // sequences of so many stages are not split: joining costs more than it gains
-constexpr int kFewWorkers = 304;   // two halves of a CTA on each of a GB300's 152 SMs
+constexpr int kFewWorkers = 304;   // groups on a GB300's 152 SMs: two of each CTA,
+constexpr int kFewWorkers3 = 456;  // or three
 constexpr int kMaxSeqs = 512;      // sequences per launch (their plan lies in shared memory)
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
 constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
@@ -95,24 +95,40 @@ __device__ __forceinline__ void seen_keys(const PagedParams& p, const Seq& s, in
 
 // The most key ranges of a sequence: the least number of rounds of all workers (at most 4) that one sequence's items
 // nearly fill (to 31/32), so that a long sequence alone, and any number of them, leave few workers idle in the last round.
-__host__ __device__ inline int few_max_splits(int Hkv) {
+__host__ __device__ inline int few_max_splits(int workers, int Hkv) {
     int best = 1, best_items = 0, best_rounds = 1;
     for (int rounds = 1; rounds <= 4; ++rounds) {
-        const int ns = kFewWorkers * rounds / Hkv, items = ns * Hkv;
+        const int ns = workers * rounds / Hkv, items = ns * Hkv;
         if (ns < 1) continue;
         if (items * best_rounds > best_items * rounds) best = ns, best_items = items, best_rounds = rounds;
-        if (items * 32 >= kFewWorkers * rounds * 31) break;
+        if (items * 32 >= workers * rounds * 31) break;
     }
     return best;
 }
 
-// Key ranges of a sequence: `tiles` key tiles of its class cut into ns ranges of st tiles.
-__host__ __device__ inline void few_split(int tiles, int Hkv, int& ns, int& st) {
-    const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(Hkv);
+// Workers that can serve a sequence of n tokens (launch_few's choice for a call of such sequences).
+__host__ __device__ inline int few_workers(int n, int G, int D, int type) {
+    return n * G <= 8 && (type == DASH_CACHE_E4M3 || D == 64) ? kFewWorkers3 : kFewWorkers;
+}
+
+// Key ranges of a sequence: `tiles` stages cut into ns ranges of st stages.  A range costs its start, its queries and its
+// share of the join: short ones serve a lone sequence, long ones a batch, whose other sequences fill the GPU.  Measured
+// (us; Hq = 32, Hkv = 8, D = 128, e4m3; 1000 / 4000 / 8192 keys alone, 64 ragged sequences to 8192, 256 to 2000) with at
+// least 2 stages: 8.5 12.0 13.3 127 159; 4: 10.1 10.8 13.4 112 125; 8: 12.7 12.0 13.1 100 114; 16: 17.1 16.6 16.6 98 115.
+__host__ __device__ inline void few_split(int tiles, int workers, int Hkv, int& ns, int& st) {
+    const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, Hkv);
+    const int least = tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
     st = (tiles + most - 1) / most;
-    st = st < kFewSplitTiles ? kFewSplitTiles : st;
+    st = st < least ? least : st;
     ns = (tiles + st - 1) / st;
     ns = ns < 1 ? 1 : ns;
+}
+
+// The most that few_split gives for up to `tiles` stages.
+__host__ inline long long few_most_ranges(long long tiles, int workers, int Hkv) {
+    const long long by_len = tiles <= kFewWholeTiles ? 1 : tiles < 16 ? (tiles + 1) / 2 : tiles < 64 ? 8 : (tiles + 7) / 8;
+    const long long most = few_max_splits(workers, Hkv);
+    return by_len < most ? by_len : most;
 }
 
 // The launch's plan in shared memory: sequences, and running counts.
@@ -133,7 +149,7 @@ __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     Cut c;
     seen_keys(p, s, 0, s.n, c.lo, c.hi);
     c.tiles = c.hi > c.lo ? (c.hi - 1) / kFewKeys - c.lo / kFewKeys + 1 : 0;
-    few_split(c.tiles, p.c.Hkv, c.ns, c.st);
+    few_split(c.tiles, few_workers(s.n, p.G, p.c.D, p.c.type), p.c.Hkv, c.ns, c.st);
     c.items = p.c.Hkv * c.ns;
     return c;
 }
