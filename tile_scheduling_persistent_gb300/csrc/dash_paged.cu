@@ -862,12 +862,12 @@ Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv)
         if (ns > 1) r.rows += (few_q * n_few < T ? few_q * n_few : T) * Hq * ns;
     }
     if ((long long)max_q * G > kFewRows) {
-        const long long ns = max_kv / kTileSplitKeys + 2;
+        const long long by_kv = max_kv / kTileSplitKeys + 2, by_heads = kTileSms / Hkv;   // ranges of a sequence
+        const long long ns = by_kv < by_heads ? by_kv : by_heads;
         const long long least = kFewRows / G + 1;                       // tokens of the smallest many-rows sequence
         const long long n_many = T / least < nb ? T / least : nb;
-        // a split sequence has at most (2 * kTileFullItems + its items) items of kTileRows rows
-        const long long each = 3ll * kTileFullItems * kTileRows;
-        const long long by_items = n_many * each, by_len = T * Hq * (ns < 2 * kTileFullItems ? ns : 2 * kTileFullItems);
+        // a split sequence has at most kTileSms items, of at most kTileRows rows
+        const long long by_items = n_many * kTileSms * kTileRows, by_len = ns > 1 ? T * Hq * ns : 0;
         r.rows += by_items < by_len ? by_items : by_len;
     }
     return r;

@@ -28,7 +28,7 @@ constexpr int kFewWorkers3 = 456;  // or three
 constexpr int kMaxSeqs = 512;      // sequences per launch (their plan lies in shared memory)
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
 constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
-constexpr int kTileFullItems = 76;     // items that keep the GPU busy without a split
+constexpr int kTileSms = 152;          // items of one round of the many-rows kernel: a CTA on each SM
 constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
 
 struct Plan;
@@ -154,20 +154,27 @@ __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     return c;
 }
 
-// Many rows: key ranges of whole 128-key tiles of the sequence; row tiles of kTileRows rows.
+// Many rows: a sequence of `full` (row tile, head) pairs over `tiles` key tiles alone on the GPU is cut into as many key
+// ranges as one round of all SMs holds; never into a second round that is part empty: 256 and 512 new tokens over 8192
+// and 16384 keys (Hq = 32, Hkv = 8, D = 128) took 67 and 160 us with as many items as fill two rounds, 49 and 122 us so.
+// And only where that gains a sixteenth, in twentieths of a microsecond (a key tile 1.8 us, an item 3 us, joining 3 us and
+// 0.05 us for each item): to a batch, which fills the GPU anyway, ranges are a cost.
+__host__ __device__ inline int many_split(int tiles, long long full) {
+    const int most = (tiles + kTileSplitKeys / 128 - 1) / (kTileSplitKeys / 128);
+    if (most <= 1 || 2 * full > kTileSms) return 1;
+    const int want = kTileSms / (int)full, ns = want < most ? want : most;
+    const int split = (tiles + ns - 1) / ns * 36 + 60 + 60 + (int)full * ns, whole = tiles * 36 + 60;
+    return 16 * split < 15 * whole ? ns : 1;
+}
+
+// Key ranges of whole 128-key tiles of the sequence; row tiles of kTileRows rows.
 __device__ __forceinline__ Cut cut_many(const PagedParams& p, const Seq& s, int tokens_per_tile) {
     Cut c;
     seen_keys(p, s, 0, s.n, c.lo, c.hi);
     c.tiles = c.hi > c.lo ? (c.hi - 1) / 128 - c.lo / 128 + 1 : 0;
     const int row_tiles = (s.n + tokens_per_tile - 1) / tokens_per_tile;
     const long long full = (long long)row_tiles * p.c.Hkv;
-    c.ns = 1;
-    if (full < kTileFullItems) {
-        const int want = (int)((2 * kTileFullItems + full - 1) / full);
-        const int most = (c.tiles + kTileSplitKeys / 128 - 1) / (kTileSplitKeys / 128);
-        c.ns = want < most ? want : most;
-        c.ns = c.ns < 1 ? 1 : c.ns;
-    }
+    c.ns = many_split(c.tiles, full);
     c.st = (c.tiles + c.ns - 1) / c.ns;
     c.ns = c.st > 0 ? (c.tiles + c.st - 1) / c.st : 1;
     c.items = (int)full * c.ns;
