@@ -445,22 +445,16 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     if (key < it.c.lo || key >= it.c.hi) lv[n] = 0.f;
                 }
             }
-            // running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8
-            float mx[kRowTiles][2], mw[kRowTiles][2];
+            // Running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8.  Whether one does needs a
+            // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
             for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (t >= rt) continue;
-                    mx[t][e] = fmaxf(s[t][e], s[t][2 + e]);
-                    mw[t][e] = kE4M3 ? fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) : 0.f;
-#pragma unroll
-                    for (int d = 4; d <= 16; d <<= 1) {
-                        mx[t][e] = fmaxf(mx[t][e], __shfl_xor_sync(0xffffffffu, mx[t][e], d));
-                        if (kE4M3) mw[t][e] = fmaxf(mw[t][e], __shfl_xor_sync(0xffffffffu, mw[t][e], d));
-                    }
-                    raise = raise || mx[t][e] > m[t][e] + 8.f || (kE4M3 && mw[t][e] > mv[t][e] + 8.f);
+                    raise = raise || fmaxf(s[t][e], s[t][2 + e]) > m[t][e] + 8.f;
+                    if (kE4M3) raise = raise || fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) > mv[t][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -469,7 +463,13 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float nm = fmaxf(m[t][e], mx[t][e]), nv = kE4M3 ? fmaxf(mv[t][e], mw[t][e]) : nm;
+                        float mx = fmaxf(s[t][e], s[t][2 + e]), mw = kE4M3 ? fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) : 0.f;
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) {
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                            if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
+                        }
+                        const float nm = fmaxf(m[t][e], mx), nv = kE4M3 ? fmaxf(mv[t][e], mw) : nm;
                         l[t][e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[t][e] - nm);
                         f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - nv);
                         m[t][e] = nm;
