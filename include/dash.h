@@ -507,7 +507,7 @@ int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t
  *   nothing afterwards.
  * Weights are rounded to the type of the product they enter (bf16, fp16 for
  * e4m3 caches) and o to bf16; scores, maxima and sums are fp32.  In sequences of
- * more than 16 rows (n * Hq / Hkv) the values of an e4m3 cache are held to
+ * more than 32 rows (n * Hq / Hkv) the values of an e4m3 cache are held to
  * 2^-11 of themselves and 2^-31 of the largest value of the sequence's head.
  * How a sequence's keys are split over the GPU depends on its own lengths and
  * on Hq, Hkv and D alone: its outputs are the same bits whatever else is in

@@ -2,15 +2,15 @@
 // paged key/value cache (dash_attn_paged): the entry points, the kernel for
 // sequences with few rows, and the kernel that joins key ranges.
 //
-// Few rows (n * G <= 16: decoding, a drafted token or two).  The work is
-// reading the cache once: 4 n G D operations against 2 * 2 D bytes per key and
-// head is at most 16 operations per byte, where the GPU has 285 per byte of
-// memory bandwidth.  So everything serves the stream of pages:
+// Few rows (decoding, a few drafted tokens; few_most).  The work is reading the
+// cache once: 4 n G D operations against 2 * 2 D bytes per key and head is at
+// most 16 operations per byte, where the GPU has 285 per byte of memory
+// bandwidth.  So everything serves the stream of pages:
 //   - one persistent CTA per SM with two or three independent groups, each a
-//     producer warp and four consumers working through items of their own:
-//     while one group joins the results of an item or waits for the next one's
-//     queries, the others stream.  Three groups need at most 128 registers a
-//     thread, which 16 query rows, or bf16 at D = 128, do not leave;
+//     producer warp and four consumers working through items of their own (8
+//     query rows, a key/value head, a key range): while one group joins the
+//     results of an item or waits for the next one's queries, the others
+//     stream.  bf16 at D = 128 has shared memory for two;
 //   - a group's producer walks its items and keeps a ring of 64-key stages (K
 //     and V, 50 or 64 KB) full by TMA, across item boundaries, each lane
 //     issuing one of a stage's copies (one per page, 64-value column and K/V:
@@ -18,12 +18,20 @@
 //   - each consumer warp takes 16 keys of a stage, all in registers, with the
 //     keys (and the values' columns) on the 16-row side of m16n8k16 and the
 //     query rows on its 8-column side: S^T = K Q^T, a running maximum and sum
-//     per column, O^T += V^T P^T.  One such pair of products covers 8 query
-//     rows (kRowTiles = 2 covers 16); with the rows on the 16-row side, half
-//     of the work would go to rows that a group of 8 heads does not have.  The
-//     wider tcgen05 tiles (128 rows, 4 or 8 of them real) have nothing to add;
+//     per column, O^T += V^T P^T.  With the rows on the 16-row side, half of the
+//     work would go to rows that a group of 8 heads does not have.  The wider
+//     tcgen05 tiles (128 rows, 4 or 8 of them real) have nothing to add;
+//   - more than 8 rows are several items over the same pages, one after another
+//     in the order of items, so that all but the first find them in L2.  Two
+//     such products in one item halve the reads from L2 and leave registers for
+//     two groups only: 16 e4m3 sequences of 16 rows to 5000 keys took 53 us so,
+//     43 us as two items (bf16: 71 and 75 us for 64 sequences at D = 64);
 //   - at the end of an item the four warps' (O, m, l) are joined in shared
 //     memory in a fixed order.
+// Measured (Hq = 32, Hkv = 8, D = 128): 64 e4m3 sequences of 1 to 8192 tokens
+// 102 us with the join, 5.5 TB/s; two bf16 sequences of 131071 (Hkv = 16) 298 us,
+// 7.2 TB/s, as fast as memory goes; one of 1000 tokens 8.7 us.  With few or
+// ragged sequences the last round of items is what keeps it from the first two.
 //
 // e4m3 caches.  Codes become fp16 pairs in registers (exact: e4m3 has 3
 // fraction bits and exponents -9..8), so the products run in fp16: Q is scaled
@@ -115,10 +123,10 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 __device__ __forceinline__ void consumer_barrier(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 
 // ---------------------------------------------------------------- few rows
-// kRowTiles: matrix tiles of 8 query rows; kGroups: independent groups of four consumer warps and a producer.
-template <int D, bool kE4M3, int kRowTiles, int kGroups>
+// kGroups: independent groups of four consumer warps and a producer.
+template <int D, bool kE4M3, int kGroups>
 struct FewCfg {
-    static constexpr int kRows = 8 * kRowTiles;
+    static constexpr int kRows = kFewRows;
     static constexpr int kThreads = kGroups * 160;
     static constexpr int kElem = kE4M3 ? 1 : 2;
     static constexpr int kHalfStage = kFewKeys * D * kElem;   // K, then V
@@ -141,7 +149,7 @@ struct FewCfg {
 struct FewItem {
     Seq s;
     Cut c;
-    int b, hk, split, t0, t1;   // key tiles [t0, t1)
+    int b, hk, split, r0, t0, t1;   // first row; key tiles [t0, t1)
 };
 
 // The items of one CTA in ascending order: sequence b and the item in it.
@@ -152,7 +160,10 @@ struct ItemWalk {
         it.s = plan.seq[b];
         it.c = cut_few(p, it.s);
         it.b = p.b0 + b;
-        const int local = item - plan.items[b];
+        int local = item - plan.items[b];   // the parts of a head and range one after another: they share its cells in L2
+        const int at = local / it.c.parts;
+        it.r0 = kFewRows * (local - at * it.c.parts);
+        local = at;
         it.split = local / p.c.Hkv;
         it.hk = local - it.split * p.c.Hkv;
         const int first = it.c.lo / kFewKeys;
@@ -176,9 +187,9 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-template <int D, bool kE4M3, int kRowTiles, int kGroups>
+template <int D, bool kE4M3, int kGroups>
 __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
-    using C = FewCfg<D, kE4M3, kRowTiles, kGroups>;
+    using C = FewCfg<D, kE4M3, kGroups>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 
     // ================================================== consumers
     // Fragment of a lane: g = lane / 4, c = lane % 4.  S^T and P^T: keys g and g + 8 of the warp's 16, query rows
-    // 8 t + 2c and + 1; O^T: columns of the values as commented below, the same query rows.
+    // 2c and 2c + 1; O^T: columns of the values as commented below, the same query rows.
     const int g = lane >> 2, c4 = lane & 3;
     const int ws = warp & 3;
     // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
@@ -283,75 +294,66 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     int tc = 0, parity = 0;
     for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
         walk.at(p, plan, item, it);
-        const int R = it.s.n * p.G;
-        const int rt = kRowTiles == 1 || R <= 8 ? 1 : 2;   // row tiles of this item
+        const int all = it.s.n * p.G, R = min(all - it.r0, kFewRows);   // rows of the sequence, and of this item
         // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
-        int hi[kRowTiles][2], lo[kRowTiles][2], full_lo, full_hi, skip;
+        int hi[2], lo[2], full_lo, full_hi, skip;
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = min(8 * t + 2 * c4 + e, R - 1) / p.G;
-                seen_keys(p, it.s, i, i + 1, lo[t][e], hi[t][e]);
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int i = (it.r0 + min(2 * c4 + e, R - 1)) / p.G;
+            seen_keys(p, it.s, i, i + 1, lo[e], hi[e]);
+        }
         seen_keys(p, it.s, 0, 1, skip, full_hi);
         seen_keys(p, it.s, it.s.n - 1, it.s.n, full_lo, skip);
 
-        // Q^T: row 8 t + g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3
-        uint32_t qf[kRowTiles][D / 16][2];
-        float qs[kRowTiles][2];   // scale of the scores of rows 8 t + 2c + e (log2 units)
+        // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3
+        uint32_t qf[D / 16][2];
+        float qs[2];   // scale of the scores of rows 2c + e (log2 units)
+        const int r = it.r0 + min(g, R - 1);
+        const __nv_bfloat16* q =
+            p.q + (long long)(it.s.first + r / p.G) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
+        if (!kE4M3) {
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t) {
-            const int r = min(8 * t + g, R - 1);
-            const __nv_bfloat16* q =
-                p.q + (long long)(it.s.first + r / p.G) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
-            if (!kE4M3) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    qf[t][k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
-                    qf[t][k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
-                }
-                qs[t][0] = qs[t][1] = p.scale_log2e;
-            } else {
-                float top = 0.f;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
-                    qf[t][k][0] = w.x;
-                    qf[t][k][1] = w.y;
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
-                                           fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
-                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                const float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-                qs[t][0] = __shfl_sync(0xffffffffu, down, 8 * c4);
-                qs[t][1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t w = qf[t][k][x];
-                        qf[t][k][x] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                    }
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
+                qf[k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
             }
+            qs[0] = qs[1] = p.scale_log2e;
+        } else {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
+                qf[k][0] = w.x;
+                qf[k][1] = w.y;
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
+                                       fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            const float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+            qs[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
+            qs[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t w = qf[k][x];
+                    qf[k][x] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                }
         }
 
-        float o[kRowTiles][D / 16][4], m[kRowTiles][2], mv[kRowTiles][2], l[kRowTiles][2];
+        float o[D / 16][4], m[2], mv[2], l[2];
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t) {
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[t][e] = mv[t][e] = -INFINITY;
-                l[t][e] = 0.f;
-            }
+        for (int e = 0; e < 2; ++e) {
+            m[e] = mv[e] = -INFINITY;
+            l[e] = 0.f;
         }
 
         for (int kt = it.t0; kt < it.t1; ++kt, ++tc) {
@@ -377,11 +379,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 __syncwarp();
             }
 
-            float s[kRowTiles][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
+            float s[4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
 #pragma unroll
-            for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[e] = 0.f;
             if (!kE4M3) {
                 const int row = 16 * ws + (lane & 15);
 #pragma unroll
@@ -389,9 +389,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     uint32_t a[4];
                     const int chunk = 2 * (k & 3) + (lane >> 4);
                     ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
-#pragma unroll
-                    for (int t = 0; t < kRowTiles; ++t)
-                        if (t < rt) mma16816<false>(s[t], a, qf[t][k][0], qf[t][k][1]);
+                    mma16816<false>(s, a, qf[k][0], qf[k][1]);
                 }
             } else {
 #pragma unroll
@@ -409,9 +407,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t a[4] = {half2_of_e4m3(w[0][x], 0), half2_of_e4m3(w[1][x], 0), half2_of_e4m3(w[0][x], 1),
                                                half2_of_e4m3(w[1][x], 1)};
-#pragma unroll
-                        for (int t = 0; t < kRowTiles; ++t)
-                            if (t < rt) mma16816<true>(s[t], a, qf[t][4 * h + x][0], qf[t][4 * h + x][1]);
+                        mma16816<true>(s, a, qf[4 * h + x][0], qf[4 * h + x][1]);
                     }
                 }
             }
@@ -428,20 +424,16 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 }
             }
 #pragma unroll
-            for (int t = 0; t < kRowTiles; ++t)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) s[t][2 * n + e] *= kE4M3 ? qs[t][e] * ks[n] : qs[t][e];
+                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n] : qs[e];
             if (edge) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int key = key0 + 8 * n + perm(g);
 #pragma unroll
-                    for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (key < lo[t][e] || key >= hi[t][e]) s[t][2 * n + e] = -INFINITY;
+                    for (int e = 0; e < 2; ++e)
+                        if (key < lo[e] || key >= hi[e]) s[2 * n + e] = -INFINITY;
                     if (key < it.c.lo || key >= it.c.hi) lv[n] = 0.f;
                 }
             }
@@ -449,62 +441,51 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
-            for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (t >= rt) continue;
-                    raise = raise || fmaxf(s[t][e], s[t][2 + e]) > m[t][e] + 8.f;
-                    if (kE4M3) raise = raise || fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) > mv[t][e] + 8.f;
-                }
+            for (int e = 0; e < 2; ++e) {
+                raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + 8.f;
+                if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + 8.f;
+            }
             if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int t = 0; t < kRowTiles; ++t) {
-                    if (t >= rt) continue;
-                    float f[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(s[t][e], s[t][2 + e]), mw = kE4M3 ? fmaxf(s[t][e] + lv[0], s[t][2 + e] + lv[1]) : 0.f;
-#pragma unroll
-                        for (int d = 4; d <= 16; d <<= 1) {
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                            if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
-                        }
-                        const float nm = fmaxf(m[t][e], mx), nv = kE4M3 ? fmaxf(mv[t][e], mw) : nm;
-                        l[t][e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[t][e] - nm);
-                        f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - nv);
-                        m[t][e] = nm;
-                        mv[t][e] = nv;
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[t][j][0] *= f[0];
-                        o[t][j][1] *= f[1];
-                        o[t][j][2] *= f[0];
-                        o[t][j][3] *= f[1];
-                    }
-                }
-            }
-            uint32_t pb[kRowTiles][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
-#pragma unroll
-            for (int t = 0; t < kRowTiles; ++t) {
-                if (t >= rt) continue;
-                float w[4];
+                float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float mu = m[t][e] == -INFINITY ? 0.f : m[t][e], vu = mv[t][e] == -INFINITY ? 0.f : mv[t][e];
+                    float mx = fmaxf(s[e], s[2 + e]), mw = kE4M3 ? fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) : 0.f;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float x = s[t][2 * n + e];
-                        const float pr = ptx::ex2(x - mu);
-                        l[t][e] += pr;
-                        w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n] - vu)) : pr;
+                    for (int d = 4; d <= 16; d <<= 1) {
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
                     }
+                    const float nm = fmaxf(m[e], mx), nv = kE4M3 ? fmaxf(mv[e], mw) : nm;
+                    l[e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
+                    f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - nv);
+                    m[e] = nm;
+                    mv[e] = nv;
                 }
-                // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    pb[t][n] = transposed8x8(kE4M3 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
+                for (int j = 0; j < D / 16; ++j) {
+                    o[j][0] *= f[0];
+                    o[j][1] *= f[1];
+                    o[j][2] *= f[0];
+                    o[j][3] *= f[1];
+                }
             }
+            uint32_t pb[2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = mv[e] == -INFINITY ? 0.f : mv[e];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float x = s[2 * n + e];
+                    const float pr = ptx::ex2(x - mu);
+                    l[e] += pr;
+                    w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n] - vu)) : pr;
+                }
+            }
+            // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                pb[n] = transposed8x8(kE4M3 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
 
             if (!kE4M3) {   // tile j of O^T: value columns 16j + g and + 8
                 const int row = 16 * ws + (lane & 7) + 8 * (lane >> 4);
@@ -513,9 +494,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     uint32_t a[4];
                     const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
                     ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
-#pragma unroll
-                    for (int t = 0; t < kRowTiles; ++t)
-                        if (t < rt) mma16816<false>(o[t][j], a, pb[t][0], pb[t][1]);
+                    mma16816<false>(o[j], a, pb[0], pb[1]);
                 }
             } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
@@ -539,9 +518,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         const uint32_t sel = z ? 0x7362u : 0x5140u;
                         const uint32_t lo2 = __byte_perm(w[0][y], w[1][y], sel), hi2 = __byte_perm(w[2][y], w[3][y], sel);
                         const uint32_t a[4] = {half2_of_e4m3(lo2, 0), half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 0), half2_of_e4m3(hi2, 1)};
-#pragma unroll
-                        for (int t = 0; t < kRowTiles; ++t)
-                            if (t < rt) mma16816<true>(o[t][2 * y + z], a, pb[t][0], pb[t][1]);
+                        mma16816<true>(o[2 * y + z], a, pb[0], pb[1]);
                     }
             }
             if (edge) ptx::fence_proxy_async_smem();   // the zeroed rows before the next copy into the stage
@@ -552,43 +529,39 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         // ---------------------------------------------- join the four warps
         float* const mp = mrow + parity * 4 * C::kRows;
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t)
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int d = 4; d <= 16; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
-                if (g == 0) mp[ws * C::kRows + 8 * t + 2 * c4 + e] = m[t][e];
-            }
+            for (int d = 4; d <= 16; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+            if (g == 0) mp[ws * C::kRows + 2 * c4 + e] = m[e];
+        }
         consumer_barrier(group);
         float* const slot = slots + ws * C::kRows * C::kSlotRow;
 #pragma unroll
-        for (int t = 0; t < kRowTiles; ++t)
+        for (int e = 0; e < 2; ++e) {
+            const int r = 2 * c4 + e;
+            if (r >= R) continue;   // rows past R hold copies; they are neither joined nor stored
+            float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * t + 2 * c4 + e;
-                if (r >= R) continue;   // rows past R hold copies; they are neither joined nor stored
-                float top = -INFINITY;
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
+            // outputs carry 2^-mv (weights with their scales), sums 2^-m
+            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top);
+            if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
+            float* row = slot + r * C::kSlotRow;
+            if (!kE4M3) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
-                // outputs carry 2^-mv (weights with their scales), sums 2^-m
-                const float fo = (top == -INFINITY || mv[t][e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[t][e] : m[t][e]) - top);
-                if (g == 0) lrow[ws * C::kRows + r] = l[t][e] * ((top == -INFINITY || m[t][e] == -INFINITY) ? 0.f : ptx::ex2(m[t][e] - top));
-                float* row = slot + r * C::kSlotRow;
-                if (!kE4M3) {
+                for (int j = 0; j < D / 16; ++j) {
+                    row[16 * j + g] = o[j][e] * fo;
+                    row[16 * j + g + 8] = o[j][2 + e] * fo;
+                }
+            } else {
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        row[16 * j + g] = o[t][j][e] * fo;
-                        row[16 * j + g + 8] = o[t][j][2 + e] * fo;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {   // values (D / 8) g + 4k..: the chunk XOR c spreads the banks
-                        const int chunk = ((D / 32) * g + k) ^ (D == 128 ? c4 : c4 >> 1);
-                        *reinterpret_cast<float4*>(row + 4 * chunk) =
-                            make_float4(o[t][2 * k][e] * fo, o[t][2 * k][2 + e] * fo, o[t][2 * k + 1][e] * fo, o[t][2 * k + 1][2 + e] * fo);
-                    }
+                for (int k = 0; k < D / 32; ++k) {   // values (D / 8) g + 4k..: the chunk XOR c spreads the banks
+                    const int chunk = ((D / 32) * g + k) ^ (D == 128 ? c4 : c4 >> 1);
+                    *reinterpret_cast<float4*>(row + 4 * chunk) =
+                        make_float4(o[2 * k][e] * fo, o[2 * k][2 + e] * fo, o[2 * k + 1][e] * fo, o[2 * k + 1][2 + e] * fo);
                 }
             }
+        }
         consumer_barrier(group);
         for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
             const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
@@ -609,13 +582,13 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 sum += lrow[w * C::kRows + r];
             }
             if (it.c.ns == 1) {
-                const int tok = it.s.first + r / p.G, h = it.hk * p.G + r % p.G;
+                const int tok = it.s.first + (it.r0 + r) / p.G, h = it.hk * p.G + (it.r0 + r) % p.G;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key; NaN stays NaN
                 *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
                     make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
                 if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2P;
             } else {
-                const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * R + r;
+                const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * all + it.r0 + r;
                 if (row < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
                     *reinterpret_cast<float4*>(p.part_o + row * D + 4 * q4) = a;
                     if (q4 == 0) p.part_ml[row] = make_float2(top, sum);
@@ -702,7 +675,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
         if (i >= p.nb) continue;
         seq[k] = load_seq(p, p.b0 + i, false);
         if (seq[k].n == 0) continue;
-        ns_[k] = (few_rows(seq[k].n, p.G) ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G))).ns;
+        ns_[k] = (few_rows(seq[k].n, p.G, p.c.type) ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G))).ns;
         units += units_of(k);
         if (ns_[k] > 1) parts += seq[k].n * p.Hq * ns_[k];
     }
@@ -793,38 +766,30 @@ int sm_count() {
     return count[dev];
 }
 
-template <int D, bool kE4M3, int kRowTiles, int kGroups>
+template <int D, bool kE4M3, int kGroups>
 int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
-    using C = FewCfg<D, kE4M3, kRowTiles, kGroups>;
+    using C = FewCfg<D, kE4M3, kGroups>;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kRowTiles, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3, kRowTiles, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kE4M3, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-// Row tiles: 8 query rows are enough when no few-rows sequence of the call can have more (its rows are whole groups);
-// a row's bits are the same either way.  Three groups where their registers allow it.
+// Three groups where their registers and stages allow it (few_workers counts on it).
 int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
-    const int tokens = p.max_q < kFewRows / p.G ? p.max_q : kFewRows / p.G;
-    const bool two = tokens * p.G > 8;
-    if (p.c.type == DASH_CACHE_E4M3) {
-        if (p.c.D == 64)
-            return two ? launch_few_t<64, true, 2, 2>(p, many, max_items, s) : launch_few_t<64, true, 1, 3>(p, many, max_items, s);
-        return two ? launch_few_t<128, true, 2, 2>(p, many, max_items, s) : launch_few_t<128, true, 1, 3>(p, many, max_items, s);
-    }
-    if (p.c.D == 64)
-        return two ? launch_few_t<64, false, 2, 2>(p, many, max_items, s) : launch_few_t<64, false, 1, 3>(p, many, max_items, s);
-    return two ? launch_few_t<128, false, 2, 2>(p, many, max_items, s) : launch_few_t<128, false, 1, 2>(p, many, max_items, s);
+    if (p.c.type == DASH_CACHE_E4M3)
+        return p.c.D == 64 ? launch_few_t<64, true, 3>(p, many, max_items, s) : launch_few_t<128, true, 3>(p, many, max_items, s);
+    return p.c.D == 64 ? launch_few_t<64, false, 3>(p, many, max_items, s) : launch_few_t<128, false, 2>(p, many, max_items, s);
 }
 
 // As the kernel before it in the stream ends; its plan is made while that one runs.
@@ -844,7 +809,8 @@ int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-// Bounds that the host knows of a launch of nb sequences: items of the few-rows class, partial rows of both classes.
+// Bounds that the host knows of a launch of nb sequences, whatever the cache's type: items of the few-rows class, partial
+// rows of both classes.
 struct Bounds {
     long long few_items, rows;
 };
@@ -852,19 +818,23 @@ struct Bounds {
 Bounds bounds(int nb, long long T, int Hq, int Hkv, int max_q, long long max_kv) {
     const int G = Hq / Hkv;
     Bounds r{0, 0};
-    const long long few_q = G > kFewRows ? 0 : (max_q < kFewRows / G ? max_q : kFewRows / G);   // tokens of a few-rows sequence
+    const long long few_q = G > kFewMost ? 0 : (max_q < kFewMost / G ? max_q : kFewMost / G);   // tokens of a few-rows sequence
     const long long n_few = nb < T ? nb : T;
     if (few_q > 0) {
         const long long tiles = (max_kv + kFewKeys - 1) / kFewKeys;
-        const long long two = few_most_ranges(tiles, kFewWorkers, Hkv), three = few_most_ranges(tiles, kFewWorkers3, Hkv);
-        const long long ns = two > three ? two : three;
-        r.few_items = n_few * Hkv * ns;
+        long long ns = 1;   // whichever of few_workers and few_parts a sequence has
+        for (int parts = 1; parts <= kFewMost / kFewRows; ++parts)
+            for (int workers : {kFewWorkers, kFewWorkers3}) {
+                const long long most = few_most_ranges(tiles, workers, Hkv * parts);
+                ns = ns < most ? most : ns;
+            }
+        r.few_items = n_few * Hkv * ns * (kFewMost / kFewRows);
         if (ns > 1) r.rows += (few_q * n_few < T ? few_q * n_few : T) * Hq * ns;
     }
-    if ((long long)max_q * G > kFewRows) {
+    if ((long long)max_q * G > few_most(DASH_CACHE_BF16)) {
         const long long by_kv = max_kv / kTileSplitKeys + 2, by_heads = kTileSms / Hkv;   // ranges of a sequence
         const long long ns = by_kv < by_heads ? by_kv : by_heads;
-        const long long least = kFewRows / G + 1;                       // tokens of the smallest many-rows sequence
+        const long long least = few_most(DASH_CACHE_BF16) / G + 1;                       // tokens of the smallest many-rows sequence
         const long long n_many = T / least < nb ? T / least : nb;
         // a split sequence has at most kTileSms items, of at most kTileRows rows
         const long long by_items = n_many * kTileSms * kTileRows, by_len = ns > 1 ? T * Hq * ns : 0;
@@ -892,7 +862,7 @@ extern "C" int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, i
     if (B == 0 || T == 0) return DASH_OK;
     const Bounds b = bounds(B < kMaxSeqs ? B : kMaxSeqs, T, Hq, Hkv, max_q, max_kv);
     if (b.rows >= (1ll << 31) || b.few_items >= (1ll << 31)) return DASH_ERR_ARG;
-    const bool many = (long long)max_q * (Hq / Hkv) > kFewRows;
+    const bool many = (long long)max_q * (Hq / Hkv) > few_most(DASH_CACHE_BF16);
     if (b.rows || many) *bytes = kWsHeader + (size_t)b.rows * (D * sizeof(float) + sizeof(float2));
     return DASH_OK;
 }
@@ -959,7 +929,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
             prm.part_ml = (float2*)(prm.part_o + bd.rows * D);
             prm.max_rows = bd.rows;
         }
-        const bool many = (long long)max_q * prm.G > kFewRows;
+        const bool many = (long long)max_q * prm.G > few_most(cache->type);
         const int items = (int)(bd.few_items < 1 ? 1 : bd.few_items);   // at least one block: it checks the lengths
         rc = launch_few(prm, many, items, s);
         if (rc) return rc;

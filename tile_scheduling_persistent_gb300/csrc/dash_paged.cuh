@@ -5,8 +5,8 @@
 // A sequence with n new tokens has n * G rows per key/value head (row r is
 // token r / G, head r % G of the group: one row of queries reads the same keys
 // for the whole group).  Two classes, by the sequence's own size:
-//   few rows  (n * G <= 16): memory bound; items of (head, key range), dash_paged.cu
-//   many rows              : items of (head, row tile, key range), dash_paged_tile.cu
+//   few rows (few_most): memory bound; items of (8 rows, head, key range), dash_paged.cu
+//   many rows: items of (256 rows, head, key range), dash_paged_tile.cu
 // Every cut depends on the sequence's own lengths and on Hkv, G and D, never on
 // the rest of the batch or on the number of SMs, so that a sequence's results
 // are the same bits in any batch.
@@ -20,7 +20,8 @@
 
 namespace dash {
 
-constexpr int kFewRows = 16;       // rows of one m16 matrix operand
+constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel
+constexpr int kFewMost = 32;       // rows of a sequence of its class, at the most (few_most)
 constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel
 constexpr int kFewWholeTiles = 4;  // sequences of so many stages are not split: joining costs more than it gains
 constexpr int kFewWorkers = 304;   // groups on a GB300's 152 SMs: two of each CTA,
@@ -84,7 +85,13 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report
     return s;
 }
 
-__host__ __device__ inline bool few_rows(int n, int G) { return (long long)n * G <= kFewRows; }
+// The few-rows class ends where reading the pages once for every 8 rows (from L2 after the first time) costs more than
+// the many-rows kernel's 128-row products, mostly of rows that do not exist.  Measured (us; 16 sequences to 5000 keys,
+// Hq = 32, Hkv = 8; 5 tokens = 20 rows, 8 tokens = 32 rows, 12 tokens = 48 rows), few against many: e4m3, D = 128:
+// 60 / 76 / 109 against 95 / 98 / 98; D = 64: 43 / 55 / 73 against 62 / 63 / 65; bf16, D = 128: 74 / 95 / 132 against
+// 56 / 58 / 61.
+__host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_E4M3 ? kFewMost : 16; }
+__host__ __device__ inline bool few_rows(int n, int G, int type) { return (long long)n * G <= few_most(type); }
 
 // Keys [lo, hi) that rows i0 .. i1 - 1 (tokens) of a sequence see.
 __device__ __forceinline__ void seen_keys(const PagedParams& p, const Seq& s, int i0, int i1, int& lo, int& hi) {
@@ -95,10 +102,10 @@ __device__ __forceinline__ void seen_keys(const PagedParams& p, const Seq& s, in
 
 // The most key ranges of a sequence: the least number of rounds of all workers (at most 4) that one sequence's items
 // nearly fill (to 31/32), so that a long sequence alone, and any number of them, leave few workers idle in the last round.
-__host__ __device__ inline int few_max_splits(int workers, int Hkv) {
+__host__ __device__ inline int few_max_splits(int workers, int heads) {
     int best = 1, best_items = 0, best_rounds = 1;
     for (int rounds = 1; rounds <= 4; ++rounds) {
-        const int ns = workers * rounds / Hkv, items = ns * Hkv;
+        const int ns = workers * rounds / heads, items = ns * heads;
         if (ns < 1) continue;
         if (items * best_rounds > best_items * rounds) best = ns, best_items = items, best_rounds = rounds;
         if (items * 32 >= workers * rounds * 31) break;
@@ -106,17 +113,19 @@ __host__ __device__ inline int few_max_splits(int workers, int Hkv) {
     return best;
 }
 
-// Workers that can serve a sequence of n tokens (launch_few's choice for a call of such sequences).
-__host__ __device__ inline int few_workers(int n, int G, int D, int type) {
-    return n * G <= 8 && (type == DASH_CACHE_E4M3 || D == 64) ? kFewWorkers3 : kFewWorkers;
+__host__ __device__ inline int few_parts(int n, int G) { return (n * G + kFewRows - 1) / kFewRows; }
+
+// Groups that work through the items: three of a CTA, or two (launch_few).
+__host__ __device__ inline int few_workers(int D, int type) {
+    return type == DASH_CACHE_E4M3 || D == 64 ? kFewWorkers3 : kFewWorkers;
 }
 
 // Key ranges of a sequence: `tiles` stages cut into ns ranges of st stages.  A range costs its start, its queries and its
 // share of the join: short ones serve a lone sequence, long ones a batch, whose other sequences fill the GPU.  Measured
 // (us; Hq = 32, Hkv = 8, D = 128, e4m3; 1000 / 4000 / 8192 keys alone, 64 ragged sequences to 8192, 256 to 2000) with at
 // least 2 stages: 8.5 12.0 13.3 127 159; 4: 10.1 10.8 13.4 112 125; 8: 12.7 12.0 13.1 100 114; 16: 17.1 16.6 16.6 98 115.
-__host__ __device__ inline void few_split(int tiles, int workers, int Hkv, int& ns, int& st) {
-    const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, Hkv);
+__host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st) {
+    const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, heads);
     const int least = tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
     st = (tiles + most - 1) / most;
     st = st < least ? least : st;
@@ -143,14 +152,16 @@ struct Cut {
     int lo, hi;                // keys seen by any row (few rows), tiles of them
     int tiles, ns, st;
     int items;                 // items of the sequence
+    int parts;                 // few rows: items that share a head and a key range
 };
 
 __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     Cut c;
     seen_keys(p, s, 0, s.n, c.lo, c.hi);
     c.tiles = c.hi > c.lo ? (c.hi - 1) / kFewKeys - c.lo / kFewKeys + 1 : 0;
-    few_split(c.tiles, few_workers(s.n, p.G, p.c.D, p.c.type), p.c.Hkv, c.ns, c.st);
-    c.items = p.c.Hkv * c.ns;
+    c.parts = few_parts(s.n, p.G);
+    few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * c.parts, c.ns, c.st);
+    c.items = p.c.Hkv * c.ns * c.parts;
     return c;
 }
 
@@ -199,7 +210,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool
         if (k >= per || t0 + k >= p.nb) continue;
         seq[k] = load_seq(p, p.b0 + t0 + k, report);
         if (seq[k].n == 0) continue;
-        const bool f = few_rows(seq[k].n, p.G);
+        const bool f = few_rows(seq[k].n, p.G, p.c.type);
         const Cut c = f ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G));
         count[k][0] = f ? c.items : 0;
         count[k][1] = f ? 0 : c.items;
