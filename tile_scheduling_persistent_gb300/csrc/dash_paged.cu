@@ -3,9 +3,9 @@
 // sequences with few rows, and the kernel that joins key ranges.
 //
 // Few rows (decoding, a few drafted tokens; few_most).  The work is reading the
-// cache once: 4 n G D operations against 2 * 2 D bytes per key and head is at
-// most 16 operations per byte, where the GPU has 285 per byte of memory
-// bandwidth.  So everything serves the stream of pages:
+// cache once: 4 n G D operations against 4 D bytes per key and head (2 D for
+// e4m3) is 16 and 64 operations per byte at the most, where the GPU has 285 per
+// byte of memory bandwidth.  So everything serves the stream of pages:
 //   - one persistent CTA per SM with two or three independent groups, each a
 //     producer warp and four consumers working through items of their own (8
 //     query rows, a key/value head, a key range): while one group joins the
