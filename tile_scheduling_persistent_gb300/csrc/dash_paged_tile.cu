@@ -114,10 +114,11 @@ template <int D, bool kE4M3>
 struct TileCfg {
     static constexpr int kTile = D * 128 * 2;
     static constexpr int kNBox = D / 64;
+    static constexpr bool kOwn = kE4M3 && D == 64;   // an O for each half of a tile's keys (tensor memory has room for four)
     static constexpr int OFF_Q = 0;                                  // A, B
     static constexpr int OFF_KV = 2 * kTile;
-    static constexpr int OFF_MAX = OFF_KV + kKvStages * kTile;       // [column half][128 rows] fp32
-    static constexpr int OFF_SUM = OFF_MAX + 2 * 128 * 4;            // [A, B][column half][128 rows] fp32
+    static constexpr int OFF_MAX = OFF_KV + kKvStages * kTile;       // [A, B][column half][128 rows] fp32
+    static constexpr int OFF_SUM = OFF_MAX + 4 * 128 * 4;            // the same
     static constexpr int OFF_QFAC = OFF_SUM + 4 * 128 * 4;           // e4m3: [2 items][A, B][128] fp32, 2^-a of each row
     static constexpr int OFF_KSC = OFF_QFAC + (kE4M3 ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
     static constexpr int OFF_VFAC = OFF_KSC + (kE4M3 ? 4 * 128 * 4 : 0);        // [4 tiles] the factor of V
@@ -266,7 +267,7 @@ __device__ __forceinline__ void product_pv(uint32_t leader, uint32_t d_tmem, uin
     constexpr uint32_t idesc = ptx::idesc_bf16(128, D, 0, 1) & ~(kHalf ? kBf16Bits : 0u);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-        mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, h + kk > 0 ? 1u : acc);
+        mma_ts_if(leader, d_tmem, p_tmem + h * 64 + kk * 8, v_lo + (uint32_t)((4 * h + kk) * 2048 >> 4), idesc, kk > 0 ? 1u : acc);
 }
 // A vote of the 256 softmax threads; also their barrier.
 __device__ __forceinline__ bool any_of_256(bool v) {
@@ -440,14 +441,15 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             auto values = [&](int buf, int x, int u, int j, int use) -> bool {
                 const uint32_t d = tmem + 256 + 128 * x, a = tmem + 128 * buf, b = stage(u) + kDescMn;
                 if (!tile_wait_warp(BAR(T_P_READY + 2 * buf), parity(use), tw)) return false;
-                if (kE4M3 && !tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
+                // e4m3, one O: both warpgroups have scaled it by then
+                if (kE4M3 && !C::kOwn && !tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
                 ptx::tc_fence_after();
                 product_pv<D, kE4M3>(leader, d, a, b, 0, j > 0 ? 1u : 0u);
-                if (!kE4M3) {
+                if (!kE4M3 || C::kOwn) {
                     if (!tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
                     ptx::tc_fence_after();
                 }
-                product_pv<D, kE4M3>(leader, d, a, b, 1, 1u);
+                product_pv<D, kE4M3>(leader, d + (C::kOwn ? 64 : 0), a, b, 1, !C::kOwn || j > 0 ? 1u : 0u);
                 return true;
             };
             if (kE4M3) {
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t out0 = 256u + (kE4M3 ? (uint32_t)(kOut * w) : 0u);
+        const uint32_t out0 = 256u + (kE4M3 ? (uint32_t)((C::kOwn ? 64 : kOut) * w) : 0u);   // of O, what this warpgroup scales
         float* const mx_own = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * w + row;
         float* const mx_other = reinterpret_cast<float*>(smem + C::OFF_MAX) + 128 * (w ^ 1) + row;
         for (int u = 0;; ++u) {
@@ -716,9 +718,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     for (int k = 8; k < kCols; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
                     float mx = c[n] * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                     const bool over = valid[n] && mx > m_ref[n] + 8.f;
-                    const bool raise = kE4M3 ? any_of_256(over || grown != 1.f) : __any_sync(0xffffffffu, over);
+                    const bool raise = kE4M3 && !C::kOwn ? any_of_256(over || grown != 1.f) : __any_sync(0xffffffffu, over || grown != 1.f);
                     if (raise) {
-                        if (kE4M3) {
+                        if (kE4M3 && !C::kOwn) {
                             *mx_own = mx;
                             any_of_256(false);
                             mx = fmaxf(mx, *mx_other);
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             if (tiles == 1) tile_wait_warp(BAR(T_PV_DONE), parity(pv + j - 1), tw);
                             ptx::tc_fence_after();
 #pragma unroll 1
-                            for (int cc = 0; cc < kOut / 16; ++cc) {
+                            for (int cc = 0; cc < (C::kOwn ? D : kOut) / 16; ++cc) {
                                 const uint32_t tO = tbase + out0 + 128u * (uint32_t)o_of(n) + (uint32_t)(16 * cc);
                                 uint32_t r[16];
                                 ptx::tmem_ld16(tO, r);
@@ -770,16 +772,31 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     l[n] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
             }
-            float total[kN];
+            float total[kN], part0[kN], part1[kN];   // the row's sum; with an O for each half of the keys, what each is multiplied by
 #pragma unroll
-            for (int n = 0; n < kN; ++n) total[n] = l[n];
-            if constexpr (kE4M3) {   // the rows' sums over both halves of the columns, in one order
+            for (int n = 0; n < kN; ++n) total[n] = l[n], part0[n] = part1[n] = 1.f;
+            if constexpr (kE4M3) {   // over both halves of the columns, in one order
                 float* const sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+                float* const tops = reinterpret_cast<float*>(smem + C::OFF_MAX);
 #pragma unroll
-                for (int n = 0; n < 2; ++n) sums[(2 * n + w) * 128 + row] = l[n];
+                for (int n = 0; n < 2; ++n) {
+                    sums[(2 * n + w) * 128 + row] = l[n];
+                    if (C::kOwn) tops[(2 * n + w) * 128 + row] = m_ref[n];
+                }
                 any_of_256(false);
 #pragma unroll
-                for (int n = 0; n < 2; ++n) total[n] = sums[2 * n * 128 + row] + sums[(2 * n + 1) * 128 + row];
+                for (int n = 0; n < 2; ++n) {
+                    const int at = 2 * n * 128 + row;
+                    if (C::kOwn) {
+                        m_ref[n] = fmaxf(tops[at], tops[at + 128]);
+                        const float mu = m_ref[n] == -INFINITY ? 0.f : m_ref[n];
+                        part0[n] = ptx::ex2(tops[at] - mu);
+                        part1[n] = ptx::ex2(tops[at + 128] - mu);
+                        total[n] = part0[n] * sums[at] + part1[n] * sums[at + 128];
+                    } else {
+                        total[n] = sums[at] + sums[at + 128];
+                    }
+                }
             }
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
@@ -801,6 +818,14 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     uint32_t r[32];
                     if (nk > 0) {
                         ptx::tmem_ld32(tbase + 256u + 128u * (uint32_t)o + (uint32_t)col, r);
+                        if constexpr (C::kOwn) {
+                            uint32_t r1[32];
+                            ptx::tmem_ld32(tbase + 256u + 128u * (uint32_t)o + 64u + (uint32_t)col, r1);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                r[k] = __float_as_uint(part0[n] * __uint_as_float(r[k]) + part1[n] * __uint_as_float(r1[k]));
+                        }
                         ptx::tmem_ld_wait();
                     }
 #pragma unroll
