@@ -51,8 +51,9 @@ int make_tmap_2d(void* map_out, const void* base, long long rows, int D);
 int make_tmap_3d(void* map_out, const void* base, long long heads, int S, int D);
 // Cache pages [heads][page][D] (heads: pages times key/value heads), bf16 in
 // boxes of 64 columns, e4m3 in boxes of D columns (swizzled rows of 128 or 64
-// bytes), `rows` rows high.
-int make_tmap_pages(void* map_out, const void* base, long long heads, int page, int D, bool e4m3, int rows);
+// bytes), `rows` rows high; of K and of V.
+int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, bool e4m3,
+                    int rows);
 // Packed query rows [T][Hkv][G][D] bf16 with strides (elements) of tokens and
 // heads: boxes of 64 columns, the G heads of one group, `tokens` tokens.
 int make_tmap_rows(void* map_out, const void* base, int T, long long stride_t, int Hkv, int G, long long stride_h,

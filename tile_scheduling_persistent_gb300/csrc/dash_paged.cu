@@ -792,21 +792,12 @@ int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
     return p.c.D == 64 ? launch_few_t<64, false, 3>(p, many, max_items, s) : launch_few_t<128, false, 2>(p, many, max_items, s);
 }
 
-// As the kernel before it in the stream ends; its plan is made while that one runs.
+// Its plan is made while the kernel before it in the stream runs.
 template <int D>
 int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    cfg.gridDim = dim3((unsigned)(max_rows < 6ll * sms ? max_rows : 6ll * sms));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    return launch_after(combine_kernel<D>, (unsigned)(max_rows < 6ll * sms ? max_rows : 6ll * sms), 256, 0, p, s);
 }
 
 // Bounds that the host knows of a launch of nb sequences, whatever the cache's type: items of the few-rows class, partial
@@ -914,8 +905,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     prm.scale_log2e = (1.0f / sqrtf((float)D)) * kLog2eP;
     const bool e4m3 = cache->type == DASH_CACHE_E4M3;
     const int rows = cache->page_size < kFewKeys ? cache->page_size : kFewKeys;
-    if (make_tmap_pages(&prm.tm_k, cache->k, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows) ||
-        make_tmap_pages(&prm.tm_v, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows))
+    if (make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows))
         return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {

@@ -281,6 +281,22 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int ent
     return page;
 }
 
+// Starts as the kernel before it in the stream ends, for which it waits itself (wait_dependency).
+inline int launch_after(void (*kernel)(const PagedParams), unsigned grid, unsigned threads, size_t smem, const PagedParams& p,
+                        cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
 int launch_paged_many(const PagedParams& p, int max_items, cudaStream_t s);   // dash_paged_tile.cu
 
 }  // namespace dash

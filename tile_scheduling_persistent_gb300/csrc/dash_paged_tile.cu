@@ -1052,8 +1052,7 @@ int launch_tile_t(const PagedParams& p, int grid, cudaStream_t s) {
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
-    paged_tile_kernel<D, kE4M3><<<grid, C::kThreads, C::kSmem, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    return launch_after(paged_tile_kernel<D, kE4M3>, grid, C::kThreads, C::kSmem, p, s);
 }
 
 }  // namespace
@@ -1065,8 +1064,8 @@ int launch_paged_many(const PagedParams& few, int grid, cudaStream_t s) {
     const int rows = p.c.page_size < 128 ? p.c.page_size : 128;
     const long long heads = (long long)p.c.num_pages * p.c.Hkv;
     const bool e4m3 = p.c.type == DASH_CACHE_E4M3;
-    if ((!e4m3 && (make_tmap_pages(&p.tm_k, p.c.k, heads, p.c.page_size, p.c.D, false, rows) ||
-                   make_tmap_pages(&p.tm_v, p.c.v, heads, p.c.page_size, p.c.D, false, rows))) ||
+    // (pages up to the few-rows kernel's stages have its maps)
+    if ((!e4m3 && rows > kFewKeys && make_tmap_pages(&p.tm_k, &p.tm_v, p.c.k, p.c.v, heads, p.c.page_size, p.c.D, false, rows)) ||
         make_tmap_rows(&p.tm_q, p.q, p.T, p.q_t, p.c.Hkv, p.G, p.q_h, p.c.D, 128 / p.G))
         return DASH_ERR_CUDA;
     if (e4m3) return p.c.D == 64 ? launch_tile_t<64, true>(p, grid, s) : launch_tile_t<128, true>(p, grid, s);
