@@ -1,5 +1,7 @@
 """Rotary positions, the paged cache and its attention used together, as a server and a training step use them, and
 calls at the edges of what is documented."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -291,6 +293,60 @@ def test_two_graphs_share_a_workspace():
         graphs[i].replay()
         assert same(calls[i][4], calls[i][3])
     no_error()
+
+
+def test_the_bindings_own_workspace():
+    # threads on one stream, streams of one thread, and a replayed graph beside eager calls, all without a workspace of
+    # the caller's: nobody finds another's partial results in its own
+    c = paged(gen(50), [3000, 900, 2000], 2, 128, 16, True)
+    work = []
+    for n in ([1, 1, 1], [2, 150, 40], [3, 3, 9]):
+        q = randn(gen(51), sum(n), 16, 128).to(DEV)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device=DEV)
+        work.append((q, cu, max(n), run_attn(c, q, n)[0]))
+    torch.cuda.synchronize()
+
+    def call(i, o):
+        q, cu, m, _ = work[i]
+        dash.attn_paged(q, c.k_cache, c.v_cache, c.table, c.lens, o, cu_q=cu, max_q=m, **c.kw)
+
+    wrong = []
+
+    def thread(first):
+        outs = []
+        for k in range(30):
+            i = (first + k) % 3
+            outs.append((i, torch.full_like(work[i][0], 77.0)))
+            call(*outs[-1])
+        torch.cuda.synchronize()
+        wrong.extend(i for i, o in outs if not same(o, work[i][3]))
+
+    threads = [threading.Thread(target=thread, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    captured = torch.empty_like(work[1][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(1, captured)
+    side, eager = torch.cuda.Stream(), []
+    for k in range(20):
+        captured.fill_(77.0)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph.replay()
+        for i in range(3):
+            eager.append((i, torch.full_like(work[i][0], 77.0)))
+            call(*eager[-1])
+        torch.cuda.current_stream().wait_stream(side)
+        assert same(captured, work[1][3])
+    assert all(same(o, work[i][3]) for i, o in eager)
+    no_error()
+    dash.release_workspaces()
+    call(1, captured)
+    assert same(captured, work[1][3])
 
 
 @pytest.mark.parametrize("n", [[1, 1], [0, 60]])

@@ -10,6 +10,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 import numpy as np
 import torch
@@ -229,6 +230,7 @@ def set_timeout_ns(ns):
 
 
 def release_workspaces():
+    _kept.held = {}   # attn_paged's, of this thread
     _check(lib().dash_release_workspaces(), "dash_release_workspaces")
 
 
@@ -531,6 +533,26 @@ def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=Non
                               *ks, B, S, st), what)
 
 
+_KEPT_BYTES = 32 << 20
+_kept = threading.local()
+
+
+def _workspace(n, dev, st):
+    """n bytes for a call on the current stream st.  Up to _KEPT_BYTES are kept, for each thread and stream: an allocation
+    between launches costs 7 us, as much as all else in the call.  Calls of one thread on one stream run one after
+    another; a captured call, whose replays do not keep to its stream, gets memory of its graph's own."""
+    if n > _KEPT_BYTES or torch.cuda.is_current_stream_capturing():
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    try:
+        held = _kept.held
+    except AttributeError:
+        held = _kept.held = {}
+    w = held.get((dev, st))
+    if w is None or w.numel() < n:
+        w = held[dev, st] = torch.empty(max(n, 1 << 20), dtype=torch.uint8, device=dev)
+    return w
+
+
 @functools.lru_cache(maxsize=4096)   # a function of the sizes alone
 def attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv):
     """Bytes of workspace attn_paged needs; max_kv = pages per sequence * page_size."""
@@ -546,8 +568,9 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     tokens q [T, Hq, D] over its kv_lens[b] cached tokens, the new ones among them
     (see dash_attn_paged).  cu_q int32 [B+1] are the sequences' first rows (None:
     T / B rows each) and max_q bounds their new tokens (None: T with cu_q, else
-    T / B).  workspace: uint8 tensor of attn_paged_workspace bytes (None: taken
-    from torch's allocator for this call)."""
+    T / B).  workspace: uint8 tensor of attn_paged_workspace bytes (None: the
+    binding's own, kept for this thread and stream where it is small and the call
+    is not being captured; release_workspaces frees it)."""
     what = "dash_attn_paged"
     dev, st = _device_stream(stream, what)
     c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
@@ -572,7 +595,7 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
         wn, wp = attn_paged_workspace(B, T, Hq, Hkv, D, max_q, pages * page), None
         if wn:
             if stream is None:
-                workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
+                workspace = _workspace(wn, dev, st)
             else:
                 with torch.cuda.stream(stream):   # the allocator's reuse then follows this stream
                     workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
