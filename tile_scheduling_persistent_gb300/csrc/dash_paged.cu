@@ -148,29 +148,33 @@ struct FewCfg {
 
 struct FewItem {
     Seq s;
-    Cut c;
+    int lo, hi, ns;                 // keys seen by any row; key ranges
     int b, hk, split, r0, t0, t1;   // first row; key tiles [t0, t1)
 };
 
-// The items of one CTA in ascending order: sequence b and the item in it.
-struct ItemWalk {
-    int b = 0;
-    __device__ __forceinline__ void at(const PagedParams& p, const Plan& plan, int item, FewItem& it) {
-        while (plan.items[b + 1] <= item) ++b;
-        it.s = plan.seq[b];
-        it.c = cut_few(p, it.s);
-        it.b = p.b0 + b;
-        int local = item - plan.items[b];   // the parts of a head and range one after another: they share its cells in L2
-        const int at = local / it.c.parts;
-        it.r0 = kFewRows * (local - at * it.c.parts);
-        local = at;
-        it.split = local / p.c.Hkv;
-        it.hk = local - it.split * p.c.Hkv;
-        const int first = it.c.lo / kFewKeys;
-        it.t0 = first + it.split * it.c.st;
-        it.t1 = min(it.t0 + it.c.st, first + it.c.tiles);
-    }
-};
+// Item `item` of the launch; whole warps.  Its sequence is the last that begins at or before it, found by two votes over
+// the plan's counts: an item's step to the next spans tens of short sequences.
+__device__ __forceinline__ void find_item(const PagedParams& p, const Plan& plan, int item, FewItem& it) {
+    constexpr int kMark = kMaxSeqs / 32;
+    const int lane = threadIdx.x & 31;
+    const int mark = __popc(__ballot_sync(0xffffffffu, kMark * lane < p.nb && plan.items[kMark * lane] <= item)) - 1;
+    const int i = kMark * mark + lane;
+    const int b = kMark * mark + __popc(__ballot_sync(0xffffffffu, lane < kMark && i < p.nb && plan.items[i] <= item)) - 1;
+    it.s = plan.seq[b];
+    it.b = p.b0 + b;
+    const int st = plan.st[b], parts = few_parts(it.s.n, p.G);
+    seen_keys(p, it.s, 0, it.s.n, it.lo, it.hi);
+    const int first = it.lo / kFewKeys, tiles = it.hi > it.lo ? (it.hi - 1) / kFewKeys - first + 1 : 0;
+    it.ns = tiles <= st ? 1 : (tiles + st - 1) / st;
+    // the parts of a head and range come one after another: they share its cells in L2
+    const uint32_t local = (uint32_t)(item - plan.items[b]);
+    const int at = (int)(parts == 1 ? local : parts == 2 ? local / 2 : parts == 3 ? local / 3 : local / 4);
+    it.r0 = kFewRows * ((int)local - at * parts);
+    it.split = quick_div(at, p.c.Hkv, p.over_Hkv);
+    it.hk = at - it.split * p.c.Hkv;
+    it.t0 = first + it.split * st;
+    it.t1 = min(it.t0 + st, first + tiles);
+}
 
 // Waits for a phase, at most timeout_ns; after a wait that ran out (reported) nothing waits any more, so that every
 // role reaches its end.
@@ -214,7 +218,6 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     make_plan(p, plan, blockIdx.x == 0, many && blockIdx.x == 0 ? p.plan : nullptr);
     launch_dependents();
     const int items = plan.items[p.nb];
-    ItemWalk walk;
     FewItem it;
 
     if (warp >= 4 * kGroups) {
@@ -226,10 +229,10 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
-            walk.at(p, plan, item, it);
+            find_item(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
-            const int e0 = max(it.t0 * kFewKeys, it.c.lo) >> p.page_shift;
-            const int e1 = (min(it.t1 * kFewKeys, it.c.hi) - 1) >> p.page_shift;
+            const int e0 = max(it.t0 * kFewKeys, it.lo) >> p.page_shift;
+            const int e1 = (min(it.t1 * kFewKeys, it.hi) - 1) >> p.page_shift;
             int eb = (it.t0 * kFewKeys) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
             auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
             int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     next = fetch(eb + 32 + lane);
                 }
                 const int k0 = key + sub * rows;          // this lane's first key
-                const bool need = sub < subs && k0 + rows > it.c.lo && k0 < it.c.hi;
+                const bool need = sub < subs && k0 + rows > it.lo && k0 < it.hi;
                 const int pg = __shfl_sync(0xffffffffu, pages, ((k0 >> p.page_shift) - eb) & 31);
                 const int stage = tc % C::kStages;
                 const uint32_t full = bar_full + 8 * stage;
@@ -291,43 +294,54 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + group * 4 * C::kRows * C::kSlotRow;
     float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + group * 2 * 4 * C::kRows;
     float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + group * 4 * C::kRows;
+    // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3.  Loaded before the
+    // join of the item before, which hides the wait.
+    uint32_t qf[D / 16][2];
+    auto load_queries = [&](const FewItem& x) {
+        const int r = x.r0 + min(g, min(x.s.n * p.G - x.r0, kFewRows) - 1), i = quick_div(r, p.G, p.over_G);
+        const __nv_bfloat16* q = p.q + (long long)(x.s.first + i) * p.q_t + (long long)(x.hk * p.G + r - i * p.G) * p.q_h;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            if (!kE4M3) {
+                qf[k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
+                qf[k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
+                qf[k][0] = w.x;
+                qf[k][1] = w.y;
+            }
+        }
+    };
+    FewItem after;   // the next item
+    const int first_item = group * gridDim.x + blockIdx.x, step = kGroups * gridDim.x;
+    if (first_item < items) {
+        find_item(p, plan, first_item, after);
+        load_queries(after);
+    }
     int tc = 0, parity = 0;
-    for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x, parity ^= 1) {
-        walk.at(p, plan, item, it);
+    for (int item = first_item; item < items; item += step, parity ^= 1) {
+        it = after;
         const int all = it.s.n * p.G, R = min(all - it.r0, kFewRows);   // rows of the sequence, and of this item
         // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
         int hi[2], lo[2], full_lo, full_hi, skip;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int i = (it.r0 + min(2 * c4 + e, R - 1)) / p.G;
+            const int i = quick_div(it.r0 + min(2 * c4 + e, R - 1), p.G, p.over_G);
             seen_keys(p, it.s, i, i + 1, lo[e], hi[e]);
         }
         seen_keys(p, it.s, 0, 1, skip, full_hi);
         seen_keys(p, it.s, it.s.n - 1, it.s.n, full_lo, skip);
 
-        // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3
-        uint32_t qf[D / 16][2];
         float qs[2];   // scale of the scores of rows 2c + e (log2 units)
-        const int r = it.r0 + min(g, R - 1);
-        const __nv_bfloat16* q =
-            p.q + (long long)(it.s.first + r / p.G) * p.q_t + (long long)(it.hk * p.G + r % p.G) * p.q_h;
         if (!kE4M3) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qf[k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
-                qf[k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
-            }
             qs[0] = qs[1] = p.scale_log2e;
         } else {
             float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
-                qf[k][0] = w.x;
-                qf[k][1] = w.y;
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))),
-                                       fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u)))));
-            }
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[k][x] << 16)), fabsf(__uint_as_float(qf[k][x] & 0xffff0000u))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             const bool edge = key0 < full_lo || key0 + 16 > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
                 const int r = lane >> 1;
-                if (key0 + r < it.c.lo || key0 + r >= it.c.hi) {
+                if (key0 + r < it.lo || key0 + r >= it.hi) {
                     const int row = 16 * ws + r;
                     constexpr int kRow = D * C::kElem / 2;   // bytes per lane
 #pragma unroll
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         if (key < lo[e] || key >= hi[e]) s[2 * n + e] = -INFINITY;
-                    if (key < it.c.lo || key >= it.c.hi) lv[n] = 0.f;
+                    if (key < it.lo || key >= it.hi) lv[n] = 0.f;
                 }
             }
             // Running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8.  Whether one does needs a
@@ -526,6 +540,11 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
         }
 
+        if (item + step < items) {
+            find_item(p, plan, item + step, after);
+            load_queries(after);
+        }
+
         // ---------------------------------------------- join the four warps
         float* const mp = mrow + parity * 4 * C::kRows;
 #pragma unroll
@@ -581,8 +600,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 top = fmaxf(top, mp[w * C::kRows + r]);
                 sum += lrow[w * C::kRows + r];
             }
-            if (it.c.ns == 1) {
-                const int tok = it.s.first + (it.r0 + r) / p.G, h = it.hk * p.G + (it.r0 + r) % p.G;
+            if (it.ns == 1) {
+                const int token = quick_div(it.r0 + r, p.G, p.over_G), tok = it.s.first + token, h = it.hk * p.G + it.r0 + r - token * p.G;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key; NaN stays NaN
                 *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
                     make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
@@ -898,6 +917,8 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     prm.T = T;
     prm.Hq = Hq;
     prm.G = Hq / Hkv;
+    prm.over_G = reciprocal(prm.G);
+    prm.over_Hkv = reciprocal(Hkv);
     prm.max_q = max_q;
     prm.causal = causal;
     prm.window = window;

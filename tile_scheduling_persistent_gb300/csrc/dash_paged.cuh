@@ -51,12 +51,20 @@ struct PagedParams {
     unsigned long long timeout_ns;
     int b0, nb;                    // the launch's sequences
     int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
+    uint32_t over_G, over_Hkv;     // reciprocals (quick_div)
     float scale_log2e;
 };
 
 struct Seq {
     int first, n, len;             // n = 0: nothing to do
 };
+
+// x / d for launch constants d: floor(2^32 / d) + 1 times x, over 2^32, is exact while x * d < 2^32; 0 stands for no such
+// number (d = 1, or too large).  A division costs some 80 cycles of latency, and an item took six.
+inline uint32_t reciprocal(int d) { return d > 1 && d <= 4096 ? (uint32_t)((1ull << 32) / (unsigned)d) + 1u : 0u; }
+__device__ __forceinline__ int quick_div(int x, int d, uint32_t over) {
+    return over ? (int)__umulhi((uint32_t)x, over) : d == 1 ? x : x / d;
+}
 
 // What the device alone knows about sequence b, checked; report: this thread reports what is wrong.
 __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report) {
@@ -145,6 +153,7 @@ struct Plan {
     Seq seq[kMaxSeqs];
     int items[kMaxSeqs + 1];   // items of the class before each sequence
     int rows[kMaxSeqs + 1];    // partial rows before each sequence (both classes)
+    int st[kMaxSeqs];          // few rows: stages of a key range
     int warp_sum[3][16];
 };
 
@@ -203,15 +212,16 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool
     const int t0 = (int)threadIdx.x * per;
     constexpr int kPer = 2;
     Seq seq[kPer];
-    int count[kPer][3], own[3] = {0, 0, 0};   // items of few and of many rows, partial rows
+    int count[kPer][3], st[kPer], own[3] = {0, 0, 0};   // items of few and of many rows, partial rows
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        count[k][0] = count[k][1] = count[k][2] = 0;
+        count[k][0] = count[k][1] = count[k][2] = st[k] = 0;
         if (k >= per || t0 + k >= p.nb) continue;
         seq[k] = load_seq(p, p.b0 + t0 + k, report);
         if (seq[k].n == 0) continue;
         const bool f = few_rows(seq[k].n, p.G, p.c.type);
         const Cut c = f ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G));
+        st[k] = c.st;
         count[k][0] = f ? c.items : 0;
         count[k][1] = f ? 0 : c.items;
         count[k][2] = c.ns > 1 ? seq[k].n * p.Hq * c.ns : 0;
@@ -247,6 +257,7 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool
         const int i = t0 + k;
         if (k >= per || i >= p.nb) continue;
         plan.seq[i] = seq[k];
+        plan.st[i] = st[k];
         plan.items[i] = sum[0];
         plan.rows[i] = sum[2];
         if (many) {
