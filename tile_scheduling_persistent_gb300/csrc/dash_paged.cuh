@@ -131,7 +131,8 @@ __host__ __device__ inline int few_workers(int D, int type) {
 // Key ranges of a sequence: `tiles` stages cut into ns ranges of st stages.  A range costs its start, its queries and its
 // share of the join: short ones serve a lone sequence, long ones a batch, whose other sequences fill the GPU.  Measured
 // (us; Hq = 32, Hkv = 8, D = 128; 1000 bf16 keys, 4000 and 8192 e4m3 keys alone, 64 ragged e4m3 sequences to 8192, 256 to
-// 2000) with at least 2 stages: 8.5 12.0 13.3 127 159; 4: 10.1 10.8 13.4 112 125; 8: 12.7 12.0 13.1 100 114; 16: 17.1 16.6 16.6 98 115.
+// 2000), ranges of at least 2 stages: 8.3 11.8 15.1 136 149; 4: 9.6 10.3 13.2 107 117; 8: 12.5 11.7 12.7 99 109; 16: 17.6
+// 15.5 16.3 97 111; growing with the sequence, as here: 8.5 11.9 12.7 100 129.
 __host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st) {
     const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, heads);
     const int least = tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
