@@ -24,22 +24,25 @@
 // loop); the first half of P's keys is multiplied while the second is worked
 // out.  e4m3 caches: scaling the scores comes on top, so the two share every
 // tile by columns (keys 0-63 and 64-127; a thread has one row of A and the
-// same row of B), which reads the scales once for both.  The price is one vote
-// of the 256 threads for each tile (does any row outgrow its maximum?); the
-// maxima themselves are exchanged only when one does.  Measured against a
-// warpgroup for each row tile as for bf16 (the second 64 scores read twice, for
-// want of registers), Hq = 32, Hkv = 8: 16 x 5 tokens over about 5000 keys
-// 147 us against 165 (D = 128), 512 tokens over 8192 172 against 176, 2048 over
-// 8192 370 against 360, and with D = 64 280 against 282.
+// same row of B), which reads the scales once for both.  At D = 64 each half of
+// the keys has an O, a maximum and a sum of its own, joined in the epilogue; at
+// D = 128 tensor memory has room for one O, and its price is a vote of the 256
+// threads for each tile (does any row outgrow its maximum?); the maxima
+// themselves are exchanged only when one does.  (The votes cost 5% where they
+// can be left out: 272 against 259 us for 2048 tokens over 8192 at D = 64.)
+// Measured against a warpgroup for each row tile as for bf16 (the second 64
+// scores read twice, for want of registers), Hq = 32, Hkv = 8, both with votes:
+// 16 x 5 tokens over about 5000 keys 147 us against 165 (D = 128), 512 tokens
+// over 8192 172 against 176, 2048 over 8192 370 against 360, and with D = 64 280
+// against 282.
 //
 // Measured (Hq = 32, Hkv = 8): 4096 new tokens over 16384 keys, bf16, D = 128:
 // 636 us, 1510 TFLOP/s (63% of the tensor core's cycles; what is left is the
-// softmax warps' exponentials, 37% of theirs, between the products they wait
-// for); 2048 over 8192: 190 us bf16, 370 us e4m3 (conversion); 16 x 5 tokens over
-// to 5000 keys, bf16: 57 us, 3.1 TB/s (rounds of uneven items and their starts).
-// A step of 3 chunks of up to 700 tokens (D = 64, e4m3, window 4096) spends 140 of
-// its 193 us here, 19% of the exponential unit's cycles: each of the two
-// warpgroups scales, exponentiates and votes on both tiles in turn.
+// softmax between the products); 2048 over 8192: 190 us bf16, 370 us e4m3
+// (conversion); 16 x 5 tokens over to 5000 keys, bf16: 57 us, 3.1 TB/s (rounds of
+// uneven items and their starts).  2048 over 8192, D = 64, e4m3: 259 us, 2000
+// cycles for each matrix tile, of which the tensor core takes 512: 840 for the
+// exponentials, 550 to read and scale the scores, 200 to 400 waiting for them.
 //
 // Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
 // tensor memory, 2 item scheduler, 3 idle, 4-7 and 8-11 softmax and epilogue,
@@ -52,12 +55,13 @@
 // V holds code * scale, rounded once to fp16 (2^-11, against 2^-8 of the
 // output's bf16): a second scale for each column would cost the softmax as
 // much again as its exponentials, since its reads of shared memory wait behind
-// the tensor core's (K's are read once for A and B, while S is being formed).  fp16's range is met with powers of two, undone in fp32:
-// V by the largest scale so far in the item in [2^6, 2^7) (codes reach 448; when
+// the tensor core's (K's are read once for A and B, while S is being formed).
+// fp16's range is met with powers of two, undone in fp32: V by the largest scale so far in the item in [2^6, 2^7) (codes reach 448; when
 // it grows, O is rescaled as for a grown maximum), Q by row, its largest value
 // in [2^14, 2^15), converted in place.
 //
-// Tensor memory: S/P buffers at columns 0 and 128; O of A at 256, of B at 384.
+// Tensor memory: S/P buffers at columns 0 and 128; O of A at 256, of B at 384 (e4m3 at
+// D = 64: the second half of the keys 64 columns on).
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
