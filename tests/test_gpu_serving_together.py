@@ -253,11 +253,12 @@ def test_scales_far_apart(n, D):
 
 
 @pytest.mark.parametrize("n", [[1, 1], [2, 1], [50, 70]])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("quant", [False, True])
-def test_queries_that_are_not_finite_stay_in_their_rows(n, quant):
+def test_queries_that_are_not_finite_stay_in_their_rows(n, D, quant):
     g = gen(43)
-    c = paged(g, [5000, 200], 2, 128, 16, quant)   # one split into key ranges, one not
-    q = randn(g, sum(n), 8, 128)
+    c = paged(g, [5000, 200], 2, D, 16, quant)   # one split into key ranges, one not
+    q = randn(g, sum(n), 8, D)
     bad = [(0, 1), (0, 6), (sum(n) - 1, 3)]
     d = q.clone()
     for (t, h), x in zip(bad, (float("nan"), float("inf"), -float("inf"))):
