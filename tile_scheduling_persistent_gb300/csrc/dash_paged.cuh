@@ -28,7 +28,7 @@ constexpr int kFewWorkers = 304;   // groups on a GB300's 152 SMs: two of each C
 constexpr int kFewWorkers3 = 456;  // or three
 constexpr int kMaxSeqs = 512;      // sequences per launch (their plan lies in shared memory)
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
-constexpr int kTileSplitKeys = 1024;   // at least this many keys per range there
+constexpr int kTileSplitKeys = 768;    // at least this many keys per range there (many_split)
 constexpr int kTileSms = 152;          // items of one round of the many-rows kernel: a CTA on each SM
 constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
 
@@ -180,6 +180,8 @@ __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
 // and 16384 keys (Hq = 32, Hkv = 8, D = 128) took 67 and 160 us with as many items as fill two rounds, 49 and 122 us so.
 // And only where that gains a sixteenth, in twentieths of a microsecond (a key tile 1.8 us, an item 3 us, joining 3 us and
 // 0.05 us for each item): to a batch, which fills the GPU anyway, ranges are a cost.
+// The least range likewise (us; 1, 16 and 64 sequences of 5 tokens over 5000 or to 5000 bf16 keys, 40 e4m3 tokens over 929):
+// 512 keys 19.5 55.0 153 38, 768 keys 19.1 55.3 145 38, 1024 keys 22.6 54.1 142 44.
 __host__ __device__ inline int many_split(int tiles, long long full) {
     const int most = (tiles + kTileSplitKeys / 128 - 1) / (kTileSplitKeys / 128);
     if (most <= 1 || 2 * full > kTileSms) return 1;
