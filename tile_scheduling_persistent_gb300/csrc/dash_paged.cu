@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
     // this thread's sequences: units, partial rows, and the counts before
     Seq seq[kSeqs];
     int ns_[kSeqs], units = 0, parts = 0;
+    const int per = p.nb > 256 ? kSeqs : 1;
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) seq[k] = Seq{0, 0, 0}, ns_[k] = 1;
     auto units_of = [&](int k) {
@@ -690,8 +691,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
     };
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
-        const int i = kSeqs * threadIdx.x + k;
-        if (i >= p.nb) continue;
+        const int i = per * (int)threadIdx.x + k;
+        if (k >= per || i >= p.nb) continue;
         seq[k] = load_seq(p, p.b0 + i, false);
         if (seq[k].n == 0) continue;
         ns_[k] = (few_rows(seq[k].n, p.G, p.c.type) ? cut_few(p, seq[k]) : cut_many(p, seq[k], tokens_per_item(p.G))).ns;
