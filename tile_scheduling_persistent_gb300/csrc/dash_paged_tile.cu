@@ -80,8 +80,8 @@ constexpr int kItemSlots = 2;
 enum TileBar : int {
     T_Q_FULL = 0,                          // slots A, B
     T_Q_EMPTY = T_Q_FULL + 2,
-    T_Q_READY = T_Q_EMPTY + 2,             // e4m3: an item's queries are converted
-    T_KV_FULL,
+    T_Q_READY = T_Q_EMPTY + 2,             // e4m3: a slot's queries are converted (T_Q_EMPTY keeps its uses apart)
+    T_KV_FULL = T_Q_READY + 2,
     T_KV_EMPTY = T_KV_FULL + kKvStages,
     // [row tile or slot][buffer]: whoever waits for one of these sees every phase of it (parity cannot tell a phase from the
     // one after the next, and a warpgroup does not follow the items of the other)
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kE4M3 && (i == T_Q_READY || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
+            if (kE4M3 && ((i >= T_Q_READY && i < T_Q_READY + 2) || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
             if (i >= T_P_READY && i < T_P_READY + 4) count = 4;                                                         // a softmax warpgroup
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
@@ -456,13 +456,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 product_pv<D, kE4M3>(leader, d + (C::kOwn ? 64 : 0), a, b, 1, !C::kOwn || j > 0 ? 1u : 0u);
                 return true;
             };
-            if (kE4M3) {
-                ok = tile_wait_warp(BAR(T_Q_READY), parity(it.qi), tw);
-            } else {
-                for (int x = 0; ok && x < tiles; ++x) {
-                    const int q = tiles == 2 ? x : slot;
-                    ok = tile_wait_warp(BAR(T_Q_FULL + q), parity(pick(it.q_use, q)), tw);
-                }
+            for (int x = 0; ok && x < tiles; ++x) {
+                const int q = tiles == 2 ? x : slot;
+                ok = tile_wait_warp(BAR((kE4M3 ? T_Q_READY : T_Q_FULL) + q), parity(pick(it.q_use, q)), tw);
             }
             ok = ok && full(kv0);
             if (!ok) break;
@@ -1020,10 +1016,10 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                         sts128(at, make_uint4(pack_half(f[0] * up, f[1] * up), pack_half(f[2] * up, f[3] * up),
                                               pack_half(f[4] * up, f[5] * up), pack_half(f[6] * up, f[7] * up)));
                     }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY + q));
                 }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY));
                 return true;
             };
             uint4 wk[kLoads], wv[kLoads];
