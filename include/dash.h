@@ -505,10 +505,14 @@ int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t
  *   16-byte aligned, not shared with a call (or a captured graph's replay)
  *   that may run at the same time; its contents need no set-up and mean
  *   nothing afterwards.
- * Weights are rounded to the type of the product they enter (bf16, fp16 for
- * e4m3 caches) and o to bf16; scores, maxima and sums are fp32.  In sequences of
- * more than 32 rows (n * Hq / Hkv) the values of an e4m3 cache are held to
- * 2^-11 of themselves and 2^-31 of the largest value of the sequence's head.
+ * Weights are rounded to the type of the product they enter (bf16; fp16 for
+ * e4m3 caches, where each is held to 2^-11 of itself or 2^-32 of the row's
+ * largest -- in sequences of up to 32 rows, n * Hq / Hkv, of the largest product
+ * of a weight and its value's scale) and o to bf16; scores, maxima and sums are
+ * fp32.  With e4m3 caches a query's values are held to bf16's 8 bits down to
+ * 2^-29 of the largest of their row, and in sequences of more than 32 rows the
+ * cache's values to 2^-11 of themselves and 2^-31 of the largest value of the
+ * sequence's head.
  * How a sequence's keys are split over the GPU depends on its own lengths and
  * on Hq, Hkv and D alone: its outputs are the same bits whatever else is in
  * the batch, and from run to run.

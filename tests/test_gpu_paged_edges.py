@@ -34,3 +34,82 @@ def test_many_items_of_one_row_tile_and_one_key_tile(D, quant):
         again = run_attn(c, q, n)
         no_error()
         assert same(o, again[0]) and same(lse, again[1])
+
+
+def one_key_above_the_rest(c, above, q0, column):
+    """Token 0 of every sequence scores `above` powers of two over the others (its key lies along the queries' first value,
+    q0, which the other keys do not have); its value is zero (column None), or 64 in one column and zero in the others."""
+    D, page = c.k_cache.shape[3], c.k_cache.shape[2]
+    for b in range(len(c.k)):
+        ln = c.k[b].shape[0]
+        j = torch.arange(ln)
+        p, o = c.table[b].cpu().long()[j // page].to(DEV), (j % page).to(DEV)
+        k = torch.zeros(D, dtype=torch.float64)
+        k[0] = above * np.log(2.0) * np.sqrt(D) / q0
+        v = torch.zeros(D, dtype=torch.float64)
+        if column is not None:
+            v[column] = 64.0
+        raw_k, raw_v = c.k_cache.view(torch.uint8), c.v_cache.view(torch.uint8)
+        raw_k[p, :, o, 0] = 0
+        c.k[b][:, :, 0] = 0.0
+        for raw, scale, held, x in ((raw_k, c.k_scale, c.k, k), (raw_v, c.v_scale, c.v, v)):
+            s = max(float(torch.tensor(float(x.abs().max()) / 448.0, dtype=torch.float32)), 2.0 ** -126)
+            code = (x / s).to(torch.float32).to(torch.float8_e4m3fn)
+            raw[p[0], :, o[0]] = code.view(torch.uint8).to(DEV)
+            scale[p[0], :, o[0]] = s
+            held[b][0] = code.double().numpy() * s
+
+
+@pytest.mark.parametrize("n", [[1, 1], [5, 8], [9, 40], [33, 1]])   # four heads each: up to 8 tokens are few rows
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("above,column", [(16, None), (20, None), (24, None), (26, None), (16, 3), (20, 3)])
+def test_weights_far_below_the_largest(n, D, above, column):
+    # The first key takes nearly all of the weight and its value is zero, so the other keys, each 2^-above of it, are the
+    # whole output.  e4m3 caches' weights are fp16: with the largest lifted to 2^7 at least, each is off by 2^-11 of itself
+    # or, below fp16's least normal value, by 2^-25 in units of the largest over 2^7, that is 2^-32 of the largest weight:
+    #   2^-11 A                          weights
+    #   2^-32 sum |v|                    many rows: weights below 2^-14 in fp16
+    #   2^-32 max(P s) sum |v / s|       few rows: there the value's scale s is part of the weight
+    #   2^-11 A + 2^-31 max |v|          many rows: values
+    #   2^-10 A                          fp32 (see check_attn: scores here have absolute sums below 12 sqrt(D) too)
+    #   2^-8 |o|                         o's own rounding to bf16
+    g = gen(61)
+    c = paged(g, [1500, 700], 2, D, 16, True)
+    for b in range(2):   # values around one: their sum does not cancel
+        ln, page = c.k[b].shape[0], 16
+        j = torch.arange(ln)
+        p, o = c.table[b].cpu().long()[j // page].to(DEV), (j % page).to(DEV)
+        x = 1.0 + 0.25 * torch.randn(ln, 2, D, generator=g)
+        s = x.abs().amax(-1) / 448.0
+        code = (x / s[..., None]).to(torch.float8_e4m3fn)
+        c.v_cache.view(torch.uint8)[p, :, o] = code.view(torch.uint8).to(DEV)
+        c.v_scale[p, :, o] = s.to(DEV)
+        c.v[b][:] = code.double().numpy() * s.double().numpy()[..., None]
+    one_key_above_the_rest(c, above, 8.0, column)
+    q = randn(g, sum(n), 8, D)
+    q[:, :, 0] = 8.0
+    o, lse = run_attn(c, q, n)
+    no_error()
+    o, at = o.double().cpu().numpy(), 0
+    for b, m in enumerate(n):
+        ln, few = c.k[b].shape[0], m * 4 <= 32
+        x = q[at:at + m].double().numpy()
+        ro, rl = V.attend(x, c.k[b], c.v[b], ln - m)
+        A, _ = V.attend(x, c.k[b], np.abs(c.v[b]), ln - m)
+        page = 16
+        j = torch.arange(ln)
+        s = c.v_scale.cpu()[c.table[b].cpu().long()[j // page], :, j % page].double().numpy()      # [len, Hkv]
+        heads = np.arange(8) // 4
+        if few:
+            top, _ = V.attend(x, c.k[b], np.repeat(s[:, :, None], D, 2), ln - m)   # sum P s, at least max P s
+            small = 2.0 ** -32 * top * (np.abs(c.v[b]) / s[..., None]).sum(0)[heads]
+        else:
+            small = 2.0 ** -32 * np.abs(c.v[b]).sum(0)[heads] + 2.0 ** -31 * np.abs(c.v[b]).max((0, 2))[heads][:, None]
+        bound = (2.0 ** -11 * (1 if few else 2) + 2.0 ** -10) * A + 2.0 ** -8 * np.abs(ro) + small
+        d = np.abs(o[at:at + m] - ro)
+        if column is not None:   # that column is the first key's own value
+            assert (d[:, :, column] <= bound[:, :, column]).all()
+        assert (d <= bound).all(), "off by %.3g of its bound, %.3g of the value" % ((d / bound).max(), (d / np.abs(ro)).max())
+        got = lse[at:at + m].cpu().double().numpy()
+        assert (np.abs(got - rl) <= 2.0 ** -12 + 2.0 ** -20 * np.abs(rl)).all()
+        at += m

@@ -38,9 +38,10 @@
 // by a power of two per row so that its largest value lies in [2^14, 2^15) --
 // values down to 2^-29 of it keep bf16's 8 bits -- and the scale returns in
 // fp32 with the key's own scale: s = (Q 2^a . code) * ks * 2^-a.  The value's
-// scale vs joins the weight before it is rounded: w = 2^(s + log2 vs - m'),
+// scale vs joins the weight before it is rounded: w = 2^(s + log2 vs - m' + 7),
 // with m' the running maximum of s + log2 vs, so the largest contributions of
-// a row lie near 1 whatever the scales; the sum l keeps its own maximum m.
+// a row lie near 2^7 whatever the scales (kLiftE4M3); the sum l keeps its own
+// maximum m.
 //
 // Masked keys get s = -inf by a select, never by arithmetic, and value rows
 // outside the visible keys (stale or unwritten cells, freed pages) are zeroed
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = mv[e] == -INFINITY ? 0.f : mv[e];
+                const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = (mv[e] == -INFINITY ? 0.f : mv[e]) - kLiftE4M3;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const float x = s[2 * n + e];
@@ -562,8 +563,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
-            // outputs carry 2^-mv (weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top);
+            // outputs carry 2^-m (e4m3: 2^(lift - mv), weights with their scales), sums 2^-m
+            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] - kLiftE4M3 : m[e]) - top);
             if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
             float* row = slot + r * C::kSlotRow;
             if (!kE4M3) {

@@ -30,6 +30,10 @@ constexpr int kMaxSeqs = 512;      // sequences per launch (their plan lies in s
 constexpr int kTileRows = 256;     // rows per item of the many-rows kernel
 constexpr int kTileSplitKeys = 768;    // at least this many keys per range there (many_split)
 constexpr int kTileSms = 152;          // items of one round of the many-rows kernel: a CTA on each SM
+// e4m3 caches: weights become fp16 with 2^7 for the running maximum.  They exceed it by up to 2^8 before it is raised, and
+// 2^15 is fp16's last whole binade; downwards each is held to 2^-11 of itself until 2^-21 of the largest, and to 2^-32 of
+// the largest below.  (With 1 for the maximum, keys 2^24 below one whose value is small lost a fifth of their sum.)
+constexpr float kLiftE4M3 = 7.f;
 constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
 
 struct Plan;

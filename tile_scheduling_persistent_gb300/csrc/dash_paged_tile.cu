@@ -6,7 +6,8 @@
 // group.  An item is 2 matrix tiles of 128 / G tokens each (A and B, M = 128),
 // one key/value head and a range of 128-key tiles:
 //   S = Q K_j^T     (tcgen05, bf16, fp32 in tensor memory)
-//   P = 2^(scale log2e S - m), bf16 into the columns of S; l += row sums
+//   P = 2^(scale log2e S - m), bf16 (e4m3 caches: times 2^7, fp16) into the
+//                   columns of S; l += row sums
 //   O += P V_j      (A = P from tensor memory)
 // A persistent CTA takes items from a counter (which CTA runs an item does not
 // touch its bits).  The two tiles take turns: while the softmax warps work on
@@ -617,6 +618,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         // ================================================== softmax and epilogue
         // e4m3: this warpgroup w has keys 64 w .. of every key tile and columns D/2 w .. of O, of both row tiles (n = 0, 1);
         // bf16: everything of row tile w (n = 0).
+        constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.f;   // weights, l and O are relative to the maximum less this
         constexpr int kN = kE4M3 ? 2 : 1, kCols = kE4M3 ? 64 : 128, kOut = kE4M3 ? D / 2 : D;
         const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
@@ -746,9 +748,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             }
                         }
                     }
-                    const float m_use = m_ref[n] == -INFINITY ? 0.f : m_ref[n];
+                    const float m_use = (m_ref[n] == -INFINITY ? 0.f : m_ref[n]) - kLift;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    // P rounded to bf16 (e4m3 caches: fp16; at most 2^8), keys [0,64) -> columns [0,32), [64,128) -> [64,96)
+                    // P rounded to bf16 (at most 2^8; e4m3 caches: fp16, lifted, at most 2^15), keys [0,64) -> columns [0,32), [64,128) -> [64,96)
 #pragma unroll
                     for (int h = 0; h < kCols / 32; ++h) {
                         uint32_t pk[16];
@@ -846,9 +848,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 }
                 const bool stats = !kE4M3 || w == 0;
                 if (stats && keep)
-                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[n], empty ? 0.f : total[n]);
+                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[n] - kLift, empty ? 0.f : total[n]);
                 else if (stats && !split && valid[n] && p.lse)
-                    p.lse[at] = empty ? -INFINITY : (m_ref[n] + log2f(total[n])) * kLn2P;
+                    p.lse[at] = empty ? -INFINITY : (m_ref[n] - kLift + log2f(total[n])) * kLn2P;
             }
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
             __syncwarp();
