@@ -452,13 +452,13 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     if (key < it.lo || key >= it.hi) lv[n] = 0.f;
                 }
             }
-            // Running maxima (m of s; mv of s + lv), raised only when a row outgrows them by 2^8.  Whether one does needs a
+            // Running maxima (m of s; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
             // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + 8.f;
-                if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + 8.f;
+                if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + (8.f + kLiftE4M3);
             }
             if (__any_sync(0xffffffffu, raise)) {
                 float f[2];
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                         if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
                     }
-                    const float nm = fmaxf(m[e], mx), nv = kE4M3 ? fmaxf(mv[e], mw) : nm;
+                    const float nm = fmaxf(m[e], mx), nv = kE4M3 ? fmaxf(mv[e], mw - kLiftE4M3) : nm;
                     l[e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
                     f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - nv);
                     m[e] = nm;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = (mv[e] == -INFINITY ? 0.f : mv[e]) - kLiftE4M3;
+                const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = mv[e] == -INFINITY ? 0.f : mv[e];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const float x = s[2 * n + e];
@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
-            // outputs carry 2^-m (e4m3: 2^(lift - mv), weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] - kLiftE4M3 : m[e]) - top);
+            // outputs carry 2^-mv (weights with their scales), sums 2^-m
+            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top);
             if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
             float* row = slot + r * C::kSlotRow;
             if (!kE4M3) {

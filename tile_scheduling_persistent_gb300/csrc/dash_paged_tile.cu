@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         // ================================================== softmax and epilogue
         // e4m3: this warpgroup w has keys 64 w .. of every key tile and columns D/2 w .. of O, of both row tiles (n = 0, 1);
         // bf16: everything of row tile w (n = 0).
-        constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.f;   // weights, l and O are relative to the maximum less this
+        constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.f;   // maxima are held less this
         constexpr int kN = kE4M3 ? 2 : 1, kCols = kE4M3 ? 64 : 128, kOut = kE4M3 ? D / 2 : D;
         const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
@@ -718,7 +718,8 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     for (int k = 0; k < 4; ++k) part[k] = fmaxf(y[2 * k], y[2 * k + 1]);
 #pragma unroll
                     for (int k = 8; k < kCols; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
-                    float mx = c[n] * fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                    const float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                    float mx = kE4M3 ? fmaf(c[n], top, -kLift) : c[n] * top;
                     const bool over = valid[n] && mx > m_ref[n] + 8.f;
                     const bool raise = kE4M3 && !C::kOwn ? any_of_256(over || grown != 1.f) : __any_sync(0xffffffffu, over || grown != 1.f);
                     if (raise) {
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             }
                         }
                     }
-                    const float m_use = (m_ref[n] == -INFINITY ? 0.f : m_ref[n]) - kLift;
+                    const float m_use = m_ref[n] == -INFINITY ? 0.f : m_ref[n];
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
                     // P rounded to bf16 (at most 2^8; e4m3 caches: fp16, lifted, at most 2^15), keys [0,64) -> columns [0,32), [64,128) -> [64,96)
 #pragma unroll
@@ -848,9 +849,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 }
                 const bool stats = !kE4M3 || w == 0;
                 if (stats && keep)
-                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[n] - kLift, empty ? 0.f : total[n]);
+                    p.part_ml[pr] = make_float2(empty ? -INFINITY : m_ref[n], empty ? 0.f : total[n]);
                 else if (stats && !split && valid[n] && p.lse)
-                    p.lse[at] = empty ? -INFINITY : (m_ref[n] - kLift + log2f(total[n])) * kLn2P;
+                    p.lse[at] = empty ? -INFINITY : (m_ref[n] + log2f(total[n])) * kLn2P;
             }
             ptx::tc_fence_before();   // O and S are read before the next item's products (its P_READY) overwrite them
             __syncwarp();
