@@ -351,8 +351,8 @@ int dash_dq_finalize(const float* dq_accum, dash_bf16* dq, size_t numel, dash_st
  *    start 16-byte aligned, and strides of bf16 and fp32 data are multiples of
  *    8 elements.
  *  - What only the device knows (positions, slots, pages, lengths) is checked
- *    there: nothing is read or written out of range, and the first value found
- *    wrong is kept for dash_get_status_paged.
+ *    there: nothing is read or written out of range, and what was found wrong
+ *    first is kept for dash_get_status_paged.
  *  - Outputs are bitwise reproducible.
  * ------------------------------------------------------------------------- */
 
@@ -531,11 +531,16 @@ int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q_stride_h, 
 int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int64_t max_kv, size_t* bytes);
 
 /*
- * dash_get_status_paged -- synchronizes `stream`, reports the first error that
+ * dash_get_status_paged -- synchronizes `stream` and reports an error that
  * dash_kv_write, dash_kv_read or dash_attn_paged recorded on the current
- * device since the last report, on any stream, and clears it: *code = DASH_OK,
+ * device, on any stream (others are not waited for): *code = DASH_OK,
  * DASH_ERR_PAGE or DASH_ERR_TIMEOUT; info[0..3] (may be NULL) = {operator
  * (1 write, 2 read, 3 attention), sequence or token, value found, its bound}.
+ * Three records are kept, each the first error since it was last reported: of
+ * the writer and reader, of the attention's sequences of few rows (and of the
+ * lengths and row counts of all), and of those of many.  A call reports one, a
+ * DASH_ERR_TIMEOUT before the others and then in that order, and clears that
+ * one alone: the next call reports the next, until DASH_OK.
  * Returns DASH_OK, DASH_ERR_ARG (code NULL) or DASH_ERR_CUDA.
  */
 int dash_get_status_paged(dash_stream_t stream, int* code, int* info);

@@ -113,3 +113,28 @@ def test_weights_far_below_the_largest(n, D, above, column):
         got = lse[at:at + m].cpu().double().numpy()
         assert (np.abs(got - rl) <= 2.0 ** -12 + 2.0 ** -20 * np.abs(rl)).all()
         at += m
+
+
+def test_errors_of_several_kernels_are_all_reported():
+    # a slot past the cache (writer), a bad page of a sequence of few rows and one of a sequence of many: three reports,
+    # whatever their order in time, each once
+    g = gen(62)
+    c = paged(g, [300, 200], 2, 64, 16, False)
+    q = randn(g, 61, 4, 64)
+    good, bad = c.table.clone(), c.k_cache.shape[0] + 9
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    slot = torch.tensor([c.k_cache.shape[0] * 16 + 5], dtype=torch.int64, device=DEV)
+    for order in ((0, 1, 2), (2, 1, 0), (1, 2, 0)):
+        for what in order:
+            c.table = good.clone()
+            if what == 0:
+                dash.kv_write(x, x, c.k_cache, c.v_cache, slot)
+            else:   # sequence 0 has 60 new tokens (many rows), sequence 1 one (few)
+                c.table[2 - what, 2] = bad + what
+                run_attn(c, q, [60, 1])
+        c.table = good
+        got = [dash.get_status_paged() for _ in range(3)]
+        assert [code for code, _ in got] == [dash.ERR_PAGE] * 3
+        assert got[0][1] == [1, 0, int(slot), c.k_cache.shape[0] * 16]
+        assert got[1][1] == [3, 1, bad + 1, c.k_cache.shape[0]] and got[2][1] == [3, 0, bad + 2, c.k_cache.shape[0]]
+        no_error()

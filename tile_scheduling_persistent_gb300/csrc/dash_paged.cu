@@ -861,7 +861,7 @@ constexpr size_t kWsHeader = (256 + sizeof(Plan) + 255) / 256 * 256;   // the ma
 
 }  // namespace
 
-int take_error_paged(int* out5) { return take_serve_error(out5); }
+int error_paged(int* out5, bool clear) { return serve_record(out5, clear); }
 
 }  // namespace dash
 

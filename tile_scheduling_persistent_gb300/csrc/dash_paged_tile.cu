@@ -1060,7 +1060,7 @@ int launch_tile_t(const PagedParams& p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-int take_error_tile(int* out5) { return take_serve_error(out5); }
+int error_tile(int* out5, bool clear) { return serve_record(out5, clear); }
 
 int launch_paged_many(const PagedParams& few, int grid, cudaStream_t s) {
     PagedParams p = few;

@@ -441,7 +441,7 @@ int serve_check_device() {
     return DASH_OK;
 }
 
-int take_error_rope(int* out5) { return take_serve_error(out5); }
+int error_rope(int* out5, bool clear) { return serve_record(out5, clear); }
 
 }  // namespace dash
 
@@ -626,15 +626,20 @@ extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_tab
 extern "C" int dash_get_status_paged(dash_stream_t stream, int* code, int* info) {
     if (!code) return DASH_ERR_ARG;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return DASH_ERR_CUDA;
-    // one record per translation unit: the writer's and reader's first
-    int r[3][5];
-    int rc = take_error_rope(r[0]);
-    if (rc == DASH_OK) rc = take_error_paged(r[1]);
-    if (rc == DASH_OK) rc = take_error_tile(r[2]);
-    if (rc) return rc;
-    const int* e = r[0][0] ? r[0] : r[1][0] ? r[1] : r[2];
-    *code = e[0];
+    // one record per translation unit; all are read before one is cleared, and only the one reported is
+    int (*const record[3])(int*, bool) = {error_rope, error_paged, error_tile};
+    int r[3][5], pick = -1;
+    for (int i = 0; i < 3; ++i) {
+        const int rc = record[i](r[i], false);
+        if (rc) return rc;
+        if (r[i][0] && (pick < 0 || (r[i][0] == DASH_ERR_TIMEOUT && r[pick][0] != DASH_ERR_TIMEOUT))) pick = i;
+    }
+    if (pick >= 0) {
+        const int rc = record[pick](nullptr, true);
+        if (rc) return rc;
+    }
+    *code = pick < 0 ? DASH_OK : r[pick][0];
     if (info)
-        for (int i = 0; i < 4; ++i) info[i] = e[1 + i];
+        for (int i = 0; i < 4; ++i) info[i] = pick < 0 ? 0 : r[pick][1 + i];
     return DASH_OK;
 }

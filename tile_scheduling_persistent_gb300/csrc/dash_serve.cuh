@@ -13,27 +13,33 @@ namespace dash {
 enum ServeOp : int { kOpWrite = 1, kOpRead = 2, kOpAttn = 3 };
 
 // First error of this translation unit's kernels on the device since it was
-// last taken: code, then info[4].  A file-scope word needs no allocation, so
-// the calls can be captured, and it stays valid for every replay.
+// last cleared: code, then info[4]; word 7 is claimed by the thread that writes
+// them, and the code comes last, so that another stream's kernel is never seen
+// half way.  A file-scope word needs no allocation, so the calls can be
+// captured, and it stays valid for every replay.
 static __device__ int g_serve_error[8];
 
 static __device__ __noinline__ void serve_error(int code, int op, long long where, long long got, long long bound) {
-    if (atomicCAS(&g_serve_error[0], 0, code) == 0) {
+    if (atomicCAS(&g_serve_error[7], 0, 1) == 0) {
         g_serve_error[1] = op;
         g_serve_error[2] = (int)where;
         g_serve_error[3] = (int)(got > 0x7fffffffll ? 0x7fffffffll : got < -0x80000000ll ? -0x80000000ll : got);
         g_serve_error[4] = (int)(bound > 0x7fffffffll ? 0x7fffffffll : bound);
+        __threadfence();
+        atomicExch(&g_serve_error[0], code);
     }
 }
 
-// Reads and clears g_serve_error of this translation unit; the stream is idle.
-static inline int take_serve_error(int* out5) {
-    int h[8];
-    if (cudaMemcpyFromSymbol(h, g_serve_error, sizeof(h)) != cudaSuccess) return DASH_ERR_CUDA;
-    for (int i = 0; i < 5; ++i) out5[i] = h[i];
-    if (h[0] == 0) return DASH_OK;
+// This translation unit's record: read (out5[0] = DASH_OK: none), or cleared, which only one that was read is.
+static inline int serve_record(int* out5, bool clear) {
     const int zero[8] = {0};
-    return cudaMemcpyToSymbol(g_serve_error, zero, sizeof(zero)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    if (clear) return cudaMemcpyToSymbol(g_serve_error, zero, sizeof(zero)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    int h[8] = {0};
+    // (a code once seen, its info is there: the first copy may have read it too early)
+    for (int i = 0; i < 2 && (i == 0 || h[0]); ++i)
+        if (cudaMemcpyFromSymbol(h, g_serve_error, sizeof(h)) != cudaSuccess) return DASH_ERR_CUDA;
+    for (int i = 0; i < 5; ++i) out5[i] = h[i];
+    return DASH_OK;
 }
 
 // ---------------------------------------------------------------- conversions
@@ -96,8 +102,9 @@ inline int check_cache(const dash_kv_cache* c) {
 }
 
 int serve_check_device();   // DASH_OK on sm_103 (dash_rope.cu)
-int take_error_rope(int* out5);
-int take_error_paged(int* out5);
-int take_error_tile(int* out5);
+// Records of the translation units (serve_record).
+int error_rope(int* out5, bool clear);
+int error_paged(int* out5, bool clear);
+int error_tile(int* out5, bool clear);
 
 }  // namespace dash

@@ -608,8 +608,9 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
 
 
 def get_status_paged(stream=None):
-    """(code, info) of the first error that kv_write, kv_read or attn_paged recorded
-    on the current device since the last report; synchronizes `stream`."""
+    """(code, info) of an error that kv_write, kv_read or attn_paged recorded on the
+    current device, which is then cleared; synchronizes `stream`.  Errors of several
+    operators come one a call, until the code is 0 (see dash_get_status_paged)."""
     code = ctypes.c_int(0)
     info = (ctypes.c_int * 4)()
     _check(lib().dash_get_status_paged(_stream(stream), ctypes.byref(code), info), "dash_get_status_paged")
