@@ -6,6 +6,7 @@ streams come from PyTorch); the library fails loudly if it is missing.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import functools
 import os
@@ -230,7 +231,9 @@ def set_timeout_ns(ns):
 
 
 def release_workspaces():
-    _kept.held = {}   # attn_paged's, of this thread
+    """Gives back the device memory that calls keep: the library's, and attn_paged's of every thread and stream."""
+    with _kept_lock:
+        _kept.clear()
     _check(lib().dash_release_workspaces(), "dash_release_workspaces")
 
 
@@ -533,23 +536,34 @@ def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=Non
                               *ks, B, S, st), what)
 
 
-_KEPT_BYTES = 32 << 20
-_kept = threading.local()
+_KEPT_BYTES, _KEPT_TOTAL = 32 << 20, 256 << 20   # of one workspace, and of all
+_kept = collections.OrderedDict()                # (thread, device, stream): workspace, the last used at the end
+_kept_lock = threading.RLock()                   # (a finalizer that runs in here may call attn_paged)
 
 
 def _workspace(n, dev, st):
     """n bytes for a call on the current stream st.  Up to _KEPT_BYTES are kept, for each thread and stream: an allocation
     between launches costs 7 us, as much as all else in the call.  Calls of one thread on one stream run one after
-    another; a captured call, whose replays do not keep to its stream, gets memory of its graph's own."""
+    another; a captured call, whose replays do not keep to its stream, gets memory of its graph's own.  All that is kept is
+    at most _KEPT_TOTAL: the longest unused go first (the allocator hands them to later work of their stream alone, so a
+    call in flight may still use them; those of a thread that ended serve the next of its number, or go that way)."""
     if n > _KEPT_BYTES or torch.cuda.is_current_stream_capturing():
         return torch.empty(n, dtype=torch.uint8, device=dev)
-    try:
-        held = _kept.held
-    except AttributeError:
-        held = _kept.held = {}
-    w = held.get((dev, st))
-    if w is None or w.numel() < n:
-        w = held[dev, st] = torch.empty(max(n, 1 << 20), dtype=torch.uint8, device=dev)
+    key = threading.get_ident(), dev, st
+    try:   # (without the lock: another thread can only take the entry away)
+        w = _kept[key]
+        if w.numel() >= n:
+            _kept.move_to_end(key)
+            return w
+    except KeyError:
+        pass
+    w = torch.empty(max(n, 1 << 20), dtype=torch.uint8, device=dev)
+    with _kept_lock:
+        _kept[key] = w
+        _kept.move_to_end(key)
+        total = sum(t.numel() for t in _kept.values())
+        while total > _KEPT_TOTAL:
+            total -= _kept.popitem(last=False)[1].numel()
     return w
 
 
@@ -570,7 +584,7 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     T / B rows each) and max_q bounds their new tokens (None: T with cu_q, else
     T / B).  workspace: uint8 tensor of attn_paged_workspace bytes (None: the
     binding's own, kept for this thread and stream where it is small and the call
-    is not being captured; release_workspaces frees it)."""
+    is not being captured, 256 MiB in all; release_workspaces frees it)."""
     what = "dash_attn_paged"
     dev, st = _device_stream(stream, what)
     c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
