@@ -534,7 +534,9 @@ int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, i
  * dash_get_status_paged -- synchronizes `stream` and reports an error that
  * dash_kv_write, dash_kv_read or dash_attn_paged recorded on the current
  * device, on any stream (others are not waited for): *code = DASH_OK,
- * DASH_ERR_PAGE or DASH_ERR_TIMEOUT; info[0..3] (may be NULL) = {operator
+ * DASH_ERR_PAGE, DASH_ERR_TIMEOUT, or DASH_ERR_SCRATCH where sequences were cut
+ * into more partial rows than the workspace holds (an error of the library, after
+ * which outputs are undefined; nothing is written past the workspace); info[0..3] (may be NULL) = {operator
  * (1 write, 2 read, 3 attention), sequence or token, value found, its bound}.
  * Three records are kept, each the first error since it was last reported: of
  * the writer and reader, of the attention's sequences of few rows (and of the

@@ -138,3 +138,25 @@ def test_errors_of_several_kernels_are_all_reported():
         assert got[0][1] == [1, 0, int(slot), c.k_cache.shape[0] * 16]
         assert got[1][1] == [3, 1, bad + 1, c.k_cache.shape[0]] and got[2][1] == [3, 0, bad + 2, c.k_cache.shape[0]]
         no_error()
+
+
+@pytest.mark.parametrize("n,lens", [([1], [40000]), ([1] * 5, [9000] * 5), ([5, 5], [6000, 6000]), ([30, 1, 7], [5000, 9000, 7000]),
+                                    ([200], [8000])])
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_workspace_of_exactly_the_size_asked_for(n, lens, quant):
+    # every cut into key ranges lies inside it: the bytes behind stay as they are, and the results are those with a large one
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    g = gen(63)
+    c = paged(g, lens, Hkv, D, page, quant)
+    q = randn(g, sum(n), Hq, D)
+    need = dash.attn_paged_workspace(len(n), sum(n), Hq, Hkv, D, max(n), c.table.shape[1] * page)
+    assert need > 0
+    large = torch.zeros(2 * need + (1 << 20), dtype=torch.uint8, device=DEV)
+    o, lse = run_attn(c, q, n, workspace=large)
+    no_error()
+    buf = torch.full((need + 4096,), 0xa5, dtype=torch.uint8, device=DEV)
+    o2, lse2 = run_attn(c, q, n, workspace=buf[:need])
+    no_error()
+    assert same(o, o2) and same(lse, lse2)
+    assert bool((buf[need:] == 0xa5).all())
+    check_attn(c, q, n, o, lse)

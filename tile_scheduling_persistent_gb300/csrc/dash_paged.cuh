@@ -276,6 +276,8 @@ __device__ __forceinline__ void make_plan(const PagedParams& p, Plan& plan, bool
         for (int x = 0; x < 3; ++x) sum[x] += count[k][x];
     }
     if (threadIdx.x == 0) {
+        // (the host's bound holds for every cu_q that does not decrease; a row past it is not written, and its outputs neither)
+        if (report && all[2] > p.max_rows) serve_error(DASH_ERR_SCRATCH, kOpAttn, p.b0, all[2], p.max_rows);
         plan.items[p.nb] = all[0];
         plan.rows[p.nb] = all[2];
         if (many) {
