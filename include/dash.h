@@ -455,9 +455,11 @@ typedef struct {
  * to bf16, or per vector to
  *   scale = max(max|x| / 448, 2^-126),  code = e4m3_round_to_nearest_even(x / scale).
  * (NaN stays NaN in its own value and does not enter the maximum; a vector
- * that holds an infinity reads back as NaN.)  Slots must be distinct: of two
- * tokens with the same slot either may remain.  A slot past the last page is
- * not written (DASH_ERR_PAGE).
+ * that holds an infinity reads back as NaN.)  Slots must be distinct: where two
+ * tokens have the same slot (padding, say) its cells hold parts of both -- pieces
+ * of 8 values, and in e4m3 caches perhaps one's values under the other's scale --
+ * and nothing else is touched.  A slot past the last page is not written
+ * (DASH_ERR_PAGE).
  * Returns DASH_OK (also for T = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int64_t k_stride_t, int64_t k_stride_h,

@@ -486,7 +486,7 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
              interleaved=False, factor=1.0, q=None, q_out=None, stream=None):
     """Write new tokens' k, v [T, Hkv, D] (bf16, any token and head strides) into
     the pages [num_pages, Hkv, page_size, D] at slots int64 [T] (page * page_size +
-    offset; negative: skipped); an e4m3 cache (torch.float8_e4m3fn) quantises each
+    offset, no two the same; negative: skipped); an e4m3 cache (torch.float8_e4m3fn) quantises each
     vector with its own scale.  inv_freq and positions int32 [T]: k is rotated on
     the way (see rope), and q [T, Hq, D] into q_out."""
     what = "dash_kv_write"
