@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 // eight rows, one for each warp, which adds the ranges in ascending order; or one row of a sequence with many ranges
 // (more than kWarpRanges, where one warp's chain of loads would take tens of microseconds), warp w adding ranges w,
 // w + 8, ... and the eight sums added in order.  Which of the two depends on the row's own ns.  A block finds its first
-// unit while the kernel before it runs, with its share of the plan in registers and little shared memory, so that it fits
-// beside that kernel's CTA on an SM.
+// unit while the kernel before it runs.  It does not fit beside that kernel's CTA (its 18 or 24 thousand registers, where
+// those hold 54 to 65 of an SM's 65 thousand), so this overlaps with the last CTAs only: blocks start on SMs whose CTA has ended.
 constexpr int kWarpRanges = 48;
 
 // Adds ranges s0, s0 + step, ... of the partial rows base, base + stride, ...: (sum l, sum o of this lane's D / 32 columns)
@@ -818,8 +818,9 @@ template <int D>
 int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    // Three blocks for each SM, about as many as it holds: each one makes the plan, so more only repeat it (16 x 5 tokens
-    // over to 5000 bf16 keys: 54 us with three, 56.5 with six, 62 with twelve, 55 with one).
+    // Three blocks for each SM, which holds that many at D = 64 and two at D = 128 (96 registers): each one makes the plan, so
+    // more only repeat it (16 x 5 tokens over to 5000 bf16 keys, D = 128: 54 us with three, 56.5 with six, 62 with twelve, 55
+    // with one; two were not tried).
     return launch_after(combine_kernel<D>, (unsigned)(max_rows < 3ll * sms ? max_rows : 3ll * sms), 256, 0, p, s);
 }
 

@@ -4,11 +4,12 @@
 // Angles.  The rotation of pair i at position p is p * f_i radians modulo one
 // turn.  p * f_i in fp32 would be off by p * f_i * 2^-24 (0.06 rad at a
 // million), so the host turns f_i into the 64-bit fraction of a turn
-// F_i = round(f_i / 2pi * 2^64) mod 2^64, and the kernel forms p * F_i mod
+// F_i = floor(f_i / 2pi * 2^64) mod 2^64, and the kernel forms p * F_i mod
 // 2^64: an integer product whose wrap-around is the reduction modulo one turn.
 // Its top 32 bits, as a signed number, are the angle in [-1/2, 1/2) turns; the
-// error is p * 2^-65 turns from F_i (and p * f_i * 2^-53 from the double f_i)
-// plus fp32's rounding of that fraction.  Two integer multiplies replace a
+// error is p * 2^-64 turns from F_i (p * f_i * 2^-52 from the double f_i and its
+// product with 1 / 2pi) and 2^-32 from the bits dropped, plus fp32's rounding of
+// that fraction.  Two integer multiplies replace a
 // 64-bit floating multiply and reduction.  The top bits also give the quadrant
 // exactly, which leaves an angle of at most an eighth of a turn for a sine and a
 // cosine of eleven operations together: polynomials in the angle's square that
