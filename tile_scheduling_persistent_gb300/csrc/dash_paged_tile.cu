@@ -38,10 +38,10 @@
 // against 282.
 //
 // Measured (Hq = 32, Hkv = 8): 4096 new tokens over 16384 keys, bf16, D = 128:
-// 636 us, 1510 TFLOP/s (63% of the tensor core's cycles; what is left is the
-// softmax between the products); 2048 over 8192: 190 us bf16, 370 us e4m3
-// (conversion); 16 x 5 tokens over to 5000 keys, bf16: 55 us, 3.2 TB/s (rounds of
-// uneven items and their starts).  2048 over 8192, D = 64, e4m3: 259 us, 2000
+// 640 us, 1500 TFLOP/s (63% of the tensor core's cycles; what is left is the
+// softmax between the products); 2048 over 8192: 190 us bf16, 363 to 376 us e4m3
+// (votes, scaling, conversion: no unit is full); 16 x 5 tokens over to 5000 keys,
+// bf16: 55 us, 3.2 TB/s (rounds of uneven items and their starts).  2048 over 8192, D = 64, e4m3: 259 us, 2000
 // cycles for each matrix tile, of which the tensor core takes 512: 840 for the
 // exponentials, 550 to read and scale the scores, 200 to 400 waiting for them.
 //
