@@ -414,14 +414,21 @@ typedef enum {
 int dash_rope_freqs(int rot, double base, int scaling, double scale, int trained, double lo, double hi,
                     double* inv_freq, float* factor);
 
-typedef enum { DASH_CACHE_BF16 = 0, DASH_CACHE_E4M3 = 1 } dash_cache_type;
+typedef enum { DASH_CACHE_BF16 = 0, DASH_CACHE_E4M3 = 1, DASH_CACHE_E2M1 = 2 } dash_cache_type;
 
 /*
  * A paged key/value cache: pages of page_size tokens, k and v each
  * [num_pages, Hkv, page_size, D].  DASH_CACHE_E4M3 holds e4m3 values with one
  * fp32 scale for each token and head, [num_pages, Hkv, page_size] (a cached
  * vector stands for code * scale; a scale is finite and not negative);
- * DASH_CACHE_BF16 has no scales (NULL).  num_pages * Hkv < 2^31.
+ * DASH_CACHE_BF16 has no scales (NULL).  DASH_CACHE_E2M1 (4 bits) holds e2m1
+ * values two to a byte, the first of a pair in the low half, k and v each
+ * [num_pages, Hkv, page_size, D / 2] bytes, with an e4m3 scale for every 16
+ * values of a vector: k_scale and v_scale are the addresses of bytes
+ * [num_pages, Hkv, page_size, D / 16].  Its values stand for
+ * code * scale * 2^k_exp (v_exp), one exponent for the whole cache: values up to
+ * 2688 * 2^exp can be held, and a scale has all its four bits where the largest
+ * of its 16 values is at least 2^-3 * 2^exp.  num_pages * Hkv < 2^31.
  * All contiguous device memory, 16-byte aligned.  page_size: 16, 32, 64, 128
  * or 256; D in {64, 128}.  Token offset o of page p is slot p*page_size + o.
  */
@@ -431,6 +438,7 @@ typedef struct {
     float* k_scale;
     float* v_scale;
     int type, num_pages, page_size, Hkv, D;
+    int16_t k_exp, v_exp;      /* DASH_CACHE_E2M1 alone: -64 .. 64 */
 } dash_kv_cache;
 
 /* Rotation of new tokens on their way into the cache (see dash_rope). */
@@ -455,10 +463,14 @@ typedef struct {
  * to bf16, or per vector to
  *   scale = max(max|x| / 448, 2^-126),  code = e4m3_round_to_nearest_even(x / scale).
  * (NaN stays NaN in its own value and does not enter the maximum; a vector
- * that holds an infinity reads back as NaN.)  Slots must be distinct: where two
+ * that holds an infinity reads back as NaN.)  E2M1: for each 16 values b
+ *   scale = e4m3_round_to_nearest_even(max|b| / (6 * 2^exp)) within [2^-9, 448],
+ *   code = e2m1_round_to_nearest_even(b / (scale * 2^exp)), at most 6,
+ * and 16 values among which one is NaN or infinite get a NaN scale: all of them
+ * read back as NaN.  Slots must be distinct: where two
  * tokens have the same slot (padding, say) its cells hold parts of both -- pieces
- * of 8 values, and in e4m3 caches perhaps one's values under the other's scale --
- * and nothing else is touched.  A slot past the last page is not written
+ * of 8 values, and in e4m3 and E2M1 caches perhaps one's values under the other's
+ * scale -- and nothing else is touched.  A slot past the last page is not written
  * (DASH_ERR_PAGE).
  * Returns DASH_OK (also for T = 0), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
@@ -469,7 +481,8 @@ int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int64_t k_stri
 /*
  * dash_kv_read -- read the first lens[b] tokens of B sequences back into
  * contiguous bf16 tensors k, v [B, Hkv, S, D] (e.g. the keys and values of
- * dash_attn_fwd_cross): value = bf16(code * scale), or the bf16 value itself.
+ * dash_attn_fwd_cross): value = bf16(code * scale), or the bf16 value itself
+ * (E2M1: code * scale * 2^exp, which bf16 holds exactly).
  * Token j of sequence b is offset j % page_size of page
  * block_table[b*table_stride + j / page_size] (device int32, max_pages entries
  * per sequence).  Rows j >= lens[b] are left as they were; so are rows of a
@@ -514,7 +527,9 @@ int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_table, int64_t
  * fp32.  With e4m3 caches a query's values are held to bf16's 8 bits down to
  * 2^-29 of the largest of their row, and in sequences of more than 32 rows the
  * cache's values to 2^-11 of themselves and 2^-31 of the largest value of the
- * sequence's head.
+ * sequence's head.  E2M1 caches: the products run in fp16, which holds
+ * code * scale exactly; weights as with e4m3 caches, to 2^-11 of themselves or
+ * 2^-32 of the row's largest, and queries as there.
  * How a sequence's keys are split over the GPU depends on its own lengths and
  * on Hq, Hkv and D alone: its outputs are the same bits whatever else is in
  * the batch, and from run to run.

@@ -98,3 +98,20 @@ def attend(q, k, v, first, causal=True, window=0):
         o[rows, h] = (p / l) @ v[:, h // G]
         lse[rows, h] = (m + np.log(l))[:, 0]
     return o, lse
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantise4(x, exp):
+    """(values on the e2m1 grid, scale) of vectors x [..., D]: 16 values share an e4m3 scale in units of 2^exp;
+    code * scale, the scale [..., D / 16] with its unit, stands for x."""
+    b = np.asarray(x, dtype=np.float64)
+    b = b.reshape(b.shape[:-1] + (-1, 16))
+    s = e4m3_round(np.clip(np.abs(b).max(-1) / 6.0 * 2.0 ** -exp, 2.0 ** -9, E4M3_MAX)) * 2.0 ** exp
+    y = np.minimum(np.abs(b) / s[..., None], 6.0)
+    i = np.searchsorted(E2M1, y, side="left")            # E2M1[i - 1] < y <= E2M1[i]
+    lo, hi = E2M1[np.maximum(i - 1, 0)], E2M1[i]
+    mid = (lo + hi) / 2
+    up = (y > mid) | ((y == mid) & (i % 2 == 0))         # ties to the even code
+    return (np.where(up, hi, lo) * np.sign(b)).reshape(np.asarray(x).shape), s

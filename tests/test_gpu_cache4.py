@@ -1,0 +1,275 @@
+"""A paged cache of 4 bits on the GPU: written, read back and attended to, against the formulas in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as V
+from tile_scheduling_persistent_gb300 import dash
+
+from cache4_helpers import check_attn4, paged4, quantised4, values4
+from serving_helpers import DEV, E4M3, no_error, randn, rope_bound, run_attn, same
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ---------------------------------------------------------------------------------------------------------------- writing
+WRITES = {
+    # name: (T, Hq, Hkv, D, page, rot, interleaved)
+    "one_token": (1, 2, 1, 64, 16, 64, False),
+    "halves": (67, 8, 2, 128, 16, 128, False),
+    "pairs": (130, 4, 4, 64, 64, 64, True),
+    "quarter": (33, 6, 2, 64, 32, 16, True),
+    "odd_sixteenths": (50, 3, 3, 128, 128, 48, False),
+    "odd_sixteenths_pairs": (19, 4, 1, 128, 256, 80, True),
+    "many_heads": (700, 28, 4, 128, 16, 112, False),
+}
+
+
+def empty4(N, Hkv, page, D):
+    return [torch.full((N, Hkv, page, D // w), 3, dtype=torch.uint8, device=DEV) for w in (2, 2, 16, 16)]
+
+
+def written(name, rotate, seed=3, special=False):
+    T, Hq, Hkv, D, page, rot, pairs = WRITES[name]
+    g = gen(seed)
+    qkv = randn(g, T, Hq + 2 * Hkv, D)
+    if special:   # zeros, far magnitudes, and what is not finite
+        qkv[0, Hq:, :16] = 0
+        qkv[0, Hq:, 16:32] = 2.0 ** -20
+        qkv[0, Hq:, 32:48] *= 2.0 ** 20
+        qkv[T // 2, Hq:, 3] = float("inf")
+        qkv[T // 2, Hq:, 63] = float("nan")
+        qkv[T - 1, Hq:, 17] = float("-inf")
+    N = -(-T // page) + 2
+    slots = (torch.randperm(N, generator=g)[:, None] * page + torch.arange(page)).flatten()[:T].clone()
+    if T > 10:
+        slots[5] = -1
+        slots[T - 1] = -9
+    kc, vc, ks, vs = empty4(N, Hkv, page, D)
+    d = qkv.to(DEV)
+    q, k, v = d.split([Hq, Hkv, Hkv], dim=1)
+    out = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=DEV)
+    freqs, factor = dash.rope_freqs(rot)
+    pos = torch.randint(0, 100000, (T,), generator=g, dtype=torch.int32)
+    turn = dict(inv_freq=freqs, positions=pos.to(DEV), interleaved=pairs, factor=factor, q=q, q_out=out) if rotate else {}
+    dash.kv_write(k, v, kc, vc, slots.to(DEV), k_scale=ks.view(E4M3), v_scale=vs.view(E4M3), k_exp=-3, v_exp=2, **turn)
+    no_error()
+    return qkv, slots, pos, freqs, factor, (kc, vc, ks, vs), out
+
+
+@pytest.mark.parametrize("name", list(WRITES))
+@pytest.mark.parametrize("special", [False, True])
+def test_write_without_rotation(name, special):
+    """Byte for byte what the definition gives in fp32; every other cell keeps its bytes."""
+    T, Hq, Hkv, D, page, _, _ = WRITES[name]
+    qkv, slots, _, _, _, got, _ = written(name, False, special=special)
+    ok = slots >= 0
+    p, o = slots[ok] // page, slots[ok] % page
+    for x, exp, codes, scales in ((qkv[:, Hq:Hq + Hkv], -3, got[0], got[2]), (qkv[:, Hq + Hkv:], 2, got[1], got[3])):
+        c, s = quantised4(x[ok], exp)
+        wc, ws = torch.full(codes.shape, 3, dtype=torch.uint8), torch.full(scales.shape, 3, dtype=torch.uint8)
+        wc[p, :, o], ws[p, :, o] = c, s.view(torch.uint8)
+        dead = (ws == 0x7f).repeat_interleave(8, -1)   # a NaN scale says it all: its codes may be anything
+        assert torch.equal(scales.cpu(), ws)
+        assert torch.equal(codes.cpu()[~dead], wc[~dead])
+
+
+@pytest.mark.parametrize("name", list(WRITES))
+def test_write_with_rotation(name):
+    """A rotated key is off by fp32's rounding (rope_bound's first term), so that its code or its block's scale is another
+    where it lies that near to a border: a share of a few 2^-19 of each other code's step, so one value in a thousand is
+    far more than can come of it; such a value is off by a step (of a third at most) of its block's largest."""
+    T, Hq, Hkv, D, page, rot, pairs = WRITES[name]
+    qkv, slots, pos, freqs, factor, got, out = written(name, True)
+    x = qkv.double().numpy()
+    turned = V.rope(x[:, :Hq + Hkv], pos.numpy()[:, None], freqs.numpy(), factor, pairs)
+    ref = turned[:, :Hq]
+    assert (np.abs(out.float().cpu().double().numpy() - ref) <= rope_bound(x[:, :Hq], freqs.numpy(), factor, pairs, True, ref)).all()
+    ok = (slots >= 0).numpy()
+    p, o = slots[slots >= 0] // page, slots[slots >= 0] % page
+    for y, exp, codes, scales in ((turned[ok, Hq:], -3, got[0], got[2]), (x[ok, Hq + Hkv:], 2, got[1], got[3])):
+        held = values4(codes.cpu()[p, :, o], scales.cpu()[p, :, o].view(E4M3), exp).numpy()
+        code, scale = V.quantise4(y, exp)
+        want = code * np.repeat(scale, 16, -1)
+        d = np.abs(held - want)
+        top = np.repeat(np.abs(y).reshape(y.shape[:-1] + (-1, 16)).max(-1), 16, -1)
+        assert (d > 0).mean() <= 1e-3
+        assert (d <= 0.375 * top).all()
+
+
+def test_write_reports_a_slot_past_the_cache():
+    kc, vc, ks, vs = empty4(2, 1, 16, 64)
+    x = torch.ones(3, 1, 64, dtype=torch.bfloat16, device=DEV)
+    dash.kv_write(x, x, kc, vc, torch.tensor([1, 32, 31], device=DEV), k_scale=ks.view(E4M3), v_scale=vs.view(E4M3))
+    code, info = dash.get_status_paged()
+    assert code == dash.ERR_PAGE and info == [1, 1, 32, 32]
+    assert (kc[0, 0, 1] != 3).all() and (kc[1, 0, 15] != 3).all() and int((kc != 3).sum()) == 64
+
+
+# ---------------------------------------------------------------------------------------------------------------- reading
+@pytest.mark.parametrize("D,Hkv,page,lens,S", [(64, 2, 16, [1, 0, 33], 40), (128, 4, 64, [300, 129], 300), (128, 1, 256, [700], 600),
+                                               (64, 3, 128, [5, 6, 7, 1000], 1000)])
+def test_read(D, Hkv, page, lens, S):
+    c = paged4(gen(4), lens, Hkv, D, page, exps=(5, -7))
+    k, v = (torch.full((len(lens), S, Hkv, D), 9.0, dtype=torch.bfloat16, device=DEV).transpose(1, 2) for _ in range(2))
+    dash.kv_read(c.k_cache, c.v_cache, c.table, c.lens, k, v, **c.kw)
+    no_error()
+    for got, ref in ((k, c.k), (v, c.v)):
+        got = got.float().cpu().double().numpy()
+        for b, n in enumerate(lens):
+            m = min(n, S)
+            # (two bits of a code, four of a scale, a power of two: bf16 holds it)
+            assert np.array_equal(got[b, :, :m], ref[b][:m].transpose(1, 0, 2)) and (got[b, :, m:] == 9.0).all()
+
+
+def test_a_block_that_is_not_finite_reads_back_as_nan():
+    D, page = 64, 16
+    kc, vc, ks, vs = empty4(1, 1, page, D)
+    kw = dict(k_scale=ks.view(E4M3), v_scale=vs.view(E4M3))
+    x = torch.ones(2, 1, D, dtype=torch.bfloat16, device=DEV)
+    x[0, 0, 20] = float("nan")
+    x[1, 0, 40] = float("-inf")
+    dash.kv_write(x, x, kc, vc, torch.tensor([0, 1], device=DEV), **kw)
+    k, v = (torch.zeros(1, 1, 2, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dash.kv_read(kc, vc, torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([2], dtype=torch.int32, device=DEV), k, v, **kw)
+    no_error()
+    want = torch.full((2, D), 6 * 11 / 64)   # 1 / 6 rounds to the scale 11 / 64, 1 over it to the code of 6
+    want[0, 16:32] = want[1, 32:48] = float("nan")
+    for t in (k, v):
+        assert torch.equal(torch.nan_to_num(t[0, 0].float().cpu(), 5.0), torch.nan_to_num(want, 5.0))
+
+
+# -------------------------------------------------------------------------------------------------------------- attention
+CASES = {
+    # name: (Hq, Hkv, D, page, lens, new tokens, window, padding rows)
+    "one_token": (2, 2, 64, 16, [1], [1], None, 0),
+    "one_of_1000": (32, 8, 128, 16, [1000], [1], None, 0),
+    "decode_ragged": (32, 8, 128, 64, [1, 17, 300, 129, 1025, 64], [1] * 6, None, 3),
+    "decode_mha": (4, 4, 128, 128, [127, 128, 129, 2049], [1] * 4, None, 0),
+    "decode_wide_group": (64, 2, 64, 32, [70, 700], [1, 1], None, 1),
+    "decode_odd_group": (14, 2, 128, 16, [333, 34], [1, 1], None, 0),
+    "decode_empty": (8, 2, 128, 16, [0, 40, 0], [1, 1, 1], None, 0),
+    "decode_window": (8, 2, 64, 16, [5, 100, 1500], [1, 1, 1], 37, 0),
+    "decode_d64": (8, 1, 64, 256, [2500, 3], [1, 1], None, 0),
+    "two_tokens": (32, 8, 128, 16, [2, 515], [2, 2], None, 0),
+    "verify": (32, 8, 128, 32, [700, 5, 260], [5, 5, 5], None, 2),
+    "verify_small_group": (6, 2, 64, 16, [130, 512], [4, 3], None, 0),
+    "rows_16_to_33": (8, 2, 128, 16, [400, 300, 290, 500], [4, 5, 8, 9], None, 0),
+    "rows_16_to_33_d64": (8, 2, 64, 32, [400, 300, 290, 500], [4, 5, 8, 9], 200, 0),
+    "chunk": (8, 2, 128, 64, [400], [200], None, 0),
+    "chunk_ragged": (4, 4, 128, 16, [130, 900, 77], [130, 65, 1], None, 5),
+    "chunk_odd_group": (14, 2, 64, 128, [640], [150], None, 0),
+    "chunk_window": (8, 2, 128, 16, [700, 300], [150, 300], 100, 0),
+    "chunk_window_tiny": (4, 2, 64, 16, [500], [300], 1, 0),
+    "chunk_more_new_than_cached": (4, 2, 64, 16, [20, 0], [50, 3], None, 0),
+    "chunk_long": (4, 1, 128, 32, [5000], [70], None, 0),
+    "mixed": (16, 4, 64, 16, [1300, 1, 500, 64, 0], [1, 1, 260, 0, 1], None, 4),
+    "mixed_window": (8, 8, 128, 32, [900, 800, 33], [1, 140, 33], 300, 0),
+    # several items for every SM, and mixtures of one and two row tiles
+    "decode_many": (16, 8, 64, 16, [37 * i % 900 + 1 for i in range(70)], [1] * 70, None, 0),
+    "verify_many": (32, 8, 128, 32, [301 * i % 1900 + 6 for i in range(40)], [5] * 40, None, 0),
+    "verify_many_window": (32, 8, 64, 16, [301 * i % 1900 + 6 for i in range(40)], [6] * 40, 500, 0),
+    "chunk_many": (8, 8, 128, 64, [211 * i % 700 + 300 for i in range(30)], [17 * i % 300 + 17 for i in range(30)], None, 3),
+    "group_128": (128, 1, 64, 16, [90, 300], [1, 3], None, 0),
+}
+
+
+def inputs(name, seed=1, **kw):
+    Hq, Hkv, D, page, lens, n, window, pad = CASES[name]
+    g = gen(seed)
+    c = paged4(g, lens, Hkv, D, page, **kw)
+    return c, randn(g, sum(n) + pad, Hq, D), n, window
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_attention_against_the_oracle(name):
+    c, q, n, window = inputs(name)
+    o, lse = run_attn(c, q, n, window=window)
+    no_error()
+    check_attn4(c, q, n, o, lse, window=window)
+
+
+@pytest.mark.parametrize("name", ["decode_ragged", "verify", "chunk_ragged", "mixed", "rows_16_to_33"])
+def test_full_mask(name):
+    c, q, n, _ = inputs(name, seed=2)
+    o, lse = run_attn(c, q, n, causal=False)
+    no_error()
+    check_attn4(c, q, n, o, lse, causal=False)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_page_size(page, D):
+    g = gen(3)
+    c = paged4(g, [page * 2 + 3, 300, 1], 2, D, page)
+    for n in ([1, 1, 1], [40, 33, 1]):
+        q = randn(g, sum(n), 8, D)
+        o, lse = run_attn(c, q, n)
+        no_error()
+        check_attn4(c, q, n, o, lse)
+
+
+@pytest.mark.parametrize("sigma,exps", [(1.0, (0, 0)), (300.0, (0, 3)), (1e-3, (-12, -12)), (1.0, (-8, 7))])
+@pytest.mark.parametrize("n", [1, 40])
+def test_exponents_and_far_magnitudes(sigma, exps, n):
+    """Values near the ends of what the scales hold, saturated ones among them (exponents that do not suit the data)."""
+    g = gen(7)
+    c = paged4(g, [500, 90], 2, 128, 16, sigma=sigma, exps=exps)
+    q = (randn(g, 2 * n, 8, 128).float() / max(sigma, 1.0)).to(torch.bfloat16)
+    o, lse = run_attn(c, q, [n, n])
+    no_error()
+    check_attn4(c, q, [n, n], o, lse)
+
+
+@pytest.mark.parametrize("name", ["decode_ragged", "verify_many", "chunk_many", "mixed"])
+def test_the_same_bits_in_any_batch_and_run(name):
+    c, q, n, window = inputs(name, seed=5)
+    o, lse = run_attn(c, q, n, window=window)
+    again, lse2 = run_attn(c, q, n, window=window)
+    assert same(o, again) and same(lse, lse2)
+    at = np.concatenate([[0], np.cumsum(n)])
+    for b in range(0, len(n), max(1, len(n) // 4)):
+        rows = slice(int(at[b]), int(at[b + 1]))
+        if n[b] == 0:
+            continue
+        one = type(c)([c.k[b]], [c.v[b]], c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table[b:b + 1].contiguous(), c.lens[b:b + 1].contiguous(), c.kw)
+        oo, ol = run_attn(one, q[rows], [n[b]], window=window)
+        assert same(oo, o[rows]) and same(ol, lse[rows])
+
+
+def test_a_key_far_above_the_others():
+    """One key some 2^20 above the rest, with a small value: the others' weights have to keep their bits."""
+    Hkv, D, page, L = 1, 64, 16, 300
+    for n in (1, 40):
+        g = gen(9)
+        c = paged4(g, [L], Hkv, D, page, exps=(0, 0))
+        codes, scales = c.k_cache.cpu(), c.k_scale.cpu().view(torch.uint8)
+        vc = c.v_cache.cpu()
+        p = int(c.table[0, 0])
+        codes[p, 0, 0] = 0x22                       # all ones
+        scales[p, 0, 0] = torch.tensor([2.0]).to(E4M3).view(torch.uint8)
+        vc[p, 0, 0] = 0                             # its value: zero
+        c.k_cache, c.k_scale, c.v_cache = codes.to(DEV), scales.view(E4M3).to(DEV), vc.to(DEV)
+        c.kw.update(k_scale=c.k_scale)
+        c.k[0][0], c.v[0][0] = 2.0, 0.0
+        q = torch.full((n, 2, D), 0.875).to(torch.bfloat16)   # scores of 14 where the others are near zero
+        o, lse = run_attn(c, q, [n])
+        no_error()
+        check_attn4(c, q, [n], o, lse)
+
+
+def test_pages_out_of_range_are_reported_and_other_sequences_untouched():
+    c, q, n, _ = inputs("decode_ragged")
+    c.table[2, 1] = 10 ** 6
+    o, lse = run_attn(c, q, n)
+    code, info = dash.get_status_paged()
+    assert code == dash.ERR_PAGE and info[:3] == [3, 2, 10 ** 6]
+    for b in (0, 1, 3, 4, 5):
+        one = type(c)([c.k[b]], [c.v[b]], c.k_cache, c.v_cache, None, None, c.table[b:b + 1].contiguous(), c.lens[b:b + 1].contiguous(), c.kw)
+        oo, ol = run_attn(one, q[b:b + 1], [1])
+        assert same(oo, o[b:b + 1]) and same(ol, lse[b:b + 1])
+    no_error()

@@ -117,6 +117,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -125,19 +130,21 @@ __device__ __forceinline__ void consumer_barrier(int group) { asm volatile("bar.
 
 // ---------------------------------------------------------------- few rows
 // kGroups: independent groups of four consumer warps and a producer.
-template <int D, bool kE4M3, int kGroups>
+template <int D, int kType, int kGroups>
 struct FewCfg {
+    static constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
     static constexpr int kRows = kFewRows;
     static constexpr int kThreads = kGroups * 160;
-    static constexpr int kElem = kE4M3 ? 1 : 2;
-    static constexpr int kHalfStage = kFewKeys * D * kElem;   // K, then V
+    static constexpr int kRow = cell_bytes(kType, D), kScaleRow = scale_bytes(kType, D);   // of a key
+    static constexpr int kHalfStage = kFewKeys * kRow;        // K, then V
     static constexpr int kStage = 2 * kHalfStage;
     static constexpr int kRing = kGroups == 2 ? 65536 : 51200;                     // bytes of a group's stages
-    static constexpr int kStages = (kRing / kStage) < 8 ? kRing / kStage : 8;      // of each group
+    static constexpr int kMostStages = kE2M1 && D == 128 ? 5 : 8;                  // (what shared memory has room for)
+    static constexpr int kStages = (kRing / kStage) < kMostStages ? kRing / kStage : kMostStages;   // of each group
     static_assert(kStages >= 2, "stage ring");
-    static constexpr int kSlotRow = !kE4M3 ? D + 4 : D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
-    static constexpr int OFF_SCALE = kGroups * kStages * kStage;   // [group][stage][K, V][kFewKeys] fp32
-    static constexpr int OFF_SLOT = OFF_SCALE + (kE4M3 ? kGroups * kStages * 2 * kFewKeys * 4 : 0);   // [group][warp][row]
+    static constexpr int kSlotRow = kType == DASH_CACHE_BF16 ? D + 4 : D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
+    static constexpr int OFF_SCALE = kGroups * kStages * kStage;   // [group][stage][K, V][kFewKeys][kScaleRow]
+    static constexpr int OFF_SLOT = OFF_SCALE + kGroups * kStages * 2 * kFewKeys * kScaleRow;   // [group][warp][row]
     static constexpr int OFF_M = OFF_SLOT + kGroups * 4 * kRows * kSlotRow * 4;   // [group][parity][warp][row]
     static constexpr int OFF_L = OFF_M + kGroups * 2 * 4 * kRows * 4;             // [group][warp][row]
     static constexpr int OFF_PLAN = OFF_L + kGroups * 4 * kRows * 4;
@@ -192,9 +199,10 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-template <int D, bool kE4M3, int kGroups>
+template <int D, int kType, int kGroups>
 __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
-    using C = FewCfg<D, kE4M3, kGroups>;
+    using C = FewCfg<D, kType, kGroups>;
+    constexpr bool kBf16 = kType == DASH_CACHE_BF16, kE4M3 = C::kE4M3, kE2M1 = C::kE2M1;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
@@ -225,9 +233,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         // ================================================== producer
         const int page = p.c.page_size, rows = page < kFewKeys ? page : kFewKeys;
         const int subs = kFewKeys / rows;                 // copies of one kind along a stage's keys
-        const int kinds = kE4M3 ? 4 : D / 32;             // K (per 64 values), V (same), or K, V and their scales
+        const int kinds = !kBf16 ? 4 : D / 32;            // K (per 64 values), V (same), or K, V and their scales
         const int sub = lane / kinds, kind = lane % kinds;
-        const uint32_t sub_bytes = (uint32_t)rows * (2 * D * C::kElem + (kE4M3 ? 8 : 0));
+        const uint32_t sub_bytes = (uint32_t)rows * 2 * (C::kRow + C::kScaleRow);
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
             find_item(p, plan, item, it);
@@ -257,17 +265,19 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 if (need) {
                     const int y = k0 & (page - 1), head = pg * p.c.Hkv + it.hk;
                     const uint32_t base = ring + stage * C::kStage;
-                    if (!kE4M3) {
+                    if (kBf16) {
                         constexpr int kBoxes = D / 64;
                         const int box = kind % kBoxes, val = kind / kBoxes;
                         ptx::tma_load_3d(base + val * C::kHalfStage + box * (kFewKeys * 128) + sub * rows * 128,
                                          val ? &p.tm_v : &p.tm_k, 64 * box, y, head, full);
                     } else if (kind < 2) {
-                        ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * D, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
+                        ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * C::kRow, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
                     } else {
-                        const float* src = (kind == 3 ? p.c.v_scale : p.c.k_scale) + (long long)head * page + y;
-                        bulk_load(sbase + C::OFF_SCALE + (((group * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * 4, src,
-                                  rows * 4, full);
+                        const uint8_t* src = reinterpret_cast<const uint8_t*>(kind == 3 ? p.c.v_scale : p.c.k_scale) +
+                                             ((long long)head * page + y) * C::kScaleRow;
+                        bulk_load(sbase + C::OFF_SCALE +
+                                      (((group * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * C::kScaleRow,
+                                  src, rows * C::kScaleRow, full);
                     }
                 }
             }
@@ -290,24 +300,29 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     const int g = lane >> 2, c4 = lane & 3;
     const int ws = warp & 3;
     // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
-    // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle
-    auto perm = [](int n) { return kE4M3 ? (int)((0x36147250u >> (4 * n)) & 7u) : n; };
+    // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle.
+    // E2M1: the same for rows of 64 bytes (V: 8-byte reads of rows 0, 4, 1, 5 by half a warp) and of 32 (K: 8-byte reads
+    // of rows 0 to 3; V: 4-byte reads of rows 0, 2, 5, 7, one in each quarter of the banks).
+    auto perm = [](int n) {
+        constexpr uint32_t order = kE4M3 ? 0x36147250u : D == 128 ? 0x65217430u : 0x67453210u;
+        return kBf16 ? n : (int)((order >> (4 * n)) & 7u);
+    };
     float* const slots = reinterpret_cast<float*>(smem + C::OFF_SLOT) + group * 4 * C::kRows * C::kSlotRow;
     float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + group * 2 * 4 * C::kRows;
     float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + group * 4 * C::kRows;
-    // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3.  Loaded before the
-    // join of the item before, which hides the wait.
+    // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3; E2M1: (D/4)c + 4k
+    // + 0..3.  Loaded before the join of the item before, which hides the wait.
     uint32_t qf[D / 16][2];
     auto load_queries = [&](const FewItem& x) {
         const int r = x.r0 + min(g, min(x.s.n * p.G - x.r0, kFewRows) - 1), i = quick_div(r, p.G, p.over_G);
         const __nv_bfloat16* q = p.q + (long long)(x.s.first + i) * p.q_t + (long long)(x.hk * p.G + r - i * p.G) * p.q_h;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            if (!kE4M3) {
+            if (kBf16) {
                 qf[k][0] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4);
                 qf[k][1] = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c4 + 8);
             } else {
-                const uint2 w = *reinterpret_cast<const uint2*>(q + 64 * (k >> 2) + 16 * c4 + 4 * (k & 3));
+                const uint2 w = *reinterpret_cast<const uint2*>(q + (kE2M1 ? D / 4 * c4 + 4 * k : 64 * (k >> 2) + 16 * c4 + 4 * (k & 3)));
                 qf[k][0] = w.x;
                 qf[k][1] = w.y;
             }
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         seen_keys(p, it.s, it.s.n - 1, it.s.n, full_lo, skip);
 
         float qs[2];   // scale of the scores of rows 2c + e (log2 units)
-        if (!kE4M3) {
+        if (kBf16) {
             qs[0] = qs[1] = p.scale_log2e;
         } else {
             float top = 0.f;
@@ -376,19 +391,26 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
             __syncwarp();
             const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
+            constexpr float kLift = kE2M1 ? kLiftE4M3 : 0.f;   // the maxima m are held less this
             const int key0 = kt * kFewKeys + 16 * ws;   // this warp's first key
             const bool edge = key0 < full_lo || key0 + 16 > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
                 const int r = lane >> 1;
                 if (key0 + r < it.lo || key0 + r >= it.hi) {
                     const int row = 16 * ws + r;
-                    constexpr int kRow = D * C::kElem / 2;   // bytes per lane
+                    constexpr int kRow = C::kRow / 2;   // bytes per lane
 #pragma unroll
                     for (int x = 0; x < kRow; x += 16) {
                         const int byte = (lane & 1) * kRow + x;   // rows are zeroed whole: the swizzle stays inside a row
-                        sts128(kE4M3 || D == 64 ? sv + row * (D * C::kElem) + byte
-                                                : sv + (byte >> 7) * (kFewKeys * 128) + row * 128 + (byte & 127),
+                        sts128(!kBf16 || D == 64 ? sv + row * C::kRow + byte
+                                                 : sv + (byte >> 7) * (kFewKeys * 128) + row * 128 + (byte & 127),
                                make_uint4(0, 0, 0, 0));
+                    }
+                    if (kE2M1 && !(lane & 1)) {   // their scales enter the products too
+                        uint32_t* sc = reinterpret_cast<uint32_t*>(
+                            smem + C::OFF_SCALE + (((group * C::kStages + stage) * 2 + 1) * kFewKeys + row) * C::kScaleRow);
+#pragma unroll
+                        for (int x = 0; x < C::kScaleRow / 4; ++x) sc[x] = 0;
                     }
                 }
                 __syncwarp();
@@ -397,7 +419,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float s[4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = 0.f;
-            if (!kE4M3) {
+            // E2M1: scales of K's keys of this stage, then of V's
+            [[maybe_unused]] const uint8_t* const scales = smem + C::OFF_SCALE + (group * C::kStages + stage) * 2 * kFewKeys * C::kScaleRow;
+            if (kBf16) {
                 const int row = 16 * ws + (lane & 15);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -405,6 +429,39 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     const int chunk = 2 * (k & 3) + (lane >> 4);
                     ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
                     mma16816<false>(s, a, qf[k][0], qf[k][1]);
+                }
+            } else if (kE2M1) {   // a lane reads D / 4 values of a key in one: one or two scales
+                constexpr int kWords = D / 32;
+                uint32_t w[2][kWords], f[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int row = 16 * ws + 8 * n + perm(g);
+                    if (D == 128) {
+                        const uint4 v = lds128(sk + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
+                        w[n][0] = v.x, w[n][1] = v.y, w[n][kWords - 2] = v.z, w[n][kWords - 1] = v.w;
+                        f[n] = half2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(scales + row * 8 + 2 * c4));
+                    } else {
+                        const uint2 v = lds64(sk + row * 32 + c4 * 8);
+                        w[n][0] = v.x, w[n][1] = v.y;
+                        f[n] = half2_of_e4m3x2(scales[row * 4 + c4]);
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < kWords; ++y) {
+                    uint32_t h[2][4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t ff = __byte_perm(f[n], 0u, y < 2 ? 0x1010u : 0x3232u);
+                        h[n][0] = mul_half2(half2_of_e2m1<0>(w[n][y]), ff);
+                        h[n][1] = mul_half2(half2_of_e2m1<1>(w[n][y]), ff);
+                        h[n][2] = mul_half2(half2_of_e2m1<2>(w[n][y]), ff);
+                        h[n][3] = mul_half2(half2_of_e2m1<3>(w[n][y]), ff);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t a[4] = {h[0][2 * z], h[1][2 * z], h[0][2 * z + 1], h[1][2 * z + 1]};
+                        mma16816<true>(s, a, qf[2 * y + z][0], qf[2 * y + z][1]);
+                    }
                 }
             } else {
 #pragma unroll
@@ -452,12 +509,12 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     if (key < it.lo || key >= it.hi) lv[n] = 0.f;
                 }
             }
-            // Running maxima (m of s; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
+            // Running maxima (m of s, less the lift with E2M1; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
             // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + 8.f;
+                raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + (8.f + kLift);
                 if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + (8.f + kLiftE4M3);
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -470,7 +527,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                         if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
                     }
-                    const float nm = fmaxf(m[e], mx), nv = kE4M3 ? fmaxf(mv[e], mw - kLiftE4M3) : nm;
+                    const float nm = fmaxf(m[e], mx - kLift), nv = kE4M3 ? fmaxf(mv[e], mw - kLiftE4M3) : nm;
                     l[e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
                     f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - nv);
                     m[e] = nm;
@@ -500,9 +557,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
 #pragma unroll
             for (int n = 0; n < 2; ++n)
-                pb[n] = transposed8x8(kE4M3 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
+                pb[n] = transposed8x8(!kBf16 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
 
-            if (!kE4M3) {   // tile j of O^T: value columns 16j + g and + 8
+            if (kBf16) {   // tile j of O^T: value columns 16j + g and + 8
                 const int row = 16 * ws + (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
@@ -510,6 +567,48 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
                     ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
                     mma16816<false>(o[j], a, pb[0], pb[1]);
+                }
+            } else if (kE2M1) {   // the same columns, of one scale (D = 64: half of one)
+                constexpr int kWords = D / 64;   // words of a lane's D / 8 columns
+                const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
+                const uint8_t* const sc = scales + kFewKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
+                uint32_t w[4][kWords], f[2];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = (x & 1 ? r1 : r0) + 8 * (x >> 1);
+                    if (D == 128) {
+                        const uint2 v = lds64(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                        w[x][0] = v.x, w[x][kWords - 1] = v.y;
+                    } else {
+                        w[x][0] = lds32(sv + row * 32 + g * 4);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    f[n] = half2_of_e4m3x2(sc[(r0 + 8 * n) * C::kScaleRow] | (uint32_t)sc[(r1 + 8 * n) * C::kScaleRow] << 8);
+                // a word holds 8 columns of one key: the low and the high halves of its bytes beside those of the other key
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+                for (int y = 0; y < kWords; ++y) {
+                    uint32_t h[2][8];   // [keys 2c.., + 8][column]
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint32_t a = w[2 * n][y], b = w[2 * n + 1][y];
+                        const uint32_t even = (a & kLow) | ((b << 4) & ~kLow), odd = ((a >> 4) & kLow) | (b & ~kLow);
+                        h[n][0] = mul_half2(half2_of_e2m1<0>(even), f[n]);
+                        h[n][1] = mul_half2(half2_of_e2m1<0>(odd), f[n]);
+                        h[n][2] = mul_half2(half2_of_e2m1<1>(even), f[n]);
+                        h[n][3] = mul_half2(half2_of_e2m1<1>(odd), f[n]);
+                        h[n][4] = mul_half2(half2_of_e2m1<2>(even), f[n]);
+                        h[n][5] = mul_half2(half2_of_e2m1<2>(odd), f[n]);
+                        h[n][6] = mul_half2(half2_of_e2m1<3>(even), f[n]);
+                        h[n][7] = mul_half2(half2_of_e2m1<3>(odd), f[n]);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t a[4] = {h[0][2 * z], h[0][2 * z + 1], h[1][2 * z], h[1][2 * z + 1]};
+                        mma16816<true>(o[4 * y + z], a, pb[0], pb[1]);
+                    }
                 }
             } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
@@ -564,10 +663,11 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
             // outputs carry 2^-mv (weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top);
+            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f
+                             : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top) * (kE2M1 ? p.v_unit : 1.f);
             if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
             float* row = slot + r * C::kSlotRow;
-            if (!kE4M3) {
+            if (kBf16) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     row[16 * j + g] = o[j][e] * fo;
@@ -585,7 +685,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         consumer_barrier(group);
         for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
             const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
-            const int chunk = kE4M3 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
+            const int chunk = !kBf16 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -787,30 +887,33 @@ int sm_count() {
     return count[dev];
 }
 
-template <int D, bool kE4M3, int kGroups>
+template <int D, int kType, int kGroups>
 int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
-    using C = FewCfg<D, kE4M3, kGroups>;
+    using C = FewCfg<D, kType, kGroups>;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kType, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kE4M3, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kType, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 // Three groups where their registers and stages allow it (few_workers counts on it).
 int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
+    const bool d64 = p.c.D == 64;
+    if (p.c.type == DASH_CACHE_E2M1)
+        return d64 ? launch_few_t<64, DASH_CACHE_E2M1, 3>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_E2M1, 3>(p, many, max_items, s);
     if (p.c.type == DASH_CACHE_E4M3)
-        return p.c.D == 64 ? launch_few_t<64, true, 3>(p, many, max_items, s) : launch_few_t<128, true, 3>(p, many, max_items, s);
-    return p.c.D == 64 ? launch_few_t<64, false, 3>(p, many, max_items, s) : launch_few_t<128, false, 2>(p, many, max_items, s);
+        return d64 ? launch_few_t<64, DASH_CACHE_E4M3, 3>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_E4M3, 3>(p, many, max_items, s);
+    return d64 ? launch_few_t<64, DASH_CACHE_BF16, 3>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_BF16, 2>(p, many, max_items, s);
 }
 
 // Its plan is made while the kernel before it in the stream runs.
@@ -929,9 +1032,13 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     prm.window = window;
     while ((1 << prm.page_shift) < cache->page_size) ++prm.page_shift;
     prm.scale_log2e = (1.0f / sqrtf((float)D)) * kLog2eP;
-    const bool e4m3 = cache->type == DASH_CACHE_E4M3;
+    prm.v_unit = 1.f;
+    if (cache->type == DASH_CACHE_E2M1) {
+        prm.scale_log2e = ldexpf(prm.scale_log2e, cache->k_exp);
+        prm.v_unit = ldexpf(1.f, cache->v_exp);
+    }
     const int rows = cache->page_size < kFewKeys ? cache->page_size : kFewKeys;
-    if (make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, e4m3, rows))
+    if (make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
         return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {

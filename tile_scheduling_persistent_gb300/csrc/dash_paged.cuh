@@ -33,6 +33,7 @@ constexpr int kTileSms = 152;          // items of one round of the many-rows ke
 // e4m3 caches: weights become fp16 with 2^7 for the running maximum.  They exceed it by up to 2^8 before it is raised, and
 // 2^15 is fp16's last whole binade; downwards each is held to 2^-11 of itself until 2^-21 of the largest, and to 2^-32 of
 // the largest below.  (With 1 for the maximum, keys 2^24 below one whose value is small lost a fifth of their sum.)
+// E2M1 caches: likewise (the products run in fp16, the largest value is 6 * 448).
 constexpr float kLiftE4M3 = 7.f;
 constexpr float kLog2eP = 1.4426950408889634f, kLn2P = 0.69314718055994531f;
 
@@ -56,7 +57,8 @@ struct PagedParams {
     int b0, nb;                    // the launch's sequences
     int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
     uint32_t over_G, over_Hkv;     // reciprocals (quick_div)
-    float scale_log2e;
+    float scale_log2e;             // of the scores: log2(e) / sqrt(D), times the keys' 2^k_exp
+    float v_unit;                  // E2M1: the values' 2^v_exp (else 1)
 };
 
 struct Seq {
@@ -102,7 +104,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report
 // Hq = 32, Hkv = 8; 5 tokens = 20 rows, 8 tokens = 32 rows, 12 tokens = 48 rows), few against many: e4m3, D = 128:
 // 60 / 76 / 109 against 95 / 98 / 98; D = 64: 43 / 55 / 73 against 62 / 63 / 65; bf16, D = 128: 74 / 95 / 132 against
 // 56 / 58 / 61.
-__host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_E4M3 ? kFewMost : 16; }
+__host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_E4M3 ? kFewMost : 16; }   // E2M1: not measured yet
 __host__ __device__ inline bool few_rows(int n, int G, int type) { return (long long)n * G <= few_most(type); }
 
 // Keys [lo, hi) that rows i0 .. i1 - 1 (tokens) of a sequence see.
@@ -129,7 +131,7 @@ __host__ __device__ inline int few_parts(int n, int G) { return (n * G + kFewRow
 
 // Groups that work through the items: three of a CTA, or two (launch_few).
 __host__ __device__ inline int few_workers(int D, int type) {
-    return type == DASH_CACHE_E4M3 || D == 64 ? kFewWorkers3 : kFewWorkers;
+    return type != DASH_CACHE_BF16 || D == 64 ? kFewWorkers3 : kFewWorkers;
 }
 
 // Key ranges of a sequence: `tiles` stages cut into ns ranges of st stages.  A range costs its start, its queries and its

@@ -115,8 +115,10 @@ struct TileItem {
     long long part;     // partial row of the item's first row
 };
 
-template <int D, bool kE4M3>
+template <int D, int kType>
 struct TileCfg {
+    static constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
+    static constexpr bool kConv = kType != DASH_CACHE_BF16;   // converters, and products in fp16
     static constexpr int kTile = D * 128 * 2;
     static constexpr int kNBox = D / 64;
     static constexpr bool kOwn = kE4M3 && D == 64;   // an O for each half of a tile's keys (tensor memory has room for four)
@@ -124,8 +126,8 @@ struct TileCfg {
     static constexpr int OFF_KV = 2 * kTile;
     static constexpr int OFF_MAX = OFF_KV + kKvStages * kTile;       // [A, B][column half][128 rows] fp32
     static constexpr int OFF_SUM = OFF_MAX + 4 * 128 * 4;            // the same
-    static constexpr int OFF_QFAC = OFF_SUM + 4 * 128 * 4;           // e4m3: [2 items][A, B][128] fp32, 2^-a of each row
-    static constexpr int OFF_KSC = OFF_QFAC + (kE4M3 ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
+    static constexpr int OFF_QFAC = OFF_SUM + 4 * 128 * 4;           // converted: [2 items][A, B][128] fp32, 2^-a of each row
+    static constexpr int OFF_KSC = OFF_QFAC + (kConv ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
     static constexpr int OFF_VFAC = OFF_KSC + (kE4M3 ? 4 * 128 * 4 : 0);        // [4 tiles] the factor of V
     static constexpr int OFF_ITEM = OFF_VFAC + (kE4M3 ? 16 : 0);
     static constexpr int kItemBytes = 128;
@@ -133,13 +135,13 @@ struct TileCfg {
     static constexpr int OFF_CTL = OFF_BAR + T_COUNT * 8;            // tensor memory address, abort flag
     // at least ~117 KB, so that one CTA (and its 512 tensor memory columns) holds an SM
     static constexpr int kSmem = OFF_CTL + 16 > 120000 ? OFF_CTL + 16 : 120000;
-    static constexpr int kThreads = kE4M3 ? 512 : 384;
+    static constexpr int kThreads = kConv ? 512 : 384;
     // registers of the kinds of warpgroups (setmaxnreg), within what the launch grants
-    static constexpr int kRegsLaunch = kE4M3 ? 128 : 168, kRegsCtl = kE4M3 ? 56 : 72, kRegsConv = 120;
-    static constexpr int kRegsSoftmax = kE4M3 ? 168 : 216;
-    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
+    static constexpr int kRegsLaunch = kConv ? 128 : 168, kRegsCtl = kE2M1 ? 48 : kE4M3 ? 56 : 72, kRegsConv = kE2M1 ? 64 : 120;
+    static constexpr int kRegsSoftmax = kE2M1 ? 200 : kE4M3 ? 168 : 216;
+    static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kConv ? 128 * kRegsConv : 0) <= kThreads * kRegsLaunch, "register split");
     // dec must not raise and inc must not lower what the launch granted
-    static_assert(kRegsCtl <= kRegsLaunch && (!kE4M3 || kRegsConv <= kRegsLaunch) && kRegsSoftmax >= kRegsLaunch, "register split");
+    static_assert(kRegsCtl <= kRegsLaunch && (!kConv || kRegsConv <= kRegsLaunch) && kRegsSoftmax >= kRegsLaunch, "register split");
     static_assert(sizeof(TileItem) <= kItemBytes && kSmem <= 232448, "shared memory budget");
 };
 
@@ -284,9 +286,10 @@ __device__ __forceinline__ bool any_of_256(bool v) {
     return r != 0;
 }
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_kernel(const __grid_constant__ PagedParams p) {
-    using C = TileCfg<D, kE4M3>;
+template <int D, int kType>
+__global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_kernel(const __grid_constant__ PagedParams p) {
+    using C = TileCfg<D, kType>;
+    constexpr bool kE4M3 = C::kE4M3, kE2M1 = C::kE2M1, kConv = C::kConv;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -301,9 +304,9 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kE4M3 && ((i >= T_Q_READY && i < T_Q_READY + 2) || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
+            if (kConv && ((i >= T_Q_READY && i < T_Q_READY + 2) || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
             if (i >= T_P_READY && i < T_P_READY + 4) count = 4;                                                         // a softmax warpgroup
-            if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kE4M3 ? 4 : 0);
+            if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kConv ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
         }
         ptx::fence_mbar_init();
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                                     BAR(T_Q_FULL + slot));
                 }
             }
-            if (kE4M3) continue;
+            if (kConv) continue;
             const int sub = lane / C::kNBox, box = lane % C::kNBox;
             const int t1 = it.t0 + it.nk;
             const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(t1 * 128, it.hi) - 1) >> p.page_shift;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             auto q_lo = [&](int x) { return lo0 + kDescK + ((C::OFF_Q + x * C::kTile) >> 4); };
             auto empty = [&](int u) { commit_if(leader, BAR(T_KV_EMPTY + u % kKvStages)); };
             auto scores = [&](int buf, int q, int u) {
-                product_s<D, kE4M3>(leader, tmem + 128 * buf, q_lo(q), stage(u) + kDescK);
+                product_s<D, kConv>(leader, tmem + 128 * buf, q_lo(q), stage(u) + kDescK);
                 commit_if(leader, BAR(T_S_FULL + 2 * q + buf));
             };
             // O_x (+)= P V_j.  bf16: in two halves of the keys, as the weights become ready.  e4m3: each half's warpgroup
@@ -449,17 +452,17 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 // e4m3, one O: both warpgroups have scaled it by then
                 if (kE4M3 && !C::kOwn && !tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
                 ptx::tc_fence_after();
-                product_pv<D, kE4M3>(leader, d, a, b, 0, j > 0 ? 1u : 0u);
+                product_pv<D, kConv>(leader, d, a, b, 0, j > 0 ? 1u : 0u);
                 if (!kE4M3 || C::kOwn) {
                     if (!tile_wait_warp(BAR(T_P_READY + 2 * buf + 1), parity(use), tw)) return false;
                     ptx::tc_fence_after();
                 }
-                product_pv<D, kE4M3>(leader, d + (C::kOwn ? 64 : 0), a, b, 1, !C::kOwn || j > 0 ? 1u : 0u);
+                product_pv<D, kConv>(leader, d + (C::kOwn ? 64 : 0), a, b, 1, !C::kOwn || j > 0 ? 1u : 0u);
                 return true;
             };
             for (int x = 0; ok && x < tiles; ++x) {
                 const int q = tiles == 2 ? x : slot;
-                ok = tile_wait_warp(BAR((kE4M3 ? T_Q_READY : T_Q_FULL) + q), parity(pick(it.q_use, q)), tw);
+                ok = tile_wait_warp(BAR((kConv ? T_Q_READY : T_Q_FULL) + q), parity(pick(it.q_use, q)), tw);
             }
             ok = ok && full(kv0);
             if (!ok) break;
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
         // ================================================== softmax and epilogue
         // e4m3: this warpgroup w has keys 64 w .. of every key tile and columns D/2 w .. of O, of both row tiles (n = 0, 1);
         // bf16: everything of row tile w (n = 0).
-        constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.f;   // maxima are held less this
+        constexpr float kLift = kConv ? kLiftE4M3 : 0.f;   // maxima are held less this
         constexpr int kN = kE4M3 ? 2 : 1, kCols = kE4M3 ? 64 : 128, kOut = kE4M3 ? D / 2 : D;
         const int w = (warp - 4) >> 2;
         const int row = 32 * (warp & 3) + lane;
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                 l[n] = 0.f;
                 c[n] = p.scale_log2e;
             }
-            float vfac = 1.f;   // O holds the sum over vfac
+            float vfac = kE2M1 ? p.v_unit : 1.f;   // O holds the sum over vfac
             for (int j = 0; j < nk && mine(0); ++j) {
                 const int key = (t0 + j) * 128 + (kE4M3 ? 64 * w : 0);   // the first of this thread's columns
                 uint4 s4[8];                                              // e4m3: scales of 32 of them
@@ -693,10 +696,12 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
 #pragma unroll
                         for (int k = 0; k < kCols; ++k) y[k] = __uint_as_float(r[k >> 5][k & 31]);
                     }
-                    if constexpr (kE4M3) {
+                    if constexpr (kConv) {
                         if (j == 0)
                             c[n] *= reinterpret_cast<const float*>(
-                                smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? n : slot)) * 128 + row];
+                                smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? tile(n) : slot)) * 128 + row];
+                    }
+                    if constexpr (kE4M3) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const uint4 f = s4[k & 7];
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
 #pragma unroll
                     for (int k = 8; k < kCols; k += 2) part[(k >> 1) & 3] = fmaxf(fmaxf(part[(k >> 1) & 3], y[k]), y[k + 1]);
                     const float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                    float mx = kE4M3 ? fmaf(c[n], top, -kLift) : c[n] * top;
+                    float mx = kConv ? fmaf(c[n], top, -kLift) : c[n] * top;
                     const bool over = valid[n] && mx > m_ref[n] + 8.f;
                     const bool raise = kE4M3 && !C::kOwn ? any_of_256(over || grown != 1.f) : __any_sync(0xffffffffu, over || grown != 1.f);
                     if (raise) {
@@ -762,7 +767,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                             const ptx::f2 s = ptx::add2({sum[k & 3], sum[(k + 1) & 3]}, v);
                             sum[k & 3] = s.x;
                             sum[(k + 1) & 3] = s.y;
-                            pk[k >> 1] = kE4M3 ? pack_half(v.x, v.y) : pack_bf16(v.x, v.y);
+                            pk[k >> 1] = kConv ? pack_half(v.x, v.y) : pack_bf16(v.x, v.y);
                         }
                         ptx::tmem_st16(tS + 64 * (h >> 1) + 16 * (h & 1), pk);
                         if (h & 1) {
@@ -857,7 +862,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(BAR(T_ITEM_EMPTY + at_slot));
         }
-    } else if (kE4M3) {
+    } else if (kConv) {
         ptx::setmaxnreg_dec<C::kRegsConv>();
         // ================================================== converters
         constexpr int kRows = 512 / D;          // keys that one load instruction of a warp covers (16 codes a lane)
@@ -898,7 +903,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     cell[h] = ((long long)pg * p.c.Hkv + it.hk) * p.c.page_size + (key & (p.c.page_size - 1));
                 }
             };
-            auto load = [&](const void* base, uint4 (&w)[kLoads]) {
+            [[maybe_unused]] auto load = [&](const void* base, uint4 (&w)[kLoads]) {
                 const uint8_t* from[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) from[h] = (const uint8_t*)base + (cell[h] + sub) * D + 16 * chunk;
@@ -919,7 +924,7 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
             // Scales of a key tile (they come with K): the key's own of K, those of this warp's keys of V, and the largest of
             // V so far, for which every warp reads the whole tile's.
             float ks = 0.f, vs = 0.f, vtop = 0.f, v4[4];
-            auto load_scales = [&](int t) {
+            [[maybe_unused]] auto load_scales = [&](int t) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int key = t * 128 + 32 * c + lane;
@@ -930,15 +935,48 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     if (c == cw) ks = in ? __ldg(p.c.k_scale + at) : 0.f;
                 }
             };
-            auto use_scales = [&]() {
+            [[maybe_unused]] auto use_scales = [&]() {
                 vs = cw == 0 ? v4[0] : cw == 1 ? v4[1] : cw == 2 ? v4[2] : v4[3];
                 vtop = fmaxf(vtop, fmaxf(fmaxf(v4[0], v4[1]), fmaxf(v4[2], v4[3])));
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, d));
             };
+            // With the first tile staged: the item's queries, one row per thread (of A, then of B)
+            auto queries = [&]() -> bool {
+#pragma unroll 1
+                for (int x = 0; x < it.tiles; ++x) {
+                    const int q = it.tiles == 2 ? x : it.slot;
+                    if (!tile_wait_warp(BAR(T_Q_FULL + q), parity(pick(it.q_use, q)), tw)) return false;
+                    const int row = 32 * cw + lane;
+                    const uint32_t line = sbase + C::OFF_Q + q * C::kTile + row * 128;
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        float f[8];
+                        unpack_bf16(lds128(line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                    }
+                    float up, down;
+                    power_to(top, 14, up, down);
+                    reinterpret_cast<float*>(smem + C::OFF_QFAC)[((it.qi & 1) * 2 + q) * 128 + row] = down;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t at = line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4);
+                        float f[8];
+                        unpack_bf16(lds128(at), f);
+                        sts128(at, make_uint4(pack_half(f[0] * up, f[1] * up), pack_half(f[2] * up, f[3] * up),
+                                              pack_half(f[4] * up, f[5] * up), pack_half(f[6] * up, f[7] * up)));
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY + q));
+                }
+                return true;
+            };
             // One unit: the codes `w` (loaded during the unit before it) into a stage; `next` (loaded first, so that the proxy
             // fence at the end, which waits for every access before it, finds them there) are the following unit's.
-            auto unit = [&](int u, const uint4 (&w)[kLoads], uint4 (&next)[kLoads]) -> bool {
+            [[maybe_unused]] auto unit = [&](int u, const uint4 (&w)[kLoads], uint4 (&next)[kLoads]) -> bool {
                 const int kv = it.kv + u, st = kv % kKvStages;
                 if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), parity(kv / kKvStages - 1), tw)) return false;
                 const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
@@ -992,46 +1030,68 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
                     ptx::mbar_arrive(BAR(T_KV_FULL + st));
                     if (!(u & 1)) ptx::mbar_arrive(BAR(T_SCALES + ((it.kt + (u >> 1)) & 3)));
                 }
-                if (u != 1) return true;
-                // With the first tile staged: the item's queries, one row per thread (of A, then of B)
-#pragma unroll 1
-                for (int x = 0; x < it.tiles; ++x) {
-                    const int q = it.tiles == 2 ? x : it.slot;
-                    if (!tile_wait_warp(BAR(T_Q_FULL + q), parity(pick(it.q_use, q)), tw)) return false;
-                    const int row = 32 * cw + lane;
-                    const uint32_t line = sbase + C::OFF_Q + q * C::kTile + row * 128;
-                    float top = 0.f;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        float f[8];
-                        unpack_bf16(lds128(line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)), f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-                    }
-                    float up, down;
-                    power_to(top, 14, up, down);
-                    reinterpret_cast<float*>(smem + C::OFF_QFAC)[((it.qi & 1) * 2 + q) * 128 + row] = down;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t at = line + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4);
-                        float f[8];
-                        unpack_bf16(lds128(at), f);
-                        sts128(at, make_uint4(pack_half(f[0] * up, f[1] * up), pack_half(f[2] * up, f[3] * up),
-                                              pack_half(f[4] * up, f[5] * up), pack_half(f[6] * up, f[7] * up)));
-                    }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(BAR(T_Q_READY + q));
-                }
-                return true;
+                return u != 1 || queries();
             };
-            uint4 wk[kLoads], wv[kLoads];
-            aim(it.t0);
-            load_scales(it.t0);
-            load(p.c.k, wk);
-            use_scales();
+            // E2M1: a lane's 16 codes are 8 bytes, and have one scale.  K and V alike: values code * scale, exact in fp16.
+            [[maybe_unused]] auto load4 = [&](const void* base, const void* scales, uint2 (&w)[kLoads], uint32_t (&s)[kLoads]) {
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
+                    const long long at = cell[l >= kLoads / 2] + (l & (kLoads / 2 - 1)) * kRows + sub;
+                    const int key = key0 + kRows * l + sub;
+                    w[l] = make_uint2(0, 0);
+                    s[l] = 0;
+                    if (key >= it.lo && key < it.hi) {   // keys outside the sequence's read as zero
+                        w[l] = __ldg(reinterpret_cast<const uint2*>((const uint8_t*)base + at * (D / 2) + 8 * chunk));
+                        s[l] = __ldg((const uint8_t*)scales + at * (D / 16) + chunk);
+                    }
+                }
+            };
+            [[maybe_unused]] auto unit4 = [&](int u, const uint2 (&w)[kLoads], const uint32_t (&s)[kLoads], uint2 (&next)[kLoads],
+                                              uint32_t (&next_s)[kLoads]) -> bool {
+                const int kv = it.kv + u, st = kv % kKvStages;
+                if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), parity(kv / kKvStages - 1), tw)) return false;
+                const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
+                if (u + 1 < 2 * nk) {
+                    if (u & 1) aim(it.t0 + (u + 1) / 2);
+                    load4((u & 1) ? p.c.k : p.c.v, (u & 1) ? p.c.k_scale : p.c.v_scale, next, next_s);
+                }
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
+                    const uint32_t f = half2_of_e4m3x2(s[l] | s[l] << 8);
+                    const uint32_t c2[2] = {w[l].x, w[l].y};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        o[4 * y] = mul_half2(half2_of_e2m1<0>(c2[y]), f);
+                        o[4 * y + 1] = mul_half2(half2_of_e2m1<1>(c2[y]), f);
+                        o[4 * y + 2] = mul_half2(half2_of_e2m1<2>(c2[y]), f);
+                        o[4 * y + 3] = mul_half2(half2_of_e2m1<3>(c2[y]), f);
+                    }
+                    const uint32_t flip = D == 128 && (l & 1) ? 64u : 0u;
+                    sts128(((dst + to0) ^ flip) + l * kRows * 128, make_uint4(o[0], o[1], o[2], o[3]));
+                    sts128(((dst + to1) ^ flip) + l * kRows * 128, make_uint4(o[4], o[5], o[6], o[7]));
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                return u != 1 || queries();
+            };
+            if constexpr (kE4M3) {
+                uint4 wk[kLoads], wv[kLoads];
+                aim(it.t0);
+                load_scales(it.t0);
+                load(p.c.k, wk);
+                use_scales();
 #pragma unroll 1
-            for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
+                for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
+            } else {
+                uint2 wk[kLoads], wv[kLoads];
+                uint32_t sk[kLoads], sv[kLoads];
+                aim(it.t0);
+                load4(p.c.k, p.c.k_scale, wk, sk);
+#pragma unroll 1
+                for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit4(u, wk, sk, wv, sv) && unit4(u + 1, wv, sv, wk, sk);
+            }
         }
     }
 
@@ -1043,19 +1103,19 @@ __global__ void __launch_bounds__(TileCfg<D, kE4M3>::kThreads, 1) paged_tile_ker
     }
 }
 
-template <int D, bool kE4M3>
+template <int D, int kType>
 int launch_tile_t(const PagedParams& p, int grid, cudaStream_t s) {
-    using C = TileCfg<D, kE4M3>;
+    using C = TileCfg<D, kType>;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_tile_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(paged_tile_kernel<D, kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
-    return launch_after(paged_tile_kernel<D, kE4M3>, grid, C::kThreads, C::kSmem, p, s);
+    return launch_after(paged_tile_kernel<D, kType>, grid, C::kThreads, C::kSmem, p, s);
 }
 
 }  // namespace
@@ -1066,13 +1126,16 @@ int launch_paged_many(const PagedParams& few, int grid, cudaStream_t s) {
     PagedParams p = few;
     const int rows = p.c.page_size < 128 ? p.c.page_size : 128;
     const long long heads = (long long)p.c.num_pages * p.c.Hkv;
-    const bool e4m3 = p.c.type == DASH_CACHE_E4M3;
+    const bool bf16 = p.c.type == DASH_CACHE_BF16, d64 = p.c.D == 64;
     // (pages up to the few-rows kernel's stages have its maps)
-    if ((!e4m3 && rows > kFewKeys && make_tmap_pages(&p.tm_k, &p.tm_v, p.c.k, p.c.v, heads, p.c.page_size, p.c.D, false, rows)) ||
+    if ((bf16 && rows > kFewKeys && make_tmap_pages(&p.tm_k, &p.tm_v, p.c.k, p.c.v, heads, p.c.page_size, p.c.D, p.c.type, rows)) ||
         make_tmap_rows(&p.tm_q, p.q, p.T, p.q_t, p.c.Hkv, p.G, p.q_h, p.c.D, 128 / p.G))
         return DASH_ERR_CUDA;
-    if (e4m3) return p.c.D == 64 ? launch_tile_t<64, true>(p, grid, s) : launch_tile_t<128, true>(p, grid, s);
-    return p.c.D == 64 ? launch_tile_t<64, false>(p, grid, s) : launch_tile_t<128, false>(p, grid, s);
+    if (p.c.type == DASH_CACHE_E2M1)
+        return d64 ? launch_tile_t<64, DASH_CACHE_E2M1>(p, grid, s) : launch_tile_t<128, DASH_CACHE_E2M1>(p, grid, s);
+    if (p.c.type == DASH_CACHE_E4M3)
+        return d64 ? launch_tile_t<64, DASH_CACHE_E4M3>(p, grid, s) : launch_tile_t<128, DASH_CACHE_E4M3>(p, grid, s);
+    return d64 ? launch_tile_t<64, DASH_CACHE_BF16>(p, grid, s) : launch_tile_t<128, DASH_CACHE_BF16>(p, grid, s);
 }
 
 }  // namespace dash

@@ -215,9 +215,13 @@ __device__ __forceinline__ float quotient(float x, float d, float inv) {
 
 // Heads of a token in the order queries, keys, values.  The threads of one
 // vector are U consecutive lanes, whose maximum a butterfly forms.
-template <int D, bool kE4M3>
+//   E2M1: 16 values that share a scale are chunks 2m and 2m + 1 of 8 values, which two threads may hold (or one: chunks()).
+// Each chunk's maximum comes from where its neighbour lies.  Maxima are those of the absolute values' bits, which NaN and
+// infinity lead.
+template <int D, int kType>
 __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ WriteParams p) {
     constexpr int U = D / 16, kAtOnce = 4;
+    constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
     const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
     const bool live = i / U < p.T;   // whole vectors: lanes of one vector agree
     const long long token = live ? i / U : p.T - 1;
@@ -230,6 +234,17 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
     const bool turned = p.positions && unit < rot / 16;
     float cs[8], sn[8];
     if (turned) angles(p.turns, unit, p.positions[token], 1.f, cs, sn);
+    int lane_a = 0, lane_b = 0;      // E2M1: the lanes that hold the neighbours of this thread's chunks
+    bool other_a = false, other_b = false;   // and whether as their second
+    if constexpr (kE2M1) {
+        const int base = (threadIdx.x & 31) & ~(U - 1), ru = rot / 16;
+        auto find = [&](int chunk, int& lane, bool& second) {
+            second = chunk < 2 * ru ? chunk >= ru : chunk & 1;
+            lane = base + (chunk < 2 * ru ? chunk - (second ? ru : 0) : ru + ((chunk - 2 * ru) >> 1));
+        };
+        find((c0 >> 3) ^ 1, lane_a, other_a);
+        find((c1 >> 3) ^ 1, lane_b, other_b);
+    }
 
     const long long slots = (long long)p.c.num_pages * p.c.page_size;
     long long slot = p.slots[token];
@@ -295,6 +310,39 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
                     *reinterpret_cast<uint2*>(to + c1) = make_uint2(q[2], q[3]);
                     if (unit == 0) (val ? p.c.v_scale : p.c.k_scale)[cell] = scale;
                 }
+            } else if (kE2M1) {
+                uint32_t ma = 0, mb = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ma = max(ma, __float_as_uint(a[e]) & 0x7fffffffu);
+                    mb = max(mb, __float_as_uint(b[e]) & 0x7fffffffu);
+                }
+                const uint32_t a0 = __shfl_sync(0xffffffffu, ma, lane_a), a1 = __shfl_sync(0xffffffffu, mb, lane_a);
+                const uint32_t b0 = __shfl_sync(0xffffffffu, ma, lane_b), b1 = __shfl_sync(0xffffffffu, mb, lane_b);
+                ma = max(ma, other_a ? a1 : a0);
+                mb = max(mb, other_b ? b1 : b0);
+                const float unit_ = __uint_as_float((uint32_t)(127 + (val ? p.c.v_exp : p.c.k_exp)) << 23);
+                // codes of 8 values whose 16 have the maximum `top`, and the scale's code
+                auto quantise = [&](const float (&x)[8], uint32_t top, uint32_t& codes) -> uint32_t {
+                    const float s = fminf(fmaxf(__fdiv_rn(__uint_as_float(top), 6.f * unit_), 0x1p-9f), 448.f);
+                    const uint32_t code = pack_e4m3x4(s, 0.f, 0.f, 0.f);
+                    const float d = unpack_e4m3x2((uint16_t)code).x * unit_, inv = __frcp_rn(d);
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = quotient(x[e], d, inv);
+                    codes = pack_e2m1x8(y);
+                    return top >= 0x7f800000u ? 0x7fu : code;
+                };
+                uint32_t qa, qb;
+                const uint32_t sa = quantise(a, ma, qa), sb = quantise(b, mb, qb);
+                if (kept) {
+                    uint8_t* to = reinterpret_cast<uint8_t*>(pages) + cell * (D / 2);
+                    *reinterpret_cast<uint32_t*>(to + c0 / 2) = qa;
+                    *reinterpret_cast<uint32_t*>(to + c1 / 2) = qb;
+                    uint8_t* sc = reinterpret_cast<uint8_t*>(val ? p.c.v_scale : p.c.k_scale) + cell * (D / 16);
+                    if (!(c0 & 8)) sc[c0 >> 4] = (uint8_t)sa;
+                    if (!(c1 & 8)) sc[c1 >> 4] = (uint8_t)sb;
+                }
             } else if (kept) {
                 store8<false>(pages, cell * D + c0, a);
                 store8<false>(pages, cell * D + c1, b);
@@ -314,12 +362,18 @@ struct ReadParams {
 };
 
 // 8 values as bf16: a cell's codes times its scale, or the values themselves.
-template <bool kE4M3>
+template <int D, int kType>
 struct Cell8 {
+    static constexpr bool kE4M3 = kType == DASH_CACHE_E4M3;
     uint4 w;
     float scale;
-    __device__ __forceinline__ void load(const void* pages, const float* scales, long long cell, long long at) {
-        if (kE4M3) {
+    __device__ __forceinline__ void load(const void* pages, const float* scales, long long cell, int d, float unit) {
+        const long long at = cell * D + d;
+        if (kType == DASH_CACHE_E2M1) {
+            w.x = __ldcs(reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(pages) + at / 2));
+            w.y = reinterpret_cast<const uint8_t*>(scales)[at / 16];
+            scale = unit;
+        } else if (kE4M3) {
             const uint2 u = __ldcs(reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(pages) + at));
             w.x = u.x, w.y = u.y;
             scale = scales[cell];
@@ -328,8 +382,19 @@ struct Cell8 {
         }
     }
     __device__ __forceinline__ uint4 get() const {
-        if (!kE4M3) return w;
+        if (kType == DASH_CACHE_BF16) return w;
         float x[8];
+        if (kType == DASH_CACHE_E2M1) {
+            const float s = unpack_e4m3x2((uint16_t)w.y).x * scale;
+            const uint32_t h[4] = {half2_of_e2m1<0>(w.x), half2_of_e2m1<1>(w.x), half2_of_e2m1<2>(w.x), half2_of_e2m1<3>(w.x)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = float2_of_half2(h[i]);
+                x[2 * i] = f.x * s;
+                x[2 * i + 1] = f.y * s;
+            }
+            return pack_bf16x8(x);
+        }
         unpack_e4m3x8(make_uint2(w.x, w.y), x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= scale;
@@ -338,9 +403,11 @@ struct Cell8 {
 };
 
 // D / 8 threads per token, 4 tokens of each thread at a time; blockIdx.y is the head, blockIdx.z the sequence.
-template <int D, bool kE4M3>
+template <int D, int kType>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int C = D / 8, kRows = 256 / C, kAtOnce = 4;
+    const float k_unit = kType == DASH_CACHE_E2M1 ? __uint_as_float((uint32_t)(127 + p.c.k_exp) << 23) : 1.f;
+    const float v_unit = kType == DASH_CACHE_E2M1 ? __uint_as_float((uint32_t)(127 + p.c.v_exp) << 23) : 1.f;
     const int d = 8 * (threadIdx.x % C), r = threadIdx.x / C;
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const long long cap = (long long)p.max_pages * p.c.page_size;
@@ -353,7 +420,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
         const int len = (int)(given < p.S ? given : p.S);
         for (int h = blockIdx.y; h < p.c.Hkv; h += gridDim.y)
             for (int j0 = blockIdx.x * kRows * kAtOnce + r; j0 < len; j0 += gridDim.x * kRows * kAtOnce) {
-                Cell8<kE4M3> k[kAtOnce], v[kAtOnce];
+                Cell8<D, kType> k[kAtOnce], v[kAtOnce];
                 bool ok[kAtOnce];
                 int page[kAtOnce];
 #pragma unroll
@@ -368,8 +435,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
                     if (j < len && !ok[i]) serve_error(DASH_ERR_PAGE, kOpRead, b, page[i], p.c.num_pages);
                     if (!ok[i]) continue;
                     const long long cell = ((long long)page[i] * p.c.Hkv + h) * p.c.page_size + (j & (p.c.page_size - 1));
-                    k[i].load(p.c.k, p.c.k_scale, cell, cell * D + d);
-                    v[i].load(p.c.v, p.c.v_scale, cell, cell * D + d);
+                    k[i].load(p.c.k, p.c.k_scale, cell, d, k_unit);
+                    v[i].load(p.c.v, p.c.v_scale, cell, d, v_unit);
                 }
 #pragma unroll
                 for (int i = 0; i < kAtOnce; ++i) {
@@ -572,12 +639,15 @@ extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int
     prm.per = heads_per_block(blocks, prm.Hq + 2 * cache->Hkv);
     const dim3 grid((unsigned)blocks, (unsigned)((prm.Hq + 2 * cache->Hkv + prm.per - 1) / prm.per));
     cudaStream_t s = (cudaStream_t)stream;
-    if (cache->type == DASH_CACHE_E4M3) {
-        if (D == 64) write_kernel<64, true><<<grid, 128, 0, s>>>(prm);
-        else write_kernel<128, true><<<grid, 128, 0, s>>>(prm);
+    if (cache->type == DASH_CACHE_E2M1) {
+        if (D == 64) write_kernel<64, DASH_CACHE_E2M1><<<grid, 128, 0, s>>>(prm);
+        else write_kernel<128, DASH_CACHE_E2M1><<<grid, 128, 0, s>>>(prm);
+    } else if (cache->type == DASH_CACHE_E4M3) {
+        if (D == 64) write_kernel<64, DASH_CACHE_E4M3><<<grid, 128, 0, s>>>(prm);
+        else write_kernel<128, DASH_CACHE_E4M3><<<grid, 128, 0, s>>>(prm);
     } else {
-        if (D == 64) write_kernel<64, false><<<grid, 128, 0, s>>>(prm);
-        else write_kernel<128, false><<<grid, 128, 0, s>>>(prm);
+        if (D == 64) write_kernel<64, DASH_CACHE_BF16><<<grid, 128, 0, s>>>(prm);
+        else write_kernel<128, DASH_CACHE_BF16><<<grid, 128, 0, s>>>(prm);
     }
     return launched();
 }
@@ -614,12 +684,15 @@ extern "C" int dash_kv_read(const dash_kv_cache* cache, const int32_t* block_tab
     const dim3 grid((unsigned)(x < 65536 ? x : 65536), (unsigned)(cache->Hkv < 65535 ? cache->Hkv : 65535),
                     (unsigned)(B < 65535 ? B : 65535));
     cudaStream_t s = (cudaStream_t)stream;
-    if (cache->type == DASH_CACHE_E4M3) {
-        if (D == 64) read_kernel<64, true><<<grid, 256, 0, s>>>(prm);
-        else read_kernel<128, true><<<grid, 256, 0, s>>>(prm);
+    if (cache->type == DASH_CACHE_E2M1) {
+        if (D == 64) read_kernel<64, DASH_CACHE_E2M1><<<grid, 256, 0, s>>>(prm);
+        else read_kernel<128, DASH_CACHE_E2M1><<<grid, 256, 0, s>>>(prm);
+    } else if (cache->type == DASH_CACHE_E4M3) {
+        if (D == 64) read_kernel<64, DASH_CACHE_E4M3><<<grid, 256, 0, s>>>(prm);
+        else read_kernel<128, DASH_CACHE_E4M3><<<grid, 256, 0, s>>>(prm);
     } else {
-        if (D == 64) read_kernel<64, false><<<grid, 256, 0, s>>>(prm);
-        else read_kernel<128, false><<<grid, 256, 0, s>>>(prm);
+        if (D == 64) read_kernel<64, DASH_CACHE_BF16><<<grid, 256, 0, s>>>(prm);
+        else read_kernel<128, DASH_CACHE_BF16><<<grid, 256, 0, s>>>(prm);
     }
     return launched();
 }

@@ -85,16 +85,66 @@ __device__ __forceinline__ void unpack_e4m3x8(const uint2& u, float (&x)[8]) {
     }
 }
 
+// Eight fp32 values to eight e2m1 codes (round to nearest even, at most 6), the first in the lowest bits.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+// Byte i of `codes` (two e2m1 codes) as fp16 (exact).
+template <int i>
+__device__ __forceinline__ uint32_t half2_of_e2m1(uint32_t codes) {
+    uint32_t h;
+    if (i == 0) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(codes));
+    if (i == 1) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(codes));
+    if (i == 2) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+    if (i == 3) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(h) : "r"(codes));
+    return h;
+}
+// Two e4m3 codes as fp16 (exact; NaN stays NaN).
+__device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return h;
+}
+// Two fp16 products.  An e2m1 code (2 bits) times an e4m3 scale (4 bits, 2^-9 .. 448) is exact.
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 float2_of_half2(uint32_t h2) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+    return make_float2(lo, hi);
+}
+
+// Bytes of a cached vector, and of its scales.
+__host__ __device__ constexpr int cell_bytes(int type, int D) {
+    return type == DASH_CACHE_BF16 ? 2 * D : type == DASH_CACHE_E4M3 ? D : D / 2;
+}
+__host__ __device__ constexpr int scale_bytes(int type, int D) {
+    return type == DASH_CACHE_BF16 ? 0 : type == DASH_CACHE_E4M3 ? 4 : D / 16;
+}
+
 // ---------------------------------------------------------------- host checks
 inline bool serve_aligned(const void* p) { return p && (((uintptr_t)p) & 15u) == 0; }
 inline bool serve_strides(int64_t a, int64_t b) { return a >= 0 && b >= 0 && a % 8 == 0 && b % 8 == 0; }
 
 inline int check_cache(const dash_kv_cache* c) {
     if (!c || !serve_aligned(c->k) || !serve_aligned(c->v)) return DASH_ERR_ARG;
-    if (c->type != DASH_CACHE_BF16 && c->type != DASH_CACHE_E4M3) return DASH_ERR_ARG;
-    if (c->type == DASH_CACHE_E4M3 ? (!serve_aligned(c->k_scale) || !serve_aligned(c->v_scale))
+    if (c->type != DASH_CACHE_BF16 && c->type != DASH_CACHE_E4M3 && c->type != DASH_CACHE_E2M1) return DASH_ERR_ARG;
+    if (c->type != DASH_CACHE_BF16 ? (!serve_aligned(c->k_scale) || !serve_aligned(c->v_scale))
                                    : (c->k_scale || c->v_scale))
         return DASH_ERR_ARG;
+    if (c->type == DASH_CACHE_E2M1 && (c->k_exp < -64 || c->k_exp > 64 || c->v_exp < -64 || c->v_exp > 64)) return DASH_ERR_ARG;
     if (c->num_pages <= 0 || c->Hkv <= 0 || (c->D != 64 && c->D != 128)) return DASH_ERR_ARG;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return DASH_ERR_ARG;
     if ((long long)c->num_pages * c->Hkv >= (1ll << 31)) return DASH_ERR_ARG;

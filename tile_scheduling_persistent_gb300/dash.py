@@ -58,6 +58,7 @@ class _DebugOpts(ctypes.Structure):
 # costs a fifth of a ctypes.Structure on calls that last a few microseconds.
 _HEADS = struct.Struct("@Piiqqq")
 _CACHE = struct.Struct("@PPPPiiiii0P")
+_CACHE_EXP = struct.Struct("@PPPPiiiiihh0P")   # the same, with the exponents of a cache of 4 bits
 _WRITE_ROPE = struct.Struct("@PPiifPqqPqqi0P")
 
 
@@ -341,6 +342,7 @@ def tile_probe(k, v, q, do, lse, delta, diag=False):
 # ------------------------------------------------------------------ rotary positions, paged cache, paged attention
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wave": 3, "ramp": 4}
 _BF16, _F32, _I32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
+_U8, _E2M1X2 = torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)   # two e2m1 values to a byte
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
@@ -399,7 +401,7 @@ def _heads(t, dev, what, name):
     return _HEADS.pack(t.data_ptr(), dtype is _F32, H, sb, sh, ss), (sb, sh, ss)
 
 
-def _cache(k, v, k_scale, v_scale, dev, what):
+def _cache(k, v, k_scale, v_scale, k_exp, v_exp, dev, what):
     """dash_kv_cache, its Hkv, page_size and D."""
     shape = k.shape
     if len(shape) != 4:
@@ -411,8 +413,16 @@ def _cache(k, v, k_scale, v_scale, dev, what):
         if k_scale is not None or v_scale is not None:
             _refuse(what, "a bf16 cache has no scales")
         return _CACHE.pack(kp, vp, 0, 0, 0, N, page, H, D), H, page, D
+    if dtype is _U8 or dtype is _E2M1X2:
+        if k_scale is None or v_scale is None:
+            _refuse(what, "a cache of 4 bits has k_scale and v_scale")
+        if not (-64 <= k_exp <= 64 and -64 <= v_exp <= 64):
+            _refuse(what, "k_exp and v_exp are within -64 .. 64")
+        shape = (N, H, page, D // 8)
+        return _CACHE_EXP.pack(kp, vp, _flat(k_scale, _E4M3, dev, shape, what, "k_scale"),
+                               _flat(v_scale, _E4M3, dev, shape, what, "v_scale"), 2, N, page, H, 2 * D, k_exp, v_exp), H, page, 2 * D
     if dtype is not _E4M3 or k_scale is None or v_scale is None:
-        _refuse(what, "the cache is bf16, or float8_e4m3fn with k_scale and v_scale")
+        _refuse(what, "the cache is bf16, or float8_e4m3fn or uint8 (4 bits) with k_scale and v_scale")
     shape = (N, H, page)
     return _CACHE.pack(kp, vp, _flat(k_scale, _F32, dev, shape, what, "k_scale"),
                        _flat(v_scale, _F32, dev, shape, what, "v_scale"), 1, N, page, H, D), H, page, D
@@ -483,15 +493,17 @@ def rope(x, y, inv_freq, positions=None, x2=None, y2=None, interleaved=False, fa
 
 
 def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq=None, positions=None,
-             interleaved=False, factor=1.0, q=None, q_out=None, stream=None):
+             interleaved=False, factor=1.0, q=None, q_out=None, stream=None, k_exp=0, v_exp=0):
     """Write new tokens' k, v [T, Hkv, D] (bf16, any token and head strides) into
     the pages [num_pages, Hkv, page_size, D] at slots int64 [T] (page * page_size +
     offset, no two the same; negative: skipped); an e4m3 cache (torch.float8_e4m3fn) quantises each
-    vector with its own scale.  inv_freq and positions int32 [T]: k is rotated on
+    vector with its own scale.  A cache of 4 bits is uint8 (or float4_e2m1fn_x2) [num_pages, Hkv, page_size, D / 2]
+    with float8_e4m3fn scales [num_pages, Hkv, page_size, D / 16] in units of 2^k_exp and 2^v_exp (see dash_kv_cache),
+    the same exponents in every call.  inv_freq and positions int32 [T]: k is rotated on
     the way (see rope), and q [T, Hq, D] into q_out."""
     what = "dash_kv_write"
     dev, st = _device_stream(stream, what)
-    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, dev, what)
     T = k.shape[0]
     shape = (T, Hkv, D)
     kp, kt, kh = _tokens(k, dev, shape, what, "k")
@@ -519,13 +531,13 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
     _check(lib().dash_kv_write(c, kp, kt, kh, vp, vt, vh, sp, T, r, st), what)
 
 
-def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None):
+def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None, k_exp=0, v_exp=0):
     """k, v [B, Hkv, S, D] (bf16, equal strides) <- the first lens[b] cached tokens of
     each sequence; rows past lens[b] are left as they were.  block_table int32
     [B, pages], lens int32 [B]."""
     what = "dash_kv_read"
     dev, st = _device_stream(stream, what)
-    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, dev, what)
     (_, ks), (_, vs) = _heads(k, dev, what, "k"), _heads(v, dev, what, "v")
     shape = k.shape
     B, H, S, d = shape
@@ -577,7 +589,7 @@ def attn_paged_workspace(B, T, Hq, Hkv, D, max_q, max_kv):
 
 
 def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=None, lse=None, causal=True, window=None,
-               k_scale=None, v_scale=None, workspace=None, stream=None):
+               k_scale=None, v_scale=None, workspace=None, stream=None, k_exp=0, v_exp=0):
     """o [T, Hq, D] (and lse fp32 [T, Hq]) <- attention of each sequence's newest
     tokens q [T, Hq, D] over its kv_lens[b] cached tokens, the new ones among them
     (see dash_attn_paged).  cu_q int32 [B+1] are the sequences' first rows (None:
@@ -587,7 +599,7 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     is not being captured, 256 MiB in all; release_workspaces frees it)."""
     what = "dash_attn_paged"
     dev, st = _device_stream(stream, what)
-    c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, dev, what)
+    c, Hkv, page, D = _cache(k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, dev, what)
     shape = q.shape
     if len(shape) != 3 or shape[2] != D:
         _refuse(what, "q is [T, Hq, D]")
