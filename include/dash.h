@@ -547,17 +547,105 @@ int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q_stride_h, 
 /* *bytes = the workspace dash_attn_paged needs (0: none).  Host only.  Returns DASH_OK or DASH_ERR_ARG. */
 int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, int64_t max_kv, size_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * The pages of a cache.  The state is the caller's device memory: the block
+ * table int32 [rows, max_pages] (strides in elements, at least max_pages), the
+ * rows' lengths in tokens int32 [rows], and refs int32 [num_pages], the number
+ * of table entries that hold a page (0: the page is free; more than the table's
+ * own entries: held elsewhere too, a kept prefix say).  A row of len tokens holds
+ * ceil(len / page_size) pages; entries behind them mean nothing.  One table
+ * serves every layer's cache.  page_size as in dash_kv_cache; num_pages up to
+ * 2^30; refs and workspaces 16-byte aligned.  What these calls write is whole
+ * numbers, the same in every run.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * dash_pages_fork -- the rows of a new table from those of an old one: row i of
+ * table_out [rows_out, max_pages] and lens_out holds the pages and the length of
+ * row parents[i] (device int32 [rows_out]) of table and lens [rows, ...], or
+ * nothing when parents[i] is negative; entries behind a row's pages become -1.
+ * Pages are shared, not copied, and refs follows: each page's count changes by
+ * the entries of the new table that hold it less those of the old one.  So one
+ * call forks a row (several children), keeps it (one), drops it (none: its pages
+ * are freed where nobody else holds them), and any mixture, a beam's step say.
+ * The old table is void afterwards; it and the new one must not overlap.
+ * A parent past the last row counts as none, a length or an entry out of range
+ * is left out of the counts, and a count that would fall below zero is reported
+ * too (DASH_ERR_PAGE).
+ * Returns DASH_OK (also without rows), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* lens, int rows,
+                    const int32_t* parents, int32_t* table_out, int64_t out_stride, int32_t* lens_out, int rows_out,
+                    int max_pages, int32_t* refs, int num_pages, int page_size, dash_stream_t stream);
+
+/*
+ * dash_pages_extend -- pages for new tokens: row r gets n = cu_new[r+1] - cu_new[r]
+ * more (cu_new: device int32 [rows+1], non-decreasing from 0, as cu_q of
+ * dash_attn_paged; NULL: T / rows each).  Whole pages are taken from the free
+ * ones, lowest first, for the rows in order and each row's entries in order;
+ * table, lens and refs change in place.  A partly filled last page that other
+ * entries hold too is replaced by a new one first (it comes before the row's
+ * other new pages): copies [rows][2] (device int32) lists (from, to) for
+ * dash_kv_copy, in the order of rows; where the rows that extend a page are all
+ * that hold it, the first of them keeps it.  counts[0] (device int32 [2]) = pages
+ * to copy, counts[1] = pages taken.
+ * Token cu_new[r] + i gets positions[...] = lens[r] + i (before the call) and
+ * slots[...] = its slot, for dash_kv_write (device int32 and int64 [T]); tokens
+ * from cu_new[rows] to T get slot -1 and position 0.
+ * With fewer free pages than are needed nothing is taken: counts are 0, every slot
+ * is -1, table, lens and refs are as they were, and DASH_ERR_NOMEM is reported
+ * (needed and free).  A row whose length, tokens or last page is out of range, or
+ * whose pages would pass max_pages, is reported (DASH_ERR_PAGE) and left as it
+ * is, its slots -1; other rows are not affected.  At most 4096 rows.
+ * Returns DASH_OK, DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_pages_extend(int32_t* table, int64_t table_stride, int32_t* lens, int rows, int max_pages, int32_t* refs,
+                      int num_pages, int page_size, const int32_t* cu_new, int64_t* slots, int32_t* positions, int T,
+                      int32_t* copies, int32_t* counts, dash_stream_t stream);
+
+/*
+ * dash_pages_compact -- the pages in use moved to the front of the pool: with L of
+ * them, the k-th in use from page L on moves to the k-th free one below L.
+ * table_out and refs_out (which may be table and refs, with their strides) are
+ * the renamed table and counts; copies [num_pages / 2][2] lists (from, to) in
+ * ascending order, for dash_kv_copy and for who else holds pages; counts[0] =
+ * pages that move, counts[1] = L.  lens are the rows'; entries behind a row's
+ * pages are copied as they are; an entry out of range, or of a free page, too,
+ * and is reported (DASH_ERR_PAGE).
+ *   workspace: 4 * num_pages bytes of device memory, as dash_attn_paged's.
+ * Returns DASH_OK, DASH_ERR_ARG, DASH_ERR_SCRATCH, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_pages_compact(const int32_t* table, int64_t table_stride, const int32_t* lens, int rows, int max_pages,
+                       const int32_t* refs, int num_pages, int page_size, int32_t* table_out, int64_t out_stride,
+                       int32_t* refs_out, int32_t* copies, int32_t* counts, void* workspace, size_t workspace_bytes,
+                       dash_stream_t stream);
+
+/*
+ * dash_kv_copy -- copy pages (all heads, keys, values and scales) within each of
+ * n_caches caches of one type and shape, a model's layers: page copies[i][0] to
+ * page copies[i][1] (device int32) for i < min(*n_copies, max_copies) (device
+ * int32, the counts of the calls above; NULL: max_copies).  No page is the target
+ * of two copies, or of one and the source of another.  A pair with a page outside
+ * the cache is reported (DASH_ERR_PAGE) and not copied.  caches: host memory, read
+ * before the call returns.
+ * Returns DASH_OK (also for no caches or copies), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
+ */
+int dash_kv_copy(const dash_kv_cache* caches, int n_caches, const int32_t* copies, const int32_t* n_copies,
+                 int max_copies, dash_stream_t stream);
+
 /*
  * dash_get_status_paged -- synchronizes `stream` and reports an error that
- * dash_kv_write, dash_kv_read or dash_attn_paged recorded on the current
- * device, on any stream (others are not waited for): *code = DASH_OK,
- * DASH_ERR_PAGE, DASH_ERR_TIMEOUT, or DASH_ERR_SCRATCH where sequences were cut
+ * dash_kv_write, dash_kv_read, dash_attn_paged or a call for pages recorded on the
+ * current device, on any stream (others are not waited for): *code = DASH_OK,
+ * DASH_ERR_PAGE, DASH_ERR_TIMEOUT, DASH_ERR_NOMEM where dash_pages_extend found too
+ * few free pages, or DASH_ERR_SCRATCH where sequences were cut
  * into more partial rows than the workspace holds (an error of the library, after
  * which outputs are undefined; nothing is written past the workspace); info[0..3] (may be NULL) = {operator
- * (1 write, 2 read, 3 attention), sequence or token, value found, its bound}.
- * Three records are kept, each the first error since it was last reported: of
+ * (1 write, 2 read, 3 attention, 4 fork, 5 extend, 6 compact, 7 copy), sequence, row, token or pair, value found, its
+ * bound}.
+ * Four records are kept, each the first error since it was last reported: of
  * the writer and reader, of the attention's sequences of few rows (and of the
- * lengths and row counts of all), and of those of many.  A call reports one, a
+ * lengths and row counts of all), of those of many, and of the calls for pages.  A call reports one, a
  * DASH_ERR_TIMEOUT before the others and then in that order, and clears that
  * one alone: the next call reports the next, until DASH_OK.
  * Returns DASH_OK, DASH_ERR_ARG (code NULL) or DASH_ERR_CUDA.

@@ -701,9 +701,9 @@ extern "C" int dash_get_status_paged(dash_stream_t stream, int* code, int* info)
     if (!code) return DASH_ERR_ARG;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return DASH_ERR_CUDA;
     // one record per translation unit; all are read before one is cleared, and only the one reported is
-    int (*const record[3])(int*, bool) = {error_rope, error_paged, error_tile};
-    int r[3][5], pick = -1;
-    for (int i = 0; i < 3; ++i) {
+    int (*const record[4])(int*, bool) = {error_rope, error_paged, error_tile, error_pages};
+    int r[4][5], pick = -1;
+    for (int i = 0; i < 4; ++i) {
         const int rc = record[i](r[i], false);
         if (rc) return rc;
         if (r[i][0] && (pick < 0 || (r[i][0] == DASH_ERR_TIMEOUT && r[pick][0] != DASH_ERR_TIMEOUT))) pick = i;

@@ -10,7 +10,7 @@
 
 namespace dash {
 
-enum ServeOp : int { kOpWrite = 1, kOpRead = 2, kOpAttn = 3 };
+enum ServeOp : int { kOpWrite = 1, kOpRead = 2, kOpAttn = 3, kOpFork = 4, kOpExtend = 5, kOpCompact = 6, kOpCopy = 7 };
 
 // First error of this translation unit's kernels on the device since it was
 // last cleared: code, then info[4]; word 7 is claimed by the thread that writes
@@ -156,5 +156,6 @@ int serve_check_device();   // DASH_OK on sm_103 (dash_rope.cu)
 int error_rope(int* out5, bool clear);
 int error_paged(int* out5, bool clear);
 int error_tile(int* out5, bool clear);
+int error_pages(int* out5, bool clear);
 
 }  // namespace dash

@@ -35,7 +35,7 @@ EXPORTS = (
     "dash_sim_schedule_cross", "dash_attn_bwd_cross", "dash_attn_fwd_cross", "dash_head_split", "dash_key_blocks",
     "dash_noalloc_init", "dash_get_status_noalloc",
     "dash_rope", "dash_rope_freqs", "dash_kv_write", "dash_kv_read", "dash_attn_paged", "dash_attn_paged_workspace",
-    "dash_get_status_paged",
+    "dash_get_status_paged", "dash_pages_fork", "dash_pages_extend", "dash_pages_compact", "dash_kv_copy",
 )
 
 
@@ -97,6 +97,10 @@ def lib():
     L.dash_kv_read.argtypes = [P, P, L64, I, P, P, P, L64, L64, L64, I, I, P]
     L.dash_attn_paged.argtypes = [P, L64, L64, P, P, L64, I, P, P, P, P, I, I, I, I, I, I, P, Z, P]
     L.dash_attn_paged_workspace.argtypes = [I, I, I, I, I, I, L64, ctypes.POINTER(Z)]
+    L.dash_pages_fork.argtypes = [P, L64, P, I, P, P, L64, P, I, I, P, I, I, P]
+    L.dash_pages_extend.argtypes = [P, L64, P, I, I, P, I, I, P, P, P, I, P, P, P]
+    L.dash_pages_compact.argtypes = [P, L64, P, I, I, P, I, I, P, L64, P, P, P, P, Z, P]
+    L.dash_kv_copy.argtypes = [P, I, P, P, I, P]
     L.dash_get_status_paged.argtypes = [P, ctypes.POINTER(I), ctypes.POINTER(I)]
     for name in EXPORTS:
         getattr(L, name).restype = ctypes.c_int
@@ -633,8 +637,94 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
                                  wp, wn, st), what)
 
 
+def _pool(table, lens, refs, dev, what):
+    """The addresses of a block table [rows, max_pages], lens and refs, the table's stride, rows and width, the pages."""
+    if len(lens.shape) != 1 or len(refs.shape) != 1:
+        _refuse(what, "lens is int32 [rows] and refs int32 [num_pages]")
+    rows = lens.shape[0]
+    tp, ts, width = _table(table, rows, dev, what)
+    if rows > 1 and ts < width:
+        _refuse(what, "rows of the block table do not overlap")
+    N = refs.shape[0]
+    return tp, ts, _flat(lens, _I32, dev, (rows,), what, "lens"), rows, width, _flat(refs, _I32, dev, (N,), what, "refs"), N
+
+
+def pages_fork(table, lens, parents, table_out, lens_out, refs, page_size, stream=None):
+    """table_out [rows_out, max_pages], lens_out [rows_out] <- rows parents int32 [rows_out] (negative: none) of table
+    and lens, sharing their pages; refs int32 [num_pages] counts the table entries that hold each page.  Rows without a
+    child are dropped, their pages freed (see dash_pages_fork)."""
+    what = "dash_pages_fork"
+    dev, st = _device_stream(stream, what)
+    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
+    op, os_, olp, rows_out, width_out, _, _ = _pool(table_out, lens_out, refs, dev, what)
+    if width != width_out:
+        _refuse(what, "table and table_out have the same width")
+    _check(lib().dash_pages_fork(tp, ts, lp, rows, _flat(parents, _I32, dev, (rows_out,), what, "parents"), op, os_, olp, rows_out, width,
+                                 rp, N, page_size, st), what)
+
+
+def pages_extend(table, lens, refs, page_size, slots, positions, copies, counts, cu_new=None, stream=None):
+    """Pages for new tokens of the rows of table [rows, max_pages], with lens and refs changed in place: row r gets
+    cu_new[r + 1] - cu_new[r] of them (int32 [rows + 1]; None: T / rows each), whose slots int64 [T] and positions int32
+    [T] kv_write takes.  copies int32 [rows, 2] and counts int32 [2] (pages to copy, pages taken) are for kv_copy: shared
+    pages that rows go on in (see dash_pages_extend)."""
+    what = "dash_pages_extend"
+    dev, st = _device_stream(stream, what)
+    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
+    T = slots.shape[0] if len(slots.shape) == 1 else -1
+    _check(lib().dash_pages_extend(tp, ts, lp, rows, width, rp, N, page_size,
+                                   _flat(cu_new, _I32, dev, (rows + 1,), what, "cu_new") if cu_new is not None else None,
+                                   _flat(slots, _I64, dev, (T,), what, "slots"), _flat(positions, _I32, dev, (T,), what, "positions"), T,
+                                   _flat(copies, _I32, dev, (rows, 2), what, "copies"), _flat(counts, _I32, dev, (2,), what, "counts"),
+                                   st), what)
+
+
+def pages_compact(table, lens, refs, page_size, copies, counts, table_out=None, refs_out=None, workspace=None, stream=None):
+    """table_out, refs_out (None: table and refs themselves) <- table and refs with the pages in use at the front of the
+    pool; copies int32 [num_pages / 2, 2] and counts int32 [2] (pages that move, pages in use) are for kv_copy (see
+    dash_pages_compact).  workspace: uint8 tensor of 4 * num_pages bytes (None: as attn_paged's)."""
+    what = "dash_pages_compact"
+    dev, st = _device_stream(stream, what)
+    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
+    table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
+    op, os_, _, _, width_out, orp, N_out = _pool(table_out, lens, refs_out, dev, what)
+    if width != width_out or N != N_out:
+        _refuse(what, "table_out and refs_out have the shapes of table and refs")
+    wn = 4 * N
+    if workspace is None:
+        if stream is None:
+            workspace = _workspace(wn, dev, st)
+        else:
+            with torch.cuda.stream(stream):   # the allocator's reuse then follows this stream
+                workspace = torch.empty(wn, dtype=_U8, device=table.device)
+        wp = workspace.data_ptr()
+    else:
+        wn = workspace.numel()
+        wp = _flat(workspace, _U8, dev, (wn,), what, "workspace")
+    _check(lib().dash_pages_compact(tp, ts, lp, rows, width, rp, N, page_size, op, os_, orp,
+                                    _flat(copies, _I32, dev, (N // 2, 2), what, "copies"), _flat(counts, _I32, dev, (2,), what, "counts"),
+                                    wp, wn, st), what)
+
+
+def kv_copy(k_caches, v_caches, copies, counts=None, k_scales=(), v_scales=(), stream=None):
+    """Copy pages within the caches of one or several layers (lists of caches of one shape, and of their scales): page
+    copies[i, 0] to copies[i, 1] (int32 [n, 2]) for i < counts[0] (int32 [2] as pages_extend and pages_compact leave
+    it; None: all of them)."""
+    what = "dash_kv_copy"
+    dev, st = _device_stream(stream, what)
+    n = len(k_caches)
+    if len(v_caches) != n or len(k_scales) != len(v_scales) or (len(k_scales) != n and len(k_scales) != 0):
+        _refuse(what, "there are as many caches, and scales if any, of values as of keys")
+    if len(copies.shape) != 2 or copies.shape[1] != 2:
+        _refuse(what, "copies is int32 [n, 2]")
+    packed = b"".join([_cache(k, v, ks, vs, 0, 0, dev, what)[0]
+                       for k, v, ks, vs in zip(k_caches, v_caches, k_scales or [None] * n, v_scales or [None] * n)])
+    _check(lib().dash_kv_copy(packed, n, _flat(copies, _I32, dev, (copies.shape[0], 2), what, "copies"),
+                              _flat(counts, _I32, dev, (2,), what, "counts") if counts is not None else None, copies.shape[0], st), what)
+
+
 def get_status_paged(stream=None):
-    """(code, info) of an error that kv_write, kv_read or attn_paged recorded on the
+    """(code, info) of an error that kv_write, kv_read, attn_paged or a call for pages recorded on the
     current device, which is then cleared; synchronizes `stream`.  Errors of several
     operators come one a call, until the code is 0 (see dash_get_status_paged)."""
     code = ctypes.c_int(0)
