@@ -94,7 +94,9 @@ enum TileBar : int {
     T_ITEM_EMPTY = T_ITEM_FULL + kItemSlots,
     T_PATCH = T_ITEM_EMPTY + kItemSlots,
     T_SCALES,                              // e4m3: the keys' scales of key tile t, slot t % 4
-    T_COUNT = T_SCALES + 4
+    T_RAW_FULL = T_SCALES + 4,             // E2M1: codes and scales of a K or V tile
+    T_RAW_EMPTY = T_RAW_FULL + 3,
+    T_COUNT = T_RAW_EMPTY + 3
 };
 
 // One item as its roles see it; the scheduler counts the uses of every barrier before it, so that no role has to
@@ -129,7 +131,9 @@ struct TileCfg {
     static constexpr int OFF_QFAC = OFF_SUM + 4 * 128 * 4;           // converted: [2 items][A, B][128] fp32, 2^-a of each row
     static constexpr int OFF_KSC = OFF_QFAC + (kConv ? 2 * 2 * 128 * 4 : 0);    // [4 tiles][128] fp32, the keys' scales
     static constexpr int OFF_VFAC = OFF_KSC + (kE4M3 ? 4 * 128 * 4 : 0);        // [4 tiles] the factor of V
-    static constexpr int OFF_ITEM = OFF_VFAC + (kE4M3 ? 16 : 0);
+    static constexpr int OFF_RAW = OFF_VFAC + (kE4M3 ? 16 : 0);      // E2M1: [kRawStages] of codes [128][D / 2] and scales [128][D / 16]
+    static constexpr int kRawStages = 3, kRawCodes = 128 * cell_bytes(kType, D), kRawStage = kRawCodes + 128 * scale_bytes(kType, D);
+    static constexpr int OFF_ITEM = OFF_RAW + (kE2M1 ? kRawStages * kRawStage : 0);
     static constexpr int kItemBytes = 128;
     static constexpr int OFF_BAR = OFF_ITEM + kItemSlots * kItemBytes;
     static constexpr int OFF_CTL = OFF_BAR + T_COUNT * 8;            // tensor memory address, abort flag
@@ -182,6 +186,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
         *abort = 0;
         for (int i = 0; i < T_COUNT; ++i) {
             int count = 1;
-            if (kConv && ((i >= T_Q_READY && i < T_Q_READY + 2) || i >= T_SCALES || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
+            if (kConv && ((i >= T_Q_READY && i < T_Q_READY + 2) || (i >= T_SCALES && i < T_RAW_FULL) || i >= T_RAW_EMPTY || (i >= T_KV_FULL && i < T_KV_FULL + kKvStages))) count = 4;   // converter warps
             if (i >= T_P_READY && i < T_P_READY + 4) count = 4;                                                         // a softmax warpgroup
             if (i >= T_ITEM_EMPTY && i < T_ITEM_EMPTY + kItemSlots) count = 10 + (kConv ? 4 : 0);
             ptx::mbar_init(BAR(i), count);
@@ -364,7 +373,47 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                                     BAR(T_Q_FULL + slot));
                 }
             }
-            if (kConv) continue;
+            if (kE4M3) continue;
+            if constexpr (kE2M1) {
+                // codes and scales as they lie in the pages, K and V of a tile in turn: a lane for each page's share of either
+                const int sub = lane >> 1, kind = lane & 1;
+                const uint32_t size = (uint32_t)rows * (kind ? D / 16 : D / 2);
+                const int t1 = it.t0 + it.nk;
+                const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(t1 * 128, it.hi) - 1) >> p.page_shift;
+                int eb = (it.t0 * 128) >> p.page_shift, kv = it.kv;
+                auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
+                int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
+                for (int t = it.t0; ok && t < t1; ++t) {
+                    const int key = t * 128;
+                    if ((key >> p.page_shift) - eb >= 32) {
+                        eb += 32;
+                        pages = next;
+                        next = fetch(eb + 32 + lane);
+                    }
+                    const int k0 = key + sub * rows;
+                    const bool need = sub < subs && k0 + rows > it.lo && k0 < it.hi;
+                    const int pg = __shfl_sync(0xffffffffu, pages, ((k0 >> p.page_shift) - eb) & 31);
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need && kind == 0)) * (uint32_t)rows * (D / 2 + D / 16);
+                    const long long cell = ((long long)pg * p.c.Hkv + it.hk) * page + (k0 & (page - 1));
+#pragma unroll 1
+                    for (int val = 0; val < 2; ++val, ++kv) {
+                        const int st = kv % C::kRawStages;
+                        if (kv >= C::kRawStages && !tile_wait_warp(BAR(T_RAW_EMPTY + st), parity(kv / C::kRawStages - 1), tw)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t dst = sbase + C::OFF_RAW + st * C::kRawStage;
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(BAR(T_RAW_FULL + st), bytes);
+                        __syncwarp();
+                        if (need) {
+                            const void* from = kind ? (val ? p.c.v_scale : p.c.k_scale) : (val ? p.c.v : p.c.k);
+                            bulk_load(dst + (kind ? C::kRawCodes : 0) + sub * size, (const uint8_t*)from + cell * (kind ? D / 16 : D / 2), size,
+                                      BAR(T_RAW_FULL + st));
+                        }
+                    }
+                }
+                continue;
+            }
             const int sub = lane / C::kNBox, box = lane % C::kNBox;
             const int t1 = it.t0 + it.nk;
             const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min(t1 * 128, it.hi) - 1) >> p.page_shift;
@@ -883,7 +932,7 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
             if (nk <= 0) continue;
             const int e0 = max(it.t0 * 128, it.lo) >> p.page_shift, e1 = (min((it.t0 + nk) * 128, it.hi) - 1) >> p.page_shift;
             int eb = (it.t0 * 128) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
-            auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
+            auto fetch = [&](int e) { return (kE4M3 && e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
             int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
             // Unit u is K (even) or V (odd) of key tile t0 + u / 2.  This lane's addresses in it: first and second 16 keys of
             // the warp's 32 (a page holds at least 16), and which keys the sequence sees.
@@ -1032,40 +1081,37 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                 }
                 return u != 1 || queries();
             };
-            // E2M1: a lane's 16 codes are 8 bytes, and have one scale.  K and V alike: values code * scale, exact in fp16.
-            [[maybe_unused]] auto load4 = [&](const void* base, const void* scales, uint2 (&w)[kLoads], uint32_t (&s)[kLoads]) {
-#pragma unroll
-                for (int l = 0; l < kLoads; ++l) {
-                    const long long at = cell[l >= kLoads / 2] + (l & (kLoads / 2 - 1)) * kRows + sub;
-                    const int key = key0 + kRows * l + sub;
-                    w[l] = make_uint2(0, 0);
-                    s[l] = 0;
-                    if (key >= it.lo && key < it.hi) {   // keys outside the sequence's read as zero
-                        w[l] = __ldg(reinterpret_cast<const uint2*>((const uint8_t*)base + at * (D / 2) + 8 * chunk));
-                        s[l] = __ldg((const uint8_t*)scales + at * (D / 16) + chunk);
-                    }
-                }
-            };
-            [[maybe_unused]] auto unit4 = [&](int u, const uint2 (&w)[kLoads], const uint32_t (&s)[kLoads], uint2 (&next)[kLoads],
-                                              uint32_t (&next_s)[kLoads]) -> bool {
-                const int kv = it.kv + u, st = kv % kKvStages;
+            // E2M1: the producer has staged codes and scales; a lane's 16 codes are 8 bytes, with one scale.  K and V alike: values
+            // code * scale, exact in fp16.
+            [[maybe_unused]] auto unit4 = [&](int u) -> bool {
+                const int kv = it.kv + u, st = kv % kKvStages, from = kv % C::kRawStages;
+                if (!tile_wait_warp(BAR(T_RAW_FULL + from), parity(kv / C::kRawStages), tw)) return false;
                 if (kv >= kKvStages && !tile_wait_warp(BAR(T_KV_EMPTY + st), parity(kv / kKvStages - 1), tw)) return false;
                 const uint32_t dst = sbase + C::OFF_KV + st * C::kTile;
-                if (u + 1 < 2 * nk) {
-                    if (u & 1) aim(it.t0 + (u + 1) / 2);
-                    load4((u & 1) ? p.c.k : p.c.v, (u & 1) ? p.c.k_scale : p.c.v_scale, next, next_s);
+                const uint8_t* const raw = smem + C::OFF_RAW + from * C::kRawStage + (32 * cw + sub) * (D / 2) + 8 * chunk;
+                const uint8_t* const scales = smem + C::OFF_RAW + from * C::kRawStage + C::kRawCodes + (32 * cw + sub) * (D / 16) + chunk;
+                const int first = (it.t0 + (u >> 1)) * 128 + 32 * cw;
+                const bool whole = first >= it.lo && first + 32 <= it.hi;
+                uint2 w[kLoads];
+                uint32_t f[kLoads];
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) {
+                    w[l] = *reinterpret_cast<const uint2*>(raw + l * kRows * (D / 2));
+                    f[l] = scales[l * kRows * (D / 16)];
+                    const int key = first + kRows * l + sub;
+                    if (!whole && (key < it.lo || key >= it.hi)) w[l] = make_uint2(0, 0), f[l] = 0;   // keys that no row sees: zero
                 }
 #pragma unroll
                 for (int l = 0; l < kLoads; ++l) {
-                    const uint32_t f = half2_of_e4m3x2(s[l] | s[l] << 8);
+                    const uint32_t s = half2_of_e4m3x2(f[l] | f[l] << 8);
                     const uint32_t c2[2] = {w[l].x, w[l].y};
                     uint32_t o[8];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        o[4 * y] = mul_half2(half2_of_e2m1<0>(c2[y]), f);
-                        o[4 * y + 1] = mul_half2(half2_of_e2m1<1>(c2[y]), f);
-                        o[4 * y + 2] = mul_half2(half2_of_e2m1<2>(c2[y]), f);
-                        o[4 * y + 3] = mul_half2(half2_of_e2m1<3>(c2[y]), f);
+                        o[4 * y] = mul_half2(half2_of_e2m1<0>(c2[y]), s);
+                        o[4 * y + 1] = mul_half2(half2_of_e2m1<1>(c2[y]), s);
+                        o[4 * y + 2] = mul_half2(half2_of_e2m1<2>(c2[y]), s);
+                        o[4 * y + 3] = mul_half2(half2_of_e2m1<3>(c2[y]), s);
                     }
                     const uint32_t flip = D == 128 && (l & 1) ? 64u : 0u;
                     sts128(((dst + to0) ^ flip) + l * kRows * 128, make_uint4(o[0], o[1], o[2], o[3]));
@@ -1073,7 +1119,10 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                if (lane == 0) {
+                    ptx::mbar_arrive(BAR(T_KV_FULL + st));
+                    ptx::mbar_arrive(BAR(T_RAW_EMPTY + from));
+                }
                 return u != 1 || queries();
             };
             if constexpr (kE4M3) {
@@ -1085,12 +1134,8 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
 #pragma unroll 1
                 for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit(u, wk, wv) && unit(u + 1, wv, wk);
             } else {
-                uint2 wk[kLoads], wv[kLoads];
-                uint32_t sk[kLoads], sv[kLoads];
-                aim(it.t0);
-                load4(p.c.k, p.c.k_scale, wk, sk);
 #pragma unroll 1
-                for (int u = 0; ok && u < 2 * nk; u += 2) ok = unit4(u, wk, sk, wv, sv) && unit4(u + 1, wv, sv, wk, sk);
+                for (int u = 0; ok && u < 2 * nk; ++u) ok = unit4(u);
             }
         }
     }
