@@ -70,7 +70,7 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 template <bool kHalf>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (kHalf)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -136,15 +136,15 @@ struct FewCfg {
     static constexpr int kRows = kFewRows;
     static constexpr int kThreads = kGroups * 160;
     static constexpr int kRow = cell_bytes(kType, D), kScaleRow = scale_bytes(kType, D);   // of a key
-    static constexpr int kHalfStage = kFewKeys * kRow;        // K, then V
+    static constexpr int kKeys = few_keys(kType), kSub = kKeys / 64;   // of a stage; 16-key tiles of a consumer warp
+    static constexpr int kHalfStage = kKeys * kRow;           // K, then V
     static constexpr int kStage = 2 * kHalfStage;
     static constexpr int kRing = kGroups == 2 ? 65536 : 51200;                     // bytes of a group's stages
-    static constexpr int kMostStages = kE2M1 && D == 128 ? 5 : 8;                  // (what shared memory has room for)
-    static constexpr int kStages = (kRing / kStage) < kMostStages ? kRing / kStage : kMostStages;   // of each group
+    static constexpr int kStages = (kRing / kStage) < 8 ? kRing / kStage : 8;      // of each group
     static_assert(kStages >= 2, "stage ring");
-    static constexpr int kSlotRow = kType == DASH_CACHE_BF16 ? D + 4 : D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
-    static constexpr int OFF_SCALE = kGroups * kStages * kStage;   // [group][stage][K, V][kFewKeys][kScaleRow]
-    static constexpr int OFF_SLOT = OFF_SCALE + kGroups * kStages * 2 * kFewKeys * kScaleRow;   // [group][warp][row]
+    static constexpr int kSlotRow = kType == DASH_CACHE_BF16 ? D + 4 : kE4M3 && D == 128 ? D + 16 : D + 8;   // floats; keeps the join free of bank conflicts
+    static constexpr int OFF_SCALE = kGroups * kStages * kStage;   // [group][stage][K, V][kKeys][kScaleRow]
+    static constexpr int OFF_SLOT = OFF_SCALE + kGroups * kStages * 2 * kKeys * kScaleRow;   // [group][warp][row]
     static constexpr int OFF_M = OFF_SLOT + kGroups * 4 * kRows * kSlotRow * 4;   // [group][parity][warp][row]
     static constexpr int OFF_L = OFF_M + kGroups * 2 * 4 * kRows * 4;             // [group][warp][row]
     static constexpr int OFF_PLAN = OFF_L + kGroups * 4 * kRows * 4;
@@ -162,6 +162,7 @@ struct FewItem {
 
 // Item `item` of the launch; whole warps.  Its sequence is the last that begins at or before it, found by two votes over
 // the plan's counts: an item's step to the next spans tens of short sequences.
+template <int kKeys>
 __device__ __forceinline__ void find_item(const PagedParams& p, const Plan& plan, int item, FewItem& it) {
     constexpr int kMark = kMaxSeqs / 32;
     const int lane = threadIdx.x & 31;
@@ -172,7 +173,7 @@ __device__ __forceinline__ void find_item(const PagedParams& p, const Plan& plan
     it.b = p.b0 + b;
     const int st = plan.st[b], parts = few_parts(it.s.n, p.G);
     seen_keys(p, it.s, 0, it.s.n, it.lo, it.hi);
-    const int first = it.lo / kFewKeys, tiles = it.hi > it.lo ? (it.hi - 1) / kFewKeys - first + 1 : 0;
+    const int first = it.lo / kKeys, tiles = it.hi > it.lo ? (it.hi - 1) / kKeys - first + 1 : 0;
     it.ns = tiles <= st ? 1 : (tiles + st - 1) / st;
     // the parts of a head and range come one after another: they share its cells in L2
     const uint32_t local = (uint32_t)(item - plan.items[b]);
@@ -203,6 +204,7 @@ template <int D, int kType, int kGroups>
 __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
     using C = FewCfg<D, kType, kGroups>;
     constexpr bool kBf16 = kType == DASH_CACHE_BF16, kE4M3 = C::kE4M3, kE2M1 = C::kE2M1;
+    constexpr int kKeys = C::kKeys, kSub = C::kSub;
     extern __shared__ __align__(1024) uint8_t smem[];
     Plan& plan = *reinterpret_cast<Plan*>(smem + C::OFF_PLAN);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
@@ -231,22 +233,22 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 
     if (warp >= 4 * kGroups) {
         // ================================================== producer
-        const int page = p.c.page_size, rows = page < kFewKeys ? page : kFewKeys;
-        const int subs = kFewKeys / rows;                 // copies of one kind along a stage's keys
+        const int page = p.c.page_size, rows = page < kKeys ? page : kKeys;
+        const int subs = kKeys / rows;                 // copies of one kind along a stage's keys
         const int kinds = !kBf16 ? 4 : D / 32;            // K (per 64 values), V (same), or K, V and their scales
         const int sub = lane / kinds, kind = lane % kinds;
         const uint32_t sub_bytes = (uint32_t)rows * 2 * (C::kRow + C::kScaleRow);
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
-            find_item(p, plan, item, it);
+            find_item<kKeys>(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
-            const int e0 = max(it.t0 * kFewKeys, it.lo) >> p.page_shift;
-            const int e1 = (min(it.t1 * kFewKeys, it.hi) - 1) >> p.page_shift;
-            int eb = (it.t0 * kFewKeys) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
+            const int e0 = max(it.t0 * kKeys, it.lo) >> p.page_shift;
+            const int e1 = (min(it.t1 * kKeys, it.hi) - 1) >> p.page_shift;
+            int eb = (it.t0 * kKeys) >> p.page_shift;   // a lane holds the pages of entries eb + lane and eb + 32 + lane
             auto fetch = [&](int e) { return (e >= e0 && e <= e1) ? checked_page(p, it.b, e) : 0; };
             int pages = fetch(eb + lane), next = fetch(eb + 32 + lane);
             for (int t = it.t0; t < it.t1; ++t, ++tc) {
-                const int key = t * kFewKeys;
+                const int key = t * kKeys;
                 if ((key >> p.page_shift) - eb >= 32) {
                     eb += 32;
                     pages = next;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     if (kBf16) {
                         constexpr int kBoxes = D / 64;
                         const int box = kind % kBoxes, val = kind / kBoxes;
-                        ptx::tma_load_3d(base + val * C::kHalfStage + box * (kFewKeys * 128) + sub * rows * 128,
+                        ptx::tma_load_3d(base + val * C::kHalfStage + box * (kKeys * 128) + sub * rows * 128,
                                          val ? &p.tm_v : &p.tm_k, 64 * box, y, head, full);
                     } else if (kind < 2) {
                         ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * C::kRow, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         const uint8_t* src = reinterpret_cast<const uint8_t*>(kind == 3 ? p.c.v_scale : p.c.k_scale) +
                                              ((long long)head * page + y) * C::kScaleRow;
                         bulk_load(sbase + C::OFF_SCALE +
-                                      (((group * C::kStages + stage) * 2 + kind - 2) * kFewKeys + sub * rows) * C::kScaleRow,
+                                      (((group * C::kStages + stage) * 2 + kind - 2) * kKeys + sub * rows) * C::kScaleRow,
                                   src, rows * C::kScaleRow, full);
                     }
                 }
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     FewItem after;   // the next item
     const int first_item = group * gridDim.x + blockIdx.x, step = kGroups * gridDim.x;
     if (first_item < items) {
-        find_item(p, plan, first_item, after);
+        find_item<kKeys>(p, plan, first_item, after);
         load_queries(after);
     }
     int tc = 0, parity = 0;
@@ -392,23 +394,23 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             __syncwarp();
             const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
             constexpr float kLift = kE2M1 ? kLiftE4M3 : 0.f;   // the maxima m are held less this
-            const int key0 = kt * kFewKeys + 16 * ws;   // this warp's first key
-            const bool edge = key0 < full_lo || key0 + 16 > full_hi;
+            const int key0 = kt * kKeys + 16 * kSub * ws;   // this warp's first key
+            const bool edge = key0 < full_lo || key0 + 16 * kSub > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
-                const int r = lane >> 1;
+                const int r = kSub == 2 ? lane : lane >> 1;
                 if (key0 + r < it.lo || key0 + r >= it.hi) {
-                    const int row = 16 * ws + r;
-                    constexpr int kRow = C::kRow / 2;   // bytes per lane
+                    const int row = 16 * kSub * ws + r;
+                    constexpr int kRow = C::kRow * kSub / 2;   // bytes per lane
 #pragma unroll
                     for (int x = 0; x < kRow; x += 16) {
-                        const int byte = (lane & 1) * kRow + x;   // rows are zeroed whole: the swizzle stays inside a row
+                        const int byte = (kSub == 2 ? 0 : lane & 1) * kRow + x;   // rows are zeroed whole: the swizzle stays inside a row
                         sts128(!kBf16 || D == 64 ? sv + row * C::kRow + byte
-                                                 : sv + (byte >> 7) * (kFewKeys * 128) + row * 128 + (byte & 127),
+                                                 : sv + (byte >> 7) * (kKeys * 128) + row * 128 + (byte & 127),
                                make_uint4(0, 0, 0, 0));
                     }
-                    if (kE2M1 && !(lane & 1)) {   // their scales enter the products too
+                    if (kE2M1) {   // their scales enter the products too
                         uint32_t* sc = reinterpret_cast<uint32_t*>(
-                            smem + C::OFF_SCALE + (((group * C::kStages + stage) * 2 + 1) * kFewKeys + row) * C::kScaleRow);
+                            smem + C::OFF_SCALE + (((group * C::kStages + stage) * 2 + 1) * kKeys + row) * C::kScaleRow);
 #pragma unroll
                         for (int x = 0; x < C::kScaleRow / 4; ++x) sc[x] = 0;
                     }
@@ -416,26 +418,28 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 __syncwarp();
             }
 
-            float s[4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
+            float s[4 * kSub];   // (key g, rows 2c, 2c + 1), (key g + 8, the same); (key g + 16, ...)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = 0.f;
+            for (int e = 0; e < 4 * kSub; ++e) s[e] = 0.f;
             // E2M1: scales of K's keys of this stage, then of V's
-            [[maybe_unused]] const uint8_t* const scales = smem + C::OFF_SCALE + (group * C::kStages + stage) * 2 * kFewKeys * C::kScaleRow;
+            [[maybe_unused]] const uint8_t* const scales = smem + C::OFF_SCALE + (group * C::kStages + stage) * 2 * kKeys * C::kScaleRow;
             if (kBf16) {
                 const int row = 16 * ws + (lane & 15);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t a[4];
                     const int chunk = 2 * (k & 3) + (lane >> 4);
-                    ldsm4(sk + (k >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
-                    mma16816<false>(s, a, qf[k][0], qf[k][1]);
+                    ldsm4(sk + (k >> 2) * (kKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+                    mma16816<false>(&s[0], a, qf[k][0], qf[k][1]);
                 }
             } else if (kE2M1) {   // a lane reads D / 4 values of a key in one: one or two scales
                 constexpr int kWords = D / 32;
+#pragma unroll
+                for (int t = 0; t < kSub; ++t) {
                 uint32_t w[2][kWords], f[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int row = 16 * ws + 8 * n + perm(g);
+                    const int row = 16 * (kSub * ws + t) + 8 * n + perm(g);
                     if (D == 128) {
                         const uint4 v = lds128(sk + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
                         w[n][0] = v.x, w[n][1] = v.y, w[n][kWords - 2] = v.z, w[n][kWords - 1] = v.w;
@@ -460,8 +464,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const uint32_t a[4] = {h[0][2 * z], h[1][2 * z], h[0][2 * z + 1], h[1][2 * z + 1]};
-                        mma16816<true>(s, a, qf[2 * y + z][0], qf[2 * y + z][1]);
+                        mma16816<true>(&s[4 * t], a, qf[2 * y + z][0], qf[2 * y + z][1]);
                     }
+                }
                 }
             } else {
 #pragma unroll
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t a[4] = {half2_of_e4m3(w[0][x], 0), half2_of_e4m3(w[1][x], 0), half2_of_e4m3(w[0][x], 1),
                                                half2_of_e4m3(w[1][x], 1)};
-                        mma16816<true>(s, a, qf[4 * h + x][0], qf[4 * h + x][1]);
+                        mma16816<true>(&s[0], a, qf[4 * h + x][0], qf[4 * h + x][1]);
                     }
                 }
             }
@@ -488,40 +493,41 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
             if (kE4M3) {
                 const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) +
-                                  (group * C::kStages + stage) * 2 * kFewKeys + 16 * ws + perm(g);
+                                  (group * C::kStages + stage) * 2 * kKeys + 16 * ws + perm(g);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     ks[n] = sc[8 * n];
-                    lv[n] = lg2(sc[kFewKeys + 8 * n]);
+                    lv[n] = lg2(sc[kKeys + 8 * n]);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2 * kSub; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n] : qs[e];
+                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n & 1] : qs[e];
             if (edge) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < 2 * kSub; ++n) {
                     const int key = key0 + 8 * n + perm(g);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         if (key < lo[e] || key >= hi[e]) s[2 * n + e] = -INFINITY;
-                    if (key < it.lo || key >= it.hi) lv[n] = 0.f;
+                    if (kE4M3 && (key < it.lo || key >= it.hi)) lv[n & 1] = 0.f;
                 }
             }
+            auto top_of = [&](int e) { return kSub == 1 ? fmaxf(s[e], s[2 + e]) : fmaxf(fmaxf(s[e], s[2 + e]), fmaxf(s[4 * kSub - 4 + e], s[4 * kSub - 2 + e])); };
             // Running maxima (m of s, less the lift with E2M1; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
             // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + (8.f + kLift);
+                raise = raise || top_of(e) > m[e] + (8.f + kLift);
                 if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + (8.f + kLiftE4M3);
             }
             if (__any_sync(0xffffffffu, raise)) {
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[e], s[2 + e]), mw = kE4M3 ? fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) : 0.f;
+                    float mx = top_of(e), mw = kE4M3 ? fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) : 0.f;
 #pragma unroll
                     for (int d = 4; d <= 16; d <<= 1) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -541,22 +547,22 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     o[j][3] *= f[1];
                 }
             }
-            uint32_t pb[2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
-            float w[4];
+            uint32_t pb[2 * kSub];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8, ...) of query row g
+            float w[4 * kSub];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = mv[e] == -INFINITY ? 0.f : mv[e];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < 2 * kSub; ++n) {
                     const float x = s[2 * n + e];
                     const float pr = ptx::ex2(x - mu);
                     l[e] += pr;
-                    w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n] - vu)) : pr;
+                    w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n & 1] - vu)) : pr;
                 }
             }
             // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2 * kSub; ++n)
                 pb[n] = transposed8x8(!kBf16 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
 
             if (kBf16) {   // tile j of O^T: value columns 16j + g and + 8
@@ -565,13 +571,15 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t a[4];
                     const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
-                    ldsm4_t(sv + (j >> 2) * (kFewKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+                    ldsm4_t(sv + (j >> 2) * (kKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
                     mma16816<false>(o[j], a, pb[0], pb[1]);
                 }
             } else if (kE2M1) {   // the same columns, of one scale (D = 64: half of one)
                 constexpr int kWords = D / 64;   // words of a lane's D / 8 columns
-                const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
-                const uint8_t* const sc = scales + kFewKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
+                const uint8_t* const sc = scales + kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
+#pragma unroll
+                for (int t = 0; t < kSub; ++t) {
+                const int r0 = 16 * (kSub * ws + t) + perm(2 * c4), r1 = 16 * (kSub * ws + t) + perm(2 * c4 + 1);
                 uint32_t w[4][kWords], f[2];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -607,8 +615,9 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         const uint32_t a[4] = {h[0][2 * z], h[0][2 * z + 1], h[1][2 * z], h[1][2 * z + 1]};
-                        mma16816<true>(o[4 * y + z], a, pb[0], pb[1]);
+                        mma16816<true>(o[4 * y + z], a, pb[2 * t], pb[2 * t + 1]);
                     }
+                }
                 }
             } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
         }
 
         if (item + step < items) {
-            find_item(p, plan, item + step, after);
+            find_item<kKeys>(p, plan, item + step, after);
             load_queries(after);
         }
 
@@ -1037,7 +1046,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         prm.scale_log2e = ldexpf(prm.scale_log2e, cache->k_exp);
         prm.v_unit = ldexpf(1.f, cache->v_exp);
     }
-    const int rows = cache->page_size < kFewKeys ? cache->page_size : kFewKeys;
+    const int rows = cache->page_size < few_keys(cache->type) ? cache->page_size : few_keys(cache->type);
     if (make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
         return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;

@@ -22,7 +22,7 @@ namespace dash {
 
 constexpr int kFewRows = 8;        // query rows of an item of the few-rows kernel
 constexpr int kFewMost = 32;       // rows of a sequence of its class, at the most (few_most)
-constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel
+constexpr int kFewKeys = 64;       // keys per stage of the few-rows kernel (few_keys)
 constexpr int kFewWholeTiles = 4;  // sequences of so many stages are not split: joining costs more than it gains
 constexpr int kFewWorkers = 304;   // groups on a GB300's 152 SMs: two of each CTA,
 constexpr int kFewWorkers3 = 456;  // or three
@@ -127,6 +127,9 @@ __host__ __device__ inline int few_max_splits(int workers, int heads) {
     return best;
 }
 
+// Keys per stage.  E2M1: 32 for each consumer warp instead of 16.
+__host__ __device__ constexpr int few_keys(int type) { return type == DASH_CACHE_E2M1 ? 2 * kFewKeys : kFewKeys; }
+
 __host__ __device__ inline int few_parts(int n, int G) { return (n * G + kFewRows - 1) / kFewRows; }
 
 // Groups that work through the items: three of a CTA, or two (launch_few).
@@ -174,7 +177,8 @@ struct Cut {
 __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     Cut c;
     seen_keys(p, s, 0, s.n, c.lo, c.hi);
-    c.tiles = c.hi > c.lo ? (c.hi - 1) / kFewKeys - c.lo / kFewKeys + 1 : 0;
+    const int keys = few_keys(p.c.type);
+    c.tiles = c.hi > c.lo ? (c.hi - 1) / keys - c.lo / keys + 1 : 0;
     c.parts = few_parts(s.n, p.G);
     few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * c.parts, c.ns, c.st);
     c.items = p.c.Hkv * c.ns * c.parts;
