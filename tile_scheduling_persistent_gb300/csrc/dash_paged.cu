@@ -70,7 +70,7 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 template <bool kHalf>
-__device__ __forceinline__ void mma16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (kHalf)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -134,7 +134,11 @@ template <int D, int kType, int kGroups>
 struct FewCfg {
     static constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
     static constexpr int kRows = kFewRows;
-    static constexpr int kThreads = kGroups * 160;
+    // E2M1: the producers' registers go to the consumers (setmaxnreg works on whole warpgroups: one warp stays idle)
+    static constexpr bool kRegs = kE2M1;
+    static constexpr int kRegsConsumer = 152, kRegsProducer = 56;
+    static constexpr int kThreads = kRegs ? kGroups * 128 + 128 : kGroups * 160;
+    static_assert(!kRegs || (kGroups == 3 && 384 * kRegsConsumer + 128 * kRegsProducer <= 512 * 128), "register split");
     static constexpr int kRow = cell_bytes(kType, D), kScaleRow = scale_bytes(kType, D);   // of a key
     static constexpr int kKeys = few_keys(kType), kSub = kKeys / 64;   // of a stage; 16-key tiles of a consumer warp
     static constexpr int kHalfStage = kKeys * kRow;           // K, then V
@@ -201,7 +205,7 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
 }
 
 template <int D, int kType, int kGroups>
-__global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
+__global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
     using C = FewCfg<D, kType, kGroups>;
     constexpr bool kBf16 = kType == DASH_CACHE_BF16, kE4M3 = C::kE4M3, kE2M1 = C::kE2M1;
     constexpr int kKeys = C::kKeys, kSub = C::kSub;
@@ -233,6 +237,10 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 
     if (warp >= 4 * kGroups) {
         // ================================================== producer
+        if constexpr (C::kRegs) {
+            ptx::setmaxnreg_dec<C::kRegsProducer>();
+            if (warp >= 5 * kGroups) return;
+        }
         const int page = p.c.page_size, rows = page < kKeys ? page : kKeys;
         const int subs = kKeys / rows;                 // copies of one kind along a stage's keys
         const int kinds = !kBf16 ? 4 : D / 32;            // K (per 64 values), V (same), or K, V and their scales
@@ -297,6 +305,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
     }
 
     // ================================================== consumers
+    if constexpr (C::kRegs) ptx::setmaxnreg_inc<C::kRegsConsumer>();
     // Fragment of a lane: g = lane / 4, c = lane % 4.  S^T and P^T: keys g and g + 8 of the warp's 16, query rows
     // 2c and 2c + 1; O^T: columns of the values as commented below, the same query rows.
     const int g = lane >> 2, c4 = lane & 3;
@@ -365,7 +374,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
             const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
             const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            const float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+            float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+            if (kE2M1) down = fmaxf(down, 0x1p-126f);   // (above zero: -inf times it stays -inf)
             qs[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
             qs[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 #pragma unroll
@@ -384,7 +394,8 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            m[e] = mv[e] = -INFINITY;
+            m[e] = -INFINITY;
+            mv[e] = kE2M1 ? 0.f : -INFINITY;
             l[e] = 0.f;
         }
 
@@ -393,7 +404,6 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
             few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
             __syncwarp();
             const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
-            constexpr float kLift = kE2M1 ? kLiftE4M3 : 0.f;   // the maxima m are held less this
             const int key0 = kt * kKeys + 16 * kSub * ws;   // this warp's first key
             const bool edge = key0 < full_lo || key0 + 16 * kSub > full_hi;
             if (edge) {   // value rows that no row sees: zero, whatever the cells hold
@@ -418,11 +428,159 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 __syncwarp();
             }
 
-            float s[4 * kSub];   // (key g, rows 2c, 2c + 1), (key g + 8, the same); (key g + 16, ...)
+            if constexpr (kE2M1) {
+                // 16-key tiles t = 0, 1 of the warp's 32 keys.  The tiles' products alternate, and the values' codes are on their
+                // way during the softmax.
+                const uint8_t* const scales = smem + C::OFF_SCALE + (group * C::kStages + stage) * 2 * kKeys * C::kScaleRow;
+                constexpr int kKw = D / 32, kVw = D / 64;   // words of a lane: D / 4 codes of a key, D / 8 columns of a value
+                uint32_t w[2][2][kKw], f[2][2];
 #pragma unroll
-            for (int e = 0; e < 4 * kSub; ++e) s[e] = 0.f;
-            // E2M1: scales of K's keys of this stage, then of V's
-            [[maybe_unused]] const uint8_t* const scales = smem + C::OFF_SCALE + (group * C::kStages + stage) * 2 * kKeys * C::kScaleRow;
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int row = 32 * ws + 16 * t + 8 * n + perm(g);
+                        if (D == 128) {
+                            const uint4 v = lds128(sk + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
+                            w[t][n][0] = v.x, w[t][n][1] = v.y, w[t][n][kKw - 2] = v.z, w[t][n][kKw - 1] = v.w;
+                            f[t][n] = *reinterpret_cast<const uint16_t*>(scales + row * 8 + 2 * c4);
+                        } else {
+                            const uint2 v = lds64(sk + row * 32 + c4 * 8);
+                            w[t][n][0] = v.x, w[t][n][1] = v.y;
+                            f[t][n] = scales[row * 4 + c4];
+                        }
+                    }
+                float s[2][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) f[t][n] = half2_of_e4m3x2(f[t][n]);
+#pragma unroll
+                for (int y = 0; y < kKw; ++y)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t h[2][4];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint32_t ff = __byte_perm(f[t][n], 0u, y < 2 ? 0x1010u : 0x3232u);
+                            h[n][0] = mul_half2(half2_of_e2m1<0>(w[t][n][y]), ff);
+                            h[n][1] = mul_half2(half2_of_e2m1<1>(w[t][n][y]), ff);
+                            h[n][2] = mul_half2(half2_of_e2m1<2>(w[t][n][y]), ff);
+                            h[n][3] = mul_half2(half2_of_e2m1<3>(w[t][n][y]), ff);
+                        }
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t a[4] = {h[0][2 * z], h[1][2 * z], h[0][2 * z + 1], h[1][2 * z + 1]};
+                            mma16816<true>(s[t], a, qf[2 * y + z][0], qf[2 * y + z][1]);
+                        }
+                    }
+                // values: codes of keys perm(2c), perm(2c + 1) and + 8 of each tile, this lane's D / 8 columns; their scales
+                uint32_t vw[2][4][kVw], vf[2][2];
+                const uint8_t* const sc = scales + kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int r0 = 32 * ws + 16 * t + perm(2 * c4), r1 = 32 * ws + 16 * t + perm(2 * c4 + 1);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = (x & 1 ? r1 : r0) + 8 * (x >> 1);
+                        if (D == 128) {
+                            const uint2 v = lds64(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                            vw[t][x][0] = v.x, vw[t][x][kVw - 1] = v.y;
+                        } else {
+                            vw[t][x][0] = lds32(sv + row * 32 + g * 4);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        vf[t][n] = sc[(r0 + 8 * n) * C::kScaleRow] | (uint32_t)sc[(r1 + 8 * n) * C::kScaleRow] << 8;
+                }
+                if (edge) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const int key = key0 + 16 * t + 8 * n + perm(g);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (key < lo[e] || key >= hi[e]) s[t][2 * n + e] = -INFINITY;
+                        }
+                }
+                // The running maxima m (log2 units, less the lift), as below; the scores' scale qs is above zero, so the largest
+                // of the scaled scores is the largest score's, and the exponent's argument is one multiply-add.
+                float top[2];
+                bool raise = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e])) * qs[e] - kLiftE4M3;
+                    raise = raise || top[e] > m[e] + 8.f;
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+                    float a[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], d));
+                        const float nm = fmaxf(m[e], top[e]);
+                        a[e] = nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
+                        l[e] *= a[e];
+                        m[e] = nm;
+                        mv[e] = nm == -INFINITY ? 0.f : nm;   // (what the exponents subtract)
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[j][0] *= a[0];
+                        o[j][1] *= a[1];
+                        o[j][2] *= a[0];
+                        o[j][3] *= a[1];
+                    }
+                }
+                uint32_t pb[2][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g; fp16
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[t][e] = ptx::ex2(fmaf(s[t][e], qs[e & 1], -mv[e & 1]));
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) pb[t][n] = transposed8x8(pack_half(s[t][2 * n], s[t][2 * n + 1]));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[e] += (s[0][e] + s[0][2 + e]) + (s[1][e] + s[1][2 + e]);   // the unrounded weights
+                // tile j of O^T: value columns (D / 8) g + 2j and + 1.  A word holds 8 columns of one key: the low and the high
+                // halves of its bytes beside those of the other key.
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) vf[t][n] = half2_of_e4m3x2(vf[t][n]);
+#pragma unroll
+                    for (int y = 0; y < kVw; ++y) {
+                        uint32_t h[2][8];   // [keys 2c.., + 8][column]
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint32_t a = vw[t][2 * n][y], b = vw[t][2 * n + 1][y];
+                            const uint32_t even = (a & kLow) | ((b << 4) & ~kLow), odd = ((a >> 4) & kLow) | (b & ~kLow);
+                            h[n][0] = mul_half2(half2_of_e2m1<0>(even), vf[t][n]);
+                            h[n][1] = mul_half2(half2_of_e2m1<0>(odd), vf[t][n]);
+                            h[n][2] = mul_half2(half2_of_e2m1<1>(even), vf[t][n]);
+                            h[n][3] = mul_half2(half2_of_e2m1<1>(odd), vf[t][n]);
+                            h[n][4] = mul_half2(half2_of_e2m1<2>(even), vf[t][n]);
+                            h[n][5] = mul_half2(half2_of_e2m1<2>(odd), vf[t][n]);
+                            h[n][6] = mul_half2(half2_of_e2m1<3>(even), vf[t][n]);
+                            h[n][7] = mul_half2(half2_of_e2m1<3>(odd), vf[t][n]);
+                        }
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t a[4] = {h[0][2 * z], h[0][2 * z + 1], h[1][2 * z], h[1][2 * z + 1]};
+                            mma16816<true>(o[4 * y + z], a, pb[t][0], pb[t][1]);
+                        }
+                    }
+                }
+            } else {
+            float s[4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = 0.f;
             if (kBf16) {
                 const int row = 16 * ws + (lane & 15);
 #pragma unroll
@@ -430,43 +588,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     uint32_t a[4];
                     const int chunk = 2 * (k & 3) + (lane >> 4);
                     ldsm4(sk + (k >> 2) * (kKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
-                    mma16816<false>(&s[0], a, qf[k][0], qf[k][1]);
-                }
-            } else if (kE2M1) {   // a lane reads D / 4 values of a key in one: one or two scales
-                constexpr int kWords = D / 32;
-#pragma unroll
-                for (int t = 0; t < kSub; ++t) {
-                uint32_t w[2][kWords], f[2];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int row = 16 * (kSub * ws + t) + 8 * n + perm(g);
-                    if (D == 128) {
-                        const uint4 v = lds128(sk + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
-                        w[n][0] = v.x, w[n][1] = v.y, w[n][kWords - 2] = v.z, w[n][kWords - 1] = v.w;
-                        f[n] = half2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(scales + row * 8 + 2 * c4));
-                    } else {
-                        const uint2 v = lds64(sk + row * 32 + c4 * 8);
-                        w[n][0] = v.x, w[n][1] = v.y;
-                        f[n] = half2_of_e4m3x2(scales[row * 4 + c4]);
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < kWords; ++y) {
-                    uint32_t h[2][4];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t ff = __byte_perm(f[n], 0u, y < 2 ? 0x1010u : 0x3232u);
-                        h[n][0] = mul_half2(half2_of_e2m1<0>(w[n][y]), ff);
-                        h[n][1] = mul_half2(half2_of_e2m1<1>(w[n][y]), ff);
-                        h[n][2] = mul_half2(half2_of_e2m1<2>(w[n][y]), ff);
-                        h[n][3] = mul_half2(half2_of_e2m1<3>(w[n][y]), ff);
-                    }
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t a[4] = {h[0][2 * z], h[1][2 * z], h[0][2 * z + 1], h[1][2 * z + 1]};
-                        mma16816<true>(&s[4 * t], a, qf[2 * y + z][0], qf[2 * y + z][1]);
-                    }
-                }
+                    mma16816<false>(s, a, qf[k][0], qf[k][1]);
                 }
             } else {
 #pragma unroll
@@ -484,7 +606,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t a[4] = {half2_of_e4m3(w[0][x], 0), half2_of_e4m3(w[1][x], 0), half2_of_e4m3(w[0][x], 1),
                                                half2_of_e4m3(w[1][x], 1)};
-                        mma16816<true>(&s[0], a, qf[4 * h + x][0], qf[4 * h + x][1]);
+                        mma16816<true>(s, a, qf[4 * h + x][0], qf[4 * h + x][1]);
                     }
                 }
             }
@@ -501,39 +623,38 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                 }
             }
 #pragma unroll
-            for (int n = 0; n < 2 * kSub; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n & 1] : qs[e];
+                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n] : qs[e];
             if (edge) {
 #pragma unroll
-                for (int n = 0; n < 2 * kSub; ++n) {
+                for (int n = 0; n < 2; ++n) {
                     const int key = key0 + 8 * n + perm(g);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         if (key < lo[e] || key >= hi[e]) s[2 * n + e] = -INFINITY;
-                    if (kE4M3 && (key < it.lo || key >= it.hi)) lv[n & 1] = 0.f;
+                    if (key < it.lo || key >= it.hi) lv[n] = 0.f;
                 }
             }
-            auto top_of = [&](int e) { return kSub == 1 ? fmaxf(s[e], s[2 + e]) : fmaxf(fmaxf(s[e], s[2 + e]), fmaxf(s[4 * kSub - 4 + e], s[4 * kSub - 2 + e])); };
-            // Running maxima (m of s, less the lift with E2M1; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
+            // Running maxima (m of s; mv of s + lv, less the lift), raised only when a row outgrows them by 2^8.  Whether one does needs a
             // vote alone; the maxima over the warp's keys are formed only then.
             bool raise = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                raise = raise || top_of(e) > m[e] + (8.f + kLift);
+                raise = raise || fmaxf(s[e], s[2 + e]) > m[e] + 8.f;
                 if (kE4M3) raise = raise || fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) > mv[e] + (8.f + kLiftE4M3);
             }
             if (__any_sync(0xffffffffu, raise)) {
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = top_of(e), mw = kE4M3 ? fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) : 0.f;
+                    float mx = fmaxf(s[e], s[2 + e]), mw = kE4M3 ? fmaxf(s[e] + lv[0], s[2 + e] + lv[1]) : 0.f;
 #pragma unroll
                     for (int d = 4; d <= 16; d <<= 1) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                         if (kE4M3) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, d));
                     }
-                    const float nm = fmaxf(m[e], mx - kLift), nv = kE4M3 ? fmaxf(mv[e], mw - kLiftE4M3) : nm;
+                    const float nm = fmaxf(m[e], mx), nv = kE4M3 ? fmaxf(mv[e], mw - kLiftE4M3) : nm;
                     l[e] *= nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
                     f[e] = nv == -INFINITY ? 1.f : ptx::ex2((kE4M3 ? mv[e] : m[e]) - nv);
                     m[e] = nm;
@@ -547,22 +668,22 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     o[j][3] *= f[1];
                 }
             }
-            uint32_t pb[2 * kSub];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8, ...) of query row g
-            float w[4 * kSub];
+            uint32_t pb[2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g
+            float w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float mu = m[e] == -INFINITY ? 0.f : m[e], vu = mv[e] == -INFINITY ? 0.f : mv[e];
 #pragma unroll
-                for (int n = 0; n < 2 * kSub; ++n) {
+                for (int n = 0; n < 2; ++n) {
                     const float x = s[2 * n + e];
                     const float pr = ptx::ex2(x - mu);
                     l[e] += pr;
-                    w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n & 1] - vu)) : pr;
+                    w[2 * n + e] = kE4M3 ? ptx::ex2(x + (lv[n] - vu)) : pr;
                 }
             }
             // rounded to the products' 16-bit type (bf16; fp16 with e4m3), the sum l from the unrounded weights
 #pragma unroll
-            for (int n = 0; n < 2 * kSub; ++n)
+            for (int n = 0; n < 2; ++n)
                 pb[n] = transposed8x8(!kBf16 ? pack_half(w[2 * n], w[2 * n + 1]) : pack_bf16(w[2 * n], w[2 * n + 1]));
 
             if (kBf16) {   // tile j of O^T: value columns 16j + g and + 8
@@ -573,51 +694,6 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                     const int chunk = 2 * (j & 3) + ((lane >> 3) & 1);
                     ldsm4_t(sv + (j >> 2) * (kKeys * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), a);
                     mma16816<false>(o[j], a, pb[0], pb[1]);
-                }
-            } else if (kE2M1) {   // the same columns, of one scale (D = 64: half of one)
-                constexpr int kWords = D / 64;   // words of a lane's D / 8 columns
-                const uint8_t* const sc = scales + kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
-#pragma unroll
-                for (int t = 0; t < kSub; ++t) {
-                const int r0 = 16 * (kSub * ws + t) + perm(2 * c4), r1 = 16 * (kSub * ws + t) + perm(2 * c4 + 1);
-                uint32_t w[4][kWords], f[2];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int row = (x & 1 ? r1 : r0) + 8 * (x >> 1);
-                    if (D == 128) {
-                        const uint2 v = lds64(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-                        w[x][0] = v.x, w[x][kWords - 1] = v.y;
-                    } else {
-                        w[x][0] = lds32(sv + row * 32 + g * 4);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    f[n] = half2_of_e4m3x2(sc[(r0 + 8 * n) * C::kScaleRow] | (uint32_t)sc[(r1 + 8 * n) * C::kScaleRow] << 8);
-                // a word holds 8 columns of one key: the low and the high halves of its bytes beside those of the other key
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-#pragma unroll
-                for (int y = 0; y < kWords; ++y) {
-                    uint32_t h[2][8];   // [keys 2c.., + 8][column]
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t a = w[2 * n][y], b = w[2 * n + 1][y];
-                        const uint32_t even = (a & kLow) | ((b << 4) & ~kLow), odd = ((a >> 4) & kLow) | (b & ~kLow);
-                        h[n][0] = mul_half2(half2_of_e2m1<0>(even), f[n]);
-                        h[n][1] = mul_half2(half2_of_e2m1<0>(odd), f[n]);
-                        h[n][2] = mul_half2(half2_of_e2m1<1>(even), f[n]);
-                        h[n][3] = mul_half2(half2_of_e2m1<1>(odd), f[n]);
-                        h[n][4] = mul_half2(half2_of_e2m1<2>(even), f[n]);
-                        h[n][5] = mul_half2(half2_of_e2m1<2>(odd), f[n]);
-                        h[n][6] = mul_half2(half2_of_e2m1<3>(even), f[n]);
-                        h[n][7] = mul_half2(half2_of_e2m1<3>(odd), f[n]);
-                    }
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t a[4] = {h[0][2 * z], h[0][2 * z + 1], h[1][2 * z], h[1][2 * z + 1]};
-                        mma16816<true>(o[4 * y + z], a, pb[2 * t], pb[2 * t + 1]);
-                    }
-                }
                 }
             } else {        // tile j of O^T: value columns (D / 8) g + 2j and + 1
                 const int r0 = 16 * ws + perm(2 * c4), r1 = 16 * ws + perm(2 * c4 + 1);
@@ -643,6 +719,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
                         const uint32_t a[4] = {half2_of_e4m3(lo2, 0), half2_of_e4m3(lo2, 1), half2_of_e4m3(hi2, 0), half2_of_e4m3(hi2, 1)};
                         mma16816<true>(o[2 * y + z], a, pb[0], pb[1]);
                     }
+            }
             }
             if (edge) ptx::fence_proxy_async_smem();   // the zeroed rows before the next copy into the stage
             __syncwarp();
@@ -672,7 +749,7 @@ __global__ void __launch_bounds__(kGroups * 160, 1) paged_few_kernel(const __gri
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
             // outputs carry 2^-mv (weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || mv[e] == -INFINITY) ? 0.f
+            const float fo = (top == -INFINITY || (kE4M3 ? mv[e] : m[e]) == -INFINITY) ? 0.f
                              : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top) * (kE2M1 ? p.v_unit : 1.f);
             if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
             float* row = slot + r * C::kSlotRow;
@@ -907,6 +984,11 @@ int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) 
         if (cudaFuncSetAttribute(paged_few_kernel<D, kType, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
+        if (C::kRegs) {   // the consumers' share has to be there, or they would wait for it
+            cudaFuncAttributes a;
+            if (cudaFuncGetAttributes(&a, paged_few_kernel<D, kType, kGroups>) != cudaSuccess) return DASH_ERR_CUDA;
+            if (a.numRegs * C::kThreads < kGroups * 128 * C::kRegsConsumer + 128 * C::kRegsProducer) return DASH_ERR_LAUNCH;
+        }
         ready[dev] = true;
     }
     const int sms = sm_count();

@@ -142,9 +142,14 @@ __host__ __device__ inline int few_workers(int D, int type) {
 // (us; Hq = 32, Hkv = 8, D = 128; 1000 bf16 keys, 4000 and 8192 e4m3 keys alone, 64 ragged e4m3 sequences to 8192, 256 to
 // 2000), ranges of at least 2 stages: 8.3 11.8 15.1 136 149; 4: 9.6 10.3 13.2 107 117; 8: 12.5 11.7 12.7 99 109; 16: 17.6
 // 15.5 16.3 97 111; growing with the sequence, as here: 8.5 11.9 12.7 100 129.
-__host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st) {
+// E2M1, in stages of 128 keys: a range's costs weigh more against half the bytes.  Measured (us; as above, D = 128: 1000 keys
+// alone, 64 ragged sequences, and 3 of 262143 at D = 64), ranges of at least 1024 keys from 32 stages on, a quarter of the
+// sequence before: 13.2 85.9 194.5; from 64 on, an eighth before (as for the other types): 13.1 91.8 195; 2048 from 32 on:
+// 13.2 92.4 199.
+__host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st, int type = DASH_CACHE_BF16) {
     const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, heads);
-    const int least = tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
+    const int least = type == DASH_CACHE_E2M1 ? (tiles >= 32 ? 8 : tiles > 8 ? (tiles + 3) / 4 : 2)
+                                              : tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
     st = (tiles + most - 1) / most;
     st = st < least ? least : st;
     ns = (tiles + st - 1) / st;
@@ -180,7 +185,7 @@ __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     const int keys = few_keys(p.c.type);
     c.tiles = c.hi > c.lo ? (c.hi - 1) / keys - c.lo / keys + 1 : 0;
     c.parts = few_parts(s.n, p.G);
-    few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * c.parts, c.ns, c.st);
+    few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * c.parts, c.ns, c.st, p.c.type);
     c.items = p.c.Hkv * c.ns * c.parts;
     return c;
 }
