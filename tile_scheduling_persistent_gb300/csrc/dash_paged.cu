@@ -102,6 +102,11 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
     return h;
 }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -346,6 +351,14 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
         load_queries(after);
     }
     int tc = 0, parity = 0;
+    // E2M1: where this lane reads in a stage, rows of its 32 keys 8 and 16 on at fixed distances (the swizzle repeats after 8)
+    const int kp = 32 * ws + perm(g), vp0 = 32 * ws + perm(2 * c4), vp1 = 32 * ws + perm(2 * c4 + 1);
+    const uint32_t k_at = kp * C::kRow + (D == 128 ? (c4 ^ ((kp >> 1) & 3)) << 4 : c4 * 8);
+    const uint32_t v_at0 = vp0 * C::kRow + (D == 128 ? (((g >> 1) ^ ((vp0 >> 1) & 3)) << 4) + (g & 1) * 8 : g * 4);
+    const uint32_t v_at1 = vp1 * C::kRow + (D == 128 ? (((g >> 1) ^ ((vp1 >> 1) & 3)) << 4) + (g & 1) * 8 : g * 4);
+    const uint32_t ks_at = kp * C::kScaleRow + (D == 128 ? 2 * c4 : c4), vs_col = kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
+    const uint32_t vs_at0 = vp0 * C::kScaleRow + vs_col, vs_at1 = vp1 * C::kScaleRow + vs_col;
+    int at_stage = 0, at_phase = 0;
     for (int item = first_item; item < items; item += step, parity ^= 1) {
         it = after;
         const int all = it.s.n * p.G, R = min(all - it.r0, kFewRows);   // rows of the sequence, and of this item
@@ -364,11 +377,20 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
             qs[0] = qs[1] = p.scale_log2e;
         } else {
             float top = 0.f;
+            if (kE2M1) {   // in pairs (NaN does not enter)
+                uint32_t two = 0;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
+                for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[k][x] << 16)), fabsf(__uint_as_float(qf[k][x] & 0xffff0000u))));
+                    for (int x = 0; x < 2; ++x) two = max_bf16x2(two, qf[k][x] & 0x7fff7fffu);
+                top = fmaxf(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[k][x] << 16)), fabsf(__uint_as_float(qf[k][x] & 0xffff0000u))));
+            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^a with 2^a * top in [2^14, 2^15); exponents kept where 2^a and 2^-a are normal
@@ -400,9 +422,10 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
         }
 
         for (int kt = it.t0; kt < it.t1; ++kt, ++tc) {
-            const int stage = tc % C::kStages;
-            few_wait(bar_full + 8 * stage, (uint32_t)((tc / C::kStages) & 1), abort, p.timeout_ns);
+            const int stage = kE2M1 ? at_stage : tc % C::kStages;
+            few_wait(bar_full + 8 * stage, (uint32_t)(kE2M1 ? at_phase : (tc / C::kStages) & 1), abort, p.timeout_ns);
             __syncwarp();
+            if (kE2M1 && ++at_stage == C::kStages) at_stage = 0, at_phase ^= 1;
             const uint32_t sk = ring + stage * C::kStage, sv = sk + C::kHalfStage;
             const int key0 = kt * kKeys + 16 * kSub * ws;   // this warp's first key
             const bool edge = key0 < full_lo || key0 + 16 * kSub > full_hi;
@@ -438,15 +461,16 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const int row = 32 * ws + 16 * t + 8 * n + perm(g);
+                        const uint32_t from = sk + k_at + (16 * t + 8 * n) * C::kRow;
+                        const uint8_t* const sf = scales + ks_at + (16 * t + 8 * n) * C::kScaleRow;
                         if (D == 128) {
-                            const uint4 v = lds128(sk + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4));
+                            const uint4 v = lds128(from);
                             w[t][n][0] = v.x, w[t][n][1] = v.y, w[t][n][kKw - 2] = v.z, w[t][n][kKw - 1] = v.w;
-                            f[t][n] = *reinterpret_cast<const uint16_t*>(scales + row * 8 + 2 * c4);
+                            f[t][n] = *reinterpret_cast<const uint16_t*>(sf);
                         } else {
-                            const uint2 v = lds64(sk + row * 32 + c4 * 8);
+                            const uint2 v = lds64(from);
                             w[t][n][0] = v.x, w[t][n][1] = v.y;
-                            f[t][n] = scales[row * 4 + c4];
+                            f[t][n] = *sf;
                         }
                     }
                 float s[2][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
@@ -479,24 +503,23 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                     }
                 // values: codes of keys perm(2c), perm(2c + 1) and + 8 of each tile, this lane's D / 8 columns; their scales
                 uint32_t vw[2][4][kVw], vf[2][2];
-                const uint8_t* const sc = scales + kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int r0 = 32 * ws + 16 * t + perm(2 * c4), r1 = 32 * ws + 16 * t + perm(2 * c4 + 1);
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int row = (x & 1 ? r1 : r0) + 8 * (x >> 1);
-                        if (D == 128) {
-                            const uint2 v = lds64(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-                            vw[t][x][0] = v.x, vw[t][x][kVw - 1] = v.y;
-                        } else {
-                            vw[t][x][0] = lds32(sv + row * 32 + g * 4);
+                    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t from = sv + (x ? v_at1 : v_at0) + (16 * t + 8 * n) * C::kRow;
+                            if (D == 128) {
+                                const uint2 v = lds64(from);
+                                vw[t][2 * n + x][0] = v.x, vw[t][2 * n + x][kVw - 1] = v.y;
+                            } else {
+                                vw[t][2 * n + x][0] = lds32(from);
+                            }
                         }
+                        const uint8_t* const sc = scales + (16 * t + 8 * n) * C::kScaleRow;
+                        vf[t][n] = sc[vs_at0] | (uint32_t)sc[vs_at1] << 8;
                     }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        vf[t][n] = sc[(r0 + 8 * n) * C::kScaleRow] | (uint32_t)sc[(r1 + 8 * n) * C::kScaleRow] << 8;
-                }
                 if (edge) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
