@@ -103,8 +103,8 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report
 // the many-rows kernel's 128-row products, mostly of rows that do not exist.  Measured (us; 16 sequences to 5000 keys,
 // Hq = 32, Hkv = 8; 5 tokens = 20 rows, 8 tokens = 32 rows, 12 tokens = 48 rows), few against many: e4m3, D = 128:
 // 60 / 76 / 109 against 95 / 98 / 98; D = 64: 43 / 55 / 73 against 62 / 63 / 65; bf16, D = 128: 74 / 95 / 132 against
-// 56 / 58 / 61.
-__host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_E4M3 ? kFewMost : 16; }   // E2M1: not measured yet
+// 56 / 58 / 61; E2M1, D = 128 (5, 6, 8 tokens): 52 / 54 / 65 against 65 / 68 / 68; D = 64: 43 / 43 / 51 against 51 / 51 / 51.
+__host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_BF16 ? 16 : kFewMost; }
 __host__ __device__ inline bool few_rows(int n, int G, int type) { return (long long)n * G <= few_most(type); }
 
 // Keys [lo, hi) that rows i0 .. i1 - 1 (tokens) of a sequence see.

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
             const int hh = h - (kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.c.Hkv);
             const __nv_bfloat16* base = kind == 0 ? p.q + token * p.q_t + hh * p.q_h
                                       : kind == 1 ? p.k + token * p.k_t + hh * p.k_h : p.v + token * p.v_t + hh * p.v_h;
+            if (kE2M1 && kind > 0 && !kept) base = kind == 1 ? p.k : p.v;   // (a token that is not written: any row, the first)
             ra[k].load(base, c0);
             rb[k].load(base, c1);
         }
