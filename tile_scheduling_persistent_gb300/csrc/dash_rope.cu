@@ -222,12 +222,15 @@ template <int D, int kType>
 __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ WriteParams p) {
     constexpr int U = D / 16, kAtOnce = 4;
     constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
-    const long long i = (long long)blockIdx.x * 128 + threadIdx.x;
+    const int heads = p.Hq + 2 * p.c.Hkv;
+    // the runs of heads of some tokens one after another, keys and values, which cost most, before queries
+    const unsigned runs = gridDim.y > 1 ? 1 : (unsigned)((heads + p.per - 1) / p.per);
+    const unsigned run = gridDim.y > 1 ? blockIdx.y : runs - 1 - blockIdx.x % runs;
+    const long long i = (long long)(blockIdx.x / runs) * 128 + threadIdx.x;
     const bool live = i / U < p.T;   // whole vectors: lanes of one vector agree
     const long long token = live ? i / U : p.T - 1;
     const int unit = (int)(i % U);
-    const int heads = p.Hq + 2 * p.c.Hkv;
-    const int h0 = blockIdx.y * p.per, h1 = min(h0 + p.per, heads);
+    const int h0 = (int)run * p.per, h1 = min(h0 + p.per, heads);
     const int rot = p.positions ? p.turns.rot : D;
     int c0, c1;
     chunks(unit, rot, c0, c1);
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
 
     const long long slots = (long long)p.c.num_pages * p.c.page_size;
     long long slot = p.slots[token];
-    if (slot >= slots && live && unit == 0 && blockIdx.y == 0)
+    if (slot >= slots && live && unit == 0 && run == 0)
         serve_error(DASH_ERR_PAGE, kOpWrite, token, slot, slots);
     const bool kept = live && slot >= 0 && slot < slots;
     if (!kept) slot = 0;
@@ -638,7 +641,9 @@ extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int
     const int D = cache->D;
     const long long blocks = ((long long)T * (D / 16) + 127) / 128;
     prm.per = heads_per_block(blocks, prm.Hq + 2 * cache->Hkv);
-    const dim3 grid((unsigned)blocks, (unsigned)((prm.Hq + 2 * cache->Hkv + prm.per - 1) / prm.per));
+    const int runs = (prm.Hq + 2 * cache->Hkv + prm.per - 1) / prm.per;
+    const bool flat = blocks * runs < (1ll << 31);   // (a grid holds no more in x: then the runs are its y)
+    const dim3 grid((unsigned)(flat ? blocks * runs : blocks), (unsigned)(flat ? 1 : runs));
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->type == DASH_CACHE_E2M1) {
         if (D == 64) write_kernel<64, DASH_CACHE_E2M1><<<grid, 128, 0, s>>>(prm);
