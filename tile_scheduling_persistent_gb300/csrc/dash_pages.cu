@@ -31,6 +31,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// Each kernel here is started while the one before it in the stream ends (launch_next), waits for that one's end before it
+// touches memory, and lets the next one start: two or three of them one after another are what a step launches.
+__device__ __forceinline__ void take_turn() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 // All threads of the cluster; what they wrote before it, in shared or global memory, is seen after it.
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -96,6 +102,7 @@ __device__ __forceinline__ int checked_len(const PagesParams& p, int op, int row
 // Block i writes row i of the new table, and changes the counts of the pages of row i of the old one by its children
 // less one: rows that go on as they are touch no count.
 __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesParams p) {
+    take_turn();
     const int i = blockIdx.x;
     if (i < p.rows_out) {
         int from = p.parents[i];
@@ -158,6 +165,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     const uint32_t rank = cluster_rank();
     const bool lead = rank == 0;
     const int tid = threadIdx.x, mask = at.slots - 1;
+    take_turn();
     auto hash = [&](int page) { return (int)(((uint32_t)page * 2654435761u) >> 7) & mask; };
 
     // free pages of this CTA's part of the pool
@@ -313,6 +321,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     __shared__ int scan[32];
     const uint32_t rank = cluster_rank();
     const int tid = threadIdx.x;
+    take_turn();
     const int tiles = (p.num_pages + kPoolTile - 1) / kPoolTile, per = (tiles + kCluster - 1) / kCluster;
     const int t0 = min((int)rank * per, tiles), t1 = min(t0 + per, tiles);
     auto counts_of = [&](int page0) -> int4 {
@@ -387,6 +396,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
 
 // The table with its pages renamed; blockIdx.y is the row.
 __global__ void __launch_bounds__(256) rename_kernel(const __grid_constant__ PagesParams p) {
+    take_turn();
     const int live = p.counts[1];
     for (int r = blockIdx.y; r < p.rows; r += gridDim.y) {
         const int held = pages_of(p, checked_len(p, kOpCompact, r, p.lens[r], blockIdx.x == 0 && threadIdx.x == 0));
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(256) rename_kernel(const __grid_constant__ Pag
 
 // ---------------------------------------------------------------- copy
 constexpr int kMostCaches = 64;        // of a launch
-constexpr int kCopyThreads = 256, kCopyVectors = 4;
+constexpr int kCopyThreads = 256, kCopyVectors = 8;
 constexpr int kCopyChunk = kCopyThreads * kCopyVectors * 16;
 
 struct CopyParams {
@@ -416,6 +426,7 @@ struct CopyParams {
 
 // Units of up to kCopyChunk bytes of one page, in the order of pairs.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+    take_turn();
     const int n = p.count ? min(max(*p.count, 0), p.most) : p.most;
     const int big = (int)((p.cells + kCopyChunk - 1) / kCopyChunk), small = (int)((p.scales + kCopyChunk - 1) / kCopyChunk);
     const int per_cache = 2 * big + (p.kinds > 2 ? 2 * small : 0);
@@ -474,7 +485,20 @@ PagesParams make_params(const int32_t* table, int64_t stride, const int32_t* len
     return p;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA; }
+template <typename P>
+int launch_next(void (*kernel)(const P), dim3 grid, unsigned threads, size_t smem, const P& p, dash_stream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -500,8 +524,7 @@ extern "C" int dash_pages_fork(const int32_t* table, int64_t table_stride, const
     p.stride_out = out_stride;
     p.lens_out = lens_out;
     p.rows_out = rows_out;
-    fork_kernel<<<rows > rows_out ? rows : rows_out, 256, 0, (cudaStream_t)stream>>>(p);
-    return launched();
+    return launch_next(fork_kernel, dim3(rows > rows_out ? rows : rows_out), 256, 0, p, stream);
 }
 
 extern "C" int dash_pages_extend(int32_t* table, int64_t table_stride, int32_t* lens, int rows, int max_pages, int32_t* refs, int num_pages,
@@ -533,8 +556,7 @@ extern "C" int dash_pages_extend(int32_t* table, int64_t table_stride, int32_t* 
             return DASH_ERR_CUDA;
         ready[dev] = true;
     }
-    extend_kernel<<<kCluster, kPoolThreads, smem, (cudaStream_t)stream>>>(p);
-    return launched();
+    return launch_next(extend_kernel, dim3(kCluster), kPoolThreads, smem, p, stream);
 }
 
 extern "C" int dash_pages_compact(const int32_t* table, int64_t table_stride, const int32_t* lens, int rows, int max_pages,
@@ -556,11 +578,9 @@ extern "C" int dash_pages_compact(const int32_t* table, int64_t table_stride, co
     p.copies = copies;
     p.counts = counts;
     p.rank = (int32_t*)workspace;
-    compact_kernel<<<kCluster, kPoolThreads, 0, (cudaStream_t)stream>>>(p);
-    if ((rc = launched()) || rows == 0 || max_pages == 0) return rc;
+    if ((rc = launch_next(compact_kernel, dim3(kCluster), kPoolThreads, 0, p, stream)) || rows == 0 || max_pages == 0) return rc;
     const dim3 grid((unsigned)((max_pages + 255) / 256), (unsigned)(rows < 65535 ? rows : 65535));
-    rename_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-    return launched();
+    return launch_next(rename_kernel, grid, 256, 0, p, stream);
 }
 
 extern "C" int dash_kv_copy(const dash_kv_cache* caches, int n_caches, const int32_t* copies, const int32_t* n_copies, int max_copies,
@@ -600,8 +620,7 @@ extern "C" int dash_kv_copy(const dash_kv_cache* caches, int n_caches, const int
         p.most = max_copies;
         const long long units = (long long)max_copies * p.caches * 2 *
                                 ((p.cells + kCopyChunk - 1) / kCopyChunk + (p.scales + kCopyChunk - 1) / kCopyChunk);
-        copy_kernel<<<(unsigned)(units < 8ll * sms ? units : 8ll * sms), kCopyThreads, 0, (cudaStream_t)stream>>>(p);
-        if ((rc = launched())) return rc;
+        if ((rc = launch_next(copy_kernel, dim3((unsigned)(units < 8ll * sms ? units : 8ll * sms)), kCopyThreads, 0, p, stream))) return rc;
     }
     return DASH_OK;
 }

@@ -637,16 +637,23 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
                                  wp, wn, st), what)
 
 
-def _pool(table, lens, refs, dev, what):
-    """The addresses of a block table [rows, max_pages], lens and refs, the table's stride, rows and width, the pages."""
-    if len(lens.shape) != 1 or len(refs.shape) != 1:
-        _refuse(what, "lens is int32 [rows] and refs int32 [num_pages]")
-    rows = lens.shape[0]
-    tp, ts, width = _table(table, rows, dev, what)
-    if rows > 1 and ts < width:
-        _refuse(what, "rows of the block table do not overlap")
-    N = refs.shape[0]
-    return tp, ts, _flat(lens, _I32, dev, (rows,), what, "lens"), rows, width, _flat(refs, _I32, dev, (N,), what, "refs"), N
+def _i32(t, dev, shape, what, name):
+    """The address of a contiguous int32 tensor (_flat, for the small calls on pages)."""
+    if t.dtype is not _I32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(what, "%s is a contiguous int32 tensor of shape %s on the current CUDA device" % (name, tuple(shape)))
+    return t.data_ptr()
+
+
+def _rows(table, lens, dev, what):
+    """A block table [rows, max_pages] and lens: address and stride of the table, address of lens, rows and width."""
+    shape = table.shape
+    if len(shape) != 2 or table.dtype is not _I32 or table.get_device() != dev:
+        _refuse(what, "the block table is an int32 tensor [rows, max_pages] on the current CUDA device")
+    rows, width = shape
+    row, col = table.stride()
+    if (col != 1 and width > 1) or (rows > 1 and row < width):
+        _refuse(what, "the block table is contiguous in its last dimension, and its rows do not overlap")
+    return table.data_ptr(), (row if rows > 1 else 0), _i32(lens, dev, (rows,), what, "lens"), rows, width
 
 
 def pages_fork(table, lens, parents, table_out, lens_out, refs, page_size, stream=None):
@@ -655,12 +662,13 @@ def pages_fork(table, lens, parents, table_out, lens_out, refs, page_size, strea
     child are dropped, their pages freed (see dash_pages_fork)."""
     what = "dash_pages_fork"
     dev, st = _device_stream(stream, what)
-    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
-    op, os_, olp, rows_out, width_out, _, _ = _pool(table_out, lens_out, refs, dev, what)
+    tp, ts, lp, rows, width = _rows(table, lens, dev, what)
+    op, os_, olp, rows_out, width_out = _rows(table_out, lens_out, dev, what)
     if width != width_out:
         _refuse(what, "table and table_out have the same width")
-    _check(lib().dash_pages_fork(tp, ts, lp, rows, _flat(parents, _I32, dev, (rows_out,), what, "parents"), op, os_, olp, rows_out, width,
-                                 rp, N, page_size, st), what)
+    N = refs.numel()
+    _check(lib().dash_pages_fork(tp, ts, lp, rows, _i32(parents, dev, (rows_out,), what, "parents"), op, os_, olp, rows_out, width,
+                                 _i32(refs, dev, (N,), what, "refs"), N, page_size, st), what)
 
 
 def pages_extend(table, lens, refs, page_size, slots, positions, copies, counts, cu_new=None, stream=None):
@@ -670,13 +678,12 @@ def pages_extend(table, lens, refs, page_size, slots, positions, copies, counts,
     pages that rows go on in (see dash_pages_extend)."""
     what = "dash_pages_extend"
     dev, st = _device_stream(stream, what)
-    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
-    T = slots.shape[0] if len(slots.shape) == 1 else -1
-    _check(lib().dash_pages_extend(tp, ts, lp, rows, width, rp, N, page_size,
-                                   _flat(cu_new, _I32, dev, (rows + 1,), what, "cu_new") if cu_new is not None else None,
-                                   _flat(slots, _I64, dev, (T,), what, "slots"), _flat(positions, _I32, dev, (T,), what, "positions"), T,
-                                   _flat(copies, _I32, dev, (rows, 2), what, "copies"), _flat(counts, _I32, dev, (2,), what, "counts"),
-                                   st), what)
+    tp, ts, lp, rows, width = _rows(table, lens, dev, what)
+    N, T = refs.numel(), slots.numel()
+    _check(lib().dash_pages_extend(tp, ts, lp, rows, width, _i32(refs, dev, (N,), what, "refs"), N, page_size,
+                                   _i32(cu_new, dev, (rows + 1,), what, "cu_new") if cu_new is not None else None,
+                                   _flat(slots, _I64, dev, (T,), what, "slots"), _i32(positions, dev, (T,), what, "positions"), T,
+                                   _i32(copies, dev, (rows, 2), what, "copies"), _i32(counts, dev, (2,), what, "counts"), st), what)
 
 
 def pages_compact(table, lens, refs, page_size, copies, counts, table_out=None, refs_out=None, workspace=None, stream=None):
@@ -685,11 +692,16 @@ def pages_compact(table, lens, refs, page_size, copies, counts, table_out=None, 
     dash_pages_compact).  workspace: uint8 tensor of 4 * num_pages bytes (None: as attn_paged's)."""
     what = "dash_pages_compact"
     dev, st = _device_stream(stream, what)
-    tp, ts, lp, rows, width, rp, N = _pool(table, lens, refs, dev, what)
-    table_out, refs_out = table if table_out is None else table_out, refs if refs_out is None else refs_out
-    op, os_, _, _, width_out, orp, N_out = _pool(table_out, lens, refs_out, dev, what)
-    if width != width_out or N != N_out:
-        _refuse(what, "table_out and refs_out have the shapes of table and refs")
+    tp, ts, lp, rows, width = _rows(table, lens, dev, what)
+    op, os_ = tp, ts
+    if table_out is not None:
+        op, os_, _, _, width_out = _rows(table_out, lens, dev, what)
+        if width != width_out:
+            _refuse(what, "table_out has the shape of table")
+    N = refs.numel()
+    rp = orp = _i32(refs, dev, (N,), what, "refs")
+    if refs_out is not None:
+        orp = _i32(refs_out, dev, (N,), what, "refs_out")
     wn = 4 * N
     if workspace is None:
         if stream is None:
@@ -702,8 +714,7 @@ def pages_compact(table, lens, refs, page_size, copies, counts, table_out=None, 
         wn = workspace.numel()
         wp = _flat(workspace, _U8, dev, (wn,), what, "workspace")
     _check(lib().dash_pages_compact(tp, ts, lp, rows, width, rp, N, page_size, op, os_, orp,
-                                    _flat(copies, _I32, dev, (N // 2, 2), what, "copies"), _flat(counts, _I32, dev, (2,), what, "counts"),
-                                    wp, wn, st), what)
+                                    _i32(copies, dev, (N // 2, 2), what, "copies"), _i32(counts, dev, (2,), what, "counts"), wp, wn, st), what)
 
 
 def kv_copy(k_caches, v_caches, copies, counts=None, k_scales=(), v_scales=(), stream=None):
@@ -715,12 +726,11 @@ def kv_copy(k_caches, v_caches, copies, counts=None, k_scales=(), v_scales=(), s
     n = len(k_caches)
     if len(v_caches) != n or len(k_scales) != len(v_scales) or (len(k_scales) != n and len(k_scales) != 0):
         _refuse(what, "there are as many caches, and scales if any, of values as of keys")
-    if len(copies.shape) != 2 or copies.shape[1] != 2:
-        _refuse(what, "copies is int32 [n, 2]")
+    most = copies.numel() // 2
     packed = b"".join([_cache(k, v, ks, vs, 0, 0, dev, what)[0]
                        for k, v, ks, vs in zip(k_caches, v_caches, k_scales or [None] * n, v_scales or [None] * n)])
-    _check(lib().dash_kv_copy(packed, n, _flat(copies, _I32, dev, (copies.shape[0], 2), what, "copies"),
-                              _flat(counts, _I32, dev, (2,), what, "counts") if counts is not None else None, copies.shape[0], st), what)
+    _check(lib().dash_kv_copy(packed, n, _i32(copies, dev, (most, 2), what, "copies"),
+                              _i32(counts, dev, (2,), what, "counts") if counts is not None else None, most, st), what)
 
 
 def get_status_paged(stream=None):
