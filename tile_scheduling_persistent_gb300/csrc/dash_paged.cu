@@ -231,8 +231,10 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
             ptx::mbar_init(bar + 8 * C::kStages, 4);
         }
         ptx::fence_mbar_init();
-        ptx::prefetch_tensormap(&p.tm_k);
-        ptx::prefetch_tensormap(&p.tm_v);
+        if (!kE2M1) {
+            ptx::prefetch_tensormap(&p.tm_k);
+            ptx::prefetch_tensormap(&p.tm_v);
+        }
     }
     if (many && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
     make_plan(p, plan, blockIdx.x == 0, many && blockIdx.x == 0 ? p.plan : nullptr);
@@ -285,6 +287,9 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                         const int box = kind % kBoxes, val = kind / kBoxes;
                         ptx::tma_load_3d(base + val * C::kHalfStage + box * (kKeys * 128) + sub * rows * 128,
                                          val ? &p.tm_v : &p.tm_k, 64 * box, y, head, full);
+                    } else if (kE2M1 && kind < 2) {
+                        bulk_load(base + kind * C::kHalfStage + sub * rows * C::kRow,
+                                  reinterpret_cast<const uint8_t*>(kind ? p.c.v : p.c.k) + ((long long)head * page + y) * C::kRow, rows * C::kRow, full);
                     } else if (kind < 2) {
                         ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * C::kRow, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
                     } else {
@@ -353,9 +358,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
     int tc = 0, parity = 0;
     // E2M1: where this lane reads in a stage, rows of its 32 keys 8 and 16 on at fixed distances (the swizzle repeats after 8)
     const int kp = 32 * ws + perm(g), vp0 = 32 * ws + perm(2 * c4), vp1 = 32 * ws + perm(2 * c4 + 1);
-    const uint32_t k_at = kp * C::kRow + (D == 128 ? (c4 ^ ((kp >> 1) & 3)) << 4 : c4 * 8);
-    const uint32_t v_at0 = vp0 * C::kRow + (D == 128 ? (((g >> 1) ^ ((vp0 >> 1) & 3)) << 4) + (g & 1) * 8 : g * 4);
-    const uint32_t v_at1 = vp1 * C::kRow + (D == 128 ? (((g >> 1) ^ ((vp1 >> 1) & 3)) << 4) + (g & 1) * 8 : g * 4);
+    const uint32_t k_at = kp * C::kRow + c4 * (D / 8), v_at0 = vp0 * C::kRow + g * (D / 16), v_at1 = vp1 * C::kRow + g * (D / 16);
     const uint32_t ks_at = kp * C::kScaleRow + (D == 128 ? 2 * c4 : c4), vs_col = kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
     const uint32_t vs_at0 = vp0 * C::kScaleRow + vs_col, vs_at1 = vp1 * C::kScaleRow + vs_col;
     int at_stage = 0, at_phase = 0;
@@ -1152,7 +1155,8 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
         prm.v_unit = ldexpf(1.f, cache->v_exp);
     }
     const int rows = cache->page_size < few_keys(cache->type) ? cache->page_size : few_keys(cache->type);
-    if (make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
+    if (cache->type != DASH_CACHE_E2M1 &&   // (whose vectors are copied as they lie: no tensor map to encode)
+        make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
         return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {
