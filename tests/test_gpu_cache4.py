@@ -273,3 +273,90 @@ def test_pages_out_of_range_are_reported_and_other_sequences_untouched():
         oo, ol = run_attn(one, q[b:b + 1], [1])
         assert same(oo, o[b:b + 1]) and same(ol, lse[b:b + 1])
     no_error()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_of_zero_and_least_exponents(n, D):
+    """Scores' scales far below the least normal number: masked keys stay masked, every seen one weighs the same."""
+    g = gen(11)
+    c = paged4(g, [200, 77], 2, D, 16, exps=(-64, 0))
+    q = randn(g, 2 * n, 8, D)
+    q[0] = 0
+    q[n:, 3] = 2.0 ** -120
+    o, lse = run_attn(c, q, [n, n])
+    no_error()
+    check_attn4(c, q, [n, n], o, lse)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_that_are_not_finite_give_nan_in_their_rows_alone(bad, n, D):
+    g = gen(12)
+    c = paged4(g, [300], 2, D, 16)
+    q = randn(g, n, 8, D)
+    want, _ = run_attn(c, q, [n])
+    q[n - 1, 5, 7] = bad
+    o, lse = run_attn(c, q, [n])
+    no_error()
+    assert torch.isnan(o[n - 1, 5]).all() and torch.isnan(lse[n - 1, 5])
+    keep = torch.ones(n, 8, dtype=torch.bool)
+    keep[n - 1, 5] = False
+    assert same(o[keep.to(DEV)], want[keep.to(DEV)])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_strided_queries_and_packed_types(D):
+    """Queries inside a wider projection, caches as pairs of 4-bit floats."""
+    g = gen(13)
+    c = paged4(g, [90, 400], 2, D, 32)
+    wide = randn(g, 7, 12, D).to(DEV)
+    q = wide[:, 2:10]
+    n = [3, 4]
+    o, lse = run_attn(c, q, n)
+    check_attn4(c, q.cpu().contiguous(), n, o, lse)
+    if hasattr(torch, "float4_e2m1fn_x2"):
+        packed = type(c)(c.k, c.v, c.k_cache.view(torch.float4_e2m1fn_x2), c.v_cache.view(torch.float4_e2m1fn_x2), None, None, c.table, c.lens, c.kw)
+        o2, lse2 = run_attn(packed, q, n)
+        assert same(o, o2) and same(lse, lse2)
+    no_error()
+
+
+def test_refusals_of_the_binding():
+    c = paged4(gen(14), [40], 2, 64, 16)
+    o = torch.empty(1, 8, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros_like(o)
+    good = dict(c.kw)
+    for kw in (dict(k_scale=None), dict(v_scale=c.v_scale.view(torch.uint8)), dict(k_scale=c.k_scale[..., :2]), dict(k_exp=65), dict(v_exp=-65),
+               dict(k_scale=torch.zeros(c.k_cache.shape[:3], device=DEV))):
+        with pytest.raises(dash.DashError):
+            dash.attn_paged(q, c.k_cache, c.v_cache, c.table, c.lens, o, **{**good, **kw})
+    with pytest.raises(dash.DashError):
+        dash.attn_paged(q, c.k_cache, c.v_cache.view(torch.int8), c.table, c.lens, o, **good)
+    with pytest.raises(dash.DashError):   # 32 bytes are 64 values: the queries have as many
+        dash.attn_paged(q[..., :32], c.k_cache, c.v_cache, c.table, c.lens, o, **good)
+    with pytest.raises(dash.DashError):
+        dash.kv_read(c.k_cache, c.v_cache, c.table, c.lens, o[None], o[None], **good)
+
+
+def test_captured_and_on_another_stream():
+    c, q, n, window = inputs("mixed", seed=15)
+    want, wl = run_attn(c, q, n, window=window)
+    q = q.to(DEV)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device=DEV)
+    outs = [(torch.full_like(want, 77.0), torch.full_like(wl, 77.0)) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in outs]
+    for g, (o, l) in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            dash.attn_paged(q, c.k_cache, c.v_cache, c.table, c.lens, o, cu_q=cu, max_q=max(n), lse=l, window=window, **c.kw)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for s, g in zip(streams, graphs):   # two replays at once
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, l in outs:
+        assert same(o, want) and same(l, wl)
+    no_error()

@@ -746,9 +746,11 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                         for (int k = 0; k < kCols; ++k) y[k] = __uint_as_float(r[k >> 5][k & 31]);
                     }
                     if constexpr (kConv) {
-                        if (j == 0)
+                        if (j == 0) {
                             c[n] *= reinterpret_cast<const float*>(
                                 smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? tile(n) : slot)) * 128 + row];
+                            if (kE2M1) c[n] = fmaxf(c[n], 0x1p-126f);   // (above zero, whatever k_exp: -inf times it stays -inf)
+                        }
                     }
                     if constexpr (kE4M3) {
 #pragma unroll
