@@ -51,11 +51,12 @@ typedef enum {
     DASH_ERR_LAUNCH = -3,     /* the persistent grid cannot be co-resident on this device */
     DASH_ERR_TIMEOUT = -4,    /* device-side wait exceeded the timeout (reported by dash_get_status) */
     DASH_ERR_DEADLOCK = -5,   /* a schedule table cannot complete (cycle or missing predecessor) */
-    DASH_ERR_NOMEM = -6,      /* workspace allocation failed */
+    DASH_ERR_NOMEM = -6,      /* workspace allocation failed; dash_pages_extend: too few free pages (reported by
+                               * dash_get_status_paged) */
     DASH_ERR_DEVICE = -7,     /* device is not sm_103 / lacks the needed shared memory */
     DASH_ERR_SCRATCH = -8,    /* problem needs more than dash_attn_bwd_noalloc's fixed scratch, or than the
                                * workspace given to dash_attn_paged */
-    DASH_ERR_PAGE = -9        /* a page, slot, position or length on the device lies outside what the call was
+    DASH_ERR_PAGE = -9        /* a page, slot, row, position or length on the device lies outside what the call was
                                * given (reported by dash_get_status_paged) */
 } dash_status;
 
