@@ -142,13 +142,13 @@ __host__ __device__ inline int few_workers(int D, int type) {
 // (us; Hq = 32, Hkv = 8, D = 128; 1000 bf16 keys, 4000 and 8192 e4m3 keys alone, 64 ragged e4m3 sequences to 8192, 256 to
 // 2000), ranges of at least 2 stages: 8.3 11.8 15.1 136 149; 4: 9.6 10.3 13.2 107 117; 8: 12.5 11.7 12.7 99 109; 16: 17.6
 // 15.5 16.3 97 111; growing with the sequence, as here: 8.5 11.9 12.7 100 129.
-// E2M1, in stages of 128 keys: a range's costs weigh more against half the bytes.  Measured (us; as above, D = 128: 1000 keys
-// alone, 64 ragged sequences, and 3 of 262143 at D = 64), ranges of at least 1024 keys from 32 stages on, a quarter of the
-// sequence before: 13.2 85.9 194.5; from 64 on, an eighth before (as for the other types): 13.1 91.8 195; 2048 from 32 on:
-// 13.2 92.4 199.
+// E2M1, in stages of 128 keys: a range's costs weigh more against half the bytes.  Measured (us; Hq = 32, Hkv = 8, D = 128;
+// 1000, 4000 and 8192 keys alone, 64 ragged sequences to 8192, 256 to 2000), ranges of a sixth of the sequence, 6 stages at
+// the most, as here: 9.3 12.0 13.0 81.6 99.4; of a quarter, 8 at the most: 9.3 13.5 13.6 79.9 97.5; of 3 stages, from 48 on 6:
+// 9.3 8.8 13.1 88.5 97.8; of an eighth, 5 at the most: 9.3 10.6 12.5 84.2 106.
 __host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st, int type = DASH_CACHE_BF16) {
     const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, heads);
-    const int least = type == DASH_CACHE_E2M1 ? (tiles >= 32 ? 8 : tiles > 8 ? (tiles + 3) / 4 : 2)
+    const int least = type == DASH_CACHE_E2M1 ? (tiles >= 36 ? 6 : tiles > 12 ? (tiles + 5) / 6 : 2)
                                               : tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
     st = (tiles + most - 1) / most;
     st = st < least ? least : st;
