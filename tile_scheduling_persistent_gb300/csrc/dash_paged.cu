@@ -43,6 +43,34 @@
 // a row lie near 2^7 whatever the scales (kLiftE4M3); the sum l keeps its own
 // maximum m.
 //
+// E2M1 caches.  Pairs of codes become fp16 and take their block's scale, both
+// exact (2 + 4 bits), so the products run in fp16 on the values themselves; the
+// cache's 2^k_exp is in the scores' scale, 2^v_exp in the output's.  9 bytes for
+// 16 values leave so little time for each that the work counts as much as the
+// bytes: a pair's conversion and its product with the scale run at 64 a cycle
+// and SM, two thirds of the time that memory takes for them.  So
+//   - a consumer warp takes 32 keys of a 128-key stage, as two 16-key tiles whose
+//     products alternate; waits, votes and addresses serve twice the keys
+//     (3 x 262143 tokens, D = 64: 283 us with 16 keys, 202 us so);
+//   - the scores' scale enters the exponent's multiply-add, one running maximum
+//     serves O and l (weights carry 2^7 as with e4m3);
+//   - values lie beside each other by key, but a product wants two keys of one
+//     column in a register: the halves of two keys' bytes are exchanged before the
+//     conversion, two shifts and two selections for 16 codes;
+//   - the consumers take registers that the producers do not need (152 of 128);
+//   - codes and scales are copied as they lie (no swizzle, no tensor map to encode
+//     for each call): K is read without bank conflicts (rows of 64 bytes in the
+//     order below, of 32 in its own), V two lanes to a bank at D = 128.
+// Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 82 us
+// with the join, 3.8 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 197 us,
+// 4.6 TB/s; 2 of 262144 (D = 128) 120 us, 5.0 TB/s.  Of 334 instructions for 16
+// keys of a head at D = 128, 64 convert, 64 scale, 16 multiply; with all the
+// conversions left out the long sequences still take 112 us, so memory's latency
+// and the items' ends are the rest.  Built and dropped: four groups (88.8 us and
+// spills), items from a counter (84 us), one item of up to 24 rows whose warps share
+// O by columns instead of keys, P going through shared memory (two barriers a
+// stage: 102 us, 16 x 5 tokens 43 us against 47).
+//
 // Masked keys get s = -inf by a select, never by arithmetic, and value rows
 // outside the visible keys (stale or unwritten cells, freed pages) are zeroed
 // in shared memory before they meet a zero weight.
@@ -322,8 +350,9 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
     const int ws = warp & 3;
     // key of row n of an 8-key tile: e4m3 reads whole 16-byte chunks per lane, and this order keeps both the K reads
     // (rows n, n + 1 in one quarter of a warp) and the V reads (rows 2c) free of bank conflicts under the 128-byte swizzle.
-    // E2M1: the same for rows of 64 bytes (V: 8-byte reads of rows 0, 4, 1, 5 by half a warp) and of 32 (K: 8-byte reads
-    // of rows 0 to 3; V: 4-byte reads of rows 0, 2, 5, 7, one in each quarter of the banks).
+    // E2M1, rows that are not swizzled: of 64 bytes (K: 16-byte reads of an even and an odd row; V: 8-byte reads of rows 0,
+    // 4, 1, 5 by half a warp, two to a bank) and of 32 (K: 8-byte reads of rows 0 to 3; V: 4-byte reads of rows 0, 2, 5, 7,
+    // one in each quarter of the banks).
     auto perm = [](int n) {
         constexpr uint32_t order = kE4M3 ? 0x36147250u : D == 128 ? 0x65217430u : 0x67453210u;
         return kBf16 ? n : (int)((order >> (4 * n)) & 7u);

@@ -45,9 +45,9 @@
 // cycles for each matrix tile, of which the tensor core takes 512: 840 for the
 // exponentials, 550 to read and scale the scores, 200 to 400 waiting for them.
 //
-// Warps: 0 producer (TMA: Q, and K / V pages of bf16 caches), 1 MMA issuer and
+// Warps: 0 producer (TMA: Q, and K / V pages of bf16 and E2M1 caches), 1 MMA issuer and
 // tensor memory, 2 item scheduler, 3 idle, 4-7 and 8-11 softmax and epilogue,
-// and for e4m3 caches 12-15 converters.
+// and for e4m3 and E2M1 caches 12-15 converters.
 //
 // e4m3 caches.  The converters read codes from the pages one tile ahead and
 // store them, as TMA would a bf16 cache's tile, in fp16; the products then run
@@ -60,6 +60,17 @@
 // fp16's range is met with powers of two, undone in fp32: V by the largest scale so far in the item in [2^6, 2^7) (codes reach 448; when
 // it grows, O is rescaled as for a grown maximum), Q by row, its largest value
 // in [2^14, 2^15), converted in place.
+//
+// E2M1 caches.  The producer stages codes and scales as they lie in the pages (a
+// ring of three K or V tiles, one bulk copy for each page's share), and the
+// converters turn them into fp16 tiles of code * scale, exact, from shared memory:
+// held in registers between the loads and the proxy fence, which waits for every
+// access, the codes cost a trip to memory for each tile (2048 tokens over 8192:
+// 635 us; 208 us so, 190 us for a bf16 cache).  Nothing is left to be scaled, so the
+// softmax is the bf16 caches', a warpgroup for each row tile, with fp16 weights and
+// queries as for e4m3; the cache's exponents join the scores' and the output's
+// scale.  With half of the exponentials left out it is no faster either: the
+// chain from a tile's scores to its weights bounds it as it does with bf16 caches.
 //
 // Tensor memory: S/P buffers at columns 0 and 128; O of A at 256, of B at 384 (e4m3 at
 // D = 64: the second half of the keys 64 columns on).

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
     constexpr int U = D / 16, kAtOnce = 4;
     constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
     const int heads = p.Hq + 2 * p.c.Hkv;
-    // the runs of heads of some tokens one after another, keys and values, which cost most, before queries
+    // (one y: the runs of heads of some tokens one after another, the last first)
     const unsigned runs = gridDim.y > 1 ? 1 : (unsigned)((heads + p.per - 1) / p.per);
     const unsigned run = gridDim.y > 1 ? blockIdx.y : runs - 1 - blockIdx.x % runs;
     const long long i = (long long)(blockIdx.x / runs) * 128 + threadIdx.x;
@@ -642,7 +642,10 @@ extern "C" int dash_kv_write(const dash_kv_cache* cache, const dash_bf16* k, int
     const long long blocks = ((long long)T * (D / 16) + 127) / 128;
     prm.per = heads_per_block(blocks, prm.Hq + 2 * cache->Hkv);
     const int runs = (prm.Hq + 2 * cache->Hkv + prm.per - 1) / prm.per;
-    const bool flat = blocks * runs < (1ll << 31);   // (a grid holds no more in x: then the runs are its y)
+    // E2M1: the runs of heads of some tokens one after another, keys and values first, whose quantising then overlaps with the
+    // queries' traffic (65532 tokens, 32 and 8 heads: 262 us to 243 us; e4m3, 8191 tokens: 37.9 us to 38.4 us).  A grid holds
+    // no more than 2^31 - 1 in x.
+    const bool flat = cache->type == DASH_CACHE_E2M1 && blocks * runs < (1ll << 31);
     const dim3 grid((unsigned)(flat ? blocks * runs : blocks), (unsigned)(flat ? 1 : runs));
     cudaStream_t s = (cudaStream_t)stream;
     if (cache->type == DASH_CACHE_E2M1) {
