@@ -428,7 +428,7 @@ typedef enum { DASH_CACHE_BF16 = 0, DASH_CACHE_E4M3 = 1, DASH_CACHE_E2M1 = 2 } d
  * values of a vector: k_scale and v_scale are the addresses of bytes
  * [num_pages, Hkv, page_size, D / 16].  Its values stand for
  * code * scale * 2^k_exp (v_exp), one exponent for the whole cache: values up to
- * 2688 * 2^exp can be held, and a scale has all its four bits where the largest
+ * 2688 * 2^exp can be held (larger ones become that), and a scale has all its four bits where the largest
  * of its 16 values is at least 2^-3 * 2^exp.  num_pages * Hkv < 2^31.
  * All contiguous device memory, 16-byte aligned.  page_size: 16, 32, 64, 128
  * or 256; D in {64, 128}.  Token offset o of page p is slot p*page_size + o.
@@ -595,9 +595,10 @@ int dash_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* l
  * from cu_new[rows] to T get slot -1 and position 0.
  * With fewer free pages than are needed nothing is taken: counts are 0, every slot
  * is -1, table, lens and refs are as they were, and DASH_ERR_NOMEM is reported
- * (needed and free).  A row whose length, tokens or last page is out of range, or
- * whose pages would pass max_pages, is reported (DASH_ERR_PAGE) and left as it
- * is, its slots -1; other rows are not affected.  At most 4096 rows.
+ * (needed and free).  A row whose length, tokens or last page is out of range,
+ * whose partly filled last page is counted as free, or whose pages would pass
+ * max_pages, is reported (DASH_ERR_PAGE) and left as it is, its slots -1; other
+ * rows are not affected.  At most 4096 rows.
  * Returns DASH_OK, DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_pages_extend(int32_t* table, int64_t table_stride, int32_t* lens, int rows, int max_pages, int32_t* refs,

@@ -300,3 +300,57 @@ def test_in_a_captured_graph_and_on_another_stream(make):
         assert torch.equal(t[done], want[n][done]), n
     assert all(torch.equal(t.view(torch.uint8), w) for t, w in zip((c.k_cache, c.v_cache), cells))
     no_error()
+
+
+def test_a_last_page_that_counts_as_free_is_reported():
+    p = Pool(random.Random(8), 20, 16, 4, 2, 0)
+    p.rows, p.lens, p.refs = [[4], [9]], [3, 5], [0] * 20
+    p.refs[9] = 1                                        # page 4 is free
+    p.up()
+    slots, pos, copies, counts = ints([9] * 2, torch.int64), ints([9] * 2), ints([[MARK] * 2] * 2), ints([9, 9])
+    dash.pages_extend(p.t, p.l, p.c, 16, slots, pos, copies, counts)
+    assert dash.get_status_paged() == (dash.ERR_PAGE, [5, 0, 0, 1])
+    assert slots.tolist() == [-1, 149] and p.l.tolist() == [3, 6] and counts.tolist() == [0, 0]
+    no_error()
+
+
+def test_copy_of_layers_in_one_tensor():
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randint(0, 256, (3, 5, 2, 16, 32), generator=g, dtype=torch.uint8).to(DEV) for _ in range(2))
+    ks, vs = (torch.randint(0, 256, (3, 5, 2, 16, 4), generator=g, dtype=torch.uint8).to(DEV) for _ in range(2))
+    want = [t.clone() for t in (k, v, ks, vs)]
+    for t in want:
+        t[:, 1] = t[:, 4].clone()
+    dash.kv_copy(k, v, ints([[4, 1]]), k_scales=ks.view(E4M3), v_scales=vs.view(E4M3))
+    assert all(torch.equal(a, b) for a, b in zip((k, v, ks, vs), want))
+    no_error()
+
+
+def test_calls_on_two_streams_at_once():
+    """Pools of their own on streams of their own, without waiting for one another."""
+    pools = [Pool(random.Random(s), 600, 16, 20, 30, 100) for s in (21, 22)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    torch.cuda.synchronize()
+    work = []
+    for p, st in zip(pools, streams):
+        R = len(p.rows)
+        a = dict(par=ints(list(range(R)) + [0, 0, 3]), t1=torch.zeros(R + 3, 20, dtype=torch.int32, device=DEV), l1=ints([0] * (R + 3)),
+                 slots=torch.zeros(2 * (R + 3), dtype=torch.int64, device=DEV), pos=ints([0] * (2 * (R + 3))), copies=ints([[MARK] * 2] * (R + 3)),
+                 counts=ints([0, 0]), moved=ints([[MARK] * 2] * 300), mc=ints([0, 0]))
+        work.append(a)
+    torch.cuda.synchronize()
+    for p, st, a in zip(pools, streams, work):
+        with torch.cuda.stream(st):
+            dash.pages_fork(p.t, p.l, a["par"], a["t1"], a["l1"], p.c, 16)
+            dash.pages_extend(a["t1"], a["l1"], p.c, 16, a["slots"], a["pos"], a["copies"], a["counts"])
+            dash.pages_compact(a["t1"], a["l1"], p.c, 16, a["moved"], a["mc"])
+    torch.cuda.synchronize()
+    for p, a in zip(pools, work):
+        rows, lens, refs = PG.fork(p.rows, p.lens, a["par"].tolist(), p.refs)
+        rows, lens, refs, want, taken, at, where = PG.extend(rows, lens, refs, [2] * len(rows), 16)
+        assert a["slots"].tolist() == where and a["counts"].tolist() == [len(want), taken]
+        p.rows, p.refs, moves, live = PG.compact(rows, refs)
+        p.lens, p.t, p.l = lens, a["t1"], a["l1"]
+        assert a["mc"].tolist() == [len(moves), live]
+        p.check()
+    no_error()

@@ -1169,8 +1169,11 @@ int launch_tile_t(const PagedParams& p, int grid, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_tile_kernel<D, kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        cudaFuncAttributes a;
+        if (cudaFuncSetAttribute(paged_tile_kernel<D, kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess ||
+            cudaFuncGetAttributes(&a, paged_tile_kernel<D, kType>) != cudaSuccess)
             return DASH_ERR_CUDA;
+        if (a.numRegs < C::kRegsLaunch) return DASH_ERR_LAUNCH;   // the softmax would wait for registers that are not there
         ready[dev] = true;
     }
     return launch_after(paged_tile_kernel<D, kType>, grid, C::kThreads, C::kSmem, p, s);

@@ -160,7 +160,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     __shared__ int scan_i[32];
     __shared__ long long scan_l[32];
     const ExtendLayout at(p.rows);
-    int *const start = sm + at.start(), *const len = sm + at.len(), *const cu = sm + at.cu(), *const last = sm + at.last(), *const place = sm + at.place();
+    int *const start = sm + at.start(), *const len = sm + at.len(), *const cu = sm + at.cu();
+    int *const last = sm + at.last(), *const place = sm + at.place();
     int *const key = sm + at.key(), *const count = sm + at.count(), *const first = sm + at.first();
     const uint32_t rank = cluster_rank();
     const bool lead = rank == 0;
@@ -206,7 +207,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
             if (page < 0 || page >= p.num_pages) {
                 if (lead) serve_error(DASH_ERR_PAGE, kOpExtend, r, page, p.num_pages);
                 ok = false;
-            } else if (p.refs[page] <= 1) {
+            } else if (p.refs[page] < 1) {   // held, and free: it may be another row's by the end of this call
+                if (lead) serve_error(DASH_ERR_PAGE, kOpExtend, r, p.refs[page], 1);
+                ok = false;
+            } else if (p.refs[page] == 1) {
                 page = -1;   // its own
             } else {
                 int s = hash(page);
@@ -353,7 +357,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     for (int t = t0; t < t1 && t * kPoolTile < live; ++t) {
         const int page0 = t * kPoolTile + 4 * tid;
         const int4 r = counts_of(page0);
-        mine += (r.x != 0 && page0 < live) + (r.y != 0 && page0 + 1 < live) + (r.z != 0 && page0 + 2 < live) + (r.w != 0 && page0 + 3 < live);
+        mine += (r.x != 0 && page0 < live) + (r.y != 0 && page0 + 1 < live) + (r.z != 0 && page0 + 2 < live) +
+                (r.w != 0 && page0 + 3 < live);
     }
     block_scan(mine, scan, all);
     if (tid == 0) pool_below = all;
@@ -437,7 +442,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
         const int i = (int)(of / p.caches), cache = (int)(of - (long long)i * p.caches);
         const int from = p.copies[2 * i], to = p.copies[2 * i + 1];
         if (from < 0 || to < 0 || from >= p.num_pages || to >= p.num_pages) {
-            if (threadIdx.x == 0 && part == 0 && cache == 0) serve_error(DASH_ERR_PAGE, kOpCopy, i, from < 0 || from >= p.num_pages ? from : to, p.num_pages);
+            if (threadIdx.x == 0 && part == 0 && cache == 0)
+                serve_error(DASH_ERR_PAGE, kOpCopy, i, from < 0 || from >= p.num_pages ? from : to, p.num_pages);
             continue;
         }
         int kind = 0;
@@ -513,7 +519,8 @@ extern "C" int dash_pages_fork(const int32_t* table, int64_t table_stride, const
                                int num_pages, int page_size, dash_stream_t stream) {
     if (!pool_ok(table, table_stride, lens, rows, max_pages, refs, num_pages, page_size) ||
         !pool_ok(table_out, out_stride, lens_out, rows_out, max_pages, refs, num_pages, page_size) ||
-        (rows_out > 0 && (!parents || ((uintptr_t)parents & 3u))) || (rows && rows_out && (lens == lens_out || (max_pages && table == table_out))))
+        (rows_out > 0 && (!parents || ((uintptr_t)parents & 3u))) ||
+        (rows && rows_out && (lens == lens_out || (max_pages && table == table_out))))
         return DASH_ERR_ARG;
     if (rows == 0 && rows_out == 0) return DASH_OK;
     const int rc = serve_check_device();

@@ -236,7 +236,8 @@ def set_timeout_ns(ns):
 
 
 def release_workspaces():
-    """Gives back the device memory that calls keep: the library's, and attn_paged's of every thread and stream."""
+    """Gives back the device memory that calls keep: the library's, and that of attn_paged and pages_compact for every
+    thread and stream."""
     with _kept_lock:
         _kept.clear()
     _check(lib().dash_release_workspaces(), "dash_release_workspaces")
@@ -718,7 +719,8 @@ def pages_compact(table, lens, refs, page_size, copies, counts, table_out=None, 
 
 
 def kv_copy(k_caches, v_caches, copies, counts=None, k_scales=(), v_scales=(), stream=None):
-    """Copy pages within the caches of one or several layers (lists of caches of one shape, and of their scales): page
+    """Copy pages within the caches of one or several layers (lists, or tensors with a dimension of layers in front, of
+    caches of one shape and of their scales): page
     copies[i, 0] to copies[i, 1] (int32 [n, 2]) for i < counts[0] (int32 [2] as pages_extend and pages_compact leave
     it; None: all of them)."""
     what = "dash_kv_copy"
@@ -727,8 +729,9 @@ def kv_copy(k_caches, v_caches, copies, counts=None, k_scales=(), v_scales=(), s
     if len(v_caches) != n or len(k_scales) != len(v_scales) or (len(k_scales) != n and len(k_scales) != 0):
         _refuse(what, "there are as many caches, and scales if any, of values as of keys")
     most = copies.numel() // 2
-    packed = b"".join([_cache(k, v, ks, vs, 0, 0, dev, what)[0]
-                       for k, v, ks, vs in zip(k_caches, v_caches, k_scales or [None] * n, v_scales or [None] * n)])
+    if len(k_scales) == 0:
+        k_scales = v_scales = (None,) * n
+    packed = b"".join([_cache(k, v, ks, vs, 0, 0, dev, what)[0] for k, v, ks, vs in zip(k_caches, v_caches, k_scales, v_scales)])
     _check(lib().dash_kv_copy(packed, n, _i32(copies, dev, (most, 2), what, "copies"),
                               _i32(counts, dev, (2,), what, "counts") if counts is not None else None, most, st), what)
 
