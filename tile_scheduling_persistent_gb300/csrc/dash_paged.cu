@@ -57,7 +57,7 @@
 //   - values lie beside each other by key, but a product wants two keys of one
 //     column in a register: the halves of two keys' bytes are exchanged before the
 //     conversion, two shifts and two selections for 16 codes;
-//   - the consumers take registers that the producers do not need (152 of 128);
+//   - the consumers take registers that the producers do not need (144 of 128);
 //   - codes and scales are copied as they lie (no swizzle, no tensor map to encode
 //     for each call): K is read without bank conflicts (rows of 64 bytes in the
 //     order below, of 32 in its own), V two lanes to a bank at D = 128.
@@ -169,7 +169,7 @@ struct FewCfg {
     static constexpr int kRows = kFewRows;
     // E2M1: the producers' registers go to the consumers (setmaxnreg works on whole warpgroups: one warp stays idle)
     static constexpr bool kRegs = kE2M1;
-    static constexpr int kRegsConsumer = 152, kRegsProducer = 56;
+    static constexpr int kRegsConsumer = 144, kRegsProducer = 80;
     static constexpr int kThreads = kRegs ? kGroups * 128 + 128 : kGroups * 160;
     static_assert(!kRegs || (kGroups == 3 && 384 * kRegsConsumer + 128 * kRegsProducer <= 512 * 128), "register split");
     static constexpr int kRow = cell_bytes(kType, D), kScaleRow = scale_bytes(kType, D);   // of a key
