@@ -130,6 +130,12 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
     return h;
 }
+// Bits of a where m has ones, of b elsewhere.
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+    return r;
+}
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -281,6 +287,12 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
         const int kinds = !kBf16 ? 4 : D / 32;            // K (per 64 values), V (same), or K, V and their scales
         const int sub = lane / kinds, kind = lane % kinds;
         const uint32_t sub_bytes = (uint32_t)rows * 2 * (C::kRow + C::kScaleRow);
+        // E2M1: every kind is copied as it lies, `each` bytes a key
+        const uint32_t each = kind < 2 ? C::kRow : C::kScaleRow, pitch = 2 * kKeys * each;
+        const uint8_t* const from = reinterpret_cast<const uint8_t*>(kind == 0 ? p.c.k : kind == 1 ? p.c.v
+                                                                     : kind == 2 ? (const void*)p.c.k_scale : (const void*)p.c.v_scale);
+        const uint32_t to = (kind < 2 ? ring : sbase + C::OFF_SCALE + group * C::kStages * 2 * kKeys * C::kScaleRow) +
+                            (uint32_t)((kind & 1) * kKeys + sub * rows) * each;
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
             find_item<kKeys>(p, plan, item, it);
@@ -315,9 +327,8 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                         const int box = kind % kBoxes, val = kind / kBoxes;
                         ptx::tma_load_3d(base + val * C::kHalfStage + box * (kKeys * 128) + sub * rows * 128,
                                          val ? &p.tm_v : &p.tm_k, 64 * box, y, head, full);
-                    } else if (kE2M1 && kind < 2) {
-                        bulk_load(base + kind * C::kHalfStage + sub * rows * C::kRow,
-                                  reinterpret_cast<const uint8_t*>(kind ? p.c.v : p.c.k) + ((long long)head * page + y) * C::kRow, rows * C::kRow, full);
+                    } else if (kE2M1) {
+                        bulk_load(to + stage * pitch, from + ((long long)head * page + y) * each, rows * each, full);
                     } else if (kind < 2) {
                         ptx::tma_load_3d(base + kind * C::kHalfStage + sub * rows * C::kRow, kind ? &p.tm_v : &p.tm_k, 0, y, head, full);
                     } else {
@@ -615,7 +626,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const uint32_t a = vw[t][2 * n][y], b = vw[t][2 * n + 1][y];
-                            const uint32_t even = (a & kLow) | ((b << 4) & ~kLow), odd = ((a >> 4) & kLow) | (b & ~kLow);
+                            const uint32_t even = select_bits(a, b << 4, kLow), odd = select_bits(a >> 4, b, kLow);
                             h[n][0] = mul_half2(half2_of_e2m1<0>(even), vf[t][n]);
                             h[n][1] = mul_half2(half2_of_e2m1<0>(odd), vf[t][n]);
                             h[n][2] = mul_half2(half2_of_e2m1<1>(even), vf[t][n]);
