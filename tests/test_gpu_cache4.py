@@ -173,6 +173,12 @@ CASES = {
     "decode_many": (16, 8, 64, 16, [37 * i % 900 + 1 for i in range(70)], [1] * 70, None, 0),
     "verify_many": (32, 8, 128, 32, [301 * i % 1900 + 6 for i in range(40)], [5] * 40, None, 0),
     "verify_many_window": (32, 8, 64, 16, [301 * i % 1900 + 6 for i in range(40)], [6] * 40, 500, 0),
+    # small pages in batches that fill the GPU, with windows that begin inside a page
+    "decode_many_pages_16": (16, 8, 128, 16, [53 * i % 1700 + 1 for i in range(40)], [1] * 40, None, 0),
+    "decode_many_pages_32": (16, 8, 64, 32, [53 * i % 1700 + 1 for i in range(40)], [1] * 40, 333, 0),
+    "decode_many_pages_16_window": (32, 4, 128, 16, [71 * i % 900 + 2 for i in range(50)], [2] * 50, 77, 2),
+    "chunk_pages_16": (8, 8, 128, 16, [333, 1000, 20], [100, 333, 20], 250, 0),
+    "chunk_pages_32": (8, 2, 64, 32, [333, 1000, 20], [100, 333, 20], None, 0),
     "chunk_many": (8, 8, 128, 64, [211 * i % 700 + 300 for i in range(30)], [17 * i % 300 + 17 for i in range(30)], None, 3),
     "group_128": (128, 1, 64, 16, [90, 300], [1, 3], None, 0),
 }

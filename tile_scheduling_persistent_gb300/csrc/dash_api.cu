@@ -461,6 +461,23 @@ int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long
     return r == CUDA_SUCCESS ? 0 : -2;
 }
 
+int make_tmap_gather(void* map_a, void* map_b, const void* a, const void* b, long long rows, int bytes) {
+    EncodeTiledFn fn = encode_fn();
+    ReplaceAddressFn replace = replace_address_fn();
+    if (!fn || !replace) return -2;
+    const cuuint64_t dims[2] = {(cuuint64_t)(bytes / 4), (cuuint64_t)rows};   // (a box is at most 256 elements wide)
+    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)(bytes / 4), 1};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(reinterpret_cast<CUtensorMap*>(map_a), CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(a), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return -2;
+    memcpy(map_b, map_a, sizeof(CUtensorMap));   // b's is a's at another address
+    r = replace(reinterpret_cast<CUtensorMap*>(map_b), const_cast<void*>(b));
+    return r == CUDA_SUCCESS ? 0 : -2;
+}
+
 int make_tmap_rows(void* map_out, const void* base, int T, long long stride_t, int Hkv, int G, long long stride_h,
                    int D, int tokens) {
     EncodeTiledFn fn = encode_fn();

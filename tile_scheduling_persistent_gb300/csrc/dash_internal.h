@@ -54,6 +54,9 @@ int make_tmap_3d(void* map_out, const void* base, long long heads, int S, int D)
 // of V.
 int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, int type,
                     int rows);
+// Cache pages as rows of `bytes` bytes (a multiple of 16, at most 1024), in boxes of one row: for gathers of four.  Of two
+// tensors.
+int make_tmap_gather(void* map_a, void* map_b, const void* a, const void* b, long long rows, int bytes);
 // Packed query rows [T][Hkv][G][D] bf16 with strides (elements) of tokens and
 // heads: boxes of 64 columns, the G heads of one group, `tokens` tokens.
 int make_tmap_rows(void* map_out, const void* base, int T, long long stride_t, int Hkv, int G, long long stride_h,

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
         const uint8_t* const from = reinterpret_cast<const uint8_t*>(kind == 0 ? p.c.k : kind == 1 ? p.c.v
                                                                      : kind == 2 ? (const void*)p.c.k_scale : (const void*)p.c.v_scale);
         const uint32_t to = (kind < 2 ? ring : sbase + C::OFF_SCALE + group * C::kStages * 2 * kKeys * C::kScaleRow) +
-                            (uint32_t)((kind & 1) * kKeys + sub * rows) * each;
+                            (uint32_t)((kind & 1) * kKeys + sub * (kE2M1 && p.gather ? 64 : rows)) * each;
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
             find_item<kKeys>(p, plan, item, it);
@@ -317,6 +317,16 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                 const int count = __popc(__ballot_sync(0xffffffffu, need && kind == 0));
                 if (tc >= C::kStages) few_wait(bar_empty + 8 * stage, (uint32_t)((tc / C::kStages - 1) & 1), abort, p.timeout_ns);
                 if (__any_sync(0xffffffffu, *abort)) break;
+                if (kE2M1 && p.gather) {   // (pages that no row sees are read as page 0)
+                    const int quad = lane >> 2;
+                    int row[4];
+                    gather_rows(p, pages, eb, key + 64 * (quad & 1), it.hk, row);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, kKeys * 2 * (C::kRow + C::kScaleRow));
+                    __syncwarp();
+                    if (quad < kKeys / 64)
+                        gather4(to + stage * pitch, kind == 0 ? &p.tm_k : kind == 1 ? &p.tm_v : kind == 2 ? &p.tm_ks : &p.tm_vs, row, full);
+                    continue;
+                }
                 if (lane == 0) ptx::mbar_arrive_expect_tx(full, count * sub_bytes);
                 __syncwarp();
                 if (need) {
@@ -1197,6 +1207,13 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     const int rows = cache->page_size < few_keys(cache->type) ? cache->page_size : few_keys(cache->type);
     if (cache->type != DASH_CACHE_E2M1 &&   // (whose vectors are copied as they lie: no tensor map to encode)
         make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
+        return DASH_ERR_CUDA;
+    prm.gather = cache->type == DASH_CACHE_E2M1 &&
+                 gathers(*cache, (long long)B * Hkv >= sm_count() || (long long)max_q * prm.G > few_most(cache->type));
+    if (prm.gather && (make_tmap_gather(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv * (cache->page_size / 16),
+                                        16 * cell_bytes(cache->type, D)) ||
+                       make_tmap_gather(&prm.tm_ks, &prm.tm_vs, cache->k_scale, cache->v_scale, (long long)cache->num_pages * Hkv * (cache->page_size / 16),
+                                        16 * scale_bytes(cache->type, D))))
         return DASH_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {

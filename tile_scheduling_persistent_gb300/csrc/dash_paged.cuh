@@ -42,6 +42,7 @@ struct Plan;
 struct PagedParams {
     CUtensorMap tm_k, tm_v;        // [num_pages * Hkv][page_size][D], boxes of min(page_size, tile) rows
     CUtensorMap tm_q;              // many rows: [T][Hq][D]
+    CUtensorMap tm_ks, tm_vs;      // E2M1, gathered pages: scales (tm_k and tm_v: codes), a row for 16 tokens of a page and head
     dash_kv_cache c;
     const __nv_bfloat16* q;
     long long q_t, q_h, table_stride;
@@ -54,6 +55,7 @@ struct PagedParams {
     int* counter;                  // many rows: next item
     Plan* plan;                    // many rows: the launch's plan
     unsigned long long timeout_ns;
+    int gather;                    // E2M1: pages are gathered by fours (gathers)
     int b0, nb;                    // the launch's sequences
     int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
     uint32_t over_G, over_Hkv;     // reciprocals (quick_div)
@@ -310,6 +312,31 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int ent
         return 0;
     }
     return page;
+}
+
+// E2M1: a copy takes its addresses from uniform registers, so those of a warp's lanes go out one after another, some 15
+// instructions each, and pages of 16 tokens need 32 bulk copies for 128 keys.  Pages of up to 32 tokens are rows of 16 tokens in
+// a tensor map instead, four to a copy (tile::gather4), where the call is large enough for the host to pay for the maps.
+// Measured (us; 64 sequences to 8192, D = 128 and 64, then 2 x 512 tokens over 8192 likewise), pages of 16 tokens copied one by
+// one: 99.5 154 195 161; by fours: 81 110 173 126; pages of 64, one by one: 79.9 96.9 165 122.  (Copied by every lane, 16 bytes at a time:
+// 121 136 289 183.)
+inline bool gathers(const dash_kv_cache& c, bool large) {
+    return large && c.page_size <= 32 && (long long)c.num_pages * c.Hkv * (c.page_size / 16) < (1ll << 31);
+}
+__device__ __forceinline__ void gather4(uint32_t to, const CUtensorMap* map, const int (&row)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(to),
+        "l"(map), "r"(0), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]), "r"(bar)
+        : "memory");
+}
+// Rows of the 64 keys from `key` on (whole warps, the key the lane's own; `pages` holds entries eb + lane).
+__device__ __forceinline__ void gather_rows(const PagedParams& p, int pages, int eb, int key, int hk, int (&row)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = key + 16 * i, page = __shfl_sync(0xffffffffu, pages, ((k >> p.page_shift) - eb) & 31);
+        row[i] = ((page * p.c.Hkv + hk) << (p.page_shift - 4)) + ((k & (p.c.page_size - 1)) >> 4);
+    }
 }
 
 // Starts as the kernel before it in the stream ends, for which it waits itself (wait_dependency).

@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                     const int pg = __shfl_sync(0xffffffffu, pages, ((k0 >> p.page_shift) - eb) & 31);
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need && kind == 0)) * (uint32_t)rows * (D / 2 + D / 16);
                     const long long cell = ((long long)pg * p.c.Hkv + it.hk) * page + (k0 & (page - 1));
+                    int row[4];
+                    if (p.gather) gather_rows(p, pages, eb, key + 64 * (sub & 1), it.hk, row);
 #pragma unroll 1
                     for (int val = 0; val < 2; ++val, ++kv) {
                         const int st = kv % C::kRawStages;
@@ -414,8 +416,14 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                             break;
                         }
                         const uint32_t dst = sbase + C::OFF_RAW + st * C::kRawStage;
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(BAR(T_RAW_FULL + st), bytes);
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(BAR(T_RAW_FULL + st), p.gather ? (uint32_t)C::kRawStage : bytes);
                         __syncwarp();
+                        if (p.gather) {   // (pages that no row sees are read as page 0)
+                            if (sub < 2)
+                                gather4(dst + (kind ? C::kRawCodes : 0) + 64 * sub * (kind ? D / 16 : D / 2),
+                                        kind ? (val ? &p.tm_vs : &p.tm_ks) : (val ? &p.tm_v : &p.tm_k), row, BAR(T_RAW_FULL + st));
+                            continue;
+                        }
                         if (need) {
                             const void* from = kind ? (val ? p.c.v_scale : p.c.k_scale) : (val ? p.c.v : p.c.k);
                             bulk_load(dst + (kind ? C::kRawCodes : 0) + sub * size, (const uint8_t*)from + cell * (kind ? D / 16 : D / 2), size,
