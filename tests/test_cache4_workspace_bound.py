@@ -20,7 +20,7 @@ extern "C" int ranges(int lo, int hi, int n, int G, int Hkv, int D, int type) {
     int ns, st;
     if (few_rows(n, G, type)) {
         const int keys = few_keys(type);
-        few_split(hi > lo ? (hi - 1) / keys - lo / keys + 1 : 0, few_workers(D, type), Hkv * few_parts(n, G), ns, st, type);
+        few_split(hi > lo ? (hi - 1) / keys - lo / keys + 1 : 0, few_workers(D, type), Hkv * few_parts(n, G), ns, st, type, n * G);
         return ns;
     }
     const int tiles = hi > lo ? (hi - 1) / 128 - lo / 128 + 1 : 0, tpi = tokens_per_item(G);

@@ -247,6 +247,79 @@ def test_the_same_bits_in_any_batch_and_run(name):
         assert same(oo, o[rows]) and same(ol, lse[rows])
 
 
+# batches whose sequences have more than 8 rows: products of two and three row tiles over each key
+TILES = {
+    # name: (Hq, Hkv, D, page, most new tokens, window, causal)
+    "two_of_64": (16, 4, 64, 16, 4, None, True),
+    "two_of_128": (16, 4, 128, 32, 3, None, True),
+    "two_wide_group": (64, 4, 128, 64, 1, None, True),
+    "three_of_64": (16, 4, 64, 64, 5, 300, True),
+    "three_of_128": (16, 4, 128, 16, 6, None, True),
+    "three_odd_group": (28, 4, 128, 128, 3, 70, True),
+    "three_odd_group_64": (20, 4, 64, 32, 4, 1, True),
+    "two_twice_of_64": (16, 4, 64, 128, 8, 129, True),
+    "two_twice_of_128": (16, 4, 128, 16, 7, None, True),
+    "two_twice_wide_group": (128, 4, 64, 16, 1, 500, True),
+    "three_full": (16, 4, 128, 64, 5, None, False),
+    "two_full": (16, 4, 64, 64, 4, None, False),
+}
+
+
+def tile_inputs(name, seed=1):
+    """41 sequences of 0 to `most` new tokens; some without keys, some with fewer keys than new tokens, two long ones."""
+    Hq, Hkv, D, page, most, window, causal = TILES[name]
+    g = gen(seed)
+    lens = [149 * i % 700 for i in range(38)] + [2, 4100, 6000]
+    n = [most - (i % 3 if most > 2 else 0) for i in range(41)]
+    lens[7], n[11] = 0, 0
+    c = paged4(g, lens, Hkv, D, page)
+    return c, randn(g, sum(n) + 3, Hq, D), n, window, causal
+
+
+@pytest.mark.parametrize("name", list(TILES))
+def test_row_tiles_against_the_oracle(name):
+    c, q, n, window, causal = tile_inputs(name)
+    o, lse = run_attn(c, q, n, window=window, causal=causal)
+    no_error()
+    check_attn4(c, q, n, o, lse, window=window, causal=causal)
+
+
+@pytest.mark.parametrize("name", list(TILES))
+def test_row_tiles_give_the_same_bits_as_single_ones(name):
+    """A sequence alone (single row tiles), in the batch, and in a step that prefills another sequence, too."""
+    c, q, n, window, causal = tile_inputs(name, seed=6)
+    o, lse = run_attn(c, q, n, window=window, causal=causal)
+    at = np.concatenate([[0], np.cumsum(n)])
+    for b in (0, 5, 7, 13, 38, 39, 40):
+        rows = slice(int(at[b]), int(at[b + 1]))
+        one = type(c)([c.k[b]], [c.v[b]], c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table[b:b + 1].contiguous(), c.lens[b:b + 1].contiguous(), c.kw)
+        oo, ol = run_attn(one, q[rows], [n[b]], window=window, causal=causal)
+        assert same(oo, o[rows]) and same(ol, lse[rows])
+        two = type(c)([c.k[b], c.k[3]], [c.v[b], c.v[3]], c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table[[b, 3]].contiguous(),
+                      c.lens[[b, 3]].contiguous(), c.kw)
+        g = gen(8)
+        oo, ol = run_attn(two, torch.cat([q[rows], randn(g, 40, q.shape[1], q.shape[2])]), [n[b], 40], window=window, causal=causal)
+        assert same(oo[:n[b]], o[rows]) and same(ol[:n[b]], lse[rows])
+    no_error()
+
+
+@pytest.mark.parametrize("name", ["two_of_64", "two_of_128", "three_of_64", "three_of_128", "two_twice_of_128"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_row_tiles_of_queries_that_are_not_finite(name, bad):
+    c, q, n, window, causal = tile_inputs(name, seed=7)
+    want, _ = run_attn(c, q, n, window=window)
+    at = [0, sum(n[:6]), sum(n[:41]) - 1]   # a long sequence's last token among them
+    for x, t in enumerate(at):
+        q[t, 5 * x, 3] = bad
+    o, lse = run_attn(c, q, n, window=window)
+    no_error()
+    keep = torch.ones(q.shape[0], q.shape[1], dtype=torch.bool)
+    for x, t in enumerate(at):
+        keep[t, 5 * x] = False
+    assert same(o[keep.to(DEV)], want[keep.to(DEV)])
+    assert torch.isnan(o[at[2], 10]).all() and torch.isnan(lse[at[2], 10])
+
+
 def test_a_key_far_above_the_others():
     """One key some 2^20 above the rest, with a small value: the others' weights have to keep their bits."""
     Hkv, D, page, L = 1, 64, 16, 300

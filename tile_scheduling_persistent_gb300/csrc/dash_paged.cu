@@ -25,7 +25,8 @@
 //     in the order of items, so that all but the first find them in L2.  Two
 //     such products in one item halve the reads from L2 and leave registers for
 //     two groups only: 16 e4m3 sequences of 16 rows to 5000 keys took 53 us so,
-//     43 us as two items (bf16: 71 and 75 us for 64 sequences at D = 64);
+//     43 us as two items (bf16: 71 and 75 us for 64 sequences at D = 64).  Over a
+//     cache of 4 bits it is the other way round (below);
 //   - at the end of an item the four warps' (O, m, l) are joined in shared
 //     memory in a fixed order.
 // Measured (Hq = 32, Hkv = 8, D = 128): 64 e4m3 sequences of 1 to 8192 tokens
@@ -59,17 +60,26 @@
 //     conversion, two shifts and two selections for 16 codes;
 //   - the consumers take registers that the producers do not need (144 of 128);
 //   - codes and scales are copied as they lie (no swizzle, no tensor map to encode
-//     for each call): K is read without bank conflicts (rows of 64 bytes in the
-//     order below, of 32 in its own), V two lanes to a bank at D = 128.
-// Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 82 us
-// with the join, 3.8 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 197 us,
-// 4.6 TB/s; 2 of 262144 (D = 128) 120 us, 5.0 TB/s.  Of 334 instructions for 16
-// keys of a head at D = 128, 64 convert, 64 scale, 16 multiply; with all the
-// conversions left out the long sequences still take 112 us, so memory's latency
-// and the items' ends are the rest.  Built and dropped: four groups (88.8 us and
-// spills), items from a counter (84 us), one item of up to 24 rows whose warps share
-// O by columns instead of keys, P going through shared memory (two barriers a
-// stage: 102 us, 16 x 5 tokens 43 us against 47).
+//     for each call, unless small pages are gathered: gathers): K is read without
+//     bank conflicts (rows of 64 bytes in the order below, of 32 in its own), V two
+//     lanes to a bank at D = 128;
+//   - more than 8 rows, in a batch that fills the GPU (few_item): two or three row
+//     tiles of an item share each conversion, Q lies in shared memory, and at D =
+//     128 two groups take 224 registers a thread (with 216, 100 bytes of them in
+//     local memory, a sixteenth slower).  A row gets the same bits as from single
+//     tiles: key ranges depend on its sequence alone, maxima on its tile.  64
+//     sequences of 1 to 8192 tokens, D = 128 and 64: 4 new tokens 155 us and 99 us
+//     with single tiles, 124 and 95 with two; 5 tokens 218 and 139 us, 150 and 93
+//     with three; 8 tokens 296 us, 237 with two twice.
+// Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 80 us
+// with the join, 3.9 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 193 us,
+// 4.7 TB/s; 2 of 262144 (D = 128) 107 us, 5.6 TB/s; 16 of 1 to 5000 with 5 new
+// tokens 38 us.  Of some 295 instructions for 16 keys of a head at D = 128, 64
+// convert, 64 scale, 16 multiply; what is left is latency and the items' ends.
+// Built and dropped: four groups (88.8 us where three took 82, and spills), items
+// from a counter (84 us), one item of up to 24 rows whose warps share O by columns
+// instead of keys, P going through shared memory (two barriers a stage: 102 us, 16
+// x 5 tokens 43 us).
 //
 // Masked keys get s = -inf by a select, never by arithmetic, and value rows
 // outside the visible keys (stale or unwritten cells, freed pages) are zeroed
@@ -168,16 +178,18 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 __device__ __forceinline__ void consumer_barrier(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 
 // ---------------------------------------------------------------- few rows
-// kGroups: independent groups of four consumer warps and a producer.
-template <int D, int kType, int kGroups>
+// kGroups: independent groups of four consumer warps and a producer.  kTiles: 8-row products of an item over each key.
+template <int D, int kType, int kGroups, int kTiles>
 struct FewCfg {
     static constexpr bool kE4M3 = kType == DASH_CACHE_E4M3, kE2M1 = kType == DASH_CACHE_E2M1;
     static constexpr int kRows = kFewRows;
+    static constexpr int kItem = kTiles * kRows;
+    static_assert(kTiles == 1 || kE2M1, "row tiles");
     // E2M1: the producers' registers go to the consumers (setmaxnreg works on whole warpgroups: one warp stays idle)
     static constexpr bool kRegs = kE2M1;
-    static constexpr int kRegsConsumer = 144, kRegsProducer = 80;
+    static constexpr int kRegsConsumer = kGroups == 2 ? 224 : kTiles == 1 ? 144 : 152, kRegsProducer = kTiles == 1 ? 80 : 56;
     static constexpr int kThreads = kRegs ? kGroups * 128 + 128 : kGroups * 160;
-    static_assert(!kRegs || (kGroups == 3 && 384 * kRegsConsumer + 128 * kRegsProducer <= 512 * 128), "register split");
+    static_assert(!kRegs || kGroups * 128 * kRegsConsumer + 128 * kRegsProducer <= kThreads * (65536 / kThreads / 8 * 8), "register split");
     static constexpr int kRow = cell_bytes(kType, D), kScaleRow = scale_bytes(kType, D);   // of a key
     static constexpr int kKeys = few_keys(kType), kSub = kKeys / 64;   // of a stage; 16-key tiles of a consumer warp
     static constexpr int kHalfStage = kKeys * kRow;           // K, then V
@@ -190,7 +202,10 @@ struct FewCfg {
     static constexpr int OFF_SLOT = OFF_SCALE + kGroups * kStages * 2 * kKeys * kScaleRow;   // [group][warp][row]
     static constexpr int OFF_M = OFF_SLOT + kGroups * 4 * kRows * kSlotRow * 4;   // [group][parity][warp][row]
     static constexpr int OFF_L = OFF_M + kGroups * 2 * 4 * kRows * 4;             // [group][warp][row]
-    static constexpr int OFF_PLAN = OFF_L + kGroups * 4 * kRows * 4;
+    // three products: Q of the item, [group][row tile][pair of k-steps][lane] 16 bytes, and its rows' scales
+    static constexpr int kQ = kTiles == 1 ? 0 : kTiles * (D / 32) * 512 + 16 * ((kItem + 3) / 4);
+    static constexpr int OFF_Q = OFF_L + kGroups * 4 * kRows * 4;
+    static constexpr int OFF_PLAN = OFF_Q + kGroups * kQ;
     static constexpr int OFF_BAR = (OFF_PLAN + (int)sizeof(Plan) + 15) / 16 * 16;
     static constexpr int OFF_ABORT = OFF_BAR + kGroups * 2 * kStages * 8;         // after [group][full, empty]
     static constexpr int kSmem = OFF_ABORT + 16;
@@ -205,7 +220,7 @@ struct FewItem {
 
 // Item `item` of the launch; whole warps.  Its sequence is the last that begins at or before it, found by two votes over
 // the plan's counts: an item's step to the next spans tens of short sequences.
-template <int kKeys>
+template <int kKeys, int kItem>
 __device__ __forceinline__ void find_item(const PagedParams& p, const Plan& plan, int item, FewItem& it) {
     constexpr int kMark = kMaxSeqs / 32;
     const int lane = threadIdx.x & 31;
@@ -214,14 +229,14 @@ __device__ __forceinline__ void find_item(const PagedParams& p, const Plan& plan
     const int b = kMark * mark + __popc(__ballot_sync(0xffffffffu, lane < kMark && i < p.nb && plan.items[i] <= item)) - 1;
     it.s = plan.seq[b];
     it.b = p.b0 + b;
-    const int st = plan.st[b], parts = few_parts(it.s.n, p.G);
+    const int st = plan.st[b], parts = few_parts(it.s.n, p.G, kItem);
     seen_keys(p, it.s, 0, it.s.n, it.lo, it.hi);
     const int first = it.lo / kKeys, tiles = it.hi > it.lo ? (it.hi - 1) / kKeys - first + 1 : 0;
     it.ns = tiles <= st ? 1 : (tiles + st - 1) / st;
     // the parts of a head and range come one after another: they share its cells in L2
     const uint32_t local = (uint32_t)(item - plan.items[b]);
     const int at = (int)(parts == 1 ? local : parts == 2 ? local / 2 : parts == 3 ? local / 3 : local / 4);
-    it.r0 = kFewRows * ((int)local - at * parts);
+    it.r0 = kItem * ((int)local - at * parts);
     it.split = quick_div(at, p.c.Hkv, p.over_Hkv);
     it.hk = at - it.split * p.c.Hkv;
     it.t0 = first + it.split * st;
@@ -243,9 +258,9 @@ __device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-template <int D, int kType, int kGroups>
-__global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
-    using C = FewCfg<D, kType, kGroups>;
+template <int D, int kType, int kGroups, int kTiles>
+__global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads), 1) paged_few_kernel(const __grid_constant__ PagedParams p, int many) {
+    using C = FewCfg<D, kType, kGroups, kTiles>;
     constexpr bool kBf16 = kType == DASH_CACHE_BF16, kE4M3 = C::kE4M3, kE2M1 = C::kE2M1;
     constexpr int kKeys = C::kKeys, kSub = C::kSub;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                             (uint32_t)((kind & 1) * kKeys + sub * (kE2M1 && p.gather ? 64 : rows)) * each;
         int tc = 0;                                       // stages used so far
         for (int item = group * gridDim.x + blockIdx.x; item < items; item += kGroups * gridDim.x) {
-            find_item<kKeys>(p, plan, item, it);
+            find_item<kKeys, C::kItem>(p, plan, item, it);
             if (it.t0 >= it.t1) continue;
             const int e0 = max(it.t0 * kKeys, it.lo) >> p.page_shift;
             const int e1 = (min(it.t1 * kKeys, it.hi) - 1) >> p.page_shift;
@@ -383,9 +398,12 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
     float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + group * 4 * C::kRows;
     // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3; E2M1: (D/4)c + 4k
     // + 0..3.  Loaded before the join of the item before, which hides the wait.
+    // With three row tiles warp ws loads and scales those of tile ws, for all warps (in shared memory).
     uint32_t qf[D / 16][2];
+    const uint32_t q_at = sbase + C::OFF_Q + group * C::kQ + 16 * lane;
+    float* const q_scale = reinterpret_cast<float*>(smem + C::OFF_Q + group * C::kQ + kTiles * (D / 32) * 512);
     auto load_queries = [&](const FewItem& x) {
-        const int r = x.r0 + min(g, min(x.s.n * p.G - x.r0, kFewRows) - 1), i = quick_div(r, p.G, p.over_G);
+        const int r = x.r0 + min(kTiles == 1 ? g : 8 * ws + g, min(x.s.n * p.G - x.r0, C::kItem) - 1), i = quick_div(r, p.G, p.over_G);
         const __nv_bfloat16* q = p.q + (long long)(x.s.first + i) * p.q_t + (long long)(x.hk * p.G + r - i * p.G) * p.q_h;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -402,7 +420,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
     FewItem after;   // the next item
     const int first_item = group * gridDim.x + blockIdx.x, step = kGroups * gridDim.x;
     if (first_item < items) {
-        find_item<kKeys>(p, plan, first_item, after);
+        find_item<kKeys, C::kItem>(p, plan, first_item, after);
         load_queries(after);
     }
     int tc = 0, parity = 0;
@@ -412,22 +430,30 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
     const uint32_t ks_at = kp * C::kScaleRow + (D == 128 ? 2 * c4 : c4), vs_col = kKeys * C::kScaleRow + (D == 128 ? g : g >> 1);
     const uint32_t vs_at0 = vp0 * C::kScaleRow + vs_col, vs_at1 = vp1 * C::kScaleRow + vs_col;
     int at_stage = 0, at_phase = 0;
-    for (int item = first_item; item < items; item += step, parity ^= 1) {
-        it = after;
-        const int all = it.s.n * p.G, R = min(all - it.r0, kFewRows);   // rows of the sequence, and of this item
+    for (int item = first_item; item < items; item += step) {
+        if (kTiles == 1) {
+            it = after;
+        } else {
+            find_item<kKeys, C::kItem>(p, plan, item, it);
+            load_queries(it);
+        }
+        const int all = it.s.n * p.G, R = min(all - it.r0, C::kItem);   // rows of the sequence, and of this item
         // keys [lo, hi) of this lane's query rows; key tiles in [full_lo, full_hi) are seen whole by every row
         int hi[2], lo[2], full_lo, full_hi, skip;
+        auto row_keys = [&](int tile) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = quick_div(it.r0 + min(2 * c4 + e, R - 1), p.G, p.over_G);
-            seen_keys(p, it.s, i, i + 1, lo[e], hi[e]);
-        }
+            for (int e = 0; e < 2; ++e) {
+                const int i = quick_div(it.r0 + min(8 * tile + 2 * c4 + e, R - 1), p.G, p.over_G);
+                seen_keys(p, it.s, i, i + 1, lo[e], hi[e]);
+            }
+        };
+        if (kTiles == 1) row_keys(0);
         seen_keys(p, it.s, 0, 1, skip, full_hi);
         seen_keys(p, it.s, it.s.n - 1, it.s.n, full_lo, skip);
 
-        float qs[2];   // scale of the scores of rows 2c + e (log2 units)
+        float qs[kTiles][2];   // scale of the scores of rows 2c + e (log2 units)
         if (kBf16) {
-            qs[0] = qs[1] = p.scale_log2e;
+            qs[0][0] = qs[0][1] = p.scale_log2e;
         } else {
             float top = 0.f;
             if (kE2M1) {   // in pairs (NaN does not enter)
@@ -451,8 +477,12 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
             const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
             float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
             if (kE2M1) down = fmaxf(down, 0x1p-126f);   // (above zero: -inf times it stays -inf)
-            qs[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
-            qs[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
+            if (kTiles == 1) {
+                qs[0][0] = __shfl_sync(0xffffffffu, down, 8 * c4);
+                qs[0][1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
+            } else if (ws < kTiles && c4 == 0) {
+                q_scale[8 * ws + g] = down;
+            }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -460,18 +490,31 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                     const uint32_t w = qf[k][x];
                     qf[k][x] = pack_half(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
                 }
+            if constexpr (kTiles > 1) {   // (all warps are past the last item's products: two barriers of its join)
+                if (ws < kTiles) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; k += 2)
+                        sts128(q_at + (ws * (D / 32) + k / 2) * 512, make_uint4(qf[k][0], qf[k][1], qf[k + 1][0], qf[k + 1][1]));
+                }
+                consumer_barrier(group);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) qs[i][0] = q_scale[8 * i + 2 * c4], qs[i][1] = q_scale[8 * i + 2 * c4 + 1];
+            }
         }
 
-        float o[D / 16][4], m[2], mv[2], l[2];
+        float oo[kTiles][D / 16][4], mm[kTiles][2], mvv[kTiles][2], ll[kTiles][2];
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
+        for (int i = 0; i < kTiles; ++i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            m[e] = -INFINITY;
-            mv[e] = kE2M1 ? 0.f : -INFINITY;
-            l[e] = 0.f;
+                for (int e = 0; e < 4; ++e) oo[i][j][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mm[i][e] = -INFINITY;
+                mvv[i][e] = kE2M1 ? 0.f : -INFINITY;
+                ll[i][e] = 0.f;
+            }
         }
 
         for (int kt = it.t0; kt < it.t1; ++kt, ++tc) {
@@ -526,17 +569,29 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                             f[t][n] = *sf;
                         }
                     }
-                float s[2][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
+                float s[kTiles][2][4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[i][t][e] = 0.f;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) f[t][n] = half2_of_e4m3x2(f[t][n]);
 #pragma unroll
-                for (int y = 0; y < kKw; ++y)
+                for (int y = 0; y < kKw; ++y) {
+                    uint32_t b[kTiles][4];   // Q^T of k-steps 2y, 2y + 1
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) {
+                        if (kTiles == 1) {
+                            b[i][0] = qf[2 * y][0], b[i][1] = qf[2 * y][1], b[i][2] = qf[2 * y + 1][0], b[i][3] = qf[2 * y + 1][1];
+                        } else {
+                            const uint4 v = lds128(q_at + (i * (D / 32) + y) * 512);
+                            b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
+                        }
+                    }
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         uint32_t h[2][4];
@@ -551,13 +606,14 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             const uint32_t a[4] = {h[0][2 * z], h[1][2 * z], h[0][2 * z + 1], h[1][2 * z + 1]};
-                            mma16816<true>(s[t], a, qf[2 * y + z][0], qf[2 * y + z][1]);
+#pragma unroll
+                            for (int i = 0; i < kTiles; ++i) mma16816<true>(s[i][t], a, b[i][2 * z], b[i][2 * z + 1]);
                         }
                     }
+                }
                 // values: codes of keys perm(2c), perm(2c + 1) and + 8 of each tile, this lane's D / 8 columns; their scales
                 uint32_t vw[2][4][kVw], vf[2][2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
+                auto load_values = [&](int t) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -573,61 +629,75 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
                         const uint8_t* const sc = scales + (16 * t + 8 * n) * C::kScaleRow;
                         vf[t][n] = sc[vs_at0] | (uint32_t)sc[vs_at1] << 8;
                     }
+                };
+                if (kTiles == 1) load_values(0), load_values(1);
                 if (edge) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int i = 0; i < kTiles; ++i) {
+                        if (kTiles > 1) row_keys(i);
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const int key = key0 + 16 * t + 8 * n + perm(g);
+                        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (key < lo[e] || key >= hi[e]) s[t][2 * n + e] = -INFINITY;
-                        }
+                            for (int n = 0; n < 2; ++n) {
+                                const int key = key0 + 16 * t + 8 * n + perm(g);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (key < lo[e] || key >= hi[e]) s[i][t][2 * n + e] = -INFINITY;
+                            }
+                    }
                 }
                 // The running maxima m (log2 units, less the lift), as below; the scores' scale qs is above zero, so the largest
                 // of the scaled scores is the largest score's, and the exponent's argument is one multiply-add.
-                float top[2];
-                bool raise = false;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    top[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e])) * qs[e] - kLiftE4M3;
-                    raise = raise || top[e] > m[e] + 8.f;
-                }
-                if (__any_sync(0xffffffffu, raise)) {
-                    float a[2];
+                for (int i = 0; i < kTiles; ++i) {
+                    float top[2];
+                    bool raise = false;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int d = 4; d <= 16; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], d));
-                        const float nm = fmaxf(m[e], top[e]);
-                        a[e] = nm == -INFINITY ? 1.f : ptx::ex2(m[e] - nm);
-                        l[e] *= a[e];
-                        m[e] = nm;
-                        mv[e] = nm == -INFINITY ? 0.f : nm;   // (what the exponents subtract)
+                        top[e] = fmaxf(fmaxf(s[i][0][e], s[i][0][2 + e]), fmaxf(s[i][1][e], s[i][1][2 + e])) * qs[i][e] - kLiftE4M3;
+                        raise = raise || top[e] > mm[i][e] + 8.f;
                     }
+                    if (__any_sync(0xffffffffu, raise)) {   // (for each row tile: what a row gets does not depend on the others')
+                        float a[2];
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[j][0] *= a[0];
-                        o[j][1] *= a[1];
-                        o[j][2] *= a[0];
-                        o[j][3] *= a[1];
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int d = 4; d <= 16; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], d));
+                            const float nm = fmaxf(mm[i][e], top[e]);
+                            a[e] = nm == -INFINITY ? 1.f : ptx::ex2(mm[i][e] - nm);
+                            ll[i][e] *= a[e];
+                            mm[i][e] = nm;
+                            mvv[i][e] = nm == -INFINITY ? 0.f : nm;   // (what the exponents subtract)
+                        }
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            oo[i][j][0] *= a[0];
+                            oo[i][j][1] *= a[1];
+                            oo[i][j][2] *= a[0];
+                            oo[i][j][3] *= a[1];
+                        }
                     }
                 }
-                uint32_t pb[2][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g; fp16
+                uint32_t pb[kTiles][2][2];   // P^T as the second operand: keys 2c, 2c + 1 (and + 8) of query row g; fp16
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int i = 0; i < kTiles; ++i) {
+                    const float less[2] = {mm[i][0] == -INFINITY ? 0.f : -mm[i][0], mm[i][1] == -INFINITY ? 0.f : -mm[i][1]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] = ptx::ex2(fmaf(s[t][e], qs[e & 1], -mv[e & 1]));
+                    for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) pb[t][n] = transposed8x8(pack_half(s[t][2 * n], s[t][2 * n + 1]));
+                        for (int e = 0; e < 4; ++e) s[i][t][e] = ptx::ex2(fmaf(s[i][t][e], qs[i][e & 1], kTiles == 1 ? -mvv[i][e & 1] : less[e & 1]));
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) pb[i][t][n] = transposed8x8(pack_half(s[i][t][2 * n], s[i][t][2 * n + 1]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) ll[i][e] += (s[i][0][e] + s[i][0][2 + e]) + (s[i][1][e] + s[i][1][2 + e]);   // the unrounded weights
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) l[e] += (s[0][e] + s[0][2 + e]) + (s[1][e] + s[1][2 + e]);   // the unrounded weights
                 // tile j of O^T: value columns (D / 8) g + 2j and + 1.  A word holds 8 columns of one key: the low and the high
                 // halves of its bytes beside those of the other key.
                 constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
+                    if (kTiles > 1) load_values(t);
 #pragma unroll
                     for (int n = 0; n < 2; ++n) vf[t][n] = half2_of_e4m3x2(vf[t][n]);
 #pragma unroll
@@ -649,11 +719,13 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const uint32_t a[4] = {h[0][2 * z], h[0][2 * z + 1], h[1][2 * z], h[1][2 * z + 1]};
-                            mma16816<true>(o[4 * y + z], a, pb[t][0], pb[t][1]);
+#pragma unroll
+                            for (int i = 0; i < kTiles; ++i) mma16816<true>(oo[i][4 * y + z], a, pb[i][t][0], pb[i][t][1]);
                         }
                     }
                 }
             } else {
+            float (&o)[D / 16][4] = oo[0], (&m)[2] = mm[0], (&mv)[2] = mvv[0], (&l)[2] = ll[0];
             float s[4];   // (key g, rows 2c, 2c + 1), (key g + 8, the same)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = 0.f;
@@ -701,7 +773,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[e] * ks[n] : qs[e];
+                for (int e = 0; e < 2; ++e) s[2 * n + e] *= kE4M3 ? qs[0][e] * ks[n] : qs[0][e];
             if (edge) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
@@ -803,77 +875,85 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups>::kThreads), 1) page
         }
 
         if (item + step < items) {
-            find_item<kKeys>(p, plan, item + step, after);
-            load_queries(after);
+            if (kTiles == 1) {
+                find_item<kKeys, C::kItem>(p, plan, item + step, after);
+                load_queries(after);
+            }
         }
 
-        // ---------------------------------------------- join the four warps
-        float* const mp = mrow + parity * 4 * C::kRows;
+        // ---------------------------------------------- join the four warps, a row tile after another
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int i8 = 0; i8 < kTiles; ++i8, parity ^= 1) {
+            float (&o)[D / 16][4] = oo[i8], (&m)[2] = mm[i8], (&mv)[2] = mvv[i8], (&l)[2] = ll[i8];
+            const int r0 = it.r0 + 8 * i8, R8 = kTiles == 1 ? R : min(R - 8 * i8, kFewRows);   // rows of this tile
+            if (kTiles > 1 && R8 <= 0) break;
+            float* const mp = mrow + parity * 4 * C::kRows;
 #pragma unroll
-            for (int d = 4; d <= 16; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
-            if (g == 0) mp[ws * C::kRows + 2 * c4 + e] = m[e];
-        }
-        consumer_barrier(group);
-        float* const slot = slots + ws * C::kRows * C::kSlotRow;
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 2 * c4 + e;
-            if (r >= R) continue;   // rows past R hold copies; they are neither joined nor stored
-            float top = -INFINITY;
+                for (int d = 4; d <= 16; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+                if (g == 0) mp[ws * C::kRows + 2 * c4 + e] = m[e];
+            }
+            consumer_barrier(group);
+            float* const slot = slots + ws * C::kRows * C::kSlotRow;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
-            // outputs carry 2^-mv (weights with their scales), sums 2^-m
-            const float fo = (top == -INFINITY || (kE4M3 ? mv[e] : m[e]) == -INFINITY) ? 0.f
-                             : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top) * (kE2M1 ? p.v_unit : 1.f);
-            if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
-            float* row = slot + r * C::kSlotRow;
-            if (kBf16) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * c4 + e;
+                if (r >= R8) continue;   // rows past R8 hold copies; they are neither joined nor stored
+                float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    row[16 * j + g] = o[j][e] * fo;
-                    row[16 * j + g + 8] = o[j][2 + e] * fo;
+                for (int w = 0; w < 4; ++w) top = fmaxf(top, mp[w * C::kRows + r]);
+                // outputs carry 2^-mv (weights with their scales), sums 2^-m
+                const float fo = (top == -INFINITY || (kE4M3 ? mv[e] : m[e]) == -INFINITY) ? 0.f
+                                 : ptx::ex2((kE4M3 ? mv[e] : m[e]) - top) * (kE2M1 ? p.v_unit : 1.f);
+                if (g == 0) lrow[ws * C::kRows + r] = l[e] * ((top == -INFINITY || m[e] == -INFINITY) ? 0.f : ptx::ex2(m[e] - top));
+                float* row = slot + r * C::kSlotRow;
+                if (kBf16) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        row[16 * j + g] = o[j][e] * fo;
+                        row[16 * j + g + 8] = o[j][2 + e] * fo;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {   // values (D / 8) g + 4k..: the chunk XOR c spreads the banks
+                        const int chunk = ((D / 32) * g + k) ^ (D == 128 ? c4 : c4 >> 1);
+                        *reinterpret_cast<float4*>(row + 4 * chunk) =
+                            make_float4(o[2 * k][e] * fo, o[2 * k][2 + e] * fo, o[2 * k + 1][e] * fo, o[2 * k + 1][2 + e] * fo);
+                    }
                 }
-            } else {
+            }
+            consumer_barrier(group);
+            for (int i = threadIdx.x & 127; i < R8 * (D / 4); i += 128) {
+                const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
+                const int chunk = !kBf16 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {   // values (D / 8) g + 4k..: the chunk XOR c spreads the banks
-                    const int chunk = ((D / 32) * g + k) ^ (D == 128 ? c4 : c4 >> 1);
-                    *reinterpret_cast<float4*>(row + 4 * chunk) =
-                        make_float4(o[2 * k][e] * fo, o[2 * k][2 + e] * fo, o[2 * k + 1][e] * fo, o[2 * k + 1][2 + e] * fo);
+                for (int w = 0; w < 4; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(slots + (w * C::kRows + r) * C::kSlotRow + 4 * chunk);
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
                 }
-            }
-        }
-        consumer_barrier(group);
-        for (int i = threadIdx.x & 127; i < R * (D / 4); i += 128) {
-            const int r = i / (D / 4), q4 = i % (D / 4), c = (r >> 1) & 3;
-            const int chunk = !kBf16 ? q4 ^ (D == 128 ? c : c >> 1) : q4;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 v = *reinterpret_cast<const float4*>(slots + (w * C::kRows + r) * C::kSlotRow + 4 * chunk);
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                top = fmaxf(top, mp[w * C::kRows + r]);
-                sum += lrow[w * C::kRows + r];
-            }
-            if (it.ns == 1) {
-                const int token = quick_div(it.r0 + r, p.G, p.over_G), tok = it.s.first + token, h = it.hk * p.G + it.r0 + r - token * p.G;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key; NaN stays NaN
-                *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
-                    make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-                if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2P;
-            } else {
-                const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * all + it.r0 + r;
-                if (row < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
-                    *reinterpret_cast<float4*>(p.part_o + row * D + 4 * q4) = a;
-                    if (q4 == 0) p.part_ml[row] = make_float2(top, sum);
+                for (int w = 0; w < 4; ++w) {
+                    top = fmaxf(top, mp[w * C::kRows + r]);
+                    sum += lrow[w * C::kRows + r];
+                }
+                if (it.ns == 1) {
+                    const int token = quick_div(r0 + r, p.G, p.over_G), tok = it.s.first + token, h = it.hk * p.G + r0 + r - token * p.G;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key; NaN stays NaN
+                    *reinterpret_cast<uint2*>(p.o + ((long long)tok * p.Hq + h) * D + 4 * q4) =
+                        make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+                    if (p.lse && q4 == 0) p.lse[(long long)tok * p.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2P;
+                } else {
+                    const long long row = plan.rows[it.b - p.b0] + ((long long)it.split * p.c.Hkv + it.hk) * all + r0 + r;
+                    if (row < p.max_rows) {   // always, unless cu_q (reported) decreases somewhere
+                        *reinterpret_cast<float4*>(p.part_o + row * D + 4 * q4) = a;
+                        if (q4 == 0) p.part_ml[row] = make_float2(top, sum);
+                    }
                 }
             }
         }
@@ -1049,33 +1129,37 @@ int sm_count() {
     return count[dev];
 }
 
-template <int D, int kType, int kGroups>
+template <int D, int kType, int kGroups, int kTiles = 1>
 int launch_few_t(const PagedParams& p, int many, int max_items, cudaStream_t s) {
-    using C = FewCfg<D, kType, kGroups>;
+    using C = FewCfg<D, kType, kGroups, kTiles>;
     static bool ready[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DASH_ERR_DEVICE;
     if (!ready[dev]) {
-        if (cudaFuncSetAttribute(paged_few_kernel<D, kType, kGroups>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_few_kernel<D, kType, kGroups, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return DASH_ERR_CUDA;
         if (C::kRegs) {   // the consumers' share has to be there, or they would wait for it
             cudaFuncAttributes a;
-            if (cudaFuncGetAttributes(&a, paged_few_kernel<D, kType, kGroups>) != cudaSuccess) return DASH_ERR_CUDA;
+            if (cudaFuncGetAttributes(&a, paged_few_kernel<D, kType, kGroups, kTiles>) != cudaSuccess) return DASH_ERR_CUDA;
             if (a.numRegs * C::kThreads < kGroups * 128 * C::kRegsConsumer + 128 * C::kRegsProducer) return DASH_ERR_LAUNCH;
         }
         ready[dev] = true;
     }
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    paged_few_kernel<D, kType, kGroups><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
+    paged_few_kernel<D, kType, kGroups, kTiles><<<max_items < sms ? max_items : sms, C::kThreads, C::kSmem, s>>>(p, many);
     return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-// Three groups where their registers and stages allow it (few_workers counts on it).
+// Three groups where their registers and stages allow it (few_workers counts on it; two with several row tiles at D = 128).
 int launch_few(const PagedParams& p, int many, int max_items, cudaStream_t s) {
     const bool d64 = p.c.D == 64;
+    if (p.item_rows == 3 * kFewRows)
+        return d64 ? launch_few_t<64, DASH_CACHE_E2M1, 3, 3>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_E2M1, 2, 3>(p, many, max_items, s);
+    if (p.item_rows == 2 * kFewRows)
+        return d64 ? launch_few_t<64, DASH_CACHE_E2M1, 3, 2>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_E2M1, 2, 2>(p, many, max_items, s);
     if (p.c.type == DASH_CACHE_E2M1)
         return d64 ? launch_few_t<64, DASH_CACHE_E2M1, 3>(p, many, max_items, s) : launch_few_t<128, DASH_CACHE_E2M1, 3>(p, many, max_items, s);
     if (p.c.type == DASH_CACHE_E4M3)
@@ -1219,6 +1303,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     for (int b0 = 0; b0 < B; b0 += kMaxSeqs) {
         prm.b0 = b0;
         prm.nb = B - b0 < kMaxSeqs ? B - b0 : kMaxSeqs;
+        prm.item_rows = few_item(max_q, prm.G, cache->type, (long long)prm.nb * Hkv);
         const Bounds bd = bounds(prm.nb, T, Hq, Hkv, max_q, max_kv);
         if (need) {
             prm.counter = (int*)workspace;

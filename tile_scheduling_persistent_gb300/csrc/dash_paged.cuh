@@ -5,7 +5,7 @@
 // A sequence with n new tokens has n * G rows per key/value head (row r is
 // token r / G, head r % G of the group: one row of queries reads the same keys
 // for the whole group).  Two classes, by the sequence's own size:
-//   few rows (few_most): memory bound; items of (8 rows, head, key range), dash_paged.cu
+//   few rows (few_most): memory bound; items of (8 rows, head, key range), dash_paged.cu (E2M1: 16 or 24 rows, few_item)
 //   many rows: items of (256 rows, head, key range), dash_paged_tile.cu
 // Every cut depends on the sequence's own lengths and on Hkv, G and D, never on
 // the rest of the batch or on the number of SMs, so that a sequence's results
@@ -55,6 +55,7 @@ struct PagedParams {
     int* counter;                  // many rows: next item
     Plan* plan;                    // many rows: the launch's plan
     unsigned long long timeout_ns;
+    int item_rows;                 // few rows: of an item (few_item)
     int gather;                    // E2M1: pages are gathered by fours (gathers)
     int b0, nb;                    // the launch's sequences
     int max_pages, B, T, Hq, G, max_q, causal, window, page_shift;
@@ -105,7 +106,7 @@ __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report
 // the many-rows kernel's 128-row products, mostly of rows that do not exist.  Measured (us; 16 sequences to 5000 keys,
 // Hq = 32, Hkv = 8; 5 tokens = 20 rows, 8 tokens = 32 rows, 12 tokens = 48 rows), few against many: e4m3, D = 128:
 // 60 / 76 / 109 against 95 / 98 / 98; D = 64: 43 / 55 / 73 against 62 / 63 / 65; bf16, D = 128: 74 / 95 / 132 against
-// 56 / 58 / 61; E2M1, D = 128 (5, 6, 8 tokens): 52 / 54 / 65 against 65 / 68 / 68; D = 64: 43 / 43 / 51 against 51 / 51 / 51.
+// 56 / 58 / 61; E2M1, D = 128 (5, 6, 8 tokens): 36 / 39 / 51 against 56 / 58 / 58; D = 64: 26 / 26 / 28 against 43 / 43 / 43.
 __host__ __device__ inline int few_most(int type) { return type == DASH_CACHE_BF16 ? 16 : kFewMost; }
 __host__ __device__ inline bool few_rows(int n, int G, int type) { return (long long)n * G <= few_most(type); }
 
@@ -132,7 +133,16 @@ __host__ __device__ inline int few_max_splits(int workers, int heads) {
 // Keys per stage.  E2M1: 32 for each consumer warp instead of 16.
 __host__ __device__ constexpr int few_keys(int type) { return type == DASH_CACHE_E2M1 ? 2 * kFewKeys : kFewKeys; }
 
-__host__ __device__ inline int few_parts(int n, int G) { return (n * G + kFewRows - 1) / kFewRows; }
+// Rows of an item in a launch of sequences of up to max_q tokens with `heads` key/value heads in all.  E2M1: each key's
+// conversions serve two or three row tiles, but an item with three takes longer, so the batch has to fill half of the GPU.
+// Measured (us; Hq = 32, Hkv = 8, D = 128, 5 tokens, 4 8 12 16 32 ragged sequences to 8000), single tiles 29 40 50 59 111, as
+// here 23 36 40 49 86; to 1000: 11 14 17 20 32 and 13 14 16 18 28.  What a row gets is the same.
+__host__ __device__ inline int few_item(int max_q, int G, int type, long long heads) {
+    const long long rows = (long long)max_q * G;
+    if (type != DASH_CACHE_E2M1 || rows <= kFewRows || rows > kFewMost || 2 * heads < kTileSms) return kFewRows;
+    return rows > 2 * kFewRows && rows <= 3 * kFewRows ? 3 * kFewRows : 2 * kFewRows;
+}
+__host__ __device__ inline int few_parts(int n, int G, int item_rows = kFewRows) { return (n * G + item_rows - 1) / item_rows; }
 
 // Groups that work through the items: three of a CTA, or two (launch_few).
 __host__ __device__ inline int few_workers(int D, int type) {
@@ -147,11 +157,15 @@ __host__ __device__ inline int few_workers(int D, int type) {
 // E2M1, in stages of 128 keys: a range's costs weigh more against half the bytes.  Measured (us; Hq = 32, Hkv = 8, D = 128;
 // 1000, 4000 and 8192 keys alone, 64 ragged sequences to 8192, 256 to 2000), ranges of a sixth of the sequence, 6 stages at
 // the most, as here: 9.3 12.0 13.0 81.6 99.4; of a quarter, 8 at the most: 9.3 13.5 13.6 79.9 97.5; of 3 stages, from 48 on 6:
-// 9.3 8.8 13.1 88.5 97.8; of an eighth, 5 at the most: 9.3 10.6 12.5 84.2 106.
-__host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st, int type = DASH_CACHE_BF16) {
+// 9.3 8.8 13.1 88.5 97.8; of an eighth, 5 at the most: 9.3 10.6 12.5 84.2 106.  More than 8 rows (1 and 64 sequences of 5 tokens
+// over 8000 and to 8192, 16 of 5000; 64 of 8 tokens), of a quarter, 8 at the most, as here: 17.1 152 36.8 237; of a sixth, 6 at
+// the most: 16.3 163 37.9 253; of a quarter, 12 at the most: 17.9 150 36.5 225.
+__host__ __device__ inline void few_split(int tiles, int workers, int heads, int& ns, int& st, int type = DASH_CACHE_BF16,
+                                          int rows = 1) {
     const int most = tiles <= kFewWholeTiles ? 1 : few_max_splits(workers, heads);
-    const int least = type == DASH_CACHE_E2M1 ? (tiles >= 36 ? 6 : tiles > 12 ? (tiles + 5) / 6 : 2)
-                                              : tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
+    const int least = type == DASH_CACHE_E2M1 && rows > kFewRows ? (tiles >= 32 ? 8 : tiles > 8 ? (tiles + 3) / 4 : 2)
+                      : type == DASH_CACHE_E2M1                    ? (tiles >= 36 ? 6 : tiles > 12 ? (tiles + 5) / 6 : 2)
+                                                                   : tiles >= 64 ? 8 : tiles > 16 ? (tiles + 7) / 8 : 2;
     st = (tiles + most - 1) / most;
     st = st < least ? least : st;
     ns = (tiles + st - 1) / st;
@@ -186,8 +200,8 @@ __device__ __forceinline__ Cut cut_few(const PagedParams& p, const Seq& s) {
     seen_keys(p, s, 0, s.n, c.lo, c.hi);
     const int keys = few_keys(p.c.type);
     c.tiles = c.hi > c.lo ? (c.hi - 1) / keys - c.lo / keys + 1 : 0;
-    c.parts = few_parts(s.n, p.G);
-    few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * c.parts, c.ns, c.st, p.c.type);
+    c.parts = few_parts(s.n, p.G, p.item_rows);
+    few_split(c.tiles, few_workers(p.c.D, p.c.type), p.c.Hkv * few_parts(s.n, p.G), c.ns, c.st, p.c.type, s.n * p.G);
     c.items = p.c.Hkv * c.ns * c.parts;
     return c;
 }
