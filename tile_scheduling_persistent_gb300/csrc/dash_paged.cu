@@ -68,9 +68,9 @@
 //     128 two groups take 224 registers a thread (with 216, 100 bytes of them in
 //     local memory, a sixteenth slower).  A row gets the same bits as from single
 //     tiles: key ranges depend on its sequence alone, maxima on its tile.  64
-//     sequences of 1 to 8192 tokens, D = 128 and 64: 4 new tokens 155 us and 99 us
-//     with single tiles, 124 and 95 with two; 5 tokens 218 and 139 us, 150 and 93
-//     with three; 8 tokens 296 us, 237 with two twice.
+//     sequences of 1 to 8192 tokens, D = 128: 4 new tokens 155 us with single tiles,
+//     125 with two; 5 tokens 218 us, 152 with three; 8 tokens 294 us, 237 with two
+//     twice; D = 64, 5 tokens: 139 us, 93 with three.
 // Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 80 us
 // with the join, 3.9 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 193 us,
 // 4.7 TB/s; 2 of 262144 (D = 128) 107 us, 5.6 TB/s; 16 of 1 to 5000 with 5 new

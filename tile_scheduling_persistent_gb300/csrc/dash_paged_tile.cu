@@ -66,7 +66,7 @@
 // converters turn them into fp16 tiles of code * scale, exact, from shared memory:
 // held in registers between the loads and the proxy fence, which waits for every
 // access, the codes cost a trip to memory for each tile (2048 tokens over 8192:
-// 635 us; 208 us so, 190 us for a bf16 cache).  Nothing is left to be scaled, so the
+// 635 us; 212 us so, 190 us for a bf16 cache).  Nothing is left to be scaled, so the
 // softmax is the bf16 caches', a warpgroup for each row tile, with fp16 weights and
 // queries as for e4m3; the cache's exponents join the scores' and the output's
 // scale.  With half of the exponentials left out it is no faster either: the
