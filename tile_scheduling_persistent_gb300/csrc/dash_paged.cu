@@ -69,7 +69,7 @@
 //     local memory, a sixteenth slower).  A row gets the same bits as from single
 //     tiles: key ranges depend on its sequence alone, maxima on its tile.  64
 //     sequences of 1 to 8192 tokens, D = 128: 4 new tokens 155 us with single tiles,
-//     125 with two; 5 tokens 218 us, 152 with three; 8 tokens 294 us, 237 with two
+//     123 with two; 5 tokens 218 us, 152 with three; 8 tokens 294 us, 234 with two
 //     twice; D = 64, 5 tokens: 139 us, 93 with three.
 // Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 80 us
 // with the join, 3.9 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 193 us,
@@ -202,7 +202,7 @@ struct FewCfg {
     static constexpr int OFF_SLOT = OFF_SCALE + kGroups * kStages * 2 * kKeys * kScaleRow;   // [group][warp][row]
     static constexpr int OFF_M = OFF_SLOT + kGroups * 4 * kRows * kSlotRow * 4;   // [group][parity][warp][row]
     static constexpr int OFF_L = OFF_M + kGroups * 2 * 4 * kRows * 4;             // [group][warp][row]
-    // three products: Q of the item, [group][row tile][pair of k-steps][lane] 16 bytes, and its rows' scales
+    // several products: Q of the item, [group][row tile][pair of k-steps][lane] 16 bytes, and its rows' scales
     static constexpr int kQ = kTiles == 1 ? 0 : kTiles * (D / 32) * 512 + 16 * ((kItem + 3) / 4);
     static constexpr int OFF_Q = OFF_L + kGroups * 4 * kRows * 4;
     static constexpr int OFF_PLAN = OFF_Q + kGroups * kQ;
@@ -397,8 +397,9 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
     float* const mrow = reinterpret_cast<float*>(smem + C::OFF_M) + group * 2 * 4 * C::kRows;
     float* const lrow = reinterpret_cast<float*>(smem + C::OFF_L) + group * 4 * C::kRows;
     // Q^T: row g; k-step k holds values 16k + 2c, + 1 and + 8, + 9; e4m3: 64(k/4) + 16c + 4(k%4) + 0..3; E2M1: (D/4)c + 4k
-    // + 0..3.  Loaded before the join of the item before, which hides the wait.
-    // With three row tiles warp ws loads and scales those of tile ws, for all warps (in shared memory).
+    // + 0..3.  Loaded before the join of the item before, which hides the wait.  With several row tiles warp ws loads and
+    // scales those of tile ws, for all warps (in shared memory); with three, whose outputs leave no registers for them, at
+    // the item's start (before its join, in local memory: 64 sequences of 5 tokens 180 us instead of 152).
     uint32_t qf[D / 16][2];
     const uint32_t q_at = sbase + C::OFF_Q + group * C::kQ + 16 * lane;
     float* const q_scale = reinterpret_cast<float*>(smem + C::OFF_Q + group * C::kQ + kTiles * (D / 32) * 512);
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
     };
     FewItem after;   // the next item
     const int first_item = group * gridDim.x + blockIdx.x, step = kGroups * gridDim.x;
-    if (first_item < items) {
+    if (kTiles < 3 && first_item < items) {
         find_item<kKeys, C::kItem>(p, plan, first_item, after);
         load_queries(after);
     }
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
     const uint32_t vs_at0 = vp0 * C::kScaleRow + vs_col, vs_at1 = vp1 * C::kScaleRow + vs_col;
     int at_stage = 0, at_phase = 0;
     for (int item = first_item; item < items; item += step) {
-        if (kTiles == 1) {
+        if (kTiles < 3) {
             it = after;
         } else {
             find_item<kKeys, C::kItem>(p, plan, item, it);
@@ -874,11 +875,9 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
             if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * stage);
         }
 
-        if (item + step < items) {
-            if (kTiles == 1) {
-                find_item<kKeys, C::kItem>(p, plan, item + step, after);
-                load_queries(after);
-            }
+        if (kTiles < 3 && item + step < items) {
+            find_item<kKeys, C::kItem>(p, plan, item + step, after);
+            load_queries(after);
         }
 
         // ---------------------------------------------- join the four warps, a row tile after another
