@@ -354,3 +354,30 @@ def test_calls_on_two_streams_at_once():
         assert a["mc"].tolist() == [len(moves), live]
         p.check()
     no_error()
+
+
+def test_fork_reports_a_length_out_of_range_of_a_row_that_goes_on():
+    p = Pool(random.Random(6), 20, 16, 4, 3, 40)
+    p.rows, p.lens, p.refs = [[1, 2], [3], [4]], [20, 16, 5], [0, 1, 1, 1, 1] + [0] * 15
+    p.up()
+    p.l[1] = -1
+    out, lens = torch.full((3, 4), 9, dtype=torch.int32, device=DEV), ints([9, 9, 9])
+    dash.pages_fork(p.t, p.l, ints([0, 1, 2]), out, lens, p.c, 16)
+    assert dash.get_status_paged() == (dash.ERR_PAGE, [4, 1, -1, 64])
+    assert out.tolist() == [[1, 2, -1, -1], [-1] * 4, [4, -1, -1, -1]] and lens.tolist() == [20, 0, 5] and p.c.tolist() == p.refs
+    no_error()
+
+
+def test_rows_that_overlap_may_need_more_pages_than_32_bits_count():
+    """Every other row's tokens run backwards, which is reported; the others have 2^24 tokens each, 2^31 pages in all."""
+    rows, T = 4096, 1 << 24
+    cu = ints([0, T] * (rows // 2) + [0])
+    lens, refs = ints([0] * rows), ints([0, 1] * 50)
+    table = torch.empty((rows, T // 16), dtype=torch.int32, device=DEV)   # no entry is read
+    slots, pos = torch.full((T,), 9, dtype=torch.int64, device=DEV), torch.full((T,), 9, dtype=torch.int32, device=DEV)
+    copies, counts = torch.full((rows, 2), MARK, dtype=torch.int32, device=DEV), ints([9, 9])
+    dash.pages_extend(table, lens, refs, 16, slots, pos, copies, counts, cu_new=cu)
+    assert dash.get_status_paged()[0] in (dash.ERR_PAGE, dash.ERR_NOMEM)
+    assert counts.tolist() == [0, 0] and (lens == 0).all() and refs.tolist() == [0, 1] * 50
+    assert (slots == -1).all() and (copies == MARK).all()
+    no_error()

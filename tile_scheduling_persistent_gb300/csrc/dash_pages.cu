@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
             if (threadIdx.x == 0) serve_error(DASH_ERR_PAGE, kOpFork, i, from, p.rows);
             from = -1;
         }
-        const int len = from < 0 ? 0 : checked_len(p, kOpFork, from, p.lens[from], false);
+        const int len = from < 0 ? 0 : checked_len(p, kOpFork, from, p.lens[from], threadIdx.x == 0);
         const int held = pages_of(p, len);
         for (int e = threadIdx.x; e < p.max_pages; e += blockDim.x)
             p.table_out[(long long)i * p.stride_out + e] = e < held ? p.table[(long long)from * p.stride + e] : -1;
@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
     }
     __syncthreads();
     // A shared page is copied by every row that extends it; where nobody else holds it, by all but the first of them.
-    // Needs and copies of the rows before, in one scan.
+    // Needs and copies of the rows before, in one scan (of 48 and 16 bits: rows whose tokens overlap, as reported, may need more
+    // pages than 32 bits count, and then get none).
     long long carry = 0;
     for (int r0 = 0; r0 < p.rows; r0 += kPoolThreads) {
         const int r = r0 + tid;
@@ -244,18 +245,19 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
                 copy = !(p.refs[last[r]] == count[s] && first[s] == r);
                 if (!copy) last[r] = -1;
             }
-            own = (long long)(pages_of(p, l + n) - pages_of(p, l) + copy) | (long long)copy << 32;
+            own = (long long)(pages_of(p, l + n) - pages_of(p, l) + copy) | (long long)copy << 48;
         }
         long long all;
         const long long before = carry + block_scan(own, scan_l, all);
         if (r < p.rows) {
             start[r] = (int)before;
-            place[r] = (int)(before >> 32);
+            place[r] = (int)(before >> 48);
         }
         carry += all;
     }
-    const int need = (int)carry, copies = (int)(carry >> 32);
-    if (tid == 0) start[p.rows] = need;
+    const long long need = carry & 0xffffffffffffll;
+    const int copies = (int)(carry >> 48);
+    if (tid == 0) start[p.rows] = (int)need;
     int all_free;
     block_scan(mine, scan_i, all_free);
     if (tid == 0) pool_free = all_free;
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
     if (!enough && lead && tid == 0) serve_error(DASH_ERR_NOMEM, kOpExtend, p.rows, need, total);
     if (lead && tid == 0) {
         p.counts[0] = enough ? copies : 0;
-        p.counts[1] = enough ? need : 0;
+        p.counts[1] = enough ? (int)need : 0;
     }
     if (enough) {
         // the j-th free page goes to the row whose needs reach past j
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
         const long long of = u / per_cache;
         int part = (int)(u - of * per_cache);
         const int i = (int)(of / p.caches), cache = (int)(of - (long long)i * p.caches);
-        const int from = p.copies[2 * i], to = p.copies[2 * i + 1];
+        const int from = p.copies[2ll * i], to = p.copies[2ll * i + 1];
         if (from < 0 || to < 0 || from >= p.num_pages || to >= p.num_pages) {
             if (threadIdx.x == 0 && part == 0 && cache == 0)
                 serve_error(DASH_ERR_PAGE, kOpCopy, i, from < 0 || from >= p.num_pages ? from : to, p.num_pages);
