@@ -30,7 +30,7 @@
 //   - at the end of an item the four warps' (O, m, l) are joined in shared
 //     memory in a fixed order.
 // Measured (Hq = 32, Hkv = 8, D = 128): 64 e4m3 sequences of 1 to 8192 tokens
-// 99 us with the join, 5.7 TB/s; two bf16 sequences of 131071 (Hkv = 16) 298 us,
+// 98 us with the join, 5.8 TB/s; two bf16 sequences of 131071 (Hkv = 16) 298 us,
 // 7.2 TB/s, as fast as memory goes; one of 1000 tokens 8.6 us.  With few or
 // ragged sequences the last round of items is what keeps it from the first two.
 //
@@ -71,8 +71,8 @@
 //     sequences of 1 to 8192 tokens, D = 128: 4 new tokens 155 us with single tiles,
 //     123 with two; 5 tokens 218 us, 152 with three; 8 tokens 294 us, 234 with two
 //     twice; D = 64, 5 tokens: 139 us, 93 with three.
-// Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 80 us
-// with the join, 3.9 TB/s (e4m3: 99 us); 3 of 262143 (D = 64, Hkv = 16) 193 us,
+// Measured: 64 sequences of 1 to 8192 tokens (Hq = 32, Hkv = 8, D = 128) 79 us
+// with the join, 3.9 TB/s (e4m3: 98 us); 3 of 262143 (D = 64, Hkv = 16) 192 us,
 // 4.7 TB/s; 2 of 262144 (D = 128) 107 us, 5.6 TB/s; 16 of 1 to 5000 with 5 new
 // tokens 38 us.  Of some 295 instructions for 16 keys of a head at D = 128, 64
 // convert, 64 scale, 16 multiply; what is left is latency and the items' ends.
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
 // eight rows, one for each warp, which adds the ranges in ascending order; or one row of a sequence with many ranges
 // (more than kWarpRanges, where one warp's chain of loads would take tens of microseconds), warp w adding ranges w,
 // w + 8, ... and the eight sums added in order.  Which of the two depends on the row's own ns.  A block finds its first
-// unit while the kernel before it runs.  It does not fit beside that kernel's CTA (its 18 or 24 thousand registers, where
+// unit while the kernel before it runs.  It does not fit beside that kernel's CTA (its 18 or 27 thousand registers, where
 // those hold 54 to 65 of an SM's 65 thousand), so this overlaps with the last CTAs only: blocks start on SMs whose CTA has ended.
 constexpr int kWarpRanges = 48;
 
@@ -1003,6 +1003,52 @@ __device__ __forceinline__ void add_ranges(const PagedParams& p, long long base,
         for (int k = 0; k < 8; ++k) {
             const float f = ptx::ex2(ml[k].x - mu);
             l += f * ml[k].y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] += f * v[k][e];
+        }
+    }
+}
+
+// The same by one warp for up to 32 ranges, with their maximum `top`: a lane has the (m, l) of one range, and the first
+// outputs are on their way with them, one trip to memory instead of three (1000 keys, 4 bits: 10.3 us to 10.0 us with the
+// few-rows kernel, bf16: 8.6 us to 8.3 us; 64 ragged e4m3 sequences 98.6 us to 97.7 us; the same bits).
+template <int D>
+__device__ __forceinline__ void add_all_ranges(const PagedParams& p, long long base, long long stride, int ns, float& top,
+                                               float (&a)[D / 32], float& l) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < ns) ml = p.part_ml[base + lane * stride];
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = 0.f;
+    for (int s = 0; s < ns; s += 8) {
+        float v[8][E];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+            if (s + k < ns) {
+                const float* o = p.part_o + (base + (s + k) * stride) * D + E * lane;
+                if (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(o);
+                    v[k][0] = x.x, v[k][1] = x.y, v[k][E - 2] = x.z, v[k][E - 1] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(o);
+                    v[k][0] = x.x, v[k][1] = x.y;
+                }
+            }
+        }
+        if (s == 0) {
+            top = ml.x;
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            ml.x = ptx::ex2(ml.x - (top == -INFINITY ? 0.f : top));   // this range's factor
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float f = __shfl_sync(0xffffffffu, ml.x, s + k), part = __shfl_sync(0xffffffffu, ml.y, s + k);
+            l += f * part;
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] += f * v[k][e];
         }
@@ -1080,7 +1126,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
         const long long at = (long long)(unit.first + i) * p.Hq + h;
         const bool real = i < unit.n && base + (unit.ns - 1) * stride < p.max_rows;   // (the second: unless cu_q, reported, decreases)
         float top = -INFINITY, l = 0.f, a[E];
-        if (real) {
+        if (real && unit.ns <= 32) {   // (fewer than kWarpRanges: alone)
+            add_all_ranges<D>(p, base, stride, unit.ns, top, a, l);
+        } else if (real) {
             for (int s = lane; s < unit.ns; s += 32) top = fmaxf(top, p.part_ml[base + s * stride].x);
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -1171,7 +1219,7 @@ template <int D>
 int launch_combine(const PagedParams& p, long long max_rows, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return DASH_ERR_CUDA;
-    // Three blocks for each SM, which holds that many at D = 64 and two at D = 128 (96 registers): each one makes the plan, so
+    // Three blocks for each SM, which holds that many at D = 64 and two at D = 128 (104 registers): each one makes the plan, so
     // more only repeat it (16 x 5 tokens over to 5000 bf16 keys, D = 128: 54 us with three, 56.5 with six, 62 with twelve, 55
     // with one; two were not tried).
     return launch_after(combine_kernel<D>, (unsigned)(max_rows < 3ll * sms ? max_rows : 3ll * sms), 256, 0, p, s);
