@@ -636,6 +636,20 @@ int dash_kv_copy(const dash_kv_cache* caches, int n_caches, const int32_t* copie
                  int max_copies, dash_stream_t stream);
 
 /*
+ * dash_packed -- one of the calls above with its arguments as 64-bit words, in the call's order (integers and addresses;
+ * `cache` and `rope` are passed as they are, NULL where the call has none, and left out of the words): for bindings that
+ * pay for every argument.  A word that is out of an int's range where the call takes an int is DASH_ERR_ARG; else it
+ * returns what the call returns.
+ */
+#define DASH_PACKED_KV_WRITE 0
+#define DASH_PACKED_KV_READ 1
+#define DASH_PACKED_ATTN_PAGED 2
+#define DASH_PACKED_PAGES_FORK 3
+#define DASH_PACKED_PAGES_EXTEND 4
+#define DASH_PACKED_PAGES_COMPACT 5
+int dash_packed(int call, const int64_t* words, const dash_kv_cache* cache, const dash_write_rope* rope);
+
+/*
  * dash_get_status_paged -- synchronizes `stream` and reports an error that
  * dash_kv_write, dash_kv_read, dash_attn_paged or a call for pages recorded on the
  * current device, on any stream (others are not waited for): *code = DASH_OK,

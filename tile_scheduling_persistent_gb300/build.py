@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 CUDA_SOURCES = ["dash_bwd.cu", "dash_fwd.cu", "dash_aux.cu", "dash_probe.cu", "dash_api.cu", "dash_noalloc.cu",
                 "dash_rope.cu", "dash_paged.cu", "dash_paged_tile.cu", "dash_pages.cu"]
-CXX_SOURCES = ["dash_sim.cpp"]
+CXX_SOURCES = ["dash_sim.cpp", "dash_packed.cpp"]
 
 
 def _nvcc() -> str:
