@@ -353,6 +353,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wave": 3, "ramp": 4}
 _BF16, _F32, _I32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
 _U8, _E2M1X2 = torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8)   # two e2m1 values to a byte
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (a tensor on it has started CUDA already)
 
 
 def _refuse(what, why):
@@ -364,7 +365,7 @@ def _refuse(what, why):
 
 def _device_stream(stream, what):
     """The current device, on which every tensor has to be, and the address of the stream (None: its current one)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if stream is None:
         return dev, (_raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream)
     if stream.device_index != dev:
@@ -373,7 +374,8 @@ def _device_stream(stream, what):
 
 
 # These calls last a few microseconds, so the checks are written out where they are made: every method call on a tensor
-# costs some 50 ns.  A stride of a dimension of size one is read as 0.
+# costs some 50 ns, a function's 100.  The tensors that most calls have are checked in place, and by the function below
+# once that has failed, which then says why.  A stride of a dimension of size one is read as 0.
 def _flat(t, dtype, dev, shape, what, name):
     """The address of a contiguous tensor."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
@@ -417,7 +419,10 @@ def _cache(k, v, k_scale, v_scale, k_exp, v_exp, dev, what):
         _refuse(what, "the cache is [num_pages, Hkv, page_size, D]")
     N, H, page, D = shape
     dtype = k.dtype
-    kp, vp = _flat(k, dtype, dev, shape, what, "k_cache"), _flat(v, dtype, dev, shape, what, "v_cache")
+    if (k.get_device() != dev or not k.is_contiguous() or v.dtype is not dtype or v.get_device() != dev or v.shape != shape or
+            not v.is_contiguous()):
+        _flat(k, dtype, dev, shape, what, "k_cache"), _flat(v, dtype, dev, shape, what, "v_cache")
+    kp, vp = k.data_ptr(), v.data_ptr()
     if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             _refuse(what, "a bf16 cache has no scales")
@@ -428,8 +433,10 @@ def _cache(k, v, k_scale, v_scale, k_exp, v_exp, dev, what):
         if not (-64 <= k_exp <= 64 and -64 <= v_exp <= 64):
             _refuse(what, "k_exp and v_exp are within -64 .. 64")
         shape = (N, H, page, D // 8)
-        return _CACHE_EXP.pack(kp, vp, _flat(k_scale, _E4M3, dev, shape, what, "k_scale"),
-                               _flat(v_scale, _E4M3, dev, shape, what, "v_scale"), 2, N, page, H, 2 * D, k_exp, v_exp), H, page, 2 * D
+        if (k_scale.dtype is not _E4M3 or k_scale.get_device() != dev or k_scale.shape != shape or not k_scale.is_contiguous() or
+                v_scale.dtype is not _E4M3 or v_scale.get_device() != dev or v_scale.shape != shape or not v_scale.is_contiguous()):
+            _flat(k_scale, _E4M3, dev, shape, what, "k_scale"), _flat(v_scale, _E4M3, dev, shape, what, "v_scale")
+        return _CACHE_EXP.pack(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), 2, N, page, H, 2 * D, k_exp, v_exp), H, page, 2 * D
     if dtype is not _E4M3 or k_scale is None or v_scale is None:
         _refuse(what, "the cache is bf16, or float8_e4m3fn or uint8 (4 bits) with k_scale and v_scale")
     shape = (N, H, page)
@@ -515,8 +522,17 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
     c, Hkv, _, D = _cache(k_cache, v_cache, k_scale, v_scale, k_exp, v_exp, dev, what)
     T = k.shape[0]
     shape = (T, Hkv, D)
-    kp, kt, kh = _tokens(k, dev, shape, what, "k")
-    vp, vt, vh = _tokens(v, dev, shape, what, "v")
+    if (k.dtype is not _BF16 or k.get_device() != dev or k.shape != shape or
+            v.dtype is not _BF16 or v.get_device() != dev or v.shape != shape):
+        _tokens(k, dev, shape, what, "k"), _tokens(v, dev, shape, what, "v")
+    kt, kh, one = k.stride()
+    vt, vh, also = v.stride()
+    if one != 1 or also != 1:
+        _tokens(k, dev, shape, what, "k"), _tokens(v, dev, shape, what, "v")
+    if T <= 1:
+        kt = vt = 0
+    if Hkv <= 1:
+        kh = vh = 0
     sp = _flat(slots, _I64, dev, (T,), what, "slots")
     r = keep = None
     if inv_freq is not None:
@@ -537,7 +553,7 @@ def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, inv_freq
                              qp, qt, qh, op, ot, oh, Hq)
     elif q is not None or q_out is not None or positions is not None:
         _refuse(what, "q, q_out and positions need inv_freq")
-    _check(lib().dash_packed(0, _KV_WRITE.pack(kp, kt, kh, vp, vt, vh, sp, T, st), c, r), what)
+    _check(lib().dash_packed(0, _KV_WRITE.pack(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, sp, T, st), c, r), what)
 
 
 def kv_read(k_cache, v_cache, block_table, lens, k, v, k_scale=None, v_scale=None, stream=None, k_exp=0, v_exp=0):
@@ -613,8 +629,14 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     if len(shape) != 3 or shape[2] != D:
         _refuse(what, "q is [T, Hq, D]")
     T, Hq, _ = shape
-    qp, qt, qh = _tokens(q, dev, shape, what, "q")
-    op = _flat(o, _BF16, dev, shape, what, "o")
+    qt, qh, one = q.stride()
+    if (q.dtype is not _BF16 or q.get_device() != dev or one != 1 or o.dtype is not _BF16 or o.get_device() != dev or
+            o.shape != shape or not o.is_contiguous()):
+        _tokens(q, dev, shape, what, "q"), _flat(o, _BF16, dev, shape, what, "o")
+    if T <= 1:
+        qt = 0
+    if Hq <= 1:
+        qh = 0
     lp = _flat(lse, _F32, dev, (T, Hq), what, "lse") if lse is not None else 0
     B = kv_lens.shape[0]
     tp, ts, pages = _table(block_table, B, dev, what)
@@ -638,7 +660,7 @@ def attn_paged(q, k_cache, v_cache, block_table, kv_lens, o, cu_q=None, max_q=No
     else:
         wn = workspace.numel()
         wp = _flat(workspace, torch.uint8, dev, (wn,), what, "workspace")
-    _check(lib().dash_packed(2, _ATTN_PAGED.pack(qp, qt, qh, tp, ts, pages, lens, cp, op, lp, B, T, Hq, max_q, bool(causal), window,
+    _check(lib().dash_packed(2, _ATTN_PAGED.pack(q.data_ptr(), qt, qh, tp, ts, pages, lens, cp, o.data_ptr(), lp, B, T, Hq, max_q, bool(causal), window,
                                                  wp, wn, st), c, None), what)
 
 
