@@ -439,3 +439,20 @@ def test_captured_and_on_another_stream():
     for o, l in outs:
         assert same(o, want) and same(l, wl)
     no_error()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_zeros_keep_their_sign(D):
+    """Byte for byte the definition's: -0 beside other values, beside zeros alone, and as what a tiny value becomes."""
+    x = torch.zeros(3, 1, D)
+    x[0, 0, ::3] = -0.0
+    x[0, 0, 1::4] = 1.5
+    x[1] = -0.0
+    x[2] = -2.0 ** -120
+    x = x.to(torch.bfloat16)
+    kc, vc, ks, vs = empty4(1, 1, 16, D)
+    dash.kv_write(x.to(DEV), x.neg().to(DEV), kc, vc, torch.arange(3, device=DEV), k_scale=ks.view(E4M3), v_scale=vs.view(E4M3), k_exp=-3, v_exp=5)
+    no_error()
+    for y, exp, codes, scales in ((x, -3, kc, ks), (x.neg(), 5, vc, vs)):
+        c, s = quantised4(y, exp)
+        assert torch.equal(scales.cpu()[0, 0, :3], s.view(torch.uint8)[:, 0]) and torch.equal(codes.cpu()[0, 0, :3], c[:, 0])

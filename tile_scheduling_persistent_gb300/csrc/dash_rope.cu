@@ -212,6 +212,11 @@ __device__ __forceinline__ float quotient(float x, float d, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, d, x), inv, q);
 }
+// The same, but for -0 too: the remainder is exact, so rounding it downwards changes the sign of a zero alone.
+__device__ __forceinline__ float quotient_signed(float x, float d, float inv) {
+    const float q = x * inv;
+    return fmaf(__fmaf_rd(-q, d, x), inv, q);
+}
 
 // Heads of a token in the order queries, keys, values.  The threads of one
 // vector are U consecutive lanes, whose maximum a butterfly forms.
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
                     const float d = unpack_e4m3x2((uint16_t)code).x * unit_, inv = __frcp_rn(d);
                     float y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = quotient(x[e], d, inv);
+                    for (int e = 0; e < 8; ++e) y[e] = quotient_signed(x[e], d, inv);
                     codes = pack_e2m1x8(y);
                     return top >= 0x7f800000u ? 0x7fu : code;
                 };
