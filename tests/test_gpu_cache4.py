@@ -456,3 +456,28 @@ def test_zeros_keep_their_sign(D):
     for y, exp, codes, scales in ((x, -3, kc, ks), (x.neg(), 5, vc, vs)):
         c, s = quantised4(y, exp)
         assert torch.equal(scales.cpu()[0, 0, :3], s.view(torch.uint8)[:, 0]) and torch.equal(codes.cpu()[0, 0, :3], c[:, 0])
+
+
+@pytest.mark.parametrize("exp", [-64, -40, -12, -9, 0, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_finite_values_far_past_the_range_keep_their_sign(D, exp):
+    """Every power of two that bf16 has, both signs, alone in its 16 values and with others: byte for byte the definition's."""
+    powers = torch.arange(-126, 128).double().exp2()
+    top = torch.tensor([torch.finfo(torch.bfloat16).max], dtype=torch.float64)
+    peak = torch.cat([powers, top, -powers, -top])
+    x = torch.zeros(peak.numel(), D // 16, 16, dtype=torch.float64)
+    x[:, 0, 3] = peak                              # alone
+    x[:, 1] = peak[:, None] * torch.tensor([1.0, -1.0, 0.5, -0.5, 0.25, -0.75, 0.0, 1.0] * 2, dtype=torch.float64)
+    x[:, 2] = torch.randn(peak.numel(), 16, generator=gen(5), dtype=torch.float64)
+    x[:, 2, 15] = -peak                            # beside small ones
+    x = x.flatten(1).to(torch.bfloat16)[:, None]
+    T, page = x.shape[0], 16
+    N = -(-T // page)
+    kc, vc, ks, vs = empty4(N, 1, page, D)
+    less = 0.0 - x                                 # (zeros stay without a sign)
+    dash.kv_write(x.to(DEV), less.to(DEV), kc, vc, torch.arange(T, device=DEV), k_scale=ks.view(E4M3), v_scale=vs.view(E4M3), k_exp=exp, v_exp=exp)
+    no_error()
+    for y, codes, scales in ((x, kc, ks), (less, vc, vs)):
+        c, s = quantised4(y, exp)
+        assert torch.equal(scales.cpu().flatten(0, 2)[:T], s.view(torch.uint8).flatten(0, 1))
+        assert torch.equal(codes.cpu().flatten(0, 2)[:T], c.flatten(0, 1))

@@ -331,6 +331,17 @@ __global__ void __launch_bounds__(128, 5) write_kernel(const __grid_constant__ W
                 ma = max(ma, other_a ? a1 : a0);
                 mb = max(mb, other_b ? b1 : b0);
                 const float unit_ = __uint_as_float((uint32_t)(127 + (val ? p.c.v_exp : p.c.k_exp)) << 23);
+                // A value so far past the range that its quotient would overflow, and the correction be a NaN without a sign, is
+                // cut off at 2^32 units (past 2688 they are codes of 6 all the same); the vote alone costs 1 % with long prompts.
+                const uint32_t far = (uint32_t)(127 + 32 + (val ? p.c.v_exp : p.c.k_exp)) << 23;
+                if (__any_sync(0xffffffffu, max(ma, mb) >= far)) {
+                    const float cut = __uint_as_float(far);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        a[e] = fminf(fmaxf(a[e], -cut), cut);
+                        b[e] = fminf(fmaxf(b[e], -cut), cut);
+                    }
+                }
                 // codes of 8 values whose 16 have the maximum `top`, and the scale's code
                 auto quantise = [&](const float (&x)[8], uint32_t top, uint32_t& codes) -> uint32_t {
                     const float s = fminf(fmaxf(__fdiv_rn(__uint_as_float(top), 6.f * unit_), 0x1p-9f), 448.f);
