@@ -596,9 +596,10 @@ int dash_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* l
  * With fewer free pages than are needed nothing is taken: counts are 0, every slot
  * is -1, table, lens and refs are as they were, and DASH_ERR_NOMEM is reported
  * (needed and free).  A row whose length, tokens or last page is out of range,
- * whose partly filled last page is counted as free, or whose pages would pass
- * max_pages, is reported (DASH_ERR_PAGE) and left as it is, its slots -1; other
- * rows are not affected.  At most 4096 rows.
+ * whose partly filled last page is counted as free, or for fewer entries than
+ * rows go on in it, or whose pages would pass max_pages, is reported
+ * (DASH_ERR_PAGE) and left as it is, its slots -1; other rows are not affected.
+ * At most 4096 rows.
  * Returns DASH_OK, DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_pages_extend(int32_t* table, int64_t table_stride, int32_t* lens, int rows, int max_pages, int32_t* refs,

@@ -381,3 +381,31 @@ def test_rows_that_overlap_may_need_more_pages_than_32_bits_count():
     assert counts.tolist() == [0, 0] and (lens == 0).all() and refs.tolist() == [0, 1] * 50
     assert (slots == -1).all() and (copies == MARK).all()
     no_error()
+
+
+@pytest.mark.parametrize("N", [30, 20000])
+@pytest.mark.parametrize("refs", [1, 2])
+def test_rows_that_go_on_in_a_page_of_fewer_holders_are_reported_and_left(refs, N):
+    """refs + 1 rows go on in page 7; the row behind them takes the lowest free page, in every run."""
+    p = Pool(random.Random(8), N, 16, 4, 1, 0)
+    p.rows, p.lens = [[3], [9]] + [[7]] * (refs + 1) + [[5]], [5, 7] + [2, 9, 15][:refs + 1] + [16]
+    p.refs = [0] * N
+    p.refs[3], p.refs[9], p.refs[7], p.refs[5] = 1, 2, refs, 1
+    p.up()
+    R = len(p.rows)
+    for _ in range(3):
+        t, lens, c = p.t.clone(), p.l.clone(), p.c.clone()
+        slots, pos, copies, counts = ints([9] * R, torch.int64), ints([9] * R), ints([[MARK] * 2] * R), ints([9, 9])
+        dash.pages_extend(t, lens, c, 16, slots, pos, copies, counts)
+        code, info = dash.get_status_paged()
+        assert code == dash.ERR_PAGE and info[0] == 5 and 2 <= info[1] <= 2 + refs and info[2:] == [refs, refs + 1]
+        no_error()
+        assert slots.tolist() == [53, 7] + [-1] * (refs + 1) + [16] and pos.tolist() == [5, 7] + [0] * (refs + 1) + [16]
+        assert lens.tolist() == [6, 8] + p.lens[2:2 + refs + 1] + [17]
+        assert counts.tolist() == [1, 2] and copies.tolist() == [[9, 0]] + [[MARK] * 2] * (R - 1)
+        want = list(p.refs)
+        want[0], want[1], want[9] = 1, 1, 1
+        assert c.tolist() == want
+        rows = p.t.tolist()
+        rows[1][0], rows[-1][1] = 0, 1
+        assert t.tolist() == rows

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
 }
 
 // ---------------------------------------------------------------- extend
-// Shared memory of the kernel: rows, and a hash table of the partly filled pages that several rows hold.
+// Shared memory of the kernel: rows, and a hash table of the partly filled pages that rows go on in.
 struct ExtendLayout {
     int rows, slots;   // hash slots: a power of two, at least twice the rows
     __host__ __device__ explicit ExtendLayout(int r) : rows(r), slots(64) {
@@ -216,8 +216,6 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
             } else if (p.refs[page] < 1) {   // held, and free: it may be another row's by the end of this call
                 if (lead) serve_error(DASH_ERR_PAGE, kOpExtend, r, p.refs[page], 1);
                 ok = false;
-            } else if (p.refs[page] == 1) {
-                page = -1;   // its own
             } else {
                 int s = hash(page);
                 for (int was; (was = atomicCAS(key + s, -1, page)) != -1 && was != page;) s = (s + 1) & mask;
@@ -229,7 +227,9 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
         last[r] = ok ? page : -2;
     }
     __syncthreads();
-    // A shared page is copied by every row that extends it; where nobody else holds it, by all but the first of them.
+    // A shared page is copied by every row that extends it; where nobody else holds it, by all but the first of them.  Where
+    // it has fewer holders than that by its count, none of them goes on: the count would pass zero while others look for free
+    // pages.
     // Needs and copies of the rows before, in one scan (of 48 and 16 bits: rows whose tokens overlap, as reported, may need more
     // pages than 32 bits count, and then get none).
     long long carry = 0;
@@ -242,10 +242,16 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
             if (last[r] >= 0) {
                 int s = hash(last[r]);
                 while (key[s] != last[r]) s = (s + 1) & mask;
-                copy = !(p.refs[last[r]] == count[s] && first[s] == r);
-                if (!copy) last[r] = -1;
+                const int held = p.refs[last[r]];
+                if (held < count[s]) {
+                    if (lead) serve_error(DASH_ERR_PAGE, kOpExtend, r, held, count[s]);
+                    last[r] = -2;
+                } else {
+                    copy = !(held == count[s] && first[s] == r);
+                    if (!copy) last[r] = -1;
+                }
             }
-            own = (long long)(pages_of(p, l + n) - pages_of(p, l) + copy) | (long long)copy << 48;
+            if (last[r] != -2) own = (long long)(pages_of(p, l + n) - pages_of(p, l) + copy) | (long long)copy << 48;
         }
         long long all;
         const long long before = carry + block_scan(own, scan_l, all);
