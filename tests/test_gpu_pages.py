@@ -409,3 +409,24 @@ def test_rows_that_go_on_in_a_page_of_fewer_holders_are_reported_and_left(refs, 
         rows = p.t.tolist()
         rows[1][0], rows[-1][1] = 0, 1
         assert t.tolist() == rows
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("N,at", [(20, 2), (9000, 4097), (40000, 9001), (40000, 12)])
+def test_compact_reports_an_entry_of_a_free_page_below_the_pages_in_use(N, at, in_place):
+    """The free page is where another row's page goes: the entry stays as it is, and is reported."""
+    refs = [0] * N
+    for q in range(at + 1):
+        refs[q] = 1
+    refs[at] = 0
+    refs[N - 1] = refs[N - 2] = 1                        # at + 2 pages in use; page `at` and the one behind it are free
+    rows = [[N - 1], [at], [0], [N - 2]]
+    t, lens, c = ints([r + [MARK] for r in rows]), ints([16, 3, 16, 9]), ints(refs)
+    copies, counts = torch.full((N // 2, 2), MARK, dtype=torch.int32, device=DEV), ints([9, 9])
+    to, co = (None, None) if in_place else (torch.full_like(t, 99), torch.full_like(c, 99))
+    dash.pages_compact(t, lens, c, 16, copies, counts, table_out=to, refs_out=co)
+    assert dash.get_status_paged() == (dash.ERR_PAGE, [6, 1, at, N])
+    no_error()
+    assert counts.tolist() == [2, at + 2] and copies[:2].tolist() == [[N - 2, at], [N - 1, at + 1]]
+    assert (t if in_place else to).tolist() == [[at + 1, MARK], [at, MARK], [0, MARK], [at, MARK]]
+    assert (c if in_place else co).tolist() == [1] * (at + 2) + [0] * (N - at - 2)

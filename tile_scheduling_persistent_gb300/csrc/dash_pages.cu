@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kPoolThreads) compact_kernel(const __grid_cons
             const int page = page0 + k;
             if (page >= p.num_pages) break;
             if (p.refs != p.refs_in) p.refs[page] = r[k];
-            if (page >= live) p.rank[page] = r[k] ? seen - below : -1;
+            p.rank[page] = !r[k] ? -1 : page < live ? 0 : seen - below;   // which move takes it (-1: it was free)
             if (page >= live && r[k]) {
                 p.copies[2 * (seen - below)] = page;
             } else if (page < live && !r[k]) {
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(256) rename_kernel(const __grid_constant__ Pag
         for (int e = blockIdx.x * 256 + threadIdx.x; e < p.max_pages; e += gridDim.x * 256) {
             int page = p.table[(long long)r * p.stride + e];
             if (e < held) {
-                const int k = page < live ? 0 : page < p.num_pages ? p.rank[page] : -1;
-                if (page < 0 || k < 0) serve_error(DASH_ERR_PAGE, kOpCompact, r, page, p.num_pages);   // no such page, or a free one
+                const int k = page >= 0 && page < p.num_pages ? p.rank[page] : -1;
+                if (k < 0) serve_error(DASH_ERR_PAGE, kOpCompact, r, page, p.num_pages);   // no such page, or a free one
                 else if (page >= live) page = p.copies[2 * k + 1];
             }
             p.table_out[(long long)r * p.stride_out + e] = page;
