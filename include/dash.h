@@ -570,9 +570,10 @@ int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, i
  * call forks a row (several children), keeps it (one), drops it (none: its pages
  * are freed where nobody else holds them), and any mixture, a beam's step say.
  * The old table is void afterwards; it and the new one must not overlap.
- * A parent past the last row counts as none, a length or an entry out of range
- * is left out of the counts, and a count that would fall below zero is reported
- * too (DASH_ERR_PAGE).
+ * A parent past the last row counts as none and a row of a length out of range
+ * as empty, an entry out of range is handed on as it is and left out of the
+ * counts; these, and a count that would fall below zero, are reported
+ * (DASH_ERR_PAGE).
  * Returns DASH_OK (also without rows), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* lens, int rows,

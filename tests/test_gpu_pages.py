@@ -430,3 +430,24 @@ def test_compact_reports_an_entry_of_a_free_page_below_the_pages_in_use(N, at, i
     assert counts.tolist() == [2, at + 2] and copies[:2].tolist() == [[N - 2, at], [N - 1, at + 1]]
     assert (t if in_place else to).tolist() == [[at + 1, MARK], [at, MARK], [0, MARK], [at, MARK]]
     assert (c if in_place else co).tolist() == [1] * (at + 2) + [0] * (N - at - 2)
+
+
+@pytest.mark.parametrize("entry", [20, -3])
+@pytest.mark.parametrize("parents", [[0, 1, 2], [2, 1], [1, -1], [2, 0, 1, 1]])
+def test_fork_reports_an_entry_out_of_range_of_a_row_that_goes_on(parents, entry):
+    p = Pool(random.Random(6), 20, 16, 4, 3, 40)
+    p.rows, p.lens, p.refs = [[1, 2], [3, 5], [4]], [20, 17, 5], [0, 1, 1, 1, 1, 1] + [0] * 14
+    p.up()
+    p.t[1, 1] = entry
+    out, lens = torch.full((len(parents), 4), 9, dtype=torch.int32, device=DEV), ints([9] * len(parents))
+    dash.pages_fork(p.t, p.l, ints(parents), out, lens, p.c, 16)
+    assert dash.get_status_paged() == (dash.ERR_PAGE, [4, 1, entry, 20])
+    no_error()
+    old = [[1, 2, -1, -1], [3, entry, -1, -1], [4, -1, -1, -1], [-1] * 4]
+    assert out.tolist() == [old[q] for q in parents] and lens.tolist() == [[20, 17, 5, 0][q] for q in parents]
+    children = [parents.count(r) for r in range(3)]
+    want = list(p.refs)
+    for r, row in enumerate(p.rows):
+        for q in row:
+            want[q] = children[r] if q != 5 else 1      # (the page that the bad entry stands for is not counted)
+    assert p.c.tolist() == want

@@ -118,8 +118,14 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
         }
         const int len = from < 0 ? 0 : checked_len(p, kOpFork, from, p.lens[from], threadIdx.x == 0);
         const int held = pages_of(p, len);
-        for (int e = threadIdx.x; e < p.max_pages; e += blockDim.x)
-            p.table_out[(long long)i * p.stride_out + e] = e < held ? p.table[(long long)from * p.stride + e] : -1;
+        for (int e = threadIdx.x; e < p.max_pages; e += blockDim.x) {
+            int page = -1;
+            if (e < held) {
+                page = p.table[(long long)from * p.stride + e];
+                if (page < 0 || page >= p.num_pages) serve_error(DASH_ERR_PAGE, kOpFork, from, page, p.num_pages);
+            }
+            p.table_out[(long long)i * p.stride_out + e] = page;
+        }
         if (threadIdx.x == 0) p.lens_out[i] = len;
     }
     if (i < p.rows) {
