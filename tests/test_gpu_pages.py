@@ -451,3 +451,36 @@ def test_fork_reports_an_entry_out_of_range_of_a_row_that_goes_on(parents, entry
         for q in row:
             want[q] = children[r] if q != 5 else 1      # (the page that the bad entry stands for is not counted)
     assert p.c.tolist() == want
+
+
+MOST = 2 ** 31 - 1   # rows and tokens are ints
+
+
+def test_as_many_tokens_as_an_int_counts():
+    """Three rows' tokens and padding to the end: counters do not pass 2^31."""
+    p = Pool(random.Random(9), 20, 16, 4, 3, 30)
+    n_new = [3, 1, 9]
+    slots, pos = torch.full((MOST,), 7, dtype=torch.int64, device=DEV), torch.full((MOST,), 7, dtype=torch.int32, device=DEV)
+    copies, counts = ints([[MARK] * 2] * 3), ints([MARK, MARK])
+    dash.pages_extend(p.t, p.l, p.c, 16, slots, pos, copies, counts, cu_new=ints([0, 3, 4, 13]))
+    p.rows, p.lens, p.refs, want, taken, at, where = PG.extend(p.rows, p.lens, p.refs, n_new, 16)
+    assert counts.tolist() == [len(want), taken] and slots[:13].tolist() == where and pos[:13].tolist() == at
+    assert int(slots[13:].max()) == int(slots[13:].min()) == -1 and int(pos[13:].max()) == int(pos[13:].min()) == 0
+    p.check()
+    no_error()
+
+
+def test_as_many_rows_as_an_int_counts():
+    """Forked from one row, and compacted: the first and the last hold a page, the others nothing."""
+    parents = torch.full((MOST,), -1, dtype=torch.int32, device=DEV)
+    parents[0] = parents[-1] = 0
+    table, lens = torch.full((MOST, 1), 9, dtype=torch.int32, device=DEV), torch.full((MOST,), 9, dtype=torch.int32, device=DEV)
+    refs = ints([1, 0, 0, 0, 0, 1])
+    dash.pages_fork(ints([[5]]), ints([16]), parents, table, lens, refs, 16)
+    assert table[0].tolist() == table[-1].tolist() == [5] and lens[0] == lens[-1] == 16 and refs.tolist() == [1, 0, 0, 0, 0, 2]
+    assert int(table[1:-1].max()) == int(table[1:-1].min()) == -1 and int(lens[1:-1].max()) == int(lens[1:-1].min()) == 0
+    copies, counts = ints([[MARK] * 2] * 3), ints([MARK, MARK])
+    dash.pages_compact(table, lens, refs, 16, copies, counts)
+    assert counts.tolist() == [1, 2] and copies.tolist() == [[5, 1]] + [[MARK] * 2] * 2 and refs.tolist() == [1, 2, 0, 0, 0, 0]
+    assert table[0].tolist() == table[-1].tolist() == [1] and int(table[1:-1].max()) == int(table[1:-1].min()) == -1
+    no_error()

@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
     }
     if (i < p.rows) {
         int children = 0;
-        for (int j0 = 0; j0 < p.rows_out; j0 += blockDim.x) {
-            const int j = j0 + threadIdx.x;
+        for (long long j0 = 0; j0 < p.rows_out; j0 += blockDim.x) {
+            const long long j = j0 + threadIdx.x;
             children += __syncthreads_count(j < p.rows_out && p.parents[j] == i);
         }
         if (children == 1) return;
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kPoolThreads) extend_kernel(const __grid_const
         }
     }
     cluster_barrier();   // tables are complete
-    for (int t = (int)rank * kPoolThreads + tid; t < p.T; t += (int)ctas * kPoolThreads) {
+    for (long long at_t = rank * kPoolThreads + tid; at_t < p.T; at_t += ctas * kPoolThreads) {
+        const int t = (int)at_t;
         int lo = 0, hi = p.rows;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -423,16 +424,16 @@ __global__ void __launch_bounds__(kPoolThreads) compact_kernel(const __grid_cons
 __global__ void __launch_bounds__(256) rename_kernel(const __grid_constant__ PagesParams p) {
     take_turn();
     const int live = p.counts[1];
-    for (int r = blockIdx.y; r < p.rows; r += gridDim.y) {
-        const int held = pages_of(p, checked_len(p, kOpCompact, r, p.lens[r], blockIdx.x == 0 && threadIdx.x == 0));
+    for (long long r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        const int held = pages_of(p, checked_len(p, kOpCompact, (int)r, p.lens[r], blockIdx.x == 0 && threadIdx.x == 0));
         for (int e = blockIdx.x * 256 + threadIdx.x; e < p.max_pages; e += gridDim.x * 256) {
-            int page = p.table[(long long)r * p.stride + e];
+            int page = p.table[r * p.stride + e];
             if (e < held) {
                 const int k = page >= 0 && page < p.num_pages ? p.rank[page] : -1;
                 if (k < 0) serve_error(DASH_ERR_PAGE, kOpCompact, r, page, p.num_pages);   // no such page, or a free one
                 else if (page >= live) page = p.copies[2 * k + 1];
             }
-            p.table_out[(long long)r * p.stride_out + e] = page;
+            p.table_out[r * p.stride_out + e] = page;
         }
     }
 }
