@@ -573,7 +573,7 @@ int dash_attn_paged_workspace(int B, int T, int Hq, int Hkv, int D, int max_q, i
  * A parent past the last row counts as none and a row of a length out of range
  * as empty, an entry out of range is handed on as it is and left out of the
  * counts; these, and a count that would fall below zero, are reported
- * (DASH_ERR_PAGE).
+ * (DASH_ERR_PAGE).  rows * rows_out is at most 2^40.
  * Returns DASH_OK (also without rows), DASH_ERR_ARG, DASH_ERR_DEVICE or DASH_ERR_CUDA.
  */
 int dash_pages_fork(const int32_t* table, int64_t table_stride, const int32_t* lens, int rows,

@@ -155,3 +155,8 @@ def test_the_binding_refuses_what_the_library_cannot_see(L, monkeypatch):
             dash.kv_copy(*a)
     with pytest.raises(dash.DashError):
         dash.kv_copy([k], [k], i32(1, 2), k_scales=[i32(1)], v_scales=[])
+
+
+@pytest.mark.parametrize("rows,rows_out", [(2 ** 20 + 1, 2 ** 20), (2 ** 31 - 1, 2 ** 31 - 1), (513, 2 ** 31 - 1)])
+def test_fork_refuses_more_pairs_of_rows_than_it_can_look_at(L, rows, rows_out):
+    assert fork(L, rows=rows, rows_out=rows_out, width=0, stride=0, out_stride=0) == dash.ERR_ARG

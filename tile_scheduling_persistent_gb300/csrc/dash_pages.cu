@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kCluster = 8, kPoolThreads = 1024, kPoolTile = 4 * kPoolThreads;   // pages of a tile: four a thread
 constexpr int kMaxRows = 4096;   // of dash_pages_extend: its rows lie in shared memory
+constexpr long long kMostPairs = 1ll << 40;   // of dash_pages_fork: each old row looks at all parents (2^36 pairs take 60 ms)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -550,7 +551,7 @@ extern "C" int dash_pages_fork(const int32_t* table, int64_t table_stride, const
     if (!pool_ok(table, table_stride, lens, rows, max_pages, refs, num_pages, page_size) ||
         !pool_ok(table_out, out_stride, lens_out, rows_out, max_pages, refs, num_pages, page_size) ||
         (rows_out > 0 && (!parents || ((uintptr_t)parents & 3u))) ||
-        (rows && rows_out && (lens == lens_out || (max_pages && table == table_out))))
+        (rows && rows_out && (lens == lens_out || (max_pages && table == table_out))) || (long long)rows * rows_out > kMostPairs)
         return DASH_ERR_ARG;
     if (rows == 0 && rows_out == 0) return DASH_OK;
     const int rc = serve_check_device();
