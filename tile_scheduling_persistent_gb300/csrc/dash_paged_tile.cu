@@ -365,8 +365,10 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
         bool ok = true;
         if (lane == 0) {
             ptx::prefetch_tensormap(&p.tm_q);
-            ptx::prefetch_tensormap(&p.tm_k);
-            ptx::prefetch_tensormap(&p.tm_v);
+            if (!kE2M1 || p.gather) {   // (else there are none)
+                ptx::prefetch_tensormap(&p.tm_k);
+                ptx::prefetch_tensormap(&p.tm_v);
+            }
         }
         const int page = p.c.page_size, rows = page < 128 ? page : 128, subs = 128 / rows;
         while (ok && next_item(it)) {
