@@ -438,22 +438,20 @@ int make_tmap_2d(void* map_out, const void* base, long long rows, int D) {
     return encode_2d(map_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, D, 64);
 }
 
-int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, int type,
+int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, bool e4m3,
                     int rows) {
     EncodeTiledFn fn = encode_fn();
     ReplaceAddressFn replace = replace_address_fn();
     if (!fn || !replace) return -2;
-    const bool bf16 = type == DASH_CACHE_BF16;
-    const cuuint64_t row = type == DASH_CACHE_E2M1 ? D / 2 : type == DASH_CACHE_E4M3 ? D : 2 * D;
-    const cuuint64_t dims[3] = {bf16 ? (cuuint64_t)D : row, (cuuint64_t)page, (cuuint64_t)heads};
+    const cuuint64_t row = (cuuint64_t)D * (e4m3 ? 1 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads};
     const cuuint64_t strides[2] = {row, row * page};
-    const cuuint32_t box[3] = {(cuuint32_t)(bf16 ? 64 : row), (cuuint32_t)rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(e4m3 ? D : 64), (cuuint32_t)rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(reinterpret_cast<CUtensorMap*>(map_k),
-                    bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(k),
+                    e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(k),
                     dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    bf16 || row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    (e4m3 && D == 64) ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return -2;
     memcpy(map_v, map_k, sizeof(CUtensorMap));   // V's is K's at another address

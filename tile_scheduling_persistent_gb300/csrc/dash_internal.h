@@ -49,10 +49,10 @@ unsigned long long timeout_ns();
 // Tensor maps (dash_api.cu).
 int make_tmap_2d(void* map_out, const void* base, long long rows, int D);
 int make_tmap_3d(void* map_out, const void* base, long long heads, int S, int D);
-// Cache pages [heads][page][D] (heads: pages times key/value heads) of a dash_cache_type, bf16 in boxes of 64 columns,
-// the others in boxes of a whole vector (rows of 128 or 64 bytes swizzled by them, of 32 not), `rows` rows high; of K and
-// of V.
-int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, int type,
+// Cache pages [heads][page][D] (heads: pages times key/value heads), bf16 in
+// boxes of 64 columns, e4m3 in boxes of D columns (swizzled rows of 128 or 64
+// bytes), `rows` rows high; of K and of V.
+int make_tmap_pages(void* map_k, void* map_v, const void* k, const void* v, long long heads, int page, int D, bool e4m3,
                     int rows);
 // Cache pages as rows of `bytes` bytes (a multiple of 16, at most 1024), in boxes of one row: for gathers of four.  Of two
 // tensors.

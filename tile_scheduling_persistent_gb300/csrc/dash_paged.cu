@@ -1337,7 +1337,7 @@ extern "C" int dash_attn_paged(const dash_bf16* q, int64_t q_stride_t, int64_t q
     }
     const int rows = cache->page_size < few_keys(cache->type) ? cache->page_size : few_keys(cache->type);
     if (cache->type != DASH_CACHE_E2M1 &&   // (whose vectors are copied as they lie: no tensor map to encode)
-        make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type, rows))
+        make_tmap_pages(&prm.tm_k, &prm.tm_v, cache->k, cache->v, (long long)cache->num_pages * Hkv, cache->page_size, D, cache->type == DASH_CACHE_E4M3, rows))
         return DASH_ERR_CUDA;
     prm.gather = cache->type == DASH_CACHE_E2M1 &&
                  gathers(*cache, (long long)B * Hkv >= sm_count() || (long long)max_q * prm.G > few_most(cache->type));

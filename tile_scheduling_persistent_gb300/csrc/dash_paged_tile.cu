@@ -1199,7 +1199,7 @@ int launch_paged_many(const PagedParams& few, int grid, cudaStream_t s) {
     const long long heads = (long long)p.c.num_pages * p.c.Hkv;
     const bool bf16 = p.c.type == DASH_CACHE_BF16, d64 = p.c.D == 64;
     // (pages up to the few-rows kernel's stages have its maps)
-    if ((bf16 && rows > kFewKeys && make_tmap_pages(&p.tm_k, &p.tm_v, p.c.k, p.c.v, heads, p.c.page_size, p.c.D, p.c.type, rows)) ||
+    if ((bf16 && rows > kFewKeys && make_tmap_pages(&p.tm_k, &p.tm_v, p.c.k, p.c.v, heads, p.c.page_size, p.c.D, false, rows)) ||
         make_tmap_rows(&p.tm_q, p.q, p.T, p.q_t, p.c.Hkv, p.G, p.q_h, p.c.D, 128 / p.G))
         return DASH_ERR_CUDA;
     if (p.c.type == DASH_CACHE_E2M1)
