@@ -439,7 +439,7 @@ typedef struct {
     float* k_scale;
     float* v_scale;
     int type, num_pages, page_size, Hkv, D;
-    int16_t k_exp, v_exp;      /* DASH_CACHE_E2M1 alone: -64 .. 64 */
+    int16_t k_exp, v_exp;      /* DASH_CACHE_E2M1: -64 .. 64; other types do not look at them */
 } dash_kv_cache;
 
 /* Rotation of new tokens on their way into the cache (see dash_rope). */

@@ -92,3 +92,19 @@ def test_an_empty_call_does_nothing(L):
     assert L.dash_kv_write(r, None, 128, 64, None, 128, 64, None, 0, None, None) == dash.OK
     assert L.dash_kv_read(r, None, 8, 4, None, None, None, 4096, 1024, 64, 0, 4, None) == dash.OK
     assert L.dash_attn_paged(None, 256, 64, r, None, 8, 4, None, None, None, None, 0, 0, 4, 2, 1, 0, None, 0, None) == dash.OK
+
+
+@pytest.mark.parametrize("exps", [dict(k_exp=-3), dict(v_exp=2), dict(k_exp=1, v_exp=1)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_exponents_belong_to_caches_of_4_bits(L, monkeypatch, kind, exps):
+    monkeypatch.setattr(dash, "_device_stream", lambda stream, what: (-1, 0))   # (CPU tensors stand for the device's)
+    c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn)
+    s = torch.zeros(4, 2, 16)
+    kw = dict(exps) if kind == "bf16" else dict(exps, k_scale=s, v_scale=s)
+    x, out = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: dash.kv_write(x, x, c, c, torch.zeros(3, dtype=torch.int64), **kw),
+                 lambda: dash.kv_read(c, c, table, lens, out, out, **kw),
+                 lambda: dash.attn_paged(x, c, c, table, lens, x, workspace=torch.zeros(16, dtype=torch.uint8), **kw)):
+        with pytest.raises(dash.DashError, match="k_exp"):
+            call()

@@ -423,6 +423,8 @@ def _cache(k, v, k_scale, v_scale, k_exp, v_exp, dev, what):
             not v.is_contiguous()):
         _flat(k, dtype, dev, shape, what, "k_cache"), _flat(v, dtype, dev, shape, what, "v_cache")
     kp, vp = k.data_ptr(), v.data_ptr()
+    if (k_exp or v_exp) and dtype is not _U8 and dtype is not _E2M1X2:
+        _refuse(what, "k_exp and v_exp are of caches of 4 bits")
     if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             _refuse(what, "a bf16 cache has no scales")
