@@ -481,3 +481,35 @@ def test_finite_values_far_past_the_range_keep_their_sign(D, exp):
         c, s = quantised4(y, exp)
         assert torch.equal(scales.cpu().flatten(0, 2)[:T], s.view(torch.uint8).flatten(0, 1))
         assert torch.equal(codes.cpu().flatten(0, 2)[:T], c.flatten(0, 1))
+
+
+def zero_keys(c):
+    c.k_cache.zero_()
+    c.kw["k_exp"] = 64
+    for k in c.k:
+        k[:] = 0.0
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_queries_over_keys_of_zero_and_greatest_exponents(n, D):
+    """Scores' scales far above the largest number: a score of zero stays zero, and every key weighs the same."""
+    g = gen(14)
+    c = paged4(g, [200, 77], 2, D, 16)
+    zero_keys(c)
+    q = randn(g, 2 * n, 8, D)
+    q[:, 1::2] *= 2.0 ** 100
+    q[n:, 3] = torch.finfo(torch.bfloat16).max
+    o, lse = run_attn(c, q, [n, n])
+    no_error()
+    check_attn4(c, q, [n, n], o, lse)
+
+
+@pytest.mark.parametrize("name", ["two_of_64", "two_of_128", "three_of_64", "three_of_128"])
+def test_row_tiles_of_large_queries_over_keys_of_zero(name):
+    c, q, n, window, causal = tile_inputs(name, seed=9)
+    zero_keys(c)
+    q[::2] *= 2.0 ** 100
+    o, lse = run_attn(c, q, n, window=window, causal=causal)
+    no_error()
+    check_attn4(c, q, n, o, lse, window=window, causal=causal)

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__((FewCfg<D, kType, kGroups, kTiles>::kThreads),
             const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127);
             const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
             float down = p.scale_log2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-            if (kE2M1) down = fmaxf(down, 0x1p-126f);   // (above zero: -inf times it stays -inf)
+            if (kE2M1) down = fminf(fmaxf(down, 0x1p-126f), 0x1p127f);   // (above zero: -inf times it stays -inf; finite: zero stays zero)
             if (kTiles == 1) {
                 qs[0][0] = __shfl_sync(0xffffffffu, down, 8 * c4);
                 qs[0][1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);

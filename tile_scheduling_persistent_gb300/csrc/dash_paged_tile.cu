@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(TileCfg<D, kType>::kThreads, 1) paged_tile_ker
                         if (j == 0) {
                             c[n] *= reinterpret_cast<const float*>(
                                 smem + C::OFF_QFAC)[((qi & 1) * 2 + (tiles == 2 ? tile(n) : slot)) * 128 + row];
-                            if (kE2M1) c[n] = fmaxf(c[n], 0x1p-126f);   // (above zero, whatever k_exp: -inf times it stays -inf)
+                            if (kE2M1) c[n] = fminf(fmaxf(c[n], 0x1p-126f), 0x1p127f);   // (whatever k_exp: -inf times it stays -inf, zero zero)
                         }
                     }
                     if constexpr (kE4M3) {
