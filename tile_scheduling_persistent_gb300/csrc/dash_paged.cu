@@ -31,7 +31,7 @@
 //     memory in a fixed order.
 // Measured (Hq = 32, Hkv = 8, D = 128): 64 e4m3 sequences of 1 to 8192 tokens
 // 98 us with the join, 5.8 TB/s; two bf16 sequences of 131071 (Hkv = 16) 298 us,
-// 7.2 TB/s, as fast as memory goes; one of 1000 tokens 8.6 us.  With few or
+// 7.2 TB/s, as fast as memory goes; one of 1000 tokens 8.3 us.  With few or
 // ragged sequences the last round of items is what keeps it from the first two.
 //
 // e4m3 caches.  Codes become fp16 pairs in registers (exact: e4m3 has 3

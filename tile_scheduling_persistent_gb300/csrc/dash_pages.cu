@@ -514,8 +514,8 @@ PagesParams make_params(const int32_t* table, int64_t stride, const int32_t* len
 }
 
 // CTAs of the cluster that works through a pool.  A small one is one CTA's: its barriers cost less than the other seven bring.
-// Measured (us; extend / compact, 160 rows), one CTA against eight: 64 pages 4.0 / 4.9 and 5.1 / 7.7, 2300 4.1 / 5.8 and
-// 5.3 / 9.1, 8192 4.4 / 9.6 and 5.3 / 10.8, 16384 4.8 / 14.9 and 5.3 / 10.8, 65536 7.5 / 55 and 5.7 / 15.  (A thread's pages one
+// Measured (us; extend / compact, 160 rows), one CTA against eight: 64 pages 4.3 / 4.9 and 5.6 / 7.6, 2300 4.2 / 6.0 and
+// 5.7 / 9.4, 8192 4.6 / 10.5 and 5.7 / 10.8, 16384 5.0 / 16.9 and 5.8 / 10.8, 65536 7.6 / 63 and 6.1 / 15.  (A thread's pages one
 // after another, with one scan for all of them instead of one for each tile of 4096: 9.6 / 76 against 7.1 / 39 with 262144.)
 unsigned pool_ctas(int num_pages) { return num_pages <= 2 * kPoolTile ? 1 : kCluster; }
 
